@@ -20,7 +20,8 @@
  * - Arguments are validated on the host before anything is launched.  A
  *   failed check returns a status and launches nothing.  A failed launch
  *   returns ATTN_ERR_CUDA (the CUDA error is left for cudaGetLastError).
- * - bf16 for q, K, V and out; fp32 for scale, sink logits, lse and the
+ * - bf16 for q, K, V and out (the entry points named _fp8: K and V in e4m3
+ *   with scales); fp32 for scale, sink logits, lse and the
  *   split-K workspace.  All element strides are in elements.
  * - lse is the natural-log log-sum-exp of the scaled scores, sink
  *   included; it is -inf for a row with no visible key and no sink (its
@@ -409,6 +410,203 @@ int attn_decode_noalloc(const void *q, const attn_kv_t *k, const attn_kv_t *v,
                         int num_q_rows, int num_q_heads, int group, int head_dim, int max_q_len,
                         int max_kv_len, float scale, const float *sink, int causal,
                         int num_partitions, void *out, float *lse, attn_stream_t stream);
+
+/*
+ * Filling the cache: head rows, norm and rotation
+ * -----------------------------------------------
+ * The entry points below prepare the query and key heads that the attention
+ * calls above read, and store keys and values at their slots of a cache.
+ * Every head vector x (dim channels, bf16) goes through, in fp32,
+ *
+ *   norm      y_c = x_c * rsqrt(mean_{j < norm_dim} x_j^2 + norm_eps) * w_c
+ *             for c < norm_dim (y_c = x_c for the other channels)
+ *   rotation  pair i < rot_dim / 2 of channels (a, b), at position p:
+ *               phi = 2 pi p turns[i] 2^-64
+ *               y_a' = mscale (y_a cos phi - y_b sin phi)
+ *               y_b' = mscale (y_b cos phi + y_a sin phi)
+ *             (a, b) = rot_start + (i, i + rot_dim / 2), or, interleaved,
+ *             rot_start + (2i, 2i + 1)
+ *
+ * and is rounded once, to the output's type.  turns[i] is the pair's
+ * frequency as a fraction of a turn per position, in units of 2^-64
+ * (attn_rope_turns): p * turns[i] modulo 2^64 is exact for every int32
+ * position, so far positions lose nothing.
+ */
+typedef struct attn_rope {
+    const uint64_t *turns;     /* device [rot_dim / 2], or NULL when rot_dim is 0 */
+    int32_t rot_dim;           /* rotated channels: even, >= 0 */
+    int32_t interleaved;       /* 0: pairs (i, i + rot_dim / 2); 1: (2i, 2i + 1) */
+    float mscale;              /* factor of cos and sin (1: none) */
+    int32_t reserved;          /* must be 0 */
+} attn_rope_t;
+
+/*
+ * num_heads head vectors of each of a call's rows.  Head h of row r starts at
+ * in + r * in_row_stride + h * in_head_stride and goes to out likewise;
+ * channels are contiguous.  out may be in with the same strides (in place);
+ * any other overlap of the two is undefined.
+ *
+ * Requirements: in, out and norm_weight 16-byte aligned, strides multiples of
+ * 8 elements, dim a multiple of 8 up to 1024, norm_dim a multiple of 8 up to
+ * dim, rot_start a multiple of 8 with rot_start + rot_dim <= dim.
+ */
+typedef struct attn_head_rows {
+    const void *in;            /* device bf16 */
+    int64_t in_row_stride, in_head_stride;
+    void *out;                 /* device bf16; NULL where the rows go to a cache */
+    int64_t out_row_stride, out_head_stride;
+    const void *norm_weight;   /* device bf16 [norm_dim], or NULL: weights 1 */
+    float norm_eps;
+    int32_t norm_dim;          /* normed leading channels; 0: no norm */
+    int32_t num_heads, dim;
+    int32_t rot_start;         /* first rotated channel */
+    int32_t reserved;          /* must be 0 */
+} attn_head_rows_t;
+
+enum {
+    ATTN_ROPE_PLAIN = 0,   /* f_i = theta^(-2i / rot_dim) radians per position */
+    ATTN_ROPE_LINEAR = 1,  /* f_i / factor */
+    ATTN_ROPE_NTK = 2,     /* theta * factor^(rot_dim / (rot_dim - 2)) */
+    ATTN_ROPE_YARN = 3,    /* f_i / factor below `low` turns in original_len positions, f_i
+                              above `high` turns, a ramp over the pair index in between;
+                              mscale = 0.1 ln(factor) + 1 (1 for factor <= 1) */
+    ATTN_ROPE_BANDS = 4    /* the same with a ramp over the turns */
+};
+
+/*
+ * attn_rope_turns -- the frequencies of attn_rope_t, computed on the host.
+ *
+ *   rot_dim     rotated channels (even, > 0).
+ *   theta       base, > 0.
+ *   scaling     one of ATTN_ROPE_*.  factor > 0 where it is not PLAIN;
+ *               original_len > 0 and 0 < low < high for YARN and BANDS (the
+ *               usual values are 1 and 32, and 1 and 4).  The others are
+ *               ignored.
+ *   turns       out, host [rot_dim / 2]; copy it to the device.
+ *   mscale      out, host, or NULL.
+ * Returns ATTN_OK or ATTN_ERR_INVALID_ARG.  Launches nothing.
+ */
+int attn_rope_turns(int rot_dim, double theta, int scaling, double factor, double original_len,
+                    double low, double high, uint64_t *turns, float *mscale);
+
+/*
+ * attn_qk_norm_rope -- norm and rotation of query and key heads in one pass.
+ *
+ *   q, k        head rows (k may be NULL); both with an out.
+ *   rope        the rotation, or NULL (norm alone).
+ *   positions   device int32 [num_rows]; may be NULL without a rotation.
+ *   num_rows    rows of q and k.
+ * Returns ATTN_OK, ATTN_ERR_INVALID_ARG, ATTN_ERR_UNSUPPORTED or ATTN_ERR_CUDA.
+ */
+int attn_qk_norm_rope(const attn_head_rows_t *q, const attn_head_rows_t *k,
+                      const attn_rope_t *rope, const int32_t *positions, int num_rows,
+                      attn_stream_t stream);
+
+/*
+ * attn_append_kv -- store the keys and values of new tokens in a bf16 cache,
+ * keys (and, on the way, queries) normed and rotated.
+ *
+ *   q           head rows with an out, or NULL.
+ *   k           key head rows (out NULL); num_heads = the cache's KV heads.
+ *   v           value head rows (out NULL), stored unchanged: norm_dim must be
+ *               0.  NULL, with v_cache NULL, for a cache whose V is part of K
+ *               (attn_mla_decode).
+ *   rope        applied to q and k, or NULL.
+ *   positions   device int32 [num_q_rows], or NULL: a row's token index.
+ *   k_cache, v_cache  as for attn_decode.
+ *   kv_len      device uint32 [batch]: keys of sequence b, its new tokens
+ *               included (the value the attention call that follows takes).
+ *   q_row_offsets  device uint32 [batch + 1]: rows of sequence b are
+ *               [off[b], off[b + 1]), or NULL for one row per sequence.  Rows
+ *               at or behind off[batch] belong to no sequence: nothing of them
+ *               is read or written.
+ *   batch, num_q_rows   sequences and rows (num_q_rows = batch without
+ *               offsets).
+ *   max_kv_len  host upper bound of kv_len.
+ *
+ * Row i of the n rows of sequence b is token t = kv_len[b] - n + i: slot t %
+ * page_size of page page_table[b][t / page_size].  No two rows of a call may
+ * fall on one slot.  A sequence with kv_len 0 stores nothing.  A token below 0
+ * or at or above max_kv_len sets bit 2 of the error word, a page outside the
+ * pool bit 1; such a row is not stored (its q is still written, for position 0
+ * if the token is below 0).
+ */
+int attn_append_kv(const attn_head_rows_t *q, const attn_head_rows_t *k,
+                   const attn_head_rows_t *v, const attn_rope_t *rope, const int32_t *positions,
+                   const attn_kv_t *k_cache, const attn_kv_t *v_cache, const uint32_t *kv_len,
+                   const uint32_t *q_row_offsets, int batch, int num_q_rows, int max_kv_len,
+                   attn_stream_t stream);
+
+/*
+ * The scales of a cache operand held in 8 bits (e4m3: 1 sign, 4 exponent, 3
+ * mantissa bits, largest number 448, no infinity).  Every block_tokens
+ * consecutive tokens of a page and KV head share one fp32 scale: token t of
+ * sequence b, KV head kh has
+ *   base[page * page_stride + (t % page_size) / block_tokens * block_stride
+ *        + kh * head_stride]
+ * with its page as for attn_kv_t, whose base then holds e4m3 elements and
+ * whose strides count them (base 16-byte aligned, strides multiples of 16).
+ * A key or value is code * scale.
+ */
+typedef struct attn_kv_scale {
+    float *base;               /* device; attn_decode_fp8 only reads it */
+    int64_t page_stride, block_stride, head_stride;   /* in floats */
+    int32_t block_tokens;      /* a power of two that divides page_size */
+    int32_t reserved;          /* must be 0 */
+} attn_kv_scale_t;
+
+/*
+ * attn_append_kv_fp8 -- attn_append_kv into a cache held in 8 bits, head
+ * dimension 128, K and V each with their scales.
+ *
+ * The new tokens of a block (a sequence's tokens of one block_tokens group)
+ * and KV head get the scale s = 2^e, e the least integer with amax <= 448 s
+ * over their finite values (clamped to [-60, 120]; -60 if all are 0), from the
+ * fp32 values before any other rounding.  A block that already holds earlier
+ * tokens of the sequence keeps max(s, its scale); if that grows, the codes it
+ * holds are rounded to the new scale.  Codes are rounded to nearest even;
+ * infinities and NaN become NaN.  A block may be written by one sequence only
+ * in a call (sequences that share pages must not share the block they append
+ * to).  Slots past a sequence's last token are left as they are.
+ *
+ *   k_scale, v_scale  the caches' scales (same block_tokens).
+ *   max_q_len   host upper bound of the rows of any sequence.
+ * Everything else as for attn_append_kv; v and v_cache are required.
+ */
+int attn_append_kv_fp8(const attn_head_rows_t *q, const attn_head_rows_t *k,
+                       const attn_head_rows_t *v, const attn_rope_t *rope,
+                       const int32_t *positions, const attn_kv_t *k_cache,
+                       const attn_kv_t *v_cache, const attn_kv_scale_t *k_scale,
+                       const attn_kv_scale_t *v_scale, const uint32_t *kv_len,
+                       const uint32_t *q_row_offsets, int batch, int num_q_rows, int max_q_len,
+                       int max_kv_len, attn_stream_t stream);
+
+/*
+ * attn_decode_fp8 -- attn_decode over a cache held in 8 bits: single rows or a
+ * few rows (draft tokens) per sequence, head_dim 128.
+ *
+ *   q           device bf16 [num_q_rows][num_q_heads][128], not quantised.
+ *   k, v        cache operands of e4m3 elements with their scales; K and V
+ *               share page table, page size and block_tokens.  Scales are
+ *               finite and >= 0; results are stated for scales up to 2^64.
+ *   group       query heads per KV head, 1 to 16.
+ *   max_q_len   max_q_len * group <= 16 (longer row runs:
+ *               ATTN_ERR_UNSUPPORTED).
+ *   workspace   device, 256-byte aligned, of at least
+ *               attn_decode_fp8_workspace bytes.  Contents on entry are
+ *               ignored.  Calls that can overlap on the GPU need one each.
+ * The other arguments as for attn_decode (batch <= 2048).  out and lse are
+ * those of attn_decode on the cache code * scale; a code of NaN in a visible
+ * token gives NaN.  Launches the partition kernel and the split-K reduce.
+ */
+int attn_decode_fp8_workspace(int num_sms, int batch, int num_q_heads, int group,
+                              size_t *workspace_bytes);
+int attn_decode_fp8(const void *q, const attn_kv_t *k, const attn_kv_t *v,
+                    const attn_kv_scale_t *k_scale, const attn_kv_scale_t *v_scale,
+                    const uint32_t *kv_len, const uint32_t *q_row_offsets, int batch,
+                    int num_q_rows, int num_q_heads, int group, int head_dim, int max_q_len,
+                    int max_kv_len, float scale, const float *sink, int causal, void *workspace,
+                    size_t workspace_bytes, void *out, float *lse, attn_stream_t stream);
 
 /*
  * attn_device_error_flags -- read (and optionally clear) the device-side

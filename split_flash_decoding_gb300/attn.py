@@ -43,6 +43,48 @@ class AttnError(RuntimeError):
         self.status = status
 
 
+ATTN_ROPE_SCALINGS = {"plain": 0, "linear": 1, "ntk": 2, "yarn": 3, "bands": 4}
+
+
+class attn_rope_t(ctypes.Structure):
+    _fields_ = [
+        ("turns", ctypes.c_void_p),
+        ("rot_dim", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32),
+        ("mscale", ctypes.c_float),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
+class attn_head_rows_t(ctypes.Structure):
+    _fields_ = [
+        ("in_", ctypes.c_void_p),
+        ("in_row_stride", ctypes.c_int64),
+        ("in_head_stride", ctypes.c_int64),
+        ("out", ctypes.c_void_p),
+        ("out_row_stride", ctypes.c_int64),
+        ("out_head_stride", ctypes.c_int64),
+        ("norm_weight", ctypes.c_void_p),
+        ("norm_eps", ctypes.c_float),
+        ("norm_dim", ctypes.c_int32),
+        ("num_heads", ctypes.c_int32),
+        ("dim", ctypes.c_int32),
+        ("rot_start", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
+class attn_kv_scale_t(ctypes.Structure):
+    _fields_ = [
+        ("base", ctypes.c_void_p),
+        ("page_stride", ctypes.c_int64),
+        ("block_stride", ctypes.c_int64),
+        ("head_stride", ctypes.c_int64),
+        ("block_tokens", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
 class attn_kv_t(ctypes.Structure):
     _fields_ = [
         ("base", ctypes.c_void_p),
@@ -85,6 +127,26 @@ _SIGNATURES = {
                             _c.c_void_p, _c.c_void_p, _c.c_int, _c.c_int, _c.c_int, _c.c_int,
                             _c.c_int, _c.c_int, _c.c_int, _c.c_float, _c.c_void_p, _c.c_int,
                             _c.c_int, _c.c_void_p, _c.c_void_p, _c.c_void_p],
+    "attn_rope_turns": [_c.c_int, _c.c_double, _c.c_int, _c.c_double, _c.c_double, _c.c_double,
+                        _c.c_double, _c.c_void_p, _c.POINTER(_c.c_float)],
+    "attn_qk_norm_rope": [_c.POINTER(attn_head_rows_t), _c.POINTER(attn_head_rows_t),
+                          _c.POINTER(attn_rope_t), _c.c_void_p, _c.c_int, _c.c_void_p],
+    "attn_append_kv": [_c.POINTER(attn_head_rows_t), _c.POINTER(attn_head_rows_t),
+                       _c.POINTER(attn_head_rows_t), _c.POINTER(attn_rope_t), _c.c_void_p,
+                       _c.POINTER(attn_kv_t), _c.POINTER(attn_kv_t), _c.c_void_p, _c.c_void_p,
+                       _c.c_int, _c.c_int, _c.c_int, _c.c_void_p],
+    "attn_append_kv_fp8": [_c.POINTER(attn_head_rows_t), _c.POINTER(attn_head_rows_t),
+                           _c.POINTER(attn_head_rows_t), _c.POINTER(attn_rope_t), _c.c_void_p,
+                           _c.POINTER(attn_kv_t), _c.POINTER(attn_kv_t),
+                           _c.POINTER(attn_kv_scale_t), _c.POINTER(attn_kv_scale_t), _c.c_void_p,
+                           _c.c_void_p, _c.c_int, _c.c_int, _c.c_int, _c.c_int, _c.c_void_p],
+    "attn_decode_fp8_workspace": [_c.c_int, _c.c_int, _c.c_int, _c.c_int,
+                                  _c.POINTER(_c.c_size_t)],
+    "attn_decode_fp8": [_c.c_void_p, _c.POINTER(attn_kv_t), _c.POINTER(attn_kv_t),
+                        _c.POINTER(attn_kv_scale_t), _c.POINTER(attn_kv_scale_t), _c.c_void_p,
+                        _c.c_void_p, _c.c_int, _c.c_int, _c.c_int, _c.c_int, _c.c_int, _c.c_int,
+                        _c.c_int, _c.c_float, _c.c_void_p, _c.c_int, _c.c_void_p, _c.c_size_t,
+                        _c.c_void_p, _c.c_void_p, _c.c_void_p],
 }
 
 _lib = None
@@ -125,16 +187,18 @@ def _stream_handle(stream) -> Optional[int]:
 # cache descriptors
 # ---------------------------------------------------------------------------
 
-def kv_descriptor(cache: torch.Tensor, page_table: Optional[torch.Tensor] = None) -> attn_kv_t:
-    """Describe a bf16 cache tensor for the C ABI.
+def kv_descriptor(cache: torch.Tensor, page_table: Optional[torch.Tensor] = None,
+                  dtype: torch.dtype = torch.bfloat16) -> attn_kv_t:
+    """Describe a cache tensor (bf16, or of the given dtype) for the C ABI.
 
     Paged: cache [num_pages, page_size, num_kv_heads, dim] with page_table
     int32 [batch, max_pages].  Contiguous: cache [batch, capacity,
     num_kv_heads, dim] and page_table None.  The last dimension must be
     contiguous; other strides are taken from the tensor.
     """
-    if cache.dtype != torch.bfloat16:
-        raise TypeError("cache must be bf16")
+    if cache.dtype != dtype:
+        raise TypeError("cache must be bf16" if dtype == torch.bfloat16 else
+                        f"cache must be {dtype}")
     if cache.dim() != 4 or cache.stride(3) != 1:
         raise ValueError("cache must be 4-D with contiguous channels")
     d = attn_kv_t()
@@ -154,6 +218,114 @@ def kv_descriptor(cache: torch.Tensor, page_table: Optional[torch.Tensor] = None
         d.max_pages = 0
     d.reserved = 0
     return d
+
+
+def scale_descriptor(scale: torch.Tensor, cache: torch.Tensor) -> attn_kv_scale_t:
+    """Describe the scales of an 8-bit cache [pages, page_size, heads, dim]:
+    fp32 [pages, page_size / block_tokens, heads]; strides are taken from the
+    tensor."""
+    if scale.dtype != torch.float32 or scale.dim() != 3:
+        raise ValueError("scales must be an fp32 [pages, blocks, heads] tensor")
+    pages, page_size, heads, _ = cache.shape
+    blocks = scale.shape[1]
+    if scale.shape[0] != pages or scale.shape[2] != heads or blocks == 0 or page_size % blocks:
+        raise ValueError(f"scales {tuple(scale.shape)} do not fit a cache {tuple(cache.shape)}")
+    d = attn_kv_scale_t()
+    d.base = scale.data_ptr()
+    d.page_stride, d.block_stride, d.head_stride = scale.stride()
+    d.block_tokens = page_size // blocks
+    return d
+
+
+class Rope:
+    """A rotation: turns int64 [rot_dim / 2] on the device (rope_turns), the
+    pair layout (interleaved: channels 2i and 2i + 1; otherwise i and i +
+    rot_dim / 2), the factor of cos and sin and the first rotated channel."""
+
+    def __init__(self, turns: torch.Tensor, *, interleaved: bool = False, mscale: float = 1.0,
+                 start: int = 0):
+        if turns.dtype != torch.int64 or turns.dim() != 1 or not turns.is_contiguous():
+            raise ValueError("turns must be a contiguous int64 [rot_dim / 2] tensor")
+        self.turns = turns
+        self.start = start
+        self.struct = attn_rope_t(turns.data_ptr(), 2 * turns.shape[0], 1 if interleaved else 0,
+                                  mscale, 0)
+
+
+def rope_turns(rot_dim: int, theta: float, *, scaling: str = "plain", factor: float = 1.0,
+               original_len: float = 0.0, low: Optional[float] = None,
+               high: Optional[float] = None, device=None):
+    """Frequencies of a rotation: (turns int64 [rot_dim / 2], mscale).
+
+    turns[i] is theta^(-2i / rot_dim) / 2 pi turns per position, scaled for a
+    long context, in units of 2^-64.  scaling: "plain"; "linear" (f / factor);
+    "ntk" (the base raised to factor^(rot_dim / (rot_dim - 2))); "yarn" and
+    "bands" (f / factor for pairs that turn less than `low` times in
+    original_len positions, f for those that turn more than `high` times, a
+    ramp over the pair index or over the turns in between; low and high
+    default to 1 and 32, 1 and 4).  mscale is 0.1 ln(factor) + 1 for "yarn"."""
+    if scaling not in ATTN_ROPE_SCALINGS:
+        raise ValueError(f"unknown scaling {scaling!r}")
+    low = 1.0 if low is None else low
+    high = (4.0 if scaling == "bands" else 32.0) if high is None else high
+    turns = torch.empty(max(rot_dim // 2, 0), dtype=torch.int64)
+    mscale = ctypes.c_float(1.0)
+    _check("attn_rope_turns",
+           lib().attn_rope_turns(rot_dim, theta, ATTN_ROPE_SCALINGS[scaling], factor, original_len,
+                                 low, high, turns.data_ptr(), ctypes.byref(mscale)))
+    return turns if device is None else turns.to(device), mscale.value
+
+
+def _head_rows(x: torch.Tensor, out: Optional[torch.Tensor], norm: Optional[torch.Tensor],
+               eps: float, rot_start: int) -> attn_head_rows_t:
+    if x.dtype != torch.bfloat16:
+        raise TypeError("head rows must be bf16")
+    if x.dim() != 3 or (x.stride(2) != 1 and x.shape[2] != 1):
+        raise ValueError("head rows must be [rows, heads, dim] with contiguous channels")
+    d = attn_head_rows_t()
+    d.in_ = x.data_ptr()
+    d.in_row_stride, d.in_head_stride, _ = x.stride()
+    _, d.num_heads, d.dim = x.shape
+    if out is not None:
+        if out.dtype != torch.bfloat16 or out.shape != x.shape or out.stride(2) != 1:
+            raise ValueError("out must be bf16, shaped as the input, with contiguous channels")
+        d.out = out.data_ptr()
+        d.out_row_stride, d.out_head_stride, _ = out.stride()
+    if norm is not None:
+        if norm.dtype != torch.bfloat16 or norm.dim() != 1 or not norm.is_contiguous():
+            raise ValueError("norm weights must be contiguous bf16 [norm_dim]")
+        d.norm_weight = norm.data_ptr()
+        d.norm_dim = norm.shape[0]
+        d.norm_eps = eps
+    d.rot_start = rot_start
+    return d
+
+
+def _int32(t: Optional[torch.Tensor], n: int, what: str):
+    if t is None:
+        return None
+    if t.dtype not in (torch.int32, torch.uint32) or t.shape != (n,) or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous int32 [{n}] tensor")
+    return t.data_ptr()
+
+
+def _ref(d):
+    return None if d is None else ctypes.byref(d)
+
+
+def _on_current_device(*tensors):
+    """The library works on the current device: refuse tensors from elsewhere."""
+    current = -1
+    for t in tensors:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("every tensor must be on the GPU")
+        if current < 0:
+            current = torch.cuda.current_device()
+        if t.get_device() != current:
+            raise ValueError(f"a tensor is on cuda:{t.get_device()}, the current device is "
+                             f"cuda:{current}")
 
 
 # ---------------------------------------------------------------------------
@@ -349,6 +521,172 @@ def attn_decode_noalloc(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.T
                                      group, d, max_q_len, max_kv_len, scale, _ptr(sink),
                                      1 if causal else 0, num_partitions, out.data_ptr(),
                                      _ptr(lse), _stream_handle(stream)))
+    return out, lse
+
+
+def attn_qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor] = None,
+                      positions: Optional[torch.Tensor] = None, *, rope: Optional[Rope] = None,
+                      q_norm: Optional[torch.Tensor] = None,
+                      k_norm: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                      q_out: Optional[torch.Tensor] = None,
+                      k_out: Optional[torch.Tensor] = None, stream=None):
+    """Norm and rotation of query and key heads through attn_qk_norm_rope.
+
+    q, k bf16 [rows, heads, dim], any row and head strides; positions int32
+    [rows]; q_norm / k_norm bf16 weights of the leading channels to norm, or
+    None.  q_out / k_out may be q / k (in place).  Returns (q_out, k_out)."""
+    rows = q.shape[0]
+    if k is not None and k.shape[0] != rows:
+        raise ValueError("q and k must have the same rows")
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    if k_out is None and k is not None:
+        k_out = torch.empty(k.shape, dtype=torch.bfloat16, device=k.device)
+    start = 0 if rope is None else rope.start
+    qd = _head_rows(q, q_out, q_norm, eps, start)
+    kd = None if k is None else _head_rows(k, k_out, k_norm, eps, start)
+    pos = _int32(positions, rows, "positions")
+    _on_current_device(q, k, q_out, k_out, positions, q_norm, k_norm,
+                       None if rope is None else rope.turns)
+    _check("attn_qk_norm_rope",
+           lib().attn_qk_norm_rope(ctypes.byref(qd), _ref(kd),
+                                   None if rope is None else ctypes.byref(rope.struct), pos, rows,
+                                   _stream_handle(stream)))
+    return q_out, k_out
+
+
+def _append_args(k, v, k_cache, v_cache, kv_len, page_table, q, q_out, q_row_offsets, rope,
+                 positions, q_norm, k_norm, eps, dtype):
+    rows, batch = k.shape[0], kv_len.shape[0]
+    if (v is None) != (v_cache is None):
+        raise ValueError("v and v_cache go together")
+    if (v is not None and v.shape[0] != rows) or (q is not None and q.shape[0] != rows):
+        raise ValueError("q, k and v must have the same rows")
+    if q is not None and q_out is None:
+        q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    for x, c in ((k, k_cache), (v, v_cache)):
+        if x is not None and x.shape[1:] != c.shape[2:]:
+            raise ValueError(f"rows {tuple(x.shape)} do not fit a cache {tuple(c.shape)}")
+    if page_table is not None and page_table.shape[0] != batch:
+        raise ValueError("page_table must have one row per sequence")
+    start = 0 if rope is None else rope.start
+    qd = None if q is None else _head_rows(q, q_out, q_norm, eps, start)
+    kd = _head_rows(k, None, k_norm, eps, start)
+    vd = None if v is None else _head_rows(v, None, None, eps, 0)
+    kc = kv_descriptor(k_cache, page_table, dtype)
+    vc = None if v is None else kv_descriptor(v_cache, page_table, dtype)
+    head = (_ref(qd), ctypes.byref(kd), _ref(vd),
+            None if rope is None else ctypes.byref(rope.struct),
+            _int32(positions, rows, "positions"), ctypes.byref(kc), _ref(vc))
+    tail = (_int32(kv_len, batch, "kv_len"), _int32(q_row_offsets, batch + 1, "q_row_offsets"),
+            batch, rows)
+    _on_current_device(k, v, k_cache, v_cache, kv_len, page_table, q, q_out, q_row_offsets,
+                       positions, q_norm, k_norm, None if rope is None else rope.turns)
+    return q_out, head, tail
+
+
+def attn_append_kv(k: torch.Tensor, v: Optional[torch.Tensor], k_cache: torch.Tensor,
+                   v_cache: Optional[torch.Tensor], kv_len: torch.Tensor, *, max_kv_len: int,
+                   page_table: Optional[torch.Tensor] = None, q: Optional[torch.Tensor] = None,
+                   q_out: Optional[torch.Tensor] = None,
+                   q_row_offsets: Optional[torch.Tensor] = None, rope: Optional[Rope] = None,
+                   positions: Optional[torch.Tensor] = None,
+                   q_norm: Optional[torch.Tensor] = None, k_norm: Optional[torch.Tensor] = None,
+                   eps: float = 1e-6, stream=None):
+    """Store the keys and values of new tokens through attn_append_kv.
+
+    k, v bf16 [rows, num_kv_heads, dim] (v and v_cache None for a cache whose V
+    is part of K), q [rows, num_q_heads, dim] or None; caches and page_table as
+    for kv_descriptor; kv_len int32 [batch], the new tokens included;
+    q_row_offsets int32 [batch + 1] or None (one row per sequence).  k and q
+    are normed (q_norm, k_norm) and rotated (rope) on the way.  Returns q_out."""
+    q_out, head, tail = _append_args(k, v, k_cache, v_cache, kv_len, page_table, q, q_out,
+                                     q_row_offsets, rope, positions, q_norm, k_norm, eps,
+                                     torch.bfloat16)
+    _check("attn_append_kv",
+           lib().attn_append_kv(*head, *tail, max_kv_len, _stream_handle(stream)))
+    return q_out
+
+
+def attn_append_kv_fp8(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
+                       v_cache: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
+                       kv_len: torch.Tensor, *, max_kv_len: int, max_q_len: int = 1,
+                       page_table: Optional[torch.Tensor] = None,
+                       q: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
+                       q_row_offsets: Optional[torch.Tensor] = None,
+                       rope: Optional[Rope] = None, positions: Optional[torch.Tensor] = None,
+                       q_norm: Optional[torch.Tensor] = None,
+                       k_norm: Optional[torch.Tensor] = None, eps: float = 1e-6, stream=None):
+    """attn_append_kv into caches of torch.float8_e4m3fn with fp32 scales
+    [pages, page_size / block_tokens, num_kv_heads] (attn_append_kv_fp8), head
+    dimension 128.  max_q_len bounds the rows of any sequence.  Returns q_out."""
+    q_out, head, tail = _append_args(k, v, k_cache, v_cache, kv_len, page_table, q, q_out,
+                                     q_row_offsets, rope, positions, q_norm, k_norm, eps,
+                                     torch.float8_e4m3fn)
+    ks, vs = scale_descriptor(k_scale, k_cache), scale_descriptor(v_scale, v_cache)
+    _on_current_device(k_scale, v_scale)
+    _check("attn_append_kv_fp8",
+           lib().attn_append_kv_fp8(*head, ctypes.byref(ks), ctypes.byref(vs), *tail, max_q_len,
+                                    max_kv_len, _stream_handle(stream)))
+    return q_out
+
+
+def attn_decode_fp8_workspace(batch: int, num_q_heads: int, group: int, num_sms: int = 0) -> int:
+    """Bytes of workspace that attn_decode_fp8 needs."""
+    n = ctypes.c_size_t(0)
+    _check("attn_decode_fp8_workspace",
+           lib().attn_decode_fp8_workspace(num_sms, batch, num_q_heads, group, ctypes.byref(n)))
+    return n.value
+
+
+def attn_decode_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                    k_scale: torch.Tensor, v_scale: torch.Tensor, kv_len: torch.Tensor, *,
+                    group: int, scale: float, max_kv_len: int,
+                    page_table: Optional[torch.Tensor] = None,
+                    sink: Optional[torch.Tensor] = None,
+                    q_row_offsets: Optional[torch.Tensor] = None, max_q_len: int = 1,
+                    causal: bool = False, workspace: Optional[torch.Tensor] = None,
+                    out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                    return_lse: bool = True, stream=None):
+    """Decode attention over caches of torch.float8_e4m3fn with fp32 scales
+    [pages, page_size / block_tokens, num_kv_heads] through attn_decode_fp8:
+    one row, or a few (max_q_len * group <= 16), per sequence, head dimension
+    128; everything else as for attn_decode.  Returns (out, lse)."""
+    rows, hq, d = q.shape
+    batch = kv_len.shape[0]
+    kd = kv_descriptor(k_cache, page_table, torch.float8_e4m3fn)
+    vd = kv_descriptor(v_cache, page_table, torch.float8_e4m3fn)
+    ks, vs = scale_descriptor(k_scale, k_cache), scale_descriptor(v_scale, v_cache)
+    if q.dtype != torch.bfloat16 or not q.is_contiguous():
+        raise ValueError("q must be contiguous bf16 [rows, num_q_heads, 128]")
+    if k_cache.shape[2:] != v_cache.shape[2:] or k_cache.shape[2] * group != hq:
+        raise ValueError(f"{hq} query heads in groups of {group} do not fit caches "
+                         f"{tuple(k_cache.shape)} and {tuple(v_cache.shape)}")
+    if page_table is not None and page_table.shape[0] != batch:
+        raise ValueError("page_table must have one row per sequence")
+    lens = _int32(kv_len, batch, "kv_len")
+    offs = _int32(q_row_offsets, batch + 1, "q_row_offsets")
+    if sink is not None and (sink.dtype != torch.float32 or sink.shape != (hq,) or
+                             not sink.is_contiguous()):
+        raise ValueError("sink must be contiguous fp32 [num_q_heads]")
+    if out is None:
+        out = torch.empty((rows, hq, d), dtype=torch.bfloat16, device=q.device)
+    elif out.dtype != torch.bfloat16 or out.shape != q.shape or not out.is_contiguous():
+        raise ValueError("out must be contiguous bf16, shaped as q")
+    if lse is None and return_lse:
+        lse = torch.empty((rows, hq), dtype=torch.float32, device=q.device)
+    elif lse is not None and (lse.dtype != torch.float32 or lse.shape != (rows, hq) or
+                              not lse.is_contiguous()):
+        raise ValueError("lse must be contiguous fp32 [rows, num_q_heads]")
+    _on_current_device(q, k_cache, v_cache, k_scale, v_scale, kv_len, page_table, sink,
+                       q_row_offsets, workspace, out, lse)
+    ws, ws_size = _workspace(attn_decode_fp8_workspace(batch, hq, group), q.device, workspace)
+    _check("attn_decode_fp8",
+           lib().attn_decode_fp8(q.data_ptr(), ctypes.byref(kd), ctypes.byref(vd),
+                                 ctypes.byref(ks), ctypes.byref(vs), lens, offs, batch, rows, hq,
+                                 group, d, max_q_len, max_kv_len, scale, _ptr(sink),
+                                 1 if causal else 0, _ptr(ws), ws_size, out.data_ptr(), _ptr(lse),
+                                 _stream_handle(stream)))
     return out, lse
 
 

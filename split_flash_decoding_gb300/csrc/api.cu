@@ -9,6 +9,7 @@
 #include <mutex>
 
 #include "attn_decode.h"
+#include "cache_ops.h"
 #include "launch.h"
 #include "ptx.cuh"
 
@@ -408,6 +409,29 @@ int plan_impl(int num_sms, int batch, int num_q_rows, int max_q_len, int num_q_h
 }
 
 }  // namespace
+}  // namespace attn
+
+namespace attn {
+
+int device_error_word(unsigned **out) { return error_word(out); }
+
+int encode_kv_map_8bit(CUtensorMap *map, const void *base, long long token_stride,
+                       long long head_stride, long long page_stride, int dim, int page_size,
+                       int num_kv_heads, int num_pages, int box_rows) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return ATTN_ERR_CUDA;
+    cuuint64_t gdim[4] = {cuuint64_t(dim), cuuint64_t(page_size), cuuint64_t(num_kv_heads),
+                          cuuint64_t(num_pages)};
+    cuuint64_t gstride[3] = {cuuint64_t(token_stride), cuuint64_t(head_stride),
+                             cuuint64_t(page_stride)};
+    cuuint32_t box[4] = {128, cuuint32_t(box_rows), 1, 1};
+    cuuint32_t estride[4] = {1, 1, 1, 1};
+    CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void *>(base), gdim, gstride,
+                    box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? ATTN_OK : ATTN_ERR_UNSUPPORTED;
+}
+
 }  // namespace attn
 
 extern "C" int attn_plan_partitions(int num_sms, int batch, int num_q_rows, int max_q_len,

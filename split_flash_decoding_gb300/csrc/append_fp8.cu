@@ -1,0 +1,166 @@
+// append_fp8.cu -- keys and values of new tokens into a cache held in 8 bits
+// (attn_append_kv_fp8).
+//
+// One CTA per (row, KV head, K or V); the CTA of a block's first new row does
+// the block: the new tokens' largest value gives the scale, codes already held
+// are rounded to a scale that grew, and the new tokens are encoded.
+#include <cuda_fp8.h>
+#include <float.h>
+
+#include "head_rows.cuh"
+
+namespace attn {
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kWarps = kThreads / 32;
+constexpr int kD = 128;
+constexpr int kMinExp = -60, kMaxExp = 120;
+
+// Exponent of the scale of a block whose largest finite value is amax: the
+// least e with amax <= 448 * 2^e (448 = 0.875 * 2^9), clamped.
+__device__ __forceinline__ int scale_exponent(float amax) {
+    if (!(amax > 0.f)) return kMinExp;
+    int e;
+    const float m = frexpf(amax, &e);
+    e += m > 0.875f ? -8 : -9;
+    return min(max(e, kMinExp), kMaxExp);
+}
+
+__device__ __forceinline__ float pow2i(int e) {   // -126 <= e <= 127
+    return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+}
+
+__device__ __forceinline__ uint8_t encode(float x) {
+    if (!(fabsf(x) <= FLT_MAX)) x = __uint_as_float(0x7fffffffu);   // no infinity: NaN
+    return static_cast<uint8_t>(__nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3));
+}
+
+__device__ __forceinline__ float decode(uint8_t c) {
+    const __half_raw h = __nv_cvt_fp8_to_halfraw(c, __NV_E4M3);
+    return __half2float(__half(h));
+}
+
+// Four channels 4 * lane .. of one head row, normed and rotated.
+__device__ __forceinline__ void load_row(const RowsParams &p, const HeadRows &x, int r, int h,
+                                         int pos, bool rotate, float *y, int lane) {
+    const uint16_t *src = x.in + r * x.in_row + h * x.in_head;
+    float sq = 0.f;
+    for (int c = lane; c < kD; c += 32) {
+        const float v = bf16_lo(src[c]);
+        y[c] = v;
+        if (c < x.norm_dim) sq += v * v;
+    }
+    __syncwarp();
+    if (x.norm_dim > 0) {
+        const float inv = rsqrtf(warp_sum(sq) / static_cast<float>(x.norm_dim) + x.eps);
+        for (int c = lane; c < x.norm_dim; c += 32)
+            y[c] *= inv * (x.norm ? bf16_lo(x.norm[c]) : 1.f);
+        __syncwarp();
+    }
+    if (rotate) {
+        const int half = p.rope.rot_dim / 2;
+        for (int i = lane; i < half; i += 32) {
+            const int a = x.rot_start + (p.rope.interleaved ? 2 * i : i);
+            const int b = a + (p.rope.interleaved ? 1 : half);
+            float c, s;
+            rope_cos_sin(p.rope, i, pos, c, s);
+            const float ya = y[a], yb = y[b];
+            y[a] = ya * c - yb * s;
+            y[b] = yb * c + ya * s;
+        }
+        __syncwarp();
+    }
+}
+
+__global__ void __launch_bounds__(kThreads)
+append_fp8_kernel(const __grid_constant__ RowsParams p) {
+    __shared__ float buf[kWarps][kD];
+    __shared__ float top[kWarps];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int r = blockIdx.x, h = blockIdx.y;
+    const bool is_k = blockIdx.z == 0;
+    const HeadRows &x = is_k ? p.k : p.v;
+    const CacheOut &cache = is_k ? p.kc : p.vc;
+
+    const int b = sequence_of_row(p, r);
+    if (b < 0) return;
+    const int row0 = p.q_row_offsets ? static_cast<int>(p.q_row_offsets[b]) : r;
+    const int n = p.q_row_offsets ? static_cast<int>(p.q_row_offsets[b + 1]) - row0 : 1;
+    const uint32_t L = p.kv_len[b];
+    const long long t0 = static_cast<long long>(L) - n;   // token of the first row
+    const long long tl = t0 + (r - row0);
+    if (tl < 0 || tl >= p.max_kv_len) {
+        if (L != 0 && threadIdx.x == 0) atomicOr(p.err, kErrBadLength);
+        return;
+    }
+    const int t = static_cast<int>(tl);
+    const int first = static_cast<int>(max(t0, 0LL));
+    const int B = p.block_tokens;
+    if (t != first && t % B) return;                      // not its block's first new row
+    const int page = page_of(p, b, t);
+    if (page < 0) return;
+    const int slot = t % p.page_size;
+    const int held = t == first ? t % B : 0;              // earlier tokens of the block
+    const int count = static_cast<int>(
+        min(min(static_cast<long long>(B - t % B), static_cast<long long>(L) - t),
+            min(static_cast<long long>(p.max_kv_len) - t,
+                static_cast<long long>(p.num_rows) - r)));
+    uint8_t *dst = cache.base + page * cache.page_stride + h * cache.head_stride;
+    float *scale = cache.scale + page * cache.scale_page + (slot / B) * cache.scale_block +
+                   h * cache.scale_head;
+    const bool rotate = is_k && p.rope.rot_dim > 0;
+    float *y = buf[warp];
+
+    float amax = 0.f;
+    for (int i = warp; i < count; i += kWarps) {
+        load_row(p, x, r + i, h, p.positions ? p.positions[r + i] : t + i, rotate, y, lane);
+        for (int c = lane; c < kD; c += 32) {
+            const float a = fabsf(y[c]);
+            if (a <= FLT_MAX) amax = fmaxf(amax, a);
+        }
+        __syncwarp();
+    }
+    amax = warp_max(amax);
+    if (lane == 0) top[warp] = amax;
+    __syncthreads();
+    for (int w = 0; w < kWarps; ++w) amax = fmaxf(amax, top[w]);
+    float s = pow2i(scale_exponent(amax));
+    if (held) {
+        const float old = *scale;
+        if (s > old) {
+            const float ratio = old / s;
+            for (int i = warp; i < held; i += kWarps) {
+                uint8_t *row = dst + (slot - held + i) * cache.token_stride;
+                for (int c = lane; c < kD; c += 32) row[c] = encode(decode(row[c]) * ratio);
+            }
+        } else {
+            s = old;
+        }
+    }
+    __syncthreads();   // every thread has read the old scale
+    if (threadIdx.x == 0) *scale = s;
+    const float inv = 1.f / s;
+    for (int i = warp; i < count; i += kWarps) {
+        load_row(p, x, r + i, h, p.positions ? p.positions[r + i] : t + i, rotate, y, lane);
+        uint8_t *row = dst + (slot + i) * cache.token_stride;
+        for (int c = lane; c < kD; c += 32) row[c] = encode(y[c] * inv);
+        __syncwarp();
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_append_fp8(const RowsParams &p, cudaStream_t stream) {
+    if (p.q.heads > 0) {
+        RowsParams q = p;
+        q.k.heads = q.v.heads = 0;
+        const cudaError_t e = launch_head_rows(q, stream);
+        if (e != cudaSuccess) return e;
+    }
+    if (p.num_rows == 0) return cudaSuccess;
+    append_fp8_kernel<<<dim3(p.num_rows, p.k.heads, 2), kThreads, 0, stream>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace attn

@@ -1,0 +1,435 @@
+"""Filling a KV cache on the GPU: norm and rotation of head rows, appending to a
+bf16 cache and to a cache held in 8 bits, against 64-bit references."""
+import math
+
+import pytest
+import torch
+
+from tests import cache_ref as R
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+FP8 = torch.float8_e4m3fn
+
+
+@pytest.fixture(scope="module")
+def attn():
+    from split_flash_decoding_gb300 import build
+    build.build()
+    from split_flash_decoding_gb300 import attn as a
+    a.attn_device_error_flags(clear=True)
+    yield a
+    assert a.attn_device_error_flags(clear=True) == 0
+
+
+def randn(seed, *shape, scale=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(*shape, generator=g) * scale).to(torch.bfloat16)
+
+
+def rope_of(attn, rot, *, theta=500000.0, start=0, interleaved=False, **scaling):
+    turns, mscale = attn.rope_turns(rot, theta, **scaling)
+    return turns, attn.Rope(turns.to(DEV), interleaved=interleaved, mscale=mscale, start=start)
+
+
+# ---- norm and rotation ------------------------------------------------------
+
+# dim, rotated channels, first rotated channel, normed channels
+SHAPES = [(128, 128, 0, 128), (128, 64, 0, 0), (128, 32, 96, 128), (64, 64, 0, 64),
+          (96, 96, 0, 96), (96, 32, 64, 0), (192, 64, 128, 0), (256, 128, 0, 256),
+          (576, 64, 512, 512), (8, 8, 0, 8), (128, 20, 8, 128), (128, 2, 0, 0),
+          (1024, 1024, 0, 1024), (128, 0, 0, 128), (80, 40, 40, 80), (128, 16, 16, 64)]
+
+
+@pytest.mark.parametrize("dim,rot,start,nd", SHAPES)
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_norm_and_rotation(attn, dim, rot, start, nd, interleaved):
+    rows, hq, hkv = 37, 6, 2
+    q, k = randn(dim + rot, rows, hq, dim), randn(dim + rot + 1, rows, hkv, dim, scale=30.0)
+    qn = (1 + randn(3, nd, scale=0.2)).to(torch.bfloat16) if nd else None
+    kn = (1 + randn(4, nd, scale=0.2)).to(torch.bfloat16) if nd else None
+    pos = torch.randint(0, 1 << 20, (rows,), generator=torch.Generator().manual_seed(rot),
+                        dtype=torch.int32)
+    pos[:4] = torch.tensor([0, 1, 2 ** 31 - 1, -5], dtype=torch.int32)
+    turns, rope = rope_of(attn, rot, start=start, interleaved=interleaved, scaling="yarn",
+                          factor=4.0, original_len=4096) if rot else (None, None)
+    cu = lambda t: None if t is None else t.to(DEV)   # noqa: E731
+    qo, ko = attn.attn_qk_norm_rope(cu(q), cu(k), cu(pos), rope=rope, q_norm=cu(qn),
+                                    k_norm=cu(kn), eps=1e-5)
+    m = 1.0 if rope is None else rope.struct.mscale
+    for got, x, w, name in ((qo, q, qn, "q"), (ko, k, kn, "k")):
+        exact, err = R.head_rows(x, turns, pos, norm=w, eps=1e-5, start=start,
+                                 interleaved=interleaved, mscale=m)
+        R.assert_bf16(got, exact, err, f"{name} dim {dim} rot {rot}+{start} norm {nd}")
+
+
+@pytest.mark.parametrize("rows,hq,hkv", [(1, 32, 8), (1, 1, 0), (3, 128, 1), (300, 5, 3),
+                                         (4099, 32, 8)])
+def test_rows_and_heads(attn, rows, hq, hkv):
+    """From one head of one row to many rows, out of a packed projection."""
+    packed = randn(rows, rows, hq + 2 * hkv, 128).to(DEV)
+    q = packed[:, :hq]
+    k = packed[:, hq:hq + hkv] if hkv else None
+    pos = torch.arange(rows, dtype=torch.int32) + 131000
+    turns, rope = rope_of(attn, 128)
+    qo, ko = attn.attn_qk_norm_rope(q, k, pos.to(DEV), rope=rope)
+    assert (ko is None) == (k is None)
+    pick = torch.tensor(sorted({0, rows // 2, rows - 1}))
+    for got, x in ((qo, q), (ko, k)):
+        if x is not None:
+            exact, err = R.head_rows(x.cpu()[pick], turns, pos[pick])
+            R.assert_bf16(got.cpu()[pick], exact, err, f"rows {rows}")
+    # the other rows: each as if it came alone
+    one, _ = attn.attn_qk_norm_rope(q[rows - 1:], None, pos[rows - 1:].to(DEV), rope=rope)
+    assert torch.equal(one[0], qo[rows - 1])
+
+
+def test_in_place_and_strided(attn):
+    base = randn(5, 50, 48, 160).to(DEV)
+    turns, rope = rope_of(attn, 128, interleaved=True)
+    pos = torch.arange(50, dtype=torch.int32, device=DEV)
+    x = base[:, 8:40, 16:144]                       # channels contiguous, wide strides
+    want, _ = attn.attn_qk_norm_rope(x, None, pos, rope=rope)
+    keep = base.clone()
+    attn.attn_qk_norm_rope(x, None, pos, rope=rope, q_out=x)
+    assert torch.equal(x, want)
+    keep[:, 8:40, 16:144] = want
+    assert torch.equal(base, keep)                  # nothing beside the heads
+
+
+def test_norm_without_rotation_of_extreme_rows(attn):
+    """A row of zeros, huge and tiny rows; fp32 sums of squares must not overflow below 1e19."""
+    x = torch.zeros(5, 1, 128, dtype=torch.bfloat16)
+    x[1] = 1e18
+    x[2] = 1e-18
+    x[3, 0, 7] = 3.0
+    x[4] = -1.0
+    got, _ = attn.attn_qk_norm_rope(x.to(DEV), q_norm=torch.ones(128, dtype=torch.bfloat16,
+                                                                   device=DEV), eps=1e-6)
+    exact, err = R.head_rows(x, None, None, norm=torch.ones(128), eps=1e-6)
+    R.assert_bf16(got, exact, err, "extreme rows")
+
+
+def test_no_rows(attn):
+    q = torch.empty(0, 4, 128, dtype=torch.bfloat16, device=DEV)
+    out, _ = attn.attn_qk_norm_rope(q, None, torch.empty(0, dtype=torch.int32, device=DEV),
+                                    rope=rope_of(attn, 128)[1])
+    assert out.shape == (0, 4, 128)
+
+
+# ---- appending --------------------------------------------------------------
+
+class Pool:
+    """A paged (or contiguous) cache layout with a table of scattered pages."""
+
+    def __init__(self, lens, page, seed, spare=2, contiguous=False):
+        self.lens, self.page, self.contiguous = lens, page, contiguous
+        if contiguous:
+            self.pages, self.table = len(lens), None
+            return
+        need = [max(1, -(-x // page)) for x in lens]
+        g = torch.Generator().manual_seed(seed)
+        self.pages = sum(need) + spare
+        perm = torch.randperm(self.pages, generator=g)
+        self.table = torch.zeros(len(lens), max(need), dtype=torch.int32)
+        at = 0
+        for b, n in enumerate(need):
+            self.table[b, :n] = perm[at:at + n].to(torch.int32)
+            at += n
+
+    def place(self, b, t):
+        if self.contiguous:
+            return b, t
+        return int(self.table[b, t // self.page]), t % self.page
+
+
+def rows_of(lens, q_lens):
+    """(row, sequence, token) of every row."""
+    r = 0
+    for b, n in enumerate(q_lens):
+        for i in range(n):
+            yield r, b, lens[b] - n + i
+            r += 1
+
+
+CASES = [
+    # lens, rows per sequence (None: one each), page, contiguous
+    ([1], None, 64, False),
+    ([1, 64, 65, 128, 700, 0, 33], None, 64, False),
+    ([5, 300, 17], [5, 130, 1], 16, False),
+    ([40, 200, 9, 64], [1, 200, 9, 3], 32, True),
+    ([1000, 1, 8, 513], [600, 0, 8, 2], 128, False),
+]
+
+
+@pytest.mark.parametrize("lens,q_lens,page,contiguous", CASES)
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_append_bf16(attn, lens, q_lens, page, contiguous, interleaved):
+    hq, hkv, dim = 6, 3, 128
+    rows = sum(q_lens) if q_lens else len(lens)
+    counts = q_lens or [1] * len(lens)
+    pool = Pool(lens, 256 if contiguous else page, 3, contiguous=contiguous)
+    size = 1 + rows + 2                                       # rows behind the last sequence
+    packed = randn(rows, size if q_lens else rows, hq + 2 * hkv, dim)
+    q, k, v = packed[:, :hq], packed[:, hq:hq + hkv], packed[:, hq + hkv:]
+    kc = randn(1, pool.pages, pool.page, hkv, dim)
+    vc = randn(2, pool.pages, pool.page, hkv, dim)
+    kn = (1 + randn(4, dim, scale=0.2)).to(torch.bfloat16)
+    turns, rope = rope_of(attn, 64, start=32, interleaved=interleaved)
+    kg, vg = kc.to(DEV), vc.to(DEV)
+    pg = packed.to(DEV)
+    qo = torch.full((pg.shape[0], hq, dim), 7.0, dtype=torch.bfloat16, device=DEV)
+    offs = None
+    if q_lens:
+        offs = torch.tensor([sum(q_lens[:i]) for i in range(len(lens) + 1)], dtype=torch.int32)
+    attn.attn_append_kv(pg[:, hq:hq + hkv], pg[:, hq + hkv:], kg, vg,
+                        torch.tensor(lens, dtype=torch.int32, device=DEV), max_kv_len=max(lens),
+                        page_table=None if contiguous else pool.table.to(DEV), q=pg[:, :hq],
+                        q_out=qo, q_row_offsets=None if offs is None else offs.to(DEV), rope=rope,
+                        k_norm=kn.to(DEV))
+    torch.cuda.synchronize()
+    places = [(r, b, t) for r, b, t in rows_of(lens, counts)]
+    tokens = torch.tensor([max(t, 0) for _, _, t in places], dtype=torch.int64)
+    ke, kerr = R.head_rows(k[:rows], turns, tokens, norm=kn, start=32, interleaved=interleaved)
+    qe, qerr = R.head_rows(q[:rows], turns, tokens, start=32, interleaved=interleaved)
+    R.assert_bf16(qo[:rows], qe, qerr, "q")
+    assert (qo[rows:] == 7.0).all()
+    kh, vh = kg.cpu(), vg.cpu()
+    for r, b, t in places:
+        if t < 0:
+            continue
+        pg_, slot = pool.place(b, t)
+        R.assert_bf16(kh[pg_, slot], ke[r], kerr[r], f"k of row {r}")
+        assert torch.equal(vh[pg_, slot], v[r])
+        kh[pg_, slot], vh[pg_, slot] = kc[pg_, slot], vc[pg_, slot]
+    assert torch.equal(kh, kc) and torch.equal(vh, vc)        # nothing else was written
+
+
+def test_append_latent_rows(attn):
+    """Rows of 576 channels, 512 normed and 64 rotated, without a V cache."""
+    lens, q_lens = [70, 3, 200], [2, 1, 4]
+    pool = Pool(lens, 64, 9)
+    k, q = randn(1, 7, 1, 576), randn(2, 7, 16, 576)
+    kn = (1 + randn(4, 512, scale=0.2)).to(torch.bfloat16)
+    turns, rope = rope_of(attn, 64, start=512, interleaved=True)
+    cache = torch.zeros(pool.pages, 64, 1, 576, dtype=torch.bfloat16, device=DEV)
+    qo = attn.attn_append_kv(k.to(DEV), None, cache, None,
+                             torch.tensor(lens, dtype=torch.int32, device=DEV), max_kv_len=200,
+                             page_table=pool.table.to(DEV), q=q.to(DEV),
+                             q_row_offsets=torch.tensor([0, 2, 3, 7], dtype=torch.int32,
+                                                        device=DEV), rope=rope,
+                             k_norm=kn.to(DEV))
+    places = list(rows_of(lens, q_lens))
+    tokens = torch.tensor([t for _, _, t in places])
+    ke, kerr = R.head_rows(k, turns, tokens, norm=kn, start=512, interleaved=True)
+    qe, qerr = R.head_rows(q, turns, tokens, start=512, interleaved=True)
+    R.assert_bf16(qo, qe, qerr, "q")
+    ch = cache.cpu()
+    for r, b, t in places:
+        R.assert_bf16(ch[pool.place(b, t)], ke[r], kerr[r], f"row {r}")
+    assert int((ch.abs().sum((1, 2, 3)) > 0).sum()) <= 5
+
+
+def test_append_positions_and_bad_rows(attn):
+    """Given positions replace the tokens'; a length above the bound and a page outside the pool
+    are reported, not stored."""
+    kc = torch.zeros(4, 16, 1, 128, dtype=torch.bfloat16, device=DEV)
+    vc = torch.zeros_like(kc)
+    k, v = randn(1, 4, 1, 128).to(DEV), randn(2, 4, 1, 128).to(DEV)
+    table = torch.tensor([[0, 1], [9, 9], [2, 2], [3, 3]], dtype=torch.int32, device=DEV)
+    lens = torch.tensor([17, 3, 33, 1], dtype=torch.int32, device=DEV)
+    turns, rope = rope_of(attn, 128)
+    pos = torch.tensor([100000, 5, 6, 7], dtype=torch.int32)
+    attn.attn_append_kv(k, v, kc, vc, lens, max_kv_len=32, page_table=table, rope=rope,
+                        positions=pos.to(DEV))
+    assert attn.attn_device_error_flags(clear=True) == 6
+    exact, err = R.head_rows(k.cpu(), turns, pos)
+    R.assert_bf16(kc[1, 0], exact[0], err[0], "row 0")
+    R.assert_bf16(kc[3, 0], exact[3], err[3], "row 3")
+    assert torch.equal(vc[1, 0], v[0]) and torch.equal(vc[3, 0], v[3])
+    assert int((vc != 0).any(-1).sum()) == 2
+
+
+# ---- appending to the 8-bit cache -------------------------------------------
+
+def check_fp8(attn, lens, q_lens, page, block, seed, *, contiguous=False, magnitude=0.0, hkv=2,
+              rope_kw=None):
+    dim, hq = 128, 4
+    counts = q_lens or [1] * len(lens)
+    rows = sum(counts)
+    pool = Pool(lens, page, seed, contiguous=contiguous)
+    g = torch.Generator().manual_seed(seed)
+    scale = torch.exp2(torch.randn(rows, 1, 1, generator=g) * magnitude)
+    packed = (torch.randn(rows, hq + 2 * hkv, dim, generator=g) * scale).to(torch.bfloat16)
+    old = {}
+    for name in "kv":
+        e = torch.randint(-8, 3, (pool.pages, page // block, hkv), generator=g).float()
+        codes = (torch.randn(pool.pages, page, hkv, dim, generator=g) * 100).clamp(-448, 448)
+        old[name] = (codes.to(FP8), torch.exp2(e))
+    turns, rope = rope_of(attn, 128, **(rope_kw or {}))
+    kn = (1 + randn(4, dim, scale=0.2)).to(torch.bfloat16)
+    new = {n: (old[n][0].to(DEV), old[n][1].to(DEV)) for n in "kv"}
+    offs = None
+    if q_lens:
+        offs = torch.tensor([sum(q_lens[:i]) for i in range(len(lens) + 1)], dtype=torch.int32)
+    pg = packed.to(DEV)
+    qo = attn.attn_append_kv_fp8(
+        pg[:, hq:hq + hkv], pg[:, hq + hkv:], new["k"][0], new["v"][0], new["k"][1], new["v"][1],
+        torch.tensor(lens, dtype=torch.int32, device=DEV), max_kv_len=max(lens),
+        max_q_len=max(counts), page_table=None if contiguous else pool.table.to(DEV),
+        q=pg[:, :hq], q_row_offsets=None if offs is None else offs.to(DEV), rope=rope,
+        k_norm=kn.to(DEV))
+    torch.cuda.synchronize()
+    places = list(rows_of(lens, counts))
+    tokens = torch.tensor([max(t, 0) for _, _, t in places], dtype=torch.int64)
+    inter = bool(rope.struct.interleaved)
+    qe, qerr = R.head_rows(packed[:, :hq], turns, tokens, interleaved=inter)
+    R.assert_bf16(qo, qe, qerr, "q")
+    ke, kerr = R.head_rows(packed[:, hq:hq + hkv], turns, tokens, norm=kn, interleaved=inter)
+    rows64 = {"k": (ke, kerr), "v": (packed[:, hq + hkv:].double(),
+                                     torch.zeros(rows, hkv, dim, dtype=torch.float64))}
+    for name, (x, err) in rows64.items():
+        codes = new[name][0].cpu().float().double()
+        scales = new[name][1].cpu().double()
+        c0, s0 = old[name][0].float().double(), old[name][1].double()
+        want_codes, want_scales = c0.clone(), s0.clone()
+        blocks = {}
+        for r, b, t in places:
+            if t >= 0:
+                blocks.setdefault((b, t // block), []).append((r, t))
+        for (b, _), members in blocks.items():
+            r0, t0 = members[0]
+            pgi, slot = pool.place(b, t0)
+            blk, held = slot // block, t0 % block
+            ids = [r for r, _ in members]
+            amax = x[ids].abs().amax((0, 2))
+            slack = err[ids].amax((0, 2))
+            lo, hi = R.scale_exponents(amax - slack), R.scale_exponents(amax + slack)
+            got = torch.log2(scales[pgi, blk])
+            if held:
+                lo = torch.maximum(lo, torch.log2(s0[pgi, blk]))
+                hi = torch.maximum(hi, torch.log2(s0[pgi, blk]))
+            assert ((got >= lo) & (got <= hi)).all(), f"{name} scale of block {blk}: {got} {lo} {hi}"
+            want_scales[pgi, blk] = scales[pgi, blk]
+            s = scales[pgi, blk][:, None]
+            if held:
+                first = slot - held
+                exact = c0[pgi, first:slot] * (s0[pgi, blk][:, None] / s)
+                d = (codes[pgi, first:slot] - exact).abs()
+                assert (d <= R.half_step(exact)).all(), f"{name}: a held code"
+                want_codes[pgi, first:slot] = codes[pgi, first:slot]
+            for r, t in members:
+                p2, slot2 = pool.place(b, t)
+                d = (codes[p2, slot2] - x[r] / s).abs()
+                bound = R.half_step(x[r] / s) + err[r] / s * (1 + 2.0 ** -3)
+                assert (d <= bound).all(), f"{name}: row {r}, {(d - bound).max():.3g} above"
+                want_codes[p2, slot2] = codes[p2, slot2]
+        assert torch.equal(codes, want_codes), f"{name}: a code elsewhere changed"
+        assert torch.equal(scales, want_scales), f"{name}: a scale elsewhere changed"
+
+
+@pytest.mark.parametrize("block", [1, 2, 8, 16, 64])
+def test_append_fp8_single_rows(attn, block):
+    check_fp8(attn, [1, 64, 65, 128, 700, 0, 33, 16, 17, 2], None, 64, block, 100 + block,
+              magnitude=4.0)
+
+
+@pytest.mark.parametrize("page,block,q_lens", [
+    (16, 16, [5, 130, 1]), (128, 128, [600, 1, 8]), (64, 4, [3, 0, 200]), (32, 1, [40, 40, 40]),
+    (256, 256, [700, 300, 2]), (8, 8, [9, 17, 33]), (1024, 512, [600, 3, 200])])
+def test_append_fp8_ragged(attn, page, block, q_lens):
+    lens = [n + x for n, x in zip(q_lens, (7, 130, 70))]
+    check_fp8(attn, lens, q_lens, page, block, page + block, magnitude=2.0,
+              rope_kw=dict(interleaved=True))
+
+
+def test_append_fp8_contiguous(attn):
+    check_fp8(attn, [40, 200, 9, 255], [1, 200, 9, 3], 256, 32, 5, contiguous=True, hkv=8)
+
+
+@pytest.mark.parametrize("block", [1, 64])
+def test_append_fp8_extreme_values(attn, block):
+    """Zeros, values at the borders of a scale, the largest and least bf16 numbers, infinities and
+    NaN (which become NaN and leave the scale to the finite values)."""
+    x = torch.zeros(8, 1, 128, dtype=torch.bfloat16)
+    x[1, 0, 5] = 448.0
+    x[2, 0, 5] = 450.0
+    x[3] = 3.3e38
+    x[4, 0, 1] = 1e-38
+    x[5, 0, 3], x[5, 0, 4], x[5, 0, 5] = float("inf"), float("nan"), 2.0
+    x[6, 0, 9] = -448.0 * 2.0 ** -20
+    x[7] = float("nan")
+    cache = [torch.zeros(8, 64, 1, 128, dtype=FP8, device=DEV) for _ in range(2)]
+    scales = [torch.ones(8, 64 // block, 1, device=DEV) for _ in range(2)]
+    table = torch.arange(8, dtype=torch.int32, device=DEV)[:, None].contiguous()
+    attn.attn_append_kv_fp8(x.to(DEV), x.to(DEV), *cache, *scales,
+                            torch.ones(8, dtype=torch.int32, device=DEV), max_kv_len=64,
+                            page_table=table)
+    for c, s in zip(cache, scales):
+        codes, e = c.cpu().float()[:, 0, 0], torch.log2(s.cpu()[:, 0, 0])
+        assert e.tolist()[:5] == [-60, 0, 1, 120, -60]
+        assert e[5] == -7 and e[6] == -20 and e[7] == -60
+        assert codes[0].abs().max() == 0 and codes[1, 5] == 448 and codes[2, 5] == 224
+        assert (codes[3] - 3.3e38 / 2.0 ** 120).abs().max() <= 16
+        assert codes[4].abs().max() == 0
+        assert codes[5, 3:5].isnan().all() and codes[5, 5] == 256 and not codes[5, 6:].any()
+        assert codes[6, 9] == -448 and codes[7].isnan().all()
+
+
+def test_append_fp8_again_changes_nothing(attn):
+    """The same rows appended twice: the second call finds the scales grown and the codes placed."""
+    lens, q_lens = [70, 33, 64], [3, 1, 20]
+    pool = Pool(lens, 64, 1)
+    k, v = randn(1, 24, 2, 128, scale=9.0).to(DEV), randn(2, 24, 2, 128).to(DEV)
+    cache = [(torch.randn(pool.pages, 64, 2, 128, device=DEV) * 50).to(FP8) for _ in range(2)]
+    scales = [torch.full((pool.pages, 2, 2), 2.0 ** -9, device=DEV) for _ in range(2)]
+
+    def go():
+        attn.attn_append_kv_fp8(k, v, *cache, *scales,
+                                torch.tensor(lens, dtype=torch.int32, device=DEV), max_kv_len=70,
+                                max_q_len=20, page_table=pool.table.to(DEV),
+                                q_row_offsets=torch.tensor([0, 3, 4, 24], dtype=torch.int32,
+                                                           device=DEV))
+        return [c.view(torch.uint8).clone() for c in cache] + [s.clone() for s in scales]
+
+    for a, b in zip(go(), go()):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_append_is_captured_and_replayed(attn, fp8):
+    """A captured append replayed with other lengths and rows, on another stream."""
+    lens = torch.tensor([5, 64, 17], dtype=torch.int32, device=DEV)
+    pool = Pool([128, 128, 128], 64, 1)
+    k, v = randn(1, 3, 2, 128).to(DEV), randn(2, 3, 2, 128).to(DEV)
+    dt = FP8 if fp8 else torch.bfloat16
+    turns, rope = rope_of(attn, 128)
+    table = pool.table.to(DEV)
+
+    def make():
+        c = [torch.zeros(pool.pages, 64, 2, 128, dtype=dt, device=DEV) for _ in range(2)]
+        return c + ([torch.ones(pool.pages, 4, 2, device=DEV) for _ in range(2)] if fp8 else [])
+
+    def go(c):
+        f = attn.attn_append_kv_fp8 if fp8 else attn.attn_append_kv
+        f(k, v, *c, lens, max_kv_len=128, page_table=table, rope=rope)
+
+    c1, c2 = make(), make()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(s):
+        go(make())
+        s.synchronize()
+        with torch.cuda.graph(graph, stream=s):
+            go(c1)
+    torch.cuda.synchronize()
+    for step in range(3):
+        lens += 1
+        k.copy_(randn(10 + step, 3, 2, 128))
+        graph.replay()
+        go(c2)
+        torch.cuda.synchronize()
+    for a, b in zip(c1, c2):
+        assert torch.equal(a.view(torch.uint8) if a.dtype == FP8 else a,
+                           b.view(torch.uint8) if b.dtype == FP8 else b)
