@@ -325,7 +325,7 @@ extern "C" int attn_decode_fp8(const void *q, const attn_kv_t *k, const attn_kv_
     if (!workspace || !aligned(workspace, 256)) return ATTN_ERR_WORKSPACE;
     if ((st = device_sms(&sms))) return st;
     const int ctas = fp8_decode_ctas(sms);
-    size_t off_m, off_l, off_table;
+    size_t off_m = 0, off_l = 0, off_table = 0;
     if (workspace_bytes < fp8_layout(ctas, static_cast<long long>(batch) * hkv, &off_m, &off_l,
                                      &off_table))
         return ATTN_ERR_WORKSPACE;
@@ -350,16 +350,25 @@ extern "C" int attn_decode_fp8(const void *q, const attn_kv_t *k, const attn_kv_
     p.max_pages = k->max_pages;
     p.page_size = k->page_size;
     p.num_pages = k->num_pages;
-    p.num_partitions = max_kv_len;
     p.qk_scale_log2 = scale * 1.4426950408889634f;
-    p.k_base = kc.base;
-    p.v_base = vc.base;
-    p.k_page = kc.page_stride;
-    p.k_token = kc.token_stride;
-    p.k_head = kc.head_stride;
-    p.v_page = vc.page_stride;
-    p.v_token = vc.token_stride;
-    p.v_head = vc.head_stride;
+    // the item table counts 128-key tiles of every unit
+    p.balanced = 1;
+    p.chunk = kGqaTcTileKeys;
+    p.num_partitions = max_kv_len > 0 ? (max_kv_len + kGqaTcTileKeys - 1) / kGqaTcTileKeys : 1;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    p.ws_o = reinterpret_cast<float *>(ws);
+    p.ws_m = reinterpret_cast<float *>(ws + off_m);
+    p.ws_l = reinterpret_cast<float *>(ws + off_l);
+    p.unit_slots = reinterpret_cast<int2 *>(ws + off_table);
+    p.box_rows = k->page_table && k->page_size < kGqaTcTileKeys ? k->page_size : kGqaTcTileKeys;
+    if ((st = encode_kv_map_8bit(&p.k_map, k->base, k->token_stride, k->head_stride,
+                                 k->page_stride, head_dim, k->page_size, hkv, k->num_pages,
+                                 p.box_rows)))
+        return st;
+    if ((st = encode_kv_map_8bit(&p.v_map, v->base, v->token_stride, v->head_stride,
+                                 v->page_stride, head_dim, v->page_size, hkv, v->num_pages,
+                                 p.box_rows)))
+        return st;
     p.k_scale = k_scale->base;
     p.ks_page = k_scale->page_stride;
     p.ks_block = k_scale->block_stride;
@@ -370,5 +379,26 @@ extern "C" int attn_decode_fp8(const void *q, const attn_kv_t *k, const attn_kv_
     p.vs_head = v_scale->head_stride;
     p.block_shift = 0;
     while ((1 << p.block_shift) < k_scale->block_tokens) ++p.block_shift;
-    return map_cuda(launch_gqa_decode_fp8(p, ctas, reinterpret_cast<cudaStream_t>(stream)));
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    st = map_cuda(launch_gqa_decode_fp8(p, ctas, s));
+    // Units of one tile are never cut: nothing to merge.
+    if (st || max_kv_len <= kGqaTcTileKeys) return st;
+    ReduceParams r;
+    std::memset(&r, 0, sizeof(r));
+    r.ws_o = p.ws_o;
+    r.ws_m = p.ws_m;
+    r.ws_l = p.ws_l;
+    r.sink = sink;
+    r.out = p.out;
+    r.lse = lse;
+    r.q_row_offsets = q_row_offsets;
+    r.batch = batch;
+    r.num_partitions = ctas;   // the most pieces a unit can have
+    r.rows = num_q_rows;
+    r.num_q_heads = num_q_heads;
+    r.dim_v = head_dim;
+    r.unit_slots = p.unit_slots;
+    r.group = group;
+    r.hkv = hkv;
+    return map_cuda(launch_splitk_reduce(r, s, /*pdl=*/true));
 }

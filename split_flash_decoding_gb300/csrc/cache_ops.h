@@ -53,8 +53,6 @@ struct RowsParams {
 };
 
 struct Fp8DecodeParams : GqaParams {
-    const uint8_t *k_base, *v_base;
-    long long k_page, k_token, k_head, v_page, v_token, v_head;
     const float *k_scale, *v_scale;
     long long ks_page, ks_block, ks_head, vs_page, vs_block, vs_head;
     int block_shift;              // log2(tokens per scale)

@@ -1,111 +1,779 @@
-// gqa_decode_fp8.cu -- decode attention over a cache held in 8 bits.
+// gqa_decode_fp8.cu -- split-K decode attention over a cache held in 8 bits
+// (e4m3 codes, an fp32 scale per block of tokens and KV head), head_dim 128.
 //
-// One CTA per (query row, query head): warps take keys in turn with a running
-// maximum and sum, joined at the end.
+//   s_j = scale q . (ks_j K8_j),  p_j = e^(s_j - m)
+//   out = sum_j p_j (vs_j V8_j) / (sum_j p_j + e^(sink - m))
+//
+// The work list is the balanced split of gqa_items.cuh (the 128-key tiles of
+// every (sequence, KV head) unit dealt out in ranges of equal cost), with two
+// CTAs per SM.  Both contractions of a tile run on the codes as they are,
+// as tcgen05 kind::f8f6f4 MMAs with the keys / the channels on the 128 rows of
+// M and the folded query rows and heads on N:
+//
+//   S^T [128 keys x N] = K8 [128 keys x 128 ch] . Q^T       (K-major A, B)
+//   O^T [128 ch x N]  += V8^T [128 ch x 128 keys] . P^T     (MN-major A)
+//
+// Both operands of such an MMA are 8 bits wide, so the side that is not in the
+// cache is a sum of e4m3 terms, each in a column of its own: N is padded to 16
+// anyway, and the time of an MMA this narrow is that of reading A.
+//   q = 2^-a (q0 + q1 / 16): a puts the row's largest channel in [128, 256);
+//     8 significant bits are two terms of 4, so bf16 channels down to 2^-14 of
+//     the largest are exact and smaller ones miss at most 2^-23 of it.
+//   weights = w0 + w1 / 16 + w2 / 256, each term the rest of the one before
+//     rounded to nearest: relative 2^-12.
+// A thread owns one key of the tile (its TMEM lane), so the scales cost it two
+// multiplications: ks_j goes into the score, and V's scale into the weight.
+// With vs_j = r_j 2^(e_j) (e_j its exponent, clamped to [-64, 64]), the running
+// reference m is that of s_j + e_j, so the largest weight sits at the top of
+// the e4m3 range whatever the scales are; the row sum takes the weights
+// without 2^(e_j).  m, the sum and O keep one reference, which is what the
+// split-K reduce merges.  The reference is lazy: it follows a tile's maximum
+// only when that exceeds it by more than 2^kLazy.
+//
+// Warp roles: softmax and epilogue (four warps, or two groups of four for 16
+// columns), K producer and V producer (TMA), MMA issue, and one warp that
+// turns q into its terms and fetches the scales of each tile's keys (cp.async).
 #include <cuda_fp8.h>
 
 #include "cache_ops.h"
+#include "gqa_items.cuh"
+#include "launch.h"
 #include "ptx.cuh"
+#include "tc.cuh"
 
 namespace attn {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kD = 128;
+constexpr int kBK = kGqaTcTileKeys;          // 128 keys per tile
+constexpr int kStages = 3;
+constexpr int kTileBytes = kBK * kD;         // 16 KB
+constexpr int kScStages = 3;                 // tiles of scales in flight
+constexpr int kCtasPerSm = 2;
+constexpr float kLazy = 4.f;                 // base 2
+constexpr float kWeightTop = 8.f;            // weights reach 2^kLazy * 2 * kWeightTop = 256
+constexpr int kMinVExp = -64, kMaxVExp = 64;
 
-__device__ __forceinline__ float4 decode4(uint32_t w) {
-    const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2(w & 0xffffu, __NV_E4M3);
-    const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2(w >> 16, __NV_E4M3);
-    const float2 x = __half22float2(__half2(a)), y = __half22float2(__half2(b));
-    return make_float4(x.x, x.y, y.x, y.y);
+// Columns: NC query rows x heads, in kGroups groups of NW (one group of four
+// softmax warps each).  The S columns (and Q rows) of a group are [2][NW], its
+// O columns (and P rows) [3][NW].
+template <int NC>
+struct Cfg {
+    static constexpr int kGroups = NC > 8 ? 2 : 1;
+    static constexpr int NW = NC / kGroups;
+    static constexpr int NS = 2 * NC < 16 ? 16 : 2 * NC;             // N of the score MMA
+    static constexpr int NP = (3 * NC + 15) / 16 * 16;               // N of the output MMA
+    static constexpr int kTmemO = 2 * NS;                            // after two score buffers
+    static constexpr int kTmemCols = 2 * NS + NP <= 64 ? 64 : 128;
+    static constexpr int kQBufs = NC > 8 ? 1 : 2;
+    static constexpr int kWarpK = 4 * kGroups, kWarpV = kWarpK + 1, kWarpMma = kWarpK + 2,
+                         kWarpAux = kWarpK + 3;
+    static constexpr int kThreads = 32 * (4 * kGroups + 4);
+    // shared memory
+    static constexpr int kring = 0;
+    static constexpr int vring = kring + kStages * kTileBytes;
+    static constexpr int q = vring + kStages * kTileBytes;           // [kQBufs][NS rows][128 B]
+    static constexpr int p = q + kQBufs * NS * 128;                  // [NP rows][128 B]
+    static constexpr int sc = p + NP * 128;                          // [kScStages][128] {ks, vs}
+    static constexpr int red = sc + kScStages * kBK * 8;             // float [2][4][16] tile max
+    static constexpr int lred = red + 2 * 4 * 16 * 4;                // float [2][4][16] row sums
+    static constexpr int qf = lred + 2 * 4 * 16 * 4;                 // float [kQBufs][16] 2^-a
+    static constexpr int bars = qf + 2 * 16 * 4;
+    static constexpr int tmem_slot = bars + 240;
+    static constexpr int range = bars + 256;
+    static constexpr int items = range + 32;
+};
+
+enum Bar {
+    kKFull = 0, kKEmpty = 3, kVFull = 6, kVEmpty = 9,   // [kStages] each
+    kScFull = 12, kScEmpty = 15,                        // [kScStages] each
+    kQFull = 18, kQEmpty = 20,                          // [2] each
+    kSFull = 22, kSFree = 24,                           // [2] each
+    kPFull = 26, kODone = 27,
+    kNumBars = 28
+};
+static_assert(kStages == 3 && kScStages == 3 && kNumBars * 8 <= 240, "barrier layout");
+static_assert(sizeof(GqaRange) <= 32, "range slot");
+
+template <int NC>
+size_t smem_bytes(int batch) {
+    return 1024 + size_t(Cfg<NC>::items) + sizeof(int) * size_t(batch + 1);
 }
 
-__global__ void __launch_bounds__(kWarps * 32)
-gqa_decode_fp8_kernel(const __grid_constant__ Fp8DecodeParams p) {
-    __shared__ float sm[kWarps], sl[kWarps], so[kWarps][128];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int row = blockIdx.x, h = blockIdx.y, kvh = h / p.group;
-    int b = row, row0 = row, n = 1;
-    if (p.q_row_offsets) {
-        if (row >= static_cast<int>(p.q_row_offsets[p.batch])) return;
-        int lo = 0, hi = p.batch;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (static_cast<int>(p.q_row_offsets[mid]) <= row) lo = mid; else hi = mid;
-        }
-        b = lo;
-        row0 = p.q_row_offsets[b];
-        n = p.q_row_offsets[b + 1] - row0;
+// Instruction descriptor of kind::f8f6f4 with e4m3 A and B, fp32 accumulation.
+__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, int a_mn, int b_mn) {
+    return (1u << 4) | (uint32_t(a_mn) << 15) | (uint32_t(b_mn) << 16) | (uint32_t(N >> 3) << 17) |
+           (uint32_t(M >> 4) << 24);
+}
+
+__device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                         uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate ? 1u : 0u)
+        : "memory");
+}
+
+// N (a multiple of 4) consecutive TMEM columns of the thread's lane.
+template <int N>
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, float (&v)[N]) {
+#pragma unroll
+    for (int i = 0; i + 8 <= N; i += 8) {
+        float a[8];
+        tc::tmem_ld_n<8>(taddr + i, a);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i + j] = a[j];
     }
-    const uint32_t cap = p.num_partitions;   // max_kv_len
-    if (p.kv_len[b] > cap && threadIdx.x == 0) atomicOr(p.err, kErrBadLength);
-    const int L = static_cast<int>(min(p.kv_len[b], cap));
-    const int lim = p.causal ? min(L, L - n + (row - row0) + 1) : L;
-    const uint16_t *q = p.q + (static_cast<size_t>(row) * p.num_q_heads + h) * 128;
-    float4 qv;
-    qv.x = bf16_lo(q[4 * lane]);
-    qv.y = bf16_lo(q[4 * lane + 1]);
-    qv.z = bf16_lo(q[4 * lane + 2]);
-    qv.w = bf16_lo(q[4 * lane + 3]);
-    float m = -INFINITY, l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int t = warp; t < lim; t += kWarps) {
-        int page = b;
-        if (p.page_table) {
-            page = p.page_table[static_cast<size_t>(b) * p.max_pages + t / p.page_size];
-            if (page < 0 || page >= p.num_pages) {
-                if (lane == 0) atomicOr(p.err, kErrBadPage);
-                continue;
+    if constexpr (N % 8 != 0) {
+        float a[4];
+        tc::tmem_ld_n<4>(taddr + N - 4, a);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[N - 4 + j] = a[j];
+    }
+}
+template <int N>
+__device__ __forceinline__ void tmem_st_cols(uint32_t taddr, const float (&v)[N]) {
+#pragma unroll
+    for (int i = 0; i + 8 <= N; i += 8) {
+        float a[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) a[j] = v[i + j];
+        tc::tmem_st_n<8>(taddr + i, a);
+    }
+    if constexpr (N % 8 != 0) {
+        float a[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) a[j] = v[N - 4 + j];
+        tc::tmem_st_n<4>(taddr + N - 4, a);
+    }
+}
+
+// Maximum over the 32 lanes of the warp (NaN ignored; every lane gets it).
+__device__ __forceinline__ float warp_max_redux(float v) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+__device__ __forceinline__ float pow2i(int e) {   // -126 <= e <= 127
+    return __uint_as_float(uint32_t(e + 127) << 23);
+}
+
+// Two values to e4m3 (a in the low byte) and back.
+__device__ __forceinline__ uint32_t to_e4m3x2(float a, float b) {
+    return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+}
+__device__ __forceinline__ float2 from_e4m3x2(uint32_t c) {
+    return __half22float2(__half2(
+        __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(c), __NV_E4M3)));
+}
+
+// Byte of element (row r, byte c) of an operand of 128-byte rows, 128-byte swizzle.
+__device__ __forceinline__ uint32_t operand_offset(int r, int c) {
+    return uint32_t(r * 128 + (((c >> 4) ^ (r & 7)) << 4) + (c & 15));
+}
+
+// First query row and row count of sequence b.
+__device__ __forceinline__ void seq_rows(const GqaParams &p, int b, int &row0, int &nrows) {
+    if (p.q_row_offsets) {
+        row0 = int(p.q_row_offsets[b]);
+        nrows = int(p.q_row_offsets[b + 1]) - row0;
+    } else {
+        row0 = b;
+        nrows = 1;
+    }
+}
+
+// Page and first slot of the item's 32 row boxes from box 32 * chunk on, one
+// per lane; page -1: past the end or outside the pool.
+__device__ __forceinline__ void lookup_boxes(const GqaParams &p, const GqaItem &it, int chunk,
+                                             int lane, bool report, int &page, int &slot) {
+    const int tk = it.start + ((chunk << 5) + lane) * p.box_rows;
+    page = -1;
+    slot = 0;
+    if (tk >= it.L) return;
+    if (!p.page_table) {
+        page = it.b;
+        slot = tk;
+        return;
+    }
+    const int pidx = tk / p.page_size;
+    const int e = pidx < p.max_pages ? p.page_table[size_t(it.b) * p.max_pages + pidx] : -1;
+    if (e < 0 || e >= p.num_pages) {
+        if (report) atomicOr(p.err, kErrBadPage);
+        return;
+    }
+    page = e;
+    slot = tk % p.page_size;
+}
+
+// K or V producer: walks this CTA's items and tiles and lets lane 0 issue the
+// boxes of each tile into the ring.
+template <bool kIsK, int NC>
+__device__ __forceinline__ void produce(const Fp8DecodeParams &p, const int *cum, const GqaWalk &w,
+                                        int hkv, uint8_t *smem, uint64_t *bar, int lane) {
+    const CUtensorMap *map = kIsK ? &p.k_map : &p.v_map;
+    uint64_t *full = bar + (kIsK ? kKFull : kVFull);
+    uint64_t *empty = bar + (kIsK ? kKEmpty : kVEmpty);
+    uint8_t *ring = smem + (kIsK ? Cfg<NC>::kring : Cfg<NC>::vring);
+    if (lane == 0) prefetch_tensormap(map);
+    const int box_rows = p.box_rows;        // 128, 64, 32, 16 or 8
+    const int nb = kBK / box_rows;          // row boxes per tile
+    const uint32_t box_bytes = uint32_t(box_rows) * 128u;
+    int g = 0;
+    bool aborted = false;
+    for (int j = w.first; j < w.count && !aborted; j += w.stride) {
+        const GqaItem it = gqa_balanced_item(p, cum, hkv, w, j);
+        if (it.ntiles == 0) continue;
+        int cached = -1, my_page = -1, my_slot = 0;
+        for (int t = 0; t < it.ntiles && !aborted; ++t) {
+            const int gg = g + t;
+            const int s = gg % kStages;
+            const int key0 = it.start + t * kBK;
+            const int live = min(nb, (it.L - key0 + box_rows - 1) / box_rows);
+            if (lane == 0) {
+                if (gg >= kStages && !mbar_wait(&empty[s], ((gg / kStages) - 1) & 1, p.err))
+                    aborted = true;
+                else
+                    mbar_arrive_expect_tx(&full[s], uint32_t(live) * box_bytes);
+            }
+            aborted = __shfl_sync(0xffffffffu, aborted, 0);
+            if (aborted) break;
+            uint8_t *dst = ring + s * kTileBytes;
+            for (int r = 0; r < live; ++r) {
+                const int gb = t * nb + r;                           // box index in the item
+                if ((gb >> 5) != cached) {                           // warp-uniform refill
+                    cached = gb >> 5;
+                    lookup_boxes(p, it, cached, lane, kIsK, my_page, my_slot);
+                }
+                const int page = __shfl_sync(0xffffffffu, my_page, gb & 31);
+                const int slot = __shfl_sync(0xffffffffu, my_slot, gb & 31);
+                if (lane == 0) {
+                    if (page < 0)
+                        mbar_complete_tx(&full[s], box_bytes);       // skipped bad page
+                    else
+                        tma_load_4d(dst + r * box_bytes, map, &full[s], 0, slot, it.kvh, page);
+                }
             }
         }
-        const int slot = t % p.page_size;
-        const long long blk = slot >> p.block_shift;
-        const float4 kx = decode4(*reinterpret_cast<const uint32_t *>(
-            p.k_base + page * p.k_page + slot * p.k_token + kvh * p.k_head + 4 * lane));
-        const float4 vx = decode4(*reinterpret_cast<const uint32_t *>(
-            p.v_base + page * p.v_page + slot * p.v_token + kvh * p.v_head + 4 * lane));
-        const float ks = p.k_scale[page * p.ks_page + blk * p.ks_block + kvh * p.ks_head];
-        const float vs = p.v_scale[page * p.vs_page + blk * p.vs_block + kvh * p.vs_head];
-        const float s = warp_sum(qv.x * kx.x + qv.y * kx.y + qv.z * kx.z + qv.w * kx.w) * ks *
-                        p.qk_scale_log2;
-        const float mn = fmaxf(m, s);
-        const float a = mn == -INFINITY ? 1.f : exp2f(m - mn);
-        const float w = mn == -INFINITY ? 0.f : exp2f(s - mn);
-        m = mn;
-        l = l * a + w;
-        o.x = o.x * a + w * (vs * vx.x);
-        o.y = o.y * a + w * (vs * vx.y);
-        o.z = o.z * a + w * (vs * vx.z);
-        o.w = o.w * a + w * (vs * vx.w);
+        g += it.ntiles;
     }
-    if (lane == 0) { sm[warp] = m; sl[warp] = l; }
-    *reinterpret_cast<float4 *>(&so[warp][4 * lane]) = o;
-    __syncthreads();
-    if (threadIdx.x >= 128) return;
-    const int ch = threadIdx.x;
-    const float t2 = p.sink ? p.sink[h] * kLog2e : -INFINITY;
-    float M = t2;
-    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm[w]);
-    float Z = 0.f, acc = 0.f;
-    if (M != -INFINITY) {
-        Z = exp2f(t2 - M);
-        for (int w = 0; w < kWarps; ++w) {
-            const float f = exp2f(sm[w] - M);
-            Z += f * sl[w];
-            acc += f * so[w][ch];
+    // Every copy this warp issued must land before the CTA may leave.
+    if (lane == 0)
+        for (int i = max(0, g - kStages); i < g; ++i)
+            mbar_wait(&full[i % kStages], (i / kStages) & 1, p.err);
+}
+
+__device__ __forceinline__ void cp_async_4(void *dst, const float *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(dst)), "l"(src)
+                 : "memory");
+}
+// Arrive (without raising the pending count) when this thread's copies so far are done.
+__device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar))
+                 : "memory");
+}
+
+// Auxiliary warp: the terms of each item's queries and the scales of each
+// tile's keys.
+template <int NC>
+__device__ __forceinline__ void feed(const Fp8DecodeParams &p, const int *cum, const GqaWalk &w,
+                                     int hkv, uint8_t *smem, uint64_t *bar, int lane) {
+    using C = Cfg<NC>;
+    const int G = p.group;
+    const int nb = kBK / p.box_rows;
+    int g = 0, itq = 0;
+    bool ok = true;
+    for (int j = w.first; ok && j < w.count; j += w.stride) {
+        const GqaItem it = gqa_balanced_item(p, cum, hkv, w, j);
+        if (it.ntiles == 0) continue;
+        const int qb = itq % C::kQBufs;
+        if (itq >= C::kQBufs)
+            ok = mbar_wait(&bar[kQEmpty + qb], ((itq / C::kQBufs) - 1) & 1, p.err);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        int row0, nrows;
+        seq_rows(p, it.b, row0, nrows);
+        uint8_t *qs = smem + C::q + qb * C::NS * 128;
+        float *qf = reinterpret_cast<float *>(smem + C::qf) + qb * 16;
+        const int cols = min(min(nrows, p.num_q_rows - row0) * G, NC);
+        constexpr int kBatch = 4;   // columns whose loads are in flight together
+#pragma unroll 1
+        for (int c0 = 0; c0 < cols; c0 += kBatch) {
+            uint2 raw[kBatch];
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                const int c = min(c0 + u, cols - 1);
+                const int i = c / G, h = c - i * G;
+                raw[u] = *reinterpret_cast<const uint2 *>(
+                    p.q + (size_t(row0 + i) * p.num_q_heads + it.kvh * G + h) * kD + 4 * lane);
+            }
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                const int c = c0 + u;
+                if (c >= cols) break;
+                float x[4] = {bf16_lo(raw[u].x), bf16_hi(raw[u].x), bf16_lo(raw[u].y),
+                              bf16_hi(raw[u].y)};
+                const float top = warp_max_redux(
+                    fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3]))));
+                // 2^a * top in [128, 256) (a clamped where the factor would leave fp32)
+                const int e = int(__float_as_uint(top) >> 23) - 127;
+                const int a = min(max(7 - e, -120), 120);
+                const float f = pow2i(a);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    x[k] *= f;
+                    // an infinite channel has no e4m3 code: it becomes NaN
+                    if (!(fabsf(x[k]) < INFINITY)) x[k] = __uint_as_float(0x7fffffffu);
+                }
+                const uint32_t h0 = to_e4m3x2(x[0], x[1]), h1 = to_e4m3x2(x[2], x[3]);
+                const float2 b0 = from_e4m3x2(h0), b1 = from_e4m3x2(h1);
+                const uint32_t l0 = to_e4m3x2((x[0] - b0.x) * 16.f, (x[1] - b0.y) * 16.f);
+                const uint32_t l1 = to_e4m3x2((x[2] - b1.x) * 16.f, (x[3] - b1.y) * 16.f);
+                const int r = c / C::NW * 2 * C::NW + c % C::NW;
+                *reinterpret_cast<uint32_t *>(qs + operand_offset(r, 4 * lane)) = h0 | (h1 << 16);
+                *reinterpret_cast<uint32_t *>(qs + operand_offset(r + C::NW, 4 * lane)) =
+                    l0 | (l1 << 16);
+                if (lane == 0) qf[c] = pow2i(-a);
+            }
         }
+        tc::fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar[kQFull + qb]);
+
+        int cached = -1, my_page = -1, my_slot = 0;
+        for (int t = 0; t < it.ntiles; ++t) {
+            const int gg = g + t;
+            const int s = gg % kScStages;
+            if (gg >= kScStages)
+                ok = mbar_wait(&bar[kScEmpty + s], ((gg / kScStages) - 1) & 1, p.err);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            float2 *dst = reinterpret_cast<float2 *>(smem + C::sc) + s * kBK;
+#pragma unroll
+            for (int u = 0; u < kBK / 32; ++u) {
+                const int k = 32 * u + lane;                         // key of the tile
+                const int gb = t * nb + 32 * u / p.box_rows;         // box of lane 0's key
+                // the 32 keys of a step lie in one box, or in 32 / box_rows whole boxes
+                // from gb on; both stay inside one group of 32 boxes
+                if ((gb >> 5) != cached) {
+                    cached = gb >> 5;
+                    lookup_boxes(p, it, cached, lane, false, my_page, my_slot);
+                }
+                const int box = t * nb + k / p.box_rows;
+                const int page = __shfl_sync(0xffffffffu, my_page, box & 31);
+                const int slot = __shfl_sync(0xffffffffu, my_slot, box & 31) + k % p.box_rows;
+                if (page >= 0 && slot < p.page_size && it.start + t * kBK + k < it.L) {
+                    const long long blk = slot >> p.block_shift;
+                    cp_async_4(&dst[k].x, p.k_scale + page * p.ks_page + blk * p.ks_block +
+                                              it.kvh * p.ks_head);
+                    cp_async_4(&dst[k].y, p.v_scale + page * p.vs_page + blk * p.vs_block +
+                                              it.kvh * p.vs_head);
+                }
+            }
+            cp_async_arrive(&bar[kScFull + s]);
+        }
+        g += it.ntiles;
+        ++itq;
     }
-    const size_t at = static_cast<size_t>(row) * p.num_q_heads + h;
-    p.out[at * 128 + ch] = static_cast<uint16_t>(pack_bf16x2(Z == 0.f ? 0.f : acc / Z, 0.f));
-    if (ch == 0 && p.lse) p.lse[at] = Z == 0.f ? -INFINITY : (M + log2f(Z)) * kLn2;
+    asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+template <int NC>
+__global__ void __launch_bounds__(Cfg<NC>::kThreads, kCtasPerSm)
+gqa_decode_fp8_kernel(const __grid_constant__ Fp8DecodeParams p) {
+    using C = Cfg<NC>;
+    constexpr int NW = C::NW;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t *bar = reinterpret_cast<uint64_t *>(smem + C::bars);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::tmem_slot);
+    GqaRange *range = reinterpret_cast<GqaRange *>(smem + C::range);
+    int *cum = reinterpret_cast<int *>(smem + C::items);
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const int G = p.group;
+    const int hkv = p.num_q_heads / G;
+
+    if (warp == 0) gqa_build_items(p, hkv, cum, lane, range);
+    if (threadIdx.x == 32) {
+        for (int i = 0; i < kNumBars; ++i) {
+            uint32_t n = 1;
+            if (i == kSFree || i == kSFree + 1 || i == kPFull) n = 4 * C::kGroups;
+            if (i >= kScEmpty && i < kScEmpty + kScStages) n = 4 * C::kGroups;
+            if (i == kQEmpty || i == kQEmpty + 1) n = 4 * C::kGroups + 1;
+            if (i >= kScFull && i < kScFull + kScStages) n = 32;
+            mbar_init(&bar[i], n);
+        }
+        fence_mbar_init();
+    }
+    if (warp == C::kWarpMma) {
+        tc::tmem_alloc(tmem_slot, C::kTmemCols);
+        tc::tmem_relinquish();
+    }
+    // Rows of Q and P past the columns in use stay zero.
+    for (int i = threadIdx.x; i < (C::kQBufs * C::NS + C::NP) * 8; i += C::kThreads)
+        reinterpret_cast<uint4 *>(smem + C::q)[i] = make_uint4(0u, 0u, 0u, 0u);
+    tc::fence_async_smem();
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = *tmem_slot;
+    const GqaWalk walk = gqa_balanced_walk(*range);
+
+    if (warp == C::kWarpK) {
+        produce<true, NC>(p, cum, walk, hkv, smem, bar, lane);
+    } else if (warp == C::kWarpV) {
+        produce<false, NC>(p, cum, walk, hkv, smem, bar, lane);
+    } else if (warp == C::kWarpAux) {
+        feed<NC>(p, cum, walk, hkv, smem, bar, lane);
+    } else if (warp == C::kWarpMma) {
+        // ---------------------------------------------------------- MMA issue
+        if (lane == 0) {
+            constexpr uint32_t idesc_s = idesc_e4m3(128, C::NS, 0, 0);
+            constexpr uint32_t idesc_o = idesc_e4m3(128, C::NP, 1, 0);
+            const uint32_t k_base = smem_addr(smem + C::kring);
+            const uint32_t v_base = smem_addr(smem + C::vring);
+            const uint32_t q_base = smem_addr(smem + C::q);
+            const uint64_t pd = tc::smem_desc_sw128(smem_addr(smem + C::p), 16, 1024);
+            int g = 0, itq = 0;
+            bool ok = true;
+            for (int j = walk.first; ok && j < walk.count; j += walk.stride) {
+                const GqaItem it = gqa_balanced_item(p, cum, hkv, walk, j);
+                if (it.ntiles == 0) continue;
+                const int qb = itq % C::kQBufs;
+                ok = mbar_wait(&bar[kQFull + qb], (itq / C::kQBufs) & 1, p.err);
+                for (int t = 0; ok && t <= it.ntiles; ++t) {
+                    if (t < it.ntiles) {
+                        const int gg = g + t;
+                        const int ks = gg % kStages;
+                        const int sb = gg & 1;
+                        ok = mbar_wait(&bar[kKFull + ks], (gg / kStages) & 1, p.err);
+                        if (ok && gg >= 2)
+                            ok = mbar_wait(&bar[kSFree + sb], ((gg >> 1) - 1) & 1, p.err);
+                        if (!ok) break;
+                        tc::fence_after_sync();
+                        const uint64_t kd =
+                            tc::smem_desc_sw128(k_base + ks * kTileBytes, 16, 1024);
+                        const uint64_t qd =
+                            tc::smem_desc_sw128(q_base + qb * C::NS * 128, 16, 1024);
+#pragma unroll
+                        for (int kk = 0; kk < kD / 32; ++kk)   // 32 channels = 32 bytes a step
+                            mma_e4m3(tmem + sb * C::NS, kd + uint64_t(kk * 2), qd + uint64_t(kk * 2),
+                                     idesc_s, kk > 0);
+                        tc::mma_commit(&bar[kSFull + sb]);
+                        tc::mma_commit(&bar[kKEmpty + ks]);
+                        if (t == it.ntiles - 1) tc::mma_commit(&bar[kQEmpty + qb]);
+                    }
+                    if (t >= 1) {
+                        const int gp = g + t - 1;
+                        const int vs = gp % kStages;
+                        ok = mbar_wait(&bar[kPFull], gp & 1, p.err);
+                        if (ok) ok = mbar_wait(&bar[kVFull + vs], (gp / kStages) & 1, p.err);
+                        if (!ok) break;
+                        tc::fence_after_sync();
+                        // V^T as the MN-major A operand: 128 channels are one 128-byte
+                        // atom, 8-key groups 1 KB apart, 32 keys a step.
+                        const uint64_t vd =
+                            tc::smem_desc_sw128(v_base + vs * kTileBytes, kTileBytes, 1024);
+#pragma unroll
+                        for (int kk = 0; kk < kBK / 32; ++kk)
+                            mma_e4m3(tmem + C::kTmemO, vd + uint64_t((kk * 32 * 128) >> 4),
+                                     pd + uint64_t(kk * 2), idesc_o, t > 1 || kk > 0);
+                        tc::mma_commit(&bar[kODone]);
+                        tc::mma_commit(&bar[kVEmpty + vs]);
+                    }
+                }
+                g += it.ntiles;
+                ++itq;
+            }
+        }
+    } else {
+        // ---------------------------------------------------- softmax + epilogue
+        const int kw = warp & 3;                     // key warp: TMEM lanes 32 kw ..
+        const int grp = warp >> 2;                   // column group
+        const int cg0 = grp * NW;
+        const int k = kw * 32 + lane;                // key of the tile == TMEM lane
+        const uint32_t lane_base = uint32_t(kw * 32) << 16;
+        const uint32_t o_col = tmem + lane_base + C::kTmemO + grp * 3 * NW;
+        float *red = reinterpret_cast<float *>(smem + C::red);
+        float *lred = reinterpret_cast<float *>(smem + C::lred);
+        uint8_t *pbuf = smem + C::p;
+        int g = 0, iter = 0, itq = 0;
+        bool ok = true;
+        for (int j = walk.first; j < walk.count; j += walk.stride, ++iter) {
+            const GqaItem it = gqa_balanced_item(p, cum, hkv, walk, j);
+            int row0, nrows;
+            seq_rows(p, it.b, row0, nrows);
+            nrows = min(nrows, p.num_q_rows - row0);
+            // Column cg = (row cg / G, head cg % G): keys j < lim visible.
+            int lim[NW];
+            float f[NW], m[NW], l[NW];
+#pragma unroll
+            for (int c = 0; c < NW; ++c) {
+                const int i = (cg0 + c) / G;
+                lim[c] = i >= nrows ? 0 : (p.causal ? it.L - nrows + i + 1 : it.L);
+                m[c] = -INFINITY;
+                l[c] = 0.f;
+                f[c] = 0.f;
+            }
+            if (it.ntiles > 0) {
+                const int qb = itq % C::kQBufs;
+                ok = ok && mbar_wait(&bar[kQFull + qb], (itq / C::kQBufs) & 1, p.err);
+                const float *qf = reinterpret_cast<const float *>(smem + C::qf) + qb * 16;
+#pragma unroll
+                for (int c = 0; c < NW; ++c) f[c] = qf[cg0 + c] * p.qk_scale_log2;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar[kQEmpty + qb]);
+                ++itq;
+            }
+            // First key that some row may not see.
+            const int full = p.causal && nrows > 1 ? it.L - nrows + 1 : it.L;
+            // Every warp runs every named barrier of every tile, even after a
+            // wait gave up (ok == false), so no warp can strand the others.
+            for (int t = 0; t < it.ntiles; ++t) {
+                const int gg = g + t;
+                const int sb = gg & 1;
+                const int t0 = it.start + t * kBK;
+                const bool valid = t0 + k < it.end;
+                // ---- scales and scores of this key -------------------------------
+                const int ss = gg % kScStages;
+                ok = ok && mbar_wait(&bar[kScFull + ss], (gg / kScStages) & 1, p.err);
+                float2 sc = reinterpret_cast<const float2 *>(smem + C::sc)[ss * kBK + k];
+                if (!valid) sc = make_float2(0.f, 0.f);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar[kScEmpty + ss]);
+                const int ve = min(max(int((__float_as_uint(sc.y) >> 23) & 0xffu) - 127, kMinVExp),
+                                   kMaxVExp);
+                const float vexp = static_cast<float>(ve);
+                const float v_inv = pow2i(-ve);
+                const float v_mul = sc.y * v_inv * kWeightTop;
+                ok = ok && mbar_wait(&bar[kSFull + sb], (gg >> 1) & 1, p.err);
+                tc::fence_after_sync();
+                float raw[2 * NW];
+                tmem_ld_cols<2 * NW>(tmem + lane_base + sb * C::NS + grp * 2 * NW, raw);
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar[kSFree + sb]);
+
+                // ---- tile maximum per column across the four warps ---------------
+                float s[NW];
+                float *rb = red + (gg & 1) * 64;
+#pragma unroll
+                for (int c = 0; c < NW; ++c) {
+                    const float x = fmaf(raw[NW + c], 0.0625f, raw[c]) * sc.x;
+                    s[c] = valid && t0 + k < lim[c] ? fmaf(x, f[c], vexp) : -INFINITY;
+                    const float wm = warp_max_redux(s[c]);
+                    if (lane == 0) rb[kw * 16 + cg0 + c] = wm;
+                }
+                named_sync(1 + grp, 128);
+                float alpha[NW];
+                bool moved = false;
+#pragma unroll
+                for (int c = 0; c < NW; ++c) {
+                    const int cg = cg0 + c;
+                    const float tmax =
+                        fmaxf(fmaxf(rb[cg], rb[16 + cg]), fmaxf(rb[32 + cg], rb[48 + cg]));
+                    alpha[c] = 1.f;
+                    if (tmax > m[c] + kLazy) {   // also from -inf
+                        alpha[c] = fast_exp2(m[c] - tmax);
+                        m[c] = tmax;
+                        moved = true;
+                    }
+                }
+                float wt[NW];
+#pragma unroll
+                for (int c = 0; c < NW; ++c) {
+                    const float e = s[c] != -INFINITY ? fast_exp2(s[c] - m[c]) : 0.f;
+                    l[c] = fmaf(e, v_inv, l[c] * alpha[c]);
+                    wt[c] = e * v_mul;
+                }
+                uint32_t code[3][NW / 2];
+#pragma unroll
+                for (int c = 0; c < NW; c += 2) {
+                    float a = wt[c], b = wt[c + 1];
+#pragma unroll
+                    for (int u = 0; u < 3; ++u) {
+                        const uint32_t w2 = to_e4m3x2(a, b);
+                        code[u][c / 2] = w2;
+                        if (u < 2) {
+                            const float2 d = from_e4m3x2(w2);
+                            a = (a - d.x) * 16.f;
+                            b = (b - d.y) * 16.f;
+                        }
+                    }
+                }
+                if (t >= 1) {
+                    // O^T(t-1) is complete: P^T may be overwritten and O^T
+                    // rescaled (thread = channel lane).
+                    ok = ok && mbar_wait(&bar[kODone], (gg - 1) & 1, p.err);
+                    tc::fence_after_sync();
+                    if (moved) {   // identical in every thread of the group
+                        float o[3 * NW];
+                        tmem_ld_cols<3 * NW>(o_col, o);
+#pragma unroll
+                        for (int c = 0; c < 3 * NW; ++c) o[c] *= alpha[c % NW];
+                        tmem_st_cols<3 * NW>(o_col, o);
+                        tc::tmem_wait_st();
+                    }
+                }
+                // ---- V rows that some or all rows must not see --------------------
+                if (t0 + kBK > full) {               // uniform over the CTA
+                    const int vs = gg % kStages;
+                    ok = ok && mbar_wait(&bar[kVFull + vs], (gg / kStages) & 1, p.err);
+                    uint4 *row = reinterpret_cast<uint4 *>(smem + C::vring + vs * kTileBytes) + k * 8;
+                    bool clear = t0 + k >= it.L;     // past the end: may hold anything
+                    if (t0 + k >= full && t0 + k < it.L) {
+                        // A later token of the call: a NaN in its V must not reach the
+                        // rows before it through 0 * NaN.
+                        bool nan = false;
+#pragma unroll
+                        for (int u = 0; u < 8; ++u) {
+                            const uint4 x = row[u];
+                            const uint32_t word[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                            for (int v = 0; v < 4; ++v)
+                                nan |= __vcmpeq4(word[v] & 0x7f7f7f7fu, 0x7f7f7f7fu) != 0u;
+                        }
+                        if (nan) {
+                            clear = true;
+#pragma unroll
+                            for (int c = 0; c < NW; ++c)
+                                if (t0 + k < lim[c]) {
+                                    const uint32_t bits = 0x7fu << (8 * (c & 1));
+                                    code[0][c / 2] |= bits;
+                                }
+                        }
+                    }
+                    named_sync(3, 128 * C::kGroups);
+                    if (clear && grp == 0) {
+#pragma unroll
+                        for (int u = 0; u < 8; ++u) row[u] = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    // an e4m3 zero times the NaN weight is NaN: those rows see it
+                }
+#pragma unroll
+                for (int u = 0; u < 3; ++u)
+#pragma unroll
+                    for (int c = 0; c < NW; ++c)
+                        pbuf[operand_offset(grp * 3 * NW + u * NW + c, k)] =
+                            static_cast<uint8_t>(code[u][c / 2] >> (8 * (c & 1)));
+                tc::fence_async_smem();
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar[kPFull]);
+            }
+
+            // ---- item epilogue ----------------------------------------------------
+            // The row sums first: they do not need O, so their exchange runs
+            // while the last P.V is still in flight.
+            float lsum[NW];
+            {
+                float *lb = lred + (iter & 1) * 64;   // [4 key warps][16 columns]
+#pragma unroll
+                for (int c = 0; c < NW; ++c) {
+                    const float a = warp_sum(l[c]);
+                    if (lane == 0) lb[kw * 16 + cg0 + c] = a;
+                }
+                named_sync(1 + grp, 128);
+#pragma unroll
+                for (int c = 0; c < NW; ++c) {
+                    const int cg = cg0 + c;
+                    lsum[c] = (lb[cg] + lb[16 + cg]) + (lb[32 + cg] + lb[48 + cg]);
+                }
+            }
+            float o[3 * NW];
+            if (it.ntiles > 0)
+                ok = ok && mbar_wait(&bar[kODone], (g + it.ntiles - 1) & 1, p.err);
+            if (ok && it.ntiles > 0) {
+                tc::fence_after_sync();
+                tmem_ld_cols<3 * NW>(o_col, o);
+            } else {
+#pragma unroll
+                for (int c = 0; c < 3 * NW; ++c) o[c] = 0.f;
+            }
+            tc::fence_before_sync();
+            const int ch = k;   // output channel of this thread
+#pragma unroll
+            for (int c = 0; c < NW; ++c) {
+                const int i = (cg0 + c) / G, h = (cg0 + c) - i * G;
+                if (i >= nrows) continue;
+                const int hq = it.kvh * G + h;
+                const size_t row = size_t(row0 + i);
+                const float acc = fmaf(fmaf(o[2 * NW + c], 0.0625f, o[NW + c]), 0.0625f, o[c]) *
+                                  (1.f / kWeightTop);
+                if (it.direct) {
+                    const float t2 = p.sink ? p.sink[hq] * kLog2e : -INFINITY;
+                    const float Mf = fmaxf(m[c], t2);
+                    float so = 1.f, Z = lsum[c];       // 0 without a visible key, or NaN
+                    if (Mf != -INFINITY) {
+                        so = fast_exp2(m[c] - Mf);     // 0 when m = -inf
+                        Z = lsum[c] * so + fast_exp2(t2 - Mf);
+                    }
+                    const float v = Z == 0.f ? 0.f : acc * so / Z;
+                    p.out[(row * p.num_q_heads + hq) * kD + ch] =
+                        static_cast<uint16_t>(pack_bf16x2(v, 0.f) & 0xffffu);
+                    if (ch == 0 && p.lse)
+                        p.lse[row * p.num_q_heads + hq] =
+                            Z == 0.f ? -INFINITY : (Mf + fast_log2(Z)) * kLn2;
+                } else {
+                    const size_t base = size_t(it.part) * kGqaSlotCols + (cg0 + c);
+                    p.ws_o[base * kD + ch] = acc;
+                    if (ch == 0) {
+                        // a NaN sum must not hide behind an empty slice's -inf
+                        p.ws_m[base] = lsum[c] == lsum[c] ? m[c] * kLn2 : 0.f;
+                        p.ws_l[base] = lsum[c];
+                    }
+                }
+            }
+            if (it.first && threadIdx.x == 0) {
+                // The CTA holding the unit's first tile publishes where its
+                // pieces are (as in the bf16 kernel): slots c + unit for the
+                // CTAs c holding its first through last tile.
+                const long long last = it.unit_x + it.unit_tiles - 1 +
+                                       static_cast<long long>(kGqaUnitCost) * (it.unit + 1);
+                const int c_last = static_cast<int>(((last + 1) * walk.ctas - 1) / walk.wtiles);
+                const int c_first = static_cast<int>(blockIdx.x);
+                p.unit_slots[it.unit] = make_int2(c_first + it.unit, c_last - c_first + 1);
+            }
+            g += it.ntiles;
+        }
+        pdl_launch_dependents();
+    }
+
+    tc::fence_before_sync();
+    __syncthreads();
+    if (warp == C::kWarpMma) {
+        tc::fence_after_sync();
+        tc::tmem_dealloc(tmem, C::kTmemCols);
+    }
+}
+
+template <int NC>
+cudaError_t launch_nc(const Fp8DecodeParams &p, int ctas, cudaStream_t stream) {
+    const size_t smem = smem_bytes<NC>(p.batch);
+    auto kern = gqa_decode_fp8_kernel<NC>;
+    const cudaError_t e =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    if (e != cudaSuccess) return e;
+    kern<<<dim3(static_cast<unsigned>(ctas)), Cfg<NC>::kThreads, smem, stream>>>(p);
+    return cudaGetLastError();
 }
 
 }  // namespace
 
-int fp8_decode_ctas(int num_sms) { return num_sms; }
+int fp8_decode_ctas(int num_sms) { return kCtasPerSm * num_sms; }
 
-cudaError_t launch_gqa_decode_fp8(const Fp8DecodeParams &p, int, cudaStream_t stream) {
-    gqa_decode_fp8_kernel<<<dim3(p.num_q_rows, p.num_q_heads), kWarps * 32, 0, stream>>>(p);
-    return cudaGetLastError();
+cudaError_t launch_gqa_decode_fp8(const Fp8DecodeParams &p, int ctas, cudaStream_t stream) {
+    const int cols = p.max_q_len * p.group;
+    if (cols < 1 || cols > 16) return cudaErrorInvalidValue;
+    if (cols <= 4) return launch_nc<4>(p, ctas, stream);
+    if (cols <= 8) return launch_nc<8>(p, ctas, stream);
+    return launch_nc<16>(p, ctas, stream);
 }
 
 }  // namespace attn

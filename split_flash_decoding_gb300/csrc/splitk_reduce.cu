@@ -56,12 +56,14 @@ __device__ __forceinline__ int locate_partials(const ReduceParams &p, int row, i
     if (p.unit_slots) {
         // Balanced GQA split: the unit's partials sit in consecutive slots of
         // 16 columns (query row within the sequence x head within the group).
+        if (p.q_row_offsets && row >= int(p.q_row_offsets[p.batch])) return -1;   // no sequence's
         const int b = row_sequence(p, row);
         const int first_row = p.q_row_offsets ? int(p.q_row_offsets[b]) : b;
         const int2 e = p.unit_slots[b * p.hkv + h / p.group];
-        if (e.y == 1) return -1;
+        const int col = (row - first_row) * p.group + h % p.group;
+        if (e.y == 1 || col >= kGqaSlotCols) return -1;
         stride_p = kGqaSlotCols;
-        widx0 = static_cast<size_t>(e.x) * kGqaSlotCols + (row - first_row) * p.group + h % p.group;
+        widx0 = static_cast<size_t>(e.x) * kGqaSlotCols + col;
         return e.y;
     }
     if (p.kv_len) {
