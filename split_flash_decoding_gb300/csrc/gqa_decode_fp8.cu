@@ -48,10 +48,11 @@ constexpr int kD = 128;
 constexpr int kBK = kGqaTcTileKeys;          // 128 keys per tile
 constexpr int kStages = 3;
 constexpr int kTileBytes = kBK * kD;         // 16 KB
-constexpr int kScStages = 3;                 // tiles of scales in flight
+constexpr int kMaxScStages = 6;
 constexpr int kCtasPerSm = 2;
 constexpr float kLazy = 4.f;                 // base 2
 constexpr float kWeightTop = 8.f;            // weights reach 2^kLazy * 2 * kWeightTop = 256
+constexpr int kBarBytes = 304;
 constexpr int kMinVExp = -64, kMaxVExp = 64;
 
 // Columns: NC query rows x heads, in kGroups groups of NW (one group of four
@@ -66,6 +67,7 @@ struct Cfg {
     static constexpr int kTmemO = 2 * NS;                            // after two score buffers
     static constexpr int kTmemCols = 2 * NS + NP <= 64 ? 64 : 128;
     static constexpr int kQBufs = NC > 8 ? 1 : 2;
+    static constexpr int kScStages = NC > 8 ? 4 : kMaxScStages;      // tiles of scales in flight
     static constexpr int kWarpK = 4 * kGroups, kWarpV = kWarpK + 1, kWarpMma = kWarpK + 2,
                          kWarpAux = kWarpK + 3;
     static constexpr int kThreads = 32 * (4 * kGroups + 4);
@@ -79,20 +81,20 @@ struct Cfg {
     static constexpr int lred = red + 2 * 4 * 16 * 4;                // float [2][4][16] row sums
     static constexpr int qf = lred + 2 * 4 * 16 * 4;                 // float [kQBufs][16] 2^-a
     static constexpr int bars = qf + 2 * 16 * 4;
-    static constexpr int tmem_slot = bars + 240;
-    static constexpr int range = bars + 256;
+    static constexpr int tmem_slot = bars + kBarBytes;
+    static constexpr int range = tmem_slot + 16;
     static constexpr int items = range + 32;
 };
 
 enum Bar {
     kKFull = 0, kKEmpty = 3, kVFull = 6, kVEmpty = 9,   // [kStages] each
-    kScFull = 12, kScEmpty = 15,                        // [kScStages] each
-    kQFull = 18, kQEmpty = 20,                          // [2] each
-    kSFull = 22, kSFree = 24,                           // [2] each
-    kPFull = 26, kODone = 27,
-    kNumBars = 28
+    kScFull = 12, kScEmpty = 12 + kMaxScStages,         // [kScStages] each
+    kQFull = 12 + 2 * kMaxScStages, kQEmpty = kQFull + 2,   // [2] each
+    kSFull = kQEmpty + 2, kSFree = kSFull + 2,          // [2] each
+    kPFull = kSFree + 2, kODone = kPFull + 1,
+    kNumBars = kODone + 1
 };
-static_assert(kStages == 3 && kScStages == 3 && kNumBars * 8 <= 240, "barrier layout");
+static_assert(kStages == 3 && kNumBars * 8 <= kBarBytes, "barrier layout");
 static_assert(sizeof(GqaRange) <= 32, "range slot");
 
 template <int NC>
@@ -283,7 +285,8 @@ __device__ __forceinline__ void feed(const Fp8DecodeParams &p, const int *cum, c
                                      int hkv, uint8_t *smem, uint64_t *bar, int lane) {
     using C = Cfg<NC>;
     const int G = p.group;
-    const int nb = kBK / p.box_rows;
+    const int box_shift = 31 - __clz(p.box_rows);   // a power of two
+    const int nb_shift = 7 - box_shift;             // boxes per tile
     int g = 0, itq = 0;
     bool ok = true;
     for (int j = w.first; ok && j < w.count; j += w.stride) {
@@ -343,34 +346,34 @@ __device__ __forceinline__ void feed(const Fp8DecodeParams &p, const int *cum, c
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar[kQFull + qb]);
 
+        // One box per lane and refill, as in the producers; the 32 keys of a step
+        // lie in one box or in whole boxes, within one refill.
+        const float *ksp = p.k_scale + it.kvh * p.ks_head;
+        const float *vsp = p.v_scale + it.kvh * p.vs_head;
         int cached = -1, my_page = -1, my_slot = 0;
         for (int t = 0; t < it.ntiles; ++t) {
             const int gg = g + t;
-            const int s = gg % kScStages;
-            if (gg >= kScStages)
-                ok = mbar_wait(&bar[kScEmpty + s], ((gg / kScStages) - 1) & 1, p.err);
+            const int s = gg % C::kScStages;
+            const int left = it.L - (it.start + t * kBK);            // keys of the tile on
+            if (gg >= C::kScStages)
+                ok = mbar_wait(&bar[kScEmpty + s], ((gg / C::kScStages) - 1) & 1, p.err);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
-            float2 *dst = reinterpret_cast<float2 *>(smem + C::sc) + s * kBK;
+            float2 *dst = reinterpret_cast<float2 *>(smem + C::sc) + s * kBK + lane;
 #pragma unroll
             for (int u = 0; u < kBK / 32; ++u) {
                 const int k = 32 * u + lane;                         // key of the tile
-                const int gb = t * nb + 32 * u / p.box_rows;         // box of lane 0's key
-                // the 32 keys of a step lie in one box, or in 32 / box_rows whole boxes
-                // from gb on; both stay inside one group of 32 boxes
-                if ((gb >> 5) != cached) {
-                    cached = gb >> 5;
+                const int box = (t << nb_shift) + (k >> box_shift);
+                if ((box >> 5) != cached) {                          // uniform: see above
+                    cached = box >> 5;
                     lookup_boxes(p, it, cached, lane, false, my_page, my_slot);
                 }
-                const int box = t * nb + k / p.box_rows;
-                const int page = __shfl_sync(0xffffffffu, my_page, box & 31);
-                const int slot = __shfl_sync(0xffffffffu, my_slot, box & 31) + k % p.box_rows;
-                if (page >= 0 && slot < p.page_size && it.start + t * kBK + k < it.L) {
+                const int page = __shfl_sync(0xffffffffu, my_page, box);
+                const int slot = __shfl_sync(0xffffffffu, my_slot, box) + (k & (p.box_rows - 1));
+                if (page >= 0 && slot < p.page_size && k < left) {
                     const long long blk = slot >> p.block_shift;
-                    cp_async_4(&dst[k].x, p.k_scale + page * p.ks_page + blk * p.ks_block +
-                                              it.kvh * p.ks_head);
-                    cp_async_4(&dst[k].y, p.v_scale + page * p.vs_page + blk * p.vs_block +
-                                              it.kvh * p.vs_head);
+                    cp_async_4(&dst[32 * u].x, ksp + page * p.ks_page + blk * p.ks_block);
+                    cp_async_4(&dst[32 * u].y, vsp + page * p.vs_page + blk * p.vs_block);
                 }
             }
             cp_async_arrive(&bar[kScFull + s]);
@@ -404,9 +407,9 @@ gqa_decode_fp8_kernel(const __grid_constant__ Fp8DecodeParams p) {
         for (int i = 0; i < kNumBars; ++i) {
             uint32_t n = 1;
             if (i == kSFree || i == kSFree + 1 || i == kPFull) n = 4 * C::kGroups;
-            if (i >= kScEmpty && i < kScEmpty + kScStages) n = 4 * C::kGroups;
+            if (i >= kScEmpty && i < kScEmpty + kMaxScStages) n = 4 * C::kGroups;
             if (i == kQEmpty || i == kQEmpty + 1) n = 4 * C::kGroups + 1;
-            if (i >= kScFull && i < kScFull + kScStages) n = 32;
+            if (i >= kScFull && i < kScFull + kMaxScStages) n = 32;
             mbar_init(&bar[i], n);
         }
         fence_mbar_init();
@@ -503,6 +506,7 @@ gqa_decode_fp8_kernel(const __grid_constant__ Fp8DecodeParams p) {
         float *red = reinterpret_cast<float *>(smem + C::red);
         float *lred = reinterpret_cast<float *>(smem + C::lred);
         uint8_t *pbuf = smem + C::p;
+        const int g_inv = (1 << 16) / G + 1;         // (cg * g_inv) >> 16 = cg / G for cg < 16
         int g = 0, iter = 0, itq = 0;
         bool ok = true;
         for (int j = walk.first; j < walk.count; j += walk.stride, ++iter) {
@@ -510,13 +514,12 @@ gqa_decode_fp8_kernel(const __grid_constant__ Fp8DecodeParams p) {
             int row0, nrows;
             seq_rows(p, it.b, row0, nrows);
             nrows = min(nrows, p.num_q_rows - row0);
-            // Column cg = (row cg / G, head cg % G): keys j < lim visible.
-            int lim[NW];
+            // Column cg = (row cg / G, head cg % G).
+            // Columns past the item's rows hold an earlier item's scores and are
+            // never written out.
             float f[NW], m[NW], l[NW];
 #pragma unroll
             for (int c = 0; c < NW; ++c) {
-                const int i = (cg0 + c) / G;
-                lim[c] = i >= nrows ? 0 : (p.causal ? it.L - nrows + i + 1 : it.L);
                 m[c] = -INFINITY;
                 l[c] = 0.f;
                 f[c] = 0.f;
@@ -531,8 +534,13 @@ gqa_decode_fp8_kernel(const __grid_constant__ Fp8DecodeParams p) {
                 if (lane == 0) mbar_arrive(&bar[kQEmpty + qb]);
                 ++itq;
             }
-            // First key that some row may not see.
-            const int full = p.causal && nrows > 1 ? it.L - nrows + 1 : it.L;
+            // First key that some row may not see: row i sees keys j < full + i (all
+            // L without the causal mask).
+            const bool masked_rows = p.causal && nrows > 1;
+            const int full = masked_rows ? it.L - nrows + 1 : it.L;
+            const auto sees = [&](int c, int key) {
+                return !masked_rows || key < full + (((cg0 + c) * g_inv) >> 16);
+            };
             // Every warp runs every named barrier of every tile, even after a
             // wait gave up (ok == false), so no warp can strand the others.
             for (int t = 0; t < it.ntiles; ++t) {
@@ -541,8 +549,8 @@ gqa_decode_fp8_kernel(const __grid_constant__ Fp8DecodeParams p) {
                 const int t0 = it.start + t * kBK;
                 const bool valid = t0 + k < it.end;
                 // ---- scales and scores of this key -------------------------------
-                const int ss = gg % kScStages;
-                ok = ok && mbar_wait(&bar[kScFull + ss], (gg / kScStages) & 1, p.err);
+                const int ss = gg % C::kScStages;
+                ok = ok && mbar_wait(&bar[kScFull + ss], (gg / C::kScStages) & 1, p.err);
                 float2 sc = reinterpret_cast<const float2 *>(smem + C::sc)[ss * kBK + k];
                 if (!valid) sc = make_float2(0.f, 0.f);
                 __syncwarp();
@@ -566,7 +574,8 @@ gqa_decode_fp8_kernel(const __grid_constant__ Fp8DecodeParams p) {
 #pragma unroll
                 for (int c = 0; c < NW; ++c) {
                     const float x = fmaf(raw[NW + c], 0.0625f, raw[c]) * sc.x;
-                    s[c] = valid && t0 + k < lim[c] ? fmaf(x, f[c], vexp) : -INFINITY;
+                    s[c] = valid ? fmaf(x, f[c], vexp) : -INFINITY;
+                    if (t0 + kBK > full && !sees(c, t0 + k)) s[c] = -INFINITY;
                     const float wm = warp_max_redux(s[c]);
                     if (lane == 0) rb[kw * 16 + cg0 + c] = wm;
                 }
@@ -643,7 +652,7 @@ gqa_decode_fp8_kernel(const __grid_constant__ Fp8DecodeParams p) {
                             clear = true;
 #pragma unroll
                             for (int c = 0; c < NW; ++c)
-                                if (t0 + k < lim[c]) {
+                                if (sees(c, t0 + k)) {
                                     const uint32_t bits = 0x7fu << (8 * (c & 1));
                                     code[0][c / 2] |= bits;
                                 }
@@ -700,7 +709,7 @@ gqa_decode_fp8_kernel(const __grid_constant__ Fp8DecodeParams p) {
             const int ch = k;   // output channel of this thread
 #pragma unroll
             for (int c = 0; c < NW; ++c) {
-                const int i = (cg0 + c) / G, h = (cg0 + c) - i * G;
+                const int i = ((cg0 + c) * g_inv) >> 16, h = (cg0 + c) - i * G;
                 if (i >= nrows) continue;
                 const int hq = it.kvh * G + h;
                 const size_t row = size_t(row0 + i);
