@@ -57,7 +57,7 @@ constexpr int kMinVExp = -64, kMaxVExp = 64;
 
 // Columns: NC query rows x heads, in kGroups groups of NW (one group of four
 // softmax warps each).  The S columns (and Q rows) of a group are [2][NW], its
-// O columns (and P rows) [3][NW].
+// O columns (and P columns) [3][NW].
 template <int NC>
 struct Cfg {
     static constexpr int kGroups = NC > 8 ? 2 : 1;
@@ -75,10 +75,10 @@ struct Cfg {
     static constexpr int kring = 0;
     static constexpr int vring = kring + kStages * kTileBytes;
     static constexpr int q = vring + kStages * kTileBytes;           // [kQBufs][NS rows][128 B]
-    static constexpr int p = q + kQBufs * NS * 128;                  // [NP rows][128 B]
+    static constexpr int p = q + kQBufs * NS * 128;                  // [NP / 16][128 keys][16 B]
     static constexpr int sc = p + NP * 128;                          // [kScStages][128] {ks, vs}
-    static constexpr int red = sc + kScStages * kBK * 8;             // float [2][4][16] tile max
-    static constexpr int lred = red + 2 * 4 * 16 * 4;                // float [2][4][16] row sums
+    static constexpr int red = sc + kScStages * kBK * 8;             // float [4][16] tile max
+    static constexpr int lred = red + 4 * 16 * 4;                // float [2][4][16] row sums
     static constexpr int qf = lred + 2 * 4 * 16 * 4;                 // float [kQBufs][16] 2^-a
     static constexpr int bars = qf + 2 * 16 * 4;
     static constexpr int tmem_slot = bars + kBarBytes;
@@ -116,6 +116,16 @@ __device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint6
         "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
         "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate ? 1u : 0u)
         : "memory");
+}
+
+// Shared-memory matrix descriptor without a swizzle; lbo/sbo in bytes.
+__device__ __forceinline__ uint64_t smem_desc_plain(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+    uint64_t d = 0;
+    d |= uint64_t((saddr & 0x3FFFFu) >> 4);
+    d |= uint64_t((lbo >> 4) & 0x3FFFu) << 16;
+    d |= uint64_t((sbo >> 4) & 0x3FFFu) << 32;
+    d |= uint64_t(1) << 46;
+    return d;
 }
 
 // N (a multiple of 4) consecutive TMEM columns of the thread's lane.
@@ -159,6 +169,20 @@ __device__ __forceinline__ float warp_max_redux(float v) {
     return r;
 }
 
+// Named barrier over a subset of warps that returns the OR of their predicates.
+__device__ __forceinline__ bool named_or(int id, int threads, bool pred) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %3, 0;\n\t"
+        "barrier.cta.red.or.pred q, %1, %2, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(id), "r"(threads), "r"(pred ? 1u : 0u)
+        : "memory");
+    return r != 0;
+}
+
 __device__ __forceinline__ float pow2i(int e) {   // -126 <= e <= 127
     return __uint_as_float(uint32_t(e + 127) << 23);
 }
@@ -175,6 +199,34 @@ __device__ __forceinline__ float2 from_e4m3x2(uint32_t c) {
 // Byte of element (row r, byte c) of an operand of 128-byte rows, 128-byte swizzle.
 __device__ __forceinline__ uint32_t operand_offset(int r, int c) {
     return uint32_t(r * 128 + (((c >> 4) ^ (r & 7)) << 4) + (c & 15));
+}
+
+// A key's weights (three terms of NW columns, two to a word) into the P operand:
+// MN-major without a swizzle, i.e. blocks of 16 columns, in each 16 bytes per
+// key, so a key's columns are one to three vector stores without a conflict.
+template <int NC>
+__device__ __forceinline__ void store_weights(uint8_t *pbuf, int grp, int k,
+                                              const uint32_t (&code)[3][Cfg<NC>::NW / 2]) {
+    constexpr int NW = Cfg<NC>::NW;
+    if constexpr (NW == 4) {
+        *reinterpret_cast<uint4 *>(pbuf + 16 * k) =
+            make_uint4(code[0][0] | (code[0][1] << 16), code[1][0] | (code[1][1] << 16),
+                       code[2][0] | (code[2][1] << 16), 0u);
+    } else {
+        uint2 x[3];
+#pragma unroll
+        for (int u = 0; u < 3; ++u)
+            x[u] = make_uint2(code[u][0] | (code[u][1] << 16), code[u][2] | (code[u][3] << 16));
+        constexpr int kBlock = kBK * 16;
+        if (grp == 0) {     // columns 0 .. 23
+            *reinterpret_cast<uint4 *>(pbuf + 16 * k) = make_uint4(x[0].x, x[0].y, x[1].x, x[1].y);
+            *reinterpret_cast<uint2 *>(pbuf + kBlock + 16 * k) = x[2];
+        } else {            // columns 24 .. 47
+            *reinterpret_cast<uint2 *>(pbuf + kBlock + 16 * k + 8) = x[0];
+            *reinterpret_cast<uint4 *>(pbuf + 2 * kBlock + 16 * k) =
+                make_uint4(x[1].x, x[1].y, x[2].x, x[2].y);
+        }
+    }
 }
 
 // First query row and row count of sequence b.
@@ -438,11 +490,12 @@ gqa_decode_fp8_kernel(const __grid_constant__ Fp8DecodeParams p) {
         // ---------------------------------------------------------- MMA issue
         if (lane == 0) {
             constexpr uint32_t idesc_s = idesc_e4m3(128, C::NS, 0, 0);
-            constexpr uint32_t idesc_o = idesc_e4m3(128, C::NP, 1, 0);
+            constexpr uint32_t idesc_o = idesc_e4m3(128, C::NP, 1, 1);
             const uint32_t k_base = smem_addr(smem + C::kring);
             const uint32_t v_base = smem_addr(smem + C::vring);
             const uint32_t q_base = smem_addr(smem + C::q);
-            const uint64_t pd = tc::smem_desc_sw128(smem_addr(smem + C::p), 16, 1024);
+            // 8-key groups 128 bytes apart, 16-column blocks kBK * 16
+            const uint64_t pd = smem_desc_plain(smem_addr(smem + C::p), 128, kBK * 16);
             int g = 0, itq = 0;
             bool ok = true;
             for (int j = walk.first; ok && j < walk.count; j += walk.stride) {
@@ -486,7 +539,8 @@ gqa_decode_fp8_kernel(const __grid_constant__ Fp8DecodeParams p) {
 #pragma unroll
                         for (int kk = 0; kk < kBK / 32; ++kk)
                             mma_e4m3(tmem + C::kTmemO, vd + uint64_t((kk * 32 * 128) >> 4),
-                                     pd + uint64_t(kk * 2), idesc_o, t > 1 || kk > 0);
+                                     pd + uint64_t((kk * 32 * 16) >> 4), idesc_o,
+                                     t > 1 || kk > 0);
                         tc::mma_commit(&bar[kODone]);
                         tc::mma_commit(&bar[kVEmpty + vs]);
                     }
@@ -568,37 +622,45 @@ gqa_decode_fp8_kernel(const __grid_constant__ Fp8DecodeParams p) {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar[kSFree + sb]);
 
-                // ---- tile maximum per column across the four warps ---------------
                 float s[NW];
-                float *rb = red + (gg & 1) * 64;
+                bool above = false;
 #pragma unroll
                 for (int c = 0; c < NW; ++c) {
                     const float x = fmaf(raw[NW + c], 0.0625f, raw[c]) * sc.x;
                     s[c] = valid ? fmaf(x, f[c], vexp) : -INFINITY;
                     if (t0 + kBK > full && !sees(c, t0 + k)) s[c] = -INFINITY;
-                    const float wm = warp_max_redux(s[c]);
-                    if (lane == 0) rb[kw * 16 + cg0 + c] = wm;
+                    above |= s[c] > m[c] + kLazy;   // also from -inf
                 }
-                named_sync(1 + grp, 128);
+                // ---- does any column's reference have to move? --------------------
+                // One barrier with an OR answers for the group; the columns' maxima
+                // are only taken where it says yes (the first tile and a few more).
+                const bool moved = named_or(1 + grp, 128, above);
                 float alpha[NW];
-                bool moved = false;
+                if (moved) {
 #pragma unroll
-                for (int c = 0; c < NW; ++c) {
-                    const int cg = cg0 + c;
-                    const float tmax =
-                        fmaxf(fmaxf(rb[cg], rb[16 + cg]), fmaxf(rb[32 + cg], rb[48 + cg]));
-                    alpha[c] = 1.f;
-                    if (tmax > m[c] + kLazy) {   // also from -inf
-                        alpha[c] = fast_exp2(m[c] - tmax);
-                        m[c] = tmax;
-                        moved = true;
+                    for (int c = 0; c < NW; ++c) {
+                        const float wm = warp_max_redux(s[c]);
+                        if (lane == 0) red[kw * 16 + cg0 + c] = wm;
+                    }
+                    named_sync(1 + grp, 128);
+#pragma unroll
+                    for (int c = 0; c < NW; ++c) {
+                        const int cg = cg0 + c;
+                        const float tmax = fmaxf(fmaxf(red[cg], red[16 + cg]),
+                                                 fmaxf(red[32 + cg], red[48 + cg]));
+                        alpha[c] = 1.f;
+                        if (tmax > m[c] + kLazy) {
+                            alpha[c] = fast_exp2(m[c] - tmax);
+                            m[c] = tmax;
+                            l[c] *= alpha[c];
+                        }
                     }
                 }
                 float wt[NW];
 #pragma unroll
                 for (int c = 0; c < NW; ++c) {
                     const float e = s[c] != -INFINITY ? fast_exp2(s[c] - m[c]) : 0.f;
-                    l[c] = fmaf(e, v_inv, l[c] * alpha[c]);
+                    l[c] = fmaf(e, v_inv, l[c]);
                     wt[c] = e * v_mul;
                 }
                 uint32_t code[3][NW / 2];
@@ -665,12 +727,7 @@ gqa_decode_fp8_kernel(const __grid_constant__ Fp8DecodeParams p) {
                     }
                     // an e4m3 zero times the NaN weight is NaN: those rows see it
                 }
-#pragma unroll
-                for (int u = 0; u < 3; ++u)
-#pragma unroll
-                    for (int c = 0; c < NW; ++c)
-                        pbuf[operand_offset(grp * 3 * NW + u * NW + c, k)] =
-                            static_cast<uint8_t>(code[u][c / 2] >> (8 * (c & 1)));
+                store_weights<NC>(pbuf, grp, k, code);
                 tc::fence_async_smem();
                 tc::fence_before_sync();
                 __syncwarp();
