@@ -344,17 +344,15 @@ extern "C" int attn_decode_fp8(const void *q, const attn_kv_t *k, const attn_kv_
     p.num_q_rows = num_q_rows;
     p.num_q_heads = num_q_heads;
     p.group = group;
-    p.head_dim = head_dim;
     p.max_q_len = max_q_len;
     p.causal = causal ? 1 : 0;
     p.max_pages = k->max_pages;
     p.page_size = k->page_size;
     p.num_pages = k->num_pages;
     p.qk_scale_log2 = scale * 1.4426950408889634f;
-    // the item table counts 128-key tiles of every unit
-    p.balanced = 1;
-    p.chunk = kGqaTcTileKeys;
-    p.num_partitions = max_kv_len > 0 ? (max_kv_len + kGqaTcTileKeys - 1) / kGqaTcTileKeys : 1;
+    p.max_kv_len = max_kv_len;
+    while (p.head_shift < 3 && hkv % (2 << p.head_shift) == 0) ++p.head_shift;
+    p.head_groups = hkv >> p.head_shift;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     p.ws_o = reinterpret_cast<float *>(ws);
     p.ws_m = reinterpret_cast<float *>(ws + off_m);

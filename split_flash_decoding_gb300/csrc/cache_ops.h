@@ -52,7 +52,25 @@ struct RowsParams {
     unsigned *err;
 };
 
-struct Fp8DecodeParams : GqaParams {
+struct Fp8DecodeParams {
+    CUtensorMap k_map, v_map;     // 4-D: (channel, slot, kv head, page)
+    const uint16_t *q;            // bf16 [rows][Hq][128]
+    const uint32_t *kv_len;       // [batch]
+    const uint32_t *q_row_offsets;  // [batch + 1], or nullptr: row b is sequence b
+    const int32_t *page_table;    // [batch][max_pages] or nullptr
+    const float *sink;            // [Hq] or nullptr
+    float *ws_o, *ws_m, *ws_l;    // partial slots: [16 columns][128], [16], [16]
+    int2 *unit_slots;             // [batch * kv heads] {first slot, pieces} for the reduce
+    uint16_t *out;                // bf16 [rows][Hq][128]
+    float *lse;                   // [rows][Hq] or nullptr
+    unsigned *err;
+    int batch, num_q_rows, num_q_heads, group, max_q_len, max_kv_len;
+    int causal;
+    int max_pages, page_size, num_pages;
+    int box_rows;                 // tokens per TMA box (min(128, page size))
+    int head_shift;               // log2 of the KV heads that a group of CTAs walks side by side
+    int head_groups;              // KV heads >> head_shift
+    float qk_scale_log2;          // scale * log2(e)
     const float *k_scale, *v_scale;
     long long ks_page, ks_block, ks_head, vs_page, vs_block, vs_head;
     int block_shift;              // log2(tokens per scale)

@@ -4,9 +4,9 @@
 //   s_j = scale q . (ks_j K8_j),  p_j = e^(s_j - m)
 //   out = sum_j p_j (vs_j V8_j) / (sum_j p_j + e^(sink - m))
 //
-// The work list is the balanced split of gqa_items.cuh (the 128-key tiles of
-// every (sequence, KV head) unit dealt out in ranges of equal cost), with two
-// CTAs per SM.  Both contractions of a tile run on the codes as they are,
+// The work list is the balanced split of fp8_items.cuh (the 128-key tiles of
+// the sequences dealt out in ranges of equal cost, KV heads side by side), with
+// two CTAs per SM.  Both contractions of a tile run on the codes as they are,
 // as tcgen05 kind::f8f6f4 MMAs with the keys / the channels on the 128 rows of
 // M and the folded query rows and heads on N:
 //
@@ -36,8 +36,7 @@
 #include <cuda_fp8.h>
 
 #include "cache_ops.h"
-#include "gqa_items.cuh"
-#include "launch.h"
+#include "fp8_items.cuh"
 #include "ptx.cuh"
 #include "tc.cuh"
 
@@ -95,7 +94,7 @@ enum Bar {
     kNumBars = kODone + 1
 };
 static_assert(kStages == 3 && kNumBars * 8 <= kBarBytes, "barrier layout");
-static_assert(sizeof(GqaRange) <= 32, "range slot");
+static_assert(sizeof(Fp8Range) <= 32, "range slot");
 
 template <int NC>
 size_t smem_bytes(int batch) {
@@ -230,7 +229,7 @@ __device__ __forceinline__ void store_weights(uint8_t *pbuf, int grp, int k,
 }
 
 // First query row and row count of sequence b.
-__device__ __forceinline__ void seq_rows(const GqaParams &p, int b, int &row0, int &nrows) {
+__device__ __forceinline__ void seq_rows(const Fp8DecodeParams &p, int b, int &row0, int &nrows) {
     if (p.q_row_offsets) {
         row0 = int(p.q_row_offsets[b]);
         nrows = int(p.q_row_offsets[b + 1]) - row0;
@@ -242,7 +241,7 @@ __device__ __forceinline__ void seq_rows(const GqaParams &p, int b, int &row0, i
 
 // Page and first slot of the item's 32 row boxes from box 32 * chunk on, one
 // per lane; page -1: past the end or outside the pool.
-__device__ __forceinline__ void lookup_boxes(const GqaParams &p, const GqaItem &it, int chunk,
+__device__ __forceinline__ void lookup_boxes(const Fp8DecodeParams &p, const Fp8Item &it, int chunk,
                                              int lane, bool report, int &page, int &slot) {
     const int tk = it.start + ((chunk << 5) + lane) * p.box_rows;
     page = -1;
@@ -266,8 +265,8 @@ __device__ __forceinline__ void lookup_boxes(const GqaParams &p, const GqaItem &
 // K or V producer: walks this CTA's items and tiles and lets lane 0 issue the
 // boxes of each tile into the ring.
 template <bool kIsK, int NC>
-__device__ __forceinline__ void produce(const Fp8DecodeParams &p, const int *cum, const GqaWalk &w,
-                                        int hkv, uint8_t *smem, uint64_t *bar, int lane) {
+__device__ __forceinline__ void produce(const Fp8DecodeParams &p, const int *cum, const Fp8Range &w,
+                                        uint8_t *smem, uint64_t *bar, int lane) {
     const CUtensorMap *map = kIsK ? &p.k_map : &p.v_map;
     uint64_t *full = bar + (kIsK ? kKFull : kVFull);
     uint64_t *empty = bar + (kIsK ? kKEmpty : kVEmpty);
@@ -278,8 +277,8 @@ __device__ __forceinline__ void produce(const Fp8DecodeParams &p, const int *cum
     const uint32_t box_bytes = uint32_t(box_rows) * 128u;
     int g = 0;
     bool aborted = false;
-    for (int j = w.first; j < w.count && !aborted; j += w.stride) {
-        const GqaItem it = gqa_balanced_item(p, cum, hkv, w, j);
+    for (int j = 0; j < w.count && !aborted; ++j) {
+        const Fp8Item it = fp8_item(p, cum, w, j);
         if (it.ntiles == 0) continue;
         int cached = -1, my_page = -1, my_slot = 0;
         for (int t = 0; t < it.ntiles && !aborted; ++t) {
@@ -333,16 +332,16 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
 // Auxiliary warp: the terms of each item's queries and the scales of each
 // tile's keys.
 template <int NC>
-__device__ __forceinline__ void feed(const Fp8DecodeParams &p, const int *cum, const GqaWalk &w,
-                                     int hkv, uint8_t *smem, uint64_t *bar, int lane) {
+__device__ __forceinline__ void feed(const Fp8DecodeParams &p, const int *cum, const Fp8Range &w,
+                                     uint8_t *smem, uint64_t *bar, int lane) {
     using C = Cfg<NC>;
     const int G = p.group;
     const int box_shift = 31 - __clz(p.box_rows);   // a power of two
     const int nb_shift = 7 - box_shift;             // boxes per tile
     int g = 0, itq = 0;
     bool ok = true;
-    for (int j = w.first; ok && j < w.count; j += w.stride) {
-        const GqaItem it = gqa_balanced_item(p, cum, hkv, w, j);
+    for (int j = 0; ok && j < w.count; ++j) {
+        const Fp8Item it = fp8_item(p, cum, w, j);
         if (it.ntiles == 0) continue;
         const int qb = itq % C::kQBufs;
         if (itq >= C::kQBufs)
@@ -446,15 +445,14 @@ gqa_decode_fp8_kernel(const __grid_constant__ Fp8DecodeParams p) {
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t *bar = reinterpret_cast<uint64_t *>(smem + C::bars);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::tmem_slot);
-    GqaRange *range = reinterpret_cast<GqaRange *>(smem + C::range);
+    Fp8Range *range = reinterpret_cast<Fp8Range *>(smem + C::range);
     int *cum = reinterpret_cast<int *>(smem + C::items);
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     const int G = p.group;
-    const int hkv = p.num_q_heads / G;
 
-    if (warp == 0) gqa_build_items(p, hkv, cum, lane, range);
+    if (warp == 0) fp8_build_items(p, cum, lane, range);
     if (threadIdx.x == 32) {
         for (int i = 0; i < kNumBars; ++i) {
             uint32_t n = 1;
@@ -478,14 +476,14 @@ gqa_decode_fp8_kernel(const __grid_constant__ Fp8DecodeParams p) {
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = *tmem_slot;
-    const GqaWalk walk = gqa_balanced_walk(*range);
+    const Fp8Range walk = *range;
 
     if (warp == C::kWarpK) {
-        produce<true, NC>(p, cum, walk, hkv, smem, bar, lane);
+        produce<true, NC>(p, cum, walk, smem, bar, lane);
     } else if (warp == C::kWarpV) {
-        produce<false, NC>(p, cum, walk, hkv, smem, bar, lane);
+        produce<false, NC>(p, cum, walk, smem, bar, lane);
     } else if (warp == C::kWarpAux) {
-        feed<NC>(p, cum, walk, hkv, smem, bar, lane);
+        feed<NC>(p, cum, walk, smem, bar, lane);
     } else if (warp == C::kWarpMma) {
         // ---------------------------------------------------------- MMA issue
         if (lane == 0) {
@@ -498,8 +496,8 @@ gqa_decode_fp8_kernel(const __grid_constant__ Fp8DecodeParams p) {
             const uint64_t pd = smem_desc_plain(smem_addr(smem + C::p), 128, kBK * 16);
             int g = 0, itq = 0;
             bool ok = true;
-            for (int j = walk.first; ok && j < walk.count; j += walk.stride) {
-                const GqaItem it = gqa_balanced_item(p, cum, hkv, walk, j);
+            for (int j = 0; ok && j < walk.count; ++j) {
+                const Fp8Item it = fp8_item(p, cum, walk, j);
                 if (it.ntiles == 0) continue;
                 const int qb = itq % C::kQBufs;
                 ok = mbar_wait(&bar[kQFull + qb], (itq / C::kQBufs) & 1, p.err);
@@ -563,8 +561,8 @@ gqa_decode_fp8_kernel(const __grid_constant__ Fp8DecodeParams p) {
         const int g_inv = (1 << 16) / G + 1;         // (cg * g_inv) >> 16 = cg / G for cg < 16
         int g = 0, iter = 0, itq = 0;
         bool ok = true;
-        for (int j = walk.first; j < walk.count; j += walk.stride, ++iter) {
-            const GqaItem it = gqa_balanced_item(p, cum, hkv, walk, j);
+        for (int j = 0; j < walk.count; ++j, ++iter) {
+            const Fp8Item it = fp8_item(p, cum, walk, j);
             int row0, nrows;
             seq_rows(p, it.b, row0, nrows);
             nrows = min(nrows, p.num_q_rows - row0);
@@ -787,7 +785,7 @@ gqa_decode_fp8_kernel(const __grid_constant__ Fp8DecodeParams p) {
                         p.lse[row * p.num_q_heads + hq] =
                             Z == 0.f ? -INFINITY : (Mf + fast_log2(Z)) * kLn2;
                 } else {
-                    const size_t base = size_t(it.part) * kGqaSlotCols + (cg0 + c);
+                    const size_t base = size_t(it.slot) * kGqaSlotCols + (cg0 + c);
                     p.ws_o[base * kD + ch] = acc;
                     if (ch == 0) {
                         // a NaN sum must not hide behind an empty slice's -inf
@@ -796,16 +794,10 @@ gqa_decode_fp8_kernel(const __grid_constant__ Fp8DecodeParams p) {
                     }
                 }
             }
-            if (it.first && threadIdx.x == 0) {
-                // The CTA holding the unit's first tile publishes where its
-                // pieces are (as in the bf16 kernel): slots c + unit for the
-                // CTAs c holding its first through last tile.
-                const long long last = it.unit_x + it.unit_tiles - 1 +
-                                       static_cast<long long>(kGqaUnitCost) * (it.unit + 1);
-                const int c_last = static_cast<int>(((last + 1) * walk.ctas - 1) / walk.wtiles);
-                const int c_first = static_cast<int>(blockIdx.x);
-                p.unit_slots[it.unit] = make_int2(c_first + it.unit, c_last - c_first + 1);
-            }
+            // The CTA holding the unit's first tile publishes where its pieces are.
+            if (it.first && threadIdx.x == 0)
+                p.unit_slots[it.b * (p.num_q_heads / G) + it.kvh] =
+                    make_int2(it.slot, fp8_pieces(p, walk, it));
             g += it.ntiles;
         }
         pdl_launch_dependents();
