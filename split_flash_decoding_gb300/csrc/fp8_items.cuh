@@ -23,7 +23,7 @@
 
 namespace attn {
 
-constexpr int kUnitCost = 2;
+constexpr int kUnitCost = 4;
 
 struct Fp8Range {
     int x0, x1;            // this group's tiles of the concatenation

@@ -54,19 +54,21 @@ constexpr float kWeightTop = 8.f;            // weights reach 2^kLazy * 2 * kWei
 constexpr int kBarBytes = 304;
 constexpr int kMinVExp = -64, kMaxVExp = 64;
 
-// Columns: NC query rows x heads, in kGroups groups of NW (one group of four
-// softmax warps each).  The S columns (and Q rows) of a group are [2][NW], its
-// O columns (and P columns) [3][NW].
+// Columns (query rows x heads) come in chunks of four: a chunk's S columns (and Q
+// rows) are [2 terms][4], its O columns (and P columns) [3 terms][4] and four
+// unused ones.  Sixteen columns take two groups of four softmax warps; group g
+// has the chunks g, g + 2.  Chunks past an item's columns are skipped.
 template <int NC>
 struct Cfg {
+    static constexpr int kChunks = NC / 4;
     static constexpr int kGroups = NC > 8 ? 2 : 1;
-    static constexpr int NW = NC / kGroups;
-    static constexpr int NS = 2 * NC < 16 ? 16 : 2 * NC;             // N of the score MMA
-    static constexpr int NP = (3 * NC + 15) / 16 * 16;               // N of the output MMA
+    static constexpr int NCH = kChunks / kGroups;                    // chunks per group
+    static constexpr int NS = kChunks < 2 ? 16 : 8 * kChunks;        // N of the score MMA
+    static constexpr int NP = 16 * kChunks;                          // N of the output MMA
     static constexpr int kTmemO = 2 * NS;                            // after two score buffers
     static constexpr int kTmemCols = 2 * NS + NP <= 64 ? 64 : 128;
     static constexpr int kQBufs = NC > 8 ? 1 : 2;
-    static constexpr int kScStages = NC > 8 ? 4 : kMaxScStages;      // tiles of scales in flight
+    static constexpr int kScStages = NC > 8 ? 3 : kMaxScStages;      // tiles of scales in flight
     static constexpr int kWarpK = 4 * kGroups, kWarpV = kWarpK + 1, kWarpMma = kWarpK + 2,
                          kWarpAux = kWarpK + 3;
     static constexpr int kThreads = 32 * (4 * kGroups + 4);
@@ -74,10 +76,10 @@ struct Cfg {
     static constexpr int kring = 0;
     static constexpr int vring = kring + kStages * kTileBytes;
     static constexpr int q = vring + kStages * kTileBytes;           // [kQBufs][NS rows][128 B]
-    static constexpr int p = q + kQBufs * NS * 128;                  // [NP / 16][128 keys][16 B]
+    static constexpr int p = q + kQBufs * NS * 128;                  // [chunks][128 keys][16 B]
     static constexpr int sc = p + NP * 128;                          // [kScStages][128] {ks, vs}
     static constexpr int red = sc + kScStages * kBK * 8;             // float [4][16] tile max
-    static constexpr int lred = red + 4 * 16 * 4;                // float [2][4][16] row sums
+    static constexpr int lred = red + 4 * 16 * 4;                    // float [2][4][16] row sums
     static constexpr int qf = lred + 2 * 4 * 16 * 4;                 // float [kQBufs][16] 2^-a
     static constexpr int bars = qf + 2 * 16 * 4;
     static constexpr int tmem_slot = bars + kBarBytes;
@@ -98,7 +100,7 @@ static_assert(sizeof(Fp8Range) <= 32, "range slot");
 
 template <int NC>
 size_t smem_bytes(int batch) {
-    return 1024 + size_t(Cfg<NC>::items) + sizeof(int) * size_t(batch + 1);
+    return size_t(Cfg<NC>::items) + sizeof(int) * size_t(batch + 1);
 }
 
 // Instruction descriptor of kind::f8f6f4 with e4m3 A and B, fp32 accumulation.
@@ -198,34 +200,6 @@ __device__ __forceinline__ float2 from_e4m3x2(uint32_t c) {
 // Byte of element (row r, byte c) of an operand of 128-byte rows, 128-byte swizzle.
 __device__ __forceinline__ uint32_t operand_offset(int r, int c) {
     return uint32_t(r * 128 + (((c >> 4) ^ (r & 7)) << 4) + (c & 15));
-}
-
-// A key's weights (three terms of NW columns, two to a word) into the P operand:
-// MN-major without a swizzle, i.e. blocks of 16 columns, in each 16 bytes per
-// key, so a key's columns are one to three vector stores without a conflict.
-template <int NC>
-__device__ __forceinline__ void store_weights(uint8_t *pbuf, int grp, int k,
-                                              const uint32_t (&code)[3][Cfg<NC>::NW / 2]) {
-    constexpr int NW = Cfg<NC>::NW;
-    if constexpr (NW == 4) {
-        *reinterpret_cast<uint4 *>(pbuf + 16 * k) =
-            make_uint4(code[0][0] | (code[0][1] << 16), code[1][0] | (code[1][1] << 16),
-                       code[2][0] | (code[2][1] << 16), 0u);
-    } else {
-        uint2 x[3];
-#pragma unroll
-        for (int u = 0; u < 3; ++u)
-            x[u] = make_uint2(code[u][0] | (code[u][1] << 16), code[u][2] | (code[u][3] << 16));
-        constexpr int kBlock = kBK * 16;
-        if (grp == 0) {     // columns 0 .. 23
-            *reinterpret_cast<uint4 *>(pbuf + 16 * k) = make_uint4(x[0].x, x[0].y, x[1].x, x[1].y);
-            *reinterpret_cast<uint2 *>(pbuf + kBlock + 16 * k) = x[2];
-        } else {            // columns 24 .. 47
-            *reinterpret_cast<uint2 *>(pbuf + kBlock + 16 * k + 8) = x[0];
-            *reinterpret_cast<uint4 *>(pbuf + 2 * kBlock + 16 * k) =
-                make_uint4(x[1].x, x[1].y, x[2].x, x[2].y);
-        }
-    }
 }
 
 // First query row and row count of sequence b.
@@ -386,9 +360,9 @@ __device__ __forceinline__ void feed(const Fp8DecodeParams &p, const int *cum, c
                 const float2 b0 = from_e4m3x2(h0), b1 = from_e4m3x2(h1);
                 const uint32_t l0 = to_e4m3x2((x[0] - b0.x) * 16.f, (x[1] - b0.y) * 16.f);
                 const uint32_t l1 = to_e4m3x2((x[2] - b1.x) * 16.f, (x[3] - b1.y) * 16.f);
-                const int r = c / C::NW * 2 * C::NW + c % C::NW;
+                const int r = (c >> 2) * 8 + (c & 3);
                 *reinterpret_cast<uint32_t *>(qs + operand_offset(r, 4 * lane)) = h0 | (h1 << 16);
-                *reinterpret_cast<uint32_t *>(qs + operand_offset(r + C::NW, 4 * lane)) =
+                *reinterpret_cast<uint32_t *>(qs + operand_offset(r + 4, 4 * lane)) =
                     l0 | (l1 << 16);
                 if (lane == 0) qf[c] = pow2i(-a);
             }
@@ -439,10 +413,8 @@ template <int NC>
 __global__ void __launch_bounds__(Cfg<NC>::kThreads, kCtasPerSm)
 gqa_decode_fp8_kernel(const __grid_constant__ Fp8DecodeParams p) {
     using C = Cfg<NC>;
-    constexpr int NW = C::NW;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>(
-        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    constexpr int NCH = C::NCH;
+    extern __shared__ __align__(1024) uint8_t smem[];
     uint64_t *bar = reinterpret_cast<uint64_t *>(smem + C::bars);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::tmem_slot);
     Fp8Range *range = reinterpret_cast<Fp8Range *>(smem + C::range);
@@ -492,7 +464,8 @@ gqa_decode_fp8_kernel(const __grid_constant__ Fp8DecodeParams p) {
             const uint32_t k_base = smem_addr(smem + C::kring);
             const uint32_t v_base = smem_addr(smem + C::vring);
             const uint32_t q_base = smem_addr(smem + C::q);
-            // 8-key groups 128 bytes apart, 16-column blocks kBK * 16
+            // MN-major without a swizzle: 16 bytes per key, 8-key groups 128 bytes
+            // apart, 16-column blocks kBK * 16
             const uint64_t pd = smem_desc_plain(smem_addr(smem + C::p), 128, kBK * 16);
             int g = 0, itq = 0;
             bool ok = true;
@@ -551,13 +524,10 @@ gqa_decode_fp8_kernel(const __grid_constant__ Fp8DecodeParams p) {
         // ---------------------------------------------------- softmax + epilogue
         const int kw = warp & 3;                     // key warp: TMEM lanes 32 kw ..
         const int grp = warp >> 2;                   // column group
-        const int cg0 = grp * NW;
         const int k = kw * 32 + lane;                // key of the tile == TMEM lane
         const uint32_t lane_base = uint32_t(kw * 32) << 16;
-        const uint32_t o_col = tmem + lane_base + C::kTmemO + grp * 3 * NW;
         float *red = reinterpret_cast<float *>(smem + C::red);
         float *lred = reinterpret_cast<float *>(smem + C::lred);
-        uint8_t *pbuf = smem + C::p;
         const int g_inv = (1 << 16) / G + 1;         // (cg * g_inv) >> 16 = cg / G for cg < 16
         int g = 0, iter = 0, itq = 0;
         bool ok = true;
@@ -566,22 +536,28 @@ gqa_decode_fp8_kernel(const __grid_constant__ Fp8DecodeParams p) {
             int row0, nrows;
             seq_rows(p, it.b, row0, nrows);
             nrows = min(nrows, p.num_q_rows - row0);
-            // Column cg = (row cg / G, head cg % G).
-            // Columns past the item's rows hold an earlier item's scores and are
-            // never written out.
-            float f[NW], m[NW], l[NW];
+            // Column cg = (row cg / G, head cg % G); chunk h of this group holds the
+            // columns col(h) .. col(h) + 3.  Columns past the item's rows hold an
+            // earlier item's scores and are never written out.
+            const auto col = [&](int h) { return 4 * (h * C::kGroups + grp); };
+            const int cols = nrows * G;
+            float f[NCH][4], m[NCH][4], l[NCH][4];
 #pragma unroll
-            for (int c = 0; c < NW; ++c) {
-                m[c] = -INFINITY;
-                l[c] = 0.f;
-                f[c] = 0.f;
-            }
+            for (int h = 0; h < NCH; ++h)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    m[h][c] = -INFINITY;
+                    l[h][c] = 0.f;
+                    f[h][c] = 0.f;
+                }
             if (it.ntiles > 0) {
                 const int qb = itq % C::kQBufs;
                 ok = ok && mbar_wait(&bar[kQFull + qb], (itq / C::kQBufs) & 1, p.err);
                 const float *qf = reinterpret_cast<const float *>(smem + C::qf) + qb * 16;
 #pragma unroll
-                for (int c = 0; c < NW; ++c) f[c] = qf[cg0 + c] * p.qk_scale_log2;
+                for (int h = 0; h < NCH; ++h)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) f[h][c] = qf[col(h) + c] * p.qk_scale_log2;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar[kQEmpty + qb]);
                 ++itq;
@@ -590,8 +566,8 @@ gqa_decode_fp8_kernel(const __grid_constant__ Fp8DecodeParams p) {
             // L without the causal mask).
             const bool masked_rows = p.causal && nrows > 1;
             const int full = masked_rows ? it.L - nrows + 1 : it.L;
-            const auto sees = [&](int c, int key) {
-                return !masked_rows || key < full + (((cg0 + c) * g_inv) >> 16);
+            const auto sees = [&](int cg, int key) {
+                return !masked_rows || key < full + ((cg * g_inv) >> 16);
             };
             // Every warp runs every named barrier of every tile, even after a
             // wait gave up (ok == false), so no warp can strand the others.
@@ -602,77 +578,101 @@ gqa_decode_fp8_kernel(const __grid_constant__ Fp8DecodeParams p) {
                 const bool valid = t0 + k < it.end;
                 // ---- scales and scores of this key -------------------------------
                 const int ss = gg % C::kScStages;
-                ok = ok && mbar_wait(&bar[kScFull + ss], (gg / C::kScStages) & 1, p.err);
+                // both polls in flight together
+                const bool sc_in = mbar_try_wait(&bar[kScFull + ss], (gg / C::kScStages) & 1);
+                const bool s_in = mbar_try_wait(&bar[kSFull + sb], (gg >> 1) & 1);
+                if (!sc_in)
+                    ok = ok && mbar_wait(&bar[kScFull + ss], (gg / C::kScStages) & 1, p.err);
                 float2 sc = reinterpret_cast<const float2 *>(smem + C::sc)[ss * kBK + k];
-                if (!valid) sc = make_float2(0.f, 0.f);
+                if (!s_in) ok = ok && mbar_wait(&bar[kSFull + sb], (gg >> 1) & 1, p.err);
+                tc::fence_after_sync();
+                float s[NCH][4];
+#pragma unroll
+                for (int h = 0; h < NCH; ++h) {
+                    if (col(h) >= cols) continue;
+                    float raw[8];
+                    tc::tmem_ld_n<8>(tmem + lane_base + sb * C::NS + 2 * col(h), raw);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) s[h][c] = fmaf(raw[4 + c], 0.0625f, raw[c]);
+                }
+                tc::fence_before_sync();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bar[kScEmpty + ss]);
+                if (lane == 0) {
+                    mbar_arrive(&bar[kSFree + sb]);
+                    mbar_arrive(&bar[kScEmpty + ss]);
+                }
+                if (!valid) sc = make_float2(0.f, 0.f);
                 const int ve = min(max(int((__float_as_uint(sc.y) >> 23) & 0xffu) - 127, kMinVExp),
                                    kMaxVExp);
                 const float vexp = static_cast<float>(ve);
                 const float v_inv = pow2i(-ve);
                 const float v_mul = sc.y * v_inv * kWeightTop;
-                ok = ok && mbar_wait(&bar[kSFull + sb], (gg >> 1) & 1, p.err);
-                tc::fence_after_sync();
-                float raw[2 * NW];
-                tmem_ld_cols<2 * NW>(tmem + lane_base + sb * C::NS + grp * 2 * NW, raw);
-                tc::fence_before_sync();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar[kSFree + sb]);
-
-                float s[NW];
                 bool above = false;
 #pragma unroll
-                for (int c = 0; c < NW; ++c) {
-                    const float x = fmaf(raw[NW + c], 0.0625f, raw[c]) * sc.x;
-                    s[c] = valid ? fmaf(x, f[c], vexp) : -INFINITY;
-                    if (t0 + kBK > full && !sees(c, t0 + k)) s[c] = -INFINITY;
-                    above |= s[c] > m[c] + kLazy;   // also from -inf
+                for (int h = 0; h < NCH; ++h) {
+                    if (col(h) >= cols) continue;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        s[h][c] = valid ? fmaf(s[h][c] * sc.x, f[h][c], vexp) : -INFINITY;
+                        if (t0 + kBK > full && !sees(col(h) + c, t0 + k)) s[h][c] = -INFINITY;
+                        above |= s[h][c] > m[h][c] + kLazy;   // also from -inf
+                    }
                 }
                 // ---- does any column's reference have to move? --------------------
                 // One barrier with an OR answers for the group; the columns' maxima
                 // are only taken where it says yes (the first tile and a few more).
                 const bool moved = named_or(1 + grp, 128, above);
-                float alpha[NW];
+                float alpha[NCH][4];
                 if (moved) {
 #pragma unroll
-                    for (int c = 0; c < NW; ++c) {
-                        const float wm = warp_max_redux(s[c]);
-                        if (lane == 0) red[kw * 16 + cg0 + c] = wm;
+                    for (int h = 0; h < NCH; ++h) {
+                        if (col(h) >= cols) continue;
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            const float wm = warp_max_redux(s[h][c]);
+                            if (lane == 0) red[kw * 16 + col(h) + c] = wm;
+                        }
                     }
                     named_sync(1 + grp, 128);
 #pragma unroll
-                    for (int c = 0; c < NW; ++c) {
-                        const int cg = cg0 + c;
-                        const float tmax = fmaxf(fmaxf(red[cg], red[16 + cg]),
-                                                 fmaxf(red[32 + cg], red[48 + cg]));
-                        alpha[c] = 1.f;
-                        if (tmax > m[c] + kLazy) {
-                            alpha[c] = fast_exp2(m[c] - tmax);
-                            m[c] = tmax;
-                            l[c] *= alpha[c];
+                    for (int h = 0; h < NCH; ++h) {
+                        if (col(h) >= cols) continue;
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            const int cg = col(h) + c;
+                            const float tmax = fmaxf(fmaxf(red[cg], red[16 + cg]),
+                                                     fmaxf(red[32 + cg], red[48 + cg]));
+                            alpha[h][c] = 1.f;
+                            if (tmax > m[h][c] + kLazy) {
+                                alpha[h][c] = fast_exp2(m[h][c] - tmax);
+                                m[h][c] = tmax;
+                                l[h][c] *= alpha[h][c];
+                            }
                         }
                     }
                 }
-                float wt[NW];
+                uint32_t code[NCH][3];   // four columns of a term to a word
 #pragma unroll
-                for (int c = 0; c < NW; ++c) {
-                    const float e = s[c] != -INFINITY ? fast_exp2(s[c] - m[c]) : 0.f;
-                    l[c] = fmaf(e, v_inv, l[c]);
-                    wt[c] = e * v_mul;
-                }
-                uint32_t code[3][NW / 2];
+                for (int h = 0; h < NCH; ++h) {
+                    if (col(h) >= cols) continue;
+                    float w[4];
 #pragma unroll
-                for (int c = 0; c < NW; c += 2) {
-                    float a = wt[c], b = wt[c + 1];
+                    for (int c = 0; c < 4; ++c) {
+                        const float e =
+                            s[h][c] != -INFINITY ? fast_exp2(s[h][c] - m[h][c]) : 0.f;
+                        l[h][c] = fmaf(e, v_inv, l[h][c]);
+                        w[c] = e * v_mul;
+                    }
 #pragma unroll
                     for (int u = 0; u < 3; ++u) {
-                        const uint32_t w2 = to_e4m3x2(a, b);
-                        code[u][c / 2] = w2;
+                        const uint32_t lo = to_e4m3x2(w[0], w[1]), hi = to_e4m3x2(w[2], w[3]);
+                        code[h][u] = lo | (hi << 16);
                         if (u < 2) {
-                            const float2 d = from_e4m3x2(w2);
-                            a = (a - d.x) * 16.f;
-                            b = (b - d.y) * 16.f;
+                            const float2 a = from_e4m3x2(lo), b = from_e4m3x2(hi);
+                            w[0] = (w[0] - a.x) * 16.f;
+                            w[1] = (w[1] - a.y) * 16.f;
+                            w[2] = (w[2] - b.x) * 16.f;
+                            w[3] = (w[3] - b.y) * 16.f;
                         }
                     }
                 }
@@ -682,11 +682,16 @@ gqa_decode_fp8_kernel(const __grid_constant__ Fp8DecodeParams p) {
                     ok = ok && mbar_wait(&bar[kODone], (gg - 1) & 1, p.err);
                     tc::fence_after_sync();
                     if (moved) {   // identical in every thread of the group
-                        float o[3 * NW];
-                        tmem_ld_cols<3 * NW>(o_col, o);
 #pragma unroll
-                        for (int c = 0; c < 3 * NW; ++c) o[c] *= alpha[c % NW];
-                        tmem_st_cols<3 * NW>(o_col, o);
+                        for (int h = 0; h < NCH; ++h) {
+                            if (col(h) >= cols) continue;
+                            float o[12];
+                            const uint32_t oc = tmem + lane_base + C::kTmemO + 4 * col(h);
+                            tmem_ld_cols<12>(oc, o);
+#pragma unroll
+                            for (int c = 0; c < 12; ++c) o[c] *= alpha[h][c & 3];
+                            tmem_st_cols<12>(oc, o);
+                        }
                         tc::tmem_wait_st();
                     }
                 }
@@ -698,7 +703,8 @@ gqa_decode_fp8_kernel(const __grid_constant__ Fp8DecodeParams p) {
                     bool clear = t0 + k >= it.L;     // past the end: may hold anything
                     if (t0 + k >= full && t0 + k < it.L) {
                         // A later token of the call: a NaN in its V must not reach the
-                        // rows before it through 0 * NaN.
+                        // rows before it through 0 * NaN.  Its V becomes 0 and its
+                        // weight NaN for the rows that do see it.
                         bool nan = false;
 #pragma unroll
                         for (int u = 0; u < 8; ++u) {
@@ -711,11 +717,11 @@ gqa_decode_fp8_kernel(const __grid_constant__ Fp8DecodeParams p) {
                         if (nan) {
                             clear = true;
 #pragma unroll
-                            for (int c = 0; c < NW; ++c)
-                                if (sees(c, t0 + k)) {
-                                    const uint32_t bits = 0x7fu << (8 * (c & 1));
-                                    code[0][c / 2] |= bits;
-                                }
+                            for (int h = 0; h < NCH; ++h)
+#pragma unroll
+                                for (int c = 0; c < 4; ++c)
+                                    if (col(h) < cols && sees(col(h) + c, t0 + k))
+                                        code[h][0] |= 0x7fu << (8 * c);
                         }
                     }
                     named_sync(3, 128 * C::kGroups);
@@ -723,9 +729,12 @@ gqa_decode_fp8_kernel(const __grid_constant__ Fp8DecodeParams p) {
 #pragma unroll
                         for (int u = 0; u < 8; ++u) row[u] = make_uint4(0u, 0u, 0u, 0u);
                     }
-                    // an e4m3 zero times the NaN weight is NaN: those rows see it
                 }
-                store_weights<NC>(pbuf, grp, k, code);
+#pragma unroll
+                for (int h = 0; h < NCH; ++h)
+                    if (col(h) < cols)
+                        *reinterpret_cast<uint4 *>(smem + C::p + 4 * col(h) * kBK + 16 * k) =
+                            make_uint4(code[h][0], code[h][1], code[h][2], 0u);
                 tc::fence_async_smem();
                 tc::fence_before_sync();
                 __syncwarp();
@@ -735,65 +744,65 @@ gqa_decode_fp8_kernel(const __grid_constant__ Fp8DecodeParams p) {
             // ---- item epilogue ----------------------------------------------------
             // The row sums first: they do not need O, so their exchange runs
             // while the last P.V is still in flight.
-            float lsum[NW];
-            {
-                float *lb = lred + (iter & 1) * 64;   // [4 key warps][16 columns]
+            float *lb = lred + (iter & 1) * 64;   // [4 key warps][16 columns]
 #pragma unroll
-                for (int c = 0; c < NW; ++c) {
-                    const float a = warp_sum(l[c]);
-                    if (lane == 0) lb[kw * 16 + cg0 + c] = a;
-                }
-                named_sync(1 + grp, 128);
+            for (int h = 0; h < NCH; ++h)
 #pragma unroll
-                for (int c = 0; c < NW; ++c) {
-                    const int cg = cg0 + c;
-                    lsum[c] = (lb[cg] + lb[16 + cg]) + (lb[32 + cg] + lb[48 + cg]);
+                for (int c = 0; c < 4; ++c) {
+                    const float a = warp_sum(l[h][c]);
+                    if (lane == 0) lb[kw * 16 + col(h) + c] = a;
                 }
-            }
-            float o[3 * NW];
+            named_sync(1 + grp, 128);
             if (it.ntiles > 0)
                 ok = ok && mbar_wait(&bar[kODone], (g + it.ntiles - 1) & 1, p.err);
-            if (ok && it.ntiles > 0) {
-                tc::fence_after_sync();
-                tmem_ld_cols<3 * NW>(o_col, o);
-            } else {
-#pragma unroll
-                for (int c = 0; c < 3 * NW; ++c) o[c] = 0.f;
-            }
-            tc::fence_before_sync();
+            tc::fence_after_sync();
             const int ch = k;   // output channel of this thread
 #pragma unroll
-            for (int c = 0; c < NW; ++c) {
-                const int i = ((cg0 + c) * g_inv) >> 16, h = (cg0 + c) - i * G;
-                if (i >= nrows) continue;
-                const int hq = it.kvh * G + h;
-                const size_t row = size_t(row0 + i);
-                const float acc = fmaf(fmaf(o[2 * NW + c], 0.0625f, o[NW + c]), 0.0625f, o[c]) *
-                                  (1.f / kWeightTop);
-                if (it.direct) {
-                    const float t2 = p.sink ? p.sink[hq] * kLog2e : -INFINITY;
-                    const float Mf = fmaxf(m[c], t2);
-                    float so = 1.f, Z = lsum[c];       // 0 without a visible key, or NaN
-                    if (Mf != -INFINITY) {
-                        so = fast_exp2(m[c] - Mf);     // 0 when m = -inf
-                        Z = lsum[c] * so + fast_exp2(t2 - Mf);
-                    }
-                    const float v = Z == 0.f ? 0.f : acc * so / Z;
-                    p.out[(row * p.num_q_heads + hq) * kD + ch] =
-                        static_cast<uint16_t>(pack_bf16x2(v, 0.f) & 0xffffu);
-                    if (ch == 0 && p.lse)
-                        p.lse[row * p.num_q_heads + hq] =
-                            Z == 0.f ? -INFINITY : (Mf + fast_log2(Z)) * kLn2;
+            for (int h = 0; h < NCH; ++h) {
+                if (col(h) >= cols) continue;
+                float o[12];
+                if (ok && it.ntiles > 0) {
+                    tmem_ld_cols<12>(tmem + lane_base + C::kTmemO + 4 * col(h), o);
                 } else {
-                    const size_t base = size_t(it.slot) * kGqaSlotCols + (cg0 + c);
-                    p.ws_o[base * kD + ch] = acc;
-                    if (ch == 0) {
-                        // a NaN sum must not hide behind an empty slice's -inf
-                        p.ws_m[base] = lsum[c] == lsum[c] ? m[c] * kLn2 : 0.f;
-                        p.ws_l[base] = lsum[c];
+#pragma unroll
+                    for (int c = 0; c < 12; ++c) o[c] = 0.f;
+                }
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const int cg = col(h) + c;
+                    const int i = (cg * g_inv) >> 16, hd = cg - i * G;
+                    if (i >= nrows) continue;
+                    const int hq = it.kvh * G + hd;
+                    const size_t row = size_t(row0 + i);
+                    const float lsum = (lb[cg] + lb[16 + cg]) + (lb[32 + cg] + lb[48 + cg]);
+                    const float acc = fmaf(fmaf(o[8 + c], 0.0625f, o[4 + c]), 0.0625f, o[c]) *
+                                      (1.f / kWeightTop);
+                    if (it.direct) {
+                        const float t2 = p.sink ? p.sink[hq] * kLog2e : -INFINITY;
+                        const float Mf = fmaxf(m[h][c], t2);
+                        float so = 1.f, Z = lsum;       // 0 without a visible key, or NaN
+                        if (Mf != -INFINITY) {
+                            so = fast_exp2(m[h][c] - Mf);   // 0 when m = -inf
+                            Z = lsum * so + fast_exp2(t2 - Mf);
+                        }
+                        const float v = Z == 0.f ? 0.f : acc * so / Z;
+                        p.out[(row * p.num_q_heads + hq) * kD + ch] =
+                            static_cast<uint16_t>(pack_bf16x2(v, 0.f) & 0xffffu);
+                        if (ch == 0 && p.lse)
+                            p.lse[row * p.num_q_heads + hq] =
+                                Z == 0.f ? -INFINITY : (Mf + fast_log2(Z)) * kLn2;
+                    } else {
+                        const size_t base = size_t(it.slot) * kGqaSlotCols + cg;
+                        p.ws_o[base * kD + ch] = acc;
+                        if (ch == 0) {
+                            // a NaN sum must not hide behind an empty slice's -inf
+                            p.ws_m[base] = lsum == lsum ? m[h][c] * kLn2 : 0.f;
+                            p.ws_l[base] = lsum;
+                        }
                     }
                 }
             }
+            tc::fence_before_sync();
             // The CTA holding the unit's first tile publishes where its pieces are.
             if (it.first && threadIdx.x == 0)
                 p.unit_slots[it.b * (p.num_q_heads / G) + it.kvh] =
