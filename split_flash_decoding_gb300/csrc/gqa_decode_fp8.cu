@@ -196,6 +196,15 @@ __device__ __forceinline__ float2 from_e4m3x2(uint32_t c) {
     return __half22float2(__half2(
         __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(c), __NV_E4M3)));
 }
+// 16 times what two codes leave of (a, b), given 16 a and 16 b: exact products in
+// a mixed-precision FMA, no unpacking.
+__device__ __forceinline__ void rest16(uint32_t c, float &a16, float &b16) {
+    const __half2_raw h =
+        __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(c), __NV_E4M3);
+    const unsigned short minus16 = 0xcc00;   // f16
+    asm("fma.rn.f32.f16 %0, %1, %2, %0;" : "+f"(a16) : "h"(h.x), "h"(minus16));
+    asm("fma.rn.f32.f16 %0, %1, %2, %0;" : "+f"(b16) : "h"(h.y), "h"(minus16));
+}
 
 // Byte of element (row r, byte c) of an operand of 128-byte rows, 128-byte swizzle.
 __device__ __forceinline__ uint32_t operand_offset(int r, int c) {
@@ -530,6 +539,7 @@ gqa_decode_fp8_kernel(const __grid_constant__ Fp8DecodeParams p) {
         float *lred = reinterpret_cast<float *>(smem + C::lred);
         const int g_inv = (1 << 16) / G + 1;         // (cg * g_inv) >> 16 = cg / G for cg < 16
         int g = 0, iter = 0, itq = 0;
+        int ss = 0, sph = 0;                         // stage and phase of the scale ring
         bool ok = true;
         for (int j = 0; j < walk.count; ++j, ++iter) {
             const Fp8Item it = fp8_item(p, cum, walk, j);
@@ -541,15 +551,15 @@ gqa_decode_fp8_kernel(const __grid_constant__ Fp8DecodeParams p) {
             // earlier item's scores and are never written out.
             const auto col = [&](int h) { return 4 * (h * C::kGroups + grp); };
             const int cols = nrows * G;
-            float f[NCH][4], m[NCH][4], l[NCH][4];
+            // Pairs of columns go through the packed fp32 instructions.  m is 0 until
+            // the first tile sets it: a column that sees no key there sees none at
+            // all in this item, as the mask only hides a sequence's last keys.
+            float2 f[NCH][2], m[NCH][2], l[NCH][2];
 #pragma unroll
             for (int h = 0; h < NCH; ++h)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    m[h][c] = -INFINITY;
-                    l[h][c] = 0.f;
-                    f[h][c] = 0.f;
-                }
+                for (int c = 0; c < 2; ++c)
+                    m[h][c] = l[h][c] = f[h][c] = make_float2(0.f, 0.f);
             if (it.ntiles > 0) {
                 const int qb = itq % C::kQBufs;
                 ok = ok && mbar_wait(&bar[kQFull + qb], (itq / C::kQBufs) & 1, p.err);
@@ -557,7 +567,9 @@ gqa_decode_fp8_kernel(const __grid_constant__ Fp8DecodeParams p) {
 #pragma unroll
                 for (int h = 0; h < NCH; ++h)
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) f[h][c] = qf[col(h) + c] * p.qk_scale_log2;
+                    for (int c = 0; c < 2; ++c)
+                        f[h][c] = make_float2(qf[col(h) + 2 * c] * p.qk_scale_log2,
+                                              qf[col(h) + 2 * c + 1] * p.qk_scale_log2);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar[kQEmpty + qb]);
                 ++itq;
@@ -567,7 +579,7 @@ gqa_decode_fp8_kernel(const __grid_constant__ Fp8DecodeParams p) {
             const bool masked_rows = p.causal && nrows > 1;
             const int full = masked_rows ? it.L - nrows + 1 : it.L;
             const auto sees = [&](int cg, int key) {
-                return !masked_rows || key < full + ((cg * g_inv) >> 16);
+                return key < it.L && (!masked_rows || key < full + ((cg * g_inv) >> 16));
             };
             // Every warp runs every named barrier of every tile, even after a
             // wait gave up (ok == false), so no warp can strand the others.
@@ -575,25 +587,26 @@ gqa_decode_fp8_kernel(const __grid_constant__ Fp8DecodeParams p) {
                 const int gg = g + t;
                 const int sb = gg & 1;
                 const int t0 = it.start + t * kBK;
-                const bool valid = t0 + k < it.end;
+                const bool tail = t0 + kBK > full;               // uniform over the CTA
                 // ---- scales and scores of this key -------------------------------
-                const int ss = gg % C::kScStages;
                 // both polls in flight together
-                const bool sc_in = mbar_try_wait(&bar[kScFull + ss], (gg / C::kScStages) & 1);
+                const bool sc_in = mbar_try_wait(&bar[kScFull + ss], sph);
                 const bool s_in = mbar_try_wait(&bar[kSFull + sb], (gg >> 1) & 1);
-                if (!sc_in)
-                    ok = ok && mbar_wait(&bar[kScFull + ss], (gg / C::kScStages) & 1, p.err);
+                if (!sc_in) ok = ok && mbar_wait(&bar[kScFull + ss], sph, p.err);
                 float2 sc = reinterpret_cast<const float2 *>(smem + C::sc)[ss * kBK + k];
                 if (!s_in) ok = ok && mbar_wait(&bar[kSFull + sb], (gg >> 1) & 1, p.err);
                 tc::fence_after_sync();
-                float s[NCH][4];
+                float2 s[NCH][2];                                // score, then score - m
 #pragma unroll
                 for (int h = 0; h < NCH; ++h) {
                     if (col(h) >= cols) continue;
                     float raw[8];
                     tc::tmem_ld_n<8>(tmem + lane_base + sb * C::NS + 2 * col(h), raw);
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) s[h][c] = fmaf(raw[4 + c], 0.0625f, raw[c]);
+                    for (int c = 0; c < 2; ++c)
+                        s[h][c] = __ffma2_rn(make_float2(raw[4 + 2 * c], raw[5 + 2 * c]),
+                                             make_float2(0.0625f, 0.0625f),
+                                             make_float2(raw[2 * c], raw[2 * c + 1]));
                 }
                 tc::fence_before_sync();
                 __syncwarp();
@@ -601,53 +614,68 @@ gqa_decode_fp8_kernel(const __grid_constant__ Fp8DecodeParams p) {
                     mbar_arrive(&bar[kSFree + sb]);
                     mbar_arrive(&bar[kScEmpty + ss]);
                 }
-                if (!valid) sc = make_float2(0.f, 0.f);
+                if (++ss == C::kScStages) { ss = 0; sph ^= 1; }
+                if (tail && t0 + k >= it.L) sc = make_float2(0.f, 0.f);
                 const int ve = min(max(int((__float_as_uint(sc.y) >> 23) & 0xffu) - 127, kMinVExp),
                                    kMaxVExp);
                 const float vexp = static_cast<float>(ve);
                 const float v_inv = pow2i(-ve);
                 const float v_mul = sc.y * v_inv * kWeightTop;
-                bool above = false;
+                float top = -INFINITY;
 #pragma unroll
                 for (int h = 0; h < NCH; ++h) {
                     if (col(h) >= cols) continue;
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        s[h][c] = valid ? fmaf(s[h][c] * sc.x, f[h][c], vexp) : -INFINITY;
-                        if (t0 + kBK > full && !sees(col(h) + c, t0 + k)) s[h][c] = -INFINITY;
-                        above |= s[h][c] > m[h][c] + kLazy;   // also from -inf
+                    for (int c = 0; c < 2; ++c) {
+                        s[h][c] = __ffma2_rn(__fmul2_rn(s[h][c], make_float2(sc.x, sc.x)), f[h][c],
+                                             make_float2(vexp, vexp));
+                        if (tail) {
+                            if (!sees(col(h) + 2 * c, t0 + k)) s[h][c].x = -INFINITY;
+                            if (!sees(col(h) + 2 * c + 1, t0 + k)) s[h][c].y = -INFINITY;
+                        }
+                        s[h][c] = __fadd2_rn(s[h][c], make_float2(-m[h][c].x, -m[h][c].y));
+                        top = fmax3(top, s[h][c].x, s[h][c].y);
                     }
                 }
                 // ---- does any column's reference have to move? --------------------
                 // One barrier with an OR answers for the group; the columns' maxima
                 // are only taken where it says yes (the first tile and a few more).
-                const bool moved = named_or(1 + grp, 128, above);
-                float alpha[NCH][4];
+                const bool moved = t == 0 || named_or(1 + grp, 128, top > kLazy);
+                float2 alpha[NCH][2];
                 if (moved) {
 #pragma unroll
                     for (int h = 0; h < NCH; ++h) {
                         if (col(h) >= cols) continue;
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            const float wm = warp_max_redux(s[h][c]);
-                            if (lane == 0) red[kw * 16 + col(h) + c] = wm;
+                        for (int c = 0; c < 2; ++c) {
+                            const float w0 = warp_max_redux(s[h][c].x);
+                            const float w1 = warp_max_redux(s[h][c].y);
+                            if (lane == 0)
+                                *reinterpret_cast<float2 *>(red + kw * 16 + col(h) + 2 * c) =
+                                    make_float2(w0, w1);
                         }
                     }
                     named_sync(1 + grp, 128);
+                    const float lazy = t == 0 ? -INFINITY : kLazy;
+                    const auto raise = [&](int cg, float &sx, float &mx, float &lx, float &ax) {
+                        const float up = fmaxf(fmaxf(red[cg], red[16 + cg]),
+                                               fmaxf(red[32 + cg], red[48 + cg]));
+                        const bool move = up > lazy;
+                        ax = move && t > 0 ? fast_exp2(-up) : 1.f;
+                        if (move) {
+                            mx += up;
+                            sx -= up;
+                            lx *= ax;
+                        }
+                    };
 #pragma unroll
                     for (int h = 0; h < NCH; ++h) {
                         if (col(h) >= cols) continue;
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            const int cg = col(h) + c;
-                            const float tmax = fmaxf(fmaxf(red[cg], red[16 + cg]),
-                                                     fmaxf(red[32 + cg], red[48 + cg]));
-                            alpha[h][c] = 1.f;
-                            if (tmax > m[h][c] + kLazy) {
-                                alpha[h][c] = fast_exp2(m[h][c] - tmax);
-                                m[h][c] = tmax;
-                                l[h][c] *= alpha[h][c];
-                            }
+                        for (int c = 0; c < 2; ++c) {
+                            raise(col(h) + 2 * c, s[h][c].x, m[h][c].x, l[h][c].x, alpha[h][c].x);
+                            raise(col(h) + 2 * c + 1, s[h][c].y, m[h][c].y, l[h][c].y,
+                                  alpha[h][c].y);
                         }
                     }
                 }
@@ -655,24 +683,23 @@ gqa_decode_fp8_kernel(const __grid_constant__ Fp8DecodeParams p) {
 #pragma unroll
                 for (int h = 0; h < NCH; ++h) {
                     if (col(h) >= cols) continue;
-                    float w[4];
+                    float2 w[2];
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const float e =
-                            s[h][c] != -INFINITY ? fast_exp2(s[h][c] - m[h][c]) : 0.f;
-                        l[h][c] = fmaf(e, v_inv, l[h][c]);
-                        w[c] = e * v_mul;
+                    for (int c = 0; c < 2; ++c) {
+                        const float2 e = make_float2(fast_exp2(s[h][c].x), fast_exp2(s[h][c].y));
+                        l[h][c] = __ffma2_rn(e, make_float2(v_inv, v_inv), l[h][c]);
+                        w[c] = __fmul2_rn(e, make_float2(v_mul, v_mul));
                     }
 #pragma unroll
                     for (int u = 0; u < 3; ++u) {
-                        const uint32_t lo = to_e4m3x2(w[0], w[1]), hi = to_e4m3x2(w[2], w[3]);
+                        const uint32_t lo = to_e4m3x2(w[0].x, w[0].y);
+                        const uint32_t hi = to_e4m3x2(w[1].x, w[1].y);
                         code[h][u] = lo | (hi << 16);
                         if (u < 2) {
-                            const float2 a = from_e4m3x2(lo), b = from_e4m3x2(hi);
-                            w[0] = (w[0] - a.x) * 16.f;
-                            w[1] = (w[1] - a.y) * 16.f;
-                            w[2] = (w[2] - b.x) * 16.f;
-                            w[3] = (w[3] - b.y) * 16.f;
+                            w[0] = __fmul2_rn(w[0], make_float2(16.f, 16.f));
+                            w[1] = __fmul2_rn(w[1], make_float2(16.f, 16.f));
+                            rest16(lo, w[0].x, w[0].y);
+                            rest16(hi, w[1].x, w[1].y);
                         }
                     }
                 }
@@ -689,14 +716,17 @@ gqa_decode_fp8_kernel(const __grid_constant__ Fp8DecodeParams p) {
                             const uint32_t oc = tmem + lane_base + C::kTmemO + 4 * col(h);
                             tmem_ld_cols<12>(oc, o);
 #pragma unroll
-                            for (int c = 0; c < 12; ++c) o[c] *= alpha[h][c & 3];
+                            for (int c = 0; c < 12; c += 2) {
+                                o[c] *= alpha[h][(c >> 1) & 1].x;
+                                o[c + 1] *= alpha[h][(c >> 1) & 1].y;
+                            }
                             tmem_st_cols<12>(oc, o);
                         }
                         tc::tmem_wait_st();
                     }
                 }
                 // ---- V rows that some or all rows must not see --------------------
-                if (t0 + kBK > full) {               // uniform over the CTA
+                if (tail) {
                     const int vs = gg % kStages;
                     ok = ok && mbar_wait(&bar[kVFull + vs], (gg / kStages) & 1, p.err);
                     uint4 *row = reinterpret_cast<uint4 *>(smem + C::vring + vs * kTileBytes) + k * 8;
@@ -748,9 +778,10 @@ gqa_decode_fp8_kernel(const __grid_constant__ Fp8DecodeParams p) {
 #pragma unroll
             for (int h = 0; h < NCH; ++h)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const float a = warp_sum(l[h][c]);
-                    if (lane == 0) lb[kw * 16 + col(h) + c] = a;
+                for (int c = 0; c < 2; ++c) {
+                    const float2 a = make_float2(warp_sum(l[h][c].x), warp_sum(l[h][c].y));
+                    if (lane == 0)
+                        *reinterpret_cast<float2 *>(lb + kw * 16 + col(h) + 2 * c) = a;
                 }
             named_sync(1 + grp, 128);
             if (it.ntiles > 0)
@@ -775,14 +806,17 @@ gqa_decode_fp8_kernel(const __grid_constant__ Fp8DecodeParams p) {
                     const int hq = it.kvh * G + hd;
                     const size_t row = size_t(row0 + i);
                     const float lsum = (lb[cg] + lb[16 + cg]) + (lb[32 + cg] + lb[48 + cg]);
+                    // no visible key: no sum, no reference
+                    const float mx =
+                        lsum == 0.f ? -INFINITY : c & 1 ? m[h][c >> 1].y : m[h][c >> 1].x;
                     const float acc = fmaf(fmaf(o[8 + c], 0.0625f, o[4 + c]), 0.0625f, o[c]) *
                                       (1.f / kWeightTop);
                     if (it.direct) {
                         const float t2 = p.sink ? p.sink[hq] * kLog2e : -INFINITY;
-                        const float Mf = fmaxf(m[h][c], t2);
-                        float so = 1.f, Z = lsum;       // 0 without a visible key, or NaN
+                        const float Mf = fmaxf(mx, t2);
+                        float so = 1.f, Z = lsum;
                         if (Mf != -INFINITY) {
-                            so = fast_exp2(m[h][c] - Mf);   // 0 when m = -inf
+                            so = fast_exp2(mx - Mf);    // 0 when mx = -inf
                             Z = lsum * so + fast_exp2(t2 - Mf);
                         }
                         const float v = Z == 0.f ? 0.f : acc * so / Z;
@@ -795,8 +829,7 @@ gqa_decode_fp8_kernel(const __grid_constant__ Fp8DecodeParams p) {
                         const size_t base = size_t(it.slot) * kGqaSlotCols + cg;
                         p.ws_o[base * kD + ch] = acc;
                         if (ch == 0) {
-                            // a NaN sum must not hide behind an empty slice's -inf
-                            p.ws_m[base] = lsum == lsum ? m[h][c] * kLn2 : 0.f;
+                            p.ws_m[base] = mx * kLn2;
                             p.ws_l[base] = lsum;
                         }
                     }
