@@ -45,9 +45,11 @@ namespace {
 
 constexpr int kD = 128;
 constexpr int kBK = kGqaTcTileKeys;          // 128 keys per tile
-constexpr int kStages = 3;
+constexpr int kStages = 3;                   // K tiles in flight
+constexpr int kVStages = 2;                  // V tiles in flight (three measured the same)
 constexpr int kTileBytes = kBK * kD;         // 16 KB
-constexpr int kMaxScStages = 6;
+constexpr int kScStages = 6;                 // tiles of scales in flight
+constexpr int kQBufs = 2;
 constexpr int kCtasPerSm = 2;
 constexpr float kLazy = 4.f;                 // base 2
 constexpr float kWeightTop = 8.f;            // weights reach 2^kLazy * 2 * kWeightTop = 256
@@ -61,26 +63,24 @@ constexpr int kMinVExp = -64, kMaxVExp = 64;
 template <int NC>
 struct Cfg {
     static constexpr int kChunks = NC / 4;
-    static constexpr int kGroups = NC > 8 ? 2 : 1;
+    static constexpr int kGroups = NC > 4 ? 2 : 1;
     static constexpr int NCH = kChunks / kGroups;                    // chunks per group
     static constexpr int NS = kChunks < 2 ? 16 : 8 * kChunks;        // N of the score MMA
     static constexpr int NP = 16 * kChunks;                          // N of the output MMA
     static constexpr int kTmemO = 2 * NS;                            // after two score buffers
     static constexpr int kTmemCols = 2 * NS + NP <= 64 ? 64 : 128;
-    static constexpr int kQBufs = NC > 8 ? 1 : 2;
-    static constexpr int kScStages = NC > 8 ? 3 : kMaxScStages;      // tiles of scales in flight
     static constexpr int kWarpK = 4 * kGroups, kWarpV = kWarpK + 1, kWarpMma = kWarpK + 2,
                          kWarpAux = kWarpK + 3;
     static constexpr int kThreads = 32 * (4 * kGroups + 4);
     // shared memory
     static constexpr int kring = 0;
     static constexpr int vring = kring + kStages * kTileBytes;
-    static constexpr int q = vring + kStages * kTileBytes;           // [kQBufs][NS rows][128 B]
+    static constexpr int q = vring + kVStages * kTileBytes;          // [kQBufs][NS rows][128 B]
     static constexpr int p = q + kQBufs * NS * 128;                  // [chunks][128 keys][16 B]
     static constexpr int sc = p + NP * 128;                          // [kScStages][128] {ks, vs}
     static constexpr int red = sc + kScStages * kBK * 8;             // float [4][16] tile max
-    static constexpr int lred = red + 4 * 16 * 4;                    // float [2][4][16] row sums
-    static constexpr int qf = lred + 2 * 4 * 16 * 4;                 // float [kQBufs][16] 2^-a
+    static constexpr int lred = red + 4 * 16 * 4;                    // float [2][5][16] row sums, references
+    static constexpr int qf = lred + 2 * 5 * 16 * 4;                 // float [kQBufs][16] 2^-a
     static constexpr int bars = qf + 2 * 16 * 4;
     static constexpr int tmem_slot = bars + kBarBytes;
     static constexpr int range = tmem_slot + 16;
@@ -89,8 +89,8 @@ struct Cfg {
 
 enum Bar {
     kKFull = 0, kKEmpty = 3, kVFull = 6, kVEmpty = 9,   // [kStages] each
-    kScFull = 12, kScEmpty = 12 + kMaxScStages,         // [kScStages] each
-    kQFull = 12 + 2 * kMaxScStages, kQEmpty = kQFull + 2,   // [2] each
+    kScFull = 12, kScEmpty = 12 + kScStages,         // [kScStages] each
+    kQFull = 12 + 2 * kScStages, kQEmpty = kQFull + 2,   // [2] each
     kSFull = kQEmpty + 2, kSFree = kSFull + 2,          // [2] each
     kPFull = kSFree + 2, kODone = kPFull + 1,
     kNumBars = kODone + 1
@@ -161,6 +161,18 @@ __device__ __forceinline__ void tmem_st_cols(uint32_t taddr, const float (&v)[N]
         for (int j = 0; j < 4; ++j) a[j] = v[N - 4 + j];
         tc::tmem_st_n<4>(taddr + N - 4, a);
     }
+}
+
+// The three terms of one O column, four columns apart.
+__device__ __forceinline__ void tmem_ld_terms(uint32_t taddr, float &a, float &b, float &c) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%3];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x1.b32 {%1}, [%4];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x1.b32 {%2}, [%5];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=&f"(a), "=&f"(b), "=&f"(c)
+        : "r"(taddr), "r"(taddr + 4), "r"(taddr + 8)
+        : "memory");
 }
 
 // Maximum over the 32 lanes of the warp (NaN ignored; every lane gets it).
@@ -254,6 +266,7 @@ __device__ __forceinline__ void produce(const Fp8DecodeParams &p, const int *cum
     uint64_t *full = bar + (kIsK ? kKFull : kVFull);
     uint64_t *empty = bar + (kIsK ? kKEmpty : kVEmpty);
     uint8_t *ring = smem + (kIsK ? Cfg<NC>::kring : Cfg<NC>::vring);
+    constexpr int kN = kIsK ? kStages : kVStages;
     if (lane == 0) prefetch_tensormap(map);
     const int box_rows = p.box_rows;        // 128, 64, 32, 16 or 8
     const int nb = kBK / box_rows;          // row boxes per tile
@@ -266,11 +279,11 @@ __device__ __forceinline__ void produce(const Fp8DecodeParams &p, const int *cum
         int cached = -1, my_page = -1, my_slot = 0;
         for (int t = 0; t < it.ntiles && !aborted; ++t) {
             const int gg = g + t;
-            const int s = gg % kStages;
+            const int s = gg % kN;
             const int key0 = it.start + t * kBK;
             const int live = min(nb, (it.L - key0 + box_rows - 1) / box_rows);
             if (lane == 0) {
-                if (gg >= kStages && !mbar_wait(&empty[s], ((gg / kStages) - 1) & 1, p.err))
+                if (gg >= kN && !mbar_wait(&empty[s], ((gg / kN) - 1) & 1, p.err))
                     aborted = true;
                 else
                     mbar_arrive_expect_tx(&full[s], uint32_t(live) * box_bytes);
@@ -298,8 +311,8 @@ __device__ __forceinline__ void produce(const Fp8DecodeParams &p, const int *cum
     }
     // Every copy this warp issued must land before the CTA may leave.
     if (lane == 0)
-        for (int i = max(0, g - kStages); i < g; ++i)
-            mbar_wait(&full[i % kStages], (i / kStages) & 1, p.err);
+        for (int i = max(0, g - kN); i < g; ++i)
+            mbar_wait(&full[i % kN], (i / kN) & 1, p.err);
 }
 
 __device__ __forceinline__ void cp_async_4(void *dst, const float *src) {
@@ -326,9 +339,9 @@ __device__ __forceinline__ void feed(const Fp8DecodeParams &p, const int *cum, c
     for (int j = 0; ok && j < w.count; ++j) {
         const Fp8Item it = fp8_item(p, cum, w, j);
         if (it.ntiles == 0) continue;
-        const int qb = itq % C::kQBufs;
-        if (itq >= C::kQBufs)
-            ok = mbar_wait(&bar[kQEmpty + qb], ((itq / C::kQBufs) - 1) & 1, p.err);
+        const int qb = itq % kQBufs;
+        if (itq >= kQBufs)
+            ok = mbar_wait(&bar[kQEmpty + qb], ((itq / kQBufs) - 1) & 1, p.err);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         int row0, nrows;
@@ -336,7 +349,7 @@ __device__ __forceinline__ void feed(const Fp8DecodeParams &p, const int *cum, c
         uint8_t *qs = smem + C::q + qb * C::NS * 128;
         float *qf = reinterpret_cast<float *>(smem + C::qf) + qb * 16;
         const int cols = min(min(nrows, p.num_q_rows - row0) * G, NC);
-        constexpr int kBatch = 4;   // columns whose loads are in flight together
+        constexpr int kBatch = NC < 8 ? NC : 8;   // columns whose loads are in flight together
 #pragma unroll 1
         for (int c0 = 0; c0 < cols; c0 += kBatch) {
             uint2 raw[kBatch];
@@ -387,10 +400,10 @@ __device__ __forceinline__ void feed(const Fp8DecodeParams &p, const int *cum, c
         int cached = -1, my_page = -1, my_slot = 0;
         for (int t = 0; t < it.ntiles; ++t) {
             const int gg = g + t;
-            const int s = gg % C::kScStages;
+            const int s = gg % kScStages;
             const int left = it.L - (it.start + t * kBK);            // keys of the tile on
-            if (gg >= C::kScStages)
-                ok = mbar_wait(&bar[kScEmpty + s], ((gg / C::kScStages) - 1) & 1, p.err);
+            if (gg >= kScStages)
+                ok = mbar_wait(&bar[kScEmpty + s], ((gg / kScStages) - 1) & 1, p.err);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             float2 *dst = reinterpret_cast<float2 *>(smem + C::sc) + s * kBK + lane;
@@ -438,9 +451,9 @@ gqa_decode_fp8_kernel(const __grid_constant__ Fp8DecodeParams p) {
         for (int i = 0; i < kNumBars; ++i) {
             uint32_t n = 1;
             if (i == kSFree || i == kSFree + 1 || i == kPFull) n = 4 * C::kGroups;
-            if (i >= kScEmpty && i < kScEmpty + kMaxScStages) n = 4 * C::kGroups;
+            if (i >= kScEmpty && i < kScEmpty + kScStages) n = 4 * C::kGroups;
             if (i == kQEmpty || i == kQEmpty + 1) n = 4 * C::kGroups + 1;
-            if (i >= kScFull && i < kScFull + kMaxScStages) n = 32;
+            if (i >= kScFull && i < kScFull + kScStages) n = 32;
             mbar_init(&bar[i], n);
         }
         fence_mbar_init();
@@ -450,7 +463,7 @@ gqa_decode_fp8_kernel(const __grid_constant__ Fp8DecodeParams p) {
         tc::tmem_relinquish();
     }
     // Rows of Q and P past the columns in use stay zero.
-    for (int i = threadIdx.x; i < (C::kQBufs * C::NS + C::NP) * 8; i += C::kThreads)
+    for (int i = threadIdx.x; i < (kQBufs * C::NS + C::NP) * 8; i += C::kThreads)
         reinterpret_cast<uint4 *>(smem + C::q)[i] = make_uint4(0u, 0u, 0u, 0u);
     tc::fence_async_smem();
     tc::fence_before_sync();
@@ -481,8 +494,8 @@ gqa_decode_fp8_kernel(const __grid_constant__ Fp8DecodeParams p) {
             for (int j = 0; ok && j < walk.count; ++j) {
                 const Fp8Item it = fp8_item(p, cum, walk, j);
                 if (it.ntiles == 0) continue;
-                const int qb = itq % C::kQBufs;
-                ok = mbar_wait(&bar[kQFull + qb], (itq / C::kQBufs) & 1, p.err);
+                const int qb = itq % kQBufs;
+                ok = mbar_wait(&bar[kQFull + qb], (itq / kQBufs) & 1, p.err);
                 for (int t = 0; ok && t <= it.ntiles; ++t) {
                     if (t < it.ntiles) {
                         const int gg = g + t;
@@ -507,9 +520,9 @@ gqa_decode_fp8_kernel(const __grid_constant__ Fp8DecodeParams p) {
                     }
                     if (t >= 1) {
                         const int gp = g + t - 1;
-                        const int vs = gp % kStages;
+                        const int vs = gp % kVStages;
                         ok = mbar_wait(&bar[kPFull], gp & 1, p.err);
-                        if (ok) ok = mbar_wait(&bar[kVFull + vs], (gp / kStages) & 1, p.err);
+                        if (ok) ok = mbar_wait(&bar[kVFull + vs], (gp / kVStages) & 1, p.err);
                         if (!ok) break;
                         tc::fence_after_sync();
                         // V^T as the MN-major A operand: 128 channels are one 128-byte
@@ -561,8 +574,8 @@ gqa_decode_fp8_kernel(const __grid_constant__ Fp8DecodeParams p) {
                 for (int c = 0; c < 2; ++c)
                     m[h][c] = l[h][c] = f[h][c] = make_float2(0.f, 0.f);
             if (it.ntiles > 0) {
-                const int qb = itq % C::kQBufs;
-                ok = ok && mbar_wait(&bar[kQFull + qb], (itq / C::kQBufs) & 1, p.err);
+                const int qb = itq % kQBufs;
+                ok = ok && mbar_wait(&bar[kQFull + qb], (itq / kQBufs) & 1, p.err);
                 const float *qf = reinterpret_cast<const float *>(smem + C::qf) + qb * 16;
 #pragma unroll
                 for (int h = 0; h < NCH; ++h)
@@ -614,7 +627,7 @@ gqa_decode_fp8_kernel(const __grid_constant__ Fp8DecodeParams p) {
                     mbar_arrive(&bar[kSFree + sb]);
                     mbar_arrive(&bar[kScEmpty + ss]);
                 }
-                if (++ss == C::kScStages) { ss = 0; sph ^= 1; }
+                if (++ss == kScStages) { ss = 0; sph ^= 1; }
                 if (tail && t0 + k >= it.L) sc = make_float2(0.f, 0.f);
                 const int ve = min(max(int((__float_as_uint(sc.y) >> 23) & 0xffu) - 127, kMinVExp),
                                    kMaxVExp);
@@ -727,8 +740,8 @@ gqa_decode_fp8_kernel(const __grid_constant__ Fp8DecodeParams p) {
                 }
                 // ---- V rows that some or all rows must not see --------------------
                 if (tail) {
-                    const int vs = gg % kStages;
-                    ok = ok && mbar_wait(&bar[kVFull + vs], (gg / kStages) & 1, p.err);
+                    const int vs = gg % kVStages;
+                    ok = ok && mbar_wait(&bar[kVFull + vs], (gg / kVStages) & 1, p.err);
                     uint4 *row = reinterpret_cast<uint4 *>(smem + C::vring + vs * kTileBytes) + k * 8;
                     bool clear = t0 + k >= it.L;     // past the end: may hold anything
                     if (t0 + k >= full && t0 + k < it.L) {
@@ -772,66 +785,60 @@ gqa_decode_fp8_kernel(const __grid_constant__ Fp8DecodeParams p) {
             }
 
             // ---- item epilogue ----------------------------------------------------
-            // The row sums first: they do not need O, so their exchange runs
+            // Rolled over the columns and short on purpose: it runs once an item,
+            // from a cold instruction cache (unrolled, it took 10000 cycles for 8
+            // columns a warp).  The row sums and references go through shared memory
             // while the last P.V is still in flight.
-            float *lb = lred + (iter & 1) * 64;   // [4 key warps][16 columns]
+            float *lb = lred + (iter & 1) * 80;   // [4 key warps][16 columns], then m[16]
 #pragma unroll
             for (int h = 0; h < NCH; ++h)
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     const float2 a = make_float2(warp_sum(l[h][c].x), warp_sum(l[h][c].y));
-                    if (lane == 0)
+                    if (lane == 0) {
                         *reinterpret_cast<float2 *>(lb + kw * 16 + col(h) + 2 * c) = a;
+                        if (kw == 0)
+                            *reinterpret_cast<float2 *>(lb + 64 + col(h) + 2 * c) = m[h][c];
+                    }
                 }
             named_sync(1 + grp, 128);
             if (it.ntiles > 0)
                 ok = ok && mbar_wait(&bar[kODone], (g + it.ntiles - 1) & 1, p.err);
             tc::fence_after_sync();
+            const bool has_o = ok && it.ntiles > 0;
             const int ch = k;   // output channel of this thread
-#pragma unroll
-            for (int h = 0; h < NCH; ++h) {
-                if (col(h) >= cols) continue;
-                float o[12];
-                if (ok && it.ntiles > 0) {
-                    tmem_ld_cols<12>(tmem + lane_base + C::kTmemO + 4 * col(h), o);
+#pragma unroll 1
+            for (int x = 0; x < 4 * NCH; ++x) {
+                const int cg = col(x >> 2) + (x & 3);
+                const int i = (cg * g_inv) >> 16, hd = cg - i * G;
+                if (i >= nrows) continue;
+                float o0, o1, o2;
+                tmem_ld_terms(tmem + lane_base + C::kTmemO + 4 * (cg & ~3) + (cg & 3), o0, o1, o2);
+                const float acc = has_o ? fmaf(fmaf(o2, 0.0625f, o1), 0.0625f, o0) *
+                                              (1.f / kWeightTop) : 0.f;
+                const float lsum = (lb[cg] + lb[16 + cg]) + (lb[32 + cg] + lb[48 + cg]);
+                // no visible key: no sum, no reference
+                const float mx = lsum == 0.f ? -INFINITY : lb[64 + cg];
+                const int hq = it.kvh * G + hd;
+                if (it.direct) {
+                    const float t2 = p.sink ? p.sink[hq] * kLog2e : -INFINITY;
+                    const float Mf = fmaxf(mx, t2);
+                    float so = 1.f, Z = lsum;
+                    if (Mf != -INFINITY) {
+                        so = fast_exp2(mx - Mf);    // 0 when mx = -inf
+                        Z = lsum * so + fast_exp2(t2 - Mf);
+                    }
+                    const float v = Z == 0.f ? 0.f : __fdividef(acc * so, Z);
+                    const size_t row = size_t(row0 + i) * p.num_q_heads + hq;
+                    p.out[row * kD + ch] = static_cast<uint16_t>(pack_bf16x2(v, 0.f) & 0xffffu);
+                    if (ch == 0 && p.lse)
+                        p.lse[row] = Z == 0.f ? -INFINITY : (Mf + fast_log2(Z)) * kLn2;
                 } else {
-#pragma unroll
-                    for (int c = 0; c < 12; ++c) o[c] = 0.f;
-                }
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const int cg = col(h) + c;
-                    const int i = (cg * g_inv) >> 16, hd = cg - i * G;
-                    if (i >= nrows) continue;
-                    const int hq = it.kvh * G + hd;
-                    const size_t row = size_t(row0 + i);
-                    const float lsum = (lb[cg] + lb[16 + cg]) + (lb[32 + cg] + lb[48 + cg]);
-                    // no visible key: no sum, no reference
-                    const float mx =
-                        lsum == 0.f ? -INFINITY : c & 1 ? m[h][c >> 1].y : m[h][c >> 1].x;
-                    const float acc = fmaf(fmaf(o[8 + c], 0.0625f, o[4 + c]), 0.0625f, o[c]) *
-                                      (1.f / kWeightTop);
-                    if (it.direct) {
-                        const float t2 = p.sink ? p.sink[hq] * kLog2e : -INFINITY;
-                        const float Mf = fmaxf(mx, t2);
-                        float so = 1.f, Z = lsum;
-                        if (Mf != -INFINITY) {
-                            so = fast_exp2(mx - Mf);    // 0 when mx = -inf
-                            Z = lsum * so + fast_exp2(t2 - Mf);
-                        }
-                        const float v = Z == 0.f ? 0.f : acc * so / Z;
-                        p.out[(row * p.num_q_heads + hq) * kD + ch] =
-                            static_cast<uint16_t>(pack_bf16x2(v, 0.f) & 0xffffu);
-                        if (ch == 0 && p.lse)
-                            p.lse[row * p.num_q_heads + hq] =
-                                Z == 0.f ? -INFINITY : (Mf + fast_log2(Z)) * kLn2;
-                    } else {
-                        const size_t base = size_t(it.slot) * kGqaSlotCols + cg;
-                        p.ws_o[base * kD + ch] = acc;
-                        if (ch == 0) {
-                            p.ws_m[base] = mx * kLn2;
-                            p.ws_l[base] = lsum;
-                        }
+                    const size_t base = size_t(it.slot) * kGqaSlotCols + cg;
+                    p.ws_o[base * kD + ch] = acc;
+                    if (ch == 0) {
+                        p.ws_m[base] = mx * kLn2;
+                        p.ws_l[base] = lsum;
                     }
                 }
             }
