@@ -314,6 +314,9 @@ extern "C" int attn_decode_fp8(const void *q, const attn_kv_t *k, const attn_kv_
         return ATTN_ERR_UNSUPPORTED;
     if (!aligned(q, 16) || !aligned(out, 16)) return ATTN_ERR_INVALID_ARG;
     const int hkv = num_q_heads / group;
+    // the split counts tiles and their costs in ints
+    if ((static_cast<long long>(max_kv_len) / kGqaTcTileKeys + 1) * batch * hkv >= (1LL << 27))
+        return ATTN_ERR_UNSUPPORTED;
     CacheOut kc, vc;
     int st = take_cache(k, batch, head_dim, hkv, max_kv_len, 16, &kc);
     if (st) return st;

@@ -10,12 +10,12 @@
 // with its 256-byte rows, read 64 sequences of Llama-3-8B shapes at 114.9 us.)
 //
 // A unit is (sequence b, group of H heads).  The 128-key tiles of all units,
-// concatenated, are dealt out in contiguous ranges of equal cost: every unit is
-// preceded by kUnitCost virtual tiles in a weighted concatenation (the
-// fixed cost of opening it: its queries, the pipeline refill, the epilogue), and
-// group c of C takes weighted positions [c W / C, (c + 1) W / C).  A unit of n
-// tiles from tile x on sits at [x + kUnitCost u, x + kUnitCost (u + 1) + n); a
-// position in its virtual block maps to its first tile.
+// concatenated, are dealt out in contiguous ranges of equal cost, in eighths of a
+// tile's: a tile costs 8 + (chunks of four columns that the sequence's rows fill
+// - 1), as the softmax of more columns takes longer (1 to 4 rows of 4 heads:
+// 1.58, 1.77, 1.89 and 2.11 us a tile), and every unit is preceded by kUnitCost
+// (opening it: its queries, the pipeline refill, the epilogue).  Group c of C
+// takes the tiles that start in [c W / C, (c + 1) W / C), W the cost of all.
 #pragma once
 
 #include "cache_ops.h"
@@ -23,18 +23,18 @@
 
 namespace attn {
 
-constexpr int kUnitCost = 4;
+constexpr int kUnitCost = 32;
 
 struct Fp8Range {
     int x0, x1;            // this group's tiles of the concatenation
     int u0, count;         // its first unit, and how many it meets
     int groups;            // C, after leaving out groups without tiles
-    long long wtiles;      // W
+    int cost;              // W
 };
 
 struct Fp8Item {
     int b, kvh, L, start, end, ntiles;
-    int unit, unit_x, unit_tiles;
+    int unit, unit_tiles;
     int slot;              // partial slot
     bool first, direct;    // holds the unit's first tile; holds all of it
 };
@@ -43,57 +43,79 @@ __device__ __forceinline__ int fp8_tiles(uint32_t len, uint32_t cap) {
     return max(static_cast<int>((min(len, cap) + kGqaTcTileKeys - 1) / kGqaTcTileKeys), 1);
 }
 
-// cum[0..batch]: tiles of the concatenation before sequence b (head groups
-// included); and this group's range.  One warp, all lanes.
-__device__ __forceinline__ void fp8_build_items(const Fp8DecodeParams &p, int *cum, int lane,
+// First position of group c.
+__device__ __forceinline__ int first_position(int c, int W, int C) {
+    return static_cast<int>(static_cast<long long>(c) * W / C);
+}
+
+// Cost of a tile of sequence b.
+__device__ __forceinline__ int fp8_tile_cost(const Fp8DecodeParams &p, int b) {
+    if (!p.q_row_offsets) return 7 + (p.group + 3) / 4;
+    const int rows = static_cast<int>(p.q_row_offsets[b + 1] - p.q_row_offsets[b]);
+    return 7 + min(max((rows * p.group + 3) / 4, 1), 4);
+}
+
+// cum[b].x: tiles of the concatenation before sequence b (head groups included),
+// cum[b].y: their cost, b up to the batch; and this group's range.  One warp, all
+// lanes.  (The host bounds the tiles of a call so that costs fit an int.)
+__device__ __forceinline__ void fp8_build_items(const Fp8DecodeParams &p, int2 *cum, int lane,
                                                 Fp8Range *out) {
     const int hg = p.head_groups;
     const uint32_t cap = uint32_t(p.max_kv_len);
     const int per_lane = (p.batch + 31) / 32;
     const int b0 = min(lane * per_lane, p.batch), b1 = min(b0 + per_lane, p.batch);
-    int local = 0;
+    int local = 0, cost = 0;
     for (int b = b0; b < b1; ++b) {
         const uint32_t len = p.kv_len[b];
         if (len > cap && blockIdx.x == 0) atomicOr(p.err, kErrBadLength);
-        local += fp8_tiles(len, cap) * hg;
+        const int n = fp8_tiles(len, cap);
+        local += n * hg;
+        cost += hg * (n * fp8_tile_cost(p, b) + kUnitCost);
     }
-    int incl = local;
+    int incl = local, cost_incl = cost;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += v;
+        const int w = __shfl_up_sync(0xffffffffu, cost_incl, o);
+        if (lane >= o) {
+            incl += v;
+            cost_incl += w;
+        }
     }
-    int run = incl - local;
+    int2 run = make_int2(incl - local, cost_incl - cost);
     for (int b = b0; b < b1; ++b) {
         cum[b] = run;
-        run += fp8_tiles(p.kv_len[b], cap) * hg;
+        const int n = fp8_tiles(p.kv_len[b], cap);
+        run.x += n * hg;
+        run.y += hg * (n * fp8_tile_cost(p, b) + kUnitCost);
     }
-    if (lane == 31) cum[p.batch] = incl;
+    if (lane == 31) cum[p.batch] = make_int2(incl, cost_incl);
 
-    const long long per_seq = static_cast<long long>(kUnitCost) * hg;
     const int T = __shfl_sync(0xffffffffu, incl, 31);
-    const long long W = T + per_seq * p.batch;
+    const int W = __shfl_sync(0xffffffffu, cost_incl, 31);
     const int C = min(static_cast<int>(gridDim.x) >> p.head_shift, T);
     const int c = static_cast<int>(blockIdx.x) >> p.head_shift;
-    const long long w_lo = (incl - local) + per_seq * b0, w_hi = incl + per_seq * b1;
-    // Tile of weighted position y, its unit, and whether it is the unit's first.
-    const auto locate = [&](long long y, int &unit, bool &at_first) -> int {
+    const int w_lo = cost_incl - cost, w_hi = cost_incl;
+    // First tile that starts at or after position y, and its unit; first: it
+    // opens that unit.
+    const auto locate = [&](int y, int &unit, bool &first) -> int {
         const bool mine = w_lo <= y && y < w_hi;
         const int src = __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
         int x = 0, u = 0, f = 0;
         if (lane == src) {
-            int xs = incl - local;
-            long long ws = w_lo;   // the chunk's first tile / position
+            int xs = incl - local, ws = w_lo;   // the chunk's first tile / position
             for (int b = b0; b < b1; ++b) {
                 const int n = fp8_tiles(p.kv_len[b], cap);
-                const long long span = static_cast<long long>(hg) * (n + kUnitCost);
+                const int tile = fp8_tile_cost(p, b);
+                const int unit_span = n * tile + kUnitCost;
+                const int span = hg * unit_span;
                 if (y < ws + span) {
-                    const int off = static_cast<int>(y - ws);
-                    const int h = off / (n + kUnitCost);
-                    const int o = off - h * (n + kUnitCost) - kUnitCost;
-                    x = xs + h * n + min(max(o, 0), n);
-                    u = b * hg + h;
-                    f = o <= 0;
+                    const int h = (y - ws) / unit_span;
+                    const int o = (y - ws) - h * unit_span - kUnitCost;
+                    const int i = o <= 0 ? 0 : (o + tile - 1) / tile;
+                    x = xs + h * n + i;
+                    u = b * hg + h + (i == n);   // past the unit's last tile: the next opens
+                    f = i == 0 || i == n;
                     break;
                 }
                 xs += hg * n;
@@ -101,22 +123,22 @@ __device__ __forceinline__ void fp8_build_items(const Fp8DecodeParams &p, int *c
             }
         }
         unit = __shfl_sync(0xffffffffu, u, src);
-        at_first = __shfl_sync(0xffffffffu, f, src) != 0;
+        first = __shfl_sync(0xffffffffu, f, src) != 0;
         return __shfl_sync(0xffffffffu, x, src);
     };
     Fp8Range r;
     r.x0 = r.x1 = r.u0 = r.count = 0;
     r.groups = C;
-    r.wtiles = W;
+    r.cost = W;
     if (c < C) {
         int u0, u1, u_last;
         bool f0, f1;
-        r.x0 = locate(c * W / C, u0, f0);
+        r.x0 = locate(first_position(c, W, C), u0, f0);
         if (c + 1 == C) {
             r.x1 = T;
             u_last = p.batch * hg - 1;
         } else {
-            r.x1 = locate((c + 1) * W / C, u1, f1);
+            r.x1 = locate(first_position(c + 1, W, C), u1, f1);
             u_last = f1 ? u1 - 1 : u1;   // x1 - 1 lies in the unit before when x1 opens one
         }
         r.u0 = u0;
@@ -126,7 +148,7 @@ __device__ __forceinline__ void fp8_build_items(const Fp8DecodeParams &p, int *c
 }
 
 // The piece of unit u0 + j inside the range.
-__device__ __forceinline__ Fp8Item fp8_item(const Fp8DecodeParams &p, const int *cum,
+__device__ __forceinline__ Fp8Item fp8_item(const Fp8DecodeParams &p, const int2 *cum,
                                             const Fp8Range &r, int j) {
     const int hg = p.head_groups;
     Fp8Item it;
@@ -135,9 +157,9 @@ __device__ __forceinline__ Fp8Item fp8_item(const Fp8DecodeParams &p, const int 
     const int h = it.unit - it.b * hg;
     const int member = static_cast<int>(blockIdx.x) & ((1 << p.head_shift) - 1);
     it.kvh = (h << p.head_shift) + member;
-    it.unit_tiles = (cum[it.b + 1] - cum[it.b]) / hg;
-    it.unit_x = cum[it.b] + h * it.unit_tiles;
-    const int tb = max(r.x0 - it.unit_x, 0), te = min(r.x1 - it.unit_x, it.unit_tiles);
+    it.unit_tiles = (cum[it.b + 1].x - cum[it.b].x) / hg;
+    const int x = cum[it.b].x + h * it.unit_tiles;
+    const int tb = max(r.x0 - x, 0), te = min(r.x1 - x, it.unit_tiles);
     it.L = static_cast<int>(min(p.kv_len[it.b], uint32_t(p.max_kv_len)));
     it.start = tb * kGqaTcTileKeys;
     it.end = min(te * kGqaTcTileKeys, it.L);
@@ -150,13 +172,17 @@ __device__ __forceinline__ Fp8Item fp8_item(const Fp8DecodeParams &p, const int 
     return it;
 }
 
-// Pieces of the unit whose first piece is this one: groups c hold weighted
-// position y if c = ((y + 1) C - 1) / W.
-__device__ __forceinline__ int fp8_pieces(const Fp8DecodeParams &p, const Fp8Range &r,
-                                          const Fp8Item &it) {
-    const long long last = it.unit_x + it.unit_tiles - 1 +
-                           static_cast<long long>(kUnitCost) * (it.unit + 1);
-    const int c_last = static_cast<int>(((last + 1) * r.groups - 1) / r.wtiles);
+// Pieces of the unit whose first tile this group holds: position y is group
+// ((y + 1) C - 1) / W's, and the unit's last piece is the group's that its last
+// tile starts in.
+__device__ __forceinline__ int fp8_pieces(const Fp8DecodeParams &p, const int2 *cum,
+                                          const Fp8Range &r, const Fp8Item &it) {
+    const int h = it.unit - it.b * p.head_groups;
+    const int tile = fp8_tile_cost(p, it.b);
+    const int last =
+        cum[it.b].y + (h + 1) * (it.unit_tiles * tile + kUnitCost) - tile;
+    const int c_last =
+        static_cast<int>((static_cast<long long>(last + 1) * r.groups - 1) / r.cost);
     return c_last - (static_cast<int>(blockIdx.x) >> p.head_shift) + 1;
 }
 

@@ -100,7 +100,7 @@ static_assert(sizeof(Fp8Range) <= 32, "range slot");
 
 template <int NC>
 size_t smem_bytes(int batch) {
-    return size_t(Cfg<NC>::items) + sizeof(int) * size_t(batch + 1);
+    return size_t(Cfg<NC>::items) + sizeof(int2) * size_t(batch + 1);
 }
 
 // Instruction descriptor of kind::f8f6f4 with e4m3 A and B, fp32 accumulation.
@@ -260,7 +260,7 @@ __device__ __forceinline__ void lookup_boxes(const Fp8DecodeParams &p, const Fp8
 // K or V producer: walks this CTA's items and tiles and lets lane 0 issue the
 // boxes of each tile into the ring.
 template <bool kIsK, int NC>
-__device__ __forceinline__ void produce(const Fp8DecodeParams &p, const int *cum, const Fp8Range &w,
+__device__ __forceinline__ void produce(const Fp8DecodeParams &p, const int2 *cum, const Fp8Range &w,
                                         uint8_t *smem, uint64_t *bar, int lane) {
     const CUtensorMap *map = kIsK ? &p.k_map : &p.v_map;
     uint64_t *full = bar + (kIsK ? kKFull : kVFull);
@@ -328,7 +328,7 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
 // Auxiliary warp: the terms of each item's queries and the scales of each
 // tile's keys.
 template <int NC>
-__device__ __forceinline__ void feed(const Fp8DecodeParams &p, const int *cum, const Fp8Range &w,
+__device__ __forceinline__ void feed(const Fp8DecodeParams &p, const int2 *cum, const Fp8Range &w,
                                      uint8_t *smem, uint64_t *bar, int lane) {
     using C = Cfg<NC>;
     const int G = p.group;
@@ -440,7 +440,7 @@ gqa_decode_fp8_kernel(const __grid_constant__ Fp8DecodeParams p) {
     uint64_t *bar = reinterpret_cast<uint64_t *>(smem + C::bars);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::tmem_slot);
     Fp8Range *range = reinterpret_cast<Fp8Range *>(smem + C::range);
-    int *cum = reinterpret_cast<int *>(smem + C::items);
+    int2 *cum = reinterpret_cast<int2 *>(smem + C::items);
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -846,7 +846,7 @@ gqa_decode_fp8_kernel(const __grid_constant__ Fp8DecodeParams p) {
             // The CTA holding the unit's first tile publishes where its pieces are.
             if (it.first && threadIdx.x == 0)
                 p.unit_slots[it.b * (p.num_q_heads / G) + it.kvh] =
-                    make_int2(it.slot, fp8_pieces(p, walk, it));
+                    make_int2(it.slot, fp8_pieces(p, cum, walk, it));
             g += it.ntiles;
         }
         pdl_launch_dependents();
