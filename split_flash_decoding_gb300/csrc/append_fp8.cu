@@ -41,38 +41,6 @@ __device__ __forceinline__ float decode(uint8_t c) {
     return __half2float(__half(h));
 }
 
-// Four channels 4 * lane .. of one head row, normed and rotated.
-__device__ __forceinline__ void load_row(const RowsParams &p, const HeadRows &x, int r, int h,
-                                         int pos, bool rotate, float *y, int lane) {
-    const uint16_t *src = x.in + r * x.in_row + h * x.in_head;
-    float sq = 0.f;
-    for (int c = lane; c < kD; c += 32) {
-        const float v = bf16_lo(src[c]);
-        y[c] = v;
-        if (c < x.norm_dim) sq += v * v;
-    }
-    __syncwarp();
-    if (x.norm_dim > 0) {
-        const float inv = rsqrtf(warp_sum(sq) / static_cast<float>(x.norm_dim) + x.eps);
-        for (int c = lane; c < x.norm_dim; c += 32)
-            y[c] *= inv * (x.norm ? bf16_lo(x.norm[c]) : 1.f);
-        __syncwarp();
-    }
-    if (rotate) {
-        const int half = p.rope.rot_dim / 2;
-        for (int i = lane; i < half; i += 32) {
-            const int a = x.rot_start + (p.rope.interleaved ? 2 * i : i);
-            const int b = a + (p.rope.interleaved ? 1 : half);
-            float c, s;
-            rope_cos_sin(p.rope, i, pos, c, s);
-            const float ya = y[a], yb = y[b];
-            y[a] = ya * c - yb * s;
-            y[b] = yb * c + ya * s;
-        }
-        __syncwarp();
-    }
-}
-
 __global__ void __launch_bounds__(kThreads)
 append_fp8_kernel(const __grid_constant__ RowsParams p) {
     __shared__ float buf[kWarps][kD];
@@ -83,13 +51,12 @@ append_fp8_kernel(const __grid_constant__ RowsParams p) {
     const HeadRows &x = is_k ? p.k : p.v;
     const CacheOut &cache = is_k ? p.kc : p.vc;
 
-    const int b = sequence_of_row(p, r);
+    const RowPlace at = place_of_row(p, r, lane);
+    const int b = at.b;
     if (b < 0) return;
-    const int row0 = p.q_row_offsets ? static_cast<int>(p.q_row_offsets[b]) : r;
-    const int n = p.q_row_offsets ? static_cast<int>(p.q_row_offsets[b + 1]) - row0 : 1;
-    const uint32_t L = p.kv_len[b];
-    const long long t0 = static_cast<long long>(L) - n;   // token of the first row
-    const long long tl = t0 + (r - row0);
+    const uint32_t L = at.L;
+    const long long t0 = static_cast<long long>(L) - at.n;   // token of the first row
+    const long long tl = at.t;
     if (tl < 0 || tl >= p.max_kv_len) {
         if (L != 0 && threadIdx.x == 0) atomicOr(p.err, kErrBadLength);
         return;
@@ -114,7 +81,7 @@ append_fp8_kernel(const __grid_constant__ RowsParams p) {
 
     float amax = 0.f;
     for (int i = warp; i < count; i += kWarps) {
-        load_row(p, x, r + i, h, p.positions ? p.positions[r + i] : t + i, rotate, y, lane);
+        load_head(p, x, r + i, h, p.positions ? p.positions[r + i] : t + i, rotate, y, lane);
         for (int c = lane; c < kD; c += 32) {
             const float a = fabsf(y[c]);
             if (a <= FLT_MAX) amax = fmaxf(amax, a);
@@ -142,7 +109,7 @@ append_fp8_kernel(const __grid_constant__ RowsParams p) {
     if (threadIdx.x == 0) *scale = s;
     const float inv = 1.f / s;
     for (int i = warp; i < count; i += kWarps) {
-        load_row(p, x, r + i, h, p.positions ? p.positions[r + i] : t + i, rotate, y, lane);
+        load_head(p, x, r + i, h, p.positions ? p.positions[r + i] : t + i, rotate, y, lane);
         uint8_t *row = dst + (slot + i) * cache.token_stride;
         for (int c = lane; c < kD; c += 32) row[c] = encode(y[c] * inv);
         __syncwarp();
