@@ -518,7 +518,7 @@ int attn_qk_norm_rope(const attn_head_rows_t *q, const attn_head_rows_t *k,
  *               included (the value the attention call that follows takes).
  *   q_row_offsets  device uint32 [batch + 1]: rows of sequence b are
  *               [off[b], off[b + 1]), or NULL for one row per sequence.  Rows
- *               at or behind off[batch] belong to no sequence: nothing of them
+ *               at or behind off[batch] belong to no sequence: nothing is written
  *               is read or written.
  *   batch, num_q_rows   sequences and rows (num_q_rows = batch without
  *               offsets).

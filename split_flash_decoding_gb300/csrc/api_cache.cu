@@ -42,6 +42,7 @@ int take_heads(const attn_head_rows_t &h, bool to_rows, const attn_rope_t *rope,
     x->out_row = h.out_row_stride;
     x->out_head = h.out_head_stride;
     x->eps = h.norm_eps;
+    x->mean = h.norm_dim > 0 ? 1.f / static_cast<float>(h.norm_dim) : 0.f;
     x->norm_dim = h.norm_dim;
     x->heads = h.num_heads;
     x->dim = h.dim;

@@ -1,5 +1,6 @@
-// append_fp8.cu -- keys and values of new tokens into a cache held in 8 bits
-// (attn_append_kv_fp8).
+// append_fp8.cu -- keys and values of new tokens into a cache held in 8 bits,
+// shapes that the tile kernel does not take: blocks of more than 128 tokens and
+// rotations whose pairs do not fall on whole 16-byte vectors.
 //
 // One CTA per (row, KV head, K or V); the CTA of a block's first new row does
 // the block: the new tokens' largest value gives the scale, codes already held
@@ -7,7 +8,7 @@
 #include <cuda_fp8.h>
 #include <float.h>
 
-#include "head_rows.cuh"
+#include "head_tiles.cuh"
 
 namespace attn {
 namespace {
@@ -15,22 +16,6 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kD = 128;
-constexpr int kMinExp = -60, kMaxExp = 120;
-
-// Exponent of the scale of a block whose largest finite value is amax: the
-// least e with amax <= 448 * 2^e (448 = 0.875 * 2^9), clamped.
-__device__ __forceinline__ int scale_exponent(float amax) {
-    if (!(amax > 0.f)) return kMinExp;
-    int e;
-    const float m = frexpf(amax, &e);
-    e += m > 0.875f ? -8 : -9;
-    return min(max(e, kMinExp), kMaxExp);
-}
-
-__device__ __forceinline__ float pow2i(int e) {   // -126 <= e <= 127
-    return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
-}
-
 __device__ __forceinline__ uint8_t encode(float x) {
     if (!(fabsf(x) <= FLT_MAX)) x = __uint_as_float(0x7fffffffu);   // no infinity: NaN
     return static_cast<uint8_t>(__nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3));
@@ -92,7 +77,7 @@ append_fp8_kernel(const __grid_constant__ RowsParams p) {
     if (lane == 0) top[warp] = amax;
     __syncthreads();
     for (int w = 0; w < kWarps; ++w) amax = fmaxf(amax, top[w]);
-    float s = pow2i(scale_exponent(amax));
+    float s = tiles::pow2i(tiles::scale_exponent(amax));
     if (held) {
         const float old = *scale;
         if (s > old) {
@@ -118,7 +103,11 @@ append_fp8_kernel(const __grid_constant__ RowsParams p) {
 
 }  // namespace
 
+cudaError_t launch_fp8_tiles(const RowsParams &p, cudaStream_t stream);
+
 cudaError_t launch_append_fp8(const RowsParams &p, cudaStream_t stream) {
+    if (p.block_tokens <= tiles::kGroupTokens && head_tiles_fit(p))
+        return launch_fp8_tiles(p, stream);
     if (p.q.heads > 0) {
         RowsParams q = p;
         q.k.heads = q.v.heads = 0;

@@ -17,7 +17,7 @@ struct HeadRows {
     uint16_t *out;                // nullptr: the rows go to a cache
     const uint16_t *norm;         // [norm_dim] or nullptr (weights 1)
     long long in_row, in_head, out_row, out_head;
-    float eps;
+    float eps, mean;              // mean: 1 / norm_dim
     int norm_dim, heads, dim, rot_start;
 };
 
@@ -78,6 +78,9 @@ struct Fp8DecodeParams {
 
 cudaError_t launch_head_rows(const RowsParams &p, cudaStream_t stream);
 cudaError_t launch_append_fp8(const RowsParams &p, cudaStream_t stream);
+// The tile kernels take whole rows of 128-byte-friendly shapes; false: not these.
+bool head_tiles_fit(const RowsParams &p);
+cudaError_t launch_head_tiles(const RowsParams &p, cudaStream_t stream);
 // CTAs of the 8-bit decode grid on num_sms SMs.
 int fp8_decode_ctas(int num_sms);
 cudaError_t launch_gqa_decode_fp8(const Fp8DecodeParams &p, int ctas, cudaStream_t stream);

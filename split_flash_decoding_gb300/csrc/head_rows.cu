@@ -274,6 +274,7 @@ cudaError_t launch_v(const RowsParams &p, const Steps &st, cudaStream_t stream) 
 cudaError_t launch_head_rows(const RowsParams &p, cudaStream_t stream) {
     const long long heads = p.q.heads + p.k.heads + p.v.heads;
     if (p.num_rows == 0 || heads == 0) return cudaSuccess;
+    if (head_tiles_fit(p)) return launch_head_tiles(p, stream);
     if (!on_vectors(p.rope, p.q) || !on_vectors(p.rope, p.k)) {
         const long long blocks = (p.num_rows * heads + kAnyWarps - 1) / kAnyWarps;
         if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;

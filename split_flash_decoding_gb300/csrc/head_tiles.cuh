@@ -1,0 +1,531 @@
+// head_tiles.cuh -- norm and rotation of query and key heads over tiles of rows,
+// with the three ways the results go: rows of memory, slots of a bf16 cache, slots
+// of a cache held in 8 bits.
+//
+// Bound by memory for prompts (each channel read and written once) and by latency
+// for a few rows.  A CTA of 256 threads takes a tile of rows and some of their
+// heads.  Its threads first look the rows' places up and compute the cos and sin
+// of every (row, pair) once, into shared memory; then they walk the heads, whose
+// rotation costs no more than reading that table.
+//
+// An item is one head of one row, on L lanes.  A lane holds two 16-byte vectors of
+// it, chosen so that a pair of channels is always in one lane: in the half layout
+// a vector of the rotated channels' lower half and the one rot_dim / 2 above it,
+// otherwise vector i and the one half the head above it, so that lanes side by
+// side read and write whole lines.  256 / L items are in work at once, S times
+// over: consecutive items are the tile's rows (padded to a power of two), then the
+// next heads', so that a tile of one row has many heads in work and a tile of 128
+// rows one or two.
+//
+// The 8-bit cache needs the largest value of a block of tokens before the first
+// code: a tile then is the new tokens of one sequence inside an aligned group of
+// 128 tokens (whole blocks of up to 128), the transformed values stay in registers
+// while the rows' maxima are joined over the block, and what the block holds from
+// before is rounded to a scale that grew.
+#pragma once
+
+#include <cuda_fp8.h>
+#include <float.h>
+
+#include "head_rows.cuh"
+
+namespace attn {
+namespace tiles {
+
+constexpr int kThreads = 256;
+constexpr int kGroupTokens = 128;     // 8-bit cache: aligned tokens of a tile
+constexpr int kMinExp = -60, kMaxExp = 120;
+
+// The launch's cut of the work.
+struct Cut {
+    int tile_rows;                    // rows of a tile (8-bit cache: up to kGroupTokens)
+    int chunks;                       // CTAs of a tile
+    int chunk_heads;                  // heads of a CTA
+    int heads;                        // q, k and v heads together
+    int any_norm;
+};
+
+template <int L, int S>
+struct Shape {
+    static constexpr int kItems = kThreads / L;           // at once
+    static constexpr int kMaxRows = kItems * S < kGroupTokens ? kItems * S : kGroupTokens;
+};
+
+// Shared memory: angles [rows][4][lanes] {c, s, c, s}, then per row its place.
+struct Place {
+    long long k_at, v_at;             // element offsets into the caches
+    int pos, token, page, slot;
+    int stored;                       // -1: the row belongs to no sequence; 0: not stored; 1
+};
+
+__host__ __device__ __forceinline__ int turning_lanes(const RopeParams &rope, int dim) {
+    const int R = rope.rot_dim / 8, vecs = dim / 8;
+    return rope.interleaved ? (R < (vecs + 1) / 2 ? R : (vecs + 1) / 2) : R / 2;
+}
+
+// The m-th vector (8 channels) of a head, the rotated ones first: R of them from
+// vector `start` on.
+__device__ __forceinline__ int ordered(int m, int R, int start) {
+    return m < R ? start + m : m - R < start ? m - R : m;
+}
+
+// The vectors of lane i in that order (-1: none), `vecs` in all, R of them rotated.
+__device__ __forceinline__ void pair_of(bool inter, int vecs, int R, int i, int &a, int &b) {
+    if (!inter && i < R / 2) {
+        a = i;
+        b = i + R / 2;
+        return;
+    }
+    const int base = inter ? 0 : R;
+    const int j = inter ? i : i - R / 2;
+    const int H = (vecs - base + 1) / 2;
+    a = j < H ? base + j : -1;
+    b = j < H && base + j + H < vecs ? base + j + H : -1;
+}
+
+__device__ __forceinline__ void unpack8(const uint4 &w, float2 (&x)[4]) {
+    x[0] = bf16x2_to_float2(w.x);
+    x[1] = bf16x2_to_float2(w.y);
+    x[2] = bf16x2_to_float2(w.z);
+    x[3] = bf16x2_to_float2(w.w);
+}
+
+__device__ __forceinline__ uint4 pack8(const float2 (&x)[4]) {
+    return make_uint4(pack_bf16x2(x[0].x, x[0].y), pack_bf16x2(x[1].x, x[1].y),
+                      pack_bf16x2(x[2].x, x[2].y), pack_bf16x2(x[3].x, x[3].y));
+}
+
+__device__ __forceinline__ void add_squares(const float2 (&y)[4], float2 &sum) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) sum = __ffma2_rn(y[c], y[c], sum);
+}
+
+// y *= f * weights (1 without weights)
+__device__ __forceinline__ void scale8(float2 (&y)[4], const uint4 &w, float f) {
+    float2 g[4];
+    unpack8(w, g);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) y[c] = __fmul2_rn(y[c], __fmul2_rn(g[c], make_float2(f, f)));
+}
+
+// Exponent of the scale of a block whose largest finite value is amax: the least e
+// with amax <= 448 * 2^e (448 = 0.875 * 2^9), clamped.
+__device__ __forceinline__ int scale_exponent(float amax) {
+    if (!(amax > 0.f)) return kMinExp;
+    int e;
+    const float m = frexpf(amax, &e);
+    e += m > 0.875f ? -8 : -9;
+    return min(max(e, kMinExp), kMaxExp);
+}
+
+__device__ __forceinline__ float pow2i(int e) {   // -126 <= e <= 127
+    return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+}
+
+// Largest finite |value| (infinities and NaN do not count).
+__device__ __forceinline__ float finite_abs(float x) {
+    const float a = fabsf(x);
+    return a <= FLT_MAX ? a : 0.f;
+}
+
+// Four values times f as e4m3 codes; there is no infinity: it becomes NaN.
+__device__ __forceinline__ uint32_t encode4(const float2 &a, const float2 &b, float f) {
+    float2 x = __fmul2_rn(a, make_float2(f, f)), y = __fmul2_rn(b, make_float2(f, f));
+    const float nan = __uint_as_float(0x7fffffffu);
+    if (!(fabsf(x.x) <= FLT_MAX)) x.x = nan;
+    if (!(fabsf(x.y) <= FLT_MAX)) x.y = nan;
+    if (!(fabsf(y.x) <= FLT_MAX)) y.x = nan;
+    if (!(fabsf(y.y) <= FLT_MAX)) y.y = nan;
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(x, __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
+    return lo | (hi << 16);
+}
+
+__device__ __forceinline__ float2 decode2(uint32_t c) {
+    return __half22float2(__half2(
+        __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(c & 0xffffu), __NV_E4M3)));
+}
+
+// Sequence of row r; -1: none.  (One thread a row; a warp's rows read the same lines.)
+__device__ __forceinline__ int sequence_of(const RowsParams &p, int r) {
+    if (!p.q_row_offsets) return r;
+    if (r >= static_cast<int>(p.q_row_offsets[p.batch])) return -1;
+    int lo = 0, hi = p.batch;   // off[lo] <= r < off[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (static_cast<int>(p.q_row_offsets[mid]) <= r) lo = mid; else hi = mid;
+    }
+    return lo;
+}
+
+// Tile `tile` of the 8-bit cache: the new tokens of one sequence in one aligned
+// group of kGroupTokens (tokens below 0 included: their queries are written);
+// false: there is no such tile.  With single rows tile = row.  One warp, all lanes.
+struct Tokens {
+    int b, row, count;
+    long long first, begin;   // the tile's first token; the sequence's first new token
+};
+
+__device__ __forceinline__ bool tile_tokens(const RowsParams &p, int tile, int lane, Tokens &out) {
+    static_assert(kGroupTokens == 128, "token >> 7 is its group");
+    int row0 = 0, n = 0, found = -1, index = 0;
+    long long begin = 0;
+    const auto look = [&](int b, bool report) {
+        row0 = p.q_row_offsets ? static_cast<int>(p.q_row_offsets[b]) : b;
+        n = p.q_row_offsets ? static_cast<int>(p.q_row_offsets[b + 1]) - row0 : 1;
+        const uint32_t len = p.kv_len[b];
+        begin = static_cast<long long>(len) - n;
+        if (report && n > 0 && len != 0 &&
+            (begin < 0 || len > static_cast<uint32_t>(p.max_kv_len)))
+            atomicOr(p.err, kErrBadLength);
+        n = min(n, p.num_rows - row0);
+    };
+    if (!p.q_row_offsets) {
+        found = tile;
+    } else {
+        // 32 sequences at a time: a scan of their tile counts.  (The first CTA looks
+        // at all of them, to report their lengths.)
+        int before = 0;
+        for (int b0 = 0; b0 < p.batch && (found < 0 || blockIdx.x == 0); b0 += 32) {
+            int count = 0;
+            if (b0 + lane < p.batch) {
+                look(b0 + lane, blockIdx.x == 0);
+                if (n > 0) count = static_cast<int>(((begin + n - 1) >> 7) - (begin >> 7)) + 1;
+            }
+            int incl = count;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += v;
+            }
+            const int start = before + incl - count;
+            const unsigned who =
+                __ballot_sync(0xffffffffu, found < 0 && tile >= start && tile < start + count);
+            if (who) {
+                const int src = __ffs(who) - 1;
+                found = b0 + src;
+                index = tile - __shfl_sync(0xffffffffu, start, src);
+            }
+            before += __shfl_sync(0xffffffffu, incl, 31);
+        }
+        if (found < 0) return false;
+    }
+    look(found, !p.q_row_offsets && lane == 0);
+    if (n <= 0) return false;
+    const long long group = (begin >> 7) + index;
+    out.b = found;
+    out.begin = begin;
+    out.first = max(begin, group * kGroupTokens);
+    out.count = static_cast<int>(min(begin + n, (group + 1) * kGroupTokens) - out.first);
+    out.row = row0 + static_cast<int>(out.first - begin);
+    return true;
+}
+
+template <int L, int S, bool kInter, bool kFp8>
+__global__ void __launch_bounds__(kThreads, S == 1 ? 3 : 2)
+head_tiles_kernel(const __grid_constant__ RowsParams p, const __grid_constant__ Cut cut) {
+    using Sh = Shape<L, S>;
+    constexpr int kItems = Sh::kItems;
+    extern __shared__ __align__(16) float4 angles[];             // [rows][4][lanes]
+    __shared__ Place places[Sh::kMaxRows];
+    __shared__ float row_max[kFp8 ? kItems * S : 1];             // then 1 / scale
+    __shared__ Tokens s_tile;
+    __shared__ int s_any;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int tile = static_cast<int>(blockIdx.x) / cut.chunks;
+    const int chunk = static_cast<int>(blockIdx.x) - tile * cut.chunks;
+    const int h0 = chunk * cut.chunk_heads, h1 = min(h0 + cut.chunk_heads, cut.heads);
+
+    // ---- rows of the tile and their places -------------------------------------
+    int r0, n;
+    if (kFp8) {
+        if (tid < 32) {
+            Tokens t;
+            const bool any = tile_tokens(p, tile, lane, t);
+            if (lane == 0) {
+                s_any = any;
+                s_tile = t;
+            }
+        }
+        __syncthreads();
+        if (!s_any) return;
+        r0 = s_tile.row;
+        n = min(s_tile.count, cut.tile_rows);   // (more rows than max_q_len said)
+    } else {
+        r0 = tile * cut.tile_rows;
+        n = min(cut.tile_rows, p.num_rows - r0);
+    }
+    for (int i = tid; i < n; i += kThreads) {
+        Place at;
+        at.pos = 0;
+        at.stored = 0;
+        at.k_at = at.v_at = 0;
+        at.token = at.page = at.slot = 0;
+        if (p.kv_len) {
+            const int b = kFp8 ? s_tile.b : sequence_of(p, r0 + i);
+            if (b < 0) {
+                at.stored = -1;
+            } else {
+                long long t;
+                if (kFp8) {
+                    t = s_tile.first + i;
+                } else {
+                    const int row0 =
+                        p.q_row_offsets ? static_cast<int>(p.q_row_offsets[b]) : b;
+                    const int rows =
+                        p.q_row_offsets ? static_cast<int>(p.q_row_offsets[b + 1]) - row0 : 1;
+                    const uint32_t len = p.kv_len[b];
+                    t = static_cast<long long>(len) - rows + (r0 + i - row0);
+                    if ((t < 0 || t >= p.max_kv_len) && len != 0) atomicOr(p.err, kErrBadLength);
+                }
+                at.pos = static_cast<int>(max(t, 0LL));
+                if (t >= 0 && t < p.max_kv_len && p.k.heads > 0) {
+                    const int page = page_of(p, b, at.pos);
+                    const int slot = p.page_table ? at.pos & (p.page_size - 1) : at.pos;
+                    at.stored = page >= 0;
+                    at.token = at.pos;
+                    at.page = page;
+                    at.slot = slot;
+                    at.k_at = page * p.kc.page_stride + slot * p.kc.token_stride;
+                    at.v_at = page * p.vc.page_stride + slot * p.vc.token_stride;
+                }
+            }
+        }
+        if (p.positions) at.pos = p.positions[r0 + i];
+        places[i] = at;
+    }
+    __syncthreads();
+
+    // ---- angles: one entry (two pairs) a thread ---------------------------------
+    const int R = p.rope.rot_dim / 8, half = p.rope.rot_dim / 2;
+    const int q_vecs = p.q.heads > 0 ? p.q.dim / 8 : p.k.dim / 8;
+    if (half > 0 && h0 < p.q.heads + p.k.heads) {
+        for (int e = tid; e < n * 4 * L; e += kThreads) {
+            const int row = e / (4 * L), k = e / L & 3, i = e & (L - 1);
+            int a, b;
+            pair_of(kInter, q_vecs, R, i, a, b);
+            // half: channels 2k, 2k + 1 of the lane's vectors; interleaved: pair k of
+            // vector a and pair k of vector b
+            const int j0 = kInter ? 4 * a + k : 8 * i + 2 * k;
+            const int j1 = kInter ? 4 * b + k : j0 + 1;
+            float4 v = make_float4(1.f, 0.f, 1.f, 0.f);
+            if (a >= 0 && a < R) rope_cos_sin(p.rope, j0, places[row].pos, v.x, v.y);
+            if (b >= 0 && b < R) rope_cos_sin(p.rope, j1, places[row].pos, v.z, v.w);
+            angles[e] = v;
+        }
+    }
+    __syncthreads();
+
+    // ---- items ----------------------------------------------------------------------
+    int shift = 0;                                               // rows padded to 2^shift
+    while ((1 << shift) < n) ++shift;
+    const int step_heads = kItems * S >> shift;                  // heads in work at once
+    const int i0 = tid & (L - 1);
+    const int item0 = tid / L;
+
+    const auto kind_of = [&](int h) { return h < p.q.heads ? 0 : h < p.q.heads + p.k.heads ? 1 : 2; };
+
+#pragma unroll 1
+    for (int hs = h0; hs < h1; hs += step_heads) {
+        uint4 ra[S], rb[S];
+        int ca[S], cb[S];                                        // first channels, -1: none
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            const int item = item0 + s * kItems;
+            const int row = item & ((1 << shift) - 1), h = hs + (item >> shift);
+            ra[s] = rb[s] = make_uint4(0u, 0u, 0u, 0u);
+            ca[s] = cb[s] = -1;
+            if (row >= n || h >= h1) continue;
+            const int kind = kind_of(h);
+            const HeadRows &x = kind == 0 ? p.q : kind == 1 ? p.k : p.v;
+            const int head = h - (kind == 0 ? 0 : kind == 1 ? p.q.heads : p.q.heads + p.k.heads);
+            const int turning = kind < 2 ? R : 0;
+            int a, b;
+            pair_of(kInter, x.dim / 8, turning, i0, a, b);
+            const int start = x.rot_start / 8;
+            if (a >= 0) ca[s] = 8 * ordered(a, turning, start);
+            if (b >= 0) cb[s] = 8 * ordered(b, turning, start);
+            const uint16_t *src = x.in + (r0 + row) * x.in_row + head * x.in_head;
+            if (ca[s] >= 0) ra[s] = *reinterpret_cast<const uint4 *>(src + ca[s]);
+            if (cb[s] >= 0) rb[s] = *reinterpret_cast<const uint4 *>(src + cb[s]);
+        }
+        float2 ya[S][4], yb[S][4];
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            const int item = item0 + s * kItems;
+            const int row = min(item & ((1 << shift) - 1), n - 1), h = min(hs + (item >> shift), h1 - 1);
+            const int kind = kind_of(h);
+            const HeadRows &x = kind == 0 ? p.q : kind == 1 ? p.k : p.v;
+            unpack8(ra[s], ya[s]);
+            unpack8(rb[s], yb[s]);
+            if (cut.any_norm) {
+                float2 sq = make_float2(0.f, 0.f);               // (no vector: zeros)
+                if (ca[s] < x.norm_dim) add_squares(ya[s], sq);
+                if (cb[s] < x.norm_dim) add_squares(yb[s], sq);
+                float sum = sq.x + sq.y;
+#pragma unroll
+                for (int o = 1; o < L; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                if (x.norm_dim > 0) {
+                    const float inv = rsqrtf(fmaf(sum, x.mean, x.eps));
+                    const uint4 one = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
+                    if (ca[s] >= 0 && ca[s] < x.norm_dim)
+                        scale8(ya[s], x.norm ? *reinterpret_cast<const uint4 *>(x.norm + ca[s]) : one,
+                               inv);
+                    if (cb[s] >= 0 && cb[s] < x.norm_dim)
+                        scale8(yb[s], x.norm ? *reinterpret_cast<const uint4 *>(x.norm + cb[s]) : one,
+                               inv);
+                }
+            }
+            if (kind < 2 && half > 0) {
+                int a, b;
+                pair_of(kInter, x.dim / 8, R, i0, a, b);
+                const bool ta = a >= 0 && a < R, tb = b >= 0 && b < R;
+                const float4 *t = angles + row * 4 * L + i0;
+                if (ta) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float4 v = t[k * L];
+                        const float2 y = ya[s][k], z = yb[s][k];
+                        if (kInter) {
+                            ya[s][k] = make_float2(fmaf(y.x, v.x, -y.y * v.y), fmaf(y.y, v.x, y.x * v.y));
+                            if (tb)
+                                yb[s][k] =
+                                    make_float2(fmaf(z.x, v.z, -z.y * v.w), fmaf(z.y, v.z, z.x * v.w));
+                        } else {
+                            const float2 c = make_float2(v.x, v.z), n2 = make_float2(v.y, v.w);
+                            ya[s][k] = __ffma2_rn(y, c, __fmul2_rn(z, make_float2(-n2.x, -n2.y)));
+                            yb[s][k] = __ffma2_rn(z, c, __fmul2_rn(y, n2));
+                        }
+                    }
+                }
+            }
+            if (!kFp8 || kind == 0) {
+                const int head = h - (kind == 0 ? 0 : kind == 1 ? p.q.heads : p.q.heads + p.k.heads);
+                uint16_t *dst = nullptr;
+                const Place &at = places[row];
+                if (x.out) {
+                    if (at.stored >= 0) dst = x.out + (r0 + row) * x.out_row + head * x.out_head;
+                } else if (at.stored > 0) {
+                    const CacheOut &c = kind == 1 ? p.kc : p.vc;
+                    dst = reinterpret_cast<uint16_t *>(c.base) + (kind == 1 ? at.k_at : at.v_at) +
+                          head * c.head_stride;
+                }
+                // (values of a cache go through unchanged, NaN payloads included)
+                if (dst && ca[s] >= 0)
+                    *reinterpret_cast<uint4 *>(dst + ca[s]) = kind == 2 ? ra[s] : pack8(ya[s]);
+                if (dst && cb[s] >= 0)
+                    *reinterpret_cast<uint4 *>(dst + cb[s]) = kind == 2 ? rb[s] : pack8(yb[s]);
+            }
+        }
+        if (!kFp8) continue;
+
+        // ---- 8-bit cache: scales of the blocks -----------------------------------------
+        if (hs + step_heads <= p.q.heads) continue;              // queries only: uniform
+        __syncthreads();                                         // the last heads' scales are used
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            float top = 0.f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                top = fmaxf(fmaxf(fmaxf(finite_abs(ya[s][k].x), finite_abs(ya[s][k].y)), top),
+                            fmaxf(finite_abs(yb[s][k].x), finite_abs(yb[s][k].y)));
+#pragma unroll
+            for (int o = 1; o < L; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            if (i0 == 0) row_max[item0 + s * kItems] = top;      // (no item: 0)
+        }
+        __syncthreads();
+        // The thread of a block's first stored row in the tile takes the maximum over
+        // the block's rows, writes the scale and leaves 1 / scale in their places.
+        float ratio = 1.f;
+        int held = 0;
+        const int row = tid & ((1 << shift) - 1), h = hs + (tid >> shift);
+        if (tid < kItems * S && row < n && h < h1 && h >= p.q.heads && places[row].stored > 0) {
+            const int B = p.block_tokens, t = places[row].token;
+            const int base = t - row;                            // token of row 0, may be < 0
+            const int first = max(t / B * B - base, max(-base, 0));
+            const int last = min(t / B * B + B, min(base + n, p.max_kv_len)) - base;
+            if (row == first) {
+                float top = 0.f;
+                for (int i = first; i < last; ++i) top = fmaxf(top, row_max[(tid - row) + i]);
+                const bool is_k = h < p.q.heads + p.k.heads;
+                const int head = h - p.q.heads - (is_k ? 0 : p.k.heads);
+                const CacheOut &c = is_k ? p.kc : p.vc;
+                float *where = c.scale + places[row].page * c.scale_page +
+                               (places[row].slot / B) * c.scale_block + head * c.scale_head;
+                float scale = pow2i(scale_exponent(top));
+                if (row == 0 && base == s_tile.begin && t % B != 0) {
+                    held = t % B;                                // earlier tokens of the block
+                    const float old = *where;
+                    if (scale > old) ratio = old / scale; else scale = old;
+                }
+                *where = scale;
+                const float inv = 1.f / scale;
+                for (int i = first; i < last; ++i) row_max[(tid - row) + i] = inv;
+            }
+        }
+        // What the first block held, if its scale grew: one warp a head.
+        {
+            __shared__ float s_ratio[kThreads];
+            __shared__ int s_held[kThreads];
+            const int heads_now = min(step_heads, h1 - hs);
+            if (tid < kItems * S && row == 0 && (tid >> shift) < heads_now) {
+                s_ratio[tid >> shift] = ratio;
+                s_held[tid >> shift] = held;
+            }
+            __syncthreads();
+            for (int hh = tid >> 5; hh < heads_now; hh += kThreads / 32) {
+                const int g = hs + hh;
+                if (g < p.q.heads || s_held[hh] == 0 || s_ratio[hh] == 1.f) continue;
+                const bool is_k = g < p.q.heads + p.k.heads;
+                const int head = g - p.q.heads - (is_k ? 0 : p.k.heads);
+                const CacheOut &c = is_k ? p.kc : p.vc;
+                // the held tokens are the slots just before the tile's first row's
+                uint8_t *base = c.base + (is_k ? places[0].k_at : places[0].v_at) +
+                                head * c.head_stride;
+                for (int i = 1; i <= s_held[hh]; ++i) {
+                    uint32_t *w = reinterpret_cast<uint32_t *>(base - i * c.token_stride) + lane;
+                    const uint32_t old = *w;
+                    *w = encode4(decode2(old), decode2(old >> 16), s_ratio[hh]);
+                }
+            }
+        }
+        // ---- codes ---------------------------------------------------------------------
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            const int item = item0 + s * kItems;
+            const int irow = item & ((1 << shift) - 1), ih = hs + (item >> shift);
+            if (irow >= n || ih >= h1 || ih < p.q.heads) continue;
+            const Place &at = places[irow];
+            if (at.stored <= 0) continue;
+            const bool is_k = ih < p.q.heads + p.k.heads;
+            const int head = ih - p.q.heads - (is_k ? 0 : p.k.heads);
+            const CacheOut &c = is_k ? p.kc : p.vc;
+            const float f = row_max[item];
+            uint8_t *dst = c.base + (is_k ? at.k_at : at.v_at) + head * c.head_stride;
+            *reinterpret_cast<uint2 *>(dst + ca[s]) =
+                make_uint2(encode4(ya[s][0], ya[s][1], f), encode4(ya[s][2], ya[s][3], f));
+            *reinterpret_cast<uint2 *>(dst + cb[s]) =
+                make_uint2(encode4(yb[s][0], yb[s][1], f), encode4(yb[s][2], yb[s][3], f));
+        }
+    }
+}
+
+template <int L, int S, bool kInter, bool kFp8>
+cudaError_t launch(const RowsParams &p, const Cut &cut, long long tiles, cudaStream_t stream) {
+    const long long blocks = tiles * cut.chunks;
+    if (blocks == 0) return cudaSuccess;
+    if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+    const int rows = kFp8 && !p.q_row_offsets ? 1 : cut.tile_rows;
+    const size_t smem = p.rope.rot_dim > 0 ? size_t(rows) * 4 * L * sizeof(float4) : 0;
+    auto kern = head_tiles_kernel<L, S, kInter, kFp8>;
+    if (smem > 32768) {
+        const cudaError_t e = cudaFuncSetAttribute(
+            kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+        if (e != cudaSuccess) return e;
+    }
+    kern<<<static_cast<unsigned>(blocks), kThreads, smem, stream>>>(p, cut);
+    return cudaGetLastError();
+}
+
+}  // namespace tiles
+}  // namespace attn

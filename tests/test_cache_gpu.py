@@ -38,7 +38,8 @@ def rope_of(attn, rot, *, theta=500000.0, start=0, interleaved=False, **scaling)
 SHAPES = [(128, 128, 0, 128), (128, 64, 0, 0), (128, 32, 96, 128), (64, 64, 0, 64),
           (96, 96, 0, 96), (96, 32, 64, 0), (192, 64, 128, 0), (256, 128, 0, 256),
           (576, 64, 512, 512), (8, 8, 0, 8), (128, 20, 8, 128), (128, 2, 0, 0),
-          (1024, 1024, 0, 1024), (128, 0, 0, 128), (80, 40, 40, 80), (128, 16, 16, 64)]
+          (1024, 1024, 0, 1024), (128, 0, 0, 128), (80, 40, 40, 80), (128, 16, 16, 64),
+          (128, 128, 0, 64), (128, 24, 16, 128), (640, 512, 64, 640), (40, 8, 8, 40)]
 
 
 @pytest.mark.parametrize("dim,rot,start,nd", SHAPES)
