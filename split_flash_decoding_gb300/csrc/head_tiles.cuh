@@ -12,10 +12,12 @@
 // it, chosen so that a pair of channels is always in one lane: in the half layout
 // a vector of the rotated channels' lower half and the one rot_dim / 2 above it,
 // otherwise vector i and the one half the head above it, so that lanes side by
-// side read and write whole lines.  256 / L items are in work at once, S times
-// over: consecutive items are the tile's rows (padded to a power of two), then the
-// next heads', so that a tile of one row has many heads in work and a tile of 128
-// rows one or two.
+// side read and write whole lines.  256 / L items are in work at once: the tile's
+// rows (padded to a power of two), then the next heads', so that a tile of one row
+// has many heads in work.  S > 1: S times as many rows of one head.  A thread keeps
+// its place in the list of heads (pointers, channels, weights) and adds to it; the
+// first form, which found all that for every item, spent 437 instructions on 512
+// channels and took 142 us for 24768 rows of 48 heads.
 //
 // The 8-bit cache needs the largest value of a block of tokens before the first
 // code: a tile then is the new tokens of one sequence inside an aligned group of
@@ -221,8 +223,85 @@ __device__ __forceinline__ bool tile_tokens(const RowsParams &p, int tile, int l
     return true;
 }
 
+// One of a thread's items: where it is in the list of heads (q, then k, then v).
+struct Item {
+    enum { kNormA = 1, kNormB = 2, kTurnA = 4, kTurnB = 8 };
+    const uint16_t *src;              // its head vector
+    uint16_t *dst;                    // rows: its output; a cache: the head's offset
+    long long src_step, dst_step;     // to the item's next head
+    uint4 ga, gb;                     // the norm's weights of its channels
+    float mean, eps;
+    long long row_step;               // kItems rows of src
+    int row, h, h_end, kind, head;    // h_end: first head of the next kind
+    int ca, cb;                       // its two first channels; -1: none
+    int flags;
+    bool to_cache;
+
+    template <int kItems, bool kInter>
+    __device__ __forceinline__ void open(const RowsParams &p, int r0, int i0, int h1,
+                                         int step_heads) {
+        ca = cb = -1;
+        flags = 0;
+        kind = 0;
+        head = 0;
+        h_end = 0x7fffffff;
+        src = nullptr;
+        dst = nullptr;
+        src_step = dst_step = row_step = 0;
+        mean = eps = 0.f;
+        to_cache = false;
+        ga = gb = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);   // 1
+        if (h >= h1) return;
+        const int k0 = p.q.heads, v0 = p.q.heads + p.k.heads;
+        kind = h < k0 ? 0 : h < v0 ? 1 : 2;
+        const HeadRows &x = kind == 0 ? p.q : kind == 1 ? p.k : p.v;
+        head = h - (kind == 0 ? 0 : kind == 1 ? k0 : v0);
+        h_end = min(h1, kind == 0 ? k0 : kind == 1 ? v0 : h1);
+        const int turning = kind < 2 ? p.rope.rot_dim / 8 : 0, start = x.rot_start / 8;
+        int a, b;
+        pair_of(kInter, x.dim / 8, turning, i0, a, b);
+        if (a >= 0) ca = 8 * ordered(a, turning, start);
+        if (b >= 0) cb = 8 * ordered(b, turning, start);
+        src = x.in + (r0 + row) * x.in_row + head * x.in_head;
+        src_step = step_heads * x.in_head;
+        row_step = kItems * x.in_row;
+        to_cache = x.out == nullptr;
+        if (to_cache) {
+            const CacheOut &c = kind == 1 ? p.kc : p.vc;
+            dst = reinterpret_cast<uint16_t *>(c.base) + head * c.head_stride;
+            dst_step = step_heads * c.head_stride;
+        } else {
+            dst = x.out + (r0 + row) * x.out_row + head * x.out_head;
+            dst_step = step_heads * x.out_head;
+        }
+        mean = x.mean;
+        eps = x.eps;
+        if (a >= 0 && ca < x.norm_dim) {
+            flags |= kNormA;
+            if (x.norm) ga = *reinterpret_cast<const uint4 *>(x.norm + ca);
+        }
+        if (b >= 0 && cb < x.norm_dim) {
+            flags |= kNormB;
+            if (x.norm) gb = *reinterpret_cast<const uint4 *>(x.norm + cb);
+        }
+        if (a >= 0 && a < turning) flags |= kTurnA;
+        if (b >= 0 && b < turning) flags |= kTurnB;
+    }
+
+    // step_heads heads on
+    template <int kItems, bool kInter>
+    __device__ __forceinline__ void advance(const RowsParams &p, int r0, int i0, int h1,
+                                            int step_heads) {
+        h += step_heads;
+        head += step_heads;
+        src += src_step;
+        dst += dst_step;
+        if (h >= h_end) open<kItems, kInter>(p, r0, i0, h1, step_heads);
+    }
+};
+
 template <int L, int S, bool kInter, bool kFp8>
-__global__ void __launch_bounds__(kThreads, S == 1 ? 3 : 2)
+__global__ void __launch_bounds__(kThreads, S == 1 ? 4 : 2)
 head_tiles_kernel(const __grid_constant__ RowsParams p, const __grid_constant__ Cut cut) {
     using Sh = Shape<L, S>;
     constexpr int kItems = Sh::kItems;
@@ -255,6 +334,33 @@ head_tiles_kernel(const __grid_constant__ RowsParams p, const __grid_constant__ 
         r0 = tile * cut.tile_rows;
         n = min(cut.tile_rows, p.num_rows - r0);
     }
+
+    // ---- items: the first heads' loads go out before anything else ----------------
+    int shift = 0;                                               // rows padded to 2^shift
+    while ((1 << shift) < (S > 1 ? kItems * S : n)) ++shift;
+    const int step_heads = kItems * S >> shift;                  // heads in work at once
+    const int i0 = tid & (L - 1);
+    const int item0 = tid / L;
+    const int R = p.rope.rot_dim / 8, half = p.rope.rot_dim / 2;
+    Item it;
+    it.row = item0 & ((1 << shift) - 1);                         // and + kItems, S times
+    it.h = it.row < n ? h0 + (item0 >> shift) : h1;
+    it.row = min(it.row, n - 1);
+    it.open<kItems, kInter>(p, r0, i0, h1, step_heads);
+    uint4 ra[S], rb[S];
+    const auto load = [&]() {
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            ra[s] = rb[s] = make_uint4(0u, 0u, 0u, 0u);
+            if (S > 1 && it.row + s * kItems >= n) continue;
+            const uint16_t *src = it.src + s * it.row_step;
+            if (it.ca >= 0) ra[s] = *reinterpret_cast<const uint4 *>(src + it.ca);
+            if (it.cb >= 0) rb[s] = *reinterpret_cast<const uint4 *>(src + it.cb);
+        }
+    };
+    load();
+
+    // ---- places ----------------------------------------------------------------------
     for (int i = tid; i < n; i += kThreads) {
         Place at;
         at.pos = 0;
@@ -297,7 +403,6 @@ head_tiles_kernel(const __grid_constant__ RowsParams p, const __grid_constant__ 
     __syncthreads();
 
     // ---- angles: one entry (two pairs) a thread ---------------------------------
-    const int R = p.rope.rot_dim / 8, half = p.rope.rot_dim / 2;
     const int q_vecs = p.q.heads > 0 ? p.q.dim / 8 : p.k.dim / 8;
     if (half > 0 && h0 < p.q.heads + p.k.heads) {
         for (int e = tid; e < n * 4 * L; e += kThreads) {
@@ -316,111 +421,70 @@ head_tiles_kernel(const __grid_constant__ RowsParams p, const __grid_constant__ 
     }
     __syncthreads();
 
-    // ---- items ----------------------------------------------------------------------
-    int shift = 0;                                               // rows padded to 2^shift
-    while ((1 << shift) < n) ++shift;
-    const int step_heads = kItems * S >> shift;                  // heads in work at once
-    const int i0 = tid & (L - 1);
-    const int item0 = tid / L;
-
-    const auto kind_of = [&](int h) { return h < p.q.heads ? 0 : h < p.q.heads + p.k.heads ? 1 : 2; };
-
 #pragma unroll 1
     for (int hs = h0; hs < h1; hs += step_heads) {
-        uint4 ra[S], rb[S];
-        int ca[S], cb[S];                                        // first channels, -1: none
-#pragma unroll
-        for (int s = 0; s < S; ++s) {
-            const int item = item0 + s * kItems;
-            const int row = item & ((1 << shift) - 1), h = hs + (item >> shift);
-            ra[s] = rb[s] = make_uint4(0u, 0u, 0u, 0u);
-            ca[s] = cb[s] = -1;
-            if (row >= n || h >= h1) continue;
-            const int kind = kind_of(h);
-            const HeadRows &x = kind == 0 ? p.q : kind == 1 ? p.k : p.v;
-            const int head = h - (kind == 0 ? 0 : kind == 1 ? p.q.heads : p.q.heads + p.k.heads);
-            const int turning = kind < 2 ? R : 0;
-            int a, b;
-            pair_of(kInter, x.dim / 8, turning, i0, a, b);
-            const int start = x.rot_start / 8;
-            if (a >= 0) ca[s] = 8 * ordered(a, turning, start);
-            if (b >= 0) cb[s] = 8 * ordered(b, turning, start);
-            const uint16_t *src = x.in + (r0 + row) * x.in_row + head * x.in_head;
-            if (ca[s] >= 0) ra[s] = *reinterpret_cast<const uint4 *>(src + ca[s]);
-            if (cb[s] >= 0) rb[s] = *reinterpret_cast<const uint4 *>(src + cb[s]);
-        }
         float2 ya[S][4], yb[S][4];
 #pragma unroll
         for (int s = 0; s < S; ++s) {
-            const int item = item0 + s * kItems;
-            const int row = min(item & ((1 << shift) - 1), n - 1), h = min(hs + (item >> shift), h1 - 1);
-            const int kind = kind_of(h);
-            const HeadRows &x = kind == 0 ? p.q : kind == 1 ? p.k : p.v;
+            const Item &x = it;
+            const int row = min(x.row + s * kItems, n - 1);
             unpack8(ra[s], ya[s]);
             unpack8(rb[s], yb[s]);
             if (cut.any_norm) {
                 float2 sq = make_float2(0.f, 0.f);               // (no vector: zeros)
-                if (ca[s] < x.norm_dim) add_squares(ya[s], sq);
-                if (cb[s] < x.norm_dim) add_squares(yb[s], sq);
+                if (x.flags & Item::kNormA) add_squares(ya[s], sq);
+                if (x.flags & Item::kNormB) add_squares(yb[s], sq);
                 float sum = sq.x + sq.y;
 #pragma unroll
                 for (int o = 1; o < L; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                if (x.norm_dim > 0) {
-                    const float inv = rsqrtf(fmaf(sum, x.mean, x.eps));
-                    const uint4 one = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
-                    if (ca[s] >= 0 && ca[s] < x.norm_dim)
-                        scale8(ya[s], x.norm ? *reinterpret_cast<const uint4 *>(x.norm + ca[s]) : one,
-                               inv);
-                    if (cb[s] >= 0 && cb[s] < x.norm_dim)
-                        scale8(yb[s], x.norm ? *reinterpret_cast<const uint4 *>(x.norm + cb[s]) : one,
-                               inv);
-                }
+                const float inv = rsqrtf(fmaf(sum, x.mean, x.eps));
+                if (x.flags & Item::kNormA) scale8(ya[s], x.ga, inv);
+                if (x.flags & Item::kNormB) scale8(yb[s], x.gb, inv);
             }
-            if (kind < 2 && half > 0) {
-                int a, b;
-                pair_of(kInter, x.dim / 8, R, i0, a, b);
-                const bool ta = a >= 0 && a < R, tb = b >= 0 && b < R;
+            if (x.flags & Item::kTurnA) {
                 const float4 *t = angles + row * 4 * L + i0;
-                if (ta) {
+                const bool tb = x.flags & Item::kTurnB;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float4 v = t[k * L];
-                        const float2 y = ya[s][k], z = yb[s][k];
-                        if (kInter) {
-                            ya[s][k] = make_float2(fmaf(y.x, v.x, -y.y * v.y), fmaf(y.y, v.x, y.x * v.y));
-                            if (tb)
-                                yb[s][k] =
-                                    make_float2(fmaf(z.x, v.z, -z.y * v.w), fmaf(z.y, v.z, z.x * v.w));
-                        } else {
-                            const float2 c = make_float2(v.x, v.z), n2 = make_float2(v.y, v.w);
-                            ya[s][k] = __ffma2_rn(y, c, __fmul2_rn(z, make_float2(-n2.x, -n2.y)));
-                            yb[s][k] = __ffma2_rn(z, c, __fmul2_rn(y, n2));
-                        }
+                for (int k = 0; k < 4; ++k) {
+                    const float4 v = t[k * L];
+                    const float2 y = ya[s][k], z = yb[s][k];
+                    if (kInter) {
+                        ya[s][k] = make_float2(fmaf(y.x, v.x, -y.y * v.y), fmaf(y.y, v.x, y.x * v.y));
+                        if (tb)
+                            yb[s][k] =
+                                make_float2(fmaf(z.x, v.z, -z.y * v.w), fmaf(z.y, v.z, z.x * v.w));
+                    } else {
+                        const float2 c = make_float2(v.x, v.z), n2 = make_float2(v.y, v.w);
+                        ya[s][k] = __ffma2_rn(y, c, __fmul2_rn(z, make_float2(-n2.x, -n2.y)));
+                        yb[s][k] = __ffma2_rn(z, c, __fmul2_rn(y, n2));
                     }
                 }
             }
-            if (!kFp8 || kind == 0) {
-                const int head = h - (kind == 0 ? 0 : kind == 1 ? p.q.heads : p.q.heads + p.k.heads);
-                uint16_t *dst = nullptr;
+            if (!kFp8 || x.kind == 0) {
+                uint16_t *dst = x.dst;
                 const Place &at = places[row];
-                if (x.out) {
-                    if (at.stored >= 0) dst = x.out + (r0 + row) * x.out_row + head * x.out_head;
-                } else if (at.stored > 0) {
-                    const CacheOut &c = kind == 1 ? p.kc : p.vc;
-                    dst = reinterpret_cast<uint16_t *>(c.base) + (kind == 1 ? at.k_at : at.v_at) +
-                          head * c.head_stride;
+                bool store = at.stored >= 0 && (S == 1 || x.row + s * kItems < n);
+                if (!kFp8 && x.to_cache) {
+                    dst += x.kind == 1 ? at.k_at : at.v_at;
+                    store = store && at.stored > 0;
+                } else if (S > 1) {
+                    dst += s * kItems * p.q.out_row;             // (S > 1: queries alone)
                 }
-                // (values of a cache go through unchanged, NaN payloads included)
-                if (dst && ca[s] >= 0)
-                    *reinterpret_cast<uint4 *>(dst + ca[s]) = kind == 2 ? ra[s] : pack8(ya[s]);
-                if (dst && cb[s] >= 0)
-                    *reinterpret_cast<uint4 *>(dst + cb[s]) = kind == 2 ? rb[s] : pack8(yb[s]);
+                // (what is neither normed nor rotated goes as it is, NaN payloads too)
+                const bool plain = !(x.flags & (Item::kNormA | Item::kNormB | Item::kTurnA));
+                if (store && x.ca >= 0)
+                    *reinterpret_cast<uint4 *>(dst + x.ca) = plain ? ra[s] : pack8(ya[s]);
+                if (store && x.cb >= 0)
+                    *reinterpret_cast<uint4 *>(dst + x.cb) = plain ? rb[s] : pack8(yb[s]);
             }
         }
-        if (!kFp8) continue;
+        if (!kFp8 || hs + step_heads <= p.q.heads) {             // queries only: uniform
+            it.advance<kItems, kInter>(p, r0, i0, h1, step_heads);
+            load();
+            continue;
+        }
 
         // ---- 8-bit cache: scales of the blocks -----------------------------------------
-        if (hs + step_heads <= p.q.heads) continue;              // queries only: uniform
         __syncthreads();                                         // the last heads' scales are used
 #pragma unroll
         for (int s = 0; s < S; ++s) {
@@ -492,21 +556,20 @@ head_tiles_kernel(const __grid_constant__ RowsParams p, const __grid_constant__ 
         // ---- codes ---------------------------------------------------------------------
 #pragma unroll
         for (int s = 0; s < S; ++s) {
-            const int item = item0 + s * kItems;
-            const int irow = item & ((1 << shift) - 1), ih = hs + (item >> shift);
-            if (irow >= n || ih >= h1 || ih < p.q.heads) continue;
-            const Place &at = places[irow];
-            if (at.stored <= 0) continue;
-            const bool is_k = ih < p.q.heads + p.k.heads;
-            const int head = ih - p.q.heads - (is_k ? 0 : p.k.heads);
-            const CacheOut &c = is_k ? p.kc : p.vc;
-            const float f = row_max[item];
-            uint8_t *dst = c.base + (is_k ? at.k_at : at.v_at) + head * c.head_stride;
-            *reinterpret_cast<uint2 *>(dst + ca[s]) =
+            const Item &x = it;
+            const int row = x.row + s * kItems;
+            if (x.ca < 0 || x.kind == 0 || row >= n || places[row].stored <= 0) continue;
+            const Place &at = places[row];
+            const CacheOut &c = x.kind == 1 ? p.kc : p.vc;
+            const float f = row_max[item0 + s * kItems];
+            uint8_t *dst = c.base + (x.kind == 1 ? at.k_at : at.v_at) + x.head * c.head_stride;
+            *reinterpret_cast<uint2 *>(dst + x.ca) =
                 make_uint2(encode4(ya[s][0], ya[s][1], f), encode4(ya[s][2], ya[s][3], f));
-            *reinterpret_cast<uint2 *>(dst + cb[s]) =
+            *reinterpret_cast<uint2 *>(dst + x.cb) =
                 make_uint2(encode4(yb[s][0], yb[s][1], f), encode4(yb[s][2], yb[s][3], f));
         }
+        it.advance<kItems, kInter>(p, r0, i0, h1, step_heads);
+        load();
     }
 }
 

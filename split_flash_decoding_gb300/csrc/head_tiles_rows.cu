@@ -23,38 +23,29 @@ bool head_tiles_fit(const RowsParams &p) {
 
 namespace {
 
-template <int L, int S>
-cudaError_t launch_shape(const RowsParams &p, int tile_rows, int chunk_heads, cudaStream_t stream) {
+template <int L>
+cudaError_t launch_lanes(const RowsParams &p, cudaStream_t stream) {
+    // Tiles of 8 rows: a step then reads 256 / L / 8 heads side by side of every row
+    // (1 KB at 128 channels), and the angles of a tile are two a thread.  A CTA
+    // takes all heads of its rows once the tiles fill the GPU, fewer below.
+    // us for 24768 rows of 48 heads / 8191 of 40 with norm: 4 rows 136 / 40, 8 rows
+    // 132 / 38, 16 rows 135 / 53, 32 rows and 16 heads 135 / 39.
+    constexpr int kWave = 4 * 152;                 // resident CTAs
     Cut cut;
     cut.heads = p.q.heads + p.k.heads + p.v.heads;
     cut.any_norm = (p.q.heads > 0 && p.q.norm_dim > 0) || (p.k.heads > 0 && p.k.norm_dim > 0);
-    cut.tile_rows = tile_rows;
-    cut.chunk_heads = chunk_heads;
-    cut.chunks = (cut.heads + chunk_heads - 1) / chunk_heads;
-    const long long tiles = (static_cast<long long>(p.num_rows) + tile_rows - 1) / tile_rows;
-    return p.rope.interleaved ? launch<L, S, true, false>(p, cut, tiles, stream)
-                              : launch<L, S, false, false>(p, cut, tiles, stream);
-}
-
-template <int L>
-cudaError_t launch_lanes(const RowsParams &p, cudaStream_t stream) {
-    const int heads = p.q.heads + p.k.heads + p.v.heads;
-    constexpr int kWave = 2 * 152;                 // CTAs of a wave
-    const long long items = static_cast<long long>(p.num_rows) * heads;
-    if (items < static_cast<long long>(kWave) * (kThreads / L) * 4) {
-        // few rows: small tiles, so that the angles take no time, one step a CTA
-        int rows = 8;
-        while (rows > 1 && rows / 2 >= p.num_rows) rows /= 2;
-        return launch_shape<L, 1>(p, rows, Shape<L, 1>::kItems / rows, stream);
-    }
-    // Many: the angles of a tile serve up to 16 heads a CTA, fewer where the tiles
-    // would not fill the GPU.
-    constexpr int rows = Shape<L, 4>::kMaxRows;
-    const long long tiles = (p.num_rows + rows - 1) / rows;
-    long long chunk = heads * tiles / kWave;
-    if (chunk > 16) chunk = 16;
-    if (chunk < 1) chunk = 1;
-    return launch_shape<L, 4>(p, rows, static_cast<int>(chunk), stream);
+    cut.tile_rows = 8;
+    while (cut.tile_rows > 1 && cut.tile_rows / 2 >= p.num_rows) cut.tile_rows /= 2;
+    const long long tiles = (static_cast<long long>(p.num_rows) + cut.tile_rows - 1) / cut.tile_rows;
+    const int step = Shape<L, 1>::kItems / cut.tile_rows;        // heads at once
+    const int steps = (cut.heads + step - 1) / step;
+    long long per_cta = steps * tiles / kWave;
+    if (per_cta < 1) per_cta = 1;
+    if (per_cta > steps) per_cta = steps;
+    cut.chunk_heads = static_cast<int>(per_cta) * step;
+    cut.chunks = (cut.heads + cut.chunk_heads - 1) / cut.chunk_heads;
+    return p.rope.interleaved ? launch<L, 1, true, false>(p, cut, tiles, stream)
+                              : launch<L, 1, false, false>(p, cut, tiles, stream);
 }
 
 }  // namespace
