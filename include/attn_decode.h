@@ -593,8 +593,9 @@ int attn_append_kv_fp8(const attn_head_rows_t *q, const attn_head_rows_t *k,
  *   max_q_len   max_q_len * group <= 16 (longer row runs:
  *               ATTN_ERR_UNSUPPORTED).
  *   workspace   device, 256-byte aligned, of at least
- *               attn_decode_fp8_workspace bytes.  Contents on entry are
- *               ignored.  Calls that can overlap on the GPU need one each.
+ *               attn_decode_fp8_workspace bytes; may be NULL when max_kv_len <=
+ *               128.  Contents on entry are ignored.  Calls that can overlap on
+ *               the GPU need one each.
  * The other arguments as for attn_decode (batch <= 2048).  out and lse are
  * those of attn_decode on the cache code * scale; a code of NaN in a visible
  * token gives NaN.  Launches the partition kernel and the split-K reduce.

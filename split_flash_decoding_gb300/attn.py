@@ -10,6 +10,7 @@ fallback: if libattn.so has not been built, importing the library fails.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -183,6 +184,15 @@ def _stream_handle(stream) -> Optional[int]:
     return stream.cuda_stream
 
 
+# The entry points that fill a cache are called once a layer and step with little
+# work each, so their host side is kept short: descriptors are built in one
+# call, the stream is asked for by its device.
+def _stream_of(stream, device: int) -> int:
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device)
+    return stream.cuda_stream
+
+
 # ---------------------------------------------------------------------------
 # cache descriptors
 # ---------------------------------------------------------------------------
@@ -201,23 +211,15 @@ def kv_descriptor(cache: torch.Tensor, page_table: Optional[torch.Tensor] = None
                         f"cache must be {dtype}")
     if cache.dim() != 4 or cache.stride(3) != 1:
         raise ValueError("cache must be 4-D with contiguous channels")
-    d = attn_kv_t()
-    d.base = cache.data_ptr()
-    d.page_stride = cache.stride(0)
-    d.token_stride = cache.stride(1)
-    d.head_stride = cache.stride(2)
-    d.page_size = cache.shape[1]
-    d.num_pages = cache.shape[0]
-    if page_table is not None:
-        if page_table.dtype != torch.int32 or page_table.dim() != 2 or not page_table.is_contiguous():
-            raise ValueError("page_table must be a contiguous int32 [batch, max_pages] tensor")
-        d.page_table = page_table.data_ptr()
-        d.max_pages = page_table.shape[1]
-    else:
-        d.page_table = None
-        d.max_pages = 0
-    d.reserved = 0
-    return d
+    pages, page_size, _, _ = cache.shape
+    page_stride, token_stride, head_stride, _ = cache.stride()
+    if page_table is None:
+        return attn_kv_t(cache.data_ptr(), page_stride, token_stride, head_stride, page_size,
+                         pages, None, 0, 0)
+    if page_table.dtype != torch.int32 or page_table.dim() != 2 or not page_table.is_contiguous():
+        raise ValueError("page_table must be a contiguous int32 [batch, max_pages] tensor")
+    return attn_kv_t(cache.data_ptr(), page_stride, token_stride, head_stride, page_size, pages,
+                     page_table.data_ptr(), page_table.shape[1], 0)
 
 
 def scale_descriptor(scale: torch.Tensor, cache: torch.Tensor) -> attn_kv_scale_t:
@@ -228,13 +230,9 @@ def scale_descriptor(scale: torch.Tensor, cache: torch.Tensor) -> attn_kv_scale_
         raise ValueError("scales must be an fp32 [pages, blocks, heads] tensor")
     pages, page_size, heads, _ = cache.shape
     blocks = scale.shape[1]
-    if scale.shape[0] != pages or scale.shape[2] != heads or blocks == 0 or page_size % blocks:
+    if scale.shape != (pages, blocks, heads) or blocks == 0 or page_size % blocks:
         raise ValueError(f"scales {tuple(scale.shape)} do not fit a cache {tuple(cache.shape)}")
-    d = attn_kv_scale_t()
-    d.base = scale.data_ptr()
-    d.page_stride, d.block_stride, d.head_stride = scale.stride()
-    d.block_tokens = page_size // blocks
-    return d
+    return attn_kv_scale_t(scale.data_ptr(), *scale.stride(), page_size // blocks, 0)
 
 
 class Rope:
@@ -250,6 +248,7 @@ class Rope:
         self.start = start
         self.struct = attn_rope_t(turns.data_ptr(), 2 * turns.shape[0], 1 if interleaved else 0,
                                   mscale, 0)
+        self.ref = ctypes.byref(self.struct)
 
 
 def rope_turns(rot_dim: int, theta: float, *, scaling: str = "plain", factor: float = 1.0,
@@ -280,25 +279,25 @@ def _head_rows(x: torch.Tensor, out: Optional[torch.Tensor], norm: Optional[torc
                eps: float, rot_start: int) -> attn_head_rows_t:
     if x.dtype != torch.bfloat16:
         raise TypeError("head rows must be bf16")
-    if x.dim() != 3 or (x.stride(2) != 1 and x.shape[2] != 1):
+    if x.dim() != 3:
         raise ValueError("head rows must be [rows, heads, dim] with contiguous channels")
-    d = attn_head_rows_t()
-    d.in_ = x.data_ptr()
-    d.in_row_stride, d.in_head_stride, _ = x.stride()
-    _, d.num_heads, d.dim = x.shape
+    row, head, channel = x.stride()
+    _, heads, dim = x.shape
+    if channel != 1 and dim != 1:
+        raise ValueError("head rows must be [rows, heads, dim] with contiguous channels")
+    dst, out_row, out_head = None, 0, 0
     if out is not None:
-        if out.dtype != torch.bfloat16 or out.shape != x.shape or out.stride(2) != 1:
+        out_row, out_head, channel = out.stride()
+        if out.dtype != torch.bfloat16 or out.shape != x.shape or channel != 1:
             raise ValueError("out must be bf16, shaped as the input, with contiguous channels")
-        d.out = out.data_ptr()
-        d.out_row_stride, d.out_head_stride, _ = out.stride()
+        dst = out.data_ptr()
+    weight, norm_dim = None, 0
     if norm is not None:
         if norm.dtype != torch.bfloat16 or norm.dim() != 1 or not norm.is_contiguous():
             raise ValueError("norm weights must be contiguous bf16 [norm_dim]")
-        d.norm_weight = norm.data_ptr()
-        d.norm_dim = norm.shape[0]
-        d.norm_eps = eps
-    d.rot_start = rot_start
-    return d
+        weight, norm_dim = norm.data_ptr(), norm.shape[0]
+    return attn_head_rows_t(x.data_ptr(), row, head, dst, out_row, out_head, weight, eps,
+                            norm_dim, heads, dim, rot_start, 0)
 
 
 def _int32(t: Optional[torch.Tensor], n: int, what: str):
@@ -313,19 +312,19 @@ def _ref(d):
     return None if d is None else ctypes.byref(d)
 
 
-def _on_current_device(*tensors):
-    """The library works on the current device: refuse tensors from elsewhere."""
-    current = -1
+def _on_current_device(first: torch.Tensor, *tensors) -> int:
+    """The library works on the current device: refuse tensors from elsewhere.
+    Returns the device's index."""
+    device = first.get_device()
+    if device < 0:
+        raise ValueError("every tensor must be on the GPU")
     for t in tensors:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError("every tensor must be on the GPU")
-        if current < 0:
-            current = torch.cuda.current_device()
-        if t.get_device() != current:
-            raise ValueError(f"a tensor is on cuda:{t.get_device()}, the current device is "
-                             f"cuda:{current}")
+        if t is not None and t.get_device() != device:
+            raise ValueError("every tensor must be on the GPU, and on the same")
+    current = torch.cuda.current_device()
+    if device != current:
+        raise ValueError(f"the tensors are on cuda:{device}, the current device is cuda:{current}")
+    return device
 
 
 # ---------------------------------------------------------------------------
@@ -546,17 +545,17 @@ def attn_qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor] = None,
     qd = _head_rows(q, q_out, q_norm, eps, start)
     kd = None if k is None else _head_rows(k, k_out, k_norm, eps, start)
     pos = _int32(positions, rows, "positions")
-    _on_current_device(q, k, q_out, k_out, positions, q_norm, k_norm,
-                       None if rope is None else rope.turns)
+    device = _on_current_device(q, k, q_out, k_out, positions, q_norm, k_norm,
+                                None if rope is None else rope.turns)
     _check("attn_qk_norm_rope",
            lib().attn_qk_norm_rope(ctypes.byref(qd), _ref(kd),
-                                   None if rope is None else ctypes.byref(rope.struct), pos, rows,
-                                   _stream_handle(stream)))
+                                   None if rope is None else rope.ref, pos, rows,
+                                   _stream_of(stream, device)))
     return q_out, k_out
 
 
 def _append_args(k, v, k_cache, v_cache, kv_len, page_table, q, q_out, q_row_offsets, rope,
-                 positions, q_norm, k_norm, eps, dtype):
+                 positions, q_norm, k_norm, eps, dtype, *scales):
     rows, batch = k.shape[0], kv_len.shape[0]
     if (v is None) != (v_cache is None):
         raise ValueError("v and v_cache go together")
@@ -576,13 +575,14 @@ def _append_args(k, v, k_cache, v_cache, kv_len, page_table, q, q_out, q_row_off
     kc = kv_descriptor(k_cache, page_table, dtype)
     vc = None if v is None else kv_descriptor(v_cache, page_table, dtype)
     head = (_ref(qd), ctypes.byref(kd), _ref(vd),
-            None if rope is None else ctypes.byref(rope.struct),
+            None if rope is None else rope.ref,
             _int32(positions, rows, "positions"), ctypes.byref(kc), _ref(vc))
     tail = (_int32(kv_len, batch, "kv_len"), _int32(q_row_offsets, batch + 1, "q_row_offsets"),
             batch, rows)
-    _on_current_device(k, v, k_cache, v_cache, kv_len, page_table, q, q_out, q_row_offsets,
-                       positions, q_norm, k_norm, None if rope is None else rope.turns)
-    return q_out, head, tail
+    device = _on_current_device(k, v, k_cache, v_cache, kv_len, page_table, q, q_out,
+                                q_row_offsets, positions, q_norm, k_norm,
+                                None if rope is None else rope.turns, *scales)
+    return q_out, head, tail, device
 
 
 def attn_append_kv(k: torch.Tensor, v: Optional[torch.Tensor], k_cache: torch.Tensor,
@@ -600,11 +600,11 @@ def attn_append_kv(k: torch.Tensor, v: Optional[torch.Tensor], k_cache: torch.Te
     for kv_descriptor; kv_len int32 [batch], the new tokens included;
     q_row_offsets int32 [batch + 1] or None (one row per sequence).  k and q
     are normed (q_norm, k_norm) and rotated (rope) on the way.  Returns q_out."""
-    q_out, head, tail = _append_args(k, v, k_cache, v_cache, kv_len, page_table, q, q_out,
-                                     q_row_offsets, rope, positions, q_norm, k_norm, eps,
-                                     torch.bfloat16)
+    q_out, head, tail, device = _append_args(k, v, k_cache, v_cache, kv_len, page_table, q, q_out,
+                                             q_row_offsets, rope, positions, q_norm, k_norm, eps,
+                                             torch.bfloat16)
     _check("attn_append_kv",
-           lib().attn_append_kv(*head, *tail, max_kv_len, _stream_handle(stream)))
+           lib().attn_append_kv(*head, *tail, max_kv_len, _stream_of(stream, device)))
     return q_out
 
 
@@ -620,15 +620,19 @@ def attn_append_kv_fp8(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
     """attn_append_kv into caches of torch.float8_e4m3fn with fp32 scales
     [pages, page_size / block_tokens, num_kv_heads] (attn_append_kv_fp8), head
     dimension 128.  max_q_len bounds the rows of any sequence.  Returns q_out."""
-    q_out, head, tail = _append_args(k, v, k_cache, v_cache, kv_len, page_table, q, q_out,
-                                     q_row_offsets, rope, positions, q_norm, k_norm, eps,
-                                     torch.float8_e4m3fn)
+    q_out, head, tail, device = _append_args(k, v, k_cache, v_cache, kv_len, page_table, q, q_out,
+                                             q_row_offsets, rope, positions, q_norm, k_norm, eps,
+                                             torch.float8_e4m3fn, k_scale, v_scale)
     ks, vs = scale_descriptor(k_scale, k_cache), scale_descriptor(v_scale, v_cache)
-    _on_current_device(k_scale, v_scale)
     _check("attn_append_kv_fp8",
            lib().attn_append_kv_fp8(*head, ctypes.byref(ks), ctypes.byref(vs), *tail, max_q_len,
-                                    max_kv_len, _stream_handle(stream)))
+                                    max_kv_len, _stream_of(stream, device)))
     return q_out
+
+
+@functools.lru_cache(maxsize=1024)
+def _fp8_workspace(device: int, batch: int, num_q_heads: int, group: int) -> int:
+    return attn_decode_fp8_workspace(batch, num_q_heads, group)
 
 
 def attn_decode_fp8_workspace(batch: int, num_q_heads: int, group: int, num_sms: int = 0) -> int:
@@ -678,15 +682,16 @@ def attn_decode_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     elif lse is not None and (lse.dtype != torch.float32 or lse.shape != (rows, hq) or
                               not lse.is_contiguous()):
         raise ValueError("lse must be contiguous fp32 [rows, num_q_heads]")
-    _on_current_device(q, k_cache, v_cache, k_scale, v_scale, kv_len, page_table, sink,
-                       q_row_offsets, workspace, out, lse)
-    ws, ws_size = _workspace(attn_decode_fp8_workspace(batch, hq, group), q.device, workspace)
+    device = _on_current_device(q, k_cache, v_cache, k_scale, v_scale, kv_len, page_table, sink,
+                                q_row_offsets, workspace, out, lse)
+    need = 0 if max_kv_len <= 128 else _fp8_workspace(device, batch, hq, group)
+    ws, ws_size = _workspace(need, q.device, workspace)
     _check("attn_decode_fp8",
            lib().attn_decode_fp8(q.data_ptr(), ctypes.byref(kd), ctypes.byref(vd),
                                  ctypes.byref(ks), ctypes.byref(vs), lens, offs, batch, rows, hq,
                                  group, d, max_q_len, max_kv_len, scale, _ptr(sink),
                                  1 if causal else 0, _ptr(ws), ws_size, out.data_ptr(), _ptr(lse),
-                                 _stream_handle(stream)))
+                                 _stream_of(stream, device)))
     return out, lse
 
 

@@ -325,12 +325,14 @@ extern "C" int attn_decode_fp8(const void *q, const attn_kv_t *k, const attn_kv_
     if (!same_layout(k, v)) return ATTN_ERR_UNSUPPORTED;
     if ((st = check_scale(k_scale, k)) || (st = check_scale(v_scale, v))) return st;
     if (k_scale->block_tokens != v_scale->block_tokens) return ATTN_ERR_UNSUPPORTED;
+    // Units of one tile are never cut: no partials, nothing to merge.
+    const bool cut = max_kv_len > kGqaTcTileKeys;
     int sms = 0;
-    if (!workspace || !aligned(workspace, 256)) return ATTN_ERR_WORKSPACE;
+    if (cut && (!workspace || !aligned(workspace, 256))) return ATTN_ERR_WORKSPACE;
     if ((st = device_sms(&sms))) return st;
     const int ctas = fp8_decode_ctas(sms);
     size_t off_m = 0, off_l = 0, off_table = 0;
-    if (workspace_bytes < fp8_layout(ctas, static_cast<long long>(batch) * hkv, &off_m, &off_l,
+    if (cut && workspace_bytes < fp8_layout(ctas, static_cast<long long>(batch) * hkv, &off_m, &off_l,
                                      &off_table))
         return ATTN_ERR_WORKSPACE;
 
@@ -357,11 +359,13 @@ extern "C" int attn_decode_fp8(const void *q, const attn_kv_t *k, const attn_kv_
     p.max_kv_len = max_kv_len;
     while (p.head_shift < 3 && hkv % (2 << p.head_shift) == 0) ++p.head_shift;
     p.head_groups = hkv >> p.head_shift;
-    uint8_t *ws = static_cast<uint8_t *>(workspace);
-    p.ws_o = reinterpret_cast<float *>(ws);
-    p.ws_m = reinterpret_cast<float *>(ws + off_m);
-    p.ws_l = reinterpret_cast<float *>(ws + off_l);
-    p.unit_slots = reinterpret_cast<int2 *>(ws + off_table);
+    if (cut) {
+        uint8_t *ws = static_cast<uint8_t *>(workspace);
+        p.ws_o = reinterpret_cast<float *>(ws);
+        p.ws_m = reinterpret_cast<float *>(ws + off_m);
+        p.ws_l = reinterpret_cast<float *>(ws + off_l);
+        p.unit_slots = reinterpret_cast<int2 *>(ws + off_table);
+    }
     p.box_rows = k->page_table && k->page_size < kGqaTcTileKeys ? k->page_size : kGqaTcTileKeys;
     if ((st = encode_kv_map_8bit(&p.k_map, k->base, k->token_stride, k->head_stride,
                                  k->page_stride, head_dim, k->page_size, hkv, k->num_pages,
@@ -383,8 +387,7 @@ extern "C" int attn_decode_fp8(const void *q, const attn_kv_t *k, const attn_kv_
     while ((1 << p.block_shift) < k_scale->block_tokens) ++p.block_shift;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     st = map_cuda(launch_gqa_decode_fp8(p, ctas, s));
-    // Units of one tile are never cut: nothing to merge.
-    if (st || max_kv_len <= kGqaTcTileKeys) return st;
+    if (st || !cut) return st;
     ReduceParams r;
     std::memset(&r, 0, sizeof(r));
     r.ws_o = p.ws_o;

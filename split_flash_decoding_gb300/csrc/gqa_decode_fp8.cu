@@ -844,7 +844,7 @@ gqa_decode_fp8_kernel(const __grid_constant__ Fp8DecodeParams p) {
             }
             tc::fence_before_sync();
             // The CTA holding the unit's first tile publishes where its pieces are.
-            if (it.first && threadIdx.x == 0)
+            if (it.first && threadIdx.x == 0 && p.unit_slots)
                 p.unit_slots[it.b * (p.num_q_heads / G) + it.kvh] =
                     make_int2(it.slot, fp8_pieces(p, cum, walk, it));
             g += it.ntiles;
