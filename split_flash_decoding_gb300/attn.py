@@ -235,6 +235,27 @@ def scale_descriptor(scale: torch.Tensor, cache: torch.Tensor) -> attn_kv_scale_
     return attn_kv_scale_t(scale.data_ptr(), *scale.stride(), page_size // blocks, 0)
 
 
+# K and V usually have one layout: the second descriptor then is the first with
+# another address.
+
+def _kv_pair(k_cache, v_cache, page_table, dtype):
+    k = kv_descriptor(k_cache, page_table, dtype)
+    if (v_cache.shape == k_cache.shape and v_cache.stride() == k_cache.stride() and
+            v_cache.dtype == dtype):
+        return k, attn_kv_t(v_cache.data_ptr(), k.page_stride, k.token_stride, k.head_stride,
+                            k.page_size, k.num_pages, k.page_table, k.max_pages, 0)
+    return k, kv_descriptor(v_cache, page_table, dtype)
+
+
+def _scale_pair(k_scale, v_scale, k_cache, v_cache):
+    k = scale_descriptor(k_scale, k_cache)
+    if (v_scale.shape == k_scale.shape and v_scale.stride() == k_scale.stride() and
+            v_scale.dtype == torch.float32 and v_cache.shape == k_cache.shape):
+        return k, attn_kv_scale_t(v_scale.data_ptr(), k.page_stride, k.block_stride, k.head_stride,
+                                  k.block_tokens, 0)
+    return k, scale_descriptor(v_scale, v_cache)
+
+
 class Rope:
     """A rotation: turns int64 [rot_dim / 2] on the device (rope_turns), the
     pair layout (interleaved: channels 2i and 2i + 1; otherwise i and i +
@@ -306,10 +327,6 @@ def _int32(t: Optional[torch.Tensor], n: int, what: str):
     if t.dtype not in (torch.int32, torch.uint32) or t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous int32 [{n}] tensor")
     return t.data_ptr()
-
-
-def _ref(d):
-    return None if d is None else ctypes.byref(d)
 
 
 def _on_current_device(first: torch.Tensor, *tensors) -> int:
@@ -548,8 +565,7 @@ def attn_qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor] = None,
     device = _on_current_device(q, k, q_out, k_out, positions, q_norm, k_norm,
                                 None if rope is None else rope.turns)
     _check("attn_qk_norm_rope",
-           lib().attn_qk_norm_rope(ctypes.byref(qd), _ref(kd),
-                                   None if rope is None else rope.ref, pos, rows,
+           lib().attn_qk_norm_rope(qd, kd, None if rope is None else rope.ref, pos, rows,
                                    _stream_of(stream, device)))
     return q_out, k_out
 
@@ -559,24 +575,32 @@ def _append_args(k, v, k_cache, v_cache, kv_len, page_table, q, q_out, q_row_off
     rows, batch = k.shape[0], kv_len.shape[0]
     if (v is None) != (v_cache is None):
         raise ValueError("v and v_cache go together")
-    if (v is not None and v.shape[0] != rows) or (q is not None and q.shape[0] != rows):
-        raise ValueError("q, k and v must have the same rows")
-    if q is not None and q_out is None:
-        q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-    for x, c in ((k, k_cache), (v, v_cache)):
-        if x is not None and x.shape[1:] != c.shape[2:]:
-            raise ValueError(f"rows {tuple(x.shape)} do not fit a cache {tuple(c.shape)}")
+    if k.shape[1:] != k_cache.shape[2:]:
+        raise ValueError(f"rows {tuple(k.shape)} do not fit a cache {tuple(k_cache.shape)}")
     if page_table is not None and page_table.shape[0] != batch:
         raise ValueError("page_table must have one row per sequence")
-    start = 0 if rope is None else rope.start
-    qd = None if q is None else _head_rows(q, q_out, q_norm, eps, start)
+    start, rope_ref = (0, None) if rope is None else (rope.start, rope.ref)
+    qd = vd = vc = None
+    if q is not None:
+        if q.shape[0] != rows:
+            raise ValueError("q, k and v must have the same rows")
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        qd = _head_rows(q, q_out, q_norm, eps, start)
     kd = _head_rows(k, None, k_norm, eps, start)
-    vd = None if v is None else _head_rows(v, None, None, eps, 0)
-    kc = kv_descriptor(k_cache, page_table, dtype)
-    vc = None if v is None else kv_descriptor(v_cache, page_table, dtype)
-    head = (_ref(qd), ctypes.byref(kd), _ref(vd),
-            None if rope is None else rope.ref,
-            _int32(positions, rows, "positions"), ctypes.byref(kc), _ref(vc))
+    if v is None:
+        kc = kv_descriptor(k_cache, page_table, dtype)
+    else:
+        if v.shape[0] != rows or v.shape[1:] != v_cache.shape[2:]:
+            raise ValueError(f"rows {tuple(v.shape)} do not fit {rows} rows and a cache "
+                             f"{tuple(v_cache.shape)}")
+        if v.shape == k.shape and v.stride() == k.stride() and v.dtype == torch.bfloat16:
+            vd = attn_head_rows_t(v.data_ptr(), kd.in_row_stride, kd.in_head_stride, None, 0, 0,
+                                  None, 0.0, 0, kd.num_heads, kd.dim, 0, 0)
+        else:
+            vd = _head_rows(v, None, None, eps, 0)
+        kc, vc = _kv_pair(k_cache, v_cache, page_table, dtype)
+    head = (qd, kd, vd, rope_ref, _int32(positions, rows, "positions"), kc, vc)
     tail = (_int32(kv_len, batch, "kv_len"), _int32(q_row_offsets, batch + 1, "q_row_offsets"),
             batch, rows)
     device = _on_current_device(k, v, k_cache, v_cache, kv_len, page_table, q, q_out,
@@ -623,10 +647,9 @@ def attn_append_kv_fp8(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
     q_out, head, tail, device = _append_args(k, v, k_cache, v_cache, kv_len, page_table, q, q_out,
                                              q_row_offsets, rope, positions, q_norm, k_norm, eps,
                                              torch.float8_e4m3fn, k_scale, v_scale)
-    ks, vs = scale_descriptor(k_scale, k_cache), scale_descriptor(v_scale, v_cache)
     _check("attn_append_kv_fp8",
-           lib().attn_append_kv_fp8(*head, ctypes.byref(ks), ctypes.byref(vs), *tail, max_q_len,
-                                    max_kv_len, _stream_of(stream, device)))
+           lib().attn_append_kv_fp8(*head, *_scale_pair(k_scale, v_scale, k_cache, v_cache), *tail,
+                                    max_q_len, max_kv_len, _stream_of(stream, device)))
     return q_out
 
 
@@ -658,9 +681,8 @@ def attn_decode_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     128; everything else as for attn_decode.  Returns (out, lse)."""
     rows, hq, d = q.shape
     batch = kv_len.shape[0]
-    kd = kv_descriptor(k_cache, page_table, torch.float8_e4m3fn)
-    vd = kv_descriptor(v_cache, page_table, torch.float8_e4m3fn)
-    ks, vs = scale_descriptor(k_scale, k_cache), scale_descriptor(v_scale, v_cache)
+    kd, vd = _kv_pair(k_cache, v_cache, page_table, torch.float8_e4m3fn)
+    ks, vs = _scale_pair(k_scale, v_scale, k_cache, v_cache)
     if q.dtype != torch.bfloat16 or not q.is_contiguous():
         raise ValueError("q must be contiguous bf16 [rows, num_q_heads, 128]")
     if k_cache.shape[2:] != v_cache.shape[2:] or k_cache.shape[2] * group != hq:
@@ -687,9 +709,8 @@ def attn_decode_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     need = 0 if max_kv_len <= 128 else _fp8_workspace(device, batch, hq, group)
     ws, ws_size = _workspace(need, q.device, workspace)
     _check("attn_decode_fp8",
-           lib().attn_decode_fp8(q.data_ptr(), ctypes.byref(kd), ctypes.byref(vd),
-                                 ctypes.byref(ks), ctypes.byref(vs), lens, offs, batch, rows, hq,
-                                 group, d, max_q_len, max_kv_len, scale, _ptr(sink),
+           lib().attn_decode_fp8(q.data_ptr(), kd, vd, ks, vs, lens, offs, batch, rows, hq, group,
+                                 d, max_q_len, max_kv_len, scale, _ptr(sink),
                                  1 if causal else 0, _ptr(ws), ws_size, out.data_ptr(), _ptr(lse),
                                  _stream_of(stream, device)))
     return out, lse
