@@ -301,13 +301,14 @@ struct Item {
 };
 
 template <int L, int S, bool kInter, bool kFp8>
-__global__ void __launch_bounds__(kThreads, S == 1 ? 4 : 2)
+__global__ void __launch_bounds__(kThreads, kFp8 ? 2 : 4)
 head_tiles_kernel(const __grid_constant__ RowsParams p, const __grid_constant__ Cut cut) {
     using Sh = Shape<L, S>;
     constexpr int kItems = Sh::kItems;
     extern __shared__ __align__(16) float4 angles[];             // [rows][4][lanes]
     __shared__ Place places[Sh::kMaxRows];
-    __shared__ float row_max[kFp8 ? kItems * S : 1];             // then 1 / scale
+    __shared__ float row_max[kFp8 ? kItems * S : 1];             // S = 1: then 1 / scale
+    __shared__ float s_inv[kFp8 && S > 1 ? kGroupTokens : 1];
     __shared__ Tokens s_tile;
     __shared__ int s_any;
     const int tid = threadIdx.x, lane = tid & 31;
@@ -318,6 +319,8 @@ head_tiles_kernel(const __grid_constant__ RowsParams p, const __grid_constant__ 
     // ---- rows of the tile and their places -------------------------------------
     int r0, n;
     if (kFp8) {
+        static_assert(!kFp8 || S == 1 || kItems * S == kGroupTokens, "a row an item");
+        for (int i = tid; i < kItems * S; i += kThreads) row_max[i] = 0.f;
         if (tid < 32) {
             Tokens t;
             const bool any = tile_tokens(p, tile, lane, t);
@@ -485,7 +488,12 @@ head_tiles_kernel(const __grid_constant__ RowsParams p, const __grid_constant__ 
         }
 
         // ---- 8-bit cache: scales of the blocks -----------------------------------------
-        __syncthreads();                                         // the last heads' scales are used
+        const int B = p.block_tokens, base = static_cast<int>(s_tile.first);   // row 0's token
+        // earlier tokens of the first row's block, uniform over the CTA
+        const int held = s_tile.first == s_tile.begin && base >= 0 && places[0].stored > 0
+                             ? base % B : 0;
+        float ratio = 1.f;                                       // of a held block's row 0
+        if constexpr (S == 1) __syncthreads();                   // the last heads' scales are used
 #pragma unroll
         for (int s = 0; s < S; ++s) {
             float top = 0.f;
@@ -495,64 +503,118 @@ head_tiles_kernel(const __grid_constant__ RowsParams p, const __grid_constant__ 
                             fmaxf(finite_abs(yb[s][k].x), finite_abs(yb[s][k].y)));
 #pragma unroll
             for (int o = 1; o < L; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            if (i0 == 0) row_max[item0 + s * kItems] = top;      // (no item: 0)
+            if (S == 1) {
+                if (i0 == 0) row_max[item0] = top;               // (no item: 0)
+            } else {
+                // in the place of its token in the group, so that blocks are aligned
+                const int row = it.row + s * kItems;
+                if (i0 == 0 && row < n && places[row].stored > 0)
+                    row_max[(base + row) & (kGroupTokens - 1)] = top;
+            }
         }
         __syncthreads();
-        // The thread of a block's first stored row in the tile takes the maximum over
-        // the block's rows, writes the scale and leaves 1 / scale in their places.
-        float ratio = 1.f;
-        int held = 0;
-        const int row = tid & ((1 << shift) - 1), h = hs + (tid >> shift);
-        if (tid < kItems * S && row < n && h < h1 && h >= p.q.heads && places[row].stored > 0) {
-            const int B = p.block_tokens, t = places[row].token;
-            const int base = t - row;                            // token of row 0, may be < 0
-            const int first = max(t / B * B - base, max(-base, 0));
-            const int last = min(t / B * B + B, min(base + n, p.max_kv_len)) - base;
-            if (row == first) {
-                float top = 0.f;
-                for (int i = first; i < last; ++i) top = fmaxf(top, row_max[(tid - row) + i]);
-                const bool is_k = h < p.q.heads + p.k.heads;
-                const int head = h - p.q.heads - (is_k ? 0 : p.k.heads);
+        if constexpr (S == 1) {
+            // The thread of a block's first stored row in the tile takes the maximum
+            // over the block's rows, writes the scale and leaves 1 / scale in their
+            // places.
+            const int row = tid & ((1 << shift) - 1), h = hs + (tid >> shift);
+            if (tid < kItems && row < n && h < h1 && h >= p.q.heads && places[row].stored > 0) {
+                const int t = places[row].token;
+                const int first = max(t / B * B - base, max(-base, 0));
+                const int last = min(t / B * B + B, min(base + n, p.max_kv_len)) - base;
+                if (row == first) {
+                    float top = 0.f;
+                    for (int i = first; i < last; ++i) top = fmaxf(top, row_max[(tid - row) + i]);
+                    const bool is_k = h < p.q.heads + p.k.heads;
+                    const int head = h - p.q.heads - (is_k ? 0 : p.k.heads);
+                    const CacheOut &c = is_k ? p.kc : p.vc;
+                    float *where = c.scale + places[row].page * c.scale_page +
+                                   (places[row].slot / B) * c.scale_block + head * c.scale_head;
+                    float scale = pow2i(scale_exponent(top));
+                    if (row == 0 && held > 0) {
+                        const float old = *where;
+                        if (scale > old) ratio = old / scale; else scale = old;
+                    }
+                    *where = scale;
+                    const float inv = 1.f / scale;
+                    for (int i = first; i < last; ++i) row_max[(tid - row) + i] = inv;
+                }
+            }
+        } else {
+            // One head: thread t < 128 stands for token t of the group; a block's
+            // maximum by shuffles, over warps through shared memory.
+            __shared__ float s_part[4];
+            float top = 0.f;
+            if (tid < kGroupTokens) {
+                top = row_max[tid];
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1)
+                    if (o < B) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                if (lane == 0) s_part[tid >> 5] = top;
+            }
+            if (B > 32) {
+                __syncthreads();
+                if (tid < kGroupTokens)
+                    top = B == 64 ? fmaxf(s_part[(tid >> 5) & 2], s_part[((tid >> 5) & 2) + 1])
+                                  : fmaxf(fmaxf(s_part[0], s_part[1]), fmaxf(s_part[2], s_part[3]));
+            }
+            const int row = tid - (base & (kGroupTokens - 1));
+            float *where = nullptr;
+            float scale = 0.f;
+            if (tid < kGroupTokens && row >= 0 && row < n && places[row].stored > 0 &&
+                hs >= p.q.heads) {
+                const int t = base + row;
+                const bool is_k = hs < p.q.heads + p.k.heads;
+                const int head = hs - p.q.heads - (is_k ? 0 : p.k.heads);
                 const CacheOut &c = is_k ? p.kc : p.vc;
-                float *where = c.scale + places[row].page * c.scale_page +
-                               (places[row].slot / B) * c.scale_block + head * c.scale_head;
-                float scale = pow2i(scale_exponent(top));
-                if (row == 0 && base == s_tile.begin && t % B != 0) {
-                    held = t % B;                                // earlier tokens of the block
-                    const float old = *where;
+                float *at = c.scale + places[row].page * c.scale_page +
+                            (places[row].slot / B) * c.scale_block + head * c.scale_head;
+                scale = pow2i(scale_exponent(top));
+                if (held > 0 && t / B == base / B) {
+                    const float old = *at;
                     if (scale > old) ratio = old / scale; else scale = old;
                 }
-                *where = scale;
-                const float inv = 1.f / scale;
-                for (int i = first; i < last; ++i) row_max[(tid - row) + i] = inv;
+                s_inv[row] = 1.f / scale;
+                if (t % B == 0 || row == 0) where = at;
             }
+            __syncthreads();                                     // the old scale has been read
+            if (where) *where = scale;
         }
-        // What the first block held, if its scale grew: one warp a head.
-        {
-            __shared__ float s_ratio[kThreads];
-            __shared__ int s_held[kThreads];
+        // What the first block held, where its scale grew: eight tokens a warp at a
+        // time, all their loads before the first store.
+        if (held > 0) {
+            __shared__ float s_ratio[S == 1 ? kItems : 1];
             const int heads_now = min(step_heads, h1 - hs);
-            if (tid < kItems * S && row == 0 && (tid >> shift) < heads_now) {
-                s_ratio[tid >> shift] = ratio;
-                s_held[tid >> shift] = held;
+            if (S == 1) {
+                if (tid < kItems && (tid & ((1 << shift) - 1)) == 0) s_ratio[tid >> shift] = ratio;
+            } else {
+                if (tid == (base & (kGroupTokens - 1))) s_ratio[0] = ratio;
             }
-            __syncthreads();
-            for (int hh = tid >> 5; hh < heads_now; hh += kThreads / 32) {
-                const int g = hs + hh;
-                if (g < p.q.heads || s_held[hh] == 0 || s_ratio[hh] == 1.f) continue;
+            const int batches = __syncthreads_or(ratio != 1.f) ? (held + 7) / 8 : 0;
+            for (int w = tid >> 5; w < heads_now * batches; w += kThreads / 32) {
+                const int hh = w / batches, g = hs + hh;
+                if (g < p.q.heads || s_ratio[hh] == 1.f) continue;
                 const bool is_k = g < p.q.heads + p.k.heads;
                 const int head = g - p.q.heads - (is_k ? 0 : p.k.heads);
                 const CacheOut &c = is_k ? p.kc : p.vc;
                 // the held tokens are the slots just before the tile's first row's
-                uint8_t *base = c.base + (is_k ? places[0].k_at : places[0].v_at) +
-                                head * c.head_stride;
-                for (int i = 1; i <= s_held[hh]; ++i) {
-                    uint32_t *w = reinterpret_cast<uint32_t *>(base - i * c.token_stride) + lane;
-                    const uint32_t old = *w;
-                    *w = encode4(decode2(old), decode2(old >> 16), s_ratio[hh]);
-                }
+                const int i1 = 8 * (w - hh * batches) + 1;
+                uint32_t *at = reinterpret_cast<uint32_t *>(
+                                   c.base + (is_k ? places[0].k_at : places[0].v_at) +
+                                   head * c.head_stride - i1 * c.token_stride) + lane;
+                const long long step = c.token_stride / 4;
+                uint32_t old[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (i1 + i <= held) old[i] = *(at - i * step);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (i1 + i <= held)
+                        *(at - i * step) = encode4(decode2(old[i]), decode2(old[i] >> 16),
+                                                   s_ratio[hh]);
             }
         }
+        if (S == 1 && held == 0) __syncthreads();                // 1 / scale is in place
         // ---- codes ---------------------------------------------------------------------
 #pragma unroll
         for (int s = 0; s < S; ++s) {
@@ -561,7 +623,7 @@ head_tiles_kernel(const __grid_constant__ RowsParams p, const __grid_constant__ 
             if (x.ca < 0 || x.kind == 0 || row >= n || places[row].stored <= 0) continue;
             const Place &at = places[row];
             const CacheOut &c = x.kind == 1 ? p.kc : p.vc;
-            const float f = row_max[item0 + s * kItems];
+            const float f = S == 1 ? row_max[item0] : s_inv[row];
             uint8_t *dst = c.base + (x.kind == 1 ? at.k_at : at.v_at) + x.head * c.head_stride;
             *reinterpret_cast<uint2 *>(dst + x.ca) =
                 make_uint2(encode4(ya[s][0], ya[s][1], f), encode4(ya[s][2], ya[s][3], f));

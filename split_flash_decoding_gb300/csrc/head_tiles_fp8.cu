@@ -36,7 +36,32 @@ cudaError_t launch_fp8_tiles(const RowsParams &p, cudaStream_t stream) {
         const int now = Shape<8, 1>::kItems / rows;              // heads at once
         return launch_steps<1>(p, rows, now < 16 ? now : 16, stream);
     }
-    return launch_steps<4>(p, kGroupTokens, 16, stream);
+    // Long runs: the queries go through the row tiles, which are better at them
+    // (their heads side by side), in a launch of their own.
+    RowsParams kv = p;
+    if (p.q.heads > 0) {
+        RowsParams q = p;
+        q.k.heads = q.v.heads = 0;
+        const cudaError_t e = launch_head_tiles(q, stream);
+        if (e != cudaSuccess) return e;
+        kv.q.heads = 0;
+    }
+    // A tile's angles cost about as much as two heads; as many heads to a CTA as
+    // leave the waves full.
+    constexpr int kWave = 2 * 152;
+    const int heads = p.k.heads + p.v.heads;
+    const long long tiles = p.num_rows / kGroupTokens + p.batch;
+    int best = 1;
+    long long least = 0;
+    for (int chunk = 1; chunk <= heads; ++chunk) {
+        const long long ctas = tiles * ((heads + chunk - 1) / chunk);
+        const long long cost = (ctas + kWave - 1) / kWave * (chunk + 2);
+        if (chunk == 1 || cost < least) {
+            least = cost;
+            best = chunk;
+        }
+    }
+    return launch_steps<4>(kv, kGroupTokens, best, stream);
 }
 
 }  // namespace attn
