@@ -130,7 +130,15 @@ __device__ __forceinline__ float finite_abs(float x) {
     return a <= FLT_MAX ? a : 0.f;
 }
 
-// Four values times f as e4m3 codes; there is no infinity: it becomes NaN.
+// Four finite (or NaN) values times f as e4m3 codes.
+__device__ __forceinline__ uint32_t encode4_finite(const float2 &a, const float2 &b, float f) {
+    const float2 x = __fmul2_rn(a, make_float2(f, f)), y = __fmul2_rn(b, make_float2(f, f));
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(x, __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
+    return lo | (hi << 16);
+}
+
+// The same of any values; there is no infinity: it becomes NaN.
 __device__ __forceinline__ uint32_t encode4(const float2 &a, const float2 &b, float f) {
     float2 x = __fmul2_rn(a, make_float2(f, f)), y = __fmul2_rn(b, make_float2(f, f));
     const float nan = __uint_as_float(0x7fffffffu);
@@ -493,14 +501,25 @@ head_tiles_kernel(const __grid_constant__ RowsParams p, const __grid_constant__ 
         const int held = s_tile.first == s_tile.begin && base >= 0 && places[0].stored > 0
                              ? base % B : 0;
         float ratio = 1.f;                                       // of a held block's row 0
+        unsigned infinite = 0;                                   // items with an infinity
         if constexpr (S == 1) __syncthreads();                   // the last heads' scales are used
 #pragma unroll
         for (int s = 0; s < S; ++s) {
+            // (NaN never counts; infinities do not either, but cost a second look)
             float top = 0.f;
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                top = fmaxf(fmaxf(fmaxf(finite_abs(ya[s][k].x), finite_abs(ya[s][k].y)), top),
-                            fmaxf(finite_abs(yb[s][k].x), finite_abs(yb[s][k].y)));
+            for (int k = 0; k < 4; ++k) {
+                top = fmax3(top, fabsf(ya[s][k].x), fabsf(ya[s][k].y));
+                top = fmax3(top, fabsf(yb[s][k].x), fabsf(yb[s][k].y));
+            }
+            if (top > FLT_MAX) {
+                infinite |= 1u << s;
+                top = 0.f;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    top = fmaxf(fmaxf(fmaxf(finite_abs(ya[s][k].x), finite_abs(ya[s][k].y)), top),
+                                fmaxf(finite_abs(yb[s][k].x), finite_abs(yb[s][k].y)));
+            }
 #pragma unroll
             for (int o = 1; o < L; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
             if (S == 1) {
@@ -625,10 +644,18 @@ head_tiles_kernel(const __grid_constant__ RowsParams p, const __grid_constant__ 
             const CacheOut &c = x.kind == 1 ? p.kc : p.vc;
             const float f = S == 1 ? row_max[item0] : s_inv[row];
             uint8_t *dst = c.base + (x.kind == 1 ? at.k_at : at.v_at) + x.head * c.head_stride;
-            *reinterpret_cast<uint2 *>(dst + x.ca) =
-                make_uint2(encode4(ya[s][0], ya[s][1], f), encode4(ya[s][2], ya[s][3], f));
-            *reinterpret_cast<uint2 *>(dst + x.cb) =
-                make_uint2(encode4(yb[s][0], yb[s][1], f), encode4(yb[s][2], yb[s][3], f));
+            uint2 wa, wb;
+            if (infinite >> s & 1) {
+                wa = make_uint2(encode4(ya[s][0], ya[s][1], f), encode4(ya[s][2], ya[s][3], f));
+                wb = make_uint2(encode4(yb[s][0], yb[s][1], f), encode4(yb[s][2], yb[s][3], f));
+            } else {
+                wa = make_uint2(encode4_finite(ya[s][0], ya[s][1], f),
+                                encode4_finite(ya[s][2], ya[s][3], f));
+                wb = make_uint2(encode4_finite(yb[s][0], yb[s][1], f),
+                                encode4_finite(yb[s][2], yb[s][3], f));
+            }
+            *reinterpret_cast<uint2 *>(dst + x.ca) = wa;
+            *reinterpret_cast<uint2 *>(dst + x.cb) = wb;
         }
         it.advance<kItems, kInter>(p, r0, i0, h1, step_heads);
         load();
