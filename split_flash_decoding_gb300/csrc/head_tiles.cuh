@@ -3,8 +3,7 @@
 // of a cache held in 8 bits.
 //
 // Bound by memory for prompts (each channel read and written once) and by latency
-// for a few rows.  A CTA of 256 threads takes a tile of rows and some of their
-// heads.  Its threads first look the rows' places up and compute the cos and sin
+// for a few rows.  A CTA takes a tile of rows and some of their heads.  Its threads first look the rows' places up and compute the cos and sin
 // of every (row, pair) once, into shared memory; then they walk the heads, whose
 // rotation costs no more than reading that table.
 //
@@ -12,7 +11,7 @@
 // it, chosen so that a pair of channels is always in one lane: in the half layout
 // a vector of the rotated channels' lower half and the one rot_dim / 2 above it,
 // otherwise vector i and the one half the head above it, so that lanes side by
-// side read and write whole lines.  256 / L items are in work at once: the tile's
+// side read and write whole lines.  A CTA of T threads has T / L items in work at once: the tile's
 // rows (padded to a power of two), then the next heads', so that a tile of one row
 // has many heads in work.  S > 1: S times as many rows of one head.  A thread keeps
 // its place in the list of heads (pointers, channels, weights) and adds to it; the
@@ -34,7 +33,6 @@
 namespace attn {
 namespace tiles {
 
-constexpr int kThreads = 256;
 constexpr int kGroupTokens = 128;     // 8-bit cache: aligned tokens of a tile
 constexpr int kMinExp = -60, kMaxExp = 120;
 
@@ -47,9 +45,10 @@ struct Cut {
     int any_norm;
 };
 
-template <int L, int S>
+// L lanes an item, T threads a CTA, S items a thread.
+template <int L, int S, int T>
 struct Shape {
-    static constexpr int kItems = kThreads / L;           // at once
+    static constexpr int kItems = T / L;                  // at once
     static constexpr int kMaxRows = kItems * S < kGroupTokens ? kItems * S : kGroupTokens;
 };
 
@@ -308,10 +307,11 @@ struct Item {
     }
 };
 
-template <int L, int S, bool kInter, bool kFp8>
-__global__ void __launch_bounds__(kThreads, kFp8 ? 2 : 4)
+template <int L, int S, int T, bool kInter, bool kFp8>
+__global__ void __launch_bounds__(T, kFp8 ? 2 : 4)
 head_tiles_kernel(const __grid_constant__ RowsParams p, const __grid_constant__ Cut cut) {
-    using Sh = Shape<L, S>;
+    using Sh = Shape<L, S, T>;
+    constexpr int kThreads = T;
     constexpr int kItems = Sh::kItems;
     extern __shared__ __align__(16) float4 angles[];             // [rows][4][lanes]
     __shared__ Place places[Sh::kMaxRows];
@@ -527,7 +527,7 @@ head_tiles_kernel(const __grid_constant__ RowsParams p, const __grid_constant__ 
             } else {
                 // in the place of its token in the group, so that blocks are aligned
                 const int row = it.row + s * kItems;
-                if (i0 == 0 && row < n && places[row].stored > 0)
+                if (i0 == 0 && it.ca >= 0 && row < n && places[row].stored > 0)
                     row_max[(base + row) & (kGroupTokens - 1)] = top;
             }
         }
@@ -662,20 +662,20 @@ head_tiles_kernel(const __grid_constant__ RowsParams p, const __grid_constant__ 
     }
 }
 
-template <int L, int S, bool kInter, bool kFp8>
+template <int L, int S, int T, bool kInter, bool kFp8>
 cudaError_t launch(const RowsParams &p, const Cut &cut, long long tiles, cudaStream_t stream) {
     const long long blocks = tiles * cut.chunks;
     if (blocks == 0) return cudaSuccess;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
     const int rows = kFp8 && !p.q_row_offsets ? 1 : cut.tile_rows;
     const size_t smem = p.rope.rot_dim > 0 ? size_t(rows) * 4 * L * sizeof(float4) : 0;
-    auto kern = head_tiles_kernel<L, S, kInter, kFp8>;
+    auto kern = head_tiles_kernel<L, S, T, kInter, kFp8>;
     if (smem > 32768) {
         const cudaError_t e = cudaFuncSetAttribute(
             kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
         if (e != cudaSuccess) return e;
     }
-    kern<<<static_cast<unsigned>(blocks), kThreads, smem, stream>>>(p, cut);
+    kern<<<static_cast<unsigned>(blocks), T, smem, stream>>>(p, cut);
     return cudaGetLastError();
 }
 

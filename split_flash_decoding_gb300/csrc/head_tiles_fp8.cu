@@ -8,7 +8,7 @@ using namespace tiles;
 
 namespace {
 
-template <int S>
+template <int S, int T>
 cudaError_t launch_steps(const RowsParams &p, int tile_rows, int chunk_heads, cudaStream_t stream) {
     Cut cut;
     cut.heads = p.q.heads + p.k.heads + p.v.heads;
@@ -22,19 +22,19 @@ cudaError_t launch_steps(const RowsParams &p, int tile_rows, int chunk_heads, cu
         const long long bound = p.num_rows / kGroupTokens + 2LL * p.batch;
         if (bound < tiles) tiles = bound;
     }
-    return p.rope.interleaved ? launch<8, S, true, true>(p, cut, tiles, stream)
-                              : launch<8, S, false, true>(p, cut, tiles, stream);
+    return p.rope.interleaved ? launch<8, S, T, true, true>(p, cut, tiles, stream)
+                              : launch<8, S, T, false, true>(p, cut, tiles, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_fp8_tiles(const RowsParams &p, cudaStream_t stream) {
     const int longest = p.q_row_offsets ? p.max_q_len : 1;
-    if (longest <= Shape<8, 1>::kMaxRows) {
+    if (longest <= Shape<8, 1, 256>::kMaxRows) {
         int rows = 1;
         while (rows < longest) rows *= 2;
-        const int now = Shape<8, 1>::kItems / rows;              // heads at once
-        return launch_steps<1>(p, rows, now < 16 ? now : 16, stream);
+        const int now = Shape<8, 1, 256>::kItems / rows;              // heads at once
+        return launch_steps<1, 256>(p, rows, now, stream);
     }
     // Long runs: the queries go through the row tiles, which are better at them
     // (their heads side by side), in a launch of their own.
@@ -61,7 +61,7 @@ cudaError_t launch_fp8_tiles(const RowsParams &p, cudaStream_t stream) {
             best = chunk;
         }
     }
-    return launch_steps<4>(kv, kGroupTokens, best, stream);
+    return launch_steps<4, 256>(kv, kGroupTokens, best, stream);
 }
 
 }  // namespace attn

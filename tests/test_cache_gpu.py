@@ -337,9 +337,12 @@ def test_append_fp8_single_rows(attn, block):
 
 @pytest.mark.parametrize("page,block,q_lens", [
     (16, 16, [5, 130, 1]), (128, 128, [600, 1, 8]), (64, 4, [3, 0, 200]), (32, 1, [40, 40, 40]),
-    (256, 256, [700, 300, 2]), (8, 8, [9, 17, 33]), (1024, 512, [600, 3, 200])])
+    (256, 256, [700, 300, 2]), (8, 8, [9, 17, 33]), (1024, 512, [600, 3, 200]),
+    # tiles of a few rows in calls with long runs, blocks of every size
+    (128, 16, [140, 5, 129, 33]), (128, 64, [150, 20, 131]), (32, 1, [50, 7, 130, 1]),
+    (128, 128, [40, 100, 3])])
 def test_append_fp8_ragged(attn, page, block, q_lens):
-    lens = [n + x for n, x in zip(q_lens, (7, 130, 70))]
+    lens = [n + x for n, x in zip(q_lens, (7, 130, 70, 126))]
     check_fp8(attn, lens, q_lens, page, block, page + block, magnitude=2.0,
               rope_kw=dict(interleaved=True))
 
