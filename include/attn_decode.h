@@ -519,7 +519,7 @@ int attn_qk_norm_rope(const attn_head_rows_t *q, const attn_head_rows_t *k,
  *   q_row_offsets  device uint32 [batch + 1]: rows of sequence b are
  *               [off[b], off[b + 1]), or NULL for one row per sequence.  Rows
  *               at or behind off[batch] belong to no sequence: nothing is written
- *               is read or written.
+ *               for them.
  *   batch, num_q_rows   sequences and rows (num_q_rows = batch without
  *               offsets).
  *   max_kv_len  host upper bound of kv_len.
@@ -570,6 +570,7 @@ typedef struct attn_kv_scale {
  * to).  Slots past a sequence's last token are left as they are.
  *
  *   k_scale, v_scale  the caches' scales (same block_tokens).
+ *   max_kv_len  at most 2^31 - 8193.
  *   max_q_len   host upper bound of the rows of any sequence.
  * Everything else as for attn_append_kv; v and v_cache are required.
  */
@@ -588,17 +589,23 @@ int attn_append_kv_fp8(const attn_head_rows_t *q, const attn_head_rows_t *k,
  *   q           device bf16 [num_q_rows][num_q_heads][128], not quantised.
  *   k, v        cache operands of e4m3 elements with their scales; K and V
  *               share page table, page size and block_tokens.  Scales are
- *               finite and >= 0; results are stated for scales up to 2^64.
+ *               finite and >= 0; a V scale of 2^65 and more counts as NaN.
  *   group       query heads per KV head, 1 to 16.
  *   max_q_len   max_q_len * group <= 16 (longer row runs:
  *               ATTN_ERR_UNSUPPORTED).
+ *   max_kv_len  ATTN_ERR_UNSUPPORTED where the tiles of 128 keys of all
+ *               sequences and KV heads would be about 2^30 and more, or above
+ *               2^31 - 8193 tokens.
  *   workspace   device, 256-byte aligned, of at least
  *               attn_decode_fp8_workspace bytes; may be NULL when max_kv_len <=
  *               128.  Contents on entry are ignored.  Calls that can overlap on
  *               the GPU need one each.
- * The other arguments as for attn_decode (batch <= 2048).  out and lse are
- * those of attn_decode on the cache code * scale; a code of NaN in a visible
- * token gives NaN.  Launches the partition kernel and the split-K reduce.
+ * The other arguments as for attn_decode (batch <= 2048), with this addition:
+ * rows at or behind off[batch] belong to no sequence and are left as they are.
+ * out and lse are those of attn_decode on the cache code * scale.  A code of NaN
+ * in a token makes the out of the rows that see it NaN (their lse is then
+ * undefined) and of no others, whatever slots past a sequence's last token hold.
+ * Launches the partition kernel and, for max_kv_len > 128, the split-K reduce.
  */
 int attn_decode_fp8_workspace(int num_sms, int batch, int num_q_heads, int group,
                               size_t *workspace_bytes);

@@ -269,7 +269,7 @@ extern "C" int attn_append_kv_fp8(const attn_head_rows_t *q, const attn_head_row
                          num_q_rows, max_kv_len, 16, &p);
     if (st || p.num_rows == 0) return st;
     if (!v || max_q_len < 1 || (!q_row_offsets && max_q_len != 1)) return ATTN_ERR_INVALID_ARG;
-    if (k->dim != 128 || v->dim != 128) return ATTN_ERR_UNSUPPORTED;
+    if (k->dim != 128 || v->dim != 128 || max_kv_len > kMaxFp8Tokens) return ATTN_ERR_UNSUPPORTED;
     if ((st = check_scale(k_scale, k_cache)) || (st = check_scale(v_scale, v_cache))) return st;
     if (k_scale->block_tokens != v_scale->block_tokens) return ATTN_ERR_UNSUPPORTED;
     take_scale(k_scale, &p.kc);
@@ -308,15 +308,17 @@ extern "C" int attn_decode_fp8(const void *q, const attn_kv_t *k, const attn_kv_
     if (num_q_heads % group) return ATTN_ERR_INVALID_ARG;
     if (!(scale == scale)) return ATTN_ERR_INVALID_ARG;
     if (!q_row_offsets && (num_q_rows != batch || max_q_len != 1)) return ATTN_ERR_INVALID_ARG;
-    if (q_row_offsets && max_q_len == 1 && num_q_rows != batch) return ATTN_ERR_INVALID_ARG;
     if (batch == 0 || num_q_rows == 0) return ATTN_OK;
     if (!q || !kv_len || !out) return ATTN_ERR_INVALID_ARG;
     if (head_dim != 128 || static_cast<long long>(max_q_len) * group > 16 || batch > kGqaMaxBatch)
         return ATTN_ERR_UNSUPPORTED;
     if (!aligned(q, 16) || !aligned(out, 16)) return ATTN_ERR_INVALID_ARG;
     const int hkv = num_q_heads / group;
-    // the split counts tiles and their costs in ints
-    if ((static_cast<long long>(max_kv_len) / kGqaTcTileKeys + 1) * batch * hkv >= (1LL << 27))
+    int head_shift = 0;
+    while (head_shift < 3 && hkv % (2 << head_shift) == 0) ++head_shift;
+    // the split counts the costs of its tiles in ints
+    const long long most = (max_kv_len / kGqaTcTileKeys + 1) * kFp8MostTileCost + kFp8UnitCost;
+    if (max_kv_len > kMaxFp8Tokens || most * batch * (hkv >> head_shift) > 0x7fffffffLL)
         return ATTN_ERR_UNSUPPORTED;
     CacheOut kc, vc;
     int st = take_cache(k, batch, head_dim, hkv, max_kv_len, 16, &kc);
@@ -357,7 +359,7 @@ extern "C" int attn_decode_fp8(const void *q, const attn_kv_t *k, const attn_kv_
     p.num_pages = k->num_pages;
     p.qk_scale_log2 = scale * 1.4426950408889634f;
     p.max_kv_len = max_kv_len;
-    while (p.head_shift < 3 && hkv % (2 << p.head_shift) == 0) ++p.head_shift;
+    p.head_shift = head_shift;
     p.head_groups = hkv >> p.head_shift;
     if (cut) {
         uint8_t *ws = static_cast<uint8_t *>(workspace);

@@ -103,19 +103,19 @@ append_fp8_kernel(const __grid_constant__ RowsParams p) {
 
 }  // namespace
 
-cudaError_t launch_fp8_tiles(const RowsParams &p, cudaStream_t stream);
-
 cudaError_t launch_append_fp8(const RowsParams &p, cudaStream_t stream) {
-    if (p.block_tokens <= tiles::kGroupTokens && head_tiles_fit(p))
-        return launch_fp8_tiles(p, stream);
+    const bool small_blocks = p.block_tokens <= tiles::kGroupTokens;
+    if (small_blocks && fp8_tiles_take_queries(p)) return launch_fp8_tiles(p, stream);
+    RowsParams kv = p;
     if (p.q.heads > 0) {
         RowsParams q = p;
         q.k.heads = q.v.heads = 0;
         const cudaError_t e = launch_head_rows(q, stream);
         if (e != cudaSuccess) return e;
+        kv.q.heads = 0;
     }
-    if (p.num_rows == 0) return cudaSuccess;
-    append_fp8_kernel<<<dim3(p.num_rows, p.k.heads, 2), kThreads, 0, stream>>>(p);
+    if (small_blocks && head_tiles_fit(kv)) return launch_fp8_tiles(kv, stream);
+    append_fp8_kernel<<<dim3(p.num_rows, p.k.heads, 2), kThreads, 0, stream>>>(kv);
     return cudaGetLastError();
 }
 

@@ -11,6 +11,14 @@
 
 namespace attn {
 
+// The 8-bit cache's kernels round token numbers up in ints.
+constexpr int kMaxFp8Tokens = 0x7fffffff - 8192;
+
+// Costs of the 8-bit decode's split, in eighths of a tile of up to four columns:
+// of a tile of 16 columns, and of opening a unit.
+constexpr int kFp8MostTileCost = 11;
+constexpr int kFp8UnitCost = 32;
+
 // Head vectors of a call's rows (attn_head_rows_t).
 struct HeadRows {
     const uint16_t *in;
@@ -78,9 +86,14 @@ struct Fp8DecodeParams {
 
 cudaError_t launch_head_rows(const RowsParams &p, cudaStream_t stream);
 cudaError_t launch_append_fp8(const RowsParams &p, cudaStream_t stream);
-// The tile kernels take whole rows of 128-byte-friendly shapes; false: not these.
+// The tile kernel takes heads of up to 256 channels whose rotated pairs fall on
+// whole 16-byte vectors; false: not these.
 bool head_tiles_fit(const RowsParams &p);
 cudaError_t launch_head_tiles(const RowsParams &p, cudaStream_t stream);
+// The same into a cache held in 8 bits: blocks of up to 128 tokens, and q only
+// where fp8_tiles_take_queries.
+bool fp8_tiles_take_queries(const RowsParams &p);
+cudaError_t launch_fp8_tiles(const RowsParams &p, cudaStream_t stream);
 // CTAs of the 8-bit decode grid on num_sms SMs.
 int fp8_decode_ctas(int num_sms);
 cudaError_t launch_gqa_decode_fp8(const Fp8DecodeParams &p, int ctas, cudaStream_t stream);

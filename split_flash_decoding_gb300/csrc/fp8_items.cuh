@@ -13,7 +13,7 @@
 // concatenated, are dealt out in contiguous ranges of equal cost, in eighths of a
 // tile's: a tile costs 8 + (chunks of four columns that the sequence's rows fill
 // - 1), as the softmax of more columns takes longer (1 to 4 rows of 4 heads:
-// 1.58, 1.77, 1.89 and 2.11 us a tile), and every unit is preceded by kUnitCost
+// 1.58, 1.77, 1.89 and 2.11 us a tile), and every unit is preceded by kFp8UnitCost
 // (opening it: its queries, the pipeline refill, the epilogue).  Group c of C
 // takes the tiles that start in [c W / C, (c + 1) W / C), W the cost of all.
 #pragma once
@@ -22,8 +22,6 @@
 #include "ptx.cuh"
 
 namespace attn {
-
-constexpr int kUnitCost = 32;
 
 struct Fp8Range {
     int x0, x1;            // this group's tiles of the concatenation
@@ -70,7 +68,7 @@ __device__ __forceinline__ void fp8_build_items(const Fp8DecodeParams &p, int2 *
         if (len > cap && blockIdx.x == 0) atomicOr(p.err, kErrBadLength);
         const int n = fp8_tiles(len, cap);
         local += n * hg;
-        cost += hg * (n * fp8_tile_cost(p, b) + kUnitCost);
+        cost += hg * (n * fp8_tile_cost(p, b) + kFp8UnitCost);
     }
     int incl = local, cost_incl = cost;
 #pragma unroll
@@ -87,7 +85,7 @@ __device__ __forceinline__ void fp8_build_items(const Fp8DecodeParams &p, int2 *
         cum[b] = run;
         const int n = fp8_tiles(p.kv_len[b], cap);
         run.x += n * hg;
-        run.y += hg * (n * fp8_tile_cost(p, b) + kUnitCost);
+        run.y += hg * (n * fp8_tile_cost(p, b) + kFp8UnitCost);
     }
     if (lane == 31) cum[p.batch] = make_int2(incl, cost_incl);
 
@@ -107,11 +105,11 @@ __device__ __forceinline__ void fp8_build_items(const Fp8DecodeParams &p, int2 *
             for (int b = b0; b < b1; ++b) {
                 const int n = fp8_tiles(p.kv_len[b], cap);
                 const int tile = fp8_tile_cost(p, b);
-                const int unit_span = n * tile + kUnitCost;
+                const int unit_span = n * tile + kFp8UnitCost;
                 const int span = hg * unit_span;
                 if (y < ws + span) {
                     const int h = (y - ws) / unit_span;
-                    const int o = (y - ws) - h * unit_span - kUnitCost;
+                    const int o = (y - ws) - h * unit_span - kFp8UnitCost;
                     const int i = o <= 0 ? 0 : (o + tile - 1) / tile;
                     x = xs + h * n + i;
                     u = b * hg + h + (i == n);   // past the unit's last tile: the next opens
@@ -180,7 +178,7 @@ __device__ __forceinline__ int fp8_pieces(const Fp8DecodeParams &p, const int2 *
     const int h = it.unit - it.b * p.head_groups;
     const int tile = fp8_tile_cost(p, it.b);
     const int last =
-        cum[it.b].y + (h + 1) * (it.unit_tiles * tile + kUnitCost) - tile;
+        cum[it.b].y + (h + 1) * (it.unit_tiles * tile + kFp8UnitCost) - tile;
     const int c_last =
         static_cast<int>((static_cast<long long>(last + 1) * r.groups - 1) / r.cost);
     return c_last - (static_cast<int>(blockIdx.x) >> p.head_shift) + 1;

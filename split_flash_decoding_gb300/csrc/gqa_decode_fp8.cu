@@ -629,11 +629,13 @@ gqa_decode_fp8_kernel(const __grid_constant__ Fp8DecodeParams p) {
                 }
                 if (++ss == kScStages) { ss = 0; sph ^= 1; }
                 if (tail && t0 + k >= it.L) sc = make_float2(0.f, 0.f);
-                const int ve = min(max(int((__float_as_uint(sc.y) >> 23) & 0xffu) - 127, kMinVExp),
-                                   kMaxVExp);
+                const int ve_raw = int((__float_as_uint(sc.y) >> 23) & 0xffu) - 127;
+                const int ve = min(max(ve_raw, kMinVExp), kMaxVExp);
                 const float vexp = static_cast<float>(ve);
                 const float v_inv = pow2i(-ve);
-                const float v_mul = sc.y * v_inv * kWeightTop;
+                // (a scale past the range would saturate: NaN instead)
+                const float v_mul = ve_raw > kMaxVExp ? __uint_as_float(0x7fffffffu)
+                                                      : sc.y * v_inv * kWeightTop;
                 float top = -INFINITY;
 #pragma unroll
                 for (int h = 0; h < NCH; ++h) {

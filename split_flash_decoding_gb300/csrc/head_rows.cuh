@@ -65,7 +65,10 @@ __device__ __forceinline__ RowPlace place_of_row(const RowsParams &p, int r, int
             const bool below =
                 i < len && static_cast<int>(p.q_row_offsets[lo + i]) <= r;
             const int count = __popc(__ballot_sync(0xffffffffu, below));
-            if (count == 0) break;       // r < off[0]: offsets that do not start at 0
+            if (count == 0) {            // r < off[0]
+                at.b = -1;
+                return at;
+            }
             lo += (count - 1) * step;
             len = min(step, len - (count - 1) * step);
         }

@@ -158,7 +158,9 @@ __device__ __forceinline__ float2 decode2(uint32_t c) {
 // Sequence of row r; -1: none.  (One thread a row; a warp's rows read the same lines.)
 __device__ __forceinline__ int sequence_of(const RowsParams &p, int r) {
     if (!p.q_row_offsets) return r;
-    if (r >= static_cast<int>(p.q_row_offsets[p.batch])) return -1;
+    if (r < static_cast<int>(p.q_row_offsets[0]) ||
+        r >= static_cast<int>(p.q_row_offsets[p.batch]))
+        return -1;
     int lo = 0, hi = p.batch;   // off[lo] <= r < off[hi]
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;

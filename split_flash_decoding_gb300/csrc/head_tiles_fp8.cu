@@ -26,25 +26,26 @@ cudaError_t launch_steps(const RowsParams &p, int tile_rows, int chunk_heads, cu
                               : launch<8, S, T, false, true>(p, cut, tiles, stream);
 }
 
+constexpr int kShortRun = Shape<8, 1, 256>::kMaxRows;
+
+int longest_run(const RowsParams &p) { return p.q_row_offsets ? p.max_q_len : 1; }
+
 }  // namespace
 
+// Queries join the keys' and values' launch when their heads have as many lanes
+// and the runs are short; the row tiles are better at long ones (a row's heads
+// side by side).
+bool fp8_tiles_take_queries(const RowsParams &p) {
+    return p.q.dim <= 128 && longest_run(p) <= kShortRun && head_tiles_fit(p);
+}
+
 cudaError_t launch_fp8_tiles(const RowsParams &p, cudaStream_t stream) {
-    const int longest = p.q_row_offsets ? p.max_q_len : 1;
-    if (longest <= Shape<8, 1, 256>::kMaxRows) {
+    const int longest = longest_run(p);
+    if (longest <= kShortRun) {
         int rows = 1;
         while (rows < longest) rows *= 2;
         const int now = Shape<8, 1, 256>::kItems / rows;              // heads at once
         return launch_steps<1, 256>(p, rows, now, stream);
-    }
-    // Long runs: the queries go through the row tiles, which are better at them
-    // (their heads side by side), in a launch of their own.
-    RowsParams kv = p;
-    if (p.q.heads > 0) {
-        RowsParams q = p;
-        q.k.heads = q.v.heads = 0;
-        const cudaError_t e = launch_head_tiles(q, stream);
-        if (e != cudaSuccess) return e;
-        kv.q.heads = 0;
     }
     // A tile's angles cost about as much as two heads; as many heads to a CTA as
     // leave the waves full.
@@ -61,7 +62,7 @@ cudaError_t launch_fp8_tiles(const RowsParams &p, cudaStream_t stream) {
             best = chunk;
         }
     }
-    return launch_steps<4, 256>(kv, kGroupTokens, best, stream);
+    return launch_steps<4, 256>(p, kGroupTokens, best, stream);
 }
 
 }  // namespace attn

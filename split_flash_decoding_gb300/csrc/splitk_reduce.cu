@@ -61,7 +61,7 @@ __device__ __forceinline__ int locate_partials(const ReduceParams &p, int row, i
         const int first_row = p.q_row_offsets ? int(p.q_row_offsets[b]) : b;
         const int2 e = p.unit_slots[b * p.hkv + h / p.group];
         const int col = (row - first_row) * p.group + h % p.group;
-        if (e.y == 1 || col >= kGqaSlotCols) return -1;
+        if (e.y == 1 || col < 0 || col >= kGqaSlotCols) return -1;
         stride_p = kGqaSlotCols;
         widx0 = static_cast<size_t>(e.x) * kGqaSlotCols + col;
         return e.y;

@@ -183,10 +183,11 @@ def test_decode_fp8_refusals(attn):
     assert call(group=0) == INV and call(hq=30) == INV and call(scale=float("nan")) == INV
     assert call(max_kv=-1) == INV and call(max_q=0) == INV and call(batch=-1) == INV
     assert call(rows=5) == INV and call(max_q=2) == INV
-    assert call(offs=P, rows=5) == INV                          # single rows: one per sequence
     assert call(d=64) == UNS and call(hq=34, group=17) == UNS
     assert call(offs=P, rows=20, max_q=5) == UNS                # 5 rows x 4 heads > 16
     assert call(batch=2049) == UNS
+    assert call(max_kv=2 ** 31 - 1) == UNS                      # token numbers in ints
+    assert call(batch=2048, rows=2048, hq=4 * 65535) == UNS     # costs of the split in ints
     assert call(max_kv=513) == INV
     for over in (dict(base=None), dict(base=P + 8), dict(token_stride=1032), dict(page_size=0)):
         assert call(k=kv(attn, **over)) == INV and call(v=kv(attn, **over)) == INV, over

@@ -400,6 +400,219 @@ def test_append_fp8_again_changes_nothing(attn):
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("runs", [[1, 1, 1, 1], [40, 2, 50, 1]])
+def test_append_fp8_bad_pages_and_lengths(attn, runs):
+    """A page outside the pool, a length above the bound and rows before token 0 are reported;
+    their queries are written, their keys are not, and the others' are as alone."""
+    page, hkv = 16, 2
+    lens = [max(runs[0], 17), 3, max(runs[2], 1) if runs[2] > 1 else 33, 1]
+    if runs[2] > 1:
+        lens[2] = 49                                     # 50 rows: the first has token -1
+    cap = 48
+    table = torch.tensor([[0, 1, 2, 3], [99, 99, 99, 99], [4, 5, 6, 7], [8, 8, 8, 8]],
+                         dtype=torch.int32, device=DEV)
+    rows = sum(runs)
+    x = randn(21, rows, 4 + 2 * hkv, 128).to(DEV)
+    offs = torch.tensor([sum(runs[:i]) for i in range(5)], dtype=torch.int32, device=DEV)
+    turns, rope = rope_of(attn, 128)
+
+    def go(which, lens, table, runs, offs, x):
+        c = [torch.zeros(9, page, hkv, 128, dtype=FP8, device=DEV) for _ in range(2)]
+        s = [torch.ones(9, 2, hkv, device=DEV) for _ in range(2)]
+        q = attn.attn_append_kv_fp8(
+            x[:, 4:4 + hkv], x[:, 4 + hkv:], *c, *s,
+            torch.tensor(lens, dtype=torch.int32, device=DEV), max_kv_len=cap,
+            max_q_len=max(runs), page_table=table, q=x[:, :4],
+            q_row_offsets=offs if max(runs) > 1 else None, rope=rope)
+        return q, c, s
+
+    q, c, s = go("all", lens, table, runs, offs, x)
+    # (single rows: every length within the bound)
+    assert attn.attn_device_error_flags(clear=True) == (6 if max(runs) > 1 else 2)
+    n0 = runs[0]
+    tokens = torch.cat([torch.arange(L - n, L) for L, n in zip(lens, runs)]).clamp_min(0)
+    exact, err = R.head_rows(x[:, :4].cpu(), turns, tokens)
+    R.assert_bf16(q, exact, err, "q")
+    # the first sequence alone gives the same pages
+    o1 = torch.tensor([0, n0], dtype=torch.int32, device=DEV)
+    _, c1, s1 = go("one", lens[:1], table[:1].contiguous(), runs[:1], o1, x[:n0])
+    assert attn.attn_device_error_flags(clear=True) == 0
+    for a, b in zip(c + s, c1 + s1):
+        a, b = (t.view(torch.uint8) if t.dtype == FP8 else t for t in (a, b))
+        assert torch.equal(a[:4], b[:4])
+    live = c[1].float().abs().sum((2, 3)) > 0            # [page, slot] with values
+    assert int(live[:4].sum()) == min(n0, cap) and int(live[8].sum()) == 1
+    assert int(live[4:8].sum()) == (min(lens[2], cap) if runs[2] > 1 else 1)
+
+
+@pytest.mark.parametrize("dim,rot,start", [(64, 0, 0), (192, 0, 0), (256, 0, 0), (256, 64, 32),
+                                           (576, 64, 512), (40, 0, 0)])
+@pytest.mark.parametrize("q_lens", [[1, 1, 1], [4, 1, 2], [40, 3, 130]])
+def test_append_fp8_query_heads_of_other_sizes(attn, dim, rot, start, q_lens):
+    """Queries need not have the keys' 128 channels."""
+    lens = [200, 77, 140]
+    pool = Pool(lens, 64, 3)
+    rows = sum(q_lens)
+    k, v, q = randn(1, rows, 2, 128), randn(2, rows, 2, 128), randn(3, rows, 6, dim)
+    qn = (1 + randn(4, dim, scale=0.2)).to(torch.bfloat16)
+    turns, rope = rope_of(attn, rot, start=start) if rot else (None, None)
+    offs = torch.tensor([sum(q_lens[:i]) for i in range(4)], dtype=torch.int32, device=DEV)
+    L = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    tokens = torch.tensor([t for _, _, t in rows_of(lens, q_lens)])
+    # (the rotation's place is the queries': keys rotated alike only where they fit)
+    if rot and start + rot > 128:
+        with pytest.raises(attn.AttnError):
+            attn.attn_append_kv_fp8(k.to(DEV), v.to(DEV), *fresh8(pool), L, max_kv_len=200,
+                                    max_q_len=max(q_lens), page_table=pool.table.to(DEV),
+                                    q=q.to(DEV), q_row_offsets=offs, rope=rope)
+        return
+    with_q, without = fresh8(pool), fresh8(pool)
+    kw = dict(max_kv_len=200, max_q_len=max(q_lens), page_table=pool.table.to(DEV),
+              q_row_offsets=offs, rope=rope)
+    qo = attn.attn_append_kv_fp8(k.to(DEV), v.to(DEV), *with_q, L, q=q.to(DEV), q_norm=qn.to(DEV),
+                                 **kw)
+    attn.attn_append_kv_fp8(k.to(DEV), v.to(DEV), *without, L, **kw)
+    exact, err = R.head_rows(q, turns, tokens, norm=qn, start=start)
+    R.assert_bf16(qo, exact, err, "q")
+    for a, b in zip(with_q, without):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+        assert a.float().abs().sum() > 0
+
+
+def fresh8(pool):
+    return ([torch.zeros(pool.pages, 64, 2, 128, dtype=FP8, device=DEV) for _ in range(2)] +
+            [torch.ones(pool.pages, 4, 2, device=DEV) for _ in range(2)])
+
+
+@pytest.mark.parametrize("kind", ["bf16", "latent", "odd", "fp8", "fp8 odd"])
+def test_rows_of_no_sequence_are_left(attn, kind):
+    """Rows before the first offset and behind the last: neither stored nor written."""
+    lens, q_lens, pad = [70, 3, 200], [2, 1, 60], 5
+    pool = Pool(lens, 64, 9)
+    dim = 576 if kind == "latent" else 128
+    hkv = 1 if kind == "latent" else 2
+    rows = sum(q_lens)
+    odd = "odd" in kind
+    rot = 20 if odd else 64                       # 20: pairs that cross 16-byte vectors
+    turns, rope = rope_of(attn, rot, start=8 if odd else 0)
+    x = [randn(i, rows + 2 * pad, h, dim).to(DEV) for i, h in ((1, hkv), (2, hkv), (3, 4))]
+    offs = torch.tensor([pad, pad + 2, pad + 3, pad + 63], dtype=torch.int32, device=DEV)
+    L = torch.tensor(lens, dtype=torch.int32, device=DEV)
+
+    def go(k, v, q, offs):
+        qo = torch.full(q.shape, 3.0, dtype=torch.bfloat16, device=DEV)
+        kw = dict(max_kv_len=200, page_table=pool.table.to(DEV), q=q, q_out=qo,
+                  q_row_offsets=offs, rope=rope)
+        if "fp8" in kind:
+            cache = fresh8(pool)
+            attn.attn_append_kv_fp8(k, v, *cache, L, max_q_len=60, **kw)
+        else:
+            cache = [torch.zeros(pool.pages, 64, hkv, dim, dtype=torch.bfloat16, device=DEV)
+                     for _ in range(1 if kind == "latent" else 2)]
+            vs = (None, None) if kind == "latent" else (v, cache[1])
+            attn.attn_append_kv(k, vs[0], cache[0], vs[1], L, **kw)
+        return qo, cache
+
+    qo, cache = go(*x, offs)
+    q1, cache1 = go(*[t[pad:-pad] for t in x], offs - pad)
+    assert (qo[:pad] == 3.0).all() and (qo[-pad:] == 3.0).all()
+    assert torch.equal(qo[pad:-pad], q1)
+    for a, b in zip(cache, cache1):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+        assert a.float().abs().sum() > 0
+
+
+def test_offsets_beyond_32_bits(attn):
+    """Pages whose first byte is behind 2^32, in both caches, appended to and read."""
+    pages, page, hkv = 70000, 64, 8
+    last = torch.tensor([[pages - 1, pages - 3]], dtype=torch.int32, device=DEV)
+    k, v, q = (randn(i, 100, h, 128).to(DEV) for i, h in ((1, hkv), (2, hkv), (3, 8)))
+    turns, rope = rope_of(attn, 128)
+    L = torch.tensor([100], dtype=torch.int32, device=DEV)
+    offs = torch.tensor([0, 100], dtype=torch.int32, device=DEV)
+
+    def caches(n, dtype):
+        return [torch.zeros(n, page, hkv, 128, dtype=dtype, device=DEV) for _ in range(2)]
+
+    def go(n, table):
+        kw = dict(max_kv_len=100, page_table=table, q=q, q_row_offsets=offs, rope=rope)
+        c16, c8 = caches(n, torch.bfloat16), caches(n, FP8)
+        s8 = [torch.ones(n, 4, hkv, device=DEV) for _ in range(2)]
+        q16 = attn.attn_append_kv(k, v, *c16, L, **kw)
+        q8 = attn.attn_append_kv_fp8(k, v, *c8, *s8, L, max_q_len=100, **kw)
+        kw = dict(group=1, scale=0.05, max_kv_len=100, page_table=table)
+        a, _ = attn.attn_decode(q16[-1:], *c16, L, **kw)
+        b, _ = attn.attn_decode_fp8(q8[-1:], *c8, *s8, L, **kw)
+        return a, b
+
+    near = go(2, torch.tensor([[0, 1]], dtype=torch.int32, device=DEV))
+    far = go(pages, last)
+    for a, b in zip(near, far):
+        assert torch.isfinite(a).all() and torch.equal(a, b)
+
+
+def test_append_then_attend_bf16(attn):
+    """A prompt and then single tokens: attention over the cache against attention over the rows."""
+    hq, hkv, page = 8, 2, 64
+    table = torch.tensor([[3, 1], [0, 5]], dtype=torch.int32, device=DEV)
+    kc, vc = (torch.zeros(6, page, hkv, 128, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    turns, rope = rope_of(attn, 128)
+    lens, history = [70, 31], [[], []]
+    for step in range(4):
+        n = lens if step == 0 else [1, 1]
+        if step:
+            lens = [x + 1 for x in lens]
+        x = randn(step, sum(n), hq + 2 * hkv, 128).to(DEV)
+        L = torch.tensor(lens, dtype=torch.int32, device=DEV)
+        offs = torch.tensor([0, n[0], n[0] + n[1]], dtype=torch.int32, device=DEV)
+        q = attn.attn_append_kv(x[:, hq:hq + hkv], x[:, hq + hkv:], kc, vc, L, max_kv_len=128,
+                                page_table=table, q=x[:, :hq],
+                                q_row_offsets=offs if step == 0 else None, rope=rope)
+        tokens = [torch.arange(a - b, a) for a, b in zip(lens, n)]
+        ke, _ = R.head_rows(x[:, hq:hq + hkv].cpu(), turns, torch.cat(tokens))
+        at = 0
+        for b in range(2):
+            history[b].append((ke[at:at + n[b]], x[at:at + n[b], hq + hkv:].cpu().double()))
+            at += n[b]
+        if step == 0:
+            continue
+        out, _ = attn.attn_decode(q, kc, vc, L, group=4, scale=0.05, max_kv_len=128,
+                                  page_table=table)
+        for b in range(2):
+            K, V = (torch.cat([h[i] for h in history[b]]).repeat_interleave(4, 1) for i in (0, 1))
+            s = torch.einsum("hd,thd->ht", q[b].cpu().double(), K) * 0.05
+            want = torch.einsum("ht,thd->hd", torch.softmax(s, 1), V)
+            # keys off by half a step of bf16 move a score by at most 2^-8 sum |q k| scale = d,
+            # a weight by a factor of at most e^(2 d); weights and output round to bf16 once
+            d = (torch.einsum("hd,thd->ht", q[b].cpu().double().abs(), K.abs()) * 0.05 *
+                 R.BF16_HALF).amax(1)
+            bound = (torch.expm1(2 * d)[:, None] + 2 * R.BF16_HALF) * V.abs().amax()
+            assert ((out[b].cpu().double() - want).abs() <= bound).all()
+
+
+def test_append_then_attend_latent(attn):
+    """Latent rows appended token by token, against the same rows written at once."""
+    hq, page, steps = 128, 64, 70
+    table = torch.tensor([[2, 0]], dtype=torch.int32, device=DEV)
+    turns, rope = rope_of(attn, 64, start=512, interleaved=True)
+    k, q = randn(1, steps, 1, 576).to(DEV), randn(2, steps, hq, 576).to(DEV)
+    one, all_ = (torch.zeros(3, page, 1, 576, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    outs = []
+    for t in range(steps):
+        L = torch.tensor([t + 1], dtype=torch.int32, device=DEV)
+        qt = attn.attn_append_kv(k[t:t + 1], None, one, None, L, max_kv_len=128,
+                                 page_table=table, q=q[t:t + 1], rope=rope)
+    L = torch.tensor([steps], dtype=torch.int32, device=DEV)
+    qa = attn.attn_append_kv(k, None, all_, None, L, max_kv_len=128, page_table=table, q=q,
+                             q_row_offsets=torch.tensor([0, steps], dtype=torch.int32, device=DEV),
+                             rope=rope)
+    assert torch.equal(one, all_) and torch.equal(qt[0], qa[-1])
+    for c in (one, all_):
+        outs.append(attn.attn_mla_decode(qt, c, L, scale=0.04, max_kv_len=128,
+                                         page_table=table)[0])
+    assert torch.equal(*outs) and outs[0].abs().sum() > 0
+
+
 @pytest.mark.parametrize("fp8", [False, True])
 def test_append_is_captured_and_replayed(attn, fp8):
     """A captured append replayed with other lengths and rows, on another stream."""

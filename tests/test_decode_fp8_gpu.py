@@ -222,6 +222,57 @@ def test_nan_in_a_visible_token_only(attn):
         assert out[1:3].isnan().any(-1).all()
 
 
+@pytest.mark.parametrize("q_lens", [[1, 1, 1], [3, 1, 2]])
+def test_rows_of_no_sequence_are_left(attn, q_lens):
+    """A padded batch: more rows than the offsets give out."""
+    c = Case([300, 77, 1000], q_lens, seed=14)
+    n = c.q.shape[0]
+    c.q = torch.cat([c.q, torch.full((3, 8, 128), float("nan"), dtype=torch.bfloat16)])
+    out = torch.full((n + 3, 8, 128), 3.0, dtype=torch.bfloat16, device=DEV)
+    lse = torch.full((n + 3, 8), 5.0, device=DEV)
+    c.run(attn, out=out, lse=lse)
+    assert (out[n:] == 3.0).all() and (lse[n:] == 5.0).all()
+    c.q = c.q[:n]
+    want, wl = c.check(attn, "rows")
+    assert torch.equal(out[:n], want) and torch.equal(lse[:n], wl)
+
+
+def test_sequences_that_share_pages(attn):
+    """A common prefix: two sequences' tables name the same pages."""
+    c = Case([256, 256], page=64, seed=15, garbage=False)
+    c.table[1] = c.table[0]
+    c.check(attn, "shared pages")
+
+
+def test_calls_on_two_streams_at_once(attn):
+    a, b = Case([3000, 77], seed=16), Case([900, 1], seed=17)
+    want = [x.run(attn)[0] for x in (a, b)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    data = []
+    for x in (a, b):
+        (kc, ks), (vc, vs) = [[t.to(DEV) for t in y] for y in x.caches]
+        data.append((x.q.to(DEV), kc, vc, ks, vs,
+                     torch.tensor(x.lens, dtype=torch.int32, device=DEV), x.table.to(DEV)))
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(5):
+        for s, x, d in zip(streams, (a, b), data):
+            with torch.cuda.stream(s):
+                got.append(attn.attn_decode_fp8(*d[:6], group=x.group, scale=x.scale,
+                                                max_kv_len=max(x.lens), page_table=d[6],
+                                                causal=True)[0])
+    torch.cuda.synchronize()
+    for i, o in enumerate(got):
+        assert torch.equal(o, want[i % 2])
+
+
+def test_v_scale_past_the_range_is_not_silent(attn):
+    c = Case([200], seed=18, garbage=False, block=64)
+    c.caches[1][1][int(c.table[0, 1])] = 2.0 ** 66
+    out, _ = c.run(attn)
+    assert out.isnan().all()
+
+
 def test_outputs_given_and_workspace_shared_in_order(attn):
     c = Case([300, 77, 1000], seed=10)
     ws = torch.empty(attn.attn_decode_fp8_workspace(3, 8, c.group) + 512, dtype=torch.uint8,
