@@ -94,6 +94,7 @@ cudaError_t launch_head_tiles(const RowsParams &p, cudaStream_t stream);
 // where fp8_tiles_take_queries.
 bool fp8_tiles_take_queries(const RowsParams &p);
 cudaError_t launch_fp8_tiles(const RowsParams &p, cudaStream_t stream);
+cudaError_t launch_fp8_runs(const RowsParams &p, cudaStream_t stream);   // keys and values alone
 // CTAs of the 8-bit decode grid on num_sms SMs.
 int fp8_decode_ctas(int num_sms);
 cudaError_t launch_gqa_decode_fp8(const Fp8DecodeParams &p, int ctas, cudaStream_t stream);

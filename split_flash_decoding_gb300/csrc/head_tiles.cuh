@@ -45,24 +45,18 @@ struct Cut {
     int any_norm;
 };
 
-// L lanes an item, T threads a CTA, S items a thread.
-template <int L, int S, int T>
-struct Shape {
-    static constexpr int kItems = T / L;                  // at once
-    static constexpr int kMaxRows = kItems * S < kGroupTokens ? kItems * S : kGroupTokens;
-};
+constexpr int kThreads = 256;
 
-// Shared memory: angles [rows][4][lanes] {c, s, c, s}, then per row its place.
+// Items of L lanes at once: also the most rows of a tile.
+template <int L>
+constexpr int kItemsOf = kThreads / L;
+
+// Where a row of the tile goes.
 struct Place {
     long long k_at, v_at;             // element offsets into the caches
     int pos, token, page, slot;
     int stored;                       // -1: the row belongs to no sequence; 0: not stored; 1
 };
-
-__host__ __device__ __forceinline__ int turning_lanes(const RopeParams &rope, int dim) {
-    const int R = rope.rot_dim / 8, vecs = dim / 8;
-    return rope.interleaved ? (R < (vecs + 1) / 2 ? R : (vecs + 1) / 2) : R / 2;
-}
 
 // The m-th vector (8 channels) of a head, the rotated ones first: R of them from
 // vector `start` on.
@@ -155,6 +149,62 @@ __device__ __forceinline__ float2 decode2(uint32_t c) {
         __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(c & 0xffffu), __NV_E4M3)));
 }
 
+// A lane's 16 channels as codes.
+__device__ __forceinline__ void store_codes(uint8_t *a, uint8_t *b, const float2 (&ya)[4],
+                                            const float2 (&yb)[4], float f, bool infinite) {
+    uint2 wa, wb;
+    if (infinite) {
+        wa = make_uint2(encode4(ya[0], ya[1], f), encode4(ya[2], ya[3], f));
+        wb = make_uint2(encode4(yb[0], yb[1], f), encode4(yb[2], yb[3], f));
+    } else {
+        wa = make_uint2(encode4_finite(ya[0], ya[1], f), encode4_finite(ya[2], ya[3], f));
+        wb = make_uint2(encode4_finite(yb[0], yb[1], f), encode4_finite(yb[2], yb[3], f));
+    }
+    *reinterpret_cast<uint2 *>(a) = wa;
+    *reinterpret_cast<uint2 *>(b) = wb;
+}
+
+// Four held codes at a scale that grew: ratio is the old one over the new.
+__device__ __forceinline__ uint32_t recode4(uint32_t c, float ratio) {
+    return encode4(decode2(c), decode2(c >> 16), ratio);
+}
+
+// Largest |value| of a lane's channels; NaN does not count.
+__device__ __forceinline__ float largest(const float2 (&ya)[4], const float2 (&yb)[4]) {
+    float top = 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        top = fmax3(top, fabsf(ya[k].x), fabsf(ya[k].y));
+        top = fmax3(top, fabsf(yb[k].x), fabsf(yb[k].y));
+    }
+    return top;
+}
+
+// The same where there is an infinity: it does not count either.
+__device__ __forceinline__ float largest_finite(const float2 (&ya)[4], const float2 (&yb)[4]) {
+    float top = 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        top = fmaxf(fmaxf(fmaxf(finite_abs(ya[k].x), finite_abs(ya[k].y)), top),
+                    fmaxf(finite_abs(yb[k].x), finite_abs(yb[k].y)));
+    return top;
+}
+
+// Turn entry k of a lane's two vectors (turn_b: the second is rotated as well; in
+// the half layout always).
+template <bool kInter>
+__device__ __forceinline__ void rotate_pairs(float2 &ya, float2 &yb, const float4 &v, bool turn_b) {
+    const float2 y = ya, z = yb;
+    if (kInter) {
+        ya = make_float2(fmaf(y.x, v.x, -y.y * v.y), fmaf(y.y, v.x, y.x * v.y));
+        if (turn_b) yb = make_float2(fmaf(z.x, v.z, -z.y * v.w), fmaf(z.y, v.z, z.x * v.w));
+    } else {
+        const float2 c = make_float2(v.x, v.z), n = make_float2(v.y, v.w);
+        ya = __ffma2_rn(y, c, __fmul2_rn(z, make_float2(-n.x, -n.y)));
+        yb = __ffma2_rn(z, c, __fmul2_rn(y, n));
+    }
+}
+
 // Sequence of row r; -1: none.  (One thread a row; a warp's rows read the same lines.)
 __device__ __forceinline__ int sequence_of(const RowsParams &p, int r) {
     if (!p.q_row_offsets) return r;
@@ -232,7 +282,14 @@ __device__ __forceinline__ bool tile_tokens(const RowsParams &p, int tile, int l
     return true;
 }
 
-// One of a thread's items: where it is in the list of heads (q, then k, then v).
+// At least as many tiles as a call has: a sequence of n rows meets at most
+// (n - 1) / kGroupTokens + 2 groups.
+inline long long fp8_tile_count(const RowsParams &p) {
+    const long long bound = p.num_rows / kGroupTokens + 2LL * p.batch;
+    return p.q_row_offsets && bound < p.num_rows ? bound : p.num_rows;
+}
+
+// A thread's item: where it is in the list of heads (q, then k, then v).
 struct Item {
     enum { kNormA = 1, kNormB = 2, kTurnA = 4, kTurnB = 8 };
     const uint16_t *src;              // its head vector
@@ -240,13 +297,12 @@ struct Item {
     long long src_step, dst_step;     // to the item's next head
     uint4 ga, gb;                     // the norm's weights of its channels
     float mean, eps;
-    long long row_step;               // kItems rows of src
     int row, h, h_end, kind, head;    // h_end: first head of the next kind
     int ca, cb;                       // its two first channels; -1: none
     int flags;
     bool to_cache;
 
-    template <int kItems, bool kInter>
+    template <bool kInter>
     __device__ __forceinline__ void open(const RowsParams &p, int r0, int i0, int h1,
                                          int step_heads) {
         ca = cb = -1;
@@ -256,7 +312,7 @@ struct Item {
         h_end = 0x7fffffff;
         src = nullptr;
         dst = nullptr;
-        src_step = dst_step = row_step = 0;
+        src_step = dst_step = 0;
         mean = eps = 0.f;
         to_cache = false;
         ga = gb = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);   // 1
@@ -273,7 +329,6 @@ struct Item {
         if (b >= 0) cb = 8 * ordered(b, turning, start);
         src = x.in + (r0 + row) * x.in_row + head * x.in_head;
         src_step = step_heads * x.in_head;
-        row_step = kItems * x.in_row;
         to_cache = x.out == nullptr;
         if (to_cache) {
             const CacheOut &c = kind == 1 ? p.kc : p.vc;
@@ -298,27 +353,24 @@ struct Item {
     }
 
     // step_heads heads on
-    template <int kItems, bool kInter>
+    template <bool kInter>
     __device__ __forceinline__ void advance(const RowsParams &p, int r0, int i0, int h1,
                                             int step_heads) {
         h += step_heads;
         head += step_heads;
         src += src_step;
         dst += dst_step;
-        if (h >= h_end) open<kItems, kInter>(p, r0, i0, h1, step_heads);
+        if (h >= h_end) open<kInter>(p, r0, i0, h1, step_heads);
     }
 };
 
-template <int L, int S, int T, bool kInter, bool kFp8>
-__global__ void __launch_bounds__(T, kFp8 ? 2 : 4)
+template <int L, bool kInter, bool kFp8>
+__global__ void __launch_bounds__(kThreads, kFp8 ? 2 : 4)
 head_tiles_kernel(const __grid_constant__ RowsParams p, const __grid_constant__ Cut cut) {
-    using Sh = Shape<L, S, T>;
-    constexpr int kThreads = T;
-    constexpr int kItems = Sh::kItems;
-    extern __shared__ __align__(16) float4 angles[];             // [rows][4][lanes]
-    __shared__ Place places[Sh::kMaxRows];
-    __shared__ float row_max[kFp8 ? kItems * S : 1];             // S = 1: then 1 / scale
-    __shared__ float s_inv[kFp8 && S > 1 ? kGroupTokens : 1];
+    constexpr int kItems = kItemsOf<L>;
+    extern __shared__ __align__(16) float4 angles[];             // [rows][4][lanes] {c, s, c, s}
+    __shared__ Place places[kItems];
+    __shared__ float row_max[kFp8 ? kItems : 1];                 // then 1 / scale
     __shared__ Tokens s_tile;
     __shared__ int s_any;
     const int tid = threadIdx.x, lane = tid & 31;
@@ -329,8 +381,7 @@ head_tiles_kernel(const __grid_constant__ RowsParams p, const __grid_constant__ 
     // ---- rows of the tile and their places -------------------------------------
     int r0, n;
     if (kFp8) {
-        static_assert(!kFp8 || S == 1 || kItems * S == kGroupTokens, "a row an item");
-        for (int i = tid; i < kItems * S; i += kThreads) row_max[i] = 0.f;
+        for (int i = tid; i < kItems; i += kThreads) row_max[i] = 0.f;
         if (tid < 32) {
             Tokens t;
             const bool any = tile_tokens(p, tile, lane, t);
@@ -350,26 +401,21 @@ head_tiles_kernel(const __grid_constant__ RowsParams p, const __grid_constant__ 
 
     // ---- items: the first heads' loads go out before anything else ----------------
     int shift = 0;                                               // rows padded to 2^shift
-    while ((1 << shift) < (S > 1 ? kItems * S : n)) ++shift;
-    const int step_heads = kItems * S >> shift;                  // heads in work at once
+    while ((1 << shift) < n) ++shift;
+    const int step_heads = kItems >> shift;                      // heads in work at once
     const int i0 = tid & (L - 1);
     const int item0 = tid / L;
     const int R = p.rope.rot_dim / 8, half = p.rope.rot_dim / 2;
     Item it;
-    it.row = item0 & ((1 << shift) - 1);                         // and + kItems, S times
+    it.row = item0 & ((1 << shift) - 1);
     it.h = it.row < n ? h0 + (item0 >> shift) : h1;
     it.row = min(it.row, n - 1);
-    it.open<kItems, kInter>(p, r0, i0, h1, step_heads);
-    uint4 ra[S], rb[S];
+    it.open<kInter>(p, r0, i0, h1, step_heads);
+    uint4 ra, rb;
     const auto load = [&]() {
-#pragma unroll
-        for (int s = 0; s < S; ++s) {
-            ra[s] = rb[s] = make_uint4(0u, 0u, 0u, 0u);
-            if (S > 1 && it.row + s * kItems >= n) continue;
-            const uint16_t *src = it.src + s * it.row_step;
-            if (it.ca >= 0) ra[s] = *reinterpret_cast<const uint4 *>(src + it.ca);
-            if (it.cb >= 0) rb[s] = *reinterpret_cast<const uint4 *>(src + it.cb);
-        }
+        ra = rb = make_uint4(0u, 0u, 0u, 0u);
+        if (it.ca >= 0) ra = *reinterpret_cast<const uint4 *>(it.src + it.ca);
+        if (it.cb >= 0) rb = *reinterpret_cast<const uint4 *>(it.src + it.cb);
     };
     load();
 
@@ -436,63 +482,43 @@ head_tiles_kernel(const __grid_constant__ RowsParams p, const __grid_constant__ 
 
 #pragma unroll 1
     for (int hs = h0; hs < h1; hs += step_heads) {
-        float2 ya[S][4], yb[S][4];
+        float2 ya[4], yb[4];
+        unpack8(ra, ya);
+        unpack8(rb, yb);
+        const Place &at = places[it.row];
+        if (cut.any_norm) {
+            float2 sq = make_float2(0.f, 0.f);                   // (no vector: zeros)
+            if (it.flags & Item::kNormA) add_squares(ya, sq);
+            if (it.flags & Item::kNormB) add_squares(yb, sq);
+            float sum = sq.x + sq.y;
 #pragma unroll
-        for (int s = 0; s < S; ++s) {
-            const Item &x = it;
-            const int row = min(x.row + s * kItems, n - 1);
-            unpack8(ra[s], ya[s]);
-            unpack8(rb[s], yb[s]);
-            if (cut.any_norm) {
-                float2 sq = make_float2(0.f, 0.f);               // (no vector: zeros)
-                if (x.flags & Item::kNormA) add_squares(ya[s], sq);
-                if (x.flags & Item::kNormB) add_squares(yb[s], sq);
-                float sum = sq.x + sq.y;
+            for (int o = 1; o < L; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            const float inv = rsqrtf(fmaf(sum, it.mean, it.eps));
+            if (it.flags & Item::kNormA) scale8(ya, it.ga, inv);
+            if (it.flags & Item::kNormB) scale8(yb, it.gb, inv);
+        }
+        if (it.flags & Item::kTurnA) {
+            const float4 *t = angles + it.row * 4 * L + i0;
 #pragma unroll
-                for (int o = 1; o < L; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                const float inv = rsqrtf(fmaf(sum, x.mean, x.eps));
-                if (x.flags & Item::kNormA) scale8(ya[s], x.ga, inv);
-                if (x.flags & Item::kNormB) scale8(yb[s], x.gb, inv);
+            for (int k = 0; k < 4; ++k)
+                rotate_pairs<kInter>(ya[k], yb[k], t[k * L], it.flags & Item::kTurnB);
+        }
+        if (!kFp8 || it.kind == 0) {
+            uint16_t *dst = it.dst;
+            bool store = at.stored >= 0;
+            if (!kFp8 && it.to_cache) {
+                dst += it.kind == 1 ? at.k_at : at.v_at;
+                store = at.stored > 0;
             }
-            if (x.flags & Item::kTurnA) {
-                const float4 *t = angles + row * 4 * L + i0;
-                const bool tb = x.flags & Item::kTurnB;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float4 v = t[k * L];
-                    const float2 y = ya[s][k], z = yb[s][k];
-                    if (kInter) {
-                        ya[s][k] = make_float2(fmaf(y.x, v.x, -y.y * v.y), fmaf(y.y, v.x, y.x * v.y));
-                        if (tb)
-                            yb[s][k] =
-                                make_float2(fmaf(z.x, v.z, -z.y * v.w), fmaf(z.y, v.z, z.x * v.w));
-                    } else {
-                        const float2 c = make_float2(v.x, v.z), n2 = make_float2(v.y, v.w);
-                        ya[s][k] = __ffma2_rn(y, c, __fmul2_rn(z, make_float2(-n2.x, -n2.y)));
-                        yb[s][k] = __ffma2_rn(z, c, __fmul2_rn(y, n2));
-                    }
-                }
-            }
-            if (!kFp8 || x.kind == 0) {
-                uint16_t *dst = x.dst;
-                const Place &at = places[row];
-                bool store = at.stored >= 0 && (S == 1 || x.row + s * kItems < n);
-                if (!kFp8 && x.to_cache) {
-                    dst += x.kind == 1 ? at.k_at : at.v_at;
-                    store = store && at.stored > 0;
-                } else if (S > 1) {
-                    dst += s * kItems * p.q.out_row;             // (S > 1: queries alone)
-                }
-                // (what is neither normed nor rotated goes as it is, NaN payloads too)
-                const bool plain = !(x.flags & (Item::kNormA | Item::kNormB | Item::kTurnA));
-                if (store && x.ca >= 0)
-                    *reinterpret_cast<uint4 *>(dst + x.ca) = plain ? ra[s] : pack8(ya[s]);
-                if (store && x.cb >= 0)
-                    *reinterpret_cast<uint4 *>(dst + x.cb) = plain ? rb[s] : pack8(yb[s]);
-            }
+            // (what is neither normed nor rotated goes as it is, NaN payloads too)
+            const bool plain = !(it.flags & (Item::kNormA | Item::kNormB | Item::kTurnA));
+            if (store && it.ca >= 0)
+                *reinterpret_cast<uint4 *>(dst + it.ca) = plain ? ra : pack8(ya);
+            if (store && it.cb >= 0)
+                *reinterpret_cast<uint4 *>(dst + it.cb) = plain ? rb : pack8(yb);
         }
         if (!kFp8 || hs + step_heads <= p.q.heads) {             // queries only: uniform
-            it.advance<kItems, kInter>(p, r0, i0, h1, step_heads);
+            it.advance<kInter>(p, r0, i0, h1, step_heads);
             load();
             continue;
         }
@@ -503,114 +529,46 @@ head_tiles_kernel(const __grid_constant__ RowsParams p, const __grid_constant__ 
         const int held = s_tile.first == s_tile.begin && base >= 0 && places[0].stored > 0
                              ? base % B : 0;
         float ratio = 1.f;                                       // of a held block's row 0
-        unsigned infinite = 0;                                   // items with an infinity
-        if constexpr (S == 1) __syncthreads();                   // the last heads' scales are used
+        __syncthreads();                                         // the last heads' scales are used
+        // (NaN never counts; infinities do not either, but cost a second look)
+        float top = largest(ya, yb);
+        const bool infinite = top > FLT_MAX;
+        if (infinite) top = largest_finite(ya, yb);
 #pragma unroll
-        for (int s = 0; s < S; ++s) {
-            // (NaN never counts; infinities do not either, but cost a second look)
-            float top = 0.f;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                top = fmax3(top, fabsf(ya[s][k].x), fabsf(ya[s][k].y));
-                top = fmax3(top, fabsf(yb[s][k].x), fabsf(yb[s][k].y));
-            }
-            if (top > FLT_MAX) {
-                infinite |= 1u << s;
-                top = 0.f;
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    top = fmaxf(fmaxf(fmaxf(finite_abs(ya[s][k].x), finite_abs(ya[s][k].y)), top),
-                                fmaxf(finite_abs(yb[s][k].x), finite_abs(yb[s][k].y)));
-            }
-#pragma unroll
-            for (int o = 1; o < L; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            if (S == 1) {
-                if (i0 == 0) row_max[item0] = top;               // (no item: 0)
-            } else {
-                // in the place of its token in the group, so that blocks are aligned
-                const int row = it.row + s * kItems;
-                if (i0 == 0 && it.ca >= 0 && row < n && places[row].stored > 0)
-                    row_max[(base + row) & (kGroupTokens - 1)] = top;
-            }
-        }
+        for (int o = 1; o < L; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        if (i0 == 0) row_max[item0] = top;                       // (no item: 0)
         __syncthreads();
-        if constexpr (S == 1) {
-            // The thread of a block's first stored row in the tile takes the maximum
-            // over the block's rows, writes the scale and leaves 1 / scale in their
-            // places.
-            const int row = tid & ((1 << shift) - 1), h = hs + (tid >> shift);
-            if (tid < kItems && row < n && h < h1 && h >= p.q.heads && places[row].stored > 0) {
-                const int t = places[row].token;
-                const int first = max(t / B * B - base, max(-base, 0));
-                const int last = min(t / B * B + B, min(base + n, p.max_kv_len)) - base;
-                if (row == first) {
-                    float top = 0.f;
-                    for (int i = first; i < last; ++i) top = fmaxf(top, row_max[(tid - row) + i]);
-                    const bool is_k = h < p.q.heads + p.k.heads;
-                    const int head = h - p.q.heads - (is_k ? 0 : p.k.heads);
-                    const CacheOut &c = is_k ? p.kc : p.vc;
-                    float *where = c.scale + places[row].page * c.scale_page +
-                                   (places[row].slot / B) * c.scale_block + head * c.scale_head;
-                    float scale = pow2i(scale_exponent(top));
-                    if (row == 0 && held > 0) {
-                        const float old = *where;
-                        if (scale > old) ratio = old / scale; else scale = old;
-                    }
-                    *where = scale;
-                    const float inv = 1.f / scale;
-                    for (int i = first; i < last; ++i) row_max[(tid - row) + i] = inv;
-                }
-            }
-        } else {
-            // One head: thread t < 128 stands for token t of the group; a block's
-            // maximum by shuffles, over warps through shared memory.
-            __shared__ float s_part[4];
-            float top = 0.f;
-            if (tid < kGroupTokens) {
-                top = row_max[tid];
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1)
-                    if (o < B) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                if (lane == 0) s_part[tid >> 5] = top;
-            }
-            if (B > 32) {
-                __syncthreads();
-                if (tid < kGroupTokens)
-                    top = B == 64 ? fmaxf(s_part[(tid >> 5) & 2], s_part[((tid >> 5) & 2) + 1])
-                                  : fmaxf(fmaxf(s_part[0], s_part[1]), fmaxf(s_part[2], s_part[3]));
-            }
-            const int row = tid - (base & (kGroupTokens - 1));
-            float *where = nullptr;
-            float scale = 0.f;
-            if (tid < kGroupTokens && row >= 0 && row < n && places[row].stored > 0 &&
-                hs >= p.q.heads) {
-                const int t = base + row;
-                const bool is_k = hs < p.q.heads + p.k.heads;
-                const int head = hs - p.q.heads - (is_k ? 0 : p.k.heads);
+        // The thread of a block's first stored row in the tile takes the maximum over
+        // the block's rows, writes the scale and leaves 1 / scale in their places.
+        const int row = tid & ((1 << shift) - 1), h = hs + (tid >> shift);
+        if (tid < kItems && row < n && h < h1 && h >= p.q.heads && places[row].stored > 0) {
+            const int t = places[row].token;
+            const int first = max(t / B * B - base, max(-base, 0));
+            const int last = min(t / B * B + B, min(base + n, p.max_kv_len)) - base;
+            if (row == first) {
+                float most = 0.f;
+                for (int i = first; i < last; ++i) most = fmaxf(most, row_max[(tid - row) + i]);
+                const bool is_k = h < p.q.heads + p.k.heads;
+                const int head = h - p.q.heads - (is_k ? 0 : p.k.heads);
                 const CacheOut &c = is_k ? p.kc : p.vc;
-                float *at = c.scale + places[row].page * c.scale_page +
-                            (places[row].slot / B) * c.scale_block + head * c.scale_head;
-                scale = pow2i(scale_exponent(top));
-                if (held > 0 && t / B == base / B) {
-                    const float old = *at;
+                float *where = c.scale + places[row].page * c.scale_page +
+                               (places[row].slot / B) * c.scale_block + head * c.scale_head;
+                float scale = pow2i(scale_exponent(most));
+                if (row == 0 && held > 0) {
+                    const float old = *where;
                     if (scale > old) ratio = old / scale; else scale = old;
                 }
-                s_inv[row] = 1.f / scale;
-                if (t % B == 0 || row == 0) where = at;
+                *where = scale;
+                const float inv = 1.f / scale;
+                for (int i = first; i < last; ++i) row_max[(tid - row) + i] = inv;
             }
-            __syncthreads();                                     // the old scale has been read
-            if (where) *where = scale;
         }
         // What the first block held, where its scale grew: eight tokens a warp at a
         // time, all their loads before the first store.
         if (held > 0) {
-            __shared__ float s_ratio[S == 1 ? kItems : 1];
+            __shared__ float s_ratio[kItems];
             const int heads_now = min(step_heads, h1 - hs);
-            if (S == 1) {
-                if (tid < kItems && (tid & ((1 << shift) - 1)) == 0) s_ratio[tid >> shift] = ratio;
-            } else {
-                if (tid == (base & (kGroupTokens - 1))) s_ratio[0] = ratio;
-            }
+            if (tid < kItems && (tid & ((1 << shift) - 1)) == 0) s_ratio[tid >> shift] = ratio;
             const int batches = __syncthreads_or(ratio != 1.f) ? (held + 7) / 8 : 0;
             for (int w = tid >> 5; w < heads_now * batches; w += kThreads / 32) {
                 const int hh = w / batches, g = hs + hh;
@@ -620,64 +578,42 @@ head_tiles_kernel(const __grid_constant__ RowsParams p, const __grid_constant__ 
                 const CacheOut &c = is_k ? p.kc : p.vc;
                 // the held tokens are the slots just before the tile's first row's
                 const int i1 = 8 * (w - hh * batches) + 1;
-                uint32_t *at = reinterpret_cast<uint32_t *>(
+                uint32_t *to = reinterpret_cast<uint32_t *>(
                                    c.base + (is_k ? places[0].k_at : places[0].v_at) +
                                    head * c.head_stride - i1 * c.token_stride) + lane;
                 const long long step = c.token_stride / 4;
                 uint32_t old[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    if (i1 + i <= held) old[i] = *(at - i * step);
+                    if (i1 + i <= held) old[i] = *(to - i * step);
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    if (i1 + i <= held)
-                        *(at - i * step) = encode4(decode2(old[i]), decode2(old[i] >> 16),
-                                                   s_ratio[hh]);
+                    if (i1 + i <= held) *(to - i * step) = recode4(old[i], s_ratio[hh]);
             }
+        } else {
+            __syncthreads();                                     // 1 / scale is in place
         }
-        if (S == 1 && held == 0) __syncthreads();                // 1 / scale is in place
         // ---- codes ---------------------------------------------------------------------
-#pragma unroll
-        for (int s = 0; s < S; ++s) {
-            const Item &x = it;
-            const int row = x.row + s * kItems;
-            if (x.ca < 0 || x.kind == 0 || row >= n || places[row].stored <= 0) continue;
-            const Place &at = places[row];
-            const CacheOut &c = x.kind == 1 ? p.kc : p.vc;
-            const float f = S == 1 ? row_max[item0] : s_inv[row];
-            uint8_t *dst = c.base + (x.kind == 1 ? at.k_at : at.v_at) + x.head * c.head_stride;
-            uint2 wa, wb;
-            if (infinite >> s & 1) {
-                wa = make_uint2(encode4(ya[s][0], ya[s][1], f), encode4(ya[s][2], ya[s][3], f));
-                wb = make_uint2(encode4(yb[s][0], yb[s][1], f), encode4(yb[s][2], yb[s][3], f));
-            } else {
-                wa = make_uint2(encode4_finite(ya[s][0], ya[s][1], f),
-                                encode4_finite(ya[s][2], ya[s][3], f));
-                wb = make_uint2(encode4_finite(yb[s][0], yb[s][1], f),
-                                encode4_finite(yb[s][2], yb[s][3], f));
-            }
-            *reinterpret_cast<uint2 *>(dst + x.ca) = wa;
-            *reinterpret_cast<uint2 *>(dst + x.cb) = wb;
+        if (it.ca >= 0 && it.kind != 0 && at.stored > 0) {
+            const CacheOut &c = it.kind == 1 ? p.kc : p.vc;
+            const float f = row_max[item0];
+            uint8_t *dst = c.base + (it.kind == 1 ? at.k_at : at.v_at) + it.head * c.head_stride;
+            store_codes(dst + it.ca, dst + it.cb, ya, yb, f, infinite);
         }
-        it.advance<kItems, kInter>(p, r0, i0, h1, step_heads);
+        it.advance<kInter>(p, r0, i0, h1, step_heads);
         load();
     }
 }
 
-template <int L, int S, int T, bool kInter, bool kFp8>
+template <int L, bool kInter, bool kFp8>
 cudaError_t launch(const RowsParams &p, const Cut &cut, long long tiles, cudaStream_t stream) {
     const long long blocks = tiles * cut.chunks;
     if (blocks == 0) return cudaSuccess;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-    const int rows = kFp8 && !p.q_row_offsets ? 1 : cut.tile_rows;
-    const size_t smem = p.rope.rot_dim > 0 ? size_t(rows) * 4 * L * sizeof(float4) : 0;
-    auto kern = head_tiles_kernel<L, S, T, kInter, kFp8>;
-    if (smem > 32768) {
-        const cudaError_t e = cudaFuncSetAttribute(
-            kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
-        if (e != cudaSuccess) return e;
-    }
-    kern<<<static_cast<unsigned>(blocks), T, smem, stream>>>(p, cut);
+    const size_t smem =
+        p.rope.rot_dim > 0 ? size_t(cut.tile_rows) * 4 * L * sizeof(float4) : 0;   // up to 16 KB
+    head_tiles_kernel<L, kInter, kFp8>
+        <<<static_cast<unsigned>(blocks), kThreads, smem, stream>>>(p, cut);
     return cudaGetLastError();
 }
 

@@ -37,15 +37,15 @@ cudaError_t launch_lanes(const RowsParams &p, cudaStream_t stream) {
     cut.tile_rows = 8;
     while (cut.tile_rows > 1 && cut.tile_rows / 2 >= p.num_rows) cut.tile_rows /= 2;
     const long long tiles = (static_cast<long long>(p.num_rows) + cut.tile_rows - 1) / cut.tile_rows;
-    const int step = Shape<L, 1, 256>::kItems / cut.tile_rows;        // heads at once
+    const int step = kItemsOf<L> / cut.tile_rows;        // heads at once
     const int steps = (cut.heads + step - 1) / step;
     long long per_cta = steps * tiles / kWave;
     if (per_cta < 1) per_cta = 1;
     if (per_cta > steps) per_cta = steps;
     cut.chunk_heads = static_cast<int>(per_cta) * step;
     cut.chunks = (cut.heads + cut.chunk_heads - 1) / cut.chunk_heads;
-    return p.rope.interleaved ? launch<L, 1, 256, true, false>(p, cut, tiles, stream)
-                              : launch<L, 1, 256, false, false>(p, cut, tiles, stream);
+    return p.rope.interleaved ? launch<L, true, false>(p, cut, tiles, stream)
+                              : launch<L, false, false>(p, cut, tiles, stream);
 }
 
 }  // namespace
