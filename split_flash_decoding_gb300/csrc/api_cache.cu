@@ -275,6 +275,7 @@ extern "C" int attn_append_kv_fp8(const attn_head_rows_t *q, const attn_head_row
     take_scale(k_scale, &p.kc);
     take_scale(v_scale, &p.vc);
     p.block_tokens = k_scale->block_tokens;
+    while ((1 << p.block_shift) < p.block_tokens) ++p.block_shift;
     p.max_q_len = max_q_len;
     if ((st = device_error_word(&p.err))) return st;
     return map_cuda(launch_append_fp8(p, reinterpret_cast<cudaStream_t>(stream)));

@@ -111,15 +111,15 @@ append_fp8_runs_kernel(const __grid_constant__ RowsParams p, int chunks, int chu
         const int t = group0 + i, row = t - first;
         at.pos = t;
         // (tokens that the first block holds from before have a place too)
-        if (t >= first / B * B && row < count && t < p.max_kv_len) {
+        if (t >= (first & ~(B - 1)) && row < count && t < p.max_kv_len) {
             const int page = page_of(p, s_tile.b, t);
             const int slot = p.page_table ? t & (p.page_size - 1) : t;
             if (page >= 0) {
                 at.stored = 1;
                 at.k_at = page * p.kc.page_stride + slot * p.kc.token_stride;
                 at.v_at = page * p.vc.page_stride + slot * p.vc.token_stride;
-                at.ks_at = page * p.kc.scale_page + (slot / B) * p.kc.scale_block;
-                at.vs_at = page * p.vc.scale_page + (slot / B) * p.vc.scale_block;
+                at.ks_at = page * p.kc.scale_page + (slot >> p.block_shift) * p.kc.scale_block;
+                at.vs_at = page * p.vc.scale_page + (slot >> p.block_shift) * p.vc.scale_block;
             }
         }
         if (p.positions && row >= 0 && row < count) at.pos = p.positions[r0 + row];
@@ -130,7 +130,7 @@ append_fp8_runs_kernel(const __grid_constant__ RowsParams p, int chunks, int chu
     // ---- the first block's old scales; angles, one entry (two pairs) a thread -------
     const int first_slot = first - group0;
     // (B is at most 128, and a first block without a place has no held tokens)
-    const int held = s_tile.first == s_tile.begin && places[first_slot].stored ? first % B : 0;
+    const int held = s_tile.first == s_tile.begin && places[first_slot].stored ? first & (B - 1) : 0;
     if (held > 0 && tid < h1 - h0) {
         const int h = h0 + tid;
         const SlotPlace &at = places[first_slot];
@@ -230,17 +230,24 @@ append_fp8_runs_kernel(const __grid_constant__ RowsParams p, int chunks, int chu
         // ---- scales and codes ------------------------------------------------------------
         const CacheOut &c = is_k ? p.kc : p.vc;
         const int head = is_k ? h : h - p.k.heads;
+        float scale = 0.f, f = 0.f, ratio = 1.f;
 #pragma unroll
         for (int s = 0; s < kS; ++s) {
-            const int slot = 4 * item + s, t = group0 + slot, row = row0 + s;
+            const int slot = 4 * item + s, row = row0 + s;
+            if (s == 0 || B < 4) {                               // (four tokens share blocks of 4)
+                scale = pow2i(scale_exponent(top[s]));
+                ratio = 1.f;
+                if (held > 0 && (slot ^ first_slot) < B) {       // the block of the first token
+                    const float old = s_old[h - h0];
+                    if (scale > old) ratio = old / scale; else scale = old;
+                }
+                f = __frcp_rn(scale);
+            }
             const SlotPlace &at = places[slot];
             if (!at.stored) continue;
             uint8_t *dst = c.base + (is_k ? at.k_at : at.v_at) + head * c.head_stride;
-            float scale = pow2i(scale_exponent(top[s]));
-            const float old = held > 0 && t / B == first / B ? s_old[h - h0] : 0.f;
             if (row < 0) {                                       // held from before
-                if (held > 0 && scale > old) {
-                    const float ratio = old / scale;
+                if (ratio != 1.f) {
                     uint2 *wa = reinterpret_cast<uint2 *>(dst + ca);
                     uint2 *wb = reinterpret_cast<uint2 *>(dst + cb);
                     const uint2 oa = *wa, ob = *wb;
@@ -249,10 +256,8 @@ append_fp8_runs_kernel(const __grid_constant__ RowsParams p, int chunks, int chu
                 }
                 continue;
             }
-            if (!(scale > old) && held > 0 && t / B == first / B) scale = old;
-            if (i0 == 0 && (t % B == 0 || row == 0))
+            if (i0 == 0 && ((slot & (B - 1)) == 0 || row == 0))
                 c.scale[(is_k ? at.ks_at : at.vs_at) + head * c.scale_head] = scale;
-            const float f = 1.f / scale;
             store_codes(dst + ca, dst + cb, ya[s], yb[s], f, infinite >> s & 1);
         }
     }

@@ -55,7 +55,7 @@ struct RowsParams {
     const uint32_t *q_row_offsets;
     const int32_t *page_table;
     int batch, max_kv_len, page_size, num_pages, max_pages;
-    int block_tokens;             // 8-bit caches: tokens per scale
+    int block_tokens, block_shift;  // 8-bit caches: tokens per scale, a power of two
     int max_q_len;
     unsigned *err;
 };

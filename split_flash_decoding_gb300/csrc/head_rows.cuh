@@ -83,9 +83,10 @@ __device__ __forceinline__ RowPlace place_of_row(const RowsParams &p, int r, int
 }
 
 // Page of token t of sequence b; -1 (and error bit 1) if it is not in the pool.
+// (Pages of a table are a power of two long.)
 __device__ __forceinline__ int page_of(const RowsParams &p, int b, int t) {
     if (!p.page_table) return b;
-    const int e = p.page_table[static_cast<size_t>(b) * p.max_pages + t / p.page_size];
+    const int e = p.page_table[static_cast<size_t>(b) * p.max_pages + (t >> (31 - __clz(p.page_size)))];
     if (e < 0 || e >= p.num_pages) {
         atomicOr(p.err, kErrBadPage);
         return -1;

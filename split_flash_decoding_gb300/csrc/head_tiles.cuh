@@ -106,11 +106,9 @@ __device__ __forceinline__ void scale8(float2 (&y)[4], const uint4 &w, float f) 
 // Exponent of the scale of a block whose largest finite value is amax: the least e
 // with amax <= 448 * 2^e (448 = 0.875 * 2^9), clamped.
 __device__ __forceinline__ int scale_exponent(float amax) {
-    if (!(amax > 0.f)) return kMinExp;
-    int e;
-    const float m = frexpf(amax, &e);
-    e += m > 0.875f ? -8 : -9;
-    return min(max(e, kMinExp), kMaxExp);
+    const uint32_t bits = __float_as_uint(amax);
+    const int e = static_cast<int>(bits >> 23) - 127;            // (0 and subnormal: clamped)
+    return min(max(e - ((bits & 0x7fffffu) > 0x600000u ? 7 : 8), kMinExp), kMaxExp);
 }
 
 __device__ __forceinline__ float pow2i(int e) {   // -126 <= e <= 127
@@ -527,7 +525,7 @@ head_tiles_kernel(const __grid_constant__ RowsParams p, const __grid_constant__ 
         const int B = p.block_tokens, base = static_cast<int>(s_tile.first);   // row 0's token
         // earlier tokens of the first row's block, uniform over the CTA
         const int held = s_tile.first == s_tile.begin && base >= 0 && places[0].stored > 0
-                             ? base % B : 0;
+                             ? base & (B - 1) : 0;
         float ratio = 1.f;                                       // of a held block's row 0
         __syncthreads();                                         // the last heads' scales are used
         // (NaN never counts; infinities do not either, but cost a second look)
@@ -543,8 +541,9 @@ head_tiles_kernel(const __grid_constant__ RowsParams p, const __grid_constant__ 
         const int row = tid & ((1 << shift) - 1), h = hs + (tid >> shift);
         if (tid < kItems && row < n && h < h1 && h >= p.q.heads && places[row].stored > 0) {
             const int t = places[row].token;
-            const int first = max(t / B * B - base, max(-base, 0));
-            const int last = min(t / B * B + B, min(base + n, p.max_kv_len)) - base;
+            const int block0 = t & ~(B - 1);
+            const int first = max(block0 - base, max(-base, 0));
+            const int last = min(block0 + B, min(base + n, p.max_kv_len)) - base;
             if (row == first) {
                 float most = 0.f;
                 for (int i = first; i < last; ++i) most = fmaxf(most, row_max[(tid - row) + i]);
@@ -552,14 +551,15 @@ head_tiles_kernel(const __grid_constant__ RowsParams p, const __grid_constant__ 
                 const int head = h - p.q.heads - (is_k ? 0 : p.k.heads);
                 const CacheOut &c = is_k ? p.kc : p.vc;
                 float *where = c.scale + places[row].page * c.scale_page +
-                               (places[row].slot / B) * c.scale_block + head * c.scale_head;
+                               (places[row].slot >> p.block_shift) * c.scale_block +
+                               head * c.scale_head;
                 float scale = pow2i(scale_exponent(most));
                 if (row == 0 && held > 0) {
                     const float old = *where;
                     if (scale > old) ratio = old / scale; else scale = old;
                 }
                 *where = scale;
-                const float inv = 1.f / scale;
+                const float inv = __frcp_rn(scale);
                 for (int i = first; i < last; ++i) row_max[(tid - row) + i] = inv;
             }
         }
