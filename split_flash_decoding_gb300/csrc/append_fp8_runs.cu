@@ -26,13 +26,13 @@ namespace {
 constexpr int kT = 256, kL = 8, kS = 4;        // threads, lanes of a head, tokens of a thread
 constexpr int kMaxChunk = 32;                  // heads of a CTA
 
-struct SlotPlace {
-    long long k_at, v_at, ks_at, vs_at;        // offsets into the caches and their scales
-    int pos, stored;
+// Heads of a CTA and CTAs of a tile, keys and values apart; CTAs of all keys.
+struct RunCut {
+    int k_chunk, v_chunk, k_chunks, v_chunks, k_ctas;
 };
 
-// Shared memory: angles [128][4][8] {c, s, c, s} when there is a rotation, then
-// the vectors in flight [kS][2][kT].
+// Shared memory: angles [128][4][8] when there is a rotation, then the vectors in
+// flight [kS][2][kT].
 size_t run_smem(const RowsParams &p) {
     return (p.rope.rot_dim > 0 ? size_t(kGroupTokens) * 4 * kL * sizeof(float4) : 0) +
            size_t(kT) * 2 * kS * sizeof(uint4);
@@ -45,17 +45,20 @@ __device__ __forceinline__ void copy_16(void *dst, const void *src) {
 
 template <bool kInter>
 __global__ void __launch_bounds__(kT, 2)
-append_fp8_runs_kernel(const __grid_constant__ RowsParams p, int chunks, int chunk_heads) {
+append_fp8_runs_kernel(const __grid_constant__ RowsParams p, const __grid_constant__ RunCut cut) {
     extern __shared__ __align__(16) float4 angles[];
-    __shared__ SlotPlace places[kGroupTokens];
     __shared__ float s_old[kMaxChunk];         // scales of the block that holds earlier tokens
     __shared__ float s_part[2][kT / 32];       // maxima of 16 tokens
     __shared__ Tokens s_tile;
     __shared__ int s_any;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int tile = static_cast<int>(blockIdx.x) / chunks;
-    const int h0 = (static_cast<int>(blockIdx.x) - tile * chunks) * chunk_heads;
-    const int h1 = min(h0 + chunk_heads, p.k.heads + p.v.heads);
+    // keys' CTAs first: they take longer
+    const int x = static_cast<int>(blockIdx.x) - cut.k_ctas;
+    const bool is_k = x < 0;
+    const int chunks = is_k ? cut.k_chunks : cut.v_chunks;
+    const int y = is_k ? static_cast<int>(blockIdx.x) : x;
+    const int tile = y / chunks, chunk = is_k ? cut.k_chunk : cut.v_chunk;
+    const int h0 = (y - tile * chunks) * chunk, h1 = min(h0 + chunk, p.k.heads);
 
     if (warp == 0) {
         Tokens t;
@@ -68,94 +71,73 @@ append_fp8_runs_kernel(const __grid_constant__ RowsParams p, int chunks, int chu
     __syncthreads();
     if (!s_any || s_tile.first < 0) return;    // (a group of tokens below 0 is stored nowhere)
     const int first = static_cast<int>(s_tile.first), count = s_tile.count, r0 = s_tile.row;
-    const int group0 = first & ~(kGroupTokens - 1);
+    const int group0 = first & ~(kGroupTokens - 1), first_slot = first - group0;
     const int B = p.block_tokens;
 
     // ---- this thread's tokens and channels; the first head's loads -------------------
+    const HeadRows &in = is_k ? p.k : p.v;
+    const CacheOut &c = is_k ? p.kc : p.vc;
     const int item = tid / kL, i0 = tid & (kL - 1);
-    const int R = p.rope.rot_dim / 8, half = p.rope.rot_dim / 2;
+    const int R = p.rope.rot_dim / 8, half = is_k ? p.rope.rot_dim / 2 : 0;
     const int start = p.k.rot_start / 8;
     int va, vb;
     pair_of(kInter, 16, R, i0, va, vb);        // of 16 vectors no lane goes without
-    const bool turn_a = va < R, turn_b = vb < R;
+    const bool turn_a = half > 0 && va < R, turn_b = half > 0 && vb < R;
     const int ca = 8 * ordered(va, R, start), cb = 8 * ordered(vb, R, start);
-    const bool norm_a = ca < p.k.norm_dim, norm_b = cb < p.k.norm_dim;
+    const bool norm_a = ca < in.norm_dim, norm_b = cb < in.norm_dim;
     uint4 ga = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u), gb = ga;   // 1
-    if (p.k.norm && norm_a) ga = *reinterpret_cast<const uint4 *>(p.k.norm + ca);
-    if (p.k.norm && norm_b) gb = *reinterpret_cast<const uint4 *>(p.k.norm + cb);
-    uint4 *ahead = reinterpret_cast<uint4 *>(angles + (half > 0 ? kGroupTokens * 4 * kL : 0)) + tid;
-    const int row0 = 4 * item - (first - group0);                // row of its first token
-    const auto fetch = [&](int h) {
-        const bool is_k = h < p.k.heads;
-        const long long step = is_k ? p.k.in_row : p.v.in_row;
-        const uint16_t *src = (is_k ? p.k.in + h * p.k.in_head
-                                    : p.v.in + (h - p.k.heads) * p.v.in_head) + (r0 + row0) * step;
+    if (in.norm && norm_a) ga = *reinterpret_cast<const uint4 *>(in.norm + ca);
+    if (in.norm && norm_b) gb = *reinterpret_cast<const uint4 *>(in.norm + cb);
+    // Its four tokens lie in one page, side by side (pages have at least 8 slots); so
+    // do the tokens that the first block holds from before.
+    const int t0 = group0 + 4 * item, row0 = t0 - first;
+    int page = -1, slot0 = t0;
+    if (t0 + 3 >= (first & ~(B - 1)) && row0 < count && t0 < p.max_kv_len) {
+        page = page_of(p, s_tile.b, t0);
+        if (p.page_table) slot0 = t0 & (p.page_size - 1);
+    }
+    unsigned stored = 0;                       // new tokens, a bit each
 #pragma unroll
-        for (int s = 0; s < kS; ++s) {
-            if (row0 + s < 0 || row0 + s >= count) continue;
-            copy_16(ahead + 2 * s * kT, src + s * step + ca);
-            copy_16(ahead + (2 * s + 1) * kT, src + s * step + cb);
-        }
+    for (int s = 0; s < kS; ++s)
+        if (page >= 0 && row0 + s >= 0 && row0 + s < count && t0 + s < p.max_kv_len)
+            stored |= 1u << s;
+    uint4 *ahead = reinterpret_cast<uint4 *>(angles + (half > 0 ? kGroupTokens * 4 * kL : 0)) + tid;
+    const uint16_t *src = in.in + (r0 + row0) * in.in_row + h0 * in.in_head;
+    const auto fetch = [&]() {
+#pragma unroll
+        for (int s = 0; s < kS; ++s)
+            if (stored >> s & 1) {
+                copy_16(ahead + 2 * s * kT, src + s * in.in_row + ca);
+                copy_16(ahead + (2 * s + 1) * kT, src + s * in.in_row + cb);
+            }
     };
 #pragma unroll
     for (int s = 0; s < kS; ++s)
-        if (row0 + s < 0 || row0 + s >= count)                   // never fetched
+        if (!(stored >> s & 1))                // never fetched: 0, which no maximum sees
             ahead[2 * s * kT] = ahead[(2 * s + 1) * kT] = make_uint4(0u, 0u, 0u, 0u);
-    fetch(h0);
+    fetch();
 
-    // ---- places ----------------------------------------------------------------------
-    for (int i = tid; i < kGroupTokens; i += kT) {
-        SlotPlace at;
-        at.k_at = at.v_at = at.ks_at = at.vs_at = 0;
-        at.stored = 0;
-        const int t = group0 + i, row = t - first;
-        at.pos = t;
-        // (tokens that the first block holds from before have a place too)
-        if (t >= (first & ~(B - 1)) && row < count && t < p.max_kv_len) {
-            const int page = page_of(p, s_tile.b, t);
-            const int slot = p.page_table ? t & (p.page_size - 1) : t;
-            if (page >= 0) {
-                at.stored = 1;
-                at.k_at = page * p.kc.page_stride + slot * p.kc.token_stride;
-                at.v_at = page * p.vc.page_stride + slot * p.vc.token_stride;
-                at.ks_at = page * p.kc.scale_page + (slot >> p.block_shift) * p.kc.scale_block;
-                at.vs_at = page * p.vc.scale_page + (slot >> p.block_shift) * p.vc.scale_block;
-            }
-        }
-        if (p.positions && row >= 0 && row < count) at.pos = p.positions[r0 + row];
-        places[i] = at;
+    // ---- the first block's old scales; angles, one entry a thread ---------------------
+    int held = s_tile.first == s_tile.begin ? first & (B - 1) : 0;
+    if (held > 0) {
+        const int at = first < p.max_kv_len ? page_of(p, s_tile.b, first) : -1;
+        if (at < 0) held = 0;                  // the first token is not stored
+        const int slot = p.page_table ? first & (p.page_size - 1) : first;
+        if (held > 0 && tid < h1 - h0)
+            s_old[tid] = c.scale[at * c.scale_page + (slot >> p.block_shift) * c.scale_block +
+                                 (h0 + tid) * c.scale_head];
     }
-    __syncthreads();
-
-    // ---- the first block's old scales; angles, one entry (two pairs) a thread -------
-    const int first_slot = first - group0;
-    // (B is at most 128, and a first block without a place has no held tokens)
-    const int held = s_tile.first == s_tile.begin && places[first_slot].stored ? first & (B - 1) : 0;
-    if (held > 0 && tid < h1 - h0) {
-        const int h = h0 + tid;
-        const SlotPlace &at = places[first_slot];
-        s_old[tid] = h < p.k.heads ? p.kc.scale[at.ks_at + h * p.kc.scale_head]
-                                   : p.vc.scale[at.vs_at + (h - p.k.heads) * p.vc.scale_head];
-    }
-    if (half > 0 && h0 < p.k.heads) {
+    if (half > 0)
         for (int e = tid; e < kGroupTokens * 4 * kL; e += kT) {
-            const int slot = e / (4 * kL), k = e / kL & 3, i = e & (kL - 1);
-            if (slot < first_slot || slot >= first_slot + count) continue;
-            int a, b;
-            pair_of(kInter, 16, R, i, a, b);
-            const int j0 = kInter ? 4 * a + k : 8 * i + 2 * k;
-            const int j1 = kInter ? 4 * b + k : j0 + 1;
-            float4 v = make_float4(1.f, 0.f, 1.f, 0.f);
-            if (a < R) rope_cos_sin(p.rope, j0, places[slot].pos, v.x, v.y);
-            if (b < R) rope_cos_sin(p.rope, j1, places[slot].pos, v.z, v.w);
-            angles[e] = v;
+            const int row = e / (4 * kL) - first_slot;
+            if (row < 0 || row >= count) continue;
+            angles[e] = angle_entry<kInter>(p.rope, 16, e / kL & 3, e & (kL - 1),
+                                            p.positions ? p.positions[r0 + row] : first + row);
         }
-    }
     __syncthreads();
 
 #pragma unroll 1
     for (int h = h0; h < h1; ++h) {
-        const bool is_k = h < p.k.heads;
         float2 ya[kS][4], yb[kS][4];
         asm volatile("cp.async.wait_all;" ::: "memory");
 #pragma unroll
@@ -163,7 +145,7 @@ append_fp8_runs_kernel(const __grid_constant__ RowsParams p, int chunks, int chu
             unpack8(ahead[2 * s * kT], ya[s]);
             unpack8(ahead[(2 * s + 1) * kT], yb[s]);
         }
-        if (is_k && p.k.norm_dim > 0) {
+        if (in.norm_dim > 0) {
 #pragma unroll
             for (int s = 0; s < kS; ++s) {
                 float2 sq = make_float2(0.f, 0.f);
@@ -172,12 +154,12 @@ append_fp8_runs_kernel(const __grid_constant__ RowsParams p, int chunks, int chu
                 float sum = sq.x + sq.y;
 #pragma unroll
                 for (int o = 1; o < kL; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                const float inv = rsqrtf(fmaf(sum, p.k.mean, p.k.eps));
+                const float inv = rsqrtf(fmaf(sum, in.mean, in.eps));
                 if (norm_a) scale8(ya[s], ga, inv);
                 if (norm_b) scale8(yb[s], gb, inv);
             }
         }
-        if (is_k && turn_a) {
+        if (turn_a) {
 #pragma unroll
             for (int s = 0; s < kS; ++s) {
                 const float4 *t = angles + (4 * item + s) * 4 * kL + i0;
@@ -196,7 +178,6 @@ append_fp8_runs_kernel(const __grid_constant__ RowsParams p, int chunks, int chu
                 infinite |= 1u << s;
                 top[s] = largest_finite(ya[s], yb[s]);
             }
-            if (row0 + s < 0 || row0 + s >= count || !places[4 * item + s].stored) top[s] = 0.f;
         }
         if (B >= 4) {
             float m = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
@@ -225,15 +206,17 @@ append_fp8_runs_kernel(const __grid_constant__ RowsParams p, int chunks, int chu
             }
         }
         // This head's vectors have all been used: the next one's may take their place.
-        if (h + 1 < h1) fetch(h + 1);
+        src += in.in_head;
+        if (h + 1 < h1) fetch();
 
         // ---- scales and codes ------------------------------------------------------------
-        const CacheOut &c = is_k ? p.kc : p.vc;
-        const int head = is_k ? h : h - p.k.heads;
+        if (page < 0) continue;
+        uint8_t *dst = c.base + page * c.page_stride + slot0 * c.token_stride + h * c.head_stride;
+        float *scales = c.scale + page * c.scale_page + h * c.scale_head;
         float scale = 0.f, f = 0.f, ratio = 1.f;
 #pragma unroll
         for (int s = 0; s < kS; ++s) {
-            const int slot = 4 * item + s, row = row0 + s;
+            const int slot = 4 * item + s;
             if (s == 0 || B < 4) {                               // (four tokens share blocks of 4)
                 scale = pow2i(scale_exponent(top[s]));
                 ratio = 1.f;
@@ -243,22 +226,18 @@ append_fp8_runs_kernel(const __grid_constant__ RowsParams p, int chunks, int chu
                 }
                 f = __frcp_rn(scale);
             }
-            const SlotPlace &at = places[slot];
-            if (!at.stored) continue;
-            uint8_t *dst = c.base + (is_k ? at.k_at : at.v_at) + head * c.head_stride;
-            if (row < 0) {                                       // held from before
-                if (ratio != 1.f) {
-                    uint2 *wa = reinterpret_cast<uint2 *>(dst + ca);
-                    uint2 *wb = reinterpret_cast<uint2 *>(dst + cb);
-                    const uint2 oa = *wa, ob = *wb;
-                    *wa = make_uint2(recode4(oa.x, ratio), recode4(oa.y, ratio));
-                    *wb = make_uint2(recode4(ob.x, ratio), recode4(ob.y, ratio));
-                }
-                continue;
+            uint8_t *at = dst + s * c.token_stride;
+            if (stored >> s & 1) {
+                if (i0 == 0 && ((slot & (B - 1)) == 0 || slot == first_slot))
+                    scales[((slot0 + s) >> p.block_shift) * c.scale_block] = scale;
+                store_codes(at + ca, at + cb, ya[s], yb[s], f, infinite >> s & 1);
+            } else if (ratio != 1.f && slot < first_slot) {      // held from before
+                uint2 *wa = reinterpret_cast<uint2 *>(at + ca);
+                uint2 *wb = reinterpret_cast<uint2 *>(at + cb);
+                const uint2 oa = *wa, ob = *wb;
+                *wa = make_uint2(recode4(oa.x, ratio), recode4(oa.y, ratio));
+                *wb = make_uint2(recode4(ob.x, ratio), recode4(ob.y, ratio));
             }
-            if (i0 == 0 && ((slot & (B - 1)) == 0 || row == 0))
-                c.scale[(is_k ? at.ks_at : at.vs_at) + head * c.scale_head] = scale;
-            store_codes(dst + ca, dst + cb, ya[s], yb[s], f, infinite >> s & 1);
         }
     }
 }
@@ -266,30 +245,41 @@ append_fp8_runs_kernel(const __grid_constant__ RowsParams p, int chunks, int chu
 }  // namespace
 
 cudaError_t launch_fp8_runs(const RowsParams &p, cudaStream_t stream) {
-    // A tile's angles cost about as much as two heads; as many heads to a CTA as
-    // leave the waves full.
+    // In units of a values' head: a keys' head costs about two, the angles of a tile
+    // six, opening a tile one.  The cut with the least estimate is taken: the work of
+    // a resident CTA, and half of a CTA of the last ones.  (24768 rows of 8 + 8 heads,
+    // 8 keys' and 4 values' heads a CTA: 47.7 us; 8 and 2 47.8, 4 and 4 51.0, 4 and 8
+    // 57.7.)
     constexpr int kWave = 2 * 152;
-    const int heads = p.k.heads + p.v.heads;
     const long long likely = p.num_rows / kGroupTokens + p.batch;
-    int best = 1;
+    const int heads = p.k.heads;
+    const int angles = p.rope.rot_dim > 0 ? 6 : 0;
+    RunCut cut;
+    cut.k_chunk = cut.v_chunk = 1;
     long long least = 0;
-    for (int chunk = 1; chunk <= heads && chunk <= kMaxChunk; ++chunk) {
-        const long long ctas = likely * ((heads + chunk - 1) / chunk);
-        const long long cost = (ctas + kWave - 1) / kWave * (chunk + 2);
-        if (chunk == 1 || cost < least) {
-            least = cost;
-            best = chunk;
+    for (int ck = 1; ck <= heads && ck <= kMaxChunk; ++ck)
+        for (int cv = 1; cv <= heads && cv <= kMaxChunk; ++cv) {
+            const int nk = (heads + ck - 1) / ck, nv = (heads + cv - 1) / cv;
+            const long long work = likely * (nk * (1 + angles) + nv + 3 * heads) / kWave;
+            const long long most = max(1 + angles + 2 * ck, 1 + cv);
+            const long long cost = 2 * max(work, most) + 1 + cv;
+            if ((ck == 1 && cv == 1) || cost < least) {
+                least = cost;
+                cut.k_chunk = ck;
+                cut.v_chunk = cv;
+            }
         }
-    }
-    const int chunks = (heads + best - 1) / best;
-    const long long blocks = fp8_tile_count(p) * chunks;
+    cut.k_chunks = (heads + cut.k_chunk - 1) / cut.k_chunk;
+    cut.v_chunks = (heads + cut.v_chunk - 1) / cut.v_chunk;
+    const long long tiles = fp8_tile_count(p), blocks = tiles * (cut.k_chunks + cut.v_chunks);
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+    cut.k_ctas = static_cast<int>(tiles * cut.k_chunks);
     auto kern = p.rope.interleaved ? append_fp8_runs_kernel<true> : append_fp8_runs_kernel<false>;
     const size_t smem = run_smem(p);
     const cudaError_t e =
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
     if (e != cudaSuccess) return e;
-    kern<<<static_cast<unsigned>(blocks), kT, smem, stream>>>(p, chunks, best);
+    kern<<<static_cast<unsigned>(blocks), kT, smem, stream>>>(p, cut);
     return cudaGetLastError();
 }
 

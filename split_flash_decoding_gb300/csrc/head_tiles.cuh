@@ -203,6 +203,22 @@ __device__ __forceinline__ void rotate_pairs(float2 &ya, float2 &yb, const float
     }
 }
 
+// Entry k of lane i's angles {cos, sin, cos, sin}: half layout those of channels 2k
+// and 2k + 1 of its vectors, interleaved those of pair k of each vector.
+template <bool kInter>
+__device__ __forceinline__ float4 angle_entry(const RopeParams &rope, int vecs, int k, int i,
+                                              int pos) {
+    const int R = rope.rot_dim / 8;
+    int a, b;
+    pair_of(kInter, vecs, R, i, a, b);
+    const int j0 = kInter ? 4 * a + k : 8 * i + 2 * k;
+    const int j1 = kInter ? 4 * b + k : j0 + 1;
+    float4 v = make_float4(1.f, 0.f, 1.f, 0.f);
+    if (a >= 0 && a < R) rope_cos_sin(rope, j0, pos, v.x, v.y);
+    if (b >= 0 && b < R) rope_cos_sin(rope, j1, pos, v.z, v.w);
+    return v;
+}
+
 // Sequence of row r; -1: none.  (One thread a row; a warp's rows read the same lines.)
 __device__ __forceinline__ int sequence_of(const RowsParams &p, int r) {
     if (!p.q_row_offsets) return r;
@@ -366,7 +382,7 @@ template <int L, bool kInter, bool kFp8>
 __global__ void __launch_bounds__(kThreads, kFp8 ? 2 : 4)
 head_tiles_kernel(const __grid_constant__ RowsParams p, const __grid_constant__ Cut cut) {
     constexpr int kItems = kItemsOf<L>;
-    extern __shared__ __align__(16) float4 angles[];             // [rows][4][lanes] {c, s, c, s}
+    extern __shared__ __align__(16) float4 angles[];             // [rows][4][lanes]
     __shared__ Place places[kItems];
     __shared__ float row_max[kFp8 ? kItems : 1];                 // then 1 / scale
     __shared__ Tokens s_tile;
@@ -403,7 +419,7 @@ head_tiles_kernel(const __grid_constant__ RowsParams p, const __grid_constant__ 
     const int step_heads = kItems >> shift;                      // heads in work at once
     const int i0 = tid & (L - 1);
     const int item0 = tid / L;
-    const int R = p.rope.rot_dim / 8, half = p.rope.rot_dim / 2;
+    const int half = p.rope.rot_dim / 2;
     Item it;
     it.row = item0 & ((1 << shift) - 1);
     it.h = it.row < n ? h0 + (item0 >> shift) : h1;
@@ -463,17 +479,8 @@ head_tiles_kernel(const __grid_constant__ RowsParams p, const __grid_constant__ 
     const int q_vecs = p.q.heads > 0 ? p.q.dim / 8 : p.k.dim / 8;
     if (half > 0 && h0 < p.q.heads + p.k.heads) {
         for (int e = tid; e < n * 4 * L; e += kThreads) {
-            const int row = e / (4 * L), k = e / L & 3, i = e & (L - 1);
-            int a, b;
-            pair_of(kInter, q_vecs, R, i, a, b);
-            // half: channels 2k, 2k + 1 of the lane's vectors; interleaved: pair k of
-            // vector a and pair k of vector b
-            const int j0 = kInter ? 4 * a + k : 8 * i + 2 * k;
-            const int j1 = kInter ? 4 * b + k : j0 + 1;
-            float4 v = make_float4(1.f, 0.f, 1.f, 0.f);
-            if (a >= 0 && a < R) rope_cos_sin(p.rope, j0, places[row].pos, v.x, v.y);
-            if (b >= 0 && b < R) rope_cos_sin(p.rope, j1, places[row].pos, v.z, v.w);
-            angles[e] = v;
+            const int row = e / (4 * L);
+            angles[e] = angle_entry<kInter>(p.rope, q_vecs, e / L & 3, e & (L - 1), places[row].pos);
         }
     }
     __syncthreads();
