@@ -105,7 +105,7 @@ append_fp8_kernel(const __grid_constant__ RowsParams p) {
 
 cudaError_t launch_append_fp8(const RowsParams &p, cudaStream_t stream) {
     const bool small_blocks = p.block_tokens <= tiles::kGroupTokens;
-    if (small_blocks && fp8_tiles_take_queries(p)) return launch_fp8_tiles(p, stream);
+    if (small_blocks && fp8_tiles_take_queries(p)) return launch_fp8_tiles(p, false, stream);
     RowsParams kv = p;
     if (p.q.heads > 0) {
         RowsParams q = p;
@@ -114,7 +114,7 @@ cudaError_t launch_append_fp8(const RowsParams &p, cudaStream_t stream) {
         if (e != cudaSuccess) return e;
         kv.q.heads = 0;
     }
-    if (small_blocks && head_tiles_fit(kv)) return launch_fp8_tiles(kv, stream);
+    if (small_blocks && head_tiles_fit(kv)) return launch_fp8_tiles(kv, p.q.heads > 0, stream);
     append_fp8_kernel<<<dim3(p.num_rows, p.k.heads, 2), kThreads, 0, stream>>>(kv);
     return cudaGetLastError();
 }

@@ -69,7 +69,10 @@ append_fp8_runs_kernel(const __grid_constant__ RowsParams p, const __grid_consta
         }
     }
     __syncthreads();
-    if (!s_any || s_tile.first < 0) return;    // (a group of tokens below 0 is stored nowhere)
+    if (!s_any || s_tile.first < 0) {          // (a group of tokens below 0 is stored nowhere)
+        pdl_wait_primary();
+        return;
+    }
     const int first = static_cast<int>(s_tile.first), count = s_tile.count, r0 = s_tile.row;
     const int group0 = first & ~(kGroupTokens - 1), first_slot = first - group0;
     const int B = p.block_tokens;
@@ -240,11 +243,12 @@ append_fp8_runs_kernel(const __grid_constant__ RowsParams p, const __grid_consta
             }
         }
     }
+    pdl_wait_primary();
 }
 
 }  // namespace
 
-cudaError_t launch_fp8_runs(const RowsParams &p, cudaStream_t stream) {
+cudaError_t launch_fp8_runs(const RowsParams &p, bool behind_queries, cudaStream_t stream) {
     // In units of a values' head: a keys' head costs about two, the angles of a tile
     // six, opening a tile one.  The cut with the least estimate is taken: the work of
     // a resident CTA, and half of a CTA of the last ones.  (24768 rows of 8 + 8 heads,
@@ -279,8 +283,19 @@ cudaError_t launch_fp8_runs(const RowsParams &p, cudaStream_t stream) {
     const cudaError_t e =
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
     if (e != cudaSuccess) return e;
-    kern<<<static_cast<unsigned>(blocks), kT, smem, stream>>>(p, cut);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+    cfg.blockDim = dim3(kT);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    // Behind the queries' launch, which it does not depend on: CTAs start as that
+    // one's last ones leave, and wait for its end before they leave themselves.
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = behind_queries ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kern, p, cut);
 }
 
 }  // namespace attn

@@ -93,8 +93,9 @@ cudaError_t launch_head_tiles(const RowsParams &p, cudaStream_t stream);
 // The same into a cache held in 8 bits: blocks of up to 128 tokens, and q only
 // where fp8_tiles_take_queries.
 bool fp8_tiles_take_queries(const RowsParams &p);
-cudaError_t launch_fp8_tiles(const RowsParams &p, cudaStream_t stream);
-cudaError_t launch_fp8_runs(const RowsParams &p, cudaStream_t stream);   // keys and values alone
+cudaError_t launch_fp8_tiles(const RowsParams &p, bool behind_queries, cudaStream_t stream);
+// Keys and values alone; behind_queries: the launch before it wrote their queries.
+cudaError_t launch_fp8_runs(const RowsParams &p, bool behind_queries, cudaStream_t stream);
 // CTAs of the 8-bit decode grid on num_sms SMs.
 int fp8_decode_ctas(int num_sms);
 cudaError_t launch_gqa_decode_fp8(const Fp8DecodeParams &p, int ctas, cudaStream_t stream);

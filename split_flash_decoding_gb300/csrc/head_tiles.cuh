@@ -388,6 +388,7 @@ head_tiles_kernel(const __grid_constant__ RowsParams p, const __grid_constant__ 
     __shared__ Tokens s_tile;
     __shared__ int s_any;
     const int tid = threadIdx.x, lane = tid & 31;
+    if (!kFp8) pdl_launch_dependents();        // (the keys and values of an 8-bit append)
     const int tile = static_cast<int>(blockIdx.x) / cut.chunks;
     const int chunk = static_cast<int>(blockIdx.x) - tile * cut.chunks;
     const int h0 = chunk * cut.chunk_heads, h1 = min(h0 + cut.chunk_heads, cut.heads);

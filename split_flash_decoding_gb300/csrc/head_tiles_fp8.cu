@@ -16,9 +16,9 @@ bool fp8_tiles_take_queries(const RowsParams &p) {
     return p.q.dim <= 128 && longest_run(p) <= kItemsOf<8> && head_tiles_fit(p);
 }
 
-cudaError_t launch_fp8_tiles(const RowsParams &p, cudaStream_t stream) {
+cudaError_t launch_fp8_tiles(const RowsParams &p, bool behind_queries, cudaStream_t stream) {
     const int longest = longest_run(p);
-    if (longest > kItemsOf<8>) return launch_fp8_runs(p, stream);
+    if (longest > kItemsOf<8>) return launch_fp8_runs(p, behind_queries, stream);
     Cut cut;
     cut.heads = p.q.heads + p.k.heads + p.v.heads;
     cut.any_norm = (p.q.heads > 0 && p.q.norm_dim > 0) || p.k.norm_dim > 0;
