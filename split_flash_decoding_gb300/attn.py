@@ -12,6 +12,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+import struct
 from typing import Optional
 
 import torch
@@ -130,21 +131,21 @@ _SIGNATURES = {
                             _c.c_int, _c.c_void_p, _c.c_void_p, _c.c_void_p],
     "attn_rope_turns": [_c.c_int, _c.c_double, _c.c_int, _c.c_double, _c.c_double, _c.c_double,
                         _c.c_double, _c.c_void_p, _c.POINTER(_c.c_float)],
-    "attn_qk_norm_rope": [_c.POINTER(attn_head_rows_t), _c.POINTER(attn_head_rows_t),
-                          _c.POINTER(attn_rope_t), _c.c_void_p, _c.c_int, _c.c_void_p],
-    "attn_append_kv": [_c.POINTER(attn_head_rows_t), _c.POINTER(attn_head_rows_t),
-                       _c.POINTER(attn_head_rows_t), _c.POINTER(attn_rope_t), _c.c_void_p,
-                       _c.POINTER(attn_kv_t), _c.POINTER(attn_kv_t), _c.c_void_p, _c.c_void_p,
+    "attn_qk_norm_rope": [_c.c_void_p, _c.c_void_p,
+                          _c.c_void_p, _c.c_void_p, _c.c_int, _c.c_void_p],
+    "attn_append_kv": [_c.c_void_p, _c.c_void_p,
+                       _c.c_void_p, _c.c_void_p, _c.c_void_p,
+                       _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_void_p,
                        _c.c_int, _c.c_int, _c.c_int, _c.c_void_p],
-    "attn_append_kv_fp8": [_c.POINTER(attn_head_rows_t), _c.POINTER(attn_head_rows_t),
-                           _c.POINTER(attn_head_rows_t), _c.POINTER(attn_rope_t), _c.c_void_p,
-                           _c.POINTER(attn_kv_t), _c.POINTER(attn_kv_t),
-                           _c.POINTER(attn_kv_scale_t), _c.POINTER(attn_kv_scale_t), _c.c_void_p,
+    "attn_append_kv_fp8": [_c.c_void_p, _c.c_void_p,
+                           _c.c_void_p, _c.c_void_p, _c.c_void_p,
+                           _c.c_void_p, _c.c_void_p,
+                           _c.c_void_p, _c.c_void_p, _c.c_void_p,
                            _c.c_void_p, _c.c_int, _c.c_int, _c.c_int, _c.c_int, _c.c_void_p],
     "attn_decode_fp8_workspace": [_c.c_int, _c.c_int, _c.c_int, _c.c_int,
                                   _c.POINTER(_c.c_size_t)],
-    "attn_decode_fp8": [_c.c_void_p, _c.POINTER(attn_kv_t), _c.POINTER(attn_kv_t),
-                        _c.POINTER(attn_kv_scale_t), _c.POINTER(attn_kv_scale_t), _c.c_void_p,
+    "attn_decode_fp8": [_c.c_void_p, _c.c_void_p, _c.c_void_p,
+                        _c.c_void_p, _c.c_void_p, _c.c_void_p,
                         _c.c_void_p, _c.c_int, _c.c_int, _c.c_int, _c.c_int, _c.c_int, _c.c_int,
                         _c.c_int, _c.c_float, _c.c_void_p, _c.c_int, _c.c_void_p, _c.c_size_t,
                         _c.c_void_p, _c.c_void_p, _c.c_void_p],
@@ -184,9 +185,15 @@ def _stream_handle(stream) -> Optional[int]:
     return stream.cuda_stream
 
 
-# The entry points that fill a cache are called once a layer and step with little
-# work each, so their host side is kept short: descriptors are built in one
-# call, the stream is asked for by its device.
+# The entry points that fill a cache, and attention over one held in 8 bits, are
+# called once a layer and step with little work each, so their host side is kept
+# short: descriptors are packed (0.1 us each; a ctypes structure takes 0.6), shapes
+# and strides are asked for once, the stream by its device. 
+_pack_head_rows = struct.Struct("@PqqPqqPfiiiii").pack      # attn_head_rows_t
+_pack_kv = struct.Struct("@PqqqiiPii").pack                 # attn_kv_t
+_pack_kv_scale = struct.Struct("@Pqqqii").pack              # attn_kv_scale_t
+
+
 def _stream_of(stream, device: int) -> int:
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(device)
@@ -206,54 +213,60 @@ def kv_descriptor(cache: torch.Tensor, page_table: Optional[torch.Tensor] = None
     num_kv_heads, dim] and page_table None.  The last dimension must be
     contiguous; other strides are taken from the tensor.
     """
+    return attn_kv_t(*_kv_fields(cache, page_table, dtype))
+
+
+def _kv_fields(cache, page_table, dtype):
     if cache.dtype != dtype:
         raise TypeError("cache must be bf16" if dtype == torch.bfloat16 else
                         f"cache must be {dtype}")
-    if cache.dim() != 4 or cache.stride(3) != 1:
+    strides = cache.stride()
+    if len(strides) != 4 or strides[3] != 1:
         raise ValueError("cache must be 4-D with contiguous channels")
     pages, page_size, _, _ = cache.shape
-    page_stride, token_stride, head_stride, _ = cache.stride()
     if page_table is None:
-        return attn_kv_t(cache.data_ptr(), page_stride, token_stride, head_stride, page_size,
-                         pages, None, 0, 0)
+        return (cache.data_ptr(), *strides[:3], page_size, pages, 0, 0, 0)
     if page_table.dtype != torch.int32 or page_table.dim() != 2 or not page_table.is_contiguous():
         raise ValueError("page_table must be a contiguous int32 [batch, max_pages] tensor")
-    return attn_kv_t(cache.data_ptr(), page_stride, token_stride, head_stride, page_size, pages,
-                     page_table.data_ptr(), page_table.shape[1], 0)
+    return (cache.data_ptr(), *strides[:3], page_size, pages, page_table.data_ptr(),
+            page_table.shape[1], 0)
 
 
 def scale_descriptor(scale: torch.Tensor, cache: torch.Tensor) -> attn_kv_scale_t:
     """Describe the scales of an 8-bit cache [pages, page_size, heads, dim]:
     fp32 [pages, page_size / block_tokens, heads]; strides are taken from the
     tensor."""
-    if scale.dtype != torch.float32 or scale.dim() != 3:
+    return attn_kv_scale_t(*_scale_fields(scale, cache.shape))
+
+
+def _scale_fields(scale, cache_shape):
+    strides = scale.stride()
+    if scale.dtype != torch.float32 or len(strides) != 3:
         raise ValueError("scales must be an fp32 [pages, blocks, heads] tensor")
-    pages, page_size, heads, _ = cache.shape
     blocks = scale.shape[1]
-    if scale.shape != (pages, blocks, heads) or blocks == 0 or page_size % blocks:
-        raise ValueError(f"scales {tuple(scale.shape)} do not fit a cache {tuple(cache.shape)}")
-    return attn_kv_scale_t(scale.data_ptr(), *scale.stride(), page_size // blocks, 0)
+    if (scale.shape != (cache_shape[0], blocks, cache_shape[2]) or blocks == 0 or
+            cache_shape[1] % blocks):
+        raise ValueError(f"scales {tuple(scale.shape)} do not fit a cache {tuple(cache_shape)}")
+    return (scale.data_ptr(), *strides, cache_shape[1] // blocks, 0)
 
 
 # K and V usually have one layout: the second descriptor then is the first with
 # another address.
 
 def _kv_pair(k_cache, v_cache, page_table, dtype):
-    k = kv_descriptor(k_cache, page_table, dtype)
+    k = _kv_fields(k_cache, page_table, dtype)
     if (v_cache.shape == k_cache.shape and v_cache.stride() == k_cache.stride() and
             v_cache.dtype == dtype):
-        return k, attn_kv_t(v_cache.data_ptr(), k.page_stride, k.token_stride, k.head_stride,
-                            k.page_size, k.num_pages, k.page_table, k.max_pages, 0)
-    return k, kv_descriptor(v_cache, page_table, dtype)
+        return _pack_kv(*k), _pack_kv(v_cache.data_ptr(), *k[1:])
+    return _pack_kv(*k), _pack_kv(*_kv_fields(v_cache, page_table, dtype))
 
 
-def _scale_pair(k_scale, v_scale, k_cache, v_cache):
-    k = scale_descriptor(k_scale, k_cache)
-    if (v_scale.shape == k_scale.shape and v_scale.stride() == k_scale.stride() and
-            v_scale.dtype == torch.float32 and v_cache.shape == k_cache.shape):
-        return k, attn_kv_scale_t(v_scale.data_ptr(), k.page_stride, k.block_stride, k.head_stride,
-                                  k.block_tokens, 0)
-    return k, scale_descriptor(v_scale, v_cache)
+def _scale_pair(k_scale, v_scale, k_shape, v_shape):
+    k = _scale_fields(k_scale, k_shape)
+    if (v_shape == k_shape and v_scale.shape == k_scale.shape and
+            v_scale.stride() == k_scale.stride() and v_scale.dtype == torch.float32):
+        return _pack_kv_scale(*k), _pack_kv_scale(v_scale.data_ptr(), *k[1:])
+    return _pack_kv_scale(*k), _pack_kv_scale(*_scale_fields(v_scale, v_shape))
 
 
 class Rope:
@@ -296,29 +309,27 @@ def rope_turns(rot_dim: int, theta: float, *, scaling: str = "plain", factor: fl
     return turns if device is None else turns.to(device), mscale.value
 
 
-def _head_rows(x: torch.Tensor, out: Optional[torch.Tensor], norm: Optional[torch.Tensor],
-               eps: float, rot_start: int) -> attn_head_rows_t:
+def _head_rows(x: torch.Tensor, shape, out: Optional[torch.Tensor], norm: Optional[torch.Tensor],
+               eps: float, rot_start: int) -> bytes:
+    """x (of this shape) as packed attn_head_rows_t."""
     if x.dtype != torch.bfloat16:
         raise TypeError("head rows must be bf16")
-    if x.dim() != 3:
+    strides = x.stride()
+    if len(strides) != 3 or (strides[2] != 1 and shape[2] != 1):
         raise ValueError("head rows must be [rows, heads, dim] with contiguous channels")
-    row, head, channel = x.stride()
-    _, heads, dim = x.shape
-    if channel != 1 and dim != 1:
-        raise ValueError("head rows must be [rows, heads, dim] with contiguous channels")
-    dst, out_row, out_head = None, 0, 0
+    dst = out_row = out_head = 0
     if out is not None:
         out_row, out_head, channel = out.stride()
-        if out.dtype != torch.bfloat16 or out.shape != x.shape or channel != 1:
+        if out.dtype != torch.bfloat16 or out.shape != shape or channel != 1:
             raise ValueError("out must be bf16, shaped as the input, with contiguous channels")
         dst = out.data_ptr()
-    weight, norm_dim = None, 0
+    weight = norm_dim = 0
     if norm is not None:
         if norm.dtype != torch.bfloat16 or norm.dim() != 1 or not norm.is_contiguous():
             raise ValueError("norm weights must be contiguous bf16 [norm_dim]")
         weight, norm_dim = norm.data_ptr(), norm.shape[0]
-    return attn_head_rows_t(x.data_ptr(), row, head, dst, out_row, out_head, weight, eps,
-                            norm_dim, heads, dim, rot_start, 0)
+    return _pack_head_rows(x.data_ptr(), strides[0], strides[1], dst, out_row, out_head, weight, eps,
+                           norm_dim, shape[1], shape[2], rot_start, 0)
 
 
 def _int32(t: Optional[torch.Tensor], n: int, what: str):
@@ -559,8 +570,8 @@ def attn_qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor] = None,
     if k_out is None and k is not None:
         k_out = torch.empty(k.shape, dtype=torch.bfloat16, device=k.device)
     start = 0 if rope is None else rope.start
-    qd = _head_rows(q, q_out, q_norm, eps, start)
-    kd = None if k is None else _head_rows(k, k_out, k_norm, eps, start)
+    qd = _head_rows(q, q.shape, q_out, q_norm, eps, start)
+    kd = None if k is None else _head_rows(k, k.shape, k_out, k_norm, eps, start)
     pos = _int32(positions, rows, "positions")
     device = _on_current_device(q, k, q_out, k_out, positions, q_norm, k_norm,
                                 None if rope is None else rope.turns)
@@ -572,33 +583,33 @@ def attn_qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor] = None,
 
 def _append_args(k, v, k_cache, v_cache, kv_len, page_table, q, q_out, q_row_offsets, rope,
                  positions, q_norm, k_norm, eps, dtype, *scales):
-    rows, batch = k.shape[0], kv_len.shape[0]
+    k_shape, kc_shape, batch = k.shape, k_cache.shape, kv_len.shape[0]
+    rows = k_shape[0]
     if (v is None) != (v_cache is None):
         raise ValueError("v and v_cache go together")
-    if k.shape[1:] != k_cache.shape[2:]:
-        raise ValueError(f"rows {tuple(k.shape)} do not fit a cache {tuple(k_cache.shape)}")
+    if k_shape[1:] != kc_shape[2:]:
+        raise ValueError(f"rows {tuple(k_shape)} do not fit a cache {tuple(kc_shape)}")
     if page_table is not None and page_table.shape[0] != batch:
         raise ValueError("page_table must have one row per sequence")
     start, rope_ref = (0, None) if rope is None else (rope.start, rope.ref)
     qd = vd = vc = None
     if q is not None:
-        if q.shape[0] != rows:
+        q_shape = q.shape
+        if q_shape[0] != rows:
             raise ValueError("q, k and v must have the same rows")
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-        qd = _head_rows(q, q_out, q_norm, eps, start)
-    kd = _head_rows(k, None, k_norm, eps, start)
+            q_out = torch.empty(q_shape, dtype=torch.bfloat16, device=q.device)
+        qd = _head_rows(q, q_shape, q_out, q_norm, eps, start)
+    kd = _head_rows(k, k_shape, None, k_norm, eps, start)
     if v is None:
-        kc = kv_descriptor(k_cache, page_table, dtype)
+        kc = _pack_kv(*_kv_fields(k_cache, page_table, dtype))
     else:
-        if v.shape[0] != rows or v.shape[1:] != v_cache.shape[2:]:
-            raise ValueError(f"rows {tuple(v.shape)} do not fit {rows} rows and a cache "
+        v_shape = v.shape
+        if (v_shape != k_shape or v_cache.shape != kc_shape) and (
+                v_shape[0] != rows or v_shape[1:] != v_cache.shape[2:]):
+            raise ValueError(f"rows {tuple(v_shape)} do not fit {rows} rows and a cache "
                              f"{tuple(v_cache.shape)}")
-        if v.shape == k.shape and v.stride() == k.stride() and v.dtype == torch.bfloat16:
-            vd = attn_head_rows_t(v.data_ptr(), kd.in_row_stride, kd.in_head_stride, None, 0, 0,
-                                  None, 0.0, 0, kd.num_heads, kd.dim, 0, 0)
-        else:
-            vd = _head_rows(v, None, None, eps, 0)
+        vd = _head_rows(v, v_shape, None, None, eps, 0)
         kc, vc = _kv_pair(k_cache, v_cache, page_table, dtype)
     head = (qd, kd, vd, rope_ref, _int32(positions, rows, "positions"), kc, vc)
     tail = (_int32(kv_len, batch, "kv_len"), _int32(q_row_offsets, batch + 1, "q_row_offsets"),
@@ -648,7 +659,8 @@ def attn_append_kv_fp8(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
                                              q_row_offsets, rope, positions, q_norm, k_norm, eps,
                                              torch.float8_e4m3fn, k_scale, v_scale)
     _check("attn_append_kv_fp8",
-           lib().attn_append_kv_fp8(*head, *_scale_pair(k_scale, v_scale, k_cache, v_cache), *tail,
+           lib().attn_append_kv_fp8(*head, *_scale_pair(k_scale, v_scale, k_cache.shape,
+                                                       v_cache.shape), *tail,
                                     max_q_len, max_kv_len, _stream_of(stream, device)))
     return q_out
 
@@ -682,12 +694,13 @@ def attn_decode_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     rows, hq, d = q.shape
     batch = kv_len.shape[0]
     kd, vd = _kv_pair(k_cache, v_cache, page_table, torch.float8_e4m3fn)
-    ks, vs = _scale_pair(k_scale, v_scale, k_cache, v_cache)
+    k_shape, v_shape = k_cache.shape, v_cache.shape
+    ks, vs = _scale_pair(k_scale, v_scale, k_shape, v_shape)
     if q.dtype != torch.bfloat16 or not q.is_contiguous():
         raise ValueError("q must be contiguous bf16 [rows, num_q_heads, 128]")
-    if k_cache.shape[2:] != v_cache.shape[2:] or k_cache.shape[2] * group != hq:
+    if k_shape[2:] != v_shape[2:] or k_shape[2] * group != hq:
         raise ValueError(f"{hq} query heads in groups of {group} do not fit caches "
-                         f"{tuple(k_cache.shape)} and {tuple(v_cache.shape)}")
+                         f"{tuple(k_shape)} and {tuple(v_shape)}")
     if page_table is not None and page_table.shape[0] != batch:
         raise ValueError("page_table must have one row per sequence")
     lens = _int32(kv_len, batch, "kv_len")

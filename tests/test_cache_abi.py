@@ -314,3 +314,14 @@ def test_binding_refuses_wrong_tensors(attn):
     with pytest.raises(TypeError):
         attn.attn_decode_fp8(x, cache, cache, s, s, lens, group=1, scale=1.0, max_kv_len=64,
                              page_table=table, workspace=torch.zeros(8, dtype=torch.uint8))
+
+
+def test_packed_descriptors_are_the_structures(attn):
+    """The binding packs descriptors; their bytes are those of the C structures."""
+    n = [0x1111111111111000 + 16 * i for i in range(8)]
+    pairs = [(attn._pack_head_rows, attn.attn_head_rows_t,
+              (n[0], -8, 16, n[1], 24, 32, n[2], 0.5, 64, 5, 128, 8, 0)),
+             (attn._pack_kv, attn.attn_kv_t, (n[0], n[1], 16, 32, 64, 7, n[2], 9, 0)),
+             (attn._pack_kv_scale, attn.attn_kv_scale_t, (n[0], n[1], 2, 3, 16, 0))]
+    for pack, struct, fields in pairs:
+        assert pack(*fields) == bytes(struct(*fields))
