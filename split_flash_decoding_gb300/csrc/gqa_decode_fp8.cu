@@ -163,15 +163,33 @@ __device__ __forceinline__ void tmem_st_cols(uint32_t taddr, const float (&v)[N]
     }
 }
 
-// The three terms of one O column, four columns apart.
-__device__ __forceinline__ void tmem_ld_terms(uint32_t taddr, float &a, float &b, float &c) {
+// The three terms of two O columns side by side, four columns apart.
+__device__ __forceinline__ void tmem_ld_terms(uint32_t taddr, float (&a)[2], float (&b)[2],
+                                              float (&c)[2]) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%3];\n\t"
-        "tcgen05.ld.sync.aligned.32x32b.x1.b32 {%1}, [%4];\n\t"
-        "tcgen05.ld.sync.aligned.32x32b.x1.b32 {%2}, [%5];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0, %1}, [%6];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x2.b32 {%2, %3}, [%7];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x2.b32 {%4, %5}, [%8];\n\t"
         "tcgen05.wait::ld.sync.aligned;"
-        : "=&f"(a), "=&f"(b), "=&f"(c)
+        : "=&f"(a[0]), "=&f"(a[1]), "=&f"(b[0]), "=&f"(b[1]), "=&f"(c[0]), "=&f"(c[1])
         : "r"(taddr), "r"(taddr + 4), "r"(taddr + 8)
+        : "memory");
+}
+
+// Eight columns at each of the thread's chunks, one wait for all.
+__device__ __forceinline__ void tmem_ld_scores(uint32_t t0, uint32_t, float (&v)[1][8]) {
+    tc::tmem_ld_n<8>(t0, v[0]);
+}
+__device__ __forceinline__ void tmem_ld_scores(uint32_t t0, uint32_t t1, float (&v)[2][8]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%16];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%8, %9, %10, %11, %12, %13, %14, %15}, [%17];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=&f"(v[0][0]), "=&f"(v[0][1]), "=&f"(v[0][2]), "=&f"(v[0][3]), "=&f"(v[0][4]),
+          "=&f"(v[0][5]), "=&f"(v[0][6]), "=&f"(v[0][7]), "=&f"(v[1][0]), "=&f"(v[1][1]),
+          "=&f"(v[1][2]), "=&f"(v[1][3]), "=&f"(v[1][4]), "=&f"(v[1][5]), "=&f"(v[1][6]),
+          "=&f"(v[1][7])
+        : "r"(t0), "r"(t1)
         : "memory");
 }
 
@@ -200,13 +218,9 @@ __device__ __forceinline__ float pow2i(int e) {   // -126 <= e <= 127
     return __uint_as_float(uint32_t(e + 127) << 23);
 }
 
-// Two values to e4m3 (a in the low byte) and back.
+// Two values to e4m3 (a in the low byte).
 __device__ __forceinline__ uint32_t to_e4m3x2(float a, float b) {
     return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-}
-__device__ __forceinline__ float2 from_e4m3x2(uint32_t c) {
-    return __half22float2(__half2(
-        __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(c), __NV_E4M3)));
 }
 // 16 times what two codes leave of (a, b), given 16 a and 16 b: exact products in
 // a mixed-precision FMA, no unpacking.
@@ -319,6 +333,10 @@ __device__ __forceinline__ void cp_async_4(void *dst, const float *src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(dst)), "l"(src)
                  : "memory");
 }
+__device__ __forceinline__ void cp_async_16(void *dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src)
+                 : "memory");
+}
 // Arrive (without raising the pending count) when this thread's copies so far are done.
 __device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar))
@@ -332,6 +350,7 @@ __device__ __forceinline__ void feed(const Fp8DecodeParams &p, const int2 *cum, 
                                      uint8_t *smem, uint64_t *bar, int lane) {
     using C = Cfg<NC>;
     const int G = p.group;
+    const int g_inv = (1 << 16) / G + 1;            // (c * g_inv) >> 16 = c / G for c < 16
     const int box_shift = 31 - __clz(p.box_rows);   // a power of two
     const int nb_shift = 7 - box_shift;             // boxes per tile
     int g = 0, itq = 0;
@@ -349,44 +368,60 @@ __device__ __forceinline__ void feed(const Fp8DecodeParams &p, const int2 *cum, 
         uint8_t *qs = smem + C::q + qb * C::NS * 128;
         float *qf = reinterpret_cast<float *>(smem + C::qf) + qb * 16;
         const int cols = min(min(nrows, p.num_q_rows - row0) * G, NC);
-        constexpr int kBatch = NC < 8 ? NC : 8;   // columns whose loads are in flight together
+        // Four columns at a time, 16 channels a lane.  The bf16 rows are first copied
+        // to where their own terms go; both loops are rolled, as they run from a
+        // cold instruction cache (8 columns unrolled: 13000 cycles for 16 columns).
+        const int cq = lane >> 3, li = lane & 7;
 #pragma unroll 1
-        for (int c0 = 0; c0 < cols; c0 += kBatch) {
-            uint2 raw[kBatch];
+        for (int c = cq; c < cols; c += 4) {
+            const int i = (c * g_inv) >> 16, h = c - i * G;
+            const uint16_t *src =
+                p.q + (size_t(row0 + i) * p.num_q_heads + it.kvh * G + h) * kD + 16 * li;
+            uint8_t *dst = qs + (2 * (c - cq) + cq + (li & 4)) * 128 + (li & 3) * 32;
+            cp_async_16(dst, src);
+            cp_async_16(dst + 16, src + 8);
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncwarp();
+#pragma unroll 1
+        for (int c0 = 0; c0 < cols; c0 += 4) {
+            const int c = c0 + cq, r = 2 * c0 + cq;              // rows r and r + 4: its terms
+            const uint4 *raw =
+                reinterpret_cast<const uint4 *>(qs + (r + (li & 4)) * 128 + (li & 3) * 32);
+            const uint4 u = raw[0], v = raw[1];
+            float2 x[8] = {bf16x2_to_float2(u.x), bf16x2_to_float2(u.y), bf16x2_to_float2(u.z),
+                           bf16x2_to_float2(u.w), bf16x2_to_float2(v.x), bf16x2_to_float2(v.y),
+                           bf16x2_to_float2(v.z), bf16x2_to_float2(v.w)};
+            float top = 0.f;
 #pragma unroll
-            for (int u = 0; u < kBatch; ++u) {
-                const int c = min(c0 + u, cols - 1);
-                const int i = c / G, h = c - i * G;
-                raw[u] = *reinterpret_cast<const uint2 *>(
-                    p.q + (size_t(row0 + i) * p.num_q_heads + it.kvh * G + h) * kD + 4 * lane);
+            for (int k = 0; k < 8; ++k) top = fmax3(top, fabsf(x[k].x), fabsf(x[k].y));
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            // 2^a * top in [128, 256) (a clamped where the factor would leave fp32)
+            const int e = int(__float_as_uint(top) >> 23) - 127;
+            const int a = min(max(7 - e, -120), 120);
+            const float f = pow2i(a);
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                x[k] = __fmul2_rn(x[k], make_float2(f, f));
+                // an infinite channel has no e4m3 code: it becomes NaN
+                if (!(fabsf(x[k].x) < INFINITY)) x[k].x = __uint_as_float(0x7fffffffu);
+                if (!(fabsf(x[k].y) < INFINITY)) x[k].y = __uint_as_float(0x7fffffffu);
+                const uint32_t h = to_e4m3x2(x[k].x, x[k].y);
+                x[k] = __fmul2_rn(x[k], make_float2(16.f, 16.f));
+                rest16(h, x[k].x, x[k].y);
+                const uint32_t l = to_e4m3x2(x[k].x, x[k].y);
+                hi[k >> 1] = k & 1 ? hi[k >> 1] | (h << 16) : h;
+                lo[k >> 1] = k & 1 ? lo[k >> 1] | (l << 16) : l;
             }
-#pragma unroll
-            for (int u = 0; u < kBatch; ++u) {
-                const int c = c0 + u;
-                if (c >= cols) break;
-                float x[4] = {bf16_lo(raw[u].x), bf16_hi(raw[u].x), bf16_lo(raw[u].y),
-                              bf16_hi(raw[u].y)};
-                const float top = warp_max_redux(
-                    fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3]))));
-                // 2^a * top in [128, 256) (a clamped where the factor would leave fp32)
-                const int e = int(__float_as_uint(top) >> 23) - 127;
-                const int a = min(max(7 - e, -120), 120);
-                const float f = pow2i(a);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    x[k] *= f;
-                    // an infinite channel has no e4m3 code: it becomes NaN
-                    if (!(fabsf(x[k]) < INFINITY)) x[k] = __uint_as_float(0x7fffffffu);
-                }
-                const uint32_t h0 = to_e4m3x2(x[0], x[1]), h1 = to_e4m3x2(x[2], x[3]);
-                const float2 b0 = from_e4m3x2(h0), b1 = from_e4m3x2(h1);
-                const uint32_t l0 = to_e4m3x2((x[0] - b0.x) * 16.f, (x[1] - b0.y) * 16.f);
-                const uint32_t l1 = to_e4m3x2((x[2] - b1.x) * 16.f, (x[3] - b1.y) * 16.f);
-                const int r = (c >> 2) * 8 + (c & 3);
-                *reinterpret_cast<uint32_t *>(qs + operand_offset(r, 4 * lane)) = h0 | (h1 << 16);
-                *reinterpret_cast<uint32_t *>(qs + operand_offset(r + 4, 4 * lane)) =
-                    l0 | (l1 << 16);
-                if (lane == 0) qf[c] = pow2i(-a);
+            __syncwarp();                                        // the four rows are read
+            if (c < cols) {
+                *reinterpret_cast<uint4 *>(qs + operand_offset(r, 16 * li)) =
+                    make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                *reinterpret_cast<uint4 *>(qs + operand_offset(r + 4, 16 * li)) =
+                    make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                if (li == 0) qf[c] = pow2i(-a);
             }
         }
         tc::fence_async_smem();
@@ -610,17 +645,16 @@ gqa_decode_fp8_kernel(const __grid_constant__ Fp8DecodeParams p) {
                 if (!s_in) ok = ok && mbar_wait(&bar[kSFull + sb], (gg >> 1) & 1, p.err);
                 tc::fence_after_sync();
                 float2 s[NCH][2];                                // score, then score - m
+                float raw[NCH][8];
+                const uint32_t s_at = tmem + lane_base + sb * C::NS;
+                tmem_ld_scores(s_at + 2 * col(0), s_at + 2 * col(NCH - 1), raw);
 #pragma unroll
-                for (int h = 0; h < NCH; ++h) {
-                    if (col(h) >= cols) continue;
-                    float raw[8];
-                    tc::tmem_ld_n<8>(tmem + lane_base + sb * C::NS + 2 * col(h), raw);
+                for (int h = 0; h < NCH; ++h)
 #pragma unroll
                     for (int c = 0; c < 2; ++c)
-                        s[h][c] = __ffma2_rn(make_float2(raw[4 + 2 * c], raw[5 + 2 * c]),
+                        s[h][c] = __ffma2_rn(make_float2(raw[h][4 + 2 * c], raw[h][5 + 2 * c]),
                                              make_float2(0.0625f, 0.0625f),
-                                             make_float2(raw[2 * c], raw[2 * c + 1]));
-                }
+                                             make_float2(raw[h][2 * c], raw[h][2 * c + 1]));
                 tc::fence_before_sync();
                 __syncwarp();
                 if (lane == 0) {
@@ -792,17 +826,33 @@ gqa_decode_fp8_kernel(const __grid_constant__ Fp8DecodeParams p) {
             // columns a warp).  The row sums and references go through shared memory
             // while the last P.V is still in flight.
             float *lb = lred + (iter & 1) * 80;   // [4 key warps][16 columns], then m[16]
+            // (halving butterfly: the warp's sum of column n ends up in the lanes whose
+            // upper bits are n)
+            float part[4 * NCH];
 #pragma unroll
-            for (int h = 0; h < NCH; ++h)
+            for (int n = 0; n < 4 * NCH; ++n)
+                part[n] = n & 1 ? l[n >> 2][(n >> 1) & 1].y : l[n >> 2][(n >> 1) & 1].x;
+            int at = 0, o = 16;
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const float2 a = make_float2(warp_sum(l[h][c].x), warp_sum(l[h][c].y));
-                    if (lane == 0) {
-                        *reinterpret_cast<float2 *>(lb + kw * 16 + col(h) + 2 * c) = a;
-                        if (kw == 0)
-                            *reinterpret_cast<float2 *>(lb + 64 + col(h) + 2 * c) = m[h][c];
-                    }
+            for (int n = 2 * NCH; n > 0; n >>= 1, o >>= 1) {
+                const bool upper = lane & o;
+                at += upper ? n : 0;
+#pragma unroll
+                for (int i = 0; i < n; ++i) {
+                    const float keep = upper ? part[n + i] : part[i];
+                    const float give = upper ? part[i] : part[n + i];
+                    part[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
                 }
+            }
+            for (; o > 0; o >>= 1) part[0] += __shfl_xor_sync(0xffffffffu, part[0], o);
+            if ((lane & (32 / (4 * NCH) - 1)) == 0) lb[kw * 16 + col(at >> 2) + (at & 3)] = part[0];
+            if (kw == 0 && lane == 0) {
+#pragma unroll
+                for (int h = 0; h < NCH; ++h)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+                        *reinterpret_cast<float2 *>(lb + 64 + col(h) + 2 * c) = m[h][c];
+            }
             named_sync(1 + grp, 128);
             if (it.ntiles > 0)
                 ok = ok && mbar_wait(&bar[kODone], (g + it.ntiles - 1) & 1, p.err);
@@ -810,37 +860,41 @@ gqa_decode_fp8_kernel(const __grid_constant__ Fp8DecodeParams p) {
             const bool has_o = ok && it.ntiles > 0;
             const int ch = k;   // output channel of this thread
 #pragma unroll 1
-            for (int x = 0; x < 4 * NCH; ++x) {
-                const int cg = col(x >> 2) + (x & 3);
-                const int i = (cg * g_inv) >> 16, hd = cg - i * G;
-                if (i >= nrows) continue;
-                float o0, o1, o2;
-                tmem_ld_terms(tmem + lane_base + C::kTmemO + 4 * (cg & ~3) + (cg & 3), o0, o1, o2);
-                const float acc = has_o ? fmaf(fmaf(o2, 0.0625f, o1), 0.0625f, o0) *
-                                              (1.f / kWeightTop) : 0.f;
-                const float lsum = (lb[cg] + lb[16 + cg]) + (lb[32 + cg] + lb[48 + cg]);
-                // no visible key: no sum, no reference
-                const float mx = lsum == 0.f ? -INFINITY : lb[64 + cg];
-                const int hq = it.kvh * G + hd;
-                if (it.direct) {
-                    const float t2 = p.sink ? p.sink[hq] * kLog2e : -INFINITY;
-                    const float Mf = fmaxf(mx, t2);
-                    float so = 1.f, Z = lsum;
-                    if (Mf != -INFINITY) {
-                        so = fast_exp2(mx - Mf);    // 0 when mx = -inf
-                        Z = lsum * so + fast_exp2(t2 - Mf);
-                    }
-                    const float v = Z == 0.f ? 0.f : __fdividef(acc * so, Z);
-                    const size_t row = size_t(row0 + i) * p.num_q_heads + hq;
-                    p.out[row * kD + ch] = static_cast<uint16_t>(pack_bf16x2(v, 0.f) & 0xffffu);
-                    if (ch == 0 && p.lse)
-                        p.lse[row] = Z == 0.f ? -INFINITY : (Mf + fast_log2(Z)) * kLn2;
-                } else {
-                    const size_t base = size_t(it.slot) * kGqaSlotCols + cg;
-                    p.ws_o[base * kD + ch] = acc;
-                    if (ch == 0) {
-                        p.ws_m[base] = mx * kLn2;
-                        p.ws_l[base] = lsum;
+            for (int x = 0; x < 4 * NCH; x += 2) {
+                const int c0 = col(x >> 2) + (x & 3);
+                if (c0 >= cols) break;
+                float o0[2], o1[2], o2[2];
+                tmem_ld_terms(tmem + lane_base + C::kTmemO + 4 * (c0 & ~3) + (c0 & 3), o0, o1, o2);
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int cg = c0 + u, i = (cg * g_inv) >> 16;
+                    if (i >= nrows) continue;
+                    const float acc = has_o ? fmaf(fmaf(o2[u], 0.0625f, o1[u]), 0.0625f, o0[u]) *
+                                                  (1.f / kWeightTop) : 0.f;
+                    const float lsum = (lb[cg] + lb[16 + cg]) + (lb[32 + cg] + lb[48 + cg]);
+                    // no visible key: no sum, no reference
+                    const float mx = lsum == 0.f ? -INFINITY : lb[64 + cg];
+                    const int hq = it.kvh * G + cg - i * G;
+                    if (it.direct) {
+                        const float t2 = p.sink ? p.sink[hq] * kLog2e : -INFINITY;
+                        const float Mf = fmaxf(mx, t2);
+                        float so = 1.f, Z = lsum;
+                        if (Mf != -INFINITY) {
+                            so = fast_exp2(mx - Mf);    // 0 when mx = -inf
+                            Z = lsum * so + fast_exp2(t2 - Mf);
+                        }
+                        const float v = Z == 0.f ? 0.f : __fdividef(acc * so, Z);
+                        const size_t row = size_t(row0 + i) * p.num_q_heads + hq;
+                        p.out[row * kD + ch] = static_cast<uint16_t>(pack_bf16x2(v, 0.f) & 0xffffu);
+                        if (ch == 0 && p.lse)
+                            p.lse[row] = Z == 0.f ? -INFINITY : (Mf + fast_log2(Z)) * kLn2;
+                    } else {
+                        const size_t base = size_t(it.slot) * kGqaSlotCols + cg;
+                        p.ws_o[base * kD + ch] = acc;
+                        if (ch == 0) {
+                            p.ws_m[base] = mx * kLn2;
+                            p.ws_l[base] = lsum;
+                        }
                     }
                 }
             }
