@@ -25,9 +25,10 @@ namespace attn {
 
 struct Fp8Range {
     int x0, x1;            // this group's tiles of the concatenation
-    int u0, count;         // its first unit, and how many it meets
+    int u0, u1;            // its first and last unit
     int groups;            // C, after leaving out groups without tiles
     int cost;              // W
+    __device__ __forceinline__ int count() const { return x1 > x0 ? u1 - u0 + 1 : 0; }
 };
 
 struct Fp8Item {
@@ -41,10 +42,15 @@ __device__ __forceinline__ int fp8_tiles(uint32_t len, uint32_t cap) {
     return max(static_cast<int>((min(len, cap) + kGqaTcTileKeys - 1) / kGqaTcTileKeys), 1);
 }
 
-// First position of group c.
+// First position of group c: c W / C, in 32 bits (c <= C, and C C fits).
 __device__ __forceinline__ int first_position(int c, int W, int C) {
-    return static_cast<int>(static_cast<long long>(c) * W / C);
+    const int q = W / C;
+    return c * q + c * (W - q * C) / C;
 }
+
+// By the number of head groups, which usually is 1 (an integer division is some
+// forty instructions, on the way to a CTA's first load).
+__device__ __forceinline__ int by_groups(int x, int hg) { return hg == 1 ? x : x / hg; }
 
 // Cost of a tile of sequence b.
 __device__ __forceinline__ int fp8_tile_cost(const Fp8DecodeParams &p, int b) {
@@ -54,10 +60,11 @@ __device__ __forceinline__ int fp8_tile_cost(const Fp8DecodeParams &p, int b) {
 }
 
 // cum[b].x: tiles of the concatenation before sequence b (head groups included),
-// cum[b].y: their cost, b up to the batch; and this group's range.  One warp, all
-// lanes.  (The host bounds the tiles of a call so that costs fit an int.)
-__device__ __forceinline__ void fp8_build_items(const Fp8DecodeParams &p, int2 *cum, int lane,
-                                                Fp8Range *out) {
+// cum[b].y: their cost, b up to the batch; and this group's range.  Two warps, all
+// lanes: warp 0 finds where the range begins (and writes cum), warp 1 where it
+// ends.  (The host bounds the tiles of a call so that costs fit an int.)
+__device__ __forceinline__ void fp8_build_items(const Fp8DecodeParams &p, int2 *cum, int warp,
+                                                int lane, Fp8Range *out) {
     const int hg = p.head_groups;
     const uint32_t cap = uint32_t(p.max_kv_len);
     const int per_lane = (p.batch + 31) / 32;
@@ -65,7 +72,7 @@ __device__ __forceinline__ void fp8_build_items(const Fp8DecodeParams &p, int2 *
     int local = 0, cost = 0;
     for (int b = b0; b < b1; ++b) {
         const uint32_t len = p.kv_len[b];
-        if (len > cap && blockIdx.x == 0) atomicOr(p.err, kErrBadLength);
+        if (len > cap && blockIdx.x == 0 && warp == 0) atomicOr(p.err, kErrBadLength);
         const int n = fp8_tiles(len, cap);
         local += n * hg;
         cost += hg * (n * fp8_tile_cost(p, b) + kFp8UnitCost);
@@ -80,14 +87,16 @@ __device__ __forceinline__ void fp8_build_items(const Fp8DecodeParams &p, int2 *
             cost_incl += w;
         }
     }
-    int2 run = make_int2(incl - local, cost_incl - cost);
-    for (int b = b0; b < b1; ++b) {
-        cum[b] = run;
-        const int n = fp8_tiles(p.kv_len[b], cap);
-        run.x += n * hg;
-        run.y += hg * (n * fp8_tile_cost(p, b) + kFp8UnitCost);
+    if (warp == 0) {
+        int2 run = make_int2(incl - local, cost_incl - cost);
+        for (int b = b0; b < b1; ++b) {
+            cum[b] = run;
+            const int n = fp8_tiles(p.kv_len[b], cap);
+            run.x += n * hg;
+            run.y += hg * (n * fp8_tile_cost(p, b) + kFp8UnitCost);
+        }
+        if (lane == 31) cum[p.batch] = make_int2(incl, cost_incl);
     }
-    if (lane == 31) cum[p.batch] = make_int2(incl, cost_incl);
 
     const int T = __shfl_sync(0xffffffffu, incl, 31);
     const int W = __shfl_sync(0xffffffffu, cost_incl, 31);
@@ -108,7 +117,7 @@ __device__ __forceinline__ void fp8_build_items(const Fp8DecodeParams &p, int2 *
                 const int unit_span = n * tile + kFp8UnitCost;
                 const int span = hg * unit_span;
                 if (y < ws + span) {
-                    const int h = (y - ws) / unit_span;
+                    const int h = hg == 1 ? 0 : (y - ws) / unit_span;
                     const int o = (y - ws) - h * unit_span - kFp8UnitCost;
                     const int i = o <= 0 ? 0 : (o + tile - 1) / tile;
                     x = xs + h * n + i;
@@ -124,25 +133,29 @@ __device__ __forceinline__ void fp8_build_items(const Fp8DecodeParams &p, int2 *
         first = __shfl_sync(0xffffffffu, f, src) != 0;
         return __shfl_sync(0xffffffffu, x, src);
     };
-    Fp8Range r;
-    r.x0 = r.x1 = r.u0 = r.count = 0;
-    r.groups = C;
-    r.cost = W;
-    if (c < C) {
-        int u0, u1, u_last;
-        bool f0, f1;
-        r.x0 = locate(first_position(c, W, C), u0, f0);
-        if (c + 1 == C) {
-            r.x1 = T;
-            u_last = p.batch * hg - 1;
-        } else {
-            r.x1 = locate(first_position(c + 1, W, C), u1, f1);
-            u_last = f1 ? u1 - 1 : u1;   // x1 - 1 lies in the unit before when x1 opens one
+    int u = 0, x = 0;
+    bool opens;
+    if (warp == 0) {
+        if (c < C) x = locate(first_position(c, W, C), u, opens);
+        if (lane == 0) {
+            out->x0 = x;
+            out->u0 = u;
+            out->groups = C;
+            out->cost = W;
         }
-        r.u0 = u0;
-        r.count = r.x1 > r.x0 ? u_last - u0 + 1 : 0;
+    } else {
+        if (c + 1 < C) {
+            x = locate(first_position(c + 1, W, C), u, opens);
+            u -= opens;    // tile x - 1 lies in the unit before when x opens one
+        } else if (c + 1 == C) {
+            x = T;
+            u = p.batch * hg - 1;
+        }
+        if (lane == 0) {
+            out->x1 = x;
+            out->u1 = u;
+        }
     }
-    if (lane == 0) *out = r;
 }
 
 // The piece of unit u0 + j inside the range.
@@ -151,11 +164,11 @@ __device__ __forceinline__ Fp8Item fp8_item(const Fp8DecodeParams &p, const int2
     const int hg = p.head_groups;
     Fp8Item it;
     it.unit = r.u0 + j;
-    it.b = it.unit / hg;
+    it.b = by_groups(it.unit, hg);
     const int h = it.unit - it.b * hg;
     const int member = static_cast<int>(blockIdx.x) & ((1 << p.head_shift) - 1);
     it.kvh = (h << p.head_shift) + member;
-    it.unit_tiles = (cum[it.b + 1].x - cum[it.b].x) / hg;
+    it.unit_tiles = by_groups(cum[it.b + 1].x - cum[it.b].x, hg);
     const int x = cum[it.b].x + h * it.unit_tiles;
     const int tb = max(r.x0 - x, 0), te = min(r.x1 - x, it.unit_tiles);
     it.L = static_cast<int>(min(p.kv_len[it.b], uint32_t(p.max_kv_len)));

@@ -261,14 +261,14 @@ __device__ __forceinline__ void lookup_boxes(const Fp8DecodeParams &p, const Fp8
         slot = tk;
         return;
     }
-    const int pidx = tk / p.page_size;
+    const int pidx = tk >> (31 - __clz(p.page_size));   // (pages of a table: powers of two)
     const int e = pidx < p.max_pages ? p.page_table[size_t(it.b) * p.max_pages + pidx] : -1;
     if (e < 0 || e >= p.num_pages) {
         if (report) atomicOr(p.err, kErrBadPage);
         return;
     }
     page = e;
-    slot = tk % p.page_size;
+    slot = tk & (p.page_size - 1);
 }
 
 // K or V producer: walks this CTA's items and tiles and lets lane 0 issue the
@@ -281,13 +281,12 @@ __device__ __forceinline__ void produce(const Fp8DecodeParams &p, const int2 *cu
     uint64_t *empty = bar + (kIsK ? kKEmpty : kVEmpty);
     uint8_t *ring = smem + (kIsK ? Cfg<NC>::kring : Cfg<NC>::vring);
     constexpr int kN = kIsK ? kStages : kVStages;
-    if (lane == 0) prefetch_tensormap(map);
     const int box_rows = p.box_rows;        // 128, 64, 32, 16 or 8
     const int nb = kBK / box_rows;          // row boxes per tile
     const uint32_t box_bytes = uint32_t(box_rows) * 128u;
     int g = 0;
     bool aborted = false;
-    for (int j = 0; j < w.count && !aborted; ++j) {
+    for (int j = 0, items = w.count(); j < items && !aborted; ++j) {
         const Fp8Item it = fp8_item(p, cum, w, j);
         if (it.ntiles == 0) continue;
         int cached = -1, my_page = -1, my_slot = 0;
@@ -355,7 +354,7 @@ __device__ __forceinline__ void feed(const Fp8DecodeParams &p, const int2 *cum, 
     const int nb_shift = 7 - box_shift;             // boxes per tile
     int g = 0, itq = 0;
     bool ok = true;
-    for (int j = 0; ok && j < w.count; ++j) {
+    for (int j = 0, items = w.count(); ok && j < items; ++j) {
         const Fp8Item it = fp8_item(p, cum, w, j);
         if (it.ntiles == 0) continue;
         const int qb = itq % kQBufs;
@@ -481,8 +480,10 @@ gqa_decode_fp8_kernel(const __grid_constant__ Fp8DecodeParams p) {
     const int lane = threadIdx.x & 31;
     const int G = p.group;
 
-    if (warp == 0) fp8_build_items(p, cum, lane, range);
-    if (threadIdx.x == 32) {
+    if (warp < 2) fp8_build_items(p, cum, warp, lane, range);
+    if (lane == 0 && (warp == C::kWarpK || warp == C::kWarpV))
+        prefetch_tensormap(warp == C::kWarpK ? &p.k_map : &p.v_map);
+    if (threadIdx.x == 64) {
         for (int i = 0; i < kNumBars; ++i) {
             uint32_t n = 1;
             if (i == kSFree || i == kSFree + 1 || i == kPFull) n = 4 * C::kGroups;
@@ -498,14 +499,16 @@ gqa_decode_fp8_kernel(const __grid_constant__ Fp8DecodeParams p) {
         tc::tmem_relinquish();
     }
     // Rows of Q and P past the columns in use stay zero.
-    for (int i = threadIdx.x; i < (kQBufs * C::NS + C::NP) * 8; i += C::kThreads)
-        reinterpret_cast<uint4 *>(smem + C::q)[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (warp >= 2)
+        for (int i = threadIdx.x - 64; i < (kQBufs * C::NS + C::NP) * 8; i += C::kThreads - 64)
+            reinterpret_cast<uint4 *>(smem + C::q)[i] = make_uint4(0u, 0u, 0u, 0u);
     tc::fence_async_smem();
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = *tmem_slot;
     const Fp8Range walk = *range;
+    const int items = walk.count();
 
     if (warp == C::kWarpK) {
         produce<true, NC>(p, cum, walk, smem, bar, lane);
@@ -526,7 +529,7 @@ gqa_decode_fp8_kernel(const __grid_constant__ Fp8DecodeParams p) {
             const uint64_t pd = smem_desc_plain(smem_addr(smem + C::p), 128, kBK * 16);
             int g = 0, itq = 0;
             bool ok = true;
-            for (int j = 0; ok && j < walk.count; ++j) {
+            for (int j = 0; ok && j < items; ++j) {
                 const Fp8Item it = fp8_item(p, cum, walk, j);
                 if (it.ntiles == 0) continue;
                 const int qb = itq % kQBufs;
@@ -589,7 +592,7 @@ gqa_decode_fp8_kernel(const __grid_constant__ Fp8DecodeParams p) {
         int g = 0, iter = 0, itq = 0;
         int ss = 0, sph = 0;                         // stage and phase of the scale ring
         bool ok = true;
-        for (int j = 0; j < walk.count; ++j, ++iter) {
+        for (int j = 0; j < items; ++j, ++iter) {
             const Fp8Item it = fp8_item(p, cum, walk, j);
             int row0, nrows;
             seq_rows(p, it.b, row0, nrows);
