@@ -862,6 +862,8 @@ gqa_decode_fp8_kernel(const __grid_constant__ Fp8DecodeParams p) {
             tc::fence_after_sync();
             const bool has_o = ok && it.ntiles > 0;
             const int ch = k;   // output channel of this thread
+            const size_t head0 = size_t(row0) * p.num_q_heads + it.kvh * G;
+            const size_t slot0 = size_t(it.slot) * kGqaSlotCols;
 #pragma unroll 1
             for (int x = 0; x < 4 * NCH; x += 2) {
                 const int c0 = col(x >> 2) + (x & 3);
@@ -877,9 +879,8 @@ gqa_decode_fp8_kernel(const __grid_constant__ Fp8DecodeParams p) {
                     const float lsum = (lb[cg] + lb[16 + cg]) + (lb[32 + cg] + lb[48 + cg]);
                     // no visible key: no sum, no reference
                     const float mx = lsum == 0.f ? -INFINITY : lb[64 + cg];
-                    const int hq = it.kvh * G + cg - i * G;
                     if (it.direct) {
-                        const float t2 = p.sink ? p.sink[hq] * kLog2e : -INFINITY;
+                        const float t2 = p.sink ? p.sink[it.kvh * G + cg - i * G] * kLog2e : -INFINITY;
                         const float Mf = fmaxf(mx, t2);
                         float so = 1.f, Z = lsum;
                         if (Mf != -INFINITY) {
@@ -887,12 +888,12 @@ gqa_decode_fp8_kernel(const __grid_constant__ Fp8DecodeParams p) {
                             Z = lsum * so + fast_exp2(t2 - Mf);
                         }
                         const float v = Z == 0.f ? 0.f : __fdividef(acc * so, Z);
-                        const size_t row = size_t(row0 + i) * p.num_q_heads + hq;
+                        const size_t row = head0 + i * p.num_q_heads + cg - i * G;
                         p.out[row * kD + ch] = static_cast<uint16_t>(pack_bf16x2(v, 0.f) & 0xffffu);
                         if (ch == 0 && p.lse)
                             p.lse[row] = Z == 0.f ? -INFINITY : (Mf + fast_log2(Z)) * kLn2;
                     } else {
-                        const size_t base = size_t(it.slot) * kGqaSlotCols + cg;
+                        const size_t base = slot0 + cg;
                         p.ws_o[base * kD + ch] = acc;
                         if (ch == 0) {
                             p.ws_m[base] = mx * kLn2;
