@@ -14,7 +14,9 @@
 // The work on one head is a chain (load, sum of squares, maximum, codes), so the
 // next head's vectors are fetched into shared memory meanwhile, each thread's own
 // (in registers, they would spill).  cos and sin of the tokens' positions are
-// shared by the CTA's heads.
+// shared by the CTA's heads.  Bound by that chain, with the two CTAs an SM that the
+// registers allow: 24768 rows of 8 + 8 heads (152 MB) take 49 us where their bytes
+// take 22; the tile kernel of the short runs with four items a thread took 77.
 #include "head_tiles.cuh"
 
 namespace attn {

@@ -30,9 +30,21 @@
 // split-K reduce merges.  The reference is lazy: it follows a tile's maximum
 // only when that exceeds it by more than 2^kLazy.
 //
-// Warp roles: softmax and epilogue (four warps, or two groups of four for 16
-// columns), K producer and V producer (TMA), MMA issue, and one warp that
+// Warp roles: softmax and epilogue (four warps, or two groups of four for more
+// than 4 columns), K producer and V producer (TMA), MMA issue, and one warp that
 // turns q into its terms and fetches the scales of each tile's keys (cp.async).
+//
+// What bounds it.  Up to 4 columns the stream of codes: 64 sequences of 32 + 8
+// heads and 512 to 8192 keys (580 MB) take 96.7 us, 6.0 TB/s with everything,
+// about 7 while the stream runs.  The rest is 5 us until the first scores
+// (range, page table, first tile), the ends of the CTAs and the reduce.  With 16
+// columns the softmax of a tile takes longer than its bytes (1 to 4 draft
+// rows of 4 heads: 85 us for 318 MB).  What runs once an item (opening it, the first
+// tile's maxima, the epilogue) runs from a cold instruction cache, at 100 cycles
+// and more per eight instructions: hence the rolled loops and the care for code
+// length there.  (Heads taken one after the other 114.9 us, P through a swizzled
+// K-major layout 201 instead of 158 us for the draft rows, one group of warps for
+// 16 columns 147 instead of 103, 3 V stages the same.)
 #include <cuda_fp8.h>
 
 #include "cache_ops.h"
@@ -58,7 +70,7 @@ constexpr int kMinVExp = -64, kMaxVExp = 64;
 
 // Columns (query rows x heads) come in chunks of four: a chunk's S columns (and Q
 // rows) are [2 terms][4], its O columns (and P columns) [3 terms][4] and four
-// unused ones.  Sixteen columns take two groups of four softmax warps; group g
+// unused ones.  More than one chunk takes two groups of four softmax warps; group g
 // has the chunks g, g + 2.  Chunks past an item's columns are skipped.
 template <int NC>
 struct Cfg {
@@ -824,10 +836,10 @@ gqa_decode_fp8_kernel(const __grid_constant__ Fp8DecodeParams p) {
             }
 
             // ---- item epilogue ----------------------------------------------------
-            // Rolled over the columns and short on purpose: it runs once an item,
-            // from a cold instruction cache (unrolled, it took 10000 cycles for 8
-            // columns a warp).  The row sums and references go through shared memory
-            // while the last P.V is still in flight.
+            // Rolled over pairs of columns and short on purpose: it runs once an item,
+            // from a cold instruction cache (all 8 columns of a warp unrolled: 10000
+            // cycles; a pair at a time: 3000 to 5000).  The row sums and references go
+            // through shared memory while the last P.V is still in flight.
             float *lb = lred + (iter & 1) * 80;   // [4 key warps][16 columns], then m[16]
             // (halving butterfly: the warp's sum of column n ends up in the lanes whose
             // upper bits are n)

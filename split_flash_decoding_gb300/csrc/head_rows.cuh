@@ -10,9 +10,9 @@ namespace attn {
 // cos and sin of pair i's angle at a position, times mscale.  The phase is a
 // 64-bit fraction of a turn, so the product wraps exactly.  Its two top bits
 // (rounded) are the quadrant; what is left, within an eighth of a turn, becomes
-// an fp32 angle and the rest of it, and the Taylor series end where the
-// next term is below 2^-28.  Within 1.3 steps of the exact cos and sin: a plain fp32 angle would miss by up to 2^-25 pi, which
-// moves roundings to 8 bits.
+// an fp32 angle and the rest of it, and the Taylor series end where the next term
+// is below 2^-28.  Within 1.3 steps of the exact cos and sin: a plain fp32 angle
+// would miss by up to 2^-25 pi, which moves roundings to 8 bits.
 __device__ __forceinline__ void rope_cos_sin(const RopeParams &rope, int i, int pos, float &c,
                                              float &s) {
     const uint64_t phase = static_cast<uint64_t>(static_cast<int64_t>(pos)) * rope.turns[i];
