@@ -40,11 +40,6 @@ size_t run_smem(const RowsParams &p) {
            size_t(kT) * 2 * kS * sizeof(uint4);
 }
 
-__device__ __forceinline__ void copy_16(void *dst, const void *src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src)
-                 : "memory");
-}
-
 template <bool kInter>
 __global__ void __launch_bounds__(kT, 2)
 append_fp8_runs_kernel(const __grid_constant__ RowsParams p, const __grid_constant__ RunCut cut) {

@@ -50,6 +50,7 @@ struct Cut {
 };
 
 constexpr int kThreads = 256;
+constexpr int kAhead = 2;             // heads whose vectors are on their way
 
 // Items of L lanes at once: also the most rows of a tile.
 template <int L>
@@ -80,6 +81,11 @@ __device__ __forceinline__ void pair_of(bool inter, int vecs, int R, int i, int 
     const int H = (vecs - base + 1) / 2;
     a = j < H ? base + j : -1;
     b = j < H && base + j + H < vecs ? base + j + H : -1;
+}
+
+__device__ __forceinline__ void copy_16(void *dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src)
+                 : "memory");
 }
 
 __device__ __forceinline__ void unpack8(const uint4 &w, float2 (&x)[4]) {
@@ -307,15 +313,79 @@ inline long long fp8_tile_count(const RowsParams &p) {
     return p.q_row_offsets && bound < p.num_rows ? bound : p.num_rows;
 }
 
-// A thread's item: where it is in the list of heads (q, then k, then v).
+// The kind of head h of the list (q, then k, then v), its number among them and
+// the end of its kind (within h1).
+struct KindOf {
+    int kind, head, end;
+};
+
+__device__ __forceinline__ KindOf kind_of(const RowsParams &p, int h, int h1) {
+    const int k0 = p.q.heads, v0 = p.q.heads + p.k.heads;
+    KindOf x;
+    x.kind = h < k0 ? 0 : h < v0 ? 1 : 2;
+    x.head = h - (x.kind == 0 ? 0 : x.kind == 1 ? k0 : v0);
+    x.end = min(h1, x.kind == 0 ? k0 : x.kind == 1 ? v0 : h1);
+    return x;
+}
+
+__device__ __forceinline__ const HeadRows &rows_of_kind(const RowsParams &p, int kind) {
+    return kind == 0 ? p.q : kind == 1 ? p.k : p.v;
+}
+
+// First channels of lane i's two vectors; -1: none.
+template <bool kInter>
+__device__ __forceinline__ void channels_of(const RowsParams &p, const HeadRows &x, int kind, int i,
+                                            int &ca, int &cb) {
+    const int turning = kind < 2 ? p.rope.rot_dim / 8 : 0, start = x.rot_start / 8;
+    int a, b;
+    pair_of(kInter, x.dim / 8, turning, i, a, b);
+    ca = a >= 0 ? 8 * ordered(a, turning, start) : -1;
+    cb = b >= 0 ? 8 * ordered(b, turning, start) : -1;
+}
+
+// Where a thread's next vectors come from.
+struct Source {
+    const uint16_t *src;              // the head vector
+    long long step;                   // to the thread's next head
+    int h, h_end, ca, cb;
+
+    template <bool kInter>
+    __device__ __forceinline__ void open(const RowsParams &p, int row, int i0, int h1,
+                                         int step_heads) {
+        ca = cb = -1;
+        h_end = 0x7fffffff;
+        src = nullptr;
+        step = 0;
+        if (h >= h1) return;
+        const KindOf k = kind_of(p, h, h1);
+        const HeadRows &x = rows_of_kind(p, k.kind);
+        channels_of<kInter>(p, x, k.kind, i0, ca, cb);
+        h_end = k.end;
+        src = x.in + row * x.in_row + k.head * x.in_head;
+        step = step_heads * x.in_head;
+    }
+
+    // Sends for the vectors (if any) and moves on.
+    template <bool kInter>
+    __device__ __forceinline__ void fetch(const RowsParams &p, int row, int i0, int h1,
+                                          int step_heads, uint4 *to) {
+        if (ca >= 0) copy_16(to, src + ca);
+        if (cb >= 0) copy_16(to + kThreads, src + cb);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        h += step_heads;
+        src += step;
+        if (h >= h_end) open<kInter>(p, row, i0, h1, step_heads);
+    }
+};
+
+// A thread's item: where it is in the list of heads.
 struct Item {
     enum { kNormA = 1, kNormB = 2, kTurnA = 4, kTurnB = 8 };
-    const uint16_t *src;              // its head vector
     uint16_t *dst;                    // rows: its output; a cache: the head's offset
-    long long src_step, dst_step;     // to the item's next head
+    long long dst_step;               // to the thread's next head
     uint4 ga, gb;                     // the norm's weights of its channels
     float mean, eps;
-    int row, h, h_end, kind, head;    // h_end: first head of the next kind
+    int row, h, h_end, kind, head;
     int ca, cb;                       // its two first channels; -1: none
     int flags;
     bool to_cache;
@@ -328,25 +398,18 @@ struct Item {
         kind = 0;
         head = 0;
         h_end = 0x7fffffff;
-        src = nullptr;
         dst = nullptr;
-        src_step = dst_step = 0;
+        dst_step = 0;
         mean = eps = 0.f;
         to_cache = false;
         ga = gb = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);   // 1
         if (h >= h1) return;
-        const int k0 = p.q.heads, v0 = p.q.heads + p.k.heads;
-        kind = h < k0 ? 0 : h < v0 ? 1 : 2;
-        const HeadRows &x = kind == 0 ? p.q : kind == 1 ? p.k : p.v;
-        head = h - (kind == 0 ? 0 : kind == 1 ? k0 : v0);
-        h_end = min(h1, kind == 0 ? k0 : kind == 1 ? v0 : h1);
-        const int turning = kind < 2 ? p.rope.rot_dim / 8 : 0, start = x.rot_start / 8;
-        int a, b;
-        pair_of(kInter, x.dim / 8, turning, i0, a, b);
-        if (a >= 0) ca = 8 * ordered(a, turning, start);
-        if (b >= 0) cb = 8 * ordered(b, turning, start);
-        src = x.in + (r0 + row) * x.in_row + head * x.in_head;
-        src_step = step_heads * x.in_head;
+        const KindOf k = kind_of(p, h, h1);
+        const HeadRows &x = rows_of_kind(p, k.kind);
+        kind = k.kind;
+        head = k.head;
+        h_end = k.end;
+        channels_of<kInter>(p, x, kind, i0, ca, cb);
         to_cache = x.out == nullptr;
         if (to_cache) {
             const CacheOut &c = kind == 1 ? p.kc : p.vc;
@@ -358,16 +421,17 @@ struct Item {
         }
         mean = x.mean;
         eps = x.eps;
-        if (a >= 0 && ca < x.norm_dim) {
+        if (ca >= 0 && ca < x.norm_dim) {
             flags |= kNormA;
             if (x.norm) ga = *reinterpret_cast<const uint4 *>(x.norm + ca);
         }
-        if (b >= 0 && cb < x.norm_dim) {
+        if (cb >= 0 && cb < x.norm_dim) {
             flags |= kNormB;
             if (x.norm) gb = *reinterpret_cast<const uint4 *>(x.norm + cb);
         }
-        if (a >= 0 && a < turning) flags |= kTurnA;
-        if (b >= 0 && b < turning) flags |= kTurnB;
+        const int turn0 = x.rot_start, turn1 = kind < 2 ? turn0 + p.rope.rot_dim : turn0;
+        if (ca >= turn0 && ca < turn1) flags |= kTurnA;
+        if (cb >= turn0 && cb < turn1) flags |= kTurnB;
     }
 
     // step_heads heads on
@@ -376,13 +440,13 @@ struct Item {
                                             int step_heads) {
         h += step_heads;
         head += step_heads;
-        src += src_step;
         dst += dst_step;
         if (h >= h_end) open<kInter>(p, r0, i0, h1, step_heads);
     }
 };
 
-template <int L, bool kInter, bool kFp8>
+// kMany: a CTA has more heads than it works on at once (never with kFp8).
+template <int L, bool kInter, bool kFp8, bool kMany>
 __global__ void __launch_bounds__(kThreads, kFp8 ? 2 : 4)
 head_tiles_kernel(const __grid_constant__ RowsParams p, const __grid_constant__ Cut cut) {
     constexpr int kItems = kItemsOf<L>;
@@ -429,14 +493,24 @@ head_tiles_kernel(const __grid_constant__ RowsParams p, const __grid_constant__ 
     it.row = item0 & ((1 << shift) - 1);
     it.h = it.row < n ? h0 + (item0 >> shift) : h1;
     it.row = min(it.row, n - 1);
+    Source from;
+    from.h = it.h;
+    from.open<kInter>(p, r0 + it.row, i0, h1, step_heads);
+    // kMany: the vectors go through shared memory, each thread's own, two heads ahead;
+    // as many bytes as that have to be on their way for the memory's rate (in
+    // registers and none ahead, 24768 rows of 48 heads took 131.7 us, not 108.4).
+    uint4 *ring = reinterpret_cast<uint4 *>(angles) + (half > 0 ? cut.tile_rows * 4 * L : 0) + tid;
+    uint4 ra = make_uint4(0u, 0u, 0u, 0u), rb = ra;
+    if (kMany) {
+#pragma unroll
+        for (int s = 0; s < kAhead; ++s)
+            from.fetch<kInter>(p, r0 + it.row, i0, h1, step_heads, ring + 2 * s * kThreads);
+    } else {
+        if (from.ca >= 0) ra = *reinterpret_cast<const uint4 *>(from.src + from.ca);
+        if (from.cb >= 0) rb = *reinterpret_cast<const uint4 *>(from.src + from.cb);
+    }
     it.open<kInter>(p, r0, i0, h1, step_heads);
-    uint4 ra, rb;
-    const auto load = [&]() {
-        ra = rb = make_uint4(0u, 0u, 0u, 0u);
-        if (it.ca >= 0) ra = *reinterpret_cast<const uint4 *>(it.src + it.ca);
-        if (it.cb >= 0) rb = *reinterpret_cast<const uint4 *>(it.src + it.cb);
-    };
-    load();
+    int slot = 0;                                                // of this head's vectors
 
     // ---- places ----------------------------------------------------------------------
     for (int i = tid; i < n; i += kThreads) {
@@ -492,6 +566,15 @@ head_tiles_kernel(const __grid_constant__ RowsParams p, const __grid_constant__ 
 
 #pragma unroll 1
     for (int hs = h0; hs < h1; hs += step_heads) {
+        if (kMany) {
+            const int last = slot == 0 ? kAhead : slot - 1;      // used up one head ago
+            from.fetch<kInter>(p, r0 + it.row, i0, h1, step_heads, ring + 2 * last * kThreads);
+            asm volatile("cp.async.wait_group %0;" ::"n"(kAhead) : "memory");
+            ra = rb = make_uint4(0u, 0u, 0u, 0u);
+            if (it.ca >= 0) ra = ring[2 * slot * kThreads];
+            if (it.cb >= 0) rb = ring[(2 * slot + 1) * kThreads];
+            slot = slot == kAhead ? 0 : slot + 1;
+        }
         float2 ya[4], yb[4];
         unpack8(ra, ya);
         unpack8(rb, yb);
@@ -527,11 +610,12 @@ head_tiles_kernel(const __grid_constant__ RowsParams p, const __grid_constant__ 
             if (store && it.cb >= 0)
                 *reinterpret_cast<uint4 *>(dst + it.cb) = plain ? rb : pack8(yb);
         }
-        if (!kFp8 || hs + step_heads <= p.q.heads) {             // queries only: uniform
+        if (!kFp8) {
+            if (!kMany) return;
             it.advance<kInter>(p, r0, i0, h1, step_heads);
-            load();
             continue;
         }
+        if (hs + step_heads <= p.q.heads) return;                // queries only: uniform
 
         // ---- 8-bit cache: scales of the blocks -----------------------------------------
         const int B = p.block_tokens, base = static_cast<int>(s_tile.first);   // row 0's token
@@ -539,7 +623,6 @@ head_tiles_kernel(const __grid_constant__ RowsParams p, const __grid_constant__ 
         const int held = s_tile.first == s_tile.begin && base >= 0 && places[0].stored > 0
                              ? base & (B - 1) : 0;
         float ratio = 1.f;                                       // of a held block's row 0
-        __syncthreads();                                         // the last heads' scales are used
         // (NaN never counts; infinities do not either, but cost a second look)
         float top = largest(ya, yb);
         const bool infinite = top > FLT_MAX;
@@ -612,20 +695,21 @@ head_tiles_kernel(const __grid_constant__ RowsParams p, const __grid_constant__ 
             uint8_t *dst = c.base + (it.kind == 1 ? at.k_at : at.v_at) + it.head * c.head_stride;
             store_codes(dst + it.ca, dst + it.cb, ya, yb, f, infinite);
         }
-        it.advance<kInter>(p, r0, i0, h1, step_heads);
-        load();
+        return;
     }
 }
 
-template <int L, bool kInter, bool kFp8>
+template <int L, bool kFp8, bool kMany>
 cudaError_t launch(const RowsParams &p, const Cut &cut, long long tiles, cudaStream_t stream) {
     const long long blocks = tiles * cut.chunks;
     if (blocks == 0) return cudaSuccess;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-    const size_t smem =
-        p.rope.rot_dim > 0 ? size_t(cut.tile_rows) * 4 * L * sizeof(float4) : 0;   // up to 16 KB
-    head_tiles_kernel<L, kInter, kFp8>
-        <<<static_cast<unsigned>(blocks), kThreads, smem, stream>>>(p, cut);
+    const size_t smem =                                              // up to 40 KB
+        (p.rope.rot_dim > 0 ? size_t(cut.tile_rows) * 4 * L * sizeof(float4) : 0) +
+        (kMany ? size_t(kAhead + 1) * 2 * kThreads * sizeof(uint4) : 0);
+    auto kern = p.rope.interleaved ? head_tiles_kernel<L, true, kFp8, kMany>
+                                   : head_tiles_kernel<L, false, kFp8, kMany>;
+    kern<<<static_cast<unsigned>(blocks), kThreads, smem, stream>>>(p, cut);
     return cudaGetLastError();
 }
 

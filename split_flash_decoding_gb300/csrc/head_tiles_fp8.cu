@@ -26,9 +26,7 @@ cudaError_t launch_fp8_tiles(const RowsParams &p, bool behind_queries, cudaStrea
     while (cut.tile_rows < longest) cut.tile_rows *= 2;
     cut.chunk_heads = kItemsOf<8> / cut.tile_rows;               // heads at once
     cut.chunks = (cut.heads + cut.chunk_heads - 1) / cut.chunk_heads;
-    const long long tiles = fp8_tile_count(p);
-    return p.rope.interleaved ? launch<8, true, true>(p, cut, tiles, stream)
-                              : launch<8, false, true>(p, cut, tiles, stream);
+    return launch<8, true, false>(p, cut, fp8_tile_count(p), stream);
 }
 
 }  // namespace attn

@@ -44,8 +44,8 @@ cudaError_t launch_lanes(const RowsParams &p, cudaStream_t stream) {
     if (per_cta > steps) per_cta = steps;
     cut.chunk_heads = static_cast<int>(per_cta) * step;
     cut.chunks = (cut.heads + cut.chunk_heads - 1) / cut.chunk_heads;
-    return p.rope.interleaved ? launch<L, true, false>(p, cut, tiles, stream)
-                              : launch<L, false, false>(p, cut, tiles, stream);
+    return per_cta > 1 ? launch<L, false, true>(p, cut, tiles, stream)
+                       : launch<L, false, false>(p, cut, tiles, stream);
 }
 
 }  // namespace
