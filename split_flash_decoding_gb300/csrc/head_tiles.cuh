@@ -17,9 +17,9 @@
 // one row has many heads in work.  A thread keeps its place in the list of heads
 // (pointers, channels, weights) and adds to it; a first form, which found all that
 // for every item, spent 437 instructions on 512 channels and took 142 us for 24768
-// rows of 48 heads (now 131.5: 609 MB at 4.6 TB/s, where a bare copy in the same
-// pattern reaches 4.9).  8191 rows of 40 heads with norms: 38.2 us; 64 rows of 48
-// heads 3.3 us, one row 2.8.
+// rows of 48 heads (now 98.5: 609 MB at 6.2 TB/s).  8191 rows of 40 heads with norms:
+// 32.6 us (5.1 TB/s; a little over two waves of CTAs); 64 rows of 48 heads 3.3 us, one
+// row 2.7.
 //
 // The 8-bit cache needs the largest value of a block of tokens before the first
 // code: a tile then is the new tokens of one sequence inside an aligned group of
@@ -50,7 +50,7 @@ struct Cut {
 };
 
 constexpr int kThreads = 256;
-constexpr int kAhead = 2;             // heads whose vectors are on their way
+constexpr int kAhead = 3;             // heads whose vectors are on their way
 
 // Items of L lanes at once: also the most rows of a tile.
 template <int L>
@@ -447,7 +447,7 @@ struct Item {
 
 // kMany: a CTA has more heads than it works on at once (never with kFp8).
 template <int L, bool kInter, bool kFp8, bool kMany>
-__global__ void __launch_bounds__(kThreads, kFp8 ? 2 : 4)
+__global__ void __launch_bounds__(kThreads, kFp8 ? 2 : kMany ? 3 : 4)
 head_tiles_kernel(const __grid_constant__ RowsParams p, const __grid_constant__ Cut cut) {
     constexpr int kItems = kItemsOf<L>;
     extern __shared__ __align__(16) float4 angles[];             // [rows][4][lanes]
@@ -496,9 +496,10 @@ head_tiles_kernel(const __grid_constant__ RowsParams p, const __grid_constant__ 
     Source from;
     from.h = it.h;
     from.open<kInter>(p, r0 + it.row, i0, h1, step_heads);
-    // kMany: the vectors go through shared memory, each thread's own, two heads ahead;
+    // kMany: the vectors go through shared memory, each thread's own, three heads ahead;
     // as many bytes as that have to be on their way for the memory's rate (in
-    // registers and none ahead, 24768 rows of 48 heads took 131.7 us, not 108.4).
+    // registers and none ahead, 24768 rows of 48 heads took 131.7 us, two ahead 108.2;
+    // 2, 3, 4 ahead, 8191 rows of 40 heads: 33.4, 32.5, 34.4).
     uint4 *ring = reinterpret_cast<uint4 *>(angles) + (half > 0 ? cut.tile_rows * 4 * L : 0) + tid;
     uint4 ra = make_uint4(0u, 0u, 0u, 0u), rb = ra;
     if (kMany) {
@@ -704,11 +705,16 @@ cudaError_t launch(const RowsParams &p, const Cut &cut, long long tiles, cudaStr
     const long long blocks = tiles * cut.chunks;
     if (blocks == 0) return cudaSuccess;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-    const size_t smem =                                              // up to 40 KB
+    const size_t smem =                                              // up to 48 KB
         (p.rope.rot_dim > 0 ? size_t(cut.tile_rows) * 4 * L * sizeof(float4) : 0) +
         (kMany ? size_t(kAhead + 1) * 2 * kThreads * sizeof(uint4) : 0);
     auto kern = p.rope.interleaved ? head_tiles_kernel<L, true, kFp8, kMany>
                                    : head_tiles_kernel<L, false, kFp8, kMany>;
+    if (smem > 40 * 1024) {                                          // (48 KB with the static part)
+        const cudaError_t e =
+            cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+        if (e != cudaSuccess) return e;
+    }
     kern<<<static_cast<unsigned>(blocks), kThreads, smem, stream>>>(p, cut);
     return cudaGetLastError();
 }

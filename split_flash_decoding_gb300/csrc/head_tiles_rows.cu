@@ -26,15 +26,18 @@ namespace {
 template <int L>
 cudaError_t launch_lanes(const RowsParams &p, cudaStream_t stream) {
     // Tiles of 8 rows: a step then reads 256 / L / 8 heads side by side of every row
-    // (1 KB at 128 channels), and the angles of a tile are two a thread.  A CTA
-    // takes all heads of its rows once the tiles fill the GPU, fewer below.
-    // us for 24768 rows of 48 heads / 8191 of 40 with norm: 4 rows 136 / 40, 8 rows
-    // 132 / 38, 16 rows 135 / 53, 32 rows and 16 heads 135 / 39.
-    constexpr int kWave = 4 * 152;                 // resident CTAs
+    // (1 KB at 128 channels), and the angles of a tile are two a thread.  16 rows where
+    // each row's place has to be found and there are enough of them: a CTA's start is
+    // longer then.  A CTA takes all heads of its rows once the tiles fill the GPU,
+    // fewer below.  us with 4, 8, 16 rows:
+    //   norms, 40 heads: 1000 rows 8.6, 8.2, 8.9; 8191 37.7, 32.7, 34.9; 16384 69.4, 57.3,
+    //   60.2; 32768 132.8, 107.3, 108.0
+    //   to a cache, 48 heads: 3096 rows (8, 16) 20.6, 21.8; 6192 34.1, 33.1; 24768 104.8, 98.6
+    constexpr int kWave = 3 * 152;                 // resident CTAs
     Cut cut;
     cut.heads = p.q.heads + p.k.heads + p.v.heads;
     cut.any_norm = (p.q.heads > 0 && p.q.norm_dim > 0) || (p.k.heads > 0 && p.k.norm_dim > 0);
-    cut.tile_rows = 8;
+    cut.tile_rows = p.kv_len && p.num_rows >= 16 * 2 * 152 ? 16 : 8;
     while (cut.tile_rows > 1 && cut.tile_rows / 2 >= p.num_rows) cut.tile_rows /= 2;
     const long long tiles = (static_cast<long long>(p.num_rows) + cut.tile_rows - 1) / cut.tile_rows;
     const int step = kItemsOf<L> / cut.tile_rows;        // heads at once

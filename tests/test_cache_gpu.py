@@ -445,6 +445,36 @@ def test_append_fp8_bad_pages_and_lengths(attn, runs):
     assert int(live[4:8].sum()) == (min(lens[2], cap) if runs[2] > 1 else 1)
 
 
+@pytest.mark.parametrize("dim,inter", [(256, False), (256, True), (200, False), (64, True)])
+def test_append_bf16_many_rows(attn, dim, inter):
+    """Enough rows for CTAs of several heads and 16 rows, in sequences of every length."""
+    lens = [700, 3000, 1, 900, 640]
+    q_lens = [650, 2999, 1, 900, 577]
+    rows, page = sum(q_lens), 64
+    pool = Pool(lens, page, 8)
+    rot = 64
+    x = randn(5, rows, 5, dim)
+    turns, rope = rope_of(attn, rot, interleaved=inter)
+    kn = (1 + randn(6, dim, scale=0.2)).to(torch.bfloat16)
+    offs = torch.tensor([sum(q_lens[:i]) for i in range(6)], dtype=torch.int32, device=DEV)
+    kc, vc = (torch.zeros(pool.pages, page, 1, dim, dtype=torch.bfloat16, device=DEV)
+              for _ in range(2))
+    g = x.to(DEV)
+    qo = attn.attn_append_kv(g[:, 3:4], g[:, 4:], kc, vc,
+                             torch.tensor(lens, dtype=torch.int32, device=DEV), max_kv_len=3000,
+                             page_table=pool.table.to(DEV), q=g[:, :3], q_row_offsets=offs,
+                             rope=rope, k_norm=kn.to(DEV))
+    places = list(rows_of(lens, q_lens))
+    tokens = torch.tensor([t for _, _, t in places])
+    qe, qerr = R.head_rows(x[:, :3], turns, tokens, interleaved=inter)
+    R.assert_bf16(qo, qe, qerr, "q")
+    at = torch.tensor([pool.place(b, t) for _, b, t in places])
+    ke, kerr = R.head_rows(x[:, 3:4], turns, tokens, norm=kn, interleaved=inter)
+    R.assert_bf16(kc.cpu()[at[:, 0], at[:, 1]], ke, kerr, "k")
+    assert torch.equal(vc.cpu()[at[:, 0], at[:, 1]], x[:, 4:])
+    assert int((vc != 0).any(-1).sum()) <= rows
+
+
 @pytest.mark.parametrize("dim,rot,start", [(64, 0, 0), (192, 0, 0), (256, 0, 0), (256, 64, 32),
                                            (576, 64, 512), (40, 0, 0)])
 @pytest.mark.parametrize("q_lens", [[1, 1, 1], [4, 1, 2], [40, 3, 130]])
