@@ -680,3 +680,96 @@ def test_append_is_captured_and_replayed(attn, fp8):
     for a, b in zip(c1, c2):
         assert torch.equal(a.view(torch.uint8) if a.dtype == FP8 else a,
                            b.view(torch.uint8) if b.dtype == FP8 else b)
+
+
+@pytest.mark.parametrize("qd,kd,rot,start", [(64, 128, 64, 0), (192, 128, 32, 64), (576, 192, 64, 128)])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_query_and_key_heads_of_unequal_dims(attn, qd, kd, rot, start, interleaved):
+    q, k = randn(1, 70, 5, qd), randn(2, 70, 3, kd)
+    qn, kn = ((1 + randn(i, d, scale=0.2)).to(torch.bfloat16) for i, d in ((3, qd), (4, kd)))
+    pos = torch.arange(70, dtype=torch.int32) * 977
+    turns, rope = rope_of(attn, rot, start=start, interleaved=interleaved)
+    got = attn.attn_qk_norm_rope(q.to(DEV), k.to(DEV), pos.to(DEV), rope=rope, q_norm=qn.to(DEV),
+                                 k_norm=kn.to(DEV))
+    for y, x, n in zip(got, (q, k), (qn, kn)):
+        exact, err = R.head_rows(x, turns, pos, norm=n, start=start, interleaved=interleaved)
+        R.assert_bf16(y, exact, err, f"dim {x.shape[2]}")
+
+
+def test_append_fp8_many_heads(attn):
+    check_fp8(attn, [70, 200], [40, 150], 64, 16, 9, hkv=40, magnitude=2.0)
+
+
+@pytest.mark.parametrize("q_lens", [[3, 1], [50, 2]])
+def test_append_fp8_given_positions_and_in_place(attn, q_lens):
+    """Positions of the tokens given: the same result; queries in place of themselves."""
+    lens = [60, 140]
+    pool = Pool(lens, 64, 2)
+    rows = sum(q_lens)
+    x = randn(7, rows, 8, 128).to(DEV)
+    turns, rope = rope_of(attn, 128)
+    offs = torch.tensor([0, q_lens[0], rows], dtype=torch.int32, device=DEV)
+    L = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    tokens = torch.tensor([t for _, _, t in rows_of(lens, q_lens)], dtype=torch.int32)
+
+    def go(x, shift=None, in_place=False):
+        c = fresh8(pool)
+        q = x[:, :4]
+        pos = None if shift is None else (tokens + shift).to(DEV)
+        out = attn.attn_append_kv_fp8(x[:, 4:6], x[:, 6:], *c, L, max_kv_len=140,
+                                      max_q_len=max(q_lens), page_table=pool.table.to(DEV), q=q,
+                                      q_out=q if in_place else None, q_row_offsets=offs, rope=rope,
+                                      positions=pos)
+        return [out.clone()] + [t.view(torch.uint8) if t.dtype == FP8 else t for t in c]
+
+    want = go(x)
+    for a, b in zip(want, go(x, 0)):
+        assert torch.equal(a, b)
+    y = x.clone()
+    for a, b in zip(want, go(y, in_place=True)):
+        assert torch.equal(a, b)
+    assert torch.equal(y[:, 4:], x[:, 4:])
+    far = go(x, 1 << 30)
+    exact, err = R.head_rows(x[:, :4].cpu(), turns, tokens + (1 << 30))
+    R.assert_bf16(far[0], exact, err, "far positions")
+    assert not torch.equal(far[1], want[1]) and torch.equal(far[2], want[2])
+
+
+def test_long_append_and_decode_in_one_graph(attn):
+    """A prompt's append (two overlapping launches) and the decode behind it, captured together
+    and replayed with other rows and lengths."""
+    lens = torch.tensor([300, 70], dtype=torch.int32, device=DEV)
+    runs = torch.tensor([0, 260, 300], dtype=torch.int32, device=DEV)
+    pool = Pool([384, 384], 64, 4)
+    table = pool.table.to(DEV)
+    x = randn(1, 300, 8 + 4, 128).to(DEV)
+    turns, rope = rope_of(attn, 128)
+
+    def go(c):
+        q = attn.attn_append_kv_fp8(x[:, 8:10], x[:, 10:], *c, lens, max_kv_len=384,
+                                    max_q_len=260, page_table=table, q=x[:, :8],
+                                    q_row_offsets=runs, rope=rope)
+        last = q[259::40].contiguous()                   # the last row of each
+        return attn.attn_decode_fp8(last, *c, lens, group=4, scale=0.09, max_kv_len=384,
+                                    page_table=table)
+
+    c1, c2 = fresh8(pool), fresh8(pool)
+    graph = torch.cuda.CUDAGraph()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        go(fresh8(pool))
+        s.synchronize()
+        with torch.cuda.graph(graph, stream=s):
+            out, lse = go(c1)
+    torch.cuda.synchronize()
+    for step in range(4):
+        lens += torch.tensor([11, 40], dtype=torch.int32, device=DEV)
+        x.copy_(randn(20 + step, 300, 12, 128))
+        graph.replay()
+        want, wl = go(c2)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(lse, wl)
+        assert torch.isfinite(out).all()
+    for a, b in zip(c1, c2):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
