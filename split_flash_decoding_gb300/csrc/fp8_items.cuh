@@ -60,9 +60,9 @@ __device__ __forceinline__ int fp8_tile_cost(const Fp8DecodeParams &p, int b) {
 }
 
 // cum[b].x: tiles of the concatenation before sequence b (head groups included),
-// cum[b].y: their cost, b up to the batch; and this group's range.  Two warps, all
-// lanes: warp 0 finds where the range begins (and writes cum), warp 1 where it
-// ends.  (The host bounds the tiles of a call so that costs fit an int.)
+// cum[b].y: their cost, b up to the batch; and this group's range.  Three warps, all
+// lanes: warp 0 finds where the range begins, warp 1 where it ends, warp 2 writes
+// cum.  (The host bounds the tiles of a call so that costs fit an int.)
 __device__ __forceinline__ void fp8_build_items(const Fp8DecodeParams &p, int2 *cum, int warp,
                                                 int lane, Fp8Range *out) {
     const int hg = p.head_groups;
@@ -87,7 +87,7 @@ __device__ __forceinline__ void fp8_build_items(const Fp8DecodeParams &p, int2 *
             cost_incl += w;
         }
     }
-    if (warp == 0) {
+    if (warp == 2) {
         int2 run = make_int2(incl - local, cost_incl - cost);
         for (int b = b0; b < b1; ++b) {
             cum[b] = run;
@@ -96,6 +96,7 @@ __device__ __forceinline__ void fp8_build_items(const Fp8DecodeParams &p, int2 *
             run.y += hg * (n * fp8_tile_cost(p, b) + kFp8UnitCost);
         }
         if (lane == 31) cum[p.batch] = make_int2(incl, cost_incl);
+        return;
     }
 
     const int T = __shfl_sync(0xffffffffu, incl, 31);

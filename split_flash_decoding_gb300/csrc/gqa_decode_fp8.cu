@@ -294,7 +294,8 @@ __device__ __forceinline__ void produce(const Fp8DecodeParams &p, const int2 *cu
     uint8_t *ring = smem + (kIsK ? Cfg<NC>::kring : Cfg<NC>::vring);
     constexpr int kN = kIsK ? kStages : kVStages;
     const int box_rows = p.box_rows;        // 128, 64, 32, 16 or 8
-    const int nb = kBK / box_rows;          // row boxes per tile
+    const int box_shift = 31 - __clz(box_rows);
+    const int nb = kBK >> box_shift;        // row boxes per tile
     const uint32_t box_bytes = uint32_t(box_rows) * 128u;
     int g = 0;
     bool aborted = false;
@@ -306,7 +307,7 @@ __device__ __forceinline__ void produce(const Fp8DecodeParams &p, const int2 *cu
             const int gg = g + t;
             const int s = gg % kN;
             const int key0 = it.start + t * kBK;
-            const int live = min(nb, (it.L - key0 + box_rows - 1) / box_rows);
+            const int live = min(nb, (it.L - key0 + box_rows - 1) >> box_shift);
             if (lane == 0) {
                 if (gg >= kN && !mbar_wait(&empty[s], ((gg / kN) - 1) & 1, p.err))
                     aborted = true;
@@ -492,10 +493,10 @@ gqa_decode_fp8_kernel(const __grid_constant__ Fp8DecodeParams p) {
     const int lane = threadIdx.x & 31;
     const int G = p.group;
 
-    if (warp < 2) fp8_build_items(p, cum, warp, lane, range);
+    if (warp < 3) fp8_build_items(p, cum, warp, lane, range);
     if (lane == 0 && (warp == C::kWarpK || warp == C::kWarpV))
         prefetch_tensormap(warp == C::kWarpK ? &p.k_map : &p.v_map);
-    if (threadIdx.x == 64) {
+    if (threadIdx.x == 96) {
         for (int i = 0; i < kNumBars; ++i) {
             uint32_t n = 1;
             if (i == kSFree || i == kSFree + 1 || i == kPFull) n = 4 * C::kGroups;
@@ -511,8 +512,8 @@ gqa_decode_fp8_kernel(const __grid_constant__ Fp8DecodeParams p) {
         tc::tmem_relinquish();
     }
     // Rows of Q and P past the columns in use stay zero.
-    if (warp >= 2)
-        for (int i = threadIdx.x - 64; i < (kQBufs * C::NS + C::NP) * 8; i += C::kThreads - 64)
+    if (warp >= 3)
+        for (int i = threadIdx.x - 96; i < (kQBufs * C::NS + C::NP) * 8; i += C::kThreads - 96)
             reinterpret_cast<uint4 *>(smem + C::q)[i] = make_uint4(0u, 0u, 0u, 0u);
     tc::fence_async_smem();
     tc::fence_before_sync();
