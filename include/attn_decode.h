@@ -571,7 +571,8 @@ typedef struct attn_kv_scale {
  *
  *   k_scale, v_scale  the caches' scales (same block_tokens).
  *   max_kv_len  at most 2^31 - 8193.
- *   max_q_len   host upper bound of the rows of any sequence.
+ *   max_q_len   host upper bound of the rows of any sequence (rows above it may
+ *               be left out, with bit 2 of the error word set).
  * Everything else as for attn_append_kv; v and v_cache are required.
  */
 int attn_append_kv_fp8(const attn_head_rows_t *q, const attn_head_rows_t *k,
@@ -592,7 +593,8 @@ int attn_append_kv_fp8(const attn_head_rows_t *q, const attn_head_rows_t *k,
  *               finite and >= 0; a V scale of 2^65 and more counts as NaN.
  *   group       query heads per KV head, 1 to 16.
  *   max_q_len   max_q_len * group <= 16 (longer row runs:
- *               ATTN_ERR_UNSUPPORTED).
+ *               ATTN_ERR_UNSUPPORTED).  A sequence with more rows may have those
+ *               above it undefined, with bit 2 of the error word set.
  *   max_kv_len  ATTN_ERR_UNSUPPORTED where the tiles of 128 keys of all
  *               sequences and KV heads would be about 2^30 and more, or above
  *               2^31 - 8193 tokens.

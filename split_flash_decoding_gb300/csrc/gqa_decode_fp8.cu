@@ -379,7 +379,8 @@ __device__ __forceinline__ void feed(const Fp8DecodeParams &p, const int2 *cum, 
         seq_rows(p, it.b, row0, nrows);
         uint8_t *qs = smem + C::q + qb * C::NS * 128;
         float *qf = reinterpret_cast<float *>(smem + C::qf) + qb * 16;
-        const int cols = min(min(nrows, p.num_q_rows - row0) * G, NC);
+        const int want = min(nrows, p.num_q_rows - row0) * G, cols = min(want, NC);
+        if (want > NC && lane == 0) atomicOr(p.err, kErrBadLength);   // above max_q_len
         // Four columns at a time, 16 channels a lane.  The bf16 rows are first copied
         // to where their own terms go; both loops are rolled, as they run from a
         // cold instruction cache (8 columns unrolled: 13000 cycles for 16 columns).

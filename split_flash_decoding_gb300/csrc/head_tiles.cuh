@@ -476,7 +476,8 @@ head_tiles_kernel(const __grid_constant__ RowsParams p, const __grid_constant__ 
         __syncthreads();
         if (!s_any) return;
         r0 = s_tile.row;
-        n = min(s_tile.count, cut.tile_rows);   // (more rows than max_q_len said)
+        n = min(s_tile.count, cut.tile_rows);
+        if (n < s_tile.count && tid == 0) atomicOr(p.err, kErrBadLength);   // above max_q_len
     } else {
         r0 = tile * cut.tile_rows;
         n = min(cut.tile_rows, p.num_rows - r0);

@@ -773,3 +773,13 @@ def test_long_append_and_decode_in_one_graph(attn):
         assert torch.isfinite(out).all()
     for a, b in zip(c1, c2):
         assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+def test_append_fp8_more_rows_than_said(attn):
+    pool = Pool([100], 64, 1)
+    c = fresh8(pool)
+    k = randn(1, 40, 2, 128).to(DEV)
+    attn.attn_append_kv_fp8(k, k, *c, torch.tensor([100], dtype=torch.int32, device=DEV),
+                            max_kv_len=100, max_q_len=4, page_table=pool.table.to(DEV),
+                            q_row_offsets=torch.tensor([0, 40], dtype=torch.int32, device=DEV))
+    assert attn.attn_device_error_flags(clear=True) == 4

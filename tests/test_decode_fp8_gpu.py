@@ -327,6 +327,12 @@ def test_bad_page_and_length_are_reported(attn):
     assert attn.attn_device_error_flags(clear=True) & 4
 
 
+def test_more_rows_than_said(attn):
+    c = Case([300, 40], [6, 1], seed=19)
+    c.run(attn, max_q_len=1)
+    assert attn.attn_device_error_flags(clear=True) == 4
+
+
 def test_append_then_decode(attn):
     """A prompt and then single tokens, appended and attended to: against attention over the
     values that the cache holds, step by step."""
