@@ -7,17 +7,13 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "fp8_split.h"
 #include "launch.h"
 
 namespace attn {
 
 // The 8-bit cache's kernels round token numbers up in ints.
 constexpr int kMaxFp8Tokens = 0x7fffffff - 8192;
-
-// Costs of the 8-bit decode's split, in eighths of a tile of up to four columns:
-// of a tile of 16 columns, and of opening a unit.
-constexpr int kFp8MostTileCost = 11;
-constexpr int kFp8UnitCost = 32;
 
 // Head vectors of a call's rows (attn_head_rows_t).
 struct HeadRows {

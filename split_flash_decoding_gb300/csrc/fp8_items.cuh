@@ -15,7 +15,8 @@
 // - 1), as the softmax of more columns takes longer (1 to 4 rows of 4 heads:
 // 1.58, 1.77, 1.89 and 2.11 us a tile), and every unit is preceded by kFp8UnitCost
 // (opening it: its queries, the pipeline refill, the epilogue).  Group c of C
-// takes the tiles that start in [c W / C, (c + 1) W / C), W the cost of all.
+// takes the tiles that start in [c W / C, (c + 1) W / C), W the cost of all; C is
+// such that every group inside a unit gets one of its tiles (fp8_split_groups).
 #pragma once
 
 #include "cache_ops.h"
@@ -26,7 +27,7 @@ namespace attn {
 struct Fp8Range {
     int x0, x1;            // this group's tiles of the concatenation
     int u0, u1;            // its first and last unit
-    int groups;            // C, after leaving out groups without tiles
+    int groups;            // C: groups that take part
     int cost;              // W
     __device__ __forceinline__ int count() const { return x1 > x0 ? u1 - u0 + 1 : 0; }
 };
@@ -42,21 +43,15 @@ __device__ __forceinline__ int fp8_tiles(uint32_t len, uint32_t cap) {
     return max(static_cast<int>((min(len, cap) + kGqaTcTileKeys - 1) / kGqaTcTileKeys), 1);
 }
 
-// First position of group c: c W / C, in 32 bits (c <= C, and C C fits).
-__device__ __forceinline__ int first_position(int c, int W, int C) {
-    const int q = W / C;
-    return c * q + c * (W - q * C) / C;
-}
-
 // By the number of head groups, which usually is 1 (an integer division is some
 // forty instructions, on the way to a CTA's first load).
 __device__ __forceinline__ int by_groups(int x, int hg) { return hg == 1 ? x : x / hg; }
 
 // Cost of a tile of sequence b.
 __device__ __forceinline__ int fp8_tile_cost(const Fp8DecodeParams &p, int b) {
-    if (!p.q_row_offsets) return 7 + (p.group + 3) / 4;
+    if (!p.q_row_offsets) return fp8_cost_of_columns(p.group);
     const int rows = static_cast<int>(p.q_row_offsets[b + 1] - p.q_row_offsets[b]);
-    return 7 + min(max((rows * p.group + 3) / 4, 1), 4);
+    return fp8_cost_of_columns(rows * p.group);
 }
 
 // cum[b].x: tiles of the concatenation before sequence b (head groups included),
@@ -69,13 +64,14 @@ __device__ __forceinline__ void fp8_build_items(const Fp8DecodeParams &p, int2 *
     const uint32_t cap = uint32_t(p.max_kv_len);
     const int per_lane = (p.batch + 31) / 32;
     const int b0 = min(lane * per_lane, p.batch), b1 = min(b0 + per_lane, p.batch);
-    int local = 0, cost = 0;
+    int local = 0, cost = 0, dearest = 1;      // (a lane without sequences: 1)
     for (int b = b0; b < b1; ++b) {
         const uint32_t len = p.kv_len[b];
         if (len > cap && blockIdx.x == 0 && warp == 0) atomicOr(p.err, kErrBadLength);
-        const int n = fp8_tiles(len, cap);
+        const int n = fp8_tiles(len, cap), tile = fp8_tile_cost(p, b);
         local += n * hg;
-        cost += hg * (n * fp8_tile_cost(p, b) + kFp8UnitCost);
+        cost += hg * (n * tile + kFp8UnitCost);
+        dearest = max(dearest, tile);
     }
     int incl = local, cost_incl = cost;
 #pragma unroll
@@ -101,7 +97,8 @@ __device__ __forceinline__ void fp8_build_items(const Fp8DecodeParams &p, int2 *
 
     const int T = __shfl_sync(0xffffffffu, incl, 31);
     const int W = __shfl_sync(0xffffffffu, cost_incl, 31);
-    const int C = min(static_cast<int>(gridDim.x) >> p.head_shift, T);
+    const int C = fp8_split_groups(static_cast<int>(gridDim.x) >> p.head_shift, T, W,
+                                   __reduce_max_sync(0xffffffffu, dearest));
     const int c = static_cast<int>(blockIdx.x) >> p.head_shift;
     const int w_lo = cost_incl - cost, w_hi = cost_incl;
     // First tile that starts at or after position y, and its unit; first: it
@@ -193,8 +190,7 @@ __device__ __forceinline__ int fp8_pieces(const Fp8DecodeParams &p, const int2 *
     const int tile = fp8_tile_cost(p, it.b);
     const int last =
         cum[it.b].y + (h + 1) * (it.unit_tiles * tile + kFp8UnitCost) - tile;
-    const int c_last =
-        static_cast<int>((static_cast<long long>(last + 1) * r.groups - 1) / r.cost);
+    const int c_last = group_of_position(last, r.cost, r.groups);
     return c_last - (static_cast<int>(blockIdx.x) >> p.head_shift) + 1;
 }
 

@@ -161,6 +161,20 @@ def test_draft_rows(attn, causal, hq, hkv, q_lens):
         attn, f"draft rows {q_lens}")
 
 
+@pytest.mark.parametrize("hq,hkv,q_lens,lens", [
+    (4, 1, [1, 4], [32000, 6900]), (32, 8, [1, 4], [2944, 768]), (4, 1, [4, 1], [2560, 35840]),
+    (8, 2, [4, 1, 1, 1], [4096] * 4)])
+def test_draft_rows_of_unequal_cost(attn, hq, hkv, q_lens, lens):
+    """About as many tiles as CTAs, some dearer than others.  The merge reads what the
+    partition kernel wrote and nothing else: the partial slots are NaN before the call
+    (the table of slots behind them, 8 bytes a sequence and KV head, is 0)."""
+    n = attn.attn_decode_fp8_workspace(len(lens), hq, hq // hkv)
+    ws = torch.full((n // 4,), float("nan"), device=DEV)
+    ws[n // 4 - 64 * -(-len(lens) * hkv * 8 // 256):] = 0
+    Case(lens, q_lens, hq=hq, hkv=hkv, page=128, block=64, seed=21, garbage=False).check(
+        attn, f"rows {q_lens} of {lens}", workspace=ws)
+
+
 def test_row_that_sees_nothing(attn):
     """Two rows of a sequence with one key, bottom aligned: the first sees none."""
     c = Case([1, 300], [2, 2], seed=8)
