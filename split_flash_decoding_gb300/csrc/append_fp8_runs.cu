@@ -66,7 +66,9 @@ append_fp8_runs_kernel(const __grid_constant__ RowsParams p, const __grid_consta
         }
     }
     __syncthreads();
-    if (!s_any || s_tile.first < 0) {          // (a group of tokens below 0 is stored nowhere)
+    // A group of tokens below 0 or past the bound is stored nowhere.  (A length of up to
+    // 2^32 - 1 may come; below the bound, tokens fit an int.)
+    if (!s_any || s_tile.first < 0 || s_tile.first >= p.max_kv_len) {
         pdl_wait_primary();
         return;
     }

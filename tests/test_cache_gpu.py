@@ -783,3 +783,37 @@ def test_append_fp8_more_rows_than_said(attn):
                             max_kv_len=100, max_q_len=4, page_table=pool.table.to(DEV),
                             q_row_offsets=torch.tensor([0, 40], dtype=torch.int32, device=DEV))
     assert attn.attn_device_error_flags(clear=True) == 4
+
+
+@pytest.mark.parametrize("kind", ["rows", "short", "runs", "large_blocks"])
+def test_lengths_past_31_bits(attn, kind):
+    """Lengths that no cache has (left-over memory, a -1): reported, nothing of theirs is read
+    from the page table or stored, and the sequence between them is as alone."""
+    n = 3 if kind == "short" else 70
+    lens = [-1, 100, -2 ** 31 + 5, 2 ** 31 - 1, -2 ** 31 + n // 2]     # as 32-bit patterns
+    table = torch.tensor([[5, 6], [2, 0], [7, 3], [8, 1], [4, 4]], dtype=torch.int32, device=DEV)
+    x = randn(31, 5 * n, 4, 128).to(DEV)
+    _, rope = rope_of(attn, 128)
+    block = 256 if kind == "large_blocks" else 16
+    page = max(64, block)
+
+    def go(seqs):
+        dt = torch.bfloat16 if kind == "rows" else FP8
+        c = [torch.zeros(9, page, 2, 128, dtype=dt, device=DEV) for _ in range(2)]
+        if kind != "rows":
+            c += [torch.ones(9, page // block, 2, device=DEV) for _ in range(2)]
+        append = attn.attn_append_kv if kind == "rows" else attn.attn_append_kv_fp8
+        rows = torch.cat([x[b * n:(b + 1) * n] for b in seqs])
+        append(rows[:, :2], rows[:, 2:], *c,
+               torch.tensor([lens[b] for b in seqs], dtype=torch.int32, device=DEV), max_kv_len=128,
+               page_table=table[torch.tensor(seqs, device=DEV)].contiguous(), rope=rope,
+               q_row_offsets=torch.arange(0, n * len(seqs) + 1, n, dtype=torch.int32, device=DEV),
+               **({} if kind == "rows" else {"max_q_len": n}))
+        torch.cuda.synchronize()
+        return c
+
+    got = go([0, 1, 2, 3, 4])
+    assert attn.attn_device_error_flags(clear=True) == 4
+    for a, b in zip(got, go([1])):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    assert got[0].view(torch.uint8).any() and attn.attn_device_error_flags(clear=True) == 0
