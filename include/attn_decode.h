@@ -604,7 +604,12 @@ int attn_append_kv_fp8(const attn_head_rows_t *q, const attn_head_rows_t *k,
  *               the GPU need one each.
  * The other arguments as for attn_decode (batch <= 2048), with this addition:
  * rows at or behind off[batch] belong to no sequence and are left as they are.
- * out and lse are those of attn_decode on the cache code * scale.  A code of NaN
+ * out and lse are those of attn_decode on the cache code * scale, but for how the
+ * weights p_j enter out.  Of the keys that one CTA takes of a sequence let u be the
+ * largest p_j 2^(e_j), e_j the exponent of the key's V scale.  p_j 2^(e_j) errs by at
+ * most 2^-13 of itself or 2^-29 u, whichever is more, and by no more than a sixteenth
+ * of itself down to 2^-35 u; below 2^-40 u it is left out of out (lse counts it).
+ * (attn_decode rounds each weight to bf16, 2^-9 of itself.)  A code of NaN
  * in a token makes the out of the rows that see it NaN (their lse is then
  * undefined) and of no others, whatever slots past a sequence's last token hold.
  * Launches the partition kernel and, for max_kv_len > 128, the split-K reduce.

@@ -19,8 +19,14 @@
 //   q = 2^-a (q0 + q1 / 16): a puts the row's largest channel in [128, 256);
 //     8 significant bits are two terms of 4, so bf16 channels down to 2^-14 of
 //     the largest are exact and smaller ones miss at most 2^-23 of it.
-//   weights = w0 + w1 / 16 + w2 / 256, each term the rest of the one before
-//     rounded to nearest: relative 2^-12.
+//   weights = w0 + 2^-5 w1 + 2^-10 w2 + 2^-25 w3, each term what those before leave,
+//     rounded to nearest.  e4m3 numbers end at 2^-9, so what terms hold of a small weight
+//     is bounded below: an error of at most 2^-13 of the weight, or 2^-29 of the piece's
+//     reference where that is more (a weight of 2^-20 of it keeps 9 bits, as in bf16),
+//     though never more than a sixteenth of a weight of 2^-35 and more; what is below
+//     2^-40 is lost.  The last term starts that low because the first three already hold
+//     the larger weights; it saturates there.  (Three terms 2^-4 apart dropped all below 2^-21: a key that takes
+//     nearly all the weight and has no V, 15 nats above 131072 others, left 0 of them.)
 // A thread owns one key of the tile (its TMEM lane), so the scales cost it two
 // multiplications: ks_j goes into the score, and V's scale into the weight.
 // With vs_j = r_j 2^(e_j) (e_j its exponent, clamped to [-64, 64]), the running
@@ -63,15 +69,19 @@ constexpr int kTileBytes = kBK * kD;         // 16 KB
 constexpr int kScStages = 6;                 // tiles of scales in flight
 constexpr int kQBufs = 2;
 constexpr int kCtasPerSm = 2;
-constexpr float kLazy = 4.f;                 // base 2
-constexpr float kWeightTop = 8.f;            // weights reach 2^kLazy * 2 * kWeightTop = 256
+// A lower kLazy leaves more of the e4m3 range below the reference, a higher one moves it
+// less often (kLazy 1, 2, 3, 4: 64 single rows 100 us each, 1 to 4 draft rows of 4 heads 107,
+// 98, 93, 92).
+constexpr float kLazy = 3.f;                 // base 2
+constexpr float kWeightTop = 16.f;           // weights reach 2^kLazy * 2 * kWeightTop = 256
+// Each term's unit over the next one's (see above).
+__host__ __device__ constexpr float term_ratio(int u) { return u < 2 ? 32.f : 32768.f; }
 constexpr int kBarBytes = 304;
 constexpr int kMinVExp = -64, kMaxVExp = 64;
 
 // Columns (query rows x heads) come in chunks of four: a chunk's S columns (and Q
-// rows) are [2 terms][4], its O columns (and P columns) [3 terms][4] and four
-// unused ones.  More than one chunk takes two groups of four softmax warps; group g
-// has the chunks g, g + 2.  Chunks past an item's columns are skipped.
+// rows) are [2 terms][4], its O columns (and P columns) [4 terms][4].  More than one
+// chunk takes two groups of four softmax warps; group g has the chunks g, g + 2.  Chunks past an item's columns are skipped.
 template <int NC>
 struct Cfg {
     static constexpr int kChunks = NC / 4;
@@ -141,7 +151,7 @@ __device__ __forceinline__ uint64_t smem_desc_plain(uint32_t saddr, uint32_t lbo
     return d;
 }
 
-// N (a multiple of 4) consecutive TMEM columns of the thread's lane.
+// N (a multiple of 8) consecutive TMEM columns of the thread's lane.
 template <int N>
 __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, float (&v)[N]) {
 #pragma unroll
@@ -150,12 +160,6 @@ __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, float (&v)[N]) {
         tc::tmem_ld_n<8>(taddr + i, a);
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[i + j] = a[j];
-    }
-    if constexpr (N % 8 != 0) {
-        float a[4];
-        tc::tmem_ld_n<4>(taddr + N - 4, a);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[N - 4 + j] = a[j];
     }
 }
 template <int N>
@@ -167,24 +171,19 @@ __device__ __forceinline__ void tmem_st_cols(uint32_t taddr, const float (&v)[N]
         for (int j = 0; j < 8; ++j) a[j] = v[i + j];
         tc::tmem_st_n<8>(taddr + i, a);
     }
-    if constexpr (N % 8 != 0) {
-        float a[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) a[j] = v[N - 4 + j];
-        tc::tmem_st_n<4>(taddr + N - 4, a);
-    }
 }
 
-// The three terms of two O columns side by side, four columns apart.
-__device__ __forceinline__ void tmem_ld_terms(uint32_t taddr, float (&a)[2], float (&b)[2],
-                                              float (&c)[2]) {
+// The four terms of two O columns side by side, four columns apart.
+__device__ __forceinline__ void tmem_ld_terms(uint32_t taddr, float (&o)[4][2]) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0, %1}, [%6];\n\t"
-        "tcgen05.ld.sync.aligned.32x32b.x2.b32 {%2, %3}, [%7];\n\t"
-        "tcgen05.ld.sync.aligned.32x32b.x2.b32 {%4, %5}, [%8];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0, %1}, [%8];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x2.b32 {%2, %3}, [%9];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x2.b32 {%4, %5}, [%10];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x2.b32 {%6, %7}, [%11];\n\t"
         "tcgen05.wait::ld.sync.aligned;"
-        : "=&f"(a[0]), "=&f"(a[1]), "=&f"(b[0]), "=&f"(b[1]), "=&f"(c[0]), "=&f"(c[1])
-        : "r"(taddr), "r"(taddr + 4), "r"(taddr + 8)
+        : "=&f"(o[0][0]), "=&f"(o[0][1]), "=&f"(o[1][0]), "=&f"(o[1][1]), "=&f"(o[2][0]),
+          "=&f"(o[2][1]), "=&f"(o[3][0]), "=&f"(o[3][1])
+        : "r"(taddr), "r"(taddr + 4), "r"(taddr + 8), "r"(taddr + 12)
         : "memory");
 }
 
@@ -234,14 +233,13 @@ __device__ __forceinline__ float pow2i(int e) {   // -126 <= e <= 127
 __device__ __forceinline__ uint32_t to_e4m3x2(float a, float b) {
     return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
 }
-// 16 times what two codes leave of (a, b), given 16 a and 16 b: exact products in
-// a mixed-precision FMA, no unpacking.
-__device__ __forceinline__ void rest16(uint32_t c, float &a16, float &b16) {
+// What two codes leave of (a, b): exact, in a mixed-precision FMA, no unpacking.
+__device__ __forceinline__ void take_rest(uint32_t c, float &a, float &b) {
     const __half2_raw h =
         __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(c), __NV_E4M3);
-    const unsigned short minus16 = 0xcc00;   // f16
-    asm("fma.rn.f32.f16 %0, %1, %2, %0;" : "+f"(a16) : "h"(h.x), "h"(minus16));
-    asm("fma.rn.f32.f16 %0, %1, %2, %0;" : "+f"(b16) : "h"(h.y), "h"(minus16));
+    const unsigned short minus1 = 0xbc00;   // f16
+    asm("fma.rn.f32.f16 %0, %1, %2, %0;" : "+f"(a) : "h"(h.x), "h"(minus1));
+    asm("fma.rn.f32.f16 %0, %1, %2, %0;" : "+f"(b) : "h"(h.y), "h"(minus1));
 }
 
 // Byte of element (row r, byte c) of an operand of 128-byte rows, 128-byte swizzle.
@@ -422,8 +420,8 @@ __device__ __forceinline__ void feed(const Fp8DecodeParams &p, const int2 *cum, 
                 if (!(fabsf(x[k].x) < INFINITY)) x[k].x = __uint_as_float(0x7fffffffu);
                 if (!(fabsf(x[k].y) < INFINITY)) x[k].y = __uint_as_float(0x7fffffffu);
                 const uint32_t h = to_e4m3x2(x[k].x, x[k].y);
+                take_rest(h, x[k].x, x[k].y);
                 x[k] = __fmul2_rn(x[k], make_float2(16.f, 16.f));
-                rest16(h, x[k].x, x[k].y);
                 const uint32_t l = to_e4m3x2(x[k].x, x[k].y);
                 hi[k >> 1] = k & 1 ? hi[k >> 1] | (h << 16) : h;
                 lo[k >> 1] = k & 1 ? lo[k >> 1] | (l << 16) : l;
@@ -745,7 +743,7 @@ gqa_decode_fp8_kernel(const __grid_constant__ Fp8DecodeParams p) {
                         }
                     }
                 }
-                uint32_t code[NCH][3];   // four columns of a term to a word
+                uint32_t code[NCH][4];   // four columns of a term to a word
 #pragma unroll
                 for (int h = 0; h < NCH; ++h) {
                     if (col(h) >= cols) continue;
@@ -757,15 +755,16 @@ gqa_decode_fp8_kernel(const __grid_constant__ Fp8DecodeParams p) {
                         w[c] = __fmul2_rn(e, make_float2(v_mul, v_mul));
                     }
 #pragma unroll
-                    for (int u = 0; u < 3; ++u) {
+                    for (int u = 0; u < 4; ++u) {
                         const uint32_t lo = to_e4m3x2(w[0].x, w[0].y);
                         const uint32_t hi = to_e4m3x2(w[1].x, w[1].y);
                         code[h][u] = lo | (hi << 16);
-                        if (u < 2) {
-                            w[0] = __fmul2_rn(w[0], make_float2(16.f, 16.f));
-                            w[1] = __fmul2_rn(w[1], make_float2(16.f, 16.f));
-                            rest16(lo, w[0].x, w[0].y);
-                            rest16(hi, w[1].x, w[1].y);
+                        if (u < 3) {
+                            take_rest(lo, w[0].x, w[0].y);
+                            take_rest(hi, w[1].x, w[1].y);
+                            const float2 ratio = make_float2(term_ratio(u), term_ratio(u));
+                            w[0] = __fmul2_rn(w[0], ratio);
+                            w[1] = __fmul2_rn(w[1], ratio);
                         }
                     }
                 }
@@ -778,15 +777,15 @@ gqa_decode_fp8_kernel(const __grid_constant__ Fp8DecodeParams p) {
 #pragma unroll
                         for (int h = 0; h < NCH; ++h) {
                             if (col(h) >= cols) continue;
-                            float o[12];
+                            float o[16];
                             const uint32_t oc = tmem + lane_base + C::kTmemO + 4 * col(h);
-                            tmem_ld_cols<12>(oc, o);
+                            tmem_ld_cols<16>(oc, o);
 #pragma unroll
-                            for (int c = 0; c < 12; c += 2) {
+                            for (int c = 0; c < 16; c += 2) {
                                 o[c] *= alpha[h][(c >> 1) & 1].x;
                                 o[c + 1] *= alpha[h][(c >> 1) & 1].y;
                             }
-                            tmem_st_cols<12>(oc, o);
+                            tmem_st_cols<16>(oc, o);
                         }
                         tc::tmem_wait_st();
                     }
@@ -830,7 +829,7 @@ gqa_decode_fp8_kernel(const __grid_constant__ Fp8DecodeParams p) {
                 for (int h = 0; h < NCH; ++h)
                     if (col(h) < cols)
                         *reinterpret_cast<uint4 *>(smem + C::p + 4 * col(h) * kBK + 16 * k) =
-                            make_uint4(code[h][0], code[h][1], code[h][2], 0u);
+                            make_uint4(code[h][0], code[h][1], code[h][2], code[h][3]);
                 tc::fence_async_smem();
                 tc::fence_before_sync();
                 __syncwarp();
@@ -882,14 +881,16 @@ gqa_decode_fp8_kernel(const __grid_constant__ Fp8DecodeParams p) {
             for (int x = 0; x < 4 * NCH; x += 2) {
                 const int c0 = col(x >> 2) + (x & 3);
                 if (c0 >= cols) break;
-                float o0[2], o1[2], o2[2];
-                tmem_ld_terms(tmem + lane_base + C::kTmemO + 4 * (c0 & ~3) + (c0 & 3), o0, o1, o2);
+                float term[4][2];
+                tmem_ld_terms(tmem + lane_base + C::kTmemO + 4 * (c0 & ~3) + (c0 & 3), term);
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     const int cg = c0 + u, i = (cg * g_inv) >> 16;
                     if (i >= nrows) continue;
-                    const float acc = has_o ? fmaf(fmaf(o2[u], 0.0625f, o1[u]), 0.0625f, o0[u]) *
-                                                  (1.f / kWeightTop) : 0.f;
+                    float acc = term[3][u];
+#pragma unroll
+                    for (int v = 2; v >= 0; --v) acc = fmaf(acc, 1.f / term_ratio(v), term[v][u]);
+                    acc = has_o ? acc * (1.f / kWeightTop) : 0.f;
                     const float lsum = (lb[cg] + lb[16 + cg]) + (lb[32 + cg] + lb[48 + cg]);
                     // no visible key: no sum, no reference
                     const float mx = lsum == 0.f ? -INFINITY : lb[64 + cg];

@@ -175,6 +175,58 @@ def test_draft_rows_of_unequal_cost(attn, hq, hkv, q_lens, lens):
         attn, f"rows {q_lens} of {lens}", workspace=ws)
 
 
+def weight_error(w):
+    """Bound of |four e4m3 terms of w - w|, w = 16 at a weight of 1 with V scale mantissa 1
+    (tests/test_fp8_weight_terms.py)."""
+    return torch.maximum(2.0 ** -13 * w, torch.minimum(torch.full_like(w, 2.0 ** -25),
+                                                       (2.0 ** -4 * w).clamp_min(2.0 ** -35)))
+
+
+@pytest.mark.parametrize("n,batch", [(128, 1), (1000, 3), (4096, 304), (131072, 1), (131072, 304)])
+@pytest.mark.parametrize("where", ["first", "middle", "last"])
+@pytest.mark.parametrize("spread", [0, 6])
+def test_one_key_far_above_the_rest(attn, n, batch, where, spread):
+    """A key 10 to 20 nats above the others whose V is 0: the output is what the small weights
+    leave.  304 sequences (of one set of pages) on one KV head: a piece holds a whole one.
+
+    Beside the roundings at the top of this file, per key: the weight's terms (weight_error,
+    relative to the largest p_i 2^(e_i), e_i the exponent of the key's V scale), and the
+    accumulator's roundings, one step 2^-23 of what it holds for each of n / 32 products."""
+    g = torch.Generator(device=DEV).manual_seed(n + spread)
+    page, block, hq = 128, 64, 4
+    pages = -(-n // page)
+    k = torch.zeros(pages, page, 1, 128, device=DEV)
+    k[..., 0] = torch.randint(-4, 5, (pages, page, 1), generator=g, device=DEV) / 16.0
+    v = torch.rand(pages, page, 1, 128, generator=g, device=DEV) * 400 + 40
+    at = {"first": 0, "middle": n // 2, "last": n - 1}[where]
+    k.view(-1, 128)[at, 0] = 20.0
+    v.view(-1, 128)[at] = 0.0
+    kc, vc = k.to(FP8), v.to(FP8)
+    ks = torch.ones(pages, page // block, 1, device=DEV)
+    vs = 1.3 * torch.exp2(-torch.randint(0, spread + 1, ks.shape, generator=g, device=DEV).float())
+    q = torch.zeros(batch, hq, 128, dtype=torch.bfloat16, device=DEV)
+    q[:, :, 0] = torch.tensor([0.5, 0.625, 0.75, 1.0])                # 10 to 20 nats
+    table = torch.arange(pages, dtype=torch.int32, device=DEV).expand(batch, pages).contiguous()
+    lens = torch.full((batch,), n, dtype=torch.int32, device=DEV)
+    out, lse = attn.attn_decode_fp8(q, kc, vc, ks, vs, lens, group=hq, scale=1.0, max_kv_len=n,
+                                    page_table=table)
+    codes = vc.double().view(-1, 128)[:n]
+    vscale = vs.double().repeat_interleave(block, 1).view(-1)[:n]
+    scores = q[0, :, :1].double() * kc.double().view(-1, 128)[:n, 0]   # [heads, n]
+    el = torch.logsumexp(scores, -1)
+    p = torch.exp(scores - el[:, None])
+    exact = (p * vscale) @ codes
+    rho = 2.0 ** -16 * 20 + 2.0 ** -20
+    e2 = torch.exp2(torch.floor(torch.log2(vscale)))                  # 2^(e_j)
+    unit = (p * e2).amax(-1, keepdim=True) / 16                       # of w
+    terms = (weight_error(p * vscale / unit) * unit) @ codes
+    bound = R.BF16_HALF * exact + 1.01 * (terms + (2.0 ** -20 + 4 * rho + n / 32 * 2.0 ** -23) *
+                                          exact)
+    worst = ((out.double() - exact).abs() / bound).max().item()
+    assert worst <= 1, f"{worst:.3g} times the bound"
+    assert (lse.double() - el).abs().max() <= rho + 2.0 ** -20 * 20
+
+
 def test_row_that_sees_nothing(attn):
     """Two rows of a sequence with one key, bottom aligned: the first sees none."""
     c = Case([1, 300], [2, 2], seed=8)
