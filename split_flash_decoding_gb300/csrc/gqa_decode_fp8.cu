@@ -797,10 +797,11 @@ gqa_decode_fp8_kernel(const __grid_constant__ Fp8DecodeParams p) {
                     uint4 *row = reinterpret_cast<uint4 *>(smem + C::vring + vs * kTileBytes) + k * 8;
                     bool clear = t0 + k >= it.L;     // past the end: may hold anything
                     if (t0 + k >= full && t0 + k < it.L) {
-                        // A later token of the call: a NaN in its V must not reach the
-                        // rows before it through 0 * NaN.  Its V becomes 0 and its
-                        // weight NaN for the rows that do see it.
-                        bool nan = false;
+                        // A later token of the call: a NaN in its V, or a scale that counts
+                        // as NaN, must not reach the rows before it through 0 * NaN.  Its V
+                        // becomes 0, and its weight NaN for the rows that see it and 0 for
+                        // the others.
+                        bool nan = v_mul != v_mul;
 #pragma unroll
                         for (int u = 0; u < 8; ++u) {
                             const uint4 x = row[u];
@@ -814,9 +815,14 @@ gqa_decode_fp8_kernel(const __grid_constant__ Fp8DecodeParams p) {
 #pragma unroll
                             for (int h = 0; h < NCH; ++h)
 #pragma unroll
-                                for (int c = 0; c < 4; ++c)
-                                    if (col(h) < cols && sees(col(h) + c, t0 + k))
-                                        code[h][0] |= 0x7fu << (8 * c);
+                                for (int c = 0; c < 4; ++c) {
+                                    if (col(h) >= cols) continue;
+                                    const bool seen = sees(col(h) + c, t0 + k);
+#pragma unroll
+                                    for (int u = 0; u < 4; ++u)
+                                        code[h][u] &= ~(0xffu << (8 * c));
+                                    code[h][0] |= (seen ? 0x7fu : 0u) << (8 * c);
+                                }
                         }
                     }
                     named_sync(3, 128 * C::kGroups);

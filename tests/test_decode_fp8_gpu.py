@@ -332,6 +332,18 @@ def test_calls_on_two_streams_at_once(attn):
         assert torch.equal(o, want[i % 2])
 
 
+@pytest.mark.parametrize("hq", [4, 8])
+def test_v_scale_past_the_range_of_a_later_token(attn, hq):
+    """It counts as NaN for the rows that see its token and for no others."""
+    c = Case([300, 300], [2, 1], hq=hq, hkv=1, block=1, seed=22)
+    clean, _ = c.run(attn)
+    pg, slot = c.place(0, 299)                                # seen by row 1
+    c.caches[1][1][pg, slot] = 2.0 ** 66
+    out, _ = c.run(attn)
+    assert torch.equal(out[0], clean[0]) and torch.equal(out[2], clean[2])
+    assert out[1].isnan().all()
+
+
 def test_v_scale_past_the_range_is_not_silent(attn):
     c = Case([200], seed=18, garbage=False, block=64)
     c.caches[1][1][int(c.table[0, 1])] = 2.0 ** 66
