@@ -645,7 +645,8 @@ def attn_append_kv(k: torch.Tensor, v: Optional[torch.Tensor], k_cache: torch.Te
 
 def attn_append_kv_fp8(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
                        v_cache: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
-                       kv_len: torch.Tensor, *, max_kv_len: int, max_q_len: int = 1,
+                       kv_len: torch.Tensor, *, max_kv_len: int,
+                       max_q_len: Optional[int] = None,
                        page_table: Optional[torch.Tensor] = None,
                        q: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
                        q_row_offsets: Optional[torch.Tensor] = None,
@@ -654,10 +655,14 @@ def attn_append_kv_fp8(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
                        k_norm: Optional[torch.Tensor] = None, eps: float = 1e-6, stream=None):
     """attn_append_kv into caches of torch.float8_e4m3fn with fp32 scales
     [pages, page_size / block_tokens, num_kv_heads] (attn_append_kv_fp8), head
-    dimension 128.  max_q_len bounds the rows of any sequence.  Returns q_out."""
+    dimension 128.  max_q_len bounds the rows of any sequence; by default, with
+    q_row_offsets, it is all rows (right, but a call of short runs is faster with its
+    own bound).  Returns q_out."""
     q_out, head, tail, device = _append_args(k, v, k_cache, v_cache, kv_len, page_table, q, q_out,
                                              q_row_offsets, rope, positions, q_norm, k_norm, eps,
                                              torch.float8_e4m3fn, k_scale, v_scale)
+    if max_q_len is None:
+        max_q_len = 1 if q_row_offsets is None else max(k.shape[0], 1)
     _check("attn_append_kv_fp8",
            lib().attn_append_kv_fp8(*head, *_scale_pair(k_scale, v_scale, k_cache.shape,
                                                        v_cache.shape), *tail,
@@ -683,14 +688,16 @@ def attn_decode_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
                     group: int, scale: float, max_kv_len: int,
                     page_table: Optional[torch.Tensor] = None,
                     sink: Optional[torch.Tensor] = None,
-                    q_row_offsets: Optional[torch.Tensor] = None, max_q_len: int = 1,
+                    q_row_offsets: Optional[torch.Tensor] = None,
+                    max_q_len: Optional[int] = None,
                     causal: bool = False, workspace: Optional[torch.Tensor] = None,
                     out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
                     return_lse: bool = True, stream=None):
     """Decode attention over caches of torch.float8_e4m3fn with fp32 scales
     [pages, page_size / block_tokens, num_kv_heads] through attn_decode_fp8:
     one row, or a few (max_q_len * group <= 16), per sequence, head dimension
-    128; everything else as for attn_decode.  Returns (out, lse)."""
+    128; everything else as for attn_decode.  max_q_len is by default, with
+    q_row_offsets, the most that a call may have.  Returns (out, lse)."""
     rows, hq, d = q.shape
     batch = kv_len.shape[0]
     kd, vd = _kv_pair(k_cache, v_cache, page_table, torch.float8_e4m3fn)
@@ -717,6 +724,8 @@ def attn_decode_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     elif lse is not None and (lse.dtype != torch.float32 or lse.shape != (rows, hq) or
                               not lse.is_contiguous()):
         raise ValueError("lse must be contiguous fp32 [rows, num_q_heads]")
+    if max_q_len is None:
+        max_q_len = 1 if q_row_offsets is None or group < 1 else max(min(rows, 16 // group), 1)
     device = _on_current_device(q, k_cache, v_cache, k_scale, v_scale, kv_len, page_table, sink,
                                 q_row_offsets, workspace, out, lse)
     need = 0 if max_kv_len <= 128 else _fp8_workspace(device, batch, hq, group)

@@ -817,3 +817,24 @@ def test_lengths_past_31_bits(attn, kind):
     for a, b in zip(got, go([1])):
         assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
     assert got[0].view(torch.uint8).any() and attn.attn_device_error_flags(clear=True) == 0
+
+
+@pytest.mark.parametrize("q_lens", [[40, 1, 7], [1, 1, 1], [20, 1, 20]])
+def test_append_fp8_rows_without_a_bound(attn, q_lens):
+    """q_row_offsets without max_q_len: every row is stored."""
+    lens = [100, 1, 50]
+    pool = Pool(lens, 64, 1)
+    rows = sum(q_lens)
+    k, v = randn(2, rows, 2, 128).to(DEV), randn(3, rows, 2, 128).to(DEV)
+    offs = torch.tensor([sum(q_lens[:i]) for i in range(4)], dtype=torch.int32, device=DEV)
+
+    def go(**kw):
+        c = fresh8(pool)
+        attn.attn_append_kv_fp8(k, v, *c, torch.tensor(lens, dtype=torch.int32, device=DEV),
+                                max_kv_len=100, page_table=pool.table.to(DEV), q_row_offsets=offs,
+                                **kw)
+        return c
+
+    for a, b in zip(go(), go(max_q_len=max(q_lens))):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    assert attn.attn_device_error_flags(clear=True) == 0

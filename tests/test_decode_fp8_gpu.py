@@ -411,6 +411,16 @@ def test_more_rows_than_said(attn):
     assert attn.attn_device_error_flags(clear=True) == 4
 
 
+@pytest.mark.parametrize("hq,hkv,q_lens", [(8, 2, [4, 1, 3]), (16, 1, [1, 1, 1]), (2, 2, [16, 2, 1])])
+def test_rows_without_a_bound(attn, hq, hkv, q_lens):
+    """q_row_offsets without max_q_len: all rows all the same."""
+    c = Case([300, 40, 77], q_lens, hq=hq, hkv=hkv, seed=23)
+    want = c.check(attn, "bound given")
+    got = c.check(attn, "no bound", max_q_len=None)
+    if hq // hkv * max(q_lens) > 8:                # the same kernel
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_append_then_decode(attn):
     """A prompt and then single tokens, appended and attended to: against attention over the
     values that the cache holds, step by step."""
