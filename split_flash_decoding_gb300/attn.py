@@ -4,8 +4,11 @@ Every step of the attention path runs in the library's CUDA kernels; this
 module converts torch tensors into the pointers, sizes and cache
 descriptors that the C ABI (include/attn_decode.h) takes, and turns
 non-zero status codes into exceptions.  PyTorch supplies device memory
-(including the split-K workspace) and the current stream.  There is no CPU
-fallback: if libattn.so has not been built, importing the library fails.
+(including the split-K workspace) and the current stream.  With stream= the
+call runs there, and what it allocates belongs there; its inputs have to be
+ready for that stream, and the caller waits for it before using the outputs
+on another.  There is no CPU fallback: if libattn.so has not been built,
+importing the library fails.
 """
 from __future__ import annotations
 
@@ -374,11 +377,29 @@ def attn_plan_partitions(batch: int, num_q_rows: int, num_q_heads: int, num_kv_h
     return P.value, ws.value
 
 
-def _workspace(nbytes: int, device, workspace: Optional[torch.Tensor]):
+def _empty(shape, dtype: torch.dtype, device: torch.device, stream, returned: bool = True):
+    """Memory for a call on `stream` (None: the current one).
+
+    The allocator hands a freed block to the next request of the stream it came
+    from, in that stream's order.  So what a call on another stream uses is taken
+    there; what it returns may be used on the current stream as well."""
+    if stream is None or device.type != "cuda":
+        return torch.empty(shape, dtype=dtype, device=device)
+    current = torch.cuda.current_stream(device)
+    if stream.cuda_stream == current.cuda_stream:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if returned:
+        t.record_stream(current)
+    return t
+
+
+def _workspace(nbytes: int, device, workspace: Optional[torch.Tensor], stream):
     if nbytes == 0:
         return None, 0
     if workspace is None:
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        workspace = _empty(nbytes, torch.uint8, device, stream, returned=False)
     return workspace, workspace.numel() * workspace.element_size()
 
 
@@ -403,12 +424,12 @@ def attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     rows, hq, d = q.shape
     batch = kv_len.shape[0]
     if out is None:
-        out = torch.empty((rows, hq, d), dtype=torch.bfloat16, device=q.device)
+        out = _empty((rows, hq, d), torch.bfloat16, q.device, stream)
     if lse is None and return_lse:
-        lse = torch.empty((rows, hq), dtype=torch.float32, device=q.device)
+        lse = _empty((rows, hq), torch.float32, q.device, stream)
     P, ws_bytes = attn_plan_partitions(batch, rows, hq, hq // group, d, max_kv_len,
                                        num_partitions, max_q_len=max_q_len)
-    ws, ws_size = _workspace(ws_bytes, q.device, workspace)
+    ws, ws_size = _workspace(ws_bytes, q.device, workspace, stream)
     kd = kv_descriptor(k_cache, page_table)
     vd = kv_descriptor(v_cache, page_table)
     _check("attn_decode",
@@ -432,11 +453,11 @@ def attn_mla_decode(q: torch.Tensor, kv_cache: torch.Tensor, kv_len: torch.Tenso
     _sparse variants)."""
     batch, hq, dqk = q.shape
     if out is None:
-        out = torch.empty((batch, hq, dim_v), dtype=torch.bfloat16, device=q.device)
+        out = _empty((batch, hq, dim_v), torch.bfloat16, q.device, stream)
     if lse is None and return_lse:
-        lse = torch.empty((batch, hq), dtype=torch.float32, device=q.device)
+        lse = _empty((batch, hq), torch.float32, q.device, stream)
     P, ws_bytes = attn_plan_partitions(batch, batch, hq, 1, dim_v, max_kv_len, num_partitions)
-    ws, ws_size = _workspace(ws_bytes, q.device, workspace)
+    ws, ws_size = _workspace(ws_bytes, q.device, workspace, stream)
     kd = kv_descriptor(kv_cache, page_table)
     _check("attn_mla_decode",
            lib().attn_mla_decode(q.data_ptr(), ctypes.byref(kd), kv_len.data_ptr(), batch, hq, dqk,
@@ -462,11 +483,11 @@ def attn_mla_decode_rows(q: torch.Tensor, kv_cache: torch.Tensor, kv_len: torch.
     if q_row_offsets.shape[0] != batch + 1:
         raise ValueError("q_row_offsets must have batch + 1 entries")
     if out is None:
-        out = torch.empty((rows, hq, dim_v), dtype=torch.bfloat16, device=q.device)
+        out = _empty((rows, hq, dim_v), torch.bfloat16, q.device, stream)
     if lse is None and return_lse:
-        lse = torch.empty((rows, hq), dtype=torch.float32, device=q.device)
+        lse = _empty((rows, hq), torch.float32, q.device, stream)
     P, ws_bytes = attn_plan_partitions(batch, rows, hq, 1, dim_v, max_kv_len, num_partitions)
-    ws, ws_size = _workspace(ws_bytes, q.device, workspace)
+    ws, ws_size = _workspace(ws_bytes, q.device, workspace, stream)
     kd = kv_descriptor(kv_cache, page_table)
     _check("attn_mla_decode_rows",
            lib().attn_mla_decode_rows(q.data_ptr(), ctypes.byref(kd), kv_len.data_ptr(),
@@ -495,11 +516,11 @@ def attn_mla_decode_sparse(q: torch.Tensor, kv_cache: torch.Tensor, indices: tor
         raise ValueError("indices and topk_lengths need one row per sequence")
     stride = indices.shape[1]
     if out is None:
-        out = torch.empty((batch, hq, dim_v), dtype=torch.bfloat16, device=q.device)
+        out = _empty((batch, hq, dim_v), torch.bfloat16, q.device, stream)
     if lse is None and return_lse:
-        lse = torch.empty((batch, hq), dtype=torch.float32, device=q.device)
+        lse = _empty((batch, hq), torch.float32, q.device, stream)
     P, ws_bytes = attn_plan_partitions(batch, batch, hq, 1, dim_v, stride, num_partitions)
-    ws, ws_size = _workspace(ws_bytes, q.device, workspace)
+    ws, ws_size = _workspace(ws_bytes, q.device, workspace, stream)
     kd = kv_descriptor(kv_cache)
     _check("attn_mla_decode_sparse",
            lib().attn_mla_decode_sparse(q.data_ptr(), ctypes.byref(kd), indices.data_ptr(), stride,
@@ -518,9 +539,9 @@ def attn_splitk_reduce(ws_o: torch.Tensor, ws_m: torch.Tensor, ws_l: torch.Tenso
         if t.dtype != torch.float32 or not t.is_contiguous():
             raise ValueError("partials must be contiguous fp32")
     if out is None:
-        out = torch.empty((rows, hq, dv), dtype=torch.bfloat16, device=ws_o.device)
+        out = _empty((rows, hq, dv), torch.bfloat16, ws_o.device, stream)
     if lse is None:
-        lse = torch.empty((rows, hq), dtype=torch.float32, device=ws_o.device)
+        lse = _empty((rows, hq), torch.float32, ws_o.device, stream)
     _check("attn_splitk_reduce",
            lib().attn_splitk_reduce(ws_o.data_ptr(), ws_m.data_ptr(), ws_l.data_ptr(), P, rows,
                                     hq, dv, _ptr(sink), out.data_ptr(), _ptr(lse),
@@ -566,9 +587,9 @@ def attn_qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor] = None,
     if k is not None and k.shape[0] != rows:
         raise ValueError("q and k must have the same rows")
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        q_out = _empty(q.shape, torch.bfloat16, q.device, stream)
     if k_out is None and k is not None:
-        k_out = torch.empty(k.shape, dtype=torch.bfloat16, device=k.device)
+        k_out = _empty(k.shape, torch.bfloat16, k.device, stream)
     start = 0 if rope is None else rope.start
     qd = _head_rows(q, q.shape, q_out, q_norm, eps, start)
     kd = None if k is None else _head_rows(k, k.shape, k_out, k_norm, eps, start)
@@ -582,7 +603,7 @@ def attn_qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor] = None,
 
 
 def _append_args(k, v, k_cache, v_cache, kv_len, page_table, q, q_out, q_row_offsets, rope,
-                 positions, q_norm, k_norm, eps, dtype, *scales):
+                 positions, q_norm, k_norm, eps, stream, dtype, *scales):
     k_shape, kc_shape, batch = k.shape, k_cache.shape, kv_len.shape[0]
     rows = k_shape[0]
     if (v is None) != (v_cache is None):
@@ -598,7 +619,7 @@ def _append_args(k, v, k_cache, v_cache, kv_len, page_table, q, q_out, q_row_off
         if q_shape[0] != rows:
             raise ValueError("q, k and v must have the same rows")
         if q_out is None:
-            q_out = torch.empty(q_shape, dtype=torch.bfloat16, device=q.device)
+            q_out = _empty(q_shape, torch.bfloat16, q.device, stream)
         qd = _head_rows(q, q_shape, q_out, q_norm, eps, start)
     kd = _head_rows(k, k_shape, None, k_norm, eps, start)
     if v is None:
@@ -637,7 +658,7 @@ def attn_append_kv(k: torch.Tensor, v: Optional[torch.Tensor], k_cache: torch.Te
     are normed (q_norm, k_norm) and rotated (rope) on the way.  Returns q_out."""
     q_out, head, tail, device = _append_args(k, v, k_cache, v_cache, kv_len, page_table, q, q_out,
                                              q_row_offsets, rope, positions, q_norm, k_norm, eps,
-                                             torch.bfloat16)
+                                             stream, torch.bfloat16)
     _check("attn_append_kv",
            lib().attn_append_kv(*head, *tail, max_kv_len, _stream_of(stream, device)))
     return q_out
@@ -660,7 +681,7 @@ def attn_append_kv_fp8(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
     own bound).  Returns q_out."""
     q_out, head, tail, device = _append_args(k, v, k_cache, v_cache, kv_len, page_table, q, q_out,
                                              q_row_offsets, rope, positions, q_norm, k_norm, eps,
-                                             torch.float8_e4m3fn, k_scale, v_scale)
+                                             stream, torch.float8_e4m3fn, k_scale, v_scale)
     if max_q_len is None:
         max_q_len = 1 if q_row_offsets is None else max(k.shape[0], 1)
     _check("attn_append_kv_fp8",
@@ -716,11 +737,11 @@ def attn_decode_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
                              not sink.is_contiguous()):
         raise ValueError("sink must be contiguous fp32 [num_q_heads]")
     if out is None:
-        out = torch.empty((rows, hq, d), dtype=torch.bfloat16, device=q.device)
+        out = _empty((rows, hq, d), torch.bfloat16, q.device, stream)
     elif out.dtype != torch.bfloat16 or out.shape != q.shape or not out.is_contiguous():
         raise ValueError("out must be contiguous bf16, shaped as q")
     if lse is None and return_lse:
-        lse = torch.empty((rows, hq), dtype=torch.float32, device=q.device)
+        lse = _empty((rows, hq), torch.float32, q.device, stream)
     elif lse is not None and (lse.dtype != torch.float32 or lse.shape != (rows, hq) or
                               not lse.is_contiguous()):
         raise ValueError("lse must be contiguous fp32 [rows, num_q_heads]")
@@ -729,7 +750,7 @@ def attn_decode_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     device = _on_current_device(q, k_cache, v_cache, k_scale, v_scale, kv_len, page_table, sink,
                                 q_row_offsets, workspace, out, lse)
     need = 0 if max_kv_len <= 128 else _fp8_workspace(device, batch, hq, group)
-    ws, ws_size = _workspace(need, q.device, workspace)
+    ws, ws_size = _workspace(need, q.device, workspace, stream)
     _check("attn_decode_fp8",
            lib().attn_decode_fp8(q.data_ptr(), kd, vd, ks, vs, lens, offs, batch, rows, hq, group,
                                  d, max_q_len, max_kv_len, scale, _ptr(sink),
