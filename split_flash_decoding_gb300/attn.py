@@ -726,8 +726,8 @@ def attn_decode_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     ks, vs = _scale_pair(k_scale, v_scale, k_shape, v_shape)
     if q.dtype != torch.bfloat16 or not q.is_contiguous():
         raise ValueError("q must be contiguous bf16 [rows, num_q_heads, 128]")
-    if k_shape[2:] != v_shape[2:] or k_shape[2] * group != hq:
-        raise ValueError(f"{hq} query heads in groups of {group} do not fit caches "
+    if k_shape[2:] != v_shape[2:] or k_shape[2] * group != hq or k_shape[3] != d:
+        raise ValueError(f"{hq} query heads of {d} in groups of {group} do not fit caches "
                          f"{tuple(k_shape)} and {tuple(v_shape)}")
     if page_table is not None and page_table.shape[0] != batch:
         raise ValueError("page_table must have one row per sequence")

@@ -316,6 +316,17 @@ def test_binding_refuses_wrong_tensors(attn):
                              page_table=table, workspace=torch.zeros(8, dtype=torch.uint8))
 
 
+def test_decode_fp8_refuses_caches_of_other_channels(attn):
+    """Heads of 64 channels, or views of the first 128 of 256: not read as heads of 128."""
+    q = torch.zeros(2, 4, 128, dtype=torch.bfloat16)
+    lens = torch.ones(2, dtype=torch.int32)
+    s = torch.ones(2, 4, 1)
+    for dim, base in ((64, 64), (64, 128), (256, 256)):
+        c = torch.zeros(2, 64, 1, base, dtype=torch.bfloat16).to(torch.float8_e4m3fn)[..., :dim]
+        with pytest.raises(ValueError, match="do not fit caches"):
+            attn.attn_decode_fp8(q, c, c, s, s, lens, group=4, scale=1.0, max_kv_len=64)
+
+
 def test_packed_descriptors_are_the_structures(attn):
     """The binding packs descriptors; their bytes are those of the C structures."""
     n = [0x1111111111111000 + 16 * i for i in range(8)]
