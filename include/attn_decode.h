@@ -484,7 +484,8 @@ enum {
  *               ignored.
  *   turns       out, host [rot_dim / 2]; copy it to the device.
  *   mscale      out, host, or NULL.
- * Returns ATTN_OK or ATTN_ERR_INVALID_ARG.  Launches nothing.
+ * Returns ATTN_OK or ATTN_ERR_INVALID_ARG (also where a frequency overflows).
+ * Launches nothing.
  */
 int attn_rope_turns(int rot_dim, double theta, int scaling, double factor, double original_len,
                     double low, double high, uint64_t *turns, float *mscale);

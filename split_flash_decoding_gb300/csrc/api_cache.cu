@@ -216,6 +216,7 @@ extern "C" int attn_rope_turns(int rot_dim, double theta, int scaling, double fa
             const double x = std::fmin(1.0, std::fmax(0.0, (n - low) / (high - low)));
             f = (1.0 - x) * f / factor + x * f;
         }
+        if (!std::isfinite(f)) return ATTN_ERR_INVALID_ARG;
         double t = f / two_pi;
         t -= std::floor(t);
         turns[i] = static_cast<uint64_t>(std::ldexp(t, 64));

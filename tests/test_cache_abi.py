@@ -273,6 +273,20 @@ def test_frequency_refusals(attn):
         attn.rope_turns(64, 10000.0, scaling="other")
 
 
+def test_frequencies_that_are_no_numbers_are_refused(attn):
+    """Finite arguments whose quotients or powers overflow."""
+    for kw in (dict(scaling="linear", factor=1e-320), dict(scaling="ntk", factor=1e-320, rot_dim=4),
+               dict(scaling="yarn", factor=1e-320, original_len=4096.0),
+               dict(scaling="bands", factor=1e-320, original_len=4096.0), dict(theta=5e-324,
+                                                                               rot_dim=4096)):
+        a = {**dict(rot_dim=64, theta=10000.0), **kw}
+        with pytest.raises(attn.AttnError):
+            attn.rope_turns(a.pop("rot_dim"), a.pop("theta"), **a)
+    # a base that overflows leaves frequencies of 0: positions that far apart never turn
+    t, _ = turns_of(attn, 4, 10000.0, scaling="ntk", factor=1e300)
+    assert t[1] == 0
+
+
 # ---- the binding's own checks -----------------------------------------------
 
 def test_binding_refuses_wrong_tensors(attn):
