@@ -17,8 +17,8 @@
 // cache is a sum of e4m3 terms, each in a column of its own: N is padded to 16
 // anyway, and the time of an MMA this narrow is that of reading A.
 //   q = 2^-a (q0 + q1 / 16): a puts the row's largest channel in [128, 256);
-//     8 significant bits are two terms of 4, so bf16 channels down to 2^-14 of
-//     the largest are exact and smaller ones miss at most 2^-23 of it.
+//     8 significant bits are two terms of 4, so bf16 channels down to 2^-13 of
+//     the largest are exact and smaller ones miss at most 2^-21 of it.
 //   weights = w0 + 2^-5 w1 + 2^-10 w2 + 2^-25 w3, each term what those before leave,
 //     rounded to nearest.  e4m3 numbers end at 2^-9, so what terms hold of a small weight
 //     is bounded below: an error of at most 2^-13 of the weight, or 2^-29 of the piece's
@@ -41,11 +41,11 @@
 // turns q into its terms and fetches the scales of each tile's keys (cp.async).
 //
 // What bounds it.  Up to 4 columns the stream of codes: 64 sequences of 32 + 8
-// heads and 512 to 8192 keys (580 MB) take 96.7 us, 6.0 TB/s with everything,
+// heads and 512 to 8192 keys (580 MB) take 98 us, 5.9 TB/s with everything,
 // about 7 while the stream runs.  The rest is 5 us until the first scores
 // (range, page table, first tile), the ends of the CTAs and the reduce.  With 16
 // columns the softmax of a tile takes longer than its bytes (1 to 4 draft
-// rows of 4 heads: 85 us for 318 MB).  What runs once an item (opening it, the first
+// rows of 4 heads: 89 us for 318 MB; 83 with three terms of the weights).  What runs once an item (opening it, the first
 // tile's maxima, the epilogue) runs from a cold instruction cache, at 100 cycles
 // and more per eight instructions: hence the rolled loops and the care for code
 // length there.  (Heads taken one after the other 114.9 us, P through a swizzled
