@@ -609,10 +609,10 @@ int attn_append_kv_fp8(const attn_head_rows_t *q, const attn_head_rows_t *k,
  * weights p_j enter out.  Of the keys that one CTA takes of a sequence let u be the
  * largest p_j 2^(e_j), e_j the exponent of the key's V scale.  p_j 2^(e_j) errs by at
  * most 2^-13 of itself or 2^-29 u, whichever is more, and by no more than a sixteenth
- * of itself down to 2^-35 u; below 2^-40 u it is left out of out (lse counts it, but
- * for a key whose V scale is 2^D below the sequence's largest and whose weight is
- * below 2^(D - 126) of the largest: D is 4 or so where V is of one size).
- * (attn_decode rounds each weight to bf16, 2^-9 of itself.)  A code of NaN
+ * of itself down to 2^-35 u; below 2^-40 u it is left out of out.  (attn_decode rounds
+ * each weight to bf16, 2^-9 of itself.)  lse counts it, but for a key whose V scale is
+ * 2^D below the sequence's largest when its weight is below 2^(D - 126) of the largest
+ * weight.  A code of NaN
  * in a token makes the out of the rows that see it NaN (their lse is then
  * undefined) and of no others, whatever slots past a sequence's last token hold.
  * Launches the partition kernel and, for max_kv_len > 128, the split-K reduce.

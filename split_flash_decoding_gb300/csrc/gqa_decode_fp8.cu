@@ -25,8 +25,9 @@
 //     reference where that is more (a weight of 2^-20 of it keeps 9 bits, as in bf16),
 //     though never more than a sixteenth of a weight of 2^-35 and more; what is below
 //     2^-40 is lost.  The last term starts that low because the first three already hold
-//     the larger weights; it saturates there.  (Three terms 2^-4 apart dropped all below 2^-21: a key that takes
-//     nearly all the weight and has no V, 15 nats above 131072 others, left 0 of them.)
+//     the larger weights; it saturates there.  (Three terms 2^-4 apart dropped all below
+//     2^-21: a key that takes nearly all the weight and has no V, 15 nats above 131072
+//     others, left 0 of them.)
 // A thread owns one key of the tile (its TMEM lane), so the scales cost it two
 // multiplications: ks_j goes into the score, and V's scale into the weight.
 // With vs_j = r_j 2^(e_j) (e_j its exponent, clamped to [-64, 64]), the running
@@ -45,8 +46,8 @@
 // about 7 while the stream runs.  The rest is 5 us until the first scores
 // (range, page table, first tile), the ends of the CTAs and the reduce.  With 16
 // columns the softmax of a tile takes longer than its bytes (1 to 4 draft
-// rows of 4 heads: 89 us for 318 MB; 83 with three terms of the weights).  What runs once an item (opening it, the first
-// tile's maxima, the epilogue) runs from a cold instruction cache, at 100 cycles
+// rows of 4 heads: 89 us for 318 MB; 83 with three terms of the weights).  What runs
+// once an item (opening it, the first tile's maxima, the epilogue) runs from a cold instruction cache, at 100 cycles
 // and more per eight instructions: hence the rolled loops and the care for code
 // length there.  (Heads taken one after the other 114.9 us, P through a swizzled
 // K-major layout 201 instead of 158 us for the draft rows, one group of warps for
@@ -81,7 +82,8 @@ constexpr int kMinVExp = -64, kMaxVExp = 64;
 
 // Columns (query rows x heads) come in chunks of four: a chunk's S columns (and Q
 // rows) are [2 terms][4], its O columns (and P columns) [4 terms][4].  More than one
-// chunk takes two groups of four softmax warps; group g has the chunks g, g + 2.  Chunks past an item's columns are skipped.
+// chunk takes two groups of four softmax warps; group g has the chunks g, g + 2.  Chunks
+// past an item's columns are skipped.
 template <int NC>
 struct Cfg {
     static constexpr int kChunks = NC / 4;
