@@ -627,6 +627,78 @@ int attn_decode_fp8(const void *q, const attn_kv_t *k, const attn_kv_t *v,
                     size_t workspace_bytes, void *out, float *lse, attn_stream_t stream);
 
 /*
+ * Keys by the attention they gather
+ * ---------------------------------
+ * Every token and KV head of a bf16 cache may have an fp32 weight: the sum of the
+ * attention weights that query rows gave it.  The weights lie beside the cache,
+ * described by attn_kv_scale_t with block_tokens 1 (strides in floats; token t of
+ * sequence b, KV head kh: its page and slot as for attn_kv_t).
+ *
+ * attn_key_weights -- add the weights that a call's query rows give their keys.
+ *
+ *   q, k, kv_len, q_row_offsets, batch, num_q_rows, num_q_heads, group,
+ *   max_kv_len, scale, causal   as for the attn_decode call of the same rows (k alone);
+ *              any group up to 128.
+ *   lse        device fp32 [num_q_rows][num_q_heads]: what that call returned
+ *              (sinks, if there were any, are in it).
+ *   head_dim   64 or 128.  batch <= 2048.
+ *   max_q_len  host upper bound of the rows of any sequence: it picks the kernel,
+ *              more rows are taken as well.
+ *   decay      factor of the weights from before.
+ *   weights    read and written: for t < kv_len[b], with n the rows of sequence b,
+ *     w_t = [t < kv_len[b] - n] decay w_t
+ *           + sum over the rows that see t and the heads of the group of
+ *             exp(scale q.k_t - lse)
+ *              (the last n tokens are those of the rows: what their slots held
+ *              before is not read).  Tokens at and behind kv_len[b] are left.
+ *              Sequences of a call must not share a page.
+ *
+ * A sequence without rows has its weights multiplied by decay.  Sums are fp32 in a
+ * fixed order: equal calls give equal weights.  A page outside the pool sets bit 1 of
+ * the error word (its tokens' weights are left), a kv_len above max_kv_len bit 2 (it is
+ * clamped).  Returns ATTN_OK, ATTN_ERR_INVALID_ARG, ATTN_ERR_UNSUPPORTED or
+ * ATTN_ERR_CUDA.
+ */
+int attn_key_weights(const void *q, const attn_kv_t *k, const float *lse, const uint32_t *kv_len,
+                     const uint32_t *q_row_offsets, int batch, int num_q_rows, int num_q_heads,
+                     int group, int head_dim, int max_q_len, int max_kv_len, float scale,
+                     int causal, float decay, const attn_kv_scale_t *weights,
+                     attn_stream_t stream);
+
+/*
+ * attn_evict_kv -- keep the keys and values of the largest weights, and move them
+ * together.
+ *
+ *   k, v       caches of 2-byte elements; v may be NULL (a cache whose V is part of
+ *              K).  dim_k, dim_v: channels of a head, multiples of 8 up to 1024.
+ *   weights    the tokens' weights (block_tokens 1).  NaN counts as -inf.
+ *   kv_len     device uint32 [batch], at most max_kv_len.
+ *   keep       device int32 [batch]: tokens to keep, at most max_keep (below 0: 0).
+ *   first, recent   tokens that stay whatever their weight: of the n = min(kv_len[b],
+ *              keep[b]) kept tokens r = min(recent, n) are the last and f = min(first,
+ *              n - r) the first; the other n - r - f are those in between of the largest
+ *              weight, of equal weights the earliest.  Every KV head has its own choice.
+ *   k_out, v_out   caches that take the kept tokens, in their order, at slots 0 to
+ *              n - 1 of each sequence (any page size and layout; their own page table).
+ *              They may be pages of the same pool, but no page that the call reads.
+ *   weights_out  the kept tokens' weights beside k_out, or NULL.
+ *   kept_len   out, device uint32 [batch]: n, or NULL.
+ *   indices    out, device int32 [batch][num_kv_heads][max_keep]: the kept tokens,
+ *              rising; entries from n on are left.
+ *
+ * A kept token has its place among the keys changed, not its rotation: rows that are
+ * appended behind it need their positions given.  Pages outside a pool set bit 1 of the
+ * error word (rows of theirs are not copied), kv_len and keep above their bounds bit 2
+ * (they are clamped).  batch <= 2048, num_kv_heads <= 256.  Returns as attn_key_weights.
+ */
+int attn_evict_kv(const attn_kv_t *k, const attn_kv_t *v, const attn_kv_scale_t *weights,
+                  const uint32_t *kv_len, const int32_t *keep, int batch, int num_kv_heads,
+                  int dim_k, int dim_v, int max_kv_len, int max_keep, int first, int recent,
+                  const attn_kv_t *k_out, const attn_kv_t *v_out,
+                  const attn_kv_scale_t *weights_out, uint32_t *kept_len, int32_t *indices,
+                  attn_stream_t stream);
+
+/*
  * attn_device_error_flags -- read (and optionally clear) the device-side
  * error word that kernels set instead of hanging: bit 0 = a pipeline wait
  * ran past its time limit (250 ms), bit 1 = a page-table entry outside

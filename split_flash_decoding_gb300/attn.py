@@ -152,6 +152,13 @@ _SIGNATURES = {
                         _c.c_void_p, _c.c_int, _c.c_int, _c.c_int, _c.c_int, _c.c_int, _c.c_int,
                         _c.c_int, _c.c_float, _c.c_void_p, _c.c_int, _c.c_void_p, _c.c_size_t,
                         _c.c_void_p, _c.c_void_p, _c.c_void_p],
+    "attn_key_weights": [_c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_int,
+                         _c.c_int, _c.c_int, _c.c_int, _c.c_int, _c.c_int, _c.c_int, _c.c_float,
+                         _c.c_int, _c.c_float, _c.c_void_p, _c.c_void_p],
+    "attn_evict_kv": [_c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_int,
+                      _c.c_int, _c.c_int, _c.c_int, _c.c_int, _c.c_int, _c.c_int, _c.c_int,
+                      _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_void_p,
+                      _c.c_void_p],
 }
 
 _lib = None
@@ -757,6 +764,111 @@ def attn_decode_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
                                  1 if causal else 0, _ptr(ws), ws_size, out.data_ptr(), _ptr(lse),
                                  _stream_of(stream, device)))
     return out, lse
+
+
+def _token_floats(w: torch.Tensor, cache_shape, what: str) -> bytes:
+    """A value for each token and head beside a cache, as packed attn_kv_scale_t."""
+    if w.dtype != torch.float32 or w.shape != cache_shape[:3]:
+        raise ValueError(f"{what} must be fp32 {tuple(cache_shape[:3])}: a value for each token and "
+                         "KV head of the cache")
+    return _pack_kv_scale(w.data_ptr(), *w.stride(), 1, 0)
+
+
+def attn_key_weights(q: torch.Tensor, k_cache: torch.Tensor, lse: torch.Tensor,
+                     kv_len: torch.Tensor, weights: torch.Tensor, *, group: int, scale: float,
+                     max_kv_len: int, page_table: Optional[torch.Tensor] = None,
+                     q_row_offsets: Optional[torch.Tensor] = None,
+                     max_q_len: Optional[int] = None, causal: bool = False, decay: float = 1.0,
+                     stream=None) -> torch.Tensor:
+    """Add the attention weights of q's rows to those that the keys of a cache gathered
+    before, through attn_key_weights.
+
+    q bf16 [rows, num_q_heads, 64 or 128] and lse fp32 [rows, num_q_heads] of an
+    attn_decode call (return_lse), the other arguments as there; weights fp32
+    [pages, page_size, num_kv_heads], any strides, read (times decay) and written, but
+    for a sequence's last tokens, one for each of its rows: theirs are written only.
+    max_q_len picks the kernel; by default, with q_row_offsets, it is all rows.  Returns
+    weights."""
+    rows, hq, d = q.shape
+    batch = kv_len.shape[0]
+    if q.dtype != torch.bfloat16 or not q.is_contiguous():
+        raise ValueError("q must be contiguous bf16 [rows, num_q_heads, head_dim]")
+    if lse.dtype != torch.float32 or lse.shape != (rows, hq) or not lse.is_contiguous():
+        raise ValueError("lse must be contiguous fp32 [rows, num_q_heads]")
+    kd = _pack_kv(*_kv_fields(k_cache, page_table, torch.bfloat16))
+    k_shape = k_cache.shape
+    if k_shape[2] * group != hq or k_shape[3] != d:
+        raise ValueError(f"{hq} query heads of {d} in groups of {group} do not fit a cache "
+                         f"{tuple(k_shape)}")
+    if page_table is not None and page_table.shape[0] != batch:
+        raise ValueError("page_table must have one row per sequence")
+    wd = _token_floats(weights, k_shape, "weights")
+    lens = _int32(kv_len, batch, "kv_len")
+    offs = _int32(q_row_offsets, batch + 1, "q_row_offsets")
+    if max_q_len is None:
+        max_q_len = 1 if q_row_offsets is None else max(rows, 1)
+    device = _on_current_device(q, k_cache, lse, kv_len, weights, page_table, q_row_offsets)
+    _check("attn_key_weights",
+           lib().attn_key_weights(q.data_ptr(), kd, lse.data_ptr(), lens, offs, batch, rows, hq,
+                                  group, d, max_q_len, max_kv_len, scale, 1 if causal else 0,
+                                  decay, wd, _stream_of(stream, device)))
+    return weights
+
+
+def attn_evict_kv(k_cache: torch.Tensor, v_cache: Optional[torch.Tensor], weights: torch.Tensor,
+                  kv_len: torch.Tensor, keep: torch.Tensor, k_out: torch.Tensor,
+                  v_out: Optional[torch.Tensor], weights_out: Optional[torch.Tensor] = None, *,
+                  max_kv_len: int, max_keep: int, first: int = 0, recent: int = 0,
+                  page_table: Optional[torch.Tensor] = None,
+                  out_page_table: Optional[torch.Tensor] = None,
+                  kept_len: Optional[torch.Tensor] = None,
+                  indices: Optional[torch.Tensor] = None, stream=None):
+    """Keep the keys and values of the largest weights and move them together, through
+    attn_evict_kv.
+
+    Of sequence b the min(kv_len[b], keep[b]) tokens that stay (the last `recent` and
+    the first `first` always) go, in their order and for each KV head its own, to slots
+    0 on of the pages that out_page_table gives it in k_out and v_out (bf16; no page
+    that is read), their weights beside them.  keep int32 [batch] on the device, at most
+    max_keep.  v_cache and v_out None: a cache whose V is part of K.  Returns (kept_len
+    int32 [batch], indices int32 [batch, num_kv_heads, max_keep]: the kept tokens)."""
+    batch, heads, dim = kv_len.shape[0], k_cache.shape[2], k_cache.shape[3]
+    if (v_cache is None) != (v_out is None):
+        raise ValueError("v_cache and v_out go together")
+    for table in (page_table, out_page_table):
+        if table is not None and table.shape[0] != batch:
+            raise ValueError("page tables must have one row per sequence")
+    if k_out.shape[2:] != k_cache.shape[2:]:
+        raise ValueError(f"a cache {tuple(k_cache.shape)} does not fit {tuple(k_out.shape)}")
+    kd = _pack_kv(*_kv_fields(k_cache, page_table, torch.bfloat16))
+    kod = _pack_kv(*_kv_fields(k_out, out_page_table, torch.bfloat16))
+    vd = vod = None
+    dim_v = 0
+    if v_cache is not None:
+        dim_v = v_cache.shape[3]
+        if (v_cache.shape[:3] != k_cache.shape[:3] or v_out.shape[:3] != k_out.shape[:3] or
+                v_out.shape[3] != dim_v):
+            raise ValueError("v_cache and v_out must have the pages and heads of k_cache and k_out")
+        vd = _pack_kv(*_kv_fields(v_cache, page_table, torch.bfloat16))
+        vod = _pack_kv(*_kv_fields(v_out, out_page_table, torch.bfloat16))
+    wd = _token_floats(weights, k_cache.shape, "weights")
+    wod = None if weights_out is None else _token_floats(weights_out, k_out.shape, "weights_out")
+    lens, keeps = _int32(kv_len, batch, "kv_len"), _int32(keep, batch, "keep")
+    if kept_len is None:
+        kept_len = _empty((batch,), torch.int32, k_cache.device, stream)
+    if indices is None:
+        indices = _empty((batch, heads, max_keep), torch.int32, k_cache.device, stream)
+    elif (indices.dtype != torch.int32 or indices.shape != (batch, heads, max_keep) or
+          not indices.is_contiguous()):
+        raise ValueError("indices must be contiguous int32 [batch, num_kv_heads, max_keep]")
+    device = _on_current_device(k_cache, v_cache, weights, kv_len, keep, k_out, v_out, weights_out,
+                                page_table, out_page_table, kept_len, indices)
+    _check("attn_evict_kv",
+           lib().attn_evict_kv(kd, vd, wd, lens, keeps, batch, heads, dim, dim_v, max_kv_len,
+                               max_keep, first, recent, kod, vod, wod,
+                               _int32(kept_len, batch, "kept_len"), indices.data_ptr(),
+                               _stream_of(stream, device)))
+    return kept_len, indices
 
 
 def attn_selftest_wait_timeout(stream=None) -> None:

@@ -10,6 +10,7 @@
 
 #include "attn_decode.h"
 #include "cache_ops.h"
+#include "evict_ops.h"
 #include "launch.h"
 #include "ptx.cuh"
 
@@ -414,6 +415,29 @@ int plan_impl(int num_sms, int batch, int num_q_rows, int max_q_len, int num_q_h
 namespace attn {
 
 int device_error_word(unsigned **out) { return error_word(out); }
+
+int encode_kv_map_bf16(CUtensorMap *map, const void *base, long long token_stride,
+                       long long head_stride, long long page_stride, int dim, int page_size,
+                       int num_kv_heads, int num_pages, int box_rows) {
+    const attn_kv_t kv = {base, page_stride, token_stride, head_stride, page_size, num_pages,
+                          nullptr, 0, 0};
+    return encode_kv_map(map, kv, dim, num_kv_heads, box_rows);
+}
+
+int encode_q_map_bf16(CUtensorMap *map, const void *q, int dim, int group, int num_kv_heads,
+                      int num_q_rows, int box_rows) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return ATTN_ERR_CUDA;
+    const cuuint64_t head = cuuint64_t(dim) * 2, heads = cuuint64_t(group);
+    cuuint64_t gdim[4] = {cuuint64_t(dim), heads, cuuint64_t(num_kv_heads), cuuint64_t(num_q_rows)};
+    cuuint64_t gstride[3] = {head, heads * head, cuuint64_t(num_kv_heads) * heads * head};
+    cuuint32_t box[4] = {64, cuuint32_t(group), 1, cuuint32_t(box_rows)};
+    cuuint32_t estride[4] = {1, 1, 1, 1};
+    CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(q), gdim, gstride,
+                    box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? ATTN_OK : ATTN_ERR_UNSUPPORTED;
+}
 
 int encode_kv_map_8bit(CUtensorMap *map, const void *base, long long token_stride,
                        long long head_stride, long long page_stride, int dim, int page_size,

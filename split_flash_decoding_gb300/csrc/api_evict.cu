@@ -1,0 +1,189 @@
+// api_evict.cu -- the extern "C" entry points around the weights that a cache's keys
+// gather: host-side validation and launches.
+#include <cuda_runtime.h>
+
+#include <cstdint>
+#include <cstring>
+
+#include "attn_decode.h"
+#include "cache_ops.h"
+#include "evict_ops.h"
+
+namespace attn {
+namespace {
+
+bool is_pow2(long long x) { return x > 0 && (x & (x - 1)) == 0; }
+bool aligned(const void *p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+int map_cuda(cudaError_t e) { return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA; }
+
+// A cache operand of 2-byte elements that holds up to `tokens` of each sequence.
+int check_cache(const attn_kv_t *kv, int batch, int dim, int heads, int tokens) {
+    if (!kv || !kv->base || kv->reserved != 0 || !aligned(kv->base, 16)) return ATTN_ERR_INVALID_ARG;
+    if (kv->page_size <= 0 || kv->num_pages <= 0) return ATTN_ERR_INVALID_ARG;
+    if (kv->token_stride < dim || kv->head_stride <= 0 || kv->page_stride <= 0 ||
+        (heads > 1 && kv->head_stride < dim))
+        return ATTN_ERR_INVALID_ARG;
+    if (kv->token_stride % 8 || kv->head_stride % 8 || kv->page_stride % 8)
+        return ATTN_ERR_INVALID_ARG;
+    if (!kv->page_table)
+        return kv->page_size < tokens || kv->num_pages < batch ? ATTN_ERR_INVALID_ARG : ATTN_OK;
+    if (!is_pow2(kv->page_size) || kv->page_size < 8) return ATTN_ERR_UNSUPPORTED;
+    if (kv->max_pages <= 0 ||
+        (static_cast<long long>(tokens) + kv->page_size - 1) / kv->page_size > kv->max_pages)
+        return ATTN_ERR_INVALID_ARG;
+    return ATTN_OK;
+}
+
+int take_floats(const attn_kv_scale_t *w, TokenFloats *x) {
+    if (!w || !w->base || w->reserved != 0 || !aligned(w->base, 4) || w->block_tokens != 1)
+        return ATTN_ERR_INVALID_ARG;
+    if (w->page_stride <= 0 || w->block_stride <= 0 || w->head_stride <= 0)
+        return ATTN_ERR_INVALID_ARG;
+    *x = {w->base, w->page_stride, w->block_stride, w->head_stride};
+    return ATTN_OK;
+}
+
+MovedRows moved(const attn_kv_t *from, const attn_kv_t *to, int dim) {
+    MovedRows m;
+    m.from = static_cast<const uint8_t *>(from->base);
+    m.to = static_cast<uint8_t *>(const_cast<void *>(to->base));
+    m.from_page = 2 * from->page_stride;
+    m.from_token = 2 * from->token_stride;
+    m.from_head = 2 * from->head_stride;
+    m.to_page = 2 * to->page_stride;
+    m.to_token = 2 * to->token_stride;
+    m.to_head = 2 * to->head_stride;
+    m.vecs = dim / 8;
+    return m;
+}
+
+bool same_layout(const attn_kv_t *a, const attn_kv_t *b) {
+    return a->page_table == b->page_table && a->page_size == b->page_size &&
+           a->max_pages == b->max_pages && a->num_pages == b->num_pages;
+}
+
+int device_sms(int *sms) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return ATTN_ERR_CUDA;
+    return ATTN_OK;
+}
+
+}  // namespace
+}  // namespace attn
+
+using namespace attn;
+
+extern "C" int attn_key_weights(const void *q, const attn_kv_t *k, const float *lse,
+                                const uint32_t *kv_len, const uint32_t *q_row_offsets, int batch,
+                                int num_q_rows, int num_q_heads, int group, int head_dim,
+                                int max_q_len, int max_kv_len, float scale, int causal,
+                                float decay, const attn_kv_scale_t *weights,
+                                attn_stream_t stream) {
+    if (batch < 0 || num_q_rows < 0 || num_q_heads <= 0 || group <= 0 || max_kv_len < 0 ||
+        max_q_len < 1 || num_q_heads % group)
+        return ATTN_ERR_INVALID_ARG;
+    if (!(scale == scale) || !(decay == decay)) return ATTN_ERR_INVALID_ARG;
+    if (!q_row_offsets && (num_q_rows != batch || max_q_len != 1)) return ATTN_ERR_INVALID_ARG;
+    if (batch == 0 || max_kv_len == 0) return ATTN_OK;
+    if ((!q || !lse) && num_q_rows > 0) return ATTN_ERR_INVALID_ARG;
+    if (!kv_len || !aligned(q, 16) || !aligned(lse, 4) || !aligned(kv_len, 4) ||
+        !aligned(q_row_offsets, 4))
+        return ATTN_ERR_INVALID_ARG;
+    if ((head_dim != 64 && head_dim != 128) || group > kManyColumns || batch > kGqaMaxBatch ||
+        max_kv_len > kMaxFp8Tokens)
+        return ATTN_ERR_UNSUPPORTED;
+    const int hkv = num_q_heads / group;
+    // items are counted in ints
+    if ((max_kv_len / 128 + 1LL) * batch * hkv > 0x3fffffffLL) return ATTN_ERR_UNSUPPORTED;
+    WeightsParams p;
+    std::memset(&p, 0, sizeof(p));
+    int st = check_cache(k, batch, head_dim, hkv, max_kv_len);
+    if (st || (st = take_floats(weights, &p.w))) return st;
+    const bool few = static_cast<long long>(max_q_len) * group <= kFewColumns;
+    p.tile_rows = (few ? kFewColumns : kManyColumns) / group;
+    p.box_rows = k->page_table && k->page_size < 128 ? k->page_size : 128;
+    if ((st = encode_kv_map_bf16(&p.k_map, k->base, k->token_stride, k->head_stride, k->page_stride,
+                                 head_dim, k->page_size, hkv, k->num_pages, p.box_rows)) ||
+        // (without rows the map is not used, but has to be one)
+        (st = encode_q_map_bf16(&p.q_map, num_q_rows > 0 ? q : k->base, head_dim, group, hkv,
+                                num_q_rows > 0 ? num_q_rows : 1, p.tile_rows)) ||
+        (st = device_error_word(&p.err)))
+        return st;
+    p.lse = lse;
+    p.kv_len = kv_len;
+    p.q_row_offsets = q_row_offsets;
+    p.page_table = k->page_table;
+    p.batch = batch;
+    p.num_q_rows = num_q_rows;
+    p.num_q_heads = num_q_heads;
+    p.group = group;
+    p.hkv = hkv;
+    p.max_q_len = max_q_len;
+    p.max_kv_len = max_kv_len;
+    p.causal = causal ? 1 : 0;
+    p.max_pages = k->max_pages;
+    p.page_size = k->page_size;
+    p.num_pages = k->num_pages;
+    p.scale = scale;
+    p.decay = decay;
+    int sms = 0;
+    if ((st = device_sms(&sms))) return st;
+    return map_cuda(launch_key_weights(p, head_dim, few, sms, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+extern "C" int attn_evict_kv(const attn_kv_t *k, const attn_kv_t *v, const attn_kv_scale_t *weights,
+                             const uint32_t *kv_len, const int32_t *keep, int batch,
+                             int num_kv_heads, int dim_k, int dim_v, int max_kv_len, int max_keep,
+                             int first, int recent, const attn_kv_t *k_out, const attn_kv_t *v_out,
+                             const attn_kv_scale_t *weights_out, uint32_t *kept_len,
+                             int32_t *indices, attn_stream_t stream) {
+    if (batch < 0 || num_kv_heads <= 0 || max_kv_len < 0 || max_keep < 0 || first < 0 || recent < 0)
+        return ATTN_ERR_INVALID_ARG;
+    if ((v == nullptr) != (v_out == nullptr)) return ATTN_ERR_INVALID_ARG;
+    if (batch == 0) return ATTN_OK;
+    if (!kv_len || !keep || (!indices && max_keep > 0)) return ATTN_ERR_INVALID_ARG;
+    if (!aligned(kv_len, 4) || !aligned(keep, 4) || !aligned(kept_len, 4) || !aligned(indices, 4))
+        return ATTN_ERR_INVALID_ARG;
+    if (dim_k <= 0 || (v && dim_v <= 0)) return ATTN_ERR_INVALID_ARG;
+    if (dim_k % 8 || dim_k > 1024 || (v && (dim_v % 8 || dim_v > 1024)) || num_kv_heads > 256 ||
+        batch > kGqaMaxBatch || max_kv_len > kMaxFp8Tokens)
+        return ATTN_ERR_UNSUPPORTED;
+    EvictParams p;
+    std::memset(&p, 0, sizeof(p));
+    int st = check_cache(k, batch, dim_k, num_kv_heads, max_kv_len);
+    if (st || (st = check_cache(k_out, batch, dim_k, num_kv_heads, max_keep))) return st;
+    if (v) {
+        if ((st = check_cache(v, batch, dim_v, num_kv_heads, max_kv_len)) ||
+            (st = check_cache(v_out, batch, dim_v, num_kv_heads, max_keep)))
+            return st;
+        if (!same_layout(k, v) || !same_layout(k_out, v_out)) return ATTN_ERR_UNSUPPORTED;
+        p.v = moved(v, v_out, dim_v);
+    }
+    if ((st = take_floats(weights, &p.w))) return st;
+    if (weights_out && (st = take_floats(weights_out, &p.w_to))) return st;
+    if ((st = device_error_word(&p.err))) return st;
+    p.k = moved(k, k_out, dim_k);
+    p.kv_len = kv_len;
+    p.keep = keep;
+    p.page_table = k->page_table;
+    p.to_table = k_out->page_table;
+    p.kept_len = kept_len;
+    p.indices = indices;
+    p.batch = batch;
+    p.hkv = num_kv_heads;
+    p.max_kv_len = max_kv_len;
+    p.max_keep = max_keep;
+    p.first = first;
+    p.recent = recent;
+    p.page_size = k->page_size;
+    p.num_pages = k->num_pages;
+    p.max_pages = k->max_pages;
+    p.to_page_size = k_out->page_size;
+    p.to_num_pages = k_out->num_pages;
+    p.to_max_pages = k_out->max_pages;
+    int sms = 0;
+    if ((st = device_sms(&sms))) return st;
+    return map_cuda(launch_evict(p, sms, reinterpret_cast<cudaStream_t>(stream)));
+}
