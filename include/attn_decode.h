@@ -20,8 +20,8 @@
  * - Arguments are validated on the host before anything is launched.  A
  *   failed check returns a status and launches nothing.  A failed launch
  *   returns ATTN_ERR_CUDA (the CUDA error is left for cudaGetLastError).
- * - bf16 for q, K, V and out (the entry points named _fp8: K and V in e4m3
- *   with scales); fp32 for scale, sink logits, lse and the
+ * - bf16 for q, K, V and out (the entry points named _fp8 and _fp4: K
+ *   and V in e4m3 or e2m1 codes with scales); fp32 for scale, sink logits, lse and the
  *   split-K workspace.  All element strides are in elements.
  * - lse is the natural-log log-sum-exp of the scaled scores, sink
  *   included; it is -inf for a row with no visible key and no sink (its
@@ -620,6 +620,58 @@ int attn_append_kv_fp8(const attn_head_rows_t *q, const attn_head_rows_t *k,
 int attn_decode_fp8_workspace(int num_sms, int batch, int num_q_heads, int group,
                               size_t *workspace_bytes);
 int attn_decode_fp8(const void *q, const attn_kv_t *k, const attn_kv_t *v,
+                    const attn_kv_scale_t *k_scale, const attn_kv_scale_t *v_scale,
+                    const uint32_t *kv_len, const uint32_t *q_row_offsets, int batch,
+                    int num_q_rows, int num_q_heads, int group, int head_dim, int max_q_len,
+                    int max_kv_len, float scale, const float *sink, int causal, void *workspace,
+                    size_t workspace_bytes, void *out, float *lse, attn_stream_t stream);
+
+/*
+ * A cache held in 4 bits
+ * ----------------------
+ * Heads of 128 channels in e2m1 codes (1 sign, 2 exponent, 1 mantissa bit: 0, 0.5, 1,
+ * 1.5, 2, 3, 4, 6 and their negatives), two to a byte, the even channel in the low half:
+ * 64 bytes a token and head.  attn_kv_t then counts bytes: base 32-byte aligned,
+ * strides multiples of 32.  The scales lie beside it, a 4-byte word for every token and
+ * head, described by attn_kv_scale_t with block_tokens 1 (strides in words):
+ *   keys    four e8m0 bytes (2^(byte - 127); 255: NaN; 0 counts as 0), one for every 32
+ *           channels;
+ *   values  one fp32 number, finite and >= 0 (2^65 and more counts as NaN), for all
+ *           128: it goes into the key's weight, of which there is one.
+ * Scales of a head's tokens side by side (head_stride the largest) read best.
+ *
+ * attn_append_kv_fp4 -- attn_append_kv into such a cache, head dimension 128.
+ *
+ * A scale is 2^e, e the least integer with amax <= 6 * 2^e over its channels (clamped to
+ * [-60, 125]; -60 if all are 0), from the fp32 values before any other rounding; codes are
+ * rounded to nearest even.  If a channel is an infinity or NaN the scale is NaN and its
+ * codes are 0.  A token's codes depend on that token alone: none that is held changes.
+ *
+ *   k, v        head rows; with an out, what the new codes stand for (bf16, exact) goes
+ *               there as well, for every row of a sequence (the attention of a prompt's
+ *               own rows then sees the keys and values that later tokens will).
+ *   k_scale, v_scale  the caches' scales, as above.
+ *   max_kv_len  at most 2^31 - 8193.
+ * Everything else as for attn_append_kv; v and v_cache are required.
+ */
+int attn_append_kv_fp4(const attn_head_rows_t *q, const attn_head_rows_t *k,
+                       const attn_head_rows_t *v, const attn_rope_t *rope,
+                       const int32_t *positions, const attn_kv_t *k_cache,
+                       const attn_kv_t *v_cache, const attn_kv_scale_t *k_scale,
+                       const attn_kv_scale_t *v_scale, const uint32_t *kv_len,
+                       const uint32_t *q_row_offsets, int batch, int num_q_rows, int max_kv_len,
+                       attn_stream_t stream);
+
+/*
+ * attn_decode_fp4 -- attn_decode over a cache held in 4 bits.
+ *
+ * Arguments, limits, workspace and the weights' rounding as for attn_decode_fp8, with k,
+ * v, k_scale and v_scale as above.  A token whose key or value scale is NaN makes the out
+ * of the rows that see it NaN (their lse is then undefined) and of no others.
+ */
+int attn_decode_fp4_workspace(int num_sms, int batch, int num_q_heads, int group,
+                              size_t *workspace_bytes);
+int attn_decode_fp4(const void *q, const attn_kv_t *k, const attn_kv_t *v,
                     const attn_kv_scale_t *k_scale, const attn_kv_scale_t *v_scale,
                     const uint32_t *kv_len, const uint32_t *q_row_offsets, int batch,
                     int num_q_rows, int num_q_heads, int group, int head_dim, int max_q_len,

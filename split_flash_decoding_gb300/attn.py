@@ -152,6 +152,11 @@ _SIGNATURES = {
                         _c.c_void_p, _c.c_int, _c.c_int, _c.c_int, _c.c_int, _c.c_int, _c.c_int,
                         _c.c_int, _c.c_float, _c.c_void_p, _c.c_int, _c.c_void_p, _c.c_size_t,
                         _c.c_void_p, _c.c_void_p, _c.c_void_p],
+    "attn_append_kv_fp4": [_c.c_void_p, _c.c_void_p,
+                           _c.c_void_p, _c.c_void_p, _c.c_void_p,
+                           _c.c_void_p, _c.c_void_p,
+                           _c.c_void_p, _c.c_void_p, _c.c_void_p,
+                           _c.c_void_p, _c.c_int, _c.c_int, _c.c_int, _c.c_void_p],
     "attn_key_weights": [_c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_int,
                          _c.c_int, _c.c_int, _c.c_int, _c.c_int, _c.c_int, _c.c_int, _c.c_float,
                          _c.c_int, _c.c_float, _c.c_void_p, _c.c_void_p],
@@ -160,6 +165,8 @@ _SIGNATURES = {
                       _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_void_p,
                       _c.c_void_p],
 }
+_SIGNATURES["attn_decode_fp4_workspace"] = _SIGNATURES["attn_decode_fp8_workspace"]
+_SIGNATURES["attn_decode_fp4"] = _SIGNATURES["attn_decode_fp8"]
 
 _lib = None
 
@@ -269,6 +276,21 @@ def _kv_pair(k_cache, v_cache, page_table, dtype):
             v_cache.dtype == dtype):
         return _pack_kv(*k), _pack_kv(v_cache.data_ptr(), *k[1:])
     return _pack_kv(*k), _pack_kv(*_kv_fields(v_cache, page_table, dtype))
+
+
+def _fp4_scales(k_scale, v_scale, k_shape, v_shape):
+    """The scales of caches held in 4 bits [pages, page_size, heads, 64]: a key's four
+    float8_e8m0fnu side by side, a value's fp32."""
+    k_strides, v_strides = k_scale.stride(), v_scale.stride()
+    if k_scale.dtype != torch.float8_e8m0fnu or k_scale.shape != (*k_shape[:3], 4):
+        raise ValueError("k_scale must be float8_e8m0fnu [pages, page_size, num_kv_heads, 4]")
+    if v_scale.dtype != torch.float32 or v_scale.shape != v_shape[:3]:
+        raise ValueError("v_scale must be fp32 [pages, page_size, num_kv_heads]")
+    words = [x // 4 for x in k_strides[:3]]
+    if k_strides[3] != 1 or tuple(4 * x for x in words) != k_strides[:3] or k_scale.data_ptr() % 4:
+        raise ValueError("a key's four scales must be contiguous and 4-byte aligned")
+    return (_pack_kv_scale(k_scale.data_ptr(), *words, 1, 0),
+            _pack_kv_scale(v_scale.data_ptr(), *v_strides, 1, 0))
 
 
 def _scale_pair(k_scale, v_scale, k_shape, v_shape):
@@ -610,12 +632,13 @@ def attn_qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor] = None,
 
 
 def _append_args(k, v, k_cache, v_cache, kv_len, page_table, q, q_out, q_row_offsets, rope,
-                 positions, q_norm, k_norm, eps, stream, dtype, *scales):
+                 positions, q_norm, k_norm, eps, stream, dtype, *scales, k_out=None, v_out=None):
+    codes = 2 if dtype == torch.uint8 else 1         # channels to an element of the cache
     k_shape, kc_shape, batch = k.shape, k_cache.shape, kv_len.shape[0]
     rows = k_shape[0]
     if (v is None) != (v_cache is None):
         raise ValueError("v and v_cache go together")
-    if k_shape[1:] != kc_shape[2:]:
+    if (k_shape[1], k_shape[2]) != (kc_shape[2], codes * kc_shape[3]):
         raise ValueError(f"rows {tuple(k_shape)} do not fit a cache {tuple(kc_shape)}")
     if page_table is not None and page_table.shape[0] != batch:
         raise ValueError("page_table must have one row per sequence")
@@ -628,23 +651,24 @@ def _append_args(k, v, k_cache, v_cache, kv_len, page_table, q, q_out, q_row_off
         if q_out is None:
             q_out = _empty(q_shape, torch.bfloat16, q.device, stream)
         qd = _head_rows(q, q_shape, q_out, q_norm, eps, start)
-    kd = _head_rows(k, k_shape, None, k_norm, eps, start)
+    kd = _head_rows(k, k_shape, k_out, k_norm, eps, start)
     if v is None:
         kc = _pack_kv(*_kv_fields(k_cache, page_table, dtype))
     else:
         v_shape = v.shape
         if (v_shape != k_shape or v_cache.shape != kc_shape) and (
-                v_shape[0] != rows or v_shape[1:] != v_cache.shape[2:]):
+                v_shape[0] != rows or
+                (v_shape[1], v_shape[2]) != (v_cache.shape[2], codes * v_cache.shape[3])):
             raise ValueError(f"rows {tuple(v_shape)} do not fit {rows} rows and a cache "
                              f"{tuple(v_cache.shape)}")
-        vd = _head_rows(v, v_shape, None, None, eps, 0)
+        vd = _head_rows(v, v_shape, v_out, None, eps, 0)
         kc, vc = _kv_pair(k_cache, v_cache, page_table, dtype)
     head = (qd, kd, vd, rope_ref, _int32(positions, rows, "positions"), kc, vc)
     tail = (_int32(kv_len, batch, "kv_len"), _int32(q_row_offsets, batch + 1, "q_row_offsets"),
             batch, rows)
     device = _on_current_device(k, v, k_cache, v_cache, kv_len, page_table, q, q_out,
                                 q_row_offsets, positions, q_norm, k_norm,
-                                None if rope is None else rope.turns, *scales)
+                                None if rope is None else rope.turns, k_out, v_out, *scales)
     return q_out, head, tail, device
 
 
@@ -698,6 +722,35 @@ def attn_append_kv_fp8(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
     return q_out
 
 
+def attn_append_kv_fp4(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
+                       v_cache: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
+                       kv_len: torch.Tensor, *, max_kv_len: int,
+                       page_table: Optional[torch.Tensor] = None,
+                       q: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
+                       k_out: Optional[torch.Tensor] = None,
+                       v_out: Optional[torch.Tensor] = None,
+                       q_row_offsets: Optional[torch.Tensor] = None,
+                       rope: Optional[Rope] = None, positions: Optional[torch.Tensor] = None,
+                       q_norm: Optional[torch.Tensor] = None,
+                       k_norm: Optional[torch.Tensor] = None, eps: float = 1e-6, stream=None):
+    """attn_append_kv into caches held in 4 bits (attn_append_kv_fp4), head dimension 128.
+
+    k_cache, v_cache uint8 [pages, page_size, num_kv_heads, 64], two e2m1 codes a byte;
+    k_scale float8_e8m0fnu [pages, page_size, num_kv_heads, 4], v_scale fp32 [pages,
+    page_size, num_kv_heads], any strides (a head's tokens side by side read best).  k_out,
+    v_out: bf16 rows as k and v that take what the new codes stand for, or None.
+    Returns q_out."""
+    q_out, head, tail, device = _append_args(k, v, k_cache, v_cache, kv_len, page_table, q, q_out,
+                                             q_row_offsets, rope, positions, q_norm, k_norm, eps,
+                                             stream, torch.uint8, k_scale, v_scale, k_out=k_out,
+                                             v_out=v_out)
+    _check("attn_append_kv_fp4",
+           lib().attn_append_kv_fp4(*head, *_fp4_scales(k_scale, v_scale, k_cache.shape,
+                                                       v_cache.shape), *tail, max_kv_len,
+                                    _stream_of(stream, device)))
+    return q_out
+
+
 @functools.lru_cache(maxsize=1024)
 def _fp8_workspace(device: int, batch: int, num_q_heads: int, group: int) -> int:
     return attn_decode_fp8_workspace(batch, num_q_heads, group)
@@ -726,14 +779,49 @@ def attn_decode_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     one row, or a few (max_q_len * group <= 16), per sequence, head dimension
     128; everything else as for attn_decode.  max_q_len is by default, with
     q_row_offsets, the most that a call may have.  Returns (out, lse)."""
+    return _decode_codes("attn_decode_fp8", torch.float8_e4m3fn, 1, _scale_pair, q, k_cache, v_cache,
+                         k_scale, v_scale, kv_len, group, scale, max_kv_len, page_table, sink,
+                         q_row_offsets, max_q_len, causal, workspace, out, lse, return_lse, stream)
+
+
+def attn_decode_fp4_workspace(batch: int, num_q_heads: int, group: int, num_sms: int = 0) -> int:
+    """Bytes of workspace that attn_decode_fp4 needs."""
+    n = ctypes.c_size_t(0)
+    _check("attn_decode_fp4_workspace",
+           lib().attn_decode_fp4_workspace(num_sms, batch, num_q_heads, group, ctypes.byref(n)))
+    return n.value
+
+
+def attn_decode_fp4(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                    k_scale: torch.Tensor, v_scale: torch.Tensor, kv_len: torch.Tensor, *,
+                    group: int, scale: float, max_kv_len: int,
+                    page_table: Optional[torch.Tensor] = None,
+                    sink: Optional[torch.Tensor] = None,
+                    q_row_offsets: Optional[torch.Tensor] = None,
+                    max_q_len: Optional[int] = None,
+                    causal: bool = False, workspace: Optional[torch.Tensor] = None,
+                    out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                    return_lse: bool = True, stream=None):
+    """Decode attention over caches held in 4 bits, laid out as for attn_append_kv_fp4,
+    through attn_decode_fp4: one row, or a few (max_q_len * group <= 16), per sequence, head
+    dimension 128; everything else as for attn_decode.  max_q_len is by default, with
+    q_row_offsets, the most that a call may have.  Returns (out, lse)."""
+    return _decode_codes("attn_decode_fp4", torch.uint8, 2, _fp4_scales, q, k_cache, v_cache,
+                         k_scale, v_scale, kv_len, group, scale, max_kv_len, page_table, sink,
+                         q_row_offsets, max_q_len, causal, workspace, out, lse, return_lse, stream)
+
+
+def _decode_codes(name, dtype, codes, scale_pair, q, k_cache, v_cache, k_scale, v_scale, kv_len,
+                  group, scale, max_kv_len, page_table, sink, q_row_offsets, max_q_len, causal,
+                  workspace, out, lse, return_lse, stream):
     rows, hq, d = q.shape
     batch = kv_len.shape[0]
-    kd, vd = _kv_pair(k_cache, v_cache, page_table, torch.float8_e4m3fn)
+    kd, vd = _kv_pair(k_cache, v_cache, page_table, dtype)
     k_shape, v_shape = k_cache.shape, v_cache.shape
-    ks, vs = _scale_pair(k_scale, v_scale, k_shape, v_shape)
+    ks, vs = scale_pair(k_scale, v_scale, k_shape, v_shape)
     if q.dtype != torch.bfloat16 or not q.is_contiguous():
         raise ValueError("q must be contiguous bf16 [rows, num_q_heads, 128]")
-    if k_shape[2:] != v_shape[2:] or k_shape[2] * group != hq or k_shape[3] != d:
+    if k_shape[2:] != v_shape[2:] or k_shape[2] * group != hq or k_shape[3] * codes != d:
         raise ValueError(f"{hq} query heads of {d} in groups of {group} do not fit caches "
                          f"{tuple(k_shape)} and {tuple(v_shape)}")
     if page_table is not None and page_table.shape[0] != batch:
@@ -758,11 +846,11 @@ def attn_decode_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
                                 q_row_offsets, workspace, out, lse)
     need = 0 if max_kv_len <= 128 else _fp8_workspace(device, batch, hq, group)
     ws, ws_size = _workspace(need, q.device, workspace, stream)
-    _check("attn_decode_fp8",
-           lib().attn_decode_fp8(q.data_ptr(), kd, vd, ks, vs, lens, offs, batch, rows, hq, group,
-                                 d, max_q_len, max_kv_len, scale, _ptr(sink),
-                                 1 if causal else 0, _ptr(ws), ws_size, out.data_ptr(), _ptr(lse),
-                                 _stream_of(stream, device)))
+    _check(name,
+           getattr(lib(), name)(q.data_ptr(), kd, vd, ks, vs, lens, offs, batch, rows, hq, group, d,
+                                max_q_len, max_kv_len, scale, _ptr(sink), 1 if causal else 0,
+                                _ptr(ws), ws_size, out.data_ptr(), _ptr(lse),
+                                _stream_of(stream, device)))
     return out, lse
 
 

@@ -439,9 +439,12 @@ int encode_q_map_bf16(CUtensorMap *map, const void *q, int dim, int group, int n
     return r == CUDA_SUCCESS ? ATTN_OK : ATTN_ERR_UNSUPPORTED;
 }
 
-int encode_kv_map_8bit(CUtensorMap *map, const void *base, long long token_stride,
-                       long long head_stride, long long page_stride, int dim, int page_size,
-                       int num_kv_heads, int num_pages, int box_rows) {
+// A cache operand whose rows of `dim` elements lie on 128 bytes of shared memory; strides in
+// bytes.
+static int encode_kv_map_codes(CUtensorMapDataType type, CUtensorMap *map, const void *base,
+                               long long token_stride, long long head_stride,
+                               long long page_stride, int dim, int page_size, int num_kv_heads,
+                               int num_pages, int box_rows) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return ATTN_ERR_CUDA;
     cuuint64_t gdim[4] = {cuuint64_t(dim), cuuint64_t(page_size), cuuint64_t(num_kv_heads),
@@ -450,10 +453,25 @@ int encode_kv_map_8bit(CUtensorMap *map, const void *base, long long token_strid
                              cuuint64_t(page_stride)};
     cuuint32_t box[4] = {128, cuuint32_t(box_rows), 1, 1};
     cuuint32_t estride[4] = {1, 1, 1, 1};
-    CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void *>(base), gdim, gstride,
-                    box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+    CUresult r = fn(map, type, 4, const_cast<void *>(base), gdim, gstride, box, estride,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? ATTN_OK : ATTN_ERR_UNSUPPORTED;
+}
+
+int encode_kv_map_8bit(CUtensorMap *map, const void *base, long long token_stride,
+                       long long head_stride, long long page_stride, int dim, int page_size,
+                       int num_kv_heads, int num_pages, int box_rows) {
+    return encode_kv_map_codes(CU_TENSOR_MAP_DATA_TYPE_UINT8, map, base, token_stride, head_stride,
+                               page_stride, dim, page_size, num_kv_heads, num_pages, box_rows);
+}
+
+int encode_kv_map_4bit(CUtensorMap *map, const void *base, long long token_stride,
+                       long long head_stride, long long page_stride, int dim, int page_size,
+                       int num_kv_heads, int num_pages, int box_rows) {
+    return encode_kv_map_codes(CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, map, base, token_stride,
+                               head_stride, page_stride, dim, page_size, num_kv_heads, num_pages,
+                               box_rows);
 }
 
 }  // namespace attn

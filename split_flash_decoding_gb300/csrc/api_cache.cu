@@ -1,5 +1,5 @@
 // api_cache.cu -- the extern "C" entry points that fill a KV cache and read one
-// held in 8 bits: host-side validation and launches.
+// held in 8 or 4 bits: host-side validation and launches.
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -17,9 +17,10 @@ bool aligned(const void *p, size_t n) { return reinterpret_cast<uintptr_t>(p) % 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 int map_cuda(cudaError_t e) { return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA; }
 
-// Head rows of an entry point; to_rows: they go to rows of memory (out), else
-// to a cache.
-int take_heads(const attn_head_rows_t &h, bool to_rows, const attn_rope_t *rope, int num_rows,
+// Head rows of an entry point, and where they go: to rows of memory (out), to a
+// cache, or to a cache and, with an out, to rows as well.
+enum Goes { kToRows, kToCache, kToBoth };
+int take_heads(const attn_head_rows_t &h, Goes goes, const attn_rope_t *rope, int num_rows,
                HeadRows *x) {
     if (h.reserved != 0 || h.num_heads <= 0 || h.dim <= 0 || h.norm_dim < 0 || h.rot_start < 0)
         return ATTN_ERR_INVALID_ARG;
@@ -29,11 +30,13 @@ int take_heads(const attn_head_rows_t &h, bool to_rows, const attn_rope_t *rope,
         return ATTN_ERR_INVALID_ARG;
     if (h.norm_dim > 0 && !(h.norm_eps >= 0.f)) return ATTN_ERR_INVALID_ARG;
     if (!aligned(h.norm_weight, 16)) return ATTN_ERR_INVALID_ARG;
-    if (to_rows != (h.out != nullptr) && num_rows > 0) return ATTN_ERR_INVALID_ARG;
+    if (goes != kToBoth && (goes == kToRows) != (h.out != nullptr) && num_rows > 0)
+        return ATTN_ERR_INVALID_ARG;
     if (num_rows > 0 && !h.in) return ATTN_ERR_INVALID_ARG;
     if (!aligned(h.in, 16) || !aligned(h.out, 16)) return ATTN_ERR_INVALID_ARG;
     if (h.in_row_stride % 8 || h.in_head_stride % 8) return ATTN_ERR_INVALID_ARG;
-    if (to_rows && (h.out_row_stride % 8 || h.out_head_stride % 8)) return ATTN_ERR_INVALID_ARG;
+    if ((goes == kToRows || h.out) && (h.out_row_stride % 8 || h.out_head_stride % 8))
+        return ATTN_ERR_INVALID_ARG;
     x->in = static_cast<const uint16_t *>(h.in);
     x->out = static_cast<uint16_t *>(h.out);
     x->norm = static_cast<const uint16_t *>(h.norm_weight);
@@ -66,7 +69,8 @@ int take_rope(const attn_rope_t *rope, RopeParams *r) {
     return ATTN_OK;
 }
 
-// A cache operand that rows are stored to; unit: elements per 16 bytes.
+// A cache operand that rows are stored to; dim and unit in its elements: of a head, and
+// what strides are multiples of.
 int take_cache(const attn_kv_t *kv, int batch, int dim, int num_kv_heads, int max_kv_len, int unit,
                CacheOut *c) {
     if (!kv || !kv->base || kv->reserved != 0) return ATTN_ERR_INVALID_ARG;
@@ -106,6 +110,13 @@ int check_scale(const attn_kv_scale_t *s, const attn_kv_t *kv) {
     return ATTN_OK;
 }
 
+// The same of a cache held in 4 bits, whose rows the copies want on 32-byte boundaries.
+int check_fp4(const attn_kv_scale_t *s, const attn_kv_t *kv) {
+    const int st = check_scale(s, kv);
+    if (st) return st;
+    return s->block_tokens != 1 || !aligned(kv->base, 32) ? ATTN_ERR_INVALID_ARG : ATTN_OK;
+}
+
 void take_scale(const attn_kv_scale_t *s, CacheOut *c) {
     c->scale = s->base;
     c->scale_page = s->page_stride;
@@ -113,11 +124,12 @@ void take_scale(const attn_kv_scale_t *s, CacheOut *c) {
     c->scale_head = s->head_stride;
 }
 
-// Shared part of the two appending entry points.
+// Shared part of the appending entry points; dim_unit: channels to an element of a cache.
 int take_append(const attn_head_rows_t *q, const attn_head_rows_t *k, const attn_head_rows_t *v,
                 const attn_rope_t *rope, const int32_t *positions, const attn_kv_t *k_cache,
                 const attn_kv_t *v_cache, const uint32_t *kv_len, const uint32_t *q_row_offsets,
-                int batch, int num_q_rows, int max_kv_len, int unit, RowsParams *p) {
+                int batch, int num_q_rows, int max_kv_len, int unit, RowsParams *p,
+                Goes kv_goes = kToCache, int dim_unit = 1) {
     std::memset(p, 0, sizeof(*p));
     if (batch < 0 || num_q_rows < 0 || max_kv_len < 0) return ATTN_ERR_INVALID_ARG;
     if (!q_row_offsets && num_q_rows != batch) return ATTN_ERR_INVALID_ARG;
@@ -127,13 +139,16 @@ int take_append(const attn_head_rows_t *q, const attn_head_rows_t *k, const attn
         return ATTN_ERR_INVALID_ARG;
     int st = take_rope(rope, &p->rope);
     if (st) return st;
-    if (q && (st = take_heads(*q, true, rope, num_q_rows, &p->q))) return st;
-    if ((st = take_heads(*k, false, rope, num_q_rows, &p->k))) return st;
-    if ((st = take_cache(k_cache, batch, k->dim, k->num_heads, max_kv_len, unit, &p->kc))) return st;
+    if (q && (st = take_heads(*q, kToRows, rope, num_q_rows, &p->q))) return st;
+    if ((st = take_heads(*k, kv_goes, rope, num_q_rows, &p->k))) return st;
+    if ((st = take_cache(k_cache, batch, k->dim / dim_unit, k->num_heads, max_kv_len, unit,
+                         &p->kc)))
+        return st;
     if (v) {
-        if ((st = take_heads(*v, false, nullptr, num_q_rows, &p->v))) return st;
+        if ((st = take_heads(*v, kv_goes, nullptr, num_q_rows, &p->v))) return st;
         if (v->norm_dim != 0 || v->num_heads != k->num_heads) return ATTN_ERR_INVALID_ARG;
-        if ((st = take_cache(v_cache, batch, v->dim, v->num_heads, max_kv_len, unit, &p->vc)))
+        if ((st = take_cache(v_cache, batch, v->dim / dim_unit, v->num_heads, max_kv_len, unit,
+                             &p->vc)))
             return st;
         if (!same_layout(k_cache, v_cache)) return ATTN_ERR_UNSUPPORTED;
     }
@@ -235,8 +250,8 @@ extern "C" int attn_qk_norm_rope(const attn_head_rows_t *q, const attn_head_rows
     std::memset(&p, 0, sizeof(p));
     int st = take_rope(rope, &p.rope);
     if (st) return st;
-    if ((st = take_heads(*q, true, rope, num_rows, &p.q))) return st;
-    if (k && (st = take_heads(*k, true, rope, num_rows, &p.k))) return st;
+    if ((st = take_heads(*q, kToRows, rope, num_rows, &p.q))) return st;
+    if (k && (st = take_heads(*k, kToRows, rope, num_rows, &p.k))) return st;
     if (num_rows == 0) return ATTN_OK;
     if ((p.rope.rot_dim > 0 && !positions) || !aligned(positions, 4)) return ATTN_ERR_INVALID_ARG;
     p.positions = positions;
@@ -282,6 +297,27 @@ extern "C" int attn_append_kv_fp8(const attn_head_rows_t *q, const attn_head_row
     return map_cuda(launch_append_fp8(p, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+extern "C" int attn_append_kv_fp4(const attn_head_rows_t *q, const attn_head_rows_t *k,
+                                  const attn_head_rows_t *v, const attn_rope_t *rope,
+                                  const int32_t *positions, const attn_kv_t *k_cache,
+                                  const attn_kv_t *v_cache, const attn_kv_scale_t *k_scale,
+                                  const attn_kv_scale_t *v_scale, const uint32_t *kv_len,
+                                  const uint32_t *q_row_offsets, int batch, int num_q_rows,
+                                  int max_kv_len, attn_stream_t stream) {
+    RowsParams p;
+    int st = take_append(q, k, v, rope, positions, k_cache, v_cache, kv_len, q_row_offsets, batch,
+                         num_q_rows, max_kv_len, 32, &p, kToBoth, 2);
+    if (st || p.num_rows == 0) return st;
+    if (!v) return ATTN_ERR_INVALID_ARG;
+    if (k->dim != 128 || v->dim != 128 || max_kv_len > kMaxFp8Tokens) return ATTN_ERR_UNSUPPORTED;
+    if ((st = check_fp4(k_scale, k_cache)) || (st = check_fp4(v_scale, v_cache))) return st;
+    take_scale(k_scale, &p.kc);
+    take_scale(v_scale, &p.vc);
+    p.block_tokens = 1;
+    if ((st = device_error_word(&p.err))) return st;
+    return map_cuda(launch_append_fp4(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 extern "C" int attn_decode_fp8_workspace(int num_sms, int batch, int num_q_heads, int group,
                                          size_t *workspace_bytes) {
     if (!workspace_bytes || batch < 0 || num_q_heads <= 0 || group <= 0 || num_q_heads % group)
@@ -297,13 +333,19 @@ extern "C" int attn_decode_fp8_workspace(int num_sms, int batch, int num_q_heads
     return ATTN_OK;
 }
 
-extern "C" int attn_decode_fp8(const void *q, const attn_kv_t *k, const attn_kv_t *v,
-                               const attn_kv_scale_t *k_scale, const attn_kv_scale_t *v_scale,
-                               const uint32_t *kv_len, const uint32_t *q_row_offsets, int batch,
-                               int num_q_rows, int num_q_heads, int group, int head_dim,
-                               int max_q_len, int max_kv_len, float scale, const float *sink,
-                               int causal, void *workspace, size_t workspace_bytes, void *out,
-                               float *lse, attn_stream_t stream) {
+extern "C" int attn_decode_fp4_workspace(int num_sms, int batch, int num_q_heads, int group,
+                                         size_t *workspace_bytes) {
+    return attn_decode_fp8_workspace(num_sms, batch, num_q_heads, group, workspace_bytes);
+}
+
+// Decode over a cache held in codes: in 4 bits (fp4) or in 8.
+static int decode_codes(bool fp4, const void *q, const attn_kv_t *k, const attn_kv_t *v,
+                        const attn_kv_scale_t *k_scale, const attn_kv_scale_t *v_scale,
+                        const uint32_t *kv_len, const uint32_t *q_row_offsets, int batch,
+                        int num_q_rows, int num_q_heads, int group, int head_dim, int max_q_len,
+                        int max_kv_len, float scale, const float *sink, int causal,
+                        void *workspace, size_t workspace_bytes, void *out, float *lse,
+                        attn_stream_t stream) {
     if (batch < 0 || num_q_rows < 0 || num_q_heads <= 0 || group <= 0 || max_kv_len < 0 ||
         max_q_len < 1)
         return ATTN_ERR_INVALID_ARG;
@@ -323,11 +365,13 @@ extern "C" int attn_decode_fp8(const void *q, const attn_kv_t *k, const attn_kv_
     if (max_kv_len > kMaxFp8Tokens || most * batch * (hkv >> head_shift) > 0x7fffffffLL)
         return ATTN_ERR_UNSUPPORTED;
     CacheOut kc, vc;
-    int st = take_cache(k, batch, head_dim, hkv, max_kv_len, 16, &kc);
+    const int row_bytes = fp4 ? head_dim / 2 : head_dim, unit = fp4 ? 32 : 16;
+    int st = take_cache(k, batch, row_bytes, hkv, max_kv_len, unit, &kc);
     if (st) return st;
-    if ((st = take_cache(v, batch, head_dim, hkv, max_kv_len, 16, &vc))) return st;
+    if ((st = take_cache(v, batch, row_bytes, hkv, max_kv_len, unit, &vc))) return st;
     if (!same_layout(k, v)) return ATTN_ERR_UNSUPPORTED;
-    if ((st = check_scale(k_scale, k)) || (st = check_scale(v_scale, v))) return st;
+    const auto check = fp4 ? check_fp4 : check_scale;
+    if ((st = check(k_scale, k)) || (st = check(v_scale, v))) return st;
     if (k_scale->block_tokens != v_scale->block_tokens) return ATTN_ERR_UNSUPPORTED;
     // Units of one tile are never cut: no partials, nothing to merge.
     const bool cut = max_kv_len > kGqaTcTileKeys;
@@ -371,13 +415,11 @@ extern "C" int attn_decode_fp8(const void *q, const attn_kv_t *k, const attn_kv_
         p.unit_slots = reinterpret_cast<int2 *>(ws + off_table);
     }
     p.box_rows = k->page_table && k->page_size < kGqaTcTileKeys ? k->page_size : kGqaTcTileKeys;
-    if ((st = encode_kv_map_8bit(&p.k_map, k->base, k->token_stride, k->head_stride,
-                                 k->page_stride, head_dim, k->page_size, hkv, k->num_pages,
-                                 p.box_rows)))
-        return st;
-    if ((st = encode_kv_map_8bit(&p.v_map, v->base, v->token_stride, v->head_stride,
-                                 v->page_stride, head_dim, v->page_size, hkv, v->num_pages,
-                                 p.box_rows)))
+    const auto encode = fp4 ? encode_kv_map_4bit : encode_kv_map_8bit;
+    if ((st = encode(&p.k_map, k->base, k->token_stride, k->head_stride, k->page_stride, head_dim,
+                     k->page_size, hkv, k->num_pages, p.box_rows)) ||
+        (st = encode(&p.v_map, v->base, v->token_stride, v->head_stride, v->page_stride, head_dim,
+                     v->page_size, hkv, v->num_pages, p.box_rows)))
         return st;
     p.k_scale = k_scale->base;
     p.ks_page = k_scale->page_stride;
@@ -390,7 +432,7 @@ extern "C" int attn_decode_fp8(const void *q, const attn_kv_t *k, const attn_kv_
     p.block_shift = 0;
     while ((1 << p.block_shift) < k_scale->block_tokens) ++p.block_shift;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    st = map_cuda(launch_gqa_decode_fp8(p, ctas, s));
+    st = map_cuda(fp4 ? launch_gqa_decode_fp4(p, ctas, s) : launch_gqa_decode_fp8(p, ctas, s));
     if (st || !cut) return st;
     ReduceParams r;
     std::memset(&r, 0, sizeof(r));
@@ -410,4 +452,28 @@ extern "C" int attn_decode_fp8(const void *q, const attn_kv_t *k, const attn_kv_
     r.group = group;
     r.hkv = hkv;
     return map_cuda(launch_splitk_reduce(r, s, /*pdl=*/true));
+}
+
+extern "C" int attn_decode_fp8(const void *q, const attn_kv_t *k, const attn_kv_t *v,
+                               const attn_kv_scale_t *k_scale, const attn_kv_scale_t *v_scale,
+                               const uint32_t *kv_len, const uint32_t *q_row_offsets, int batch,
+                               int num_q_rows, int num_q_heads, int group, int head_dim,
+                               int max_q_len, int max_kv_len, float scale, const float *sink,
+                               int causal, void *workspace, size_t workspace_bytes, void *out,
+                               float *lse, attn_stream_t stream) {
+    return decode_codes(false, q, k, v, k_scale, v_scale, kv_len, q_row_offsets, batch, num_q_rows,
+                        num_q_heads, group, head_dim, max_q_len, max_kv_len, scale, sink, causal,
+                        workspace, workspace_bytes, out, lse, stream);
+}
+
+extern "C" int attn_decode_fp4(const void *q, const attn_kv_t *k, const attn_kv_t *v,
+                               const attn_kv_scale_t *k_scale, const attn_kv_scale_t *v_scale,
+                               const uint32_t *kv_len, const uint32_t *q_row_offsets, int batch,
+                               int num_q_rows, int num_q_heads, int group, int head_dim,
+                               int max_q_len, int max_kv_len, float scale, const float *sink,
+                               int causal, void *workspace, size_t workspace_bytes, void *out,
+                               float *lse, attn_stream_t stream) {
+    return decode_codes(true, q, k, v, k_scale, v_scale, kv_len, q_row_offsets, batch, num_q_rows,
+                        num_q_heads, group, head_dim, max_q_len, max_kv_len, scale, sink, causal,
+                        workspace, workspace_bytes, out, lse, stream);
 }

@@ -36,7 +36,7 @@ struct RopeParams {
 struct CacheOut {
     uint8_t *base;
     long long page_stride, token_stride, head_stride;
-    float *scale;                 // 8-bit caches
+    float *scale;                 // 8-bit caches (4-bit ones: see launch_append_fp4)
     long long scale_page, scale_block, scale_head;
 };
 
@@ -96,12 +96,22 @@ cudaError_t launch_fp8_runs(const RowsParams &p, bool behind_queries, cudaStream
 int fp8_decode_ctas(int num_sms);
 cudaError_t launch_gqa_decode_fp8(const Fp8DecodeParams &p, int ctas, cudaStream_t stream);
 
+// Caches held in 4 bits.  Their scales lie in the float words of CacheOut and
+// Fp8DecodeParams: four e8m0 bytes for a key, an fp32 number for a value.
+cudaError_t launch_append_fp4(const RowsParams &p, cudaStream_t stream);
+cudaError_t launch_gqa_decode_fp4(const Fp8DecodeParams &p, int ctas, cudaStream_t stream);
+
 // Address of the device error word in the current device's context (ATTN_OK
 // or ATTN_ERR_CUDA).
 int device_error_word(unsigned **out);
 // 4-D tensor map (channel, slot in page, KV head, page) over a cache operand
 // of 1-byte elements: boxes of 128 channels x box_rows slots, 128-byte swizzle.
 int encode_kv_map_8bit(CUtensorMap *map, const void *base, long long token_stride,
+                       long long head_stride, long long page_stride, int dim, int page_size,
+                       int num_kv_heads, int num_pages, int box_rows);
+// The same of two codes a byte (strides in bytes, multiples of 32), unpacked on the way to
+// 16 codes in the first 8 of 16 bytes.
+int encode_kv_map_4bit(CUtensorMap *map, const void *base, long long token_stride,
                        long long head_stride, long long page_stride, int dim, int page_size,
                        int num_kv_heads, int num_pages, int box_rows);
 

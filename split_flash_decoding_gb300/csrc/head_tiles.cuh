@@ -1,6 +1,6 @@
 // head_tiles.cuh -- norm and rotation of query and key heads over tiles of rows,
-// with the three ways the results go: rows of memory, slots of a bf16 cache, slots
-// of a cache held in 8 bits.
+// with the ways the results go: rows of memory, slots of a bf16 cache, slots of a
+// cache held in 8 bits or in 4.
 //
 // Bound by memory for prompts (each channel read and written once) and by latency
 // for a few rows.  A CTA takes a tile of rows and some of their heads.  Its threads
@@ -27,8 +27,13 @@
 // while the rows' maxima are joined over the block, and what the block holds from
 // before is rounded to a scale that grew.  64 single rows of 48 heads 4.4 us.  Runs
 // of more than 32 tokens have a kernel of their own (append_fp8_runs.cu).
+//
+// The 4-bit cache has scales within a token, so its tiles are those of the bf16 cache:
+// the lanes of a head join their largest values (a group of 32 channels is four lanes'
+// vectors in all but odd rotations) and store eight codes a word.
 #pragma once
 
+#include <cuda_fp4.h>
 #include <cuda_fp8.h>
 #include <float.h>
 
@@ -39,6 +44,7 @@ namespace tiles {
 
 constexpr int kGroupTokens = 128;     // 8-bit cache: aligned tokens of a tile
 constexpr int kMinExp = -60, kMaxExp = 120;
+constexpr int kFp4MaxExp = 125;       // 6 * 2^125 is finite
 
 // The launch's cut of the work.
 struct Cut {
@@ -47,7 +53,11 @@ struct Cut {
     int chunk_heads;                  // heads of a CTA
     int heads;                        // q, k and v heads together
     int any_norm;
+    int grouped;                      // 4-bit cache: four lanes hold whole groups of channels
 };
+
+// Where keys and values go: rows or a bf16 cache, a cache held in 8 bits, one in 4.
+enum Kind { kBf16, kFp8, kFp4 };
 
 constexpr int kThreads = 256;
 constexpr int kAhead = 3;             // heads whose vectors are on their way
@@ -65,12 +75,12 @@ struct Place {
 
 // The m-th vector (8 channels) of a head, the rotated ones first: R of them from
 // vector `start` on.
-__device__ __forceinline__ int ordered(int m, int R, int start) {
+__host__ __device__ __forceinline__ int ordered(int m, int R, int start) {
     return m < R ? start + m : m - R < start ? m - R : m;
 }
 
 // The vectors of lane i in that order (-1: none), `vecs` in all, R of them rotated.
-__device__ __forceinline__ void pair_of(bool inter, int vecs, int R, int i, int &a, int &b) {
+__host__ __device__ __forceinline__ void pair_of(bool inter, int vecs, int R, int i, int &a, int &b) {
     if (!inter && i < R / 2) {
         a = i;
         b = i + R / 2;
@@ -123,6 +133,13 @@ __device__ __forceinline__ int scale_exponent(float amax) {
 
 __device__ __forceinline__ float pow2i(int e) {   // -126 <= e <= 127
     return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+}
+
+// Exponent of a scale of the 4-bit cache, from the bits of the largest |value|: the least e
+// with that <= 6 * 2^e (6 = 1.5 * 2^2), clamped.
+__device__ __forceinline__ int fp4_exponent(uint32_t bits) {
+    const int e = static_cast<int>(bits >> 23) - 127;            // (0 and subnormal: clamped)
+    return min(max(e - ((bits & 0x7fffffu) > 0x400000u ? 1 : 2), kMinExp), kFp4MaxExp);
 }
 
 // Largest finite |value| (infinities and NaN do not count).
@@ -445,10 +462,86 @@ struct Item {
     }
 };
 
-// kMany: a CTA has more heads than it works on at once (never with kFp8).
-template <int L, bool kInter, bool kFp8, bool kMany>
-__global__ void __launch_bounds__(kThreads, kFp8 ? 2 : kMany ? 3 : 4)
+// One head of a row, on 8 lanes, into a cache held in 4 bits; y: the lane's two vectors.
+// The largest value decides by its bits, as a number above all finite ones where an
+// infinity or a NaN is among them: the scale is NaN then.  The code of x 2^-e is rounded
+// once, as the product is exact.
+__device__ __forceinline__ void store_fp4(const RowsParams &p, const Place &at, int kind, int head,
+                                          int row, int ca, int cb, bool grouped,
+                                          const float2 (&ya)[4], const float2 (&yb)[4]) {
+    // (a warp's other heads may be queries: the eight lanes go by themselves)
+    const unsigned mine = 0xffu << (threadIdx.x & 24);
+    uint32_t ta = 0, tb = 0;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        ta = max(max(ta, __float_as_uint(fabsf(ya[c].x))), __float_as_uint(fabsf(ya[c].y)));
+        tb = max(max(tb, __float_as_uint(fabsf(yb[c].x))), __float_as_uint(fabsf(yb[c].y)));
+    }
+    if (kind == 2) {                                             // values: one scale
+        ta = max(ta, tb);
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) ta = max(ta, __shfl_xor_sync(mine, ta, o));
+        tb = ta;
+    } else if (grouped) {
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) {
+            ta = max(ta, __shfl_xor_sync(mine, ta, o));
+            tb = max(tb, __shfl_xor_sync(mine, tb, o));
+        }
+    } else {
+        uint32_t m[4];
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            m[g] = max(ca >> 5 == g ? ta : 0u, cb >> 5 == g ? tb : 0u);
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1) m[g] = max(m[g], __shfl_xor_sync(mine, m[g], o));
+        }
+        ta = ca >> 5 == 0 ? m[0] : ca >> 5 == 1 ? m[1] : ca >> 5 == 2 ? m[2] : m[3];
+        tb = cb >> 5 == 0 ? m[0] : cb >> 5 == 1 ? m[1] : cb >> 5 == 2 ? m[2] : m[3];
+    }
+    const HeadRows &x = kind == 1 ? p.k : p.v;
+    const CacheOut &c = kind == 1 ? p.kc : p.vc;
+    const long long head_at = head * c.head_stride + (kind == 1 ? at.k_at : at.v_at);
+    uint8_t *scale = reinterpret_cast<uint8_t *>(c.scale + at.page * c.scale_page +
+                                                 at.slot * c.scale_block + head * c.scale_head);
+    const auto half = [&](uint32_t top, int ch, const float2 (&y)[4]) {
+        const bool whole = top < 0x7f800000u;
+        const int e = fp4_exponent(top);
+        const float f = pow2i(-e);
+        uint32_t word = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            word |= uint32_t(__nv_cvt_float2_to_fp4x2(__fmul2_rn(y[i], make_float2(f, f)), __NV_E2M1,
+                                                      cudaRoundNearest)) << (8 * i);
+        if (!whole) word = 0;
+        if (at.stored > 0) {
+            *reinterpret_cast<uint32_t *>(c.base + head_at + ch / 2) = word;
+            if (kind == 1 && (ch & 31) == 0) scale[ch >> 5] = whole ? uint8_t(e + 127) : 255;
+            if (kind == 2 && ch == 0)
+                *reinterpret_cast<float *>(scale) = whole ? pow2i(e) : __uint_as_float(0x7fffffffu);
+        }
+        if (x.out && at.stored >= 0) {                           // what the codes stand for
+            const float s = whole ? pow2i(e) : __uint_as_float(0x7fffffffu);
+            float2 v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                v[i] = __fmul2_rn(__half22float2(__half2(__nv_cvt_fp4x2_to_halfraw2(
+                                      static_cast<__nv_fp4x2_storage_t>(word >> (8 * i) & 0xffu),
+                                      __NV_E2M1))),
+                                  make_float2(s, s));
+            *reinterpret_cast<uint4 *>(x.out + row * x.out_row + head * x.out_head + ch) = pack8(v);
+        }
+    };
+    half(ta, ca, ya);
+    half(tb, cb, yb);
+}
+
+// kMany: a CTA has more heads than it works on at once (never with the 8-bit cache).
+template <int L, bool kInter, Kind kKind, bool kMany>
+__global__ void __launch_bounds__(kThreads, kKind == kFp8 ? 2 : kMany ? 3 : 4)
 head_tiles_kernel(const __grid_constant__ RowsParams p, const __grid_constant__ Cut cut) {
+    constexpr bool kFp8 = kKind == tiles::kFp8;
+    static_assert(kKind != kFp4 || L == 8, "a 4-bit head is 128 channels on 8 lanes");
     constexpr int kItems = kItemsOf<L>;
     extern __shared__ __align__(16) float4 angles[];             // [rows][4][lanes]
     __shared__ Place places[kItems];
@@ -598,7 +691,9 @@ head_tiles_kernel(const __grid_constant__ RowsParams p, const __grid_constant__ 
             for (int k = 0; k < 4; ++k)
                 rotate_pairs<kInter>(ya[k], yb[k], t[k * L], it.flags & Item::kTurnB);
         }
-        if (!kFp8 || it.kind == 0) {
+        if (kKind == kFp4 && it.kind != 0) {
+            store_fp4(p, at, it.kind, it.head, r0 + it.row, it.ca, it.cb, cut.grouped != 0, ya, yb);
+        } else if (!kFp8 || it.kind == 0) {
             uint16_t *dst = it.dst;
             bool store = at.stored >= 0;
             if (!kFp8 && it.to_cache) {
@@ -701,7 +796,7 @@ head_tiles_kernel(const __grid_constant__ RowsParams p, const __grid_constant__ 
     }
 }
 
-template <int L, bool kFp8, bool kMany>
+template <int L, Kind kKind, bool kMany>
 cudaError_t launch(const RowsParams &p, const Cut &cut, long long tiles, cudaStream_t stream) {
     const long long blocks = tiles * cut.chunks;
     if (blocks == 0) return cudaSuccess;
@@ -709,8 +804,8 @@ cudaError_t launch(const RowsParams &p, const Cut &cut, long long tiles, cudaStr
     const size_t smem =                                              // up to 48 KB
         (p.rope.rot_dim > 0 ? size_t(cut.tile_rows) * 4 * L * sizeof(float4) : 0) +
         (kMany ? size_t(kAhead + 1) * 2 * kThreads * sizeof(uint4) : 0);
-    auto kern = p.rope.interleaved ? head_tiles_kernel<L, true, kFp8, kMany>
-                                   : head_tiles_kernel<L, false, kFp8, kMany>;
+    auto kern = p.rope.interleaved ? head_tiles_kernel<L, true, kKind, kMany>
+                                   : head_tiles_kernel<L, false, kKind, kMany>;
     if (smem > 40 * 1024) {                                          // (48 KB with the static part)
         const cudaError_t e =
             cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
@@ -718,6 +813,36 @@ cudaError_t launch(const RowsParams &p, const Cut &cut, long long tiles, cudaStr
     }
     kern<<<static_cast<unsigned>(blocks), kThreads, smem, stream>>>(p, cut);
     return cudaGetLastError();
+}
+
+// Tiles of rows over the GPU; grouped: for a 4-bit cache.
+template <int L, Kind kKind>
+cudaError_t launch_lanes(const RowsParams &p, cudaStream_t stream, bool grouped = false) {
+    // Tiles of 8 rows: a step then reads 256 / L / 8 heads side by side of every row
+    // (1 KB at 128 channels), and the angles of a tile are two a thread.  16 rows where
+    // each row's place has to be found and there are enough of them: a CTA's start is
+    // longer then.  A CTA takes all heads of its rows once the tiles fill the GPU,
+    // fewer below.  us with 4, 8, 16 rows:
+    //   norms, 40 heads: 1000 rows 8.6, 8.2, 8.9; 8191 37.7, 32.7, 34.9; 16384 69.4, 57.3,
+    //   60.2; 32768 132.8, 107.3, 108.0
+    //   to a cache, 48 heads: 3096 rows (8, 16) 20.6, 21.8; 6192 34.1, 33.1; 24768 104.8, 98.6
+    constexpr int kWave = 3 * 152;                 // resident CTAs
+    Cut cut;
+    cut.grouped = grouped;
+    cut.heads = p.q.heads + p.k.heads + p.v.heads;
+    cut.any_norm = (p.q.heads > 0 && p.q.norm_dim > 0) || (p.k.heads > 0 && p.k.norm_dim > 0);
+    cut.tile_rows = p.kv_len && p.num_rows >= 16 * 2 * 152 ? 16 : 8;
+    while (cut.tile_rows > 1 && cut.tile_rows / 2 >= p.num_rows) cut.tile_rows /= 2;
+    const long long tiles = (static_cast<long long>(p.num_rows) + cut.tile_rows - 1) / cut.tile_rows;
+    const int step = kItemsOf<L> / cut.tile_rows;        // heads at once
+    const int steps = (cut.heads + step - 1) / step;
+    long long per_cta = steps * tiles / kWave;
+    if (per_cta < 1) per_cta = 1;
+    if (per_cta > steps) per_cta = steps;
+    cut.chunk_heads = static_cast<int>(per_cta) * step;
+    cut.chunks = (cut.heads + cut.chunk_heads - 1) / cut.chunk_heads;
+    return per_cta > 1 ? launch<L, kKind, true>(p, cut, tiles, stream)
+                       : launch<L, kKind, false>(p, cut, tiles, stream);
 }
 
 }  // namespace tiles

@@ -20,13 +20,14 @@ cudaError_t launch_fp8_tiles(const RowsParams &p, bool behind_queries, cudaStrea
     const int longest = longest_run(p);
     if (longest > kItemsOf<8>) return launch_fp8_runs(p, behind_queries, stream);
     Cut cut;
+    cut.grouped = 0;
     cut.heads = p.q.heads + p.k.heads + p.v.heads;
     cut.any_norm = (p.q.heads > 0 && p.q.norm_dim > 0) || p.k.norm_dim > 0;
     cut.tile_rows = 1;
     while (cut.tile_rows < longest) cut.tile_rows *= 2;
     cut.chunk_heads = kItemsOf<8> / cut.tile_rows;               // heads at once
     cut.chunks = (cut.heads + cut.chunk_heads - 1) / cut.chunk_heads;
-    return launch<8, true, false>(p, cut, fp8_tile_count(p), stream);
+    return launch<8, kFp8, false>(p, cut, fp8_tile_count(p), stream);
 }
 
 }  // namespace attn
