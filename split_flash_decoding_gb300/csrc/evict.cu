@@ -25,13 +25,16 @@ namespace cg = cooperative_groups;
 namespace attn {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kMaxCluster = 8;
-constexpr int kHeldKeys = 32768;             // weights of a CTA kept in shared memory (128 KB)
+constexpr int kMostPer = 16;                 // weights of a thread kept in registers
+constexpr int kHeldKeys = 32768;             // of a CTA, past that, kept in shared memory (128 KB)
 
 // A weight as a number whose order is that of weights: -0 counts as 0, NaN as -inf.
+// (kStays is above all of them, 0 below.)
+constexpr uint32_t kStays = 0xffffffffu;
 __device__ __forceinline__ uint32_t sort_key(float w) {
     if (!(w == w)) w = -INFINITY;
     const uint32_t u = __float_as_uint(w + 0.f);
@@ -68,24 +71,46 @@ __device__ __forceinline__ Lengths lengths_of(const EvictParams &p, int b) {
     return x;
 }
 
+constexpr int kPasses = 3;                   // digits of 11, 11 and 10 bits
+
 struct Shared {
-    int hist[kBins];
-    int merged[kBins];               // counts of all CTAs of the cluster
+    int hist[kPasses][kBins];        // this CTA's counts
     int warp_sum[kWarps];
     int warp_more[kWarps], warp_equal[kWarps];
     int counts[2];                   // this CTA's kept for sure, and equal to the threshold
-    int digit, rest;                 // of the last pass: the digit, and what is wanted inside it
+    int merged[kPasses][kBins];      // first CTA of a cluster: the counts of all
+    int digit, rest, all;            // of a pass: the digit, what is wanted of its keys, how many it has
 };
 
-__global__ void __launch_bounds__(kThreads)
+// Sum over the warps before this one, of a value for each warp (in shared memory), by
+// every warp for itself; total: of all.
+__device__ __forceinline__ int before_warp(const int *sums, int warp, int lane, int &total) {
+    static_assert(kWarps == 32, "a lane a warp");
+    const int mine = sums[lane];
+    total = __reduce_add_sync(0xffffffffu, mine);
+    return __reduce_add_sync(0xffffffffu, lane < warp ? mine : 0);
+}
+
+__device__ __forceinline__ int warp_inclusive(int v, int lane) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += u;
+    }
+    return v;
+}
+
+// kPer: tokens of a thread, whose keys stay in registers; 0: any number, their keys in
+// shared memory or, past held_keys, read again for every digit.
+template <int kRanks, int kPer>
+__global__ void __launch_bounds__(kThreads, 1)
 evict_select_kernel(const __grid_constant__ EvictParams p, int held_keys) {
     extern __shared__ __align__(16) uint8_t raw[];
     Shared &sh = *reinterpret_cast<Shared *>(raw);
     uint32_t *keys = reinterpret_cast<uint32_t *>(raw + sizeof(Shared));
     cg::cluster_group cluster = cg::this_cluster();
-    const int ranks = static_cast<int>(cluster.num_blocks());
-    const int rank = static_cast<int>(cluster.block_rank());
-    const int unit = static_cast<int>(blockIdx.x) / ranks;
+    const int rank = kRanks > 1 ? static_cast<int>(cluster.block_rank()) : 0;
+    const int unit = static_cast<int>(blockIdx.x) / kRanks;
     const int b = unit / p.hkv, kvh = unit - b * p.hkv;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pdl_launch_dependents();
@@ -97,7 +122,7 @@ evict_select_kernel(const __grid_constant__ EvictParams p, int held_keys) {
         if (p.kept_len) p.kept_len[b] = uint32_t(x.n);
     }
     // Tokens [t0, t1) are this CTA's; a warp has a run of them, of whole 32s.
-    const int slice = ((x.L + ranks - 1) / ranks + kThreads - 1) / kThreads * kThreads;
+    const int slice = ((x.L + kRanks - 1) / kRanks + kThreads - 1) / kThreads * kThreads;
     const int t0 = min(rank * slice, x.L), t1 = min(t0 + slice, x.L);
     const int run = slice / kWarps;
     const int w0 = min(t0 + warp * run, t1), w1 = min(w0 + run, t1);
@@ -106,89 +131,130 @@ evict_select_kernel(const __grid_constant__ EvictParams p, int held_keys) {
     const bool choose = wanted > 0 && wanted < c1 - c0;
     const bool held = slice <= held_keys;
 
-    const auto read_key = [&](int t) -> uint32_t {
+    const float *weights = p.w.base + kvh * p.w.head;
+    const auto where = [&](int t) -> const float * {
         int slot;
         const int page = page_in(p.page_table, p.max_pages, p.num_pages, p.page_size, b, t, p.err,
                                  slot);
-        return page < 0 ? 0u : sort_key(p.w.base[page * p.w.page + slot * p.w.token +
-                                                 kvh * p.w.head]);
+        return page < 0 ? nullptr : weights + page * p.w.page + slot * p.w.token;
     };
-    const auto key_of = [&](int t) -> uint32_t { return held ? keys[t - t0] : read_key(t); };
+    // The key of token t of this CTA: kStays for those that stay whatever their weight.
+    const auto read_key = [&](int t) -> uint32_t {
+        if (t < c0 || t >= c1) return kStays;
+        if (!choose) return 0u;
+        const float *at = where(t);
+        return at ? sort_key(*at) : 0u;
+    };
+    uint32_t mine[kPer > 0 ? kPer : 1] = {};
+    // f(t, index) for this thread's tokens and, all lanes of a warp at once, what is past them
+    const auto each = [&](auto f) {
+        if constexpr (kPer > 0) {
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                if (32 * i < run) f(w0 + lane + 32 * i, i);      // (uniform)
+            }
+        } else {
+            for (int t = w0 + lane; t - lane < w1; t += 32) f(t, 0);
+        }
+    };
+    const auto key_of = [&](int t, int i) -> uint32_t {
+        if (kPer > 0) return mine[i];
+        return t >= w1 ? 0u : held ? keys[t - t0] : read_key(t);
+    };
 
-    uint32_t least = 0;                      // the smallest weight that stays
-    int take = 0;                            // how many of those equal to it
+    if constexpr (kPer > 0) {
+        // eight tokens' page numbers first, then their weights: two waits for eight
+        constexpr int kBatch = kPer < 8 ? kPer : 8;
+#pragma unroll
+        for (int i0 = 0; i0 < kPer; i0 += kBatch) {
+            const float *at[kBatch];
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                const int i = i0 + u, t = w0 + lane + 32 * i;
+                const bool stays = t < c0 || t >= c1;
+                mine[i] = stays ? kStays : 0u;
+                at[u] = choose && !stays && 32 * i < run && t < w1 ? where(t) : nullptr;
+            }
+            float w[kBatch];
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) w[u] = at[u] ? *at[u] : 0.f;
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u)
+                if (at[u]) mine[i0 + u] = sort_key(w[u]);
+        }
+    } else if (held) {
+        for (int t = w0 + lane; t < w1; t += 32) keys[t - t0] = read_key(t);
+    }
+
+    uint32_t least = 0, mask = choose ? 0u : ~0u;   // the smallest weight that stays, its known digits
+    int rest = wanted;                       // how many of those equal to it, as far as known
     if (choose) {
-        if (held)
-            for (int t = t0 + tid; t < t1; t += kThreads) keys[t - t0] = read_key(t);
-        int rest = wanted;
-        uint32_t mask = 0;
+        for (int i = tid; i < kPasses * kBins; i += kThreads) (&sh.hist[0][0])[i] = 0;
+        if (kRanks > 1) {
+            for (int i = tid; i < kPasses * kBins; i += kThreads) (&sh.merged[0][0])[i] = 0;
+            cluster.sync();                  // (before other CTAs add to them)
+        }
+        __syncthreads();
 #pragma unroll 1
-        for (int pass = 0; pass < 3; ++pass) {
+        for (int pass = 0; pass < kPasses; ++pass) {
             const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
             const uint32_t bits = pass == 2 ? 1023u : 2047u;
-            for (int i = tid; i < kBins; i += kThreads) sh.hist[i] = 0;
+            int *hist = sh.hist[pass];
+            each([&](int t, int i) {
+                const uint32_t key = key_of(t, i);
+                if ((key & mask) == least && key != kStays && t < w1)
+                    atomicAdd(&hist[(key >> shift) & bits], 1);
+            });
             __syncthreads();
-            for (int t = max(t0, c0) + tid; t < min(t1, c1); t += kThreads) {
-                const uint32_t key = key_of(t);
-                if ((key & mask) == least) atomicAdd(&sh.hist[(key >> shift) & bits], 1);
+            if (kRanks > 1) {                // to the first CTA of the cluster, which does the rest
+                int *to = cluster.map_shared_rank(sh.merged[pass], 0);
+                for (int i = tid; i < kBins; i += kThreads) {
+                    const int c = hist[i];
+                    if (c) atomicAdd(to + i, c);
+                }
+                cluster.sync();
+                hist = sh.merged[pass];
             }
-            cluster.sync();
-            for (int i = tid; i < kBins; i += kThreads) {
-                int sum = 0;
-                for (int r = 0; r < ranks; ++r) sum += *cluster.map_shared_rank(&sh.hist[i], r);
-                sh.merged[i] = sum;
-            }
-            __syncthreads();
-            // the digit d with fewer than `rest` keys above it, and at least that many from it on
-            int mine[kBins / kThreads], local = 0;
-#pragma unroll
-            for (int i = 0; i < kBins / kThreads; ++i) {
-                mine[i] = sh.merged[kBins - 1 - (tid * (kBins / kThreads) + i)];
-                local += mine[i];
-            }
-            int incl = local;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(0xffffffffu, incl, o);
-                if (lane >= o) incl += v;
-            }
-            if (lane == 31) sh.warp_sum[warp] = incl;
-            __syncthreads();
-            int above = incl - local;
-            for (int i = 0; i < warp; ++i) above += sh.warp_sum[i];
-            if (above < rest && above + local >= rest) {
-#pragma unroll
-                for (int i = 0; i < kBins / kThreads; ++i) {
-                    if (above < rest && above + mine[i] >= rest) {
-                        sh.digit = kBins - 1 - (tid * (kBins / kThreads) + i);
-                        sh.rest = rest - above;
+            // The digit with fewer than `rest` keys above it, and at least that many from it
+            // on; thread t has the bins 2 t and 2 t + 1 from above.
+            static_assert(kBins == 2 * kThreads, "two bins a thread");
+            if (rank == 0) {
+                const int top = kBins - 1 - 2 * tid;
+                const int n0 = hist[top], n1 = hist[top - 1], local = n0 + n1;
+                const int incl = warp_inclusive(local, lane);
+                if (lane == 31) sh.warp_sum[warp] = incl;
+                __syncthreads();
+                int total;
+                const int above = before_warp(sh.warp_sum, warp, lane, total) + incl - local;
+                if (above < rest && above + local >= rest) {
+                    const bool first = above + n0 >= rest;
+                    for (int r = 0; r < kRanks; ++r) {
+                        Shared *to = kRanks > 1 ? cluster.map_shared_rank(&sh, r) : &sh;
+                        to->digit = first ? top : top - 1;
+                        to->rest = rest - above - (first ? 0 : n0);
+                        to->all = first ? n0 : n1;
                     }
-                    above += mine[i];
                 }
             }
-            cluster.sync();                  // (also: the others have read this CTA's counts)
+            if (kRanks > 1) cluster.sync(); else __syncthreads();
             least |= uint32_t(sh.digit) << shift;
             mask |= bits << shift;
             rest = sh.rest;
-            __syncthreads();
+            if (rest == sh.all) break;       // all keys of these digits stay: no need of the others
+            // (the next pass writes these behind its first barriers)
         }
-        take = rest;
     }
 
     // ---- what stays, per warp and CTA -------------------------------------------------
-    // 0: goes; 1: stays; 2: stays if it is among the first `take` of its weight
-    const auto kind_of = [&](int t) -> int {
-        if (t < c0 || t >= c1) return 1;
-        if (!choose) return wanted > 0;
-        const uint32_t key = key_of(t);
-        return key > least ? 1 : key == least ? 2 : 0;
-    };
+    // more: above the least key that stays; equal: that key, of which the first `rest` stay
     int more = 0, equal = 0;
-    for (int t = w0 + lane; t < w1; t += 32) {
-        const int kind = kind_of(t);
-        more += kind == 1;
-        equal += kind == 2;
-    }
+    each([&](int t, int i) {
+        const uint32_t key = key_of(t, i) & mask;
+        if (t < w1) {
+            more += key > least;
+            equal += key == least;
+        }
+    });
     more = __reduce_add_sync(0xffffffffu, more);
     equal = __reduce_add_sync(0xffffffffu, equal);
     if (lane == 0) {
@@ -196,47 +262,50 @@ evict_select_kernel(const __grid_constant__ EvictParams p, int held_keys) {
         sh.warp_equal[warp] = equal;
     }
     __syncthreads();
-    if (tid == 0) {
-        int m = 0, e = 0;
-        for (int i = 0; i < kWarps; ++i) {
-            m += sh.warp_more[i];
-            e += sh.warp_equal[i];
+    int all_more, all_equal;
+    int base = before_warp(sh.warp_more, warp, lane, all_more);
+    int equals = before_warp(sh.warp_equal, warp, lane, all_equal);   // before this warp
+    if constexpr (kRanks > 1) {
+        if (tid == 0) {
+            sh.counts[0] = all_more;
+            sh.counts[1] = all_equal;
         }
-        sh.counts[0] = m;
-        sh.counts[1] = e;
+        cluster.sync();
+        const int *c = cluster.map_shared_rank(sh.counts, lane < rank ? lane : rank);
+        const int m = c[0], e = c[1];
+        base += __reduce_add_sync(0xffffffffu, lane < rank ? m : 0);
+        equals += __reduce_add_sync(0xffffffffu, lane < rank ? e : 0);
     }
-    cluster.sync();
-    int base = 0, equals = 0;                // before this warp
-    for (int r = 0; r < rank; ++r) {
-        const int *c = cluster.map_shared_rank(sh.counts, r);
-        base += c[0];
-        equals += c[1];
-    }
-    for (int i = 0; i < warp; ++i) {
-        base += sh.warp_more[i];
-        equals += sh.warp_equal[i];
-    }
-    base += min(equals, take);
+    base += min(equals, rest);
     int32_t *out = p.indices + (size_t(b) * p.hkv + kvh) * p.max_keep;
-    for (int t = w0; t < w1; t += 32) {
-        const int kind = t + lane < w1 ? kind_of(t + lane) : 0;
-        const uint32_t below = (1u << lane) - 1u;
-        const uint32_t eq = __ballot_sync(0xffffffffu, kind == 2);
-        const bool stays = kind == 1 || (kind == 2 && equals + __popc(eq & below) < take);
+    const uint32_t below = (1u << lane) - 1u;
+    each([&](int t, int i) {
+        const uint32_t key = key_of(t, i) & mask;
+        bool stays = key > least && t < w1;
+        const uint32_t eq = __ballot_sync(0xffffffffu, key == least && t < w1);
+        if (eq) {                                  // (uniform)
+            stays = stays || ((eq >> lane & 1u) && equals + __popc(eq & below) < rest);
+            equals += __popc(eq);
+        }
         const uint32_t in = __ballot_sync(0xffffffffu, stays);
         const int j = base + __popc(in & below);
-        if (stays && j < x.n) out[j] = t + lane;   // (j < n unless weights change meanwhile)
+        if (stays && j < x.n) out[j] = t;          // (j < n unless weights change meanwhile)
         base += __popc(in);
-        equals += __popc(eq);
-    }
-    cluster.sync();                          // (the others have read this CTA's counts)
+    });
+    if (kRanks > 1) cluster.sync();          // (the others have read this CTA's counts)
 }
 
 // ---- the rows -----------------------------------------------------------------------
 
 constexpr int kMoveThreads = 256;
-constexpr int kMoveSlots = 16;               // kept tokens of a CTA
-constexpr int kMoveAhead = 4;                // vectors of a thread on their way
+constexpr int kMoveWarps = kMoveThreads / 32;
+constexpr int kMoveEntries = 256;            // (slot, head) pairs of a CTA, at most
+constexpr int kMoveAhead = 4;                // rows of a warp's lanes on their way
+
+// Where an entry's rows are and go, in bytes from the caches' bases; k_from < 0: nowhere.
+struct Entry {
+    long long k_from, v_from, k_to, v_to;
+};
 
 __device__ __forceinline__ uint4 load_once(const uint8_t *p) {
     uint4 v;
@@ -245,105 +314,140 @@ __device__ __forceinline__ uint4 load_once(const uint8_t *p) {
     return v;
 }
 
+// Copies the entries' rows of one cache, 2^lanes_shift lanes a row.
+template <bool kIsK>
+__device__ __forceinline__ void move_rows(const MovedRows &m, const Entry *entries, int count,
+                                          int lanes_shift) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int per_warp = 32 >> lanes_shift, step = kMoveWarps * per_warp;
+    const int e_of = warp * per_warp + (lane >> lanes_shift), c_of = lane & ((1 << lanes_shift) - 1);
+    for (int e0 = e_of; e0 < count; e0 += step * kMoveAhead) {
+        long long from[kMoveAhead], to[kMoveAhead];
+#pragma unroll
+        for (int u = 0; u < kMoveAhead; ++u) {
+            const int e = e0 + u * step;
+            const Entry *at = entries + (e < count ? e : e0);
+            from[u] = e < count && at->k_from >= 0 ? (kIsK ? at->k_from : at->v_from) : -1;
+            to[u] = kIsK ? at->k_to : at->v_to;
+        }
+        for (int c = c_of; c < m.vecs; c += 32) {
+            uint4 v[kMoveAhead];
+#pragma unroll
+            for (int u = 0; u < kMoveAhead; ++u)
+                if (from[u] >= 0) v[u] = load_once(m.from + from[u] + 16 * c);
+#pragma unroll
+            for (int u = 0; u < kMoveAhead; ++u)
+                if (from[u] >= 0) *reinterpret_cast<uint4 *>(m.to + to[u] + 16 * c) = v[u];
+        }
+    }
+}
+
 __global__ void __launch_bounds__(kMoveThreads)
-evict_move_kernel(const __grid_constant__ EvictParams p) {
-    extern __shared__ __align__(16) int2 from[];         // {page, slot} [kMoveSlots][hkv]
-    __shared__ int2 to[kMoveSlots];
-    const int b = blockIdx.y, j0 = static_cast<int>(blockIdx.x) * kMoveSlots;
+evict_move_kernel(const __grid_constant__ EvictParams p, int slots_of_cta, int k_shift, int v_shift) {
+    __shared__ Entry entries[kMoveEntries];
+    const int b = blockIdx.y, j0 = static_cast<int>(blockIdx.x) * slots_of_cta;
     const int tid = threadIdx.x;
     const Lengths x = lengths_of(p, b);
-    const int slots = min(kMoveSlots, x.n - j0);
+    const int slots = min(slots_of_cta, x.n - j0);
     if (slots <= 0) return;
-    if (tid < slots) {
-        int slot;
-        const int page = page_in(p.to_table, p.to_max_pages, p.to_num_pages, p.to_page_size, b,
-                                 j0 + tid, p.err, slot);
-        to[tid] = make_int2(page, slot);
-    }
+    const int count = slots * p.hkv;
+    // an entry a thread, a token's heads side by side
+    const int s = tid / p.hkv, h = tid - s * p.hkv;
+    int page_to = -1, slot_to = 0;
+    if (tid < count)
+        page_to = page_in(p.to_table, p.to_max_pages, p.to_num_pages, p.to_page_size, b, j0 + s, p.err,
+                          slot_to);
     pdl_wait_primary();
-    for (int i = tid; i < slots * p.hkv; i += kMoveThreads) {
-        const int h = i / slots, s = i - h * slots;
+    if (tid < count) {
         const int t = p.indices[(size_t(b) * p.hkv + h) * p.max_keep + j0 + s];
         int slot = 0, page = -1;
         if (t >= 0 && t < x.L)
             page = page_in(p.page_table, p.max_pages, p.num_pages, p.page_size, b, t, nullptr, slot);
-        from[s * p.hkv + h] = make_int2(page, slot);
+        Entry at;
+        at.k_from = page * p.k.from_page + slot * p.k.from_token + h * p.k.from_head;
+        at.v_from = page * p.v.from_page + slot * p.v.from_token + h * p.v.from_head;
+        at.k_to = page_to * p.k.to_page + slot_to * p.k.to_token + h * p.k.to_head;
+        at.v_to = page_to * p.v.to_page + slot_to * p.v.to_token + h * p.v.to_head;
+        const bool moves = page >= 0 && page_to >= 0;
+        if (!moves) at.k_from = -1;
+        entries[tid] = at;
+        if (moves && p.w_to.base)
+            p.w_to.base[page_to * p.w_to.page + slot_to * p.w_to.token + h * p.w_to.head] =
+                p.w.base[page * p.w.page + slot * p.w.token + h * p.w.head];
     }
     __syncthreads();
-    if (p.w_to.base)
-        for (int i = tid; i < slots * p.hkv; i += kMoveThreads) {
-            const int s = i / p.hkv, h = i - s * p.hkv;
-            const int2 f = from[i], d = to[s];
-            if (f.x >= 0 && d.x >= 0)
-                p.w_to.base[d.x * p.w_to.page + d.y * p.w_to.token + h * p.w_to.head] =
-                    p.w.base[f.x * p.w.page + f.y * p.w.token + h * p.w.head];
-        }
-    // vectors of a token: its heads' K, then its heads' V
-    const int kv = p.k.vecs + p.v.vecs, per_slot = p.hkv * kv, all = slots * per_slot;
-    for (int i0 = tid; i0 < all; i0 += kMoveThreads * kMoveAhead) {
-        uint4 v[kMoveAhead];
-        uint8_t *dst[kMoveAhead];
-#pragma unroll
-        for (int u = 0; u < kMoveAhead; ++u) {
-            const int i = i0 + u * kMoveThreads;
-            dst[u] = nullptr;
-            if (i >= all) continue;
-            const int s = i / per_slot;
-            int c = i - s * per_slot;
-            const bool is_k = c < p.hkv * p.k.vecs;
-            const MovedRows &m = is_k ? p.k : p.v;
-            if (!is_k) c -= p.hkv * p.k.vecs;
-            const int h = c / m.vecs;
-            c -= h * m.vecs;
-            const int2 f = from[s * p.hkv + h], d = to[s];
-            if (f.x < 0 || d.x < 0) continue;
-            v[u] = load_once(m.from + f.x * m.from_page + f.y * m.from_token + h * m.from_head +
-                             16 * c);
-            dst[u] = m.to + d.x * m.to_page + d.y * m.to_token + h * m.to_head + 16 * c;
-        }
-#pragma unroll
-        for (int u = 0; u < kMoveAhead; ++u)
-            if (dst[u]) *reinterpret_cast<uint4 *>(dst[u]) = v[u];
-    }
+    move_rows<true>(p.k, entries, count, k_shift);
+    if (p.v.vecs > 0) move_rows<false>(p.v, entries, count, v_shift);
+}
+
+// Lanes of a row of `vecs` vectors, as a power of two.
+int lanes_of(int vecs) {
+    int shift = 0;
+    while (shift < 5 && (1 << shift) < vecs) ++shift;
+    return shift;
+}
+
+template <int kRanks, int kPer>
+cudaError_t launch_select(const EvictParams &p, int slice, cudaStream_t stream) {
+    const int held = kPer > 0 ? 0 : slice < kHeldKeys ? slice : kHeldKeys;
+    auto kern = evict_select_kernel<kRanks, kPer>;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(p.batch * p.hkv * kRanks));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = sizeof(Shared) + sizeof(uint32_t) * size_t(held);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kRanks;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         int(cfg.dynamicSmemBytes));
+    if (e != cudaSuccess) return e;
+    return cudaLaunchKernelEx(&cfg, kern, p, held);
+}
+
+template <int kRanks>
+cudaError_t launch_ranks(const EvictParams &p, cudaStream_t stream) {
+    const int slice = ((p.max_kv_len + kRanks - 1) / kRanks + kThreads - 1) / kThreads * kThreads;
+    if (slice <= kThreads && kRanks == 1) return launch_select<kRanks, 1>(p, slice, stream);
+    if (slice <= 4 * kThreads) return launch_select<kRanks, 4>(p, slice, stream);
+    if (slice <= 8 * kThreads) return launch_select<kRanks, 8>(p, slice, stream);
+    if (slice <= kMostPer * kThreads) return launch_select<kRanks, kMostPer>(p, slice, stream);
+    return launch_select<kRanks, 0>(p, slice, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_evict(const EvictParams &p, int sms, cudaStream_t stream) {
-    // CTAs of a unit: until the GPU is full, or the weights of one no longer fit it.
+    // CTAs of a unit (one an SM, of 1024 threads): as many as fill the GPU once, and more
+    // where a thread would have more weights than its registers hold.
     const long long units = static_cast<long long>(p.batch) * p.hkv;
     int ranks = 1;
-    while (ranks < kMaxCluster && p.max_kv_len > 2048 * ranks &&
-           (units * ranks < sms || p.max_kv_len > kHeldKeys * ranks))
+    while (ranks < kMaxCluster && p.max_kv_len > 2 * kThreads * ranks &&
+           (units * ranks * 2 <= sms || p.max_kv_len > kMostPer * kThreads * ranks))
         ranks *= 2;
-    const int slice = ((p.max_kv_len + ranks - 1) / ranks + kThreads - 1) / kThreads * kThreads;
-    const int held = slice < kHeldKeys ? slice : kHeldKeys;
-    const size_t smem = sizeof(Shared) + sizeof(uint32_t) * size_t(held);
-    cudaError_t e = cudaFuncSetAttribute(evict_select_kernel,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
-    if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(units * ranks));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = static_cast<unsigned>(ranks);
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, evict_select_kernel, p, held);
+    cudaError_t e = ranks == 1   ? launch_ranks<1>(p, stream)
+                    : ranks == 2 ? launch_ranks<2>(p, stream)
+                    : ranks == 4 ? launch_ranks<4>(p, stream)
+                                 : launch_ranks<8>(p, stream);
     if (e != cudaSuccess || p.max_keep == 0) return e;
 
-    const size_t move_smem = sizeof(int2) * size_t(kMoveSlots) * size_t(p.hkv);
-    cfg.gridDim = dim3(static_cast<unsigned>((p.max_keep + kMoveSlots - 1) / kMoveSlots),
+    int slots = kMoveEntries / p.hkv;
+    if (slots > 32) slots = 32;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>((p.max_keep + slots - 1) / slots),
                        static_cast<unsigned>(p.batch));
     cfg.blockDim = dim3(kMoveThreads);
-    cfg.dynamicSmemBytes = move_smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    return cudaLaunchKernelEx(&cfg, evict_move_kernel, p);
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, evict_move_kernel, p, slots, lanes_of(p.k.vecs),
+                              lanes_of(p.v.vecs));
 }
 
 }  // namespace attn
