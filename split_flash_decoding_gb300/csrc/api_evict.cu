@@ -91,7 +91,7 @@ extern "C" int attn_key_weights(const void *q, const attn_kv_t *k, const float *
     if (!kv_len || !aligned(q, 16) || !aligned(lse, 4) || !aligned(kv_len, 4) ||
         !aligned(q_row_offsets, 4))
         return ATTN_ERR_INVALID_ARG;
-    if ((head_dim != 64 && head_dim != 128) || group > kManyColumns || batch > kGqaMaxBatch ||
+    if ((head_dim != 64 && head_dim != 128) || group > 128 || batch > kGqaMaxBatch ||
         max_kv_len > kMaxFp8Tokens)
         return ATTN_ERR_UNSUPPORTED;
     const int hkv = num_q_heads / group;
@@ -120,6 +120,7 @@ extern "C" int attn_key_weights(const void *q, const attn_kv_t *k, const float *
     p.num_q_heads = num_q_heads;
     p.group = group;
     p.hkv = hkv;
+    p.head_groups = (hkv + 3) / 4;
     p.max_q_len = max_q_len;
     p.max_kv_len = max_kv_len;
     p.causal = causal ? 1 : 0;

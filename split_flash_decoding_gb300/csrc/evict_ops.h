@@ -30,11 +30,12 @@ struct WeightsParams {
     int max_pages, page_size, num_pages;
     int box_rows;                 // tokens per TMA box (min(128, page size))
     int tile_rows;                // query rows per column tile
+    int head_groups;              // KV heads in fours, rounded up
     float scale, decay;
 };
 
 // Columns (query rows x heads of a group) of a step's score tile.
-constexpr int kFewColumns = 16, kManyColumns = 128;
+constexpr int kFewColumns = 16, kManyColumns = 256;
 
 // head_dim 64 or 128; few: column tiles of kFewColumns, else of kManyColumns.
 cudaError_t launch_key_weights(const WeightsParams &p, int head_dim, bool few, int sms,

@@ -16,15 +16,21 @@
 // An item is KT tiles of 128 keys of one (sequence, KV head); its steps are the
 // column tiles of the rows that see one of its keys.
 //   Few columns (rows x group <= 16, decode): KT = 1, one step of 16 columns.  Bound by
-//   the stream of keys; two CTAs per SM walk the items of all sequences, KV heads
-//   side by side.
-//   More (prompts): KT = 2, steps of 128 columns.  Both key tiles stay in shared memory
-//   while column tiles pass, each read once for 256 keys.  Bound by the exponentials and
-//   the MMAs.  A CTA takes one item; those that the most rows see come first.
+//   the stream of keys.  Two CTAs per SM walk the units of all sequences, a unit being a
+//   tile of up to four KV heads, an item each: a thread then has its key's weights of four
+//   heads, neighbours in memory, and reads and writes them at once (a head at a time, four
+//   bytes of every 32 were 15 of 125 us).
+//   More (prompts): KT = 2, steps of 256 columns (MMAs of 128 columns wait for shared
+//   memory: 128 bytes a cycle for A and B).  Both key tiles stay in shared memory while
+//   column tiles pass; the score tiles of the two alternate in the two halves of tensor
+//   memory, one being filled while the other is read.  A CTA takes one item; those that the
+//   most rows see come first.  4 prompts of 2070 to 4062 rows, 32 + 8 heads: 149 us, 1.1 PFLOP/s
+//   (101 us with the epilogue left out; 197 with column tiles of 128 and eight epilogue warps,
+//   174 with sixteen).  The exponential unit gives 32 a cycle and SM, as long as the MMAs take;
+//   a part of them as polynomials on the FMA units lost, as the instructions are as scarce.
 //
-// Warp roles: four epilogue warps per key tile, K producer and Q producer (TMA), MMA
-// issue, and one warp that fetches what the epilogue needs from memory (the rows' lse,
-// the keys' earlier weights and where the new ones go).
+// Warp roles: epilogue (four warps, or sixteen in four parts of the columns), K producer
+// and Q producer (TMA), MMA issue, and one warp that fetches the rows' lse.
 #include "evict_ops.h"
 #include "launch.h"
 #include "ptx.cuh"
@@ -39,37 +45,38 @@ template <int D, bool kMany>
 struct Cfg {
     static constexpr int KT = kMany ? 2 : 1;                 // key tiles of an item
     static constexpr int NQ = kMany ? kManyColumns : kFewColumns;
-    static constexpr int kKStages = kMany ? 2 : 3;           // items in flight
+    static constexpr int kKStages = kMany ? 1 : 3;           // items in flight
     static constexpr int kQStages = 2;
     static constexpr int kLseStages = 4;
-    static constexpr int kOldStages = 2;                     // items of earlier weights
-    static constexpr int kEpiWarps = 4 * KT;
+    static constexpr int kHeads = kMany ? 1 : 4;             // KV heads of a unit, at most
+    static constexpr int kParts = kMany ? 4 : 1;             // of a tile's columns, four warps each
+    static constexpr int kCols = NQ / kParts;
+    static constexpr int kEpiWarps = 4 * kParts;
     static constexpr int kWarpK = kEpiWarps, kWarpQ = kWarpK + 1, kWarpMma = kWarpK + 2,
                          kWarpAux = kWarpK + 3;
     static constexpr int kThreads = 32 * (kEpiWarps + 4);
     static constexpr int kTileBytes = kKeys * D * 2;
     static constexpr int kQBytes = NQ * D * 2;
-    static constexpr int kTmemCols = 2 * KT * NQ;            // 32 or 512
+    static constexpr int kTmemCols = 2 * NQ;                 // two score tiles: 32 or 512
     // shared memory
     static constexpr int k = 0;
     static constexpr int q = k + kKStages * KT * kTileBytes;
     static constexpr int lse = q + kQStages * kQBytes;
-    static constexpr int old = lse + kLseStages * NQ * 4;
-    static constexpr int at = old + kOldStages * KT * kKeys * 4;
-    static constexpr int bars = at + kOldStages * KT * kKeys * 8;
+    static constexpr int part = lse + kLseStages * NQ * 4;   // many: the parts' sums
+    static constexpr int bars = part + (kMany ? kParts * KT * kKeys * 4 : 0);
     static constexpr int tmem_slot = bars + 256;
     static constexpr int items = tmem_slot + 16;
     // barriers
     static constexpr int bKFull = 0, bKEmpty = bKFull + kKStages, bQFull = bKEmpty + kKStages,
                          bQEmpty = bQFull + kQStages, bLFull = bQEmpty + kQStages,
-                         bLEmpty = bLFull + kLseStages, bOFull = bLEmpty + kLseStages,
-                         bOEmpty = bOFull + kOldStages, bSFull = bOEmpty + kOldStages,   // [2][KT]
-                         bSFree = bSFull + 2 * KT, kNumBars = bSFree + 2 * KT;
+                         bLEmpty = bLFull + kLseStages, bSFull = bLEmpty + kLseStages,
+                         bSFree = bSFull + 2, kNumBars = bSFree + 2;
     static_assert(kNumBars * 8 <= 256, "barrier space");
 };
 
-struct Item {
-    int b, kvh, L, n, row0, rows;   // n: the sequence's rows; rows: those the call has
+struct Unit {
+    int b, kvh, heads;              // KV heads [kvh, kvh + heads), an item each
+    int L, n, row0, rows;           // n: the sequence's rows; rows: those the call has
     int key0;                       // first key
     int step0, steps;               // column tiles [step0, step0 + steps)
 };
@@ -82,10 +89,11 @@ __device__ __forceinline__ int tiles_of(const WeightsParams &p, int b) {
 }
 
 template <bool kMany>
-__device__ __forceinline__ void open_item(const WeightsParams &p, int b, int kvh, int tile, Item &it) {
+__device__ __forceinline__ void open_unit(const WeightsParams &p, int b, int kvh, int tile, Unit &it) {
     constexpr int KT = kMany ? 2 : 1;
     it.b = b;
     it.kvh = kvh;
+    it.heads = kMany ? 1 : min(Cfg<64, kMany>::kHeads, p.hkv - kvh);
     it.L = static_cast<int>(min(p.kv_len[b], uint32_t(p.max_kv_len)));
     it.row0 = b;
     it.n = 1;
@@ -100,27 +108,48 @@ __device__ __forceinline__ void open_item(const WeightsParams &p, int b, int kvh
     it.steps = max((it.rows + p.tile_rows - 1) / p.tile_rows - it.step0, 0);
 }
 
-// Item j of the call's list; false: there is none of that number (a later one may be).
-//   few:  (sequence, tile, KV head), the last fastest; cum: tiles before each sequence
+// The columns of step t that see key tile kt of an item: [lo, hi), and from which on a key
+// of it is seen.
+struct Columns {
+    int lo, hi, first, group;
+    bool causal;
+    __device__ __forceinline__ bool any() const { return lo < hi; }
+    __device__ __forceinline__ int seen_by(int k) const {
+        return causal ? max(first + k, 0) * group : 0;
+    }
+};
+__device__ __forceinline__ Columns columns_of(const WeightsParams &p, const Unit &it, int kt, int t) {
+    Columns c;
+    const int i0 = (it.step0 + t) * p.tile_rows;         // first row of the step
+    c.group = p.group;
+    c.causal = p.causal;
+    c.first = it.key0 + kt * kKeys - (it.L - it.n) - i0; // row of the step that is key 0 itself
+    c.lo = c.seen_by(0);
+    c.hi = min(p.tile_rows, it.rows - i0) * p.group;
+    return c;
+}
+
+// Unit j of the call's list; false: there is none of that number (a later one may be).
+//   few:  (sequence, tile, four KV heads), the last fastest; cum: tiles before each sequence
 //   many: (tile from the sequence's end, falling; sequence, KV head): where the rows are
 //         the last tokens, that many of them see the tile, so the dearest come first
 template <bool kMany>
-__device__ __forceinline__ bool find_item(const WeightsParams &p, const int *cum, int j, Item &it) {
+__device__ __forceinline__ bool find_unit(const WeightsParams &p, const int *cum, int j, Unit &it) {
     if (kMany) {
         const int units = p.batch * p.hkv, last = (p.max_kv_len - 1) / (2 * kKeys);
         const int e = last - j / units, u = j % units;
         const int b = u / p.hkv, tiles = tiles_of<2>(p, b);
         if (e >= tiles) return false;
-        open_item<kMany>(p, b, u - b * p.hkv, tiles - 1 - e, it);
+        open_unit<kMany>(p, b, u - b * p.hkv, tiles - 1 - e, it);
         return true;
     }
-    const int x = j / p.hkv;
+    const int x = j / p.head_groups;
     int lo = 0, hi = p.batch;       // cum[lo] <= x < cum[hi]
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (cum[mid] <= x) lo = mid; else hi = mid;
     }
-    open_item<kMany>(p, lo, j - x * p.hkv, x - cum[lo], it);
+    open_unit<kMany>(p, lo, (j - x * p.head_groups) * Cfg<64, kMany>::kHeads, x - cum[lo], it);
     return true;
 }
 
@@ -151,28 +180,34 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
                  : "memory");
 }
 
-// N scores of the thread's key, columns c0 on: adds their weights to sum.  kPart:
-// only columns [lo, hi) count.
-template <int N, bool kPart>
+// N scores of the thread's key: adds their weights to sum.  kPart: only columns [lo, hi)
+// count.
+//   kFast: e^(scale s - lse) = 2^(a s - b), a = scale log2 e and b = lse log2 e (in `lse`)
+//     rounded: the exponent errs by up to 2^-24 (|a s| + |b|) more than below, and a pair of
+//     columns takes five instructions instead of six.
+//   else: scale s - lse first, then the product with log2 e, which errs by a part of that
+//     small number only.
+template <int N, bool kPart, bool kFast>
 __device__ __forceinline__ void add_weights(const float (&v)[N], const float *lse, float scale,
-                                            int c0, int lo, int hi, float2 (&sum)[2]) {
+                                            int lo, int hi, float2 (&sum)[2]) {
 #pragma unroll
     for (int c = 0; c < N; c += 4) {
-        const float4 l = *reinterpret_cast<const float4 *>(lse + c0 + c);
-        const float2 f = make_float2(scale, scale), g = make_float2(kLog2e, kLog2e);
-        // (score - lse first: the product with log2 e then errs by a part of that small number)
-        const float2 x =
-            __fmul2_rn(__ffma2_rn(make_float2(v[c], v[c + 1]), f, make_float2(-l.x, -l.y)), g);
-        const float2 y =
-            __fmul2_rn(__ffma2_rn(make_float2(v[c + 2], v[c + 3]), f, make_float2(-l.z, -l.w)), g);
-        float w[4] = {fast_exp2(x.x), fast_exp2(x.y), fast_exp2(y.x), fast_exp2(y.y)};
-        if (kPart) {
+        const float4 l = *reinterpret_cast<const float4 *>(lse + c);
+        // (precise: lse - score, and a negative factor: packed numbers have no minus sign)
+        const float2 f = kFast ? make_float2(scale, scale) : make_float2(-scale, -scale);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (c0 + c + i < lo || c0 + c + i >= hi) w[i] = 0.f;
+        for (int u = 0; u < 2; ++u) {
+            float2 x = __ffma2_rn(make_float2(v[c + 2 * u], v[c + 2 * u + 1]), f,
+                                  u ? make_float2(l.z, l.w) : make_float2(l.x, l.y));
+            if (!kFast) x = __fmul2_rn(x, make_float2(-kLog2e, -kLog2e));
+            float2 w = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+            if (kPart) {
+                const int at = c + 2 * u;
+                if (at < lo || at >= hi) w.x = 0.f;
+                if (at + 1 < lo || at + 1 >= hi) w.y = 0.f;
+            }
+            sum[u] = __fadd2_rn(sum[u], w);
         }
-        sum[0] = __fadd2_rn(sum[0], make_float2(w[0], w[1]));
-        sum[1] = __fadd2_rn(sum[1], make_float2(w[2], w[3]));
     }
 }
 
@@ -196,8 +231,8 @@ key_weights_kernel(const __grid_constant__ WeightsParams p) {
         // (one item a CTA: most of those past a sequence's end leave here)
         total = ((p.max_kv_len - 1) / (KT * kKeys) + 1) * p.batch * p.hkv;
         if (stride >= total) {
-            Item it;
-            if (!find_item<kMany>(p, cum, blockIdx.x, it)) return;
+            Unit it;
+            if (!find_unit<kMany>(p, cum, blockIdx.x, it)) return;
         }
     } else if (warp == 0) {
         int before = 0;
@@ -219,9 +254,7 @@ key_weights_kernel(const __grid_constant__ WeightsParams p) {
             uint32_t n = 1;
             if (i >= C::bLFull && i < C::bLFull + C::kLseStages) n = 32;
             if (i >= C::bLEmpty && i < C::bLEmpty + C::kLseStages) n = C::kEpiWarps;
-            if (i >= C::bOFull && i < C::bOFull + C::kOldStages) n = 64;
-            if (i >= C::bOEmpty && i < C::bOEmpty + C::kOldStages) n = C::kEpiWarps;
-            if (i >= C::bSFree) n = 4;
+            if (i >= C::bSFree) n = C::kEpiWarps;
             mbar_init(&bar[i], n);
         }
         fence_mbar_init();
@@ -236,9 +269,9 @@ key_weights_kernel(const __grid_constant__ WeightsParams p) {
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = *tmem_slot;
-    if (!kMany) total = cum[p.batch] * p.hkv;
+    if (!kMany) total = cum[p.batch] * p.head_groups;
 
-    Item it;
+    Unit it;
     if (warp == C::kWarpK) {
         // ------------------------------------------------------------ K producer
         const int box_rows = p.box_rows, box_shift = 31 - __clz(box_rows);
@@ -247,33 +280,34 @@ key_weights_kernel(const __grid_constant__ WeightsParams p) {
         int g = 0;
         bool ok = true;
         for (int j = blockIdx.x; ok && j < total; j += stride) {
-            if (!find_item<kMany>(p, cum, j, it) || it.steps == 0) continue;
-            const int s = g % C::kKStages;
+            if (!find_unit<kMany>(p, cum, j, it) || it.steps == 0) continue;
             const int live = min(nb, (it.L - it.key0 + box_rows - 1) >> box_shift);
-            if (lane == 0) {
-                if (g >= C::kKStages)
-                    ok = mbar_wait(&bar[C::bKEmpty + s], ((g / C::kKStages) - 1) & 1, p.err);
-                if (ok) mbar_arrive_expect_tx(&bar[C::bKFull + s], uint32_t(live) * box_bytes);
-            }
-            ok = __shfl_sync(0xffffffffu, ok, 0);
-            if (!ok) break;
-            ++g;
-            uint8_t *dst = smem + C::k + s * (KT * C::kTileBytes);
-            for (int r = lane; r < live; r += 32) {              // a box a lane
-                int slot;
-                const int page = page_at(p, it.b, it.key0 + (r << box_shift), true, slot);
-                const int row = r << box_shift;                  // in the item
-                uint8_t *to = dst + (row / kKeys) * C::kTileBytes + (row % kKeys) * 128;
-                if (page < 0) {
-                    mbar_complete_tx(&bar[C::bKFull + s], box_bytes);   // skipped bad page
-                } else {
-#pragma unroll
-                    for (int cb = 0; cb < D / 64; ++cb)
-                        tma_load_4d(to + cb * (kKeys * 128), &p.k_map, &bar[C::bKFull + s], cb * 64,
-                                    slot, it.kvh, page);
+            int page = -1, slot = 0;                             // of the lane's box
+            if (lane < live) page = page_at(p, it.b, it.key0 + (lane << box_shift), true, slot);
+            const int row = lane << box_shift;                   // in the item
+            uint8_t *dst = smem + C::k + (row / kKeys) * C::kTileBytes + (row % kKeys) * 128;
+            for (int h = 0; ok && h < it.heads; ++h) {
+                const int s = g % C::kKStages;
+                if (lane == 0) {
+                    if (g >= C::kKStages)
+                        ok = mbar_wait(&bar[C::bKEmpty + s], ((g / C::kKStages) - 1) & 1, p.err);
+                    if (ok) mbar_arrive_expect_tx(&bar[C::bKFull + s], uint32_t(live) * box_bytes);
                 }
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+                if (!ok) break;
+                ++g;
+                if (lane < live) {
+                    if (page < 0) {
+                        mbar_complete_tx(&bar[C::bKFull + s], box_bytes);   // skipped bad page
+                    } else {
+#pragma unroll
+                        for (int cb = 0; cb < D / 64; ++cb)
+                            tma_load_4d(dst + s * (KT * C::kTileBytes) + cb * (kKeys * 128), &p.k_map,
+                                        &bar[C::bKFull + s], cb * 64, slot, it.kvh + h, page);
+                    }
+                }
+                __syncwarp();
             }
-            __syncwarp();
         }
         // every copy this warp issued must land before the CTA may leave
         if (lane == 0)
@@ -286,8 +320,9 @@ key_weights_kernel(const __grid_constant__ WeightsParams p) {
         bool ok = true;
         if (lane == 0) {
             for (int j = blockIdx.x; ok && j < total; j += stride) {
-                if (!find_item<kMany>(p, cum, j, it)) continue;
-                for (int t = 0; ok && t < it.steps; ++t) {
+                if (!find_unit<kMany>(p, cum, j, it)) continue;
+                for (int x = 0; ok && x < it.steps * it.heads; ++x) {
+                    const int h = kMany ? 0 : x / it.steps, t = x - h * it.steps;
                     const int s = g % C::kQStages;
                     if (g >= C::kQStages)
                         ok = mbar_wait(&bar[C::bQEmpty + s], ((g / C::kQStages) - 1) & 1, p.err);
@@ -297,7 +332,7 @@ key_weights_kernel(const __grid_constant__ WeightsParams p) {
 #pragma unroll
                     for (int cb = 0; cb < D / 64; ++cb)
                         tma_load_4d(smem + C::q + s * C::kQBytes + cb * (NQ * 128), &p.q_map,
-                                    &bar[C::bQFull + s], cb * 64, 0, it.kvh,
+                                    &bar[C::bQFull + s], cb * 64, 0, it.kvh + h,
                                     it.row0 + (it.step0 + t) * p.tile_rows);
                 }
             }
@@ -312,35 +347,40 @@ key_weights_kernel(const __grid_constant__ WeightsParams p) {
             int g = 0, gk = 0;
             bool ok = true;
             for (int j = blockIdx.x; ok && j < total; j += stride) {
-                if (!find_item<kMany>(p, cum, j, it) || it.steps == 0) continue;
-                const int ks = gk % C::kKStages;
-                ok = mbar_wait(&bar[C::bKFull + ks], (gk / C::kKStages) & 1, p.err);
-                for (int t = 0; ok && t < it.steps; ++t, ++g) {
-                    const int qs = g % C::kQStages, sb = g & 1;
-                    ok = mbar_wait(&bar[C::bQFull + qs], (g / C::kQStages) & 1, p.err);
-                    const uint64_t qd = tc::smem_desc_sw128(q_base + qs * C::kQBytes, 16, 1024);
+                if (!find_unit<kMany>(p, cum, j, it) || it.steps == 0) continue;
+                for (int h = 0; ok && h < it.heads; ++h) {
+                    const int ks = gk % C::kKStages;
+                    ok = mbar_wait(&bar[C::bKFull + ks], (gk / C::kKStages) & 1, p.err);
+                    for (int t = 0; ok && t < it.steps; ++t, ++g) {
+                        const int qs = g % C::kQStages;
+                        ok = mbar_wait(&bar[C::bQFull + qs], (g / C::kQStages) & 1, p.err);
+                        const uint64_t qd = tc::smem_desc_sw128(q_base + qs * C::kQBytes, 16, 1024);
 #pragma unroll
-                    for (int kt = 0; kt < KT; ++kt) {
-                        if (ok && g >= 2)
-                            ok = mbar_wait(&bar[C::bSFree + sb * KT + kt], ((g >> 1) - 1) & 1, p.err);
-                        if (!ok) break;
-                        tc::fence_after_sync();
-                        const uint64_t kd = tc::smem_desc_sw128(
-                            k_base + (ks * KT + kt) * C::kTileBytes, 16, 1024);
+                        for (int kt = 0; kt < KT; ++kt) {
+                            const int x = g * KT + kt, sb = x & 1;   // score tile and its buffer
+                            if (ok && x >= 2)
+                                ok = mbar_wait(&bar[C::bSFree + sb], ((x >> 1) - 1) & 1, p.err);
+                            if (!ok) break;
+                            tc::fence_after_sync();
+                            const uint64_t kd = tc::smem_desc_sw128(
+                                k_base + (ks * KT + kt) * C::kTileBytes, 16, 1024);
+                            if (columns_of(p, it, kt, t).any()) {
 #pragma unroll
-                        for (int kk = 0; kk < D / 16; ++kk) {
-                            const uint32_t in = (kk & 3) * 32;   // within the 64 channels' rows
-                            tc::mma_bf16(tmem + (sb * KT + kt) * NQ,
-                                         kd + uint64_t(((kk >> 2) * (kKeys * 128) + in) >> 4),
-                                         qd + uint64_t(((kk >> 2) * (NQ * 128) + in) >> 4), idesc,
-                                         kk > 0);
+                                for (int kk = 0; kk < D / 16; ++kk) {
+                                    const uint32_t in = (kk & 3) * 32;   // within the 64 channels' rows
+                                    tc::mma_bf16(tmem + sb * NQ,
+                                                 kd + uint64_t(((kk >> 2) * (kKeys * 128) + in) >> 4),
+                                                 qd + uint64_t(((kk >> 2) * (NQ * 128) + in) >> 4), idesc,
+                                                 kk > 0);
+                                }
+                            }
+                            tc::mma_commit(&bar[C::bSFull + sb]);
                         }
-                        tc::mma_commit(&bar[C::bSFull + sb * KT + kt]);
+                        if (ok) tc::mma_commit(&bar[C::bQEmpty + qs]);
                     }
-                    if (ok) tc::mma_commit(&bar[C::bQEmpty + qs]);
+                    if (ok) tc::mma_commit(&bar[C::bKEmpty + ks]);
+                    ++gk;
                 }
-                if (ok) tc::mma_commit(&bar[C::bKEmpty + ks]);
-                ++gk;
             }
         }
     } else if (warp == C::kWarpAux) {
@@ -353,119 +393,169 @@ key_weights_kernel(const __grid_constant__ WeightsParams p) {
             row_in[u] = c < p.tile_rows * p.group ? c / p.group : 0x3fffffff;
             head_in[u] = c % p.group;
         }
-        int g = 0, gi = 0;
+        int g = 0;
         bool ok = true;
         for (int j = blockIdx.x; ok && j < total; j += stride) {
-            if (!find_item<kMany>(p, cum, j, it)) continue;
-            const int os = gi % C::kOldStages;
-            if (gi >= C::kOldStages)
-                ok = mbar_wait(&bar[C::bOEmpty + os], ((gi / C::kOldStages) - 1) & 1, p.err);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            ++gi;
-            float *old = reinterpret_cast<float *>(smem + C::old) + os * (KT * kKeys);
-            long long *at = reinterpret_cast<long long *>(smem + C::at) + os * (KT * kKeys);
+            if (!find_unit<kMany>(p, cum, j, it)) continue;
+            // Many columns: -lse log2 e, a step's numbers loaded before the last one's are
+            // stored; few: the numbers as they are.
+            const auto row_of = [&](int t, int u) { return (it.step0 + t) * p.tile_rows + row_in[u]; };
+            const auto lse_of = [&](int t, int u) {
+                return p.lse + size_t(it.row0 + row_of(t, u)) * p.num_q_heads + it.kvh * p.group +
+                       head_in[u];
+            };
+            float next[kPer];
+            const auto load = [&](int t) {
 #pragma unroll
-            for (int u = 0; u < KT * kKeys / 32; ++u) {
-                const int k = lane + 32 * u, t = it.key0 + k;
-                long long where = -1;
-                if (t < it.L) {
-                    int slot;
-                    const int page = page_at(p, it.b, t, false, slot);
-                    if (page >= 0)
-                        where = page * p.w.page + slot * p.w.token + it.kvh * p.w.head;
-                }
-                at[k] = where;
-                if (where >= 0 && t < it.L - it.n)
-                    cp_async_4(old + k, p.w.base + where);
-                else
-                    old[k] = 0.f;
-            }
-            cp_async_arrive(&bar[C::bOFull + os]);
-            mbar_arrive(&bar[C::bOFull + os]);
-            for (int t = 0; t < it.steps; ++t) {
+                for (int u = 0; u < kPer; ++u)
+                    next[u] = t < it.steps && row_of(t, u) < it.rows ? *lse_of(t, u) : 0.f;
+            };
+            if (kMany) load(0);
+            for (int x = 0; x < it.steps * it.heads; ++x) {
+                const int h = kMany ? 0 : x / it.steps, t = x - h * it.steps;
                 const int s = g % C::kLseStages;
+                float *to = reinterpret_cast<float *>(smem + C::lse) + s * NQ + lane;
+                float now[kPer];
+                if (kMany) {
+#pragma unroll
+                    for (int u = 0; u < kPer; ++u) now[u] = next[u] * -kLog2e;
+                    load(t + 1);
+                }
                 if (g >= C::kLseStages)
                     ok = mbar_wait(&bar[C::bLEmpty + s], ((g / C::kLseStages) - 1) & 1, p.err);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 ++g;
-                const int i0 = (it.step0 + t) * p.tile_rows;
-                float *to = reinterpret_cast<float *>(smem + C::lse) + s * NQ + lane;
+                if (kMany) {
 #pragma unroll
-                for (int u = 0; u < kPer; ++u)
-                    if (i0 + row_in[u] < it.rows)
-                        cp_async_4(to + 32 * u, p.lse + size_t(it.row0 + i0 + row_in[u]) * p.num_q_heads +
-                                                    it.kvh * p.group + head_in[u]);
-                cp_async_arrive(&bar[C::bLFull + s]);
+                    for (int u = 0; u < kPer; ++u) to[32 * u] = now[u];
+                    mbar_arrive(&bar[C::bLFull + s]);
+                } else {
+#pragma unroll
+                    for (int u = 0; u < kPer; ++u)
+                        if (row_of(t, u) < it.rows)
+                            cp_async_4(to + 32 * u, lse_of(t, u) + h * p.group);
+                    cp_async_arrive(&bar[C::bLFull + s]);
+                }
             }
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
     } else {
         // ------------------------------------------------------------ epilogue
-        const int kt = warp >> 2;                                // key tile of the item
-        const int k = (warp & 3) * 32 + lane;                    // key == TMEM lane
-        const uint32_t s_base = tmem + (uint32_t((warp & 3) * 32) << 16) + kt * NQ;
-        int g = 0, gi = 0;
+        const int part = warp >> 2;                              // of the columns
+        const int k = (warp & 3) * 32 + lane;                    // key of a tile == TMEM lane
+        const uint32_t s_base = tmem + (uint32_t((warp & 3) * 32) << 16);
+        const float scale2 = p.scale * kLog2e;
+        int g = 0;
         bool ok = true;
-        for (int j = blockIdx.x; ok && j < total; j += stride) {
-            if (!find_item<kMany>(p, cum, j, it)) continue;
-            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-            const int tile0 = it.key0 + kt * kKeys;
-            for (int t = 0; ok && t < it.steps; ++t, ++g) {
-                const int sb = g & 1, ls = g % C::kLseStages;
-                const int i0 = (it.step0 + t) * p.tile_rows;     // first row of the columns
-                const int hi = min(p.tile_rows, it.rows - i0) * p.group;
-                // columns from which on this thread's key is seen
-                const int lo = p.causal ? max(tile0 + k - (it.L - it.n) - i0, 0) * p.group : 0;
-                const bool part = hi < NQ || (p.causal && tile0 + kKeys - 1 > it.L - it.n + i0);
-                ok = mbar_wait(&bar[C::bLFull + ls], (g / C::kLseStages) & 1, p.err);
-                if (ok) ok = mbar_wait(&bar[C::bSFull + sb * KT + kt], (g >> 1) & 1, p.err);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                tc::fence_after_sync();
-                const float *lse = reinterpret_cast<const float *>(smem + C::lse) + ls * NQ;
-                const uint32_t s_at = s_base + sb * (KT * NQ);
-                if constexpr (kMany) {
-#pragma unroll 1
-                    for (int c0 = 0; c0 < NQ && c0 < hi; c0 += 32) {
-                        float v[32];
-                        tc::tmem_ld32(s_at + c0, v);
-                        if (part)
-                            add_weights<32, true>(v, lse, p.scale, c0, lo, hi, sum);
-                        else
-                            add_weights<32, false>(v, lse, p.scale, c0, lo, hi, sum);
-                    }
+        // Every warp runs every item's named barriers, even after a wait gave up (ok ==
+        // false), so no warp can strand the others.
+        for (int j = blockIdx.x; j < total && (ok || C::kParts > 1); j += stride) {
+            if (!find_unit<kMany>(p, cum, j, it)) continue;
+            // The key that this thread stores, and its earlier weights on their way (many: the
+            // threads of part i have key tile i).
+            const int tile = part < KT ? part : 0, key = it.key0 + tile * kKeys + k;
+            float *where = nullptr;
+            float old[C::kHeads], w[C::kHeads];
+#pragma unroll
+            for (int h = 0; h < C::kHeads; ++h) old[h] = w[h] = 0.f;
+            if (part < KT && key < it.L) {
+                int slot;
+                const int page = page_at(p, it.b, key, false, slot);
+                if (page >= 0)
+                    where = p.w.base + page * p.w.page + slot * p.w.token + it.kvh * p.w.head;
+            }
+            const bool together = C::kHeads == 4 && it.heads == 4 && p.w.head == 1 &&
+                                  (reinterpret_cast<uintptr_t>(where) & 15) == 0;
+            if (where && key < it.L - it.n) {
+                if (together) {
+                    const float4 v = *reinterpret_cast<const float4 *>(where);
+                    old[0] = v.x;
+                    if (C::kHeads == 4) { old[1] = v.y; old[2] = v.z; old[3] = v.w; }
                 } else {
-#pragma unroll 1
-                    for (int c0 = 0; c0 < NQ && c0 < hi; c0 += 8) {
-                        float v[8];
-                        tc::tmem_ld_n<8>(s_at + c0, v);
-                        add_weights<8, true>(v, lse, p.scale, c0, lo, hi, sum);
-                    }
-                }
-                tc::fence_before_sync();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&bar[C::bSFree + sb * KT + kt]);
-                    mbar_arrive(&bar[C::bLEmpty + ls]);
+#pragma unroll
+                    for (int h = 0; h < C::kHeads; ++h)
+                        if (h < it.heads) old[h] = where[h * p.w.head];
                 }
             }
-            if (!ok) break;
-            const int os = gi % C::kOldStages;
-            ok = __all_sync(0xffffffffu,
-                            mbar_wait(&bar[C::bOFull + os], (gi / C::kOldStages) & 1, p.err));
-            if (!ok) break;
-            ++gi;
-            const float old =
-                reinterpret_cast<const float *>(smem + C::old)[(os * KT + kt) * kKeys + k];
-            const long long where =
-                reinterpret_cast<const long long *>(smem + C::at)[(os * KT + kt) * kKeys + k];
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bar[C::bOEmpty + os]);
-            const float w = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-            if (where >= 0)
-                p.w.base[where] = tile0 + k < it.L - it.n ? fmaf(old, p.decay, w) : w;
+#pragma unroll
+            for (int h = 0; h < C::kHeads; ++h) {
+                if (h >= it.heads) break;
+                float2 sum[KT][2];
+#pragma unroll
+                for (int kt = 0; kt < KT; ++kt) sum[kt][0] = sum[kt][1] = make_float2(0.f, 0.f);
+                for (int t = 0; ok && t < it.steps; ++t, ++g) {
+                    const int ls = g % C::kLseStages;
+                    ok = __all_sync(0xffffffffu,
+                                    mbar_wait(&bar[C::bLFull + ls], (g / C::kLseStages) & 1, p.err));
+                    const float *lse = reinterpret_cast<const float *>(smem + C::lse) + ls * NQ;
+#pragma unroll
+                    for (int kt = 0; kt < KT; ++kt) {
+                        const int x = g * KT + kt, sb = x & 1;
+                        if (ok)
+                            ok = __all_sync(0xffffffffu,
+                                            mbar_wait(&bar[C::bSFull + sb], (x >> 1) & 1, p.err));
+                        if (!ok) break;
+                        tc::fence_after_sync();
+                        const Columns cols = columns_of(p, it, kt, t);
+                        const int lo = cols.seen_by(k), c1 = min((part + 1) * C::kCols, cols.hi);
+                        const uint32_t s_at = s_base + sb * NQ;
+                        if constexpr (kMany) {
+                            // The warp's 32 keys see none of a chunk of 32 columns, all of it, or some.
+                            const int none = cols.seen_by(k & ~31), all = cols.seen_by(k | 31);
+#pragma unroll 1
+                            for (int c = max(part * C::kCols, none & ~31); c < c1; c += 32) {
+                                float v[32];
+                                tc::tmem_ld32(s_at + c, v);
+                                if (c >= all && c + 32 <= c1)
+                                    add_weights<32, false, true>(v, lse + c, scale2, 0, 32, sum[kt]);
+                                else
+                                    add_weights<32, true, true>(v, lse + c, scale2, lo - c, c1 - c,
+                                                                sum[kt]);
+                            }
+                        } else {
+#pragma unroll 1
+                            for (int c = 0; c < c1; c += 8) {
+                                float v[8];
+                                tc::tmem_ld_n<8>(s_at + c, v);
+                                add_weights<8, true, false>(v, lse + c, p.scale, lo - c, c1 - c, sum[kt]);
+                            }
+                        }
+                        tc::fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bar[C::bSFree + sb]);
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar[C::bLEmpty + ls]);
+                }
+                w[h] = (sum[0][0].x + sum[0][0].y) + (sum[0][1].x + sum[0][1].y);
+                if constexpr (C::kParts > 1) {       // the parts' sums of a key
+                    float *parts = reinterpret_cast<float *>(smem + C::part);
+#pragma unroll
+                    for (int kt = 0; kt < KT; ++kt)
+                        parts[(part * KT + kt) * kKeys + k] =
+                            (sum[kt][0].x + sum[kt][0].y) + (sum[kt][1].x + sum[kt][1].y);
+                    named_sync(1, 32 * C::kEpiWarps);
+                    w[h] = 0.f;
+#pragma unroll
+                    for (int i = 0; i < C::kParts; ++i) w[h] += parts[(i * KT + tile) * kKeys + k];
+                    named_sync(1, 32 * C::kEpiWarps);
+                }
+            }
+            if (!ok || !where) continue;
+            if (key < it.L - it.n) {
+#pragma unroll
+                for (int h = 0; h < C::kHeads; ++h) w[h] = fmaf(old[h], p.decay, w[h]);
+            }
+            if (together) {
+                *reinterpret_cast<float4 *>(where) =
+                    make_float4(w[0], w[C::kHeads > 1 ? 1 : 0], w[C::kHeads > 2 ? 2 : 0],
+                                w[C::kHeads > 3 ? 3 : 0]);
+            } else {
+#pragma unroll
+                for (int h = 0; h < C::kHeads; ++h)
+                    if (h < it.heads) where[h * p.w.head] = w[h];
+            }
         }
     }
 
@@ -485,10 +575,10 @@ cudaError_t launch(const WeightsParams &p, int sms, cudaStream_t stream) {
     const cudaError_t e =
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
     if (e != cudaSuccess) return e;
-    const long long items = (static_cast<long long>(p.max_kv_len - 1) / (C::KT * kKeys) + 1) *
-                            p.batch * p.hkv;
+    const long long units = (static_cast<long long>(p.max_kv_len - 1) / (C::KT * kKeys) + 1) *
+                            p.batch * (kMany ? p.hkv : p.head_groups);
     long long ctas = kMany ? 64LL * sms : 2LL * sms;
-    if (ctas > items) ctas = items;
+    if (ctas > units) ctas = units;
     kern<<<static_cast<unsigned>(ctas), C::kThreads, smem, stream>>>(p);
     return cudaGetLastError();
 }

@@ -5,7 +5,10 @@ What the kernel may differ by, per term p = e^x:
 
 * the score is an fp32 MMA sum of d exact products in steps of 16, one rounding a step
   and two more: rho = (d / 16 + 2) 2^-23 scale sum_c |q_c k_c|;
-* x itself is rounded once (2^-24 |x|), then multiplied by log2 e (2^-24 for the product
+* with many rows the exponent is one multiply-add of fl(scale log2 e) and fl(lse log2 e), each
+  rounded once and the product not: 2^-23 (|scale q.k| + |lse|) of x, which the bound takes for
+  all calls;
+* otherwise x itself is rounded once (2^-24 |x|), then multiplied by log2 e (2^-24 for the product
   and 2^-25 for the constant), and e^x taken to 2^-22: together 2^-22 (|x| + 1);
 * the sum of N positive terms in four running fp32 sums: (N / 4 + 8) 2^-24 of the sum;
 * weights below 2^-126 count as 0: N 2^-126.
@@ -119,6 +122,7 @@ class Case:
                 x = torch.where(s == -math.inf, s, s - lse)
                 p = torch.exp(x)
                 rel = ((self.dim / 16 + 2) * 2.0 ** -23 * a +
+                       2.0 ** -23 * (s.abs() + lse.abs()).clamp_max(1e4) +
                        2.0 ** -22 * (x.abs().clamp_max(1e4) + 1))
                 N = n * self.group
                 total = p.sum((0, 2)).T
