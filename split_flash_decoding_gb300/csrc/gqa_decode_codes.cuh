@@ -67,17 +67,19 @@ namespace codes {
 constexpr int kD = 128;
 constexpr int kBK = kGqaTcTileKeys;          // 128 keys per tile
 constexpr int kStages = 3;                   // K tiles in flight
-constexpr int kVStages = 2;                  // V tiles in flight (three measured the same)
+// V tiles in flight: as many as leave two CTAs room (8 bits: three measured the same).
+__host__ __device__ constexpr int v_stages(bool fp4, int nc) { return fp4 && nc == 4 ? 3 : 2; }
 constexpr int kTileBytes = kBK * kD;         // 16 KB (4 bits: 16 codes in the first 8 of 16 bytes)
 constexpr int kKGroups = 4;                  // 4 bits: scales of a key, 32 channels each
-constexpr int kScStages = 6;                 // tiles of scales in flight
+constexpr int kScStages = 4;                 // tiles of scales in flight
 constexpr int kQBufs = 2;
 constexpr int kCtasPerSm = 2;
 // A lower kLazy leaves more of the e4m3 range below the reference, a higher one moves it
 // less often (kLazy 1, 2, 3, 4: 64 single rows 100 us each, 1 to 4 draft rows of 4 heads 107,
 // 98, 93, 92).
 constexpr float kLazy = 3.f;                 // base 2
-constexpr float kWeightTop = 16.f;           // weights reach 2^kLazy * 2 * kWeightTop = 256
+// Weights reach 2^kLazy * 2 * this: 256 of e4m3's 448, 2^15 of e5m2's 57344.
+__host__ __device__ constexpr float weight_top(bool fp4) { return fp4 ? 2048.f : 16.f; }
 // Each term's unit over the next one's (see above).
 __host__ __device__ constexpr float term_ratio(int u) { return u < 2 ? 32.f : 32768.f; }
 constexpr int kBarBytes = 304;
@@ -110,7 +112,7 @@ struct Cfg {
     // shared memory
     static constexpr int kring = 0;
     static constexpr int vring = kring + kStages * kTileBytes;
-    static constexpr int q = vring + kVStages * kTileBytes;          // [kQBufs][terms, rows][128 B]
+    static constexpr int q = vring + v_stages(kFp4, NC) * kTileBytes;          // [kQBufs][terms, rows][128 B]
     static constexpr int p = q + kQBufs * kQBytes;                   // [chunks][128 keys][16 B]
     static constexpr int sc = p + NP * 128;                          // [kScStages][128] {ks, vs}
     static constexpr int red = sc + kScStages * kBK * 8;             // float [4][16] tile max
@@ -156,6 +158,14 @@ __device__ __forceinline__ void mma_f8f6f4(uint32_t d_tmem, uint64_t a_desc, uin
         "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
         "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate ? 1u : 0u)
         : "memory");
+}
+
+// One lane of the warp (all lanes take part).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(one));
+    return one != 0;
 }
 
 // Shared-memory matrix descriptor without a swizzle; lbo/sbo in bytes.
@@ -304,6 +314,23 @@ __device__ __forceinline__ uint32_t to_e5m2x2(float a, float b) {
     return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E5M2);
 }
 
+// Four weights as f16 and those as four e5m2 terms each, a term of all four to a word: an
+// e5m2 number is the upper half of an f16 one, so a term is what its upper half says, cut
+// off, and the next the (exact) rest's: 3 bits each of the 11.
+__device__ __forceinline__ void half_terms(const float2 &a, const float2 &b, uint32_t (&code)[4]) {
+    uint32_t x, y;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(x) : "f"(a.y), "f"(a.x));
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(b.y), "f"(b.x));
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        code[u] = __byte_perm(x, y, 0x7531);
+        if (u < 3) {
+            asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(x) : "r"(x & 0xff00ff00u));
+            asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(y) : "r"(y & 0xff00ff00u));
+        }
+    }
+}
+
 // The scale that e8m0 byte k of w stands for (2^-127 counts as 0; 255: NaN).
 __device__ __forceinline__ float e8m0(uint32_t w, int k) {
     const uint32_t e = (w >> (8 * k)) & 0xffu;
@@ -358,7 +385,7 @@ __device__ __forceinline__ void produce(const Fp8DecodeParams &p, const int2 *cu
     uint64_t *full = bar + (kIsK ? kKFull : kVFull);
     uint64_t *empty = bar + (kIsK ? kKEmpty : kVEmpty);
     uint8_t *ring = smem + (kIsK ? Cfg<NC, kFp4>::kring : Cfg<NC, kFp4>::vring);
-    constexpr int kN = kIsK ? kStages : kVStages;
+    constexpr int kN = kIsK ? kStages : v_stages(kFp4, NC);
     const int box_rows = p.box_rows;        // 128, 64, 32, 16 or 8
     const int box_shift = 31 - __clz(box_rows);
     const int nb = kBK >> box_shift;        // row boxes per tile
@@ -557,7 +584,7 @@ gqa_decode_codes_kernel(const __grid_constant__ Fp8DecodeParams p) {
     Fp8Range *range = reinterpret_cast<Fp8Range *>(smem + C::range);
     int2 *cum = reinterpret_cast<int2 *>(smem + C::items);
 
-    const int warp = threadIdx.x >> 5;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);   // (uniform)
     const int lane = threadIdx.x & 31;
     const int G = p.group;
 
@@ -599,76 +626,84 @@ gqa_decode_codes_kernel(const __grid_constant__ Fp8DecodeParams p) {
         feed<NC, kFp4>(p, cum, walk, smem, bar, lane);
     } else if (warp == C::kWarpMma) {
         // ---------------------------------------------------------- MMA issue
-        if (lane == 0) {
-            constexpr uint32_t held = kFp4 ? kE2m1 : kE4m3;
-            constexpr uint32_t idesc_s = idesc_f8f6f4(held, kE4m3, 128, C::NS, 0, 0);
-            constexpr uint32_t idesc_s1 = idesc_f8f6f4(held, kE5m2, 128, C::NS, 0, 0);
-            constexpr uint32_t idesc_o = idesc_f8f6f4(held, kE4m3, 128, C::NP, 1, 1);
-            const uint32_t k_base = smem_addr(smem + C::kring);
-            const uint32_t v_base = smem_addr(smem + C::vring);
-            const uint32_t q_base = smem_addr(smem + C::q);
-            // MN-major without a swizzle: 16 bytes per key, 8-key groups 128 bytes
-            // apart, 16-column blocks kBK * 16
-            const uint64_t pd = smem_desc_plain(smem_addr(smem + C::p), 128, kBK * 16);
-            int g = 0, itq = 0;
-            bool ok = true;
-            for (int j = 0; ok && j < items; ++j) {
-                const Fp8Item it = fp8_item(p, cum, walk, j);
-                if (it.ntiles == 0) continue;
-                const int qb = itq % kQBufs;
-                ok = mbar_wait(&bar[kQFull + qb], (itq / kQBufs) & 1, p.err);
-                for (int t = 0; ok && t <= it.ntiles; ++t) {
-                    if (t < it.ntiles) {
-                        const int gg = g + t;
-                        const int ks = gg % kStages;
-                        const int sb = gg & 1;
-                        ok = mbar_wait(&bar[kKFull + ks], (gg / kStages) & 1, p.err);
-                        if (ok && gg >= 2)
-                            ok = mbar_wait(&bar[kSFree + sb], ((gg >> 1) - 1) & 1, p.err);
-                        if (!ok) break;
-                        tc::fence_after_sync();
-                        const uint64_t kd =
-                            tc::smem_desc_sw128(k_base + ks * kTileBytes, 16, 1024);
-                        const uint64_t qd =
-                            tc::smem_desc_sw128(q_base + qb * C::kQBytes, 16, 1024);
+        // The whole warp walks, with numbers that are the same in all lanes, and one lane
+        // issues: what the tensor core is given then is in uniform registers (one lane that
+        // walks by itself took 130 cycles an MMA to move it there).
+        constexpr uint32_t held = kFp4 ? kE2m1 : kE4m3;
+        constexpr uint32_t idesc_s = idesc_f8f6f4(held, kE4m3, 128, C::NS, 0, 0);
+        constexpr uint32_t idesc_s1 = idesc_f8f6f4(held, kE5m2, 128, C::NS, 0, 0);
+        constexpr uint32_t idesc_o = idesc_f8f6f4(held, kFp4 ? kE5m2 : kE4m3, 128, C::NP, 1, 1);
+        const uint32_t k_base = smem_addr(smem + C::kring);
+        const uint32_t v_base = smem_addr(smem + C::vring);
+        const uint32_t q_base = smem_addr(smem + C::q);
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        // MN-major without a swizzle: 16 bytes per key, 8-key groups 128 bytes
+        // apart, 16-column blocks kBK * 16
+        const uint64_t pd = smem_desc_plain(smem_addr(smem + C::p), 128, kBK * 16);
+        const int count = __shfl_sync(0xffffffffu, items, 0);
+        const auto arrived = [&](int b, int phase) {
+            return __all_sync(0xffffffffu, mbar_wait(&bar[b], phase, p.err)) != 0;
+        };
+        int g = 0, itq = 0;
+        bool ok = true;
+        for (int j = 0; ok && j < count; ++j) {
+            const int ntiles = __shfl_sync(0xffffffffu, fp8_item(p, cum, walk, j).ntiles, 0);
+            if (ntiles == 0) continue;
+            const int qb = itq % kQBufs;
+            ok = arrived(kQFull + qb, (itq / kQBufs) & 1);
+            for (int t = 0; ok && t <= ntiles; ++t) {
+                if (t < ntiles) {
+                    const int gg = g + t;
+                    const int ks = gg % kStages;
+                    const int sb = gg & 1;
+                    ok = arrived(kKFull + ks, (gg / kStages) & 1);
+                    if (ok && gg >= 2) ok = arrived(kSFree + sb, ((gg >> 1) - 1) & 1);
+                    if (!ok) break;
+                    tc::fence_after_sync();
+                    const uint64_t kd = tc::smem_desc_sw128(k_base + ks * kTileBytes, 16, 1024);
+                    const uint64_t qd = tc::smem_desc_sw128(q_base + qb * C::kQBytes, 16, 1024);
+                    if (elect_one()) {
 #pragma unroll
                         for (int kk = 0; kk < kD / 32; ++kk) {   // 32 channels = 32 bytes a step
                             const uint64_t ka = kd + uint64_t(kk * 2), qa = qd + uint64_t(kk * 2);
                             if constexpr (kFp4) {                // a group's block, both terms
-                                const uint32_t to = tmem + sb * C::kSCols + kk * C::NS;
+                                const uint32_t to = tm + sb * C::kSCols + kk * C::NS;
                                 mma_f8f6f4(to, ka, qa, idesc_s, false);
                                 mma_f8f6f4(to, ka, qa + uint64_t((C::NS * 128) >> 4), idesc_s1, true);
                             } else {
-                                mma_f8f6f4(tmem + sb * C::kSCols, ka, qa, idesc_s, kk > 0);
+                                mma_f8f6f4(tm + sb * C::kSCols, ka, qa, idesc_s, kk > 0);
                             }
                         }
                         tc::mma_commit(&bar[kSFull + sb]);
                         tc::mma_commit(&bar[kKEmpty + ks]);
-                        if (t == it.ntiles - 1) tc::mma_commit(&bar[kQEmpty + qb]);
+                        if (t == ntiles - 1) tc::mma_commit(&bar[kQEmpty + qb]);
                     }
-                    if (t >= 1) {
-                        const int gp = g + t - 1;
-                        const int vs = gp % kVStages;
-                        ok = mbar_wait(&bar[kPFull], gp & 1, p.err);
-                        if (ok) ok = mbar_wait(&bar[kVFull + vs], (gp / kVStages) & 1, p.err);
-                        if (!ok) break;
-                        tc::fence_after_sync();
-                        // V^T as the MN-major A operand: 128 channels are one 128-byte
-                        // atom, 8-key groups 1 KB apart, 32 keys a step.
-                        const uint64_t vd =
-                            tc::smem_desc_sw128(v_base + vs * kTileBytes, kTileBytes, 1024);
+                    __syncwarp();
+                }
+                if (t >= 1) {
+                    const int gp = g + t - 1;
+                    const int vs = gp % v_stages(kFp4, NC);
+                    ok = arrived(kPFull, gp & 1);
+                    if (ok) ok = arrived(kVFull + vs, (gp / v_stages(kFp4, NC)) & 1);
+                    if (!ok) break;
+                    tc::fence_after_sync();
+                    // V^T as the MN-major A operand: 128 channels are one 128-byte
+                    // atom, 8-key groups 1 KB apart, 32 keys a step.
+                    const uint64_t vd =
+                        tc::smem_desc_sw128(v_base + vs * kTileBytes, kTileBytes, 1024);
+                    if (elect_one()) {
 #pragma unroll
                         for (int kk = 0; kk < kBK / 32; ++kk)
-                            mma_f8f6f4(tmem + C::kTmemO, vd + uint64_t((kk * 32 * 128) >> 4),
-                                     pd + uint64_t((kk * 32 * 16) >> 4), idesc_o,
-                                     t > 1 || kk > 0);
+                            mma_f8f6f4(tm + C::kTmemO, vd + uint64_t((kk * 32 * 128) >> 4),
+                                       pd + uint64_t((kk * 32 * 16) >> 4), idesc_o, t > 1 || kk > 0);
                         tc::mma_commit(&bar[kODone]);
                         tc::mma_commit(&bar[kVEmpty + vs]);
                     }
+                    __syncwarp();
                 }
-                g += it.ntiles;
-                ++itq;
             }
+            g += ntiles;
+            ++itq;
         }
     } else {
         // ---------------------------------------------------- softmax + epilogue
@@ -782,7 +817,7 @@ gqa_decode_codes_kernel(const __grid_constant__ Fp8DecodeParams p) {
                 const float v_inv = pow2i(-ve);
                 // (a scale past the range would saturate: NaN instead)
                 const float v_mul = ve_raw > kMaxVExp ? __uint_as_float(0x7fffffffu)
-                                                      : sc.y * v_inv * kWeightTop;
+                                                      : sc.y * v_inv * weight_top(kFp4);
                 float top = -INFINITY;
 #pragma unroll
                 for (int h = 0; h < NCH; ++h) {
@@ -852,17 +887,21 @@ gqa_decode_codes_kernel(const __grid_constant__ Fp8DecodeParams p) {
                         l[h][c] = __ffma2_rn(e, make_float2(v_inv, v_inv), l[h][c]);
                         w[c] = __fmul2_rn(e, make_float2(v_mul, v_mul));
                     }
+                    if constexpr (kFp4) {
+                        half_terms(w[0], w[1], code[h]);
+                    } else {
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        const uint32_t lo = to_e4m3x2(w[0].x, w[0].y);
-                        const uint32_t hi = to_e4m3x2(w[1].x, w[1].y);
-                        code[h][u] = lo | (hi << 16);
-                        if (u < 3) {
-                            take_rest(lo, w[0].x, w[0].y);
-                            take_rest(hi, w[1].x, w[1].y);
-                            const float2 ratio = make_float2(term_ratio(u), term_ratio(u));
-                            w[0] = __fmul2_rn(w[0], ratio);
-                            w[1] = __fmul2_rn(w[1], ratio);
+                        for (int u = 0; u < 4; ++u) {
+                            const uint32_t lo = to_e4m3x2(w[0].x, w[0].y);
+                            const uint32_t hi = to_e4m3x2(w[1].x, w[1].y);
+                            code[h][u] = lo | (hi << 16);
+                            if (u < 3) {
+                                take_rest(lo, w[0].x, w[0].y);
+                                take_rest(hi, w[1].x, w[1].y);
+                                const float2 ratio = make_float2(term_ratio(u), term_ratio(u));
+                                w[0] = __fmul2_rn(w[0], ratio);
+                                w[1] = __fmul2_rn(w[1], ratio);
+                            }
                         }
                     }
                 }
@@ -903,8 +942,8 @@ gqa_decode_codes_kernel(const __grid_constant__ Fp8DecodeParams p) {
                                 }
                     }
                 } else if (tail) {
-                    const int vs = gg % kVStages;
-                    ok = ok && mbar_wait(&bar[kVFull + vs], (gg / kVStages) & 1, p.err);
+                    const int vs = gg % v_stages(kFp4, NC);
+                    ok = ok && mbar_wait(&bar[kVFull + vs], (gg / v_stages(kFp4, NC)) & 1, p.err);
                     uint4 *row = reinterpret_cast<uint4 *>(smem + C::vring + vs * kTileBytes) + k * 8;
                     bool clear = t0 + k >= it.L;     // past the end: may hold anything
                     if (t0 + k >= full && t0 + k < it.L) {
@@ -1006,8 +1045,9 @@ gqa_decode_codes_kernel(const __grid_constant__ Fp8DecodeParams p) {
                     if (i >= nrows) continue;
                     float acc = term[3][u];
 #pragma unroll
-                    for (int v = 2; v >= 0; --v) acc = fmaf(acc, 1.f / term_ratio(v), term[v][u]);
-                    acc = has_o ? acc * (1.f / kWeightTop) : 0.f;
+                    for (int v = 2; v >= 0; --v)
+                        acc = fmaf(acc, kFp4 ? 1.f : 1.f / term_ratio(v), term[v][u]);
+                    acc = has_o ? acc * (1.f / weight_top(kFp4)) : 0.f;
                     const float lsum = (lb[cg] + lb[16 + cg]) + (lb[32 + cg] + lb[48 + cg]);
                     // no visible key: no sum, no reference
                     const float mx = lsum == 0.f ? -INFINITY : lb[64 + cg];
