@@ -92,20 +92,27 @@ constexpr int kMinVExp = -64, kMaxVExp = 64;
 template <int NC, bool kFp4>
 struct Cfg {
     static constexpr int kChunks = NC / 4;
-    static constexpr int kGroups = NC > 4 ? 2 : 1;
-    static constexpr int NCH = kChunks / kGroups;                    // chunks per group
+    // kTurns: the two groups of softmax warps take the tiles in turns, each with weights,
+    // references and an output of its own, which an item's end joins.
+    static constexpr bool kTurns = kFp4 && NC == 4;
+    static constexpr int kGroups = NC > 4 || kTurns ? 2 : 1;
+    static constexpr int kColGroups = kTurns ? 1 : kGroups;          // that share a tile's columns
+    static constexpr int kBufs = kTurns ? 2 : 1;                     // of P and O
+    static constexpr int NCH = kChunks / kColGroups;                 // chunks per group
+    // 4 bits: queries' two terms in columns of their own (as in 8 bits), or added up.
+    static constexpr bool kTermCols = !kFp4 || NC <= 8;
     // N of a score MMA, and the columns of a score buffer: 4 bits, a block of NS columns
     // for each group of channels
-    static constexpr int NS = kFp4 || kChunks < 2 ? 16 : 8 * kChunks;
+    static constexpr int NS = !kTermCols || kChunks < 2 ? 16 : 8 * kChunks;
     static constexpr int kSCols = kFp4 ? kKGroups * NS : NS;
     static constexpr int NP = 16 * kChunks;                          // N of the output MMA
     static constexpr int kTmemO = 2 * kSCols;                        // after two score buffers
-    static constexpr int kTmemUsed = kTmemO + NP;
+    static constexpr int kTmemUsed = kTmemO + kBufs * NP;
     static constexpr int kTmemCols = kTmemUsed <= 64 ? 64 : kTmemUsed <= 128 ? 128 : 256;
-    static constexpr int kQBytes = (kFp4 ? 2 : 1) * NS * 128;        // 4 bits: a tile a term
+    static constexpr int kQBytes = (kTermCols ? 1 : 2) * NS * 128;   // added up: a tile a term
     // Rows of Q: the first of column c's, and from there to its second term's.
-    static constexpr int kTermRows = kFp4 ? NS : 4;
-    static __host__ __device__ constexpr int term0(int c) { return kFp4 ? c : 2 * c - (c & 3); }
+    static constexpr int kTermRows = kTermCols ? 4 : NS;
+    static __host__ __device__ constexpr int term0(int c) { return kTermCols ? 2 * c - (c & 3) : c; }
     static constexpr int kWarpK = 4 * kGroups, kWarpV = kWarpK + 1, kWarpMma = kWarpK + 2,
                          kWarpAux = kWarpK + 3;
     static constexpr int kThreads = 32 * (4 * kGroups + 4);
@@ -114,10 +121,11 @@ struct Cfg {
     static constexpr int vring = kring + kStages * kTileBytes;
     static constexpr int q = vring + v_stages(kFp4, NC) * kTileBytes;          // [kQBufs][terms, rows][128 B]
     static constexpr int p = q + kQBufs * kQBytes;                   // [chunks][128 keys][16 B]
-    static constexpr int sc = p + NP * 128;                          // [kScStages][128] {ks, vs}
+    static constexpr int sc = p + kBufs * NP * 128;                  // [kScStages][128] {ks, vs}
     static constexpr int red = sc + kScStages * kBK * 8;             // float [4][16] tile max
-    static constexpr int lred = red + 4 * 16 * 4;                    // float [2][5][16] row sums, references
-    static constexpr int qf = lred + 2 * 5 * 16 * 4;                 // float [kQBufs][16] 2^-a
+    // (turns: of each group; the maxima have room for one row of 4 columns a group)
+    static constexpr int lred = red + 4 * 16 * 4;                    // float [2][kBufs][5][16] row sums, references
+    static constexpr int qf = lred + 2 * kBufs * 5 * 16 * 4;         // float [kQBufs][16] 2^-a
     static constexpr int bars = qf + 2 * 16 * 4;
     static constexpr int tmem_slot = bars + kBarBytes;
     static constexpr int range = tmem_slot + 16;
@@ -129,9 +137,10 @@ enum Bar {
     kScFull = 12, kScEmpty = 12 + kScStages,         // [kScStages] each
     kQFull = 12 + 2 * kScStages, kQEmpty = kQFull + 2,   // [2] each
     kSFull = kQEmpty + 2, kSFree = kSFull + 2,          // [2] each
-    kPFull = kSFree + 2, kODone = kPFull + 1,
-    kNumBars = kODone + 1
+    kPFull = kSFree + 2, kODone = kPFull + 2,           // [2] each: of a buffer of P and O
+    kNumBars = kODone + 2
 };
+static_assert((kScStages & (kScStages - 1)) == 0, "stages of scales are found with shifts");
 static_assert(kStages == 3 && kNumBars * 8 <= kBarBytes, "barrier layout");
 static_assert(sizeof(Fp8Range) <= 32, "range slot");
 
@@ -231,6 +240,25 @@ __device__ __forceinline__ void tmem_ld_scores(uint32_t t0, uint32_t t1, float (
         : "memory");
 }
 
+// Eight columns of each of the four groups' blocks, one wait for all.
+__device__ __forceinline__ void tmem_ld_group_terms(uint32_t t, float (&v)[kKGroups][8]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%32];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%8, %9, %10, %11, %12, %13, %14, %15}, [%33];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%16, %17, %18, %19, %20, %21, %22, %23}, [%34];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%24, %25, %26, %27, %28, %29, %30, %31}, [%35];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=&f"(v[0][0]), "=&f"(v[0][1]), "=&f"(v[0][2]), "=&f"(v[0][3]),
+          "=&f"(v[0][4]), "=&f"(v[0][5]), "=&f"(v[0][6]), "=&f"(v[0][7]),
+          "=&f"(v[1][0]), "=&f"(v[1][1]), "=&f"(v[1][2]), "=&f"(v[1][3]),
+          "=&f"(v[1][4]), "=&f"(v[1][5]), "=&f"(v[1][6]), "=&f"(v[1][7]),
+          "=&f"(v[2][0]), "=&f"(v[2][1]), "=&f"(v[2][2]), "=&f"(v[2][3]),
+          "=&f"(v[2][4]), "=&f"(v[2][5]), "=&f"(v[2][6]), "=&f"(v[2][7]),
+          "=&f"(v[3][0]), "=&f"(v[3][1]), "=&f"(v[3][2]), "=&f"(v[3][3]),
+          "=&f"(v[3][4]), "=&f"(v[3][5]), "=&f"(v[3][6]), "=&f"(v[3][7])
+        : "r"(t), "r"(t + 16), "r"(t + 32), "r"(t + 48)
+        : "memory");
+}
 // Four columns of each of the four groups' blocks, one chunk or two, one wait for all.
 __device__ __forceinline__ void tmem_ld_groups(uint32_t t0, uint32_t, float (&v)[1][kKGroups][4]) {
     asm volatile(
@@ -517,8 +545,9 @@ __device__ __forceinline__ void feed(const Fp8DecodeParams &p, const int2 *cum, 
                 if (!(fabsf(x[k].y) < INFINITY)) x[k].y = __uint_as_float(0x7fffffffu);
                 const uint32_t h = to_e4m3x2(x[k].x, x[k].y);
                 take_rest(h, x[k].x, x[k].y);
-                if (!kFp4) x[k] = __fmul2_rn(x[k], make_float2(16.f, 16.f));
-                const uint32_t l = kFp4 ? to_e5m2x2(x[k].x, x[k].y) : to_e4m3x2(x[k].x, x[k].y);
+                if (C::kTermCols) x[k] = __fmul2_rn(x[k], make_float2(16.f, 16.f));
+                const uint32_t l = C::kTermCols ? to_e4m3x2(x[k].x, x[k].y)
+                                                : to_e5m2x2(x[k].x, x[k].y);
                 hi[k >> 1] = k & 1 ? hi[k >> 1] | (h << 16) : h;
                 lo[k >> 1] = k & 1 ? lo[k >> 1] | (l << 16) : l;
             }
@@ -594,8 +623,9 @@ gqa_decode_codes_kernel(const __grid_constant__ Fp8DecodeParams p) {
     if (threadIdx.x == 96) {
         for (int i = 0; i < kNumBars; ++i) {
             uint32_t n = 1;
-            if (i == kSFree || i == kSFree + 1 || i == kPFull) n = 4 * C::kGroups;
-            if (i >= kScEmpty && i < kScEmpty + kScStages) n = 4 * C::kGroups;
+            if (i == kSFree || i == kSFree + 1 || i == kPFull || i == kPFull + 1)
+                n = 4 * C::kColGroups;
+            if (i >= kScEmpty && i < kScEmpty + kScStages) n = 4 * C::kColGroups;
             if (i == kQEmpty || i == kQEmpty + 1) n = 4 * C::kGroups + 1;
             if (i >= kScFull && i < kScFull + kScStages) n = 32;
             mbar_init(&bar[i], n);
@@ -608,7 +638,7 @@ gqa_decode_codes_kernel(const __grid_constant__ Fp8DecodeParams p) {
     }
     // Rows of Q and P past the columns in use stay zero.
     if (warp >= 3)
-        for (int i = threadIdx.x - 96; i < (kQBufs * C::kQBytes + C::NP * 128) / 16; i += C::kThreads - 96)
+        for (int i = threadIdx.x - 96; i < (kQBufs * C::kQBytes + C::kBufs * C::NP * 128) / 16; i += C::kThreads - 96)
             reinterpret_cast<uint4 *>(smem + C::q)[i] = make_uint4(0u, 0u, 0u, 0u);
     tc::fence_async_smem();
     tc::fence_before_sync();
@@ -666,10 +696,12 @@ gqa_decode_codes_kernel(const __grid_constant__ Fp8DecodeParams p) {
 #pragma unroll
                         for (int kk = 0; kk < kD / 32; ++kk) {   // 32 channels = 32 bytes a step
                             const uint64_t ka = kd + uint64_t(kk * 2), qa = qd + uint64_t(kk * 2);
-                            if constexpr (kFp4) {                // a group's block, both terms
+                            if constexpr (kFp4) {                // a group's block
                                 const uint32_t to = tm + sb * C::kSCols + kk * C::NS;
                                 mma_f8f6f4(to, ka, qa, idesc_s, false);
-                                mma_f8f6f4(to, ka, qa + uint64_t((C::NS * 128) >> 4), idesc_s1, true);
+                                if (!C::kTermCols)
+                                    mma_f8f6f4(to, ka, qa + uint64_t((C::NS * 128) >> 4), idesc_s1,
+                                               true);
                             } else {
                                 mma_f8f6f4(tm + sb * C::kSCols, ka, qa, idesc_s, kk > 0);
                             }
@@ -683,7 +715,9 @@ gqa_decode_codes_kernel(const __grid_constant__ Fp8DecodeParams p) {
                 if (t >= 1) {
                     const int gp = g + t - 1;
                     const int vs = gp % v_stages(kFp4, NC);
-                    ok = arrived(kPFull, gp & 1);
+                    const int ob = C::kTurns ? gp & 1 : 0;       // buffer of P and O
+                    const int turn = C::kTurns ? gp >> 1 : gp;
+                    ok = arrived(kPFull + ob, turn & 1);
                     if (ok) ok = arrived(kVFull + vs, (gp / v_stages(kFp4, NC)) & 1);
                     if (!ok) break;
                     tc::fence_after_sync();
@@ -694,9 +728,11 @@ gqa_decode_codes_kernel(const __grid_constant__ Fp8DecodeParams p) {
                     if (elect_one()) {
 #pragma unroll
                         for (int kk = 0; kk < kBK / 32; ++kk)
-                            mma_f8f6f4(tm + C::kTmemO, vd + uint64_t((kk * 32 * 128) >> 4),
-                                       pd + uint64_t((kk * 32 * 16) >> 4), idesc_o, t > 1 || kk > 0);
-                        tc::mma_commit(&bar[kODone]);
+                            mma_f8f6f4(tm + C::kTmemO + ob * C::NP,
+                                       vd + uint64_t((kk * 32 * 128) >> 4),
+                                       pd + uint64_t((ob * C::NP * 128 + kk * 32 * 16) >> 4), idesc_o,
+                                       t > C::kBufs || kk > 0);
+                        tc::mma_commit(&bar[kODone + ob]);
                         tc::mma_commit(&bar[kVEmpty + vs]);
                     }
                     __syncwarp();
@@ -715,7 +751,7 @@ gqa_decode_codes_kernel(const __grid_constant__ Fp8DecodeParams p) {
         float *lred = reinterpret_cast<float *>(smem + C::lred);
         const int g_inv = (1 << 16) / G + 1;         // (cg * g_inv) >> 16 = cg / G for cg < 16
         int g = 0, iter = 0, itq = 0;
-        int ss = 0, sph = 0;                         // stage and phase of the scale ring
+        const int buf = C::kTurns ? grp : 0;         // of P and O
         bool ok = true;
         for (int j = 0; j < items; ++j, ++iter) {
             const Fp8Item it = fp8_item(p, cum, walk, j);
@@ -725,7 +761,7 @@ gqa_decode_codes_kernel(const __grid_constant__ Fp8DecodeParams p) {
             // Column cg = (row cg / G, head cg % G); chunk h of this group holds the
             // columns col(h) .. col(h) + 3.  Columns past the item's rows hold an
             // earlier item's scores and are never written out.
-            const auto col = [&](int h) { return 4 * (h * C::kGroups + grp); };
+            const auto col = [&](int h) { return 4 * (h * C::kColGroups + (C::kTurns ? 0 : grp)); };
             const int cols = nrows * G;
             // Pairs of columns go through the packed fp32 instructions.  m is 0 until
             // the first tile sets it: a column that sees no key there sees none at
@@ -759,9 +795,13 @@ gqa_decode_codes_kernel(const __grid_constant__ Fp8DecodeParams p) {
             };
             // Every warp runs every named barrier of every tile, even after a
             // wait gave up (ok == false), so no warp can strand the others.
-            for (int t = 0; t < it.ntiles; ++t) {
+            const int t_first = C::kTurns ? (grp ^ g) & 1 : 0;
+            for (int t = t_first; t < it.ntiles; t += C::kBufs) {
                 const int gg = g + t;
                 const int sb = gg & 1;
+                const bool first = t == t_first;
+                const int ss = gg % kScStages, sph = gg / kScStages & 1;   // of the scale ring
+                const int turn = C::kTurns ? gg >> 1 : gg;                 // of the buffer
                 const int t0 = it.start + t * kBK;
                 const bool tail = t0 + kBK > full;               // uniform over the CTA
                 // ---- scales and scores of this key -------------------------------
@@ -774,11 +814,32 @@ gqa_decode_codes_kernel(const __grid_constant__ Fp8DecodeParams p) {
                 tc::fence_after_sync();
                 float2 s[NCH][2];                                // score, then score - m
                 const uint32_t s_at = tmem + lane_base + sb * C::kSCols;
-                if constexpr (kFp4) {
+                // (4 bits: the key's scales, a group of channels each)
+                const uint32_t exps = __float_as_uint(sc.x);
+                if constexpr (kFp4 && C::kTermCols) {
+                    float raw[kKGroups][8];
+                    tmem_ld_group_terms(s_at + 2 * col(0), raw);
+                    float2 lo[2];
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) s[0][c] = lo[c] = make_float2(0.f, 0.f);
+#pragma unroll
+                    for (int kk = 0; kk < kKGroups; ++kk) {
+                        const float f4 = e8m0(exps, kk);
+                        const float2 f2 = make_float2(f4, f4);
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            s[0][c] = __ffma2_rn(make_float2(raw[kk][2 * c], raw[kk][2 * c + 1]), f2,
+                                                 s[0][c]);
+                            lo[c] = __ffma2_rn(make_float2(raw[kk][4 + 2 * c], raw[kk][5 + 2 * c]),
+                                               f2, lo[c]);
+                        }
+                    }
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+                        s[0][c] = __ffma2_rn(lo[c], make_float2(0.0625f, 0.0625f), s[0][c]);
+                } else if constexpr (kFp4) {
                     float raw[NCH][kKGroups][4];
                     tmem_ld_groups(s_at + col(0), s_at + col(NCH - 1), raw);
-                    // the key's scales, a group of channels each
-                    const uint32_t exps = __float_as_uint(sc.x);
 #pragma unroll
                     for (int h = 0; h < NCH; ++h)
 #pragma unroll
@@ -809,7 +870,6 @@ gqa_decode_codes_kernel(const __grid_constant__ Fp8DecodeParams p) {
                     mbar_arrive(&bar[kSFree + sb]);
                     mbar_arrive(&bar[kScEmpty + ss]);
                 }
-                if (++ss == kScStages) { ss = 0; sph ^= 1; }
                 if (tail && t0 + k >= it.L) sc = make_float2(0.f, 0.f);
                 const int ve_raw = int((__float_as_uint(sc.y) >> 23) & 0xffu) - 127;
                 const int ve = min(max(ve_raw, kMinVExp), kMaxVExp);
@@ -837,7 +897,7 @@ gqa_decode_codes_kernel(const __grid_constant__ Fp8DecodeParams p) {
                 // ---- does any column's reference have to move? --------------------
                 // One barrier with an OR answers for the group; the columns' maxima
                 // are only taken where it says yes (the first tile and a few more).
-                const bool moved = t == 0 || named_or(1 + grp, 128, top > kLazy);
+                const bool moved = first || named_or(1 + grp, 128, top > kLazy);
                 float2 alpha[NCH][2];
                 if (moved) {
 #pragma unroll
@@ -848,17 +908,17 @@ gqa_decode_codes_kernel(const __grid_constant__ Fp8DecodeParams p) {
                             const float w0 = warp_max_redux(s[h][c].x);
                             const float w1 = warp_max_redux(s[h][c].y);
                             if (lane == 0)
-                                *reinterpret_cast<float2 *>(red + kw * 16 + col(h) + 2 * c) =
+                                *reinterpret_cast<float2 *>(red + kw * 16 + 4 * buf + col(h) + 2 * c) =
                                     make_float2(w0, w1);
                         }
                     }
                     named_sync(1 + grp, 128);
-                    const float lazy = t == 0 ? -INFINITY : kLazy;
+                    const float lazy = first ? -INFINITY : kLazy;
                     const auto raise = [&](int cg, float &sx, float &mx, float &lx, float &ax) {
-                        const float up = fmaxf(fmaxf(red[cg], red[16 + cg]),
-                                               fmaxf(red[32 + cg], red[48 + cg]));
+                        const float *r = red + 4 * buf + cg;
+                        const float up = fmaxf(fmaxf(r[0], r[16]), fmaxf(r[32], r[48]));
                         const bool move = up > lazy;
-                        ax = move && t > 0 ? fast_exp2(-up) : 1.f;
+                        ax = move && !first ? fast_exp2(-up) : 1.f;
                         if (move) {
                             mx += up;
                             sx -= up;
@@ -905,17 +965,18 @@ gqa_decode_codes_kernel(const __grid_constant__ Fp8DecodeParams p) {
                         }
                     }
                 }
-                if (t >= 1) {
-                    // O^T(t-1) is complete: P^T may be overwritten and O^T
-                    // rescaled (thread = channel lane).
-                    ok = ok && mbar_wait(&bar[kODone], (gg - 1) & 1, p.err);
+                if (!first) {
+                    // The last P.V of this buffer is complete: P^T may be overwritten and
+                    // O^T rescaled (thread = channel lane).
+                    ok = ok && mbar_wait(&bar[kODone + buf], (turn - 1) & 1, p.err);
                     tc::fence_after_sync();
                     if (moved) {   // identical in every thread of the group
 #pragma unroll
                         for (int h = 0; h < NCH; ++h) {
                             if (col(h) >= cols) continue;
                             float o[16];
-                            const uint32_t oc = tmem + lane_base + C::kTmemO + 4 * col(h);
+                            const uint32_t oc =
+                                tmem + lane_base + C::kTmemO + buf * C::NP + 4 * col(h);
                             tmem_ld_cols<16>(oc, o);
 #pragma unroll
                             for (int c = 0; c < 16; c += 2) {
@@ -984,12 +1045,13 @@ gqa_decode_codes_kernel(const __grid_constant__ Fp8DecodeParams p) {
 #pragma unroll
                 for (int h = 0; h < NCH; ++h)
                     if (col(h) < cols)
-                        *reinterpret_cast<uint4 *>(smem + C::p + 4 * col(h) * kBK + 16 * k) =
+                        *reinterpret_cast<uint4 *>(smem + C::p + buf * C::NP * 128 +
+                                                   4 * col(h) * kBK + 16 * k) =
                             make_uint4(code[h][0], code[h][1], code[h][2], code[h][3]);
                 tc::fence_async_smem();
                 tc::fence_before_sync();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bar[kPFull]);
+                if (lane == 0) mbar_arrive(&bar[kPFull + buf]);
             }
 
             // ---- item epilogue ----------------------------------------------------
@@ -997,7 +1059,9 @@ gqa_decode_codes_kernel(const __grid_constant__ Fp8DecodeParams p) {
             // from a cold instruction cache (all 8 columns of a warp unrolled: 10000
             // cycles; a pair at a time: 3000 to 5000).  The row sums and references go
             // through shared memory while the last P.V is still in flight.
-            float *lb = lred + (iter & 1) * 80;   // [4 key warps][16 columns], then m[16]
+            // [4 key warps][16 columns], then m[16]; turns: each group's
+            const float *both = lred + (iter & 1) * 80 * C::kBufs;
+            float *lb = lred + ((iter & 1) * C::kBufs + buf) * 80;
             // (halving butterfly: the warp's sum of column n ends up in the lanes whose
             // upper bits are n)
             float part[4 * NCH];
@@ -1025,32 +1089,58 @@ gqa_decode_codes_kernel(const __grid_constant__ Fp8DecodeParams p) {
                     for (int c = 0; c < 2; ++c)
                         *reinterpret_cast<float2 *>(lb + 64 + col(h) + 2 * c) = m[h][c];
             }
-            named_sync(1 + grp, 128);
-            if (it.ntiles > 0)
-                ok = ok && mbar_wait(&bar[kODone], (g + it.ntiles - 1) & 1, p.err);
+            if (C::kTurns) named_sync(3, 256); else named_sync(1 + grp, 128);
+            // the last P.V of each buffer that had a tile of the item
+            const int tiles_of[2] = {
+                C::kTurns ? (it.ntiles + 1 - (g & 1)) >> 1 : it.ntiles, (it.ntiles + (g & 1)) >> 1};
+#pragma unroll
+            for (int q = 0; q < C::kBufs; ++q) {
+                const int last = C::kTurns ? ((g + it.ntiles - 1 - q) >> 1) : g + it.ntiles - 1;
+                if (tiles_of[q] > 0) ok = ok && mbar_wait(&bar[kODone + q], last & 1, p.err);
+            }
             tc::fence_after_sync();
-            const bool has_o = ok && it.ntiles > 0;
             const int ch = k;   // output channel of this thread
             const size_t head0 = size_t(row0) * p.num_q_heads + it.kvh * G;
             const size_t slot0 = size_t(it.slot) * kGqaSlotCols;
+            // (turns: a group has two of the columns)
 #pragma unroll 1
-            for (int x = 0; x < 4 * NCH; x += 2) {
+            for (int x = C::kTurns ? 2 * grp : 0; x < (C::kTurns ? 2 * grp + 2 : 4 * NCH); x += 2) {
                 const int c0 = col(x >> 2) + (x & 3);
                 if (c0 >= cols) break;
-                float term[4][2];
-                tmem_ld_terms(tmem + lane_base + C::kTmemO + 4 * (c0 & ~3) + (c0 & 3), term);
+                float o[C::kBufs][2];
+#pragma unroll
+                for (int q = 0; q < C::kBufs; ++q) {
+                    float term[4][2];
+                    tmem_ld_terms(
+                        tmem + lane_base + C::kTmemO + q * C::NP + 4 * (c0 & ~3) + (c0 & 3), term);
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        float acc = term[3][u];
+#pragma unroll
+                        for (int v = 2; v >= 0; --v)
+                            acc = fmaf(acc, kFp4 ? 1.f : 1.f / term_ratio(v), term[v][u]);
+                        o[q][u] = ok && tiles_of[q] > 0 ? acc * (1.f / weight_top(kFp4)) : 0.f;
+                    }
+                }
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     const int cg = c0 + u, i = (cg * g_inv) >> 16;
                     if (i >= nrows) continue;
-                    float acc = term[3][u];
-#pragma unroll
-                    for (int v = 2; v >= 0; --v)
-                        acc = fmaf(acc, kFp4 ? 1.f : 1.f / term_ratio(v), term[v][u]);
-                    acc = has_o ? acc * (1.f / weight_top(kFp4)) : 0.f;
-                    const float lsum = (lb[cg] + lb[16 + cg]) + (lb[32 + cg] + lb[48 + cg]);
+                    float acc = o[0][u];
+                    float lsum = (both[cg] + both[16 + cg]) + (both[32 + cg] + both[48 + cg]);
                     // no visible key: no sum, no reference
-                    const float mx = lsum == 0.f ? -INFINITY : lb[64 + cg];
+                    float mx = lsum == 0.f ? -INFINITY : both[64 + cg];
+                    if constexpr (C::kTurns) {
+                        const float *b2 = both + 80;
+                        const float l2 = (b2[cg] + b2[16 + cg]) + (b2[32 + cg] + b2[48 + cg]);
+                        const float m2 = l2 == 0.f ? -INFINITY : b2[64 + cg];
+                        const float top = fmaxf(mx, m2);
+                        const float a1 = l2 == 0.f ? 0.f : fast_exp2(m2 - top);
+                        const float a0 = lsum == 0.f ? 0.f : fast_exp2(mx - top);
+                        acc = fmaf(acc, a0, o[1][u] * a1);
+                        lsum = fmaf(lsum, a0, l2 * a1);
+                        mx = top;
+                    }
                     if (it.direct) {
                         const float t2 = p.sink ? p.sink[it.kvh * G + cg - i * G] * kLog2e : -INFINITY;
                         const float Mf = fmaxf(mx, t2);
@@ -1075,6 +1165,7 @@ gqa_decode_codes_kernel(const __grid_constant__ Fp8DecodeParams p) {
                 }
             }
             tc::fence_before_sync();
+            if (C::kTurns) named_sync(3, 256);   // both groups have read both outputs
             // The CTA holding the unit's first tile publishes where its pieces are.
             if (it.first && threadIdx.x == 0 && p.unit_slots)
                 p.unit_slots[it.b * (p.num_q_heads / G) + it.kvh] =

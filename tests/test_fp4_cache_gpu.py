@@ -7,17 +7,24 @@ two e2m1 numbers around y or the nearest: |code 2^e - y| <= half a step of the g
 2^-e (0.25 below 2, 0.5 to 4, 1 to 6) times 2^e + err.  Keys that are neither normed nor
 rotated, and values, have no err: their codes and scales are exact, ties to the even code.
 
-Decode attends over code * scale in 64 bits; the kernel may differ by what the 8-bit one
-may (tests/test_decode_fp8_gpu.py: the weights' terms are the same, and of the queries the
-terms miss at most 2^-21 of the row's largest channel, and that only in channels below 2^-13
-of it; a score is a sum of 2 x 4 blocks of 32 exact products and four products with powers of
-two): |out - exact| <= 2^-8 |exact| + (2^-11 + 4 rho) sum_j w_j |v_j| (times 1.01) and
-|lse - exact| <= rho + 2^-20 max(1, |exact|), rho = 2^-16 max_j sum_c |q_c k_jc| scale + 2^-20.
-To that comes what the entry point says of small weights: with e_j the exponent of key j's
-value scale and u the largest w_j 2^(e_j), a w_j 2^(e_j) may miss 2^-29 u instead, so that out
-misses at most 2^-29 u sum_j 2^(-e_j) |v_j|.  The random codes of these tests make rows in
-which one key has all but 2^-25 of the weight and a value of 0: there out is small weights
-alone, and this term the whole of the bound.
+Decode attends over code * scale in 64 bits.  What the kernel may differ by:
+
+* weights: p_j 2^(e_j), e_j the exponent of the key's value scale, is rounded to f16 (2^-11 of
+  itself at most; the exponential before that errs by 2^-22) and enters the product as four
+  e5m2 terms of 3 bits each, which hold all 11 bits down to 2^-16 in units in which the
+  largest, u, is 2^11 at least: what is cut off is less than 2^-27 u.  So out misses at most
+  2^-11 sum_j w_j |v_j| + 2^-27 u sum_j 2^(-e_j) |v_j| by this, with w_j the normalised weights
+  and u the largest w_j 2^(e_j).  (The random codes of these tests make rows in which one key
+  has all but 2^-25 of the weight and a value of 0: there out is small weights alone.)
+* scores: the queries' two terms miss at most 2^-21 of the row's largest channel, and that
+  only in channels below 2^-13 of it; a score is a sum of 2 x 4 blocks of 32 exact products
+  and four products with powers of two, each step rounded in fp32.  rho = 2^-16 max_j sum_c
+  |q_c k_jc| scale + 2^-20 bounds it as for the 8-bit cache; it moves every weight and the
+  normaliser by a factor of at most 1 + 2 rho.
+* half a bf16 step of out, 2^-8 |out|.
+
+So |out - exact| <= 2^-8 |exact| + 1.01 (2^-11 + 2^-20 + 4 rho) sum_j w_j |v_j| + 2^-27 u sum_j
+2^(-e_j) |v_j|, and |lse - exact| <= rho + 2^-20 max(1, |exact|).
 """
 import math
 
@@ -374,7 +381,7 @@ class Case:
         return seqs
 
     def small_weights(self):
-        """2^-29 u sum_j 2^(-e_j) |v_j| of every row and head."""
+        """2^-27 u sum_j 2^(-e_j) |v_j| of every row and head."""
         K, V = self.sequences()
         out = torch.zeros(self.q.shape, dtype=torch.float64)
         for b, L in enumerate(self.lens):
@@ -393,7 +400,7 @@ class Case:
                     x = e[:lim, g].double()
                     f = torch.exp2(torch.floor(torch.log2(x.clamp_min(2.0 ** -126))))
                     u = (p / z * f).max()
-                    out[r, h] = 2.0 ** -29 * u * (V[b][:lim, g].abs() / f[:, None]).sum(0)
+                    out[r, h] = 2.0 ** -27 * u * (V[b][:lim, g].abs() / f[:, None]).sum(0)
         return out
 
     def reference(self):
@@ -411,7 +418,7 @@ class Case:
         n = eo.shape[0]
         o, l = o[:n], l[:n]
         rho = (2.0 ** -16 * big + 2.0 ** -20)[..., None]
-        bound = (R.BF16_HALF * eo.abs() + 1.01 * (2.0 ** -11 + 4 * rho) * mass +
+        bound = (R.BF16_HALF * eo.abs() + 1.01 * (2.0 ** -11 + 2.0 ** -20 + 4 * rho) * mass +
                  self.small_weights()[:n] + 2.0 ** -130)
         worst = ((o - eo).abs() / bound).max().item()
         assert bool(torch.isfinite(o).all()) and worst <= 1, f"{what}: {worst:.3g} times the bound"
