@@ -115,6 +115,7 @@ struct Cfg {
     static __host__ __device__ constexpr int term0(int c) { return kTermCols ? 2 * c - (c & 3) : c; }
     static constexpr int kWarpK = 4 * kGroups, kWarpV = kWarpK + 1, kWarpMma = kWarpK + 2,
                          kWarpAux = kWarpK + 3;
+    static constexpr bool kTwoMmaWarps = kFp4;           // kWarpV's is the outputs' (kWarpK loads both)
     static constexpr int kThreads = 32 * (4 * kGroups + 4);
     // shared memory
     static constexpr int kring = 0;
@@ -406,19 +407,18 @@ __device__ __forceinline__ void lookup_boxes(const Fp8DecodeParams &p, const Fp8
 
 // K or V producer: walks this CTA's items and tiles and lets lane 0 issue the
 // boxes of each tile into the ring.
-template <bool kIsK, int NC, bool kFp4>
+template <bool kIsK, int NC>
 __device__ __forceinline__ void produce(const Fp8DecodeParams &p, const int2 *cum, const Fp8Range &w,
                                         uint8_t *smem, uint64_t *bar, int lane) {
     const CUtensorMap *map = kIsK ? &p.k_map : &p.v_map;
     uint64_t *full = bar + (kIsK ? kKFull : kVFull);
     uint64_t *empty = bar + (kIsK ? kKEmpty : kVEmpty);
-    uint8_t *ring = smem + (kIsK ? Cfg<NC, kFp4>::kring : Cfg<NC, kFp4>::vring);
-    constexpr int kN = kIsK ? kStages : v_stages(kFp4, NC);
+    uint8_t *ring = smem + (kIsK ? Cfg<NC, false>::kring : Cfg<NC, false>::vring);
+    constexpr int kN = kIsK ? kStages : v_stages(false, NC);
     const int box_rows = p.box_rows;        // 128, 64, 32, 16 or 8
     const int box_shift = 31 - __clz(box_rows);
     const int nb = kBK >> box_shift;        // row boxes per tile
-    const uint32_t row_bytes = kFp4 ? 64u : 128u;               // in memory: what a copy counts
-    const uint32_t box_bytes = uint32_t(box_rows) * row_bytes;
+    const uint32_t box_bytes = uint32_t(box_rows) * 128u;
     int g = 0;
     bool aborted = false;
     for (int j = 0, items = w.count(); j < items && !aborted; ++j) {
@@ -451,7 +451,7 @@ __device__ __forceinline__ void produce(const Fp8DecodeParams &p, const int2 *cu
                     if (page < 0)
                         mbar_complete_tx(&full[s], box_bytes);       // skipped bad page
                     else
-                        tma_load_4d(dst + r * box_rows * 128, map, &full[s], 0, slot, it.kvh, page);
+                        tma_load_4d(dst + r * box_bytes, map, &full[s], 0, slot, it.kvh, page);
                 }
             }
         }
@@ -461,6 +461,66 @@ __device__ __forceinline__ void produce(const Fp8DecodeParams &p, const int2 *cu
     if (lane == 0)
         for (int i = max(0, g - kN); i < g; ++i)
             mbar_wait(&full[i % kN], (i / kN) & 1, p.err);
+}
+
+// Producer of the 4-bit kernel: the boxes of both operands of each tile, a box a lane.
+template <int NC>
+__device__ __forceinline__ void produce_both(const Fp8DecodeParams &p, const int2 *cum,
+                                             const Fp8Range &w, uint8_t *smem, uint64_t *bar,
+                                             int lane) {
+    using C = Cfg<NC, true>;
+    constexpr int kVs = v_stages(true, NC);
+    const int box_rows = p.box_rows;        // 128, 64, 32, 16 or 8
+    const int box_shift = 31 - __clz(box_rows);
+    const int nb = kBK >> box_shift;        // row boxes per tile
+    const uint32_t box_bytes = uint32_t(box_rows) * 64u;        // in memory: what a copy counts
+    int g = 0;
+    bool ok = true;
+    for (int j = 0, items = w.count(); j < items && ok; ++j) {
+        const Fp8Item it = fp8_item(p, cum, w, j);
+        if (it.ntiles == 0) continue;
+        int cached = -1, page = -1, slot = 0;
+        for (int t = 0; t < it.ntiles; ++t, ++g) {
+            const int key0 = it.start + t * kBK;
+            const int live = min(nb, (it.L - key0 + box_rows - 1) >> box_shift);
+            const int box0 = t * nb;                             // box index in the item
+            if ((box0 >> 5) != cached) {
+                cached = box0 >> 5;
+                lookup_boxes(p, it, cached, lane, true, page, slot);
+            }
+            const int r = lane - (box0 & 31);
+            const auto issue = [&](uint64_t *full, uint64_t *empty, int n, const CUtensorMap *map,
+                                   uint8_t *ring) {
+                const int s = g % n;
+                if (lane == 0) {
+                    if (g >= n) ok = mbar_wait(&empty[s], ((g / n) - 1) & 1, p.err);
+                    if (ok) mbar_arrive_expect_tx(&full[s], uint32_t(live) * box_bytes);
+                }
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+                if (!ok || r < 0 || r >= live) return;
+                if (page < 0)
+                    mbar_complete_tx(&full[s], box_bytes);       // skipped bad page
+                else
+                    tma_load_4d(ring + s * kTileBytes + r * box_rows * 128, map, &full[s], 0, slot,
+                                it.kvh, page);
+            };
+            issue(bar + kKFull, bar + kKEmpty, kStages, &p.k_map, smem + C::kring);
+            if (!ok) break;
+            __syncwarp();
+            issue(bar + kVFull, bar + kVEmpty, kVs, &p.v_map, smem + C::vring);
+            if (!ok) break;
+            __syncwarp();
+        }
+    }
+    // Every copy this warp issued must land before the CTA may leave (after a wait that gave
+    // up, tile g's keys may have been sent for as well).
+    if (lane == 0) {
+        const int k_end = ok ? g : g + 1;
+        for (int i = max(0, k_end - kStages); i < k_end; ++i)
+            mbar_wait(&bar[kKFull + i % kStages], (i / kStages) & 1, p.err);
+        for (int i = max(0, g - kVs); i < g; ++i)
+            mbar_wait(&bar[kVFull + i % kVs], (i / kVs) & 1, p.err);
+    }
 }
 
 __device__ __forceinline__ void cp_async_4(void *dst, const float *src) {
@@ -649,16 +709,22 @@ gqa_decode_codes_kernel(const __grid_constant__ Fp8DecodeParams p) {
     const int items = walk.count();
 
     if (warp == C::kWarpK) {
-        produce<true, NC, kFp4>(p, cum, walk, smem, bar, lane);
-    } else if (warp == C::kWarpV) {
-        produce<false, NC, kFp4>(p, cum, walk, smem, bar, lane);
+        if constexpr (kFp4)
+            produce_both<NC>(p, cum, walk, smem, bar, lane);
+        else
+            produce<true, NC>(p, cum, walk, smem, bar, lane);
+    } else if (!C::kTwoMmaWarps && warp == C::kWarpV) {
+        produce<false, NC>(p, cum, walk, smem, bar, lane);
     } else if (warp == C::kWarpAux) {
         feed<NC, kFp4>(p, cum, walk, smem, bar, lane);
-    } else if (warp == C::kWarpMma) {
+    } else if (warp == C::kWarpMma || (C::kTwoMmaWarps && warp == C::kWarpV)) {
         // ---------------------------------------------------------- MMA issue
-        // The whole warp walks, with numbers that are the same in all lanes, and one lane
-        // issues: what the tensor core is given then is in uniform registers (one lane that
-        // walks by itself took 130 cycles an MMA to move it there).
+        // A warp for both contractions, or (4 bits, whose tiles come twice as fast) one for
+        // each.  The whole warp walks, with numbers that are the same in all lanes, and one
+        // lane issues: what the tensor core is given then is in uniform registers (one lane
+        // that walks by itself took 130 cycles an MMA to move it there).
+        const bool scores = !C::kTwoMmaWarps || warp == C::kWarpMma;
+        const bool outputs = !C::kTwoMmaWarps || warp == C::kWarpV;
         constexpr uint32_t held = kFp4 ? kE2m1 : kE4m3;
         constexpr uint32_t idesc_s = idesc_f8f6f4(held, kE4m3, 128, C::NS, 0, 0);
         constexpr uint32_t idesc_s1 = idesc_f8f6f4(held, kE5m2, 128, C::NS, 0, 0);
@@ -676,66 +742,72 @@ gqa_decode_codes_kernel(const __grid_constant__ Fp8DecodeParams p) {
         };
         int g = 0, itq = 0;
         bool ok = true;
+        // S of tile gg of the walk, whose item's queries are in buffer qb; last: of the item
+        const auto issue_scores = [&](int gg, int qb, bool last) {
+            const int ks = gg % kStages;
+            const int sb = gg & 1;
+            ok = arrived(kKFull + ks, (gg / kStages) & 1);
+            if (ok && gg >= 2) ok = arrived(kSFree + sb, ((gg >> 1) - 1) & 1);
+            if (!ok) return;
+            tc::fence_after_sync();
+            const uint64_t kd = tc::smem_desc_sw128(k_base + ks * kTileBytes, 16, 1024);
+            const uint64_t qd = tc::smem_desc_sw128(q_base + qb * C::kQBytes, 16, 1024);
+            if (elect_one()) {
+#pragma unroll
+                for (int kk = 0; kk < kD / 32; ++kk) {           // 32 channels = 32 bytes a step
+                    const uint64_t ka = kd + uint64_t(kk * 2), qa = qd + uint64_t(kk * 2);
+                    if constexpr (kFp4) {                        // a group's block
+                        const uint32_t to = tm + sb * C::kSCols + kk * C::NS;
+                        mma_f8f6f4(to, ka, qa, idesc_s, false);
+                        if (!C::kTermCols)
+                            mma_f8f6f4(to, ka, qa + uint64_t((C::NS * 128) >> 4), idesc_s1, true);
+                    } else {
+                        mma_f8f6f4(tm + sb * C::kSCols, ka, qa, idesc_s, kk > 0);
+                    }
+                }
+                tc::mma_commit(&bar[kSFull + sb]);
+                tc::mma_commit(&bar[kKEmpty + ks]);
+                if (last) tc::mma_commit(&bar[kQEmpty + qb]);
+            }
+            __syncwarp();
+        };
+        // O += V P of tile gp, the t-th of its item
+        const auto issue_outputs = [&](int gp, int t) {
+            const int vs = gp % v_stages(kFp4, NC);
+            const int ob = C::kTurns ? gp & 1 : 0;               // buffer of P and O
+            const int turn = C::kTurns ? gp >> 1 : gp;
+            ok = arrived(kPFull + ob, turn & 1);
+            if (ok) ok = arrived(kVFull + vs, (gp / v_stages(kFp4, NC)) & 1);
+            if (!ok) return;
+            tc::fence_after_sync();
+            // V^T as the MN-major A operand: 128 channels are one 128-byte
+            // atom, 8-key groups 1 KB apart, 32 keys a step.
+            const uint64_t vd = tc::smem_desc_sw128(v_base + vs * kTileBytes, kTileBytes, 1024);
+            if (elect_one()) {
+#pragma unroll
+                for (int kk = 0; kk < kBK / 32; ++kk)
+                    mma_f8f6f4(tm + C::kTmemO + ob * C::NP, vd + uint64_t((kk * 32 * 128) >> 4),
+                               pd + uint64_t((ob * C::NP * 128 + kk * 32 * 16) >> 4), idesc_o,
+                               t >= C::kBufs || kk > 0);
+                tc::mma_commit(&bar[kODone + ob]);
+                tc::mma_commit(&bar[kVEmpty + vs]);
+            }
+            __syncwarp();
+        };
         for (int j = 0; ok && j < count; ++j) {
             const int ntiles = __shfl_sync(0xffffffffu, fp8_item(p, cum, walk, j).ntiles, 0);
             if (ntiles == 0) continue;
             const int qb = itq % kQBufs;
-            ok = arrived(kQFull + qb, (itq / kQBufs) & 1);
-            for (int t = 0; ok && t <= ntiles; ++t) {
-                if (t < ntiles) {
-                    const int gg = g + t;
-                    const int ks = gg % kStages;
-                    const int sb = gg & 1;
-                    ok = arrived(kKFull + ks, (gg / kStages) & 1);
-                    if (ok && gg >= 2) ok = arrived(kSFree + sb, ((gg >> 1) - 1) & 1);
-                    if (!ok) break;
-                    tc::fence_after_sync();
-                    const uint64_t kd = tc::smem_desc_sw128(k_base + ks * kTileBytes, 16, 1024);
-                    const uint64_t qd = tc::smem_desc_sw128(q_base + qb * C::kQBytes, 16, 1024);
-                    if (elect_one()) {
-#pragma unroll
-                        for (int kk = 0; kk < kD / 32; ++kk) {   // 32 channels = 32 bytes a step
-                            const uint64_t ka = kd + uint64_t(kk * 2), qa = qd + uint64_t(kk * 2);
-                            if constexpr (kFp4) {                // a group's block
-                                const uint32_t to = tm + sb * C::kSCols + kk * C::NS;
-                                mma_f8f6f4(to, ka, qa, idesc_s, false);
-                                if (!C::kTermCols)
-                                    mma_f8f6f4(to, ka, qa + uint64_t((C::NS * 128) >> 4), idesc_s1,
-                                               true);
-                            } else {
-                                mma_f8f6f4(tm + sb * C::kSCols, ka, qa, idesc_s, kk > 0);
-                            }
-                        }
-                        tc::mma_commit(&bar[kSFull + sb]);
-                        tc::mma_commit(&bar[kKEmpty + ks]);
-                        if (t == ntiles - 1) tc::mma_commit(&bar[kQEmpty + qb]);
-                    }
-                    __syncwarp();
+            if (scores) ok = arrived(kQFull + qb, (itq / kQBufs) & 1);
+            if (C::kTwoMmaWarps) {
+                for (int t = 0; ok && t < ntiles; ++t) {
+                    if (scores) issue_scores(g + t, qb, t == ntiles - 1);
+                    else issue_outputs(g + t, t);
                 }
-                if (t >= 1) {
-                    const int gp = g + t - 1;
-                    const int vs = gp % v_stages(kFp4, NC);
-                    const int ob = C::kTurns ? gp & 1 : 0;       // buffer of P and O
-                    const int turn = C::kTurns ? gp >> 1 : gp;
-                    ok = arrived(kPFull + ob, turn & 1);
-                    if (ok) ok = arrived(kVFull + vs, (gp / v_stages(kFp4, NC)) & 1);
-                    if (!ok) break;
-                    tc::fence_after_sync();
-                    // V^T as the MN-major A operand: 128 channels are one 128-byte
-                    // atom, 8-key groups 1 KB apart, 32 keys a step.
-                    const uint64_t vd =
-                        tc::smem_desc_sw128(v_base + vs * kTileBytes, kTileBytes, 1024);
-                    if (elect_one()) {
-#pragma unroll
-                        for (int kk = 0; kk < kBK / 32; ++kk)
-                            mma_f8f6f4(tm + C::kTmemO + ob * C::NP,
-                                       vd + uint64_t((kk * 32 * 128) >> 4),
-                                       pd + uint64_t((ob * C::NP * 128 + kk * 32 * 16) >> 4), idesc_o,
-                                       t > C::kBufs || kk > 0);
-                        tc::mma_commit(&bar[kODone + ob]);
-                        tc::mma_commit(&bar[kVEmpty + vs]);
-                    }
-                    __syncwarp();
+            } else {
+                for (int t = 0; ok && t <= ntiles; ++t) {
+                    if (t < ntiles) issue_scores(g + t, qb, t == ntiles - 1);
+                    if (ok && t >= 1) issue_outputs(g + t - 1, t - 1);
                 }
             }
             g += ntiles;
