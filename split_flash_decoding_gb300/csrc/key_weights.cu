@@ -170,6 +170,14 @@ __device__ __forceinline__ int page_at(const WeightsParams &p, int b, int t, boo
     return e;
 }
 
+// One lane of the warp (all lanes take part).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(one));
+    return one != 0;
+}
+
 __device__ __forceinline__ void cp_async_4(void *dst, const float *src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(dst)), "l"(src)
                  : "memory");
@@ -220,7 +228,7 @@ key_weights_kernel(const __grid_constant__ WeightsParams p) {
     uint64_t *bar = reinterpret_cast<uint64_t *>(smem + C::bars);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::tmem_slot);
     int *cum = reinterpret_cast<int *>(smem + C::items);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int stride = static_cast<int>(gridDim.x);
 
     if (blockIdx.x == 0 && warp == 0)
@@ -341,45 +349,56 @@ key_weights_kernel(const __grid_constant__ WeightsParams p) {
         }
     } else if (warp == C::kWarpMma) {
         // ------------------------------------------------------------ MMA issue
-        if (lane == 0) {
-            constexpr uint32_t idesc = tc::idesc_bf16_f32(128, NQ, 0, 0);
-            const uint32_t k_base = smem_addr(smem + C::k), q_base = smem_addr(smem + C::q);
-            int g = 0, gk = 0;
-            bool ok = true;
-            for (int j = blockIdx.x; ok && j < total; j += stride) {
-                if (!find_unit<kMany>(p, cum, j, it) || it.steps == 0) continue;
-                for (int h = 0; ok && h < it.heads; ++h) {
-                    const int ks = gk % C::kKStages;
-                    ok = mbar_wait(&bar[C::bKFull + ks], (gk / C::kKStages) & 1, p.err);
-                    for (int t = 0; ok && t < it.steps; ++t, ++g) {
-                        const int qs = g % C::kQStages;
-                        ok = mbar_wait(&bar[C::bQFull + qs], (g / C::kQStages) & 1, p.err);
-                        const uint64_t qd = tc::smem_desc_sw128(q_base + qs * C::kQBytes, 16, 1024);
+        // (The whole warp walks, with numbers that are the same in all lanes, and one lane
+        // issues: what the tensor core is given then is in uniform registers.)
+        constexpr uint32_t idesc = tc::idesc_bf16_f32(128, NQ, 0, 0);
+        const uint32_t k_base = smem_addr(smem + C::k), q_base = smem_addr(smem + C::q);
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        const auto arrived = [&](int b, int phase) {
+            return __all_sync(0xffffffffu, mbar_wait(&bar[b], phase, p.err)) != 0;
+        };
+        int g = 0, gk = 0;
+        bool ok = true;
+        for (int j = blockIdx.x; ok && j < total; j += stride) {
+            if (!find_unit<kMany>(p, cum, j, it)) continue;
+            const int steps = __shfl_sync(0xffffffffu, it.steps, 0);
+            const int heads = __shfl_sync(0xffffffffu, it.heads, 0);
+            if (steps == 0) continue;
+            for (int h = 0; ok && h < heads; ++h, ++gk) {
+                const int ks = gk % C::kKStages;
+                ok = arrived(C::bKFull + ks, (gk / C::kKStages) & 1);
+                for (int t = 0; ok && t < steps; ++t, ++g) {
+                    const int qs = g % C::kQStages;
+                    ok = arrived(C::bQFull + qs, (g / C::kQStages) & 1);
+                    const uint64_t qd = tc::smem_desc_sw128(q_base + qs * C::kQBytes, 16, 1024);
 #pragma unroll
-                        for (int kt = 0; kt < KT; ++kt) {
-                            const int x = g * KT + kt, sb = x & 1;   // score tile and its buffer
-                            if (ok && x >= 2)
-                                ok = mbar_wait(&bar[C::bSFree + sb], ((x >> 1) - 1) & 1, p.err);
-                            if (!ok) break;
-                            tc::fence_after_sync();
-                            const uint64_t kd = tc::smem_desc_sw128(
-                                k_base + (ks * KT + kt) * C::kTileBytes, 16, 1024);
-                            if (columns_of(p, it, kt, t).any()) {
+                    for (int kt = 0; kt < KT; ++kt) {
+                        const int x = g * KT + kt, sb = x & 1;   // score tile and its buffer
+                        if (ok && x >= 2) ok = arrived(C::bSFree + sb, ((x >> 1) - 1) & 1);
+                        if (!ok) break;
+                        tc::fence_after_sync();
+                        const uint64_t kd = tc::smem_desc_sw128(
+                            k_base + (ks * KT + kt) * C::kTileBytes, 16, 1024);
+                        const bool any =
+                            __all_sync(0xffffffffu, columns_of(p, it, kt, t).any()) != 0;
+                        if (elect_one()) {
+                            if (any) {
 #pragma unroll
                                 for (int kk = 0; kk < D / 16; ++kk) {
-                                    const uint32_t in = (kk & 3) * 32;   // within the 64 channels' rows
-                                    tc::mma_bf16(tmem + sb * NQ,
-                                                 kd + uint64_t(((kk >> 2) * (kKeys * 128) + in) >> 4),
-                                                 qd + uint64_t(((kk >> 2) * (NQ * 128) + in) >> 4), idesc,
-                                                 kk > 0);
+                                    const uint32_t in = (kk & 3) * 32;   // in the 64 channels' rows
+                                    tc::mma_bf16(
+                                        tm + sb * NQ,
+                                        kd + uint64_t(((kk >> 2) * (kKeys * 128) + in) >> 4),
+                                        qd + uint64_t(((kk >> 2) * (NQ * 128) + in) >> 4), idesc,
+                                        kk > 0);
                                 }
                             }
                             tc::mma_commit(&bar[C::bSFull + sb]);
+                            if (kt == KT - 1) tc::mma_commit(&bar[C::bQEmpty + qs]);
+                            if (kt == KT - 1 && t == steps - 1) tc::mma_commit(&bar[C::bKEmpty + ks]);
                         }
-                        if (ok) tc::mma_commit(&bar[C::bQEmpty + qs]);
+                        __syncwarp();
                     }
-                    if (ok) tc::mma_commit(&bar[C::bKEmpty + ks]);
-                    ++gk;
                 }
             }
         }
