@@ -49,11 +49,9 @@ append_fp4_kernel(const __grid_constant__ RowsParams p) {
     const int e = tiles::fp4_exponent(top);
     const float f = tiles::pow2i(-e);
     const float s = whole ? tiles::pow2i(e) : __uint_as_float(0x7fffffffu);
-    const uint32_t lo = __nv_cvt_float2_to_fp4x2(make_float2(v.x * f, v.y * f), __NV_E2M1,
-                                                 cudaRoundNearest);
-    const uint32_t hi = __nv_cvt_float2_to_fp4x2(make_float2(v.z * f, v.w * f), __NV_E2M1,
-                                                 cudaRoundNearest);
-    const uint32_t word = whole ? lo | (hi << 8) : 0u;
+    const float2 z[4] = {make_float2(v.x * f, v.y * f), make_float2(v.z * f, v.w * f),
+                         make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+    const uint32_t word = whole ? tiles::to_fp4x8(z) : 0u;
     if (page >= 0) {
         *reinterpret_cast<uint16_t *>(c.base + page * c.page_stride + slot * c.token_stride +
                                       h * c.head_stride + 2 * lane) = static_cast<uint16_t>(word);
@@ -65,13 +63,9 @@ append_fp4_kernel(const __grid_constant__ RowsParams p) {
         }
     }
     if (x.out) {
-        const auto number = [&](uint32_t two) {
-            const float2 n = __half22float2(__half2(__nv_cvt_fp4x2_to_halfraw2(
-                static_cast<__nv_fp4x2_storage_t>(two & 0xffu), __NV_E2M1)));
-            return pack_bf16x2(n.x * s, n.y * s);
-        };
+        const uint4 n = tiles::from_fp4x8(word, s);
         *reinterpret_cast<uint2 *>(x.out + r * x.out_row + h * x.out_head + 4 * lane) =
-            make_uint2(number(word), number(word >> 8));
+            make_uint2(n.x, n.y);
     }
 }
 

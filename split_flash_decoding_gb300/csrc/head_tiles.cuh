@@ -33,7 +33,7 @@
 // vectors in all but odd rotations) and store eight codes a word.
 #pragma once
 
-#include <cuda_fp4.h>
+#include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <float.h>
 
@@ -462,6 +462,36 @@ struct Item {
     }
 };
 
+// Eight numbers to e2m1, rounded to nearest even, the first in the lowest four bits.
+__device__ __forceinline__ uint32_t to_fp4x8(const float2 (&y)[4]) {
+    uint32_t w;
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+        "mov.b32 %0, {a, b, c, d};\n\t}"
+        : "=r"(w)
+        : "f"(y[0].x), "f"(y[0].y), "f"(y[1].x), "f"(y[1].y), "f"(y[2].x), "f"(y[2].y), "f"(y[3].x),
+          "f"(y[3].y));
+    return w;
+}
+
+// And what eight codes stand for, times s, as bf16 (exact for powers of two).
+__device__ __forceinline__ uint4 from_fp4x8(uint32_t w, float s) {
+    uint32_t h[4], o[4];
+    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(w));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 v = __fmul2_rn(__half22float2(*reinterpret_cast<const __half2 *>(&h[i])),
+                                    make_float2(s, s));
+        o[i] = pack_bf16x2(v.x, v.y);
+    }
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
 // One head of a row, on 8 lanes, into a cache held in 4 bits; y: the lane's two vectors.
 // The largest value decides by its bits, as a number above all finite ones where an
 // infinity or a NaN is among them: the scale is NaN then.  The code of x 2^-e is rounded
@@ -508,11 +538,9 @@ __device__ __forceinline__ void store_fp4(const RowsParams &p, const Place &at, 
         const bool whole = top < 0x7f800000u;
         const int e = fp4_exponent(top);
         const float f = pow2i(-e);
-        uint32_t word = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            word |= uint32_t(__nv_cvt_float2_to_fp4x2(__fmul2_rn(y[i], make_float2(f, f)), __NV_E2M1,
-                                                      cudaRoundNearest)) << (8 * i);
+        const float2 z[4] = {__fmul2_rn(y[0], make_float2(f, f)), __fmul2_rn(y[1], make_float2(f, f)),
+                             __fmul2_rn(y[2], make_float2(f, f)), __fmul2_rn(y[3], make_float2(f, f))};
+        uint32_t word = to_fp4x8(z);
         if (!whole) word = 0;
         if (at.stored > 0) {
             *reinterpret_cast<uint32_t *>(c.base + head_at + ch / 2) = word;
@@ -522,14 +550,8 @@ __device__ __forceinline__ void store_fp4(const RowsParams &p, const Place &at, 
         }
         if (x.out && at.stored >= 0) {                           // what the codes stand for
             const float s = whole ? pow2i(e) : __uint_as_float(0x7fffffffu);
-            float2 v[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                v[i] = __fmul2_rn(__half22float2(__half2(__nv_cvt_fp4x2_to_halfraw2(
-                                      static_cast<__nv_fp4x2_storage_t>(word >> (8 * i) & 0xffu),
-                                      __NV_E2M1))),
-                                  make_float2(s, s));
-            *reinterpret_cast<uint4 *>(x.out + row * x.out_row + head * x.out_head + ch) = pack8(v);
+            *reinterpret_cast<uint4 *>(x.out + row * x.out_row + head * x.out_head + ch) =
+                from_fp4x8(word, s);
         }
     };
     half(ta, ca, ya);
