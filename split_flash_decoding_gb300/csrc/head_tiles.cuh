@@ -492,21 +492,28 @@ __device__ __forceinline__ uint4 from_fp4x8(uint32_t w, float s) {
     return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// One head of a row, on 8 lanes, into a cache held in 4 bits; y: the lane's two vectors.
-// The largest value decides by its bits, as a number above all finite ones where an
-// infinity or a NaN is among them: the scale is NaN then.  The code of x 2^-e is rounded
-// once, as the product is exact.
+// Largest |value| of eight; NaN if there is one.
+__device__ __forceinline__ float top_of(const float2 (&y)[4]) {
+    const auto max3 = [](float a, float b, float c) {
+        float r;
+        asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+        return r;
+    };
+    return max3(max3(max3(fabsf(y[0].x), fabsf(y[0].y), fabsf(y[1].x)), fabsf(y[1].y),
+                     fabsf(y[2].x)),
+                fabsf(y[2].y), max3(fabsf(y[3].x), fabsf(y[3].y), 0.f));
+}
+
+// One head of a row, on 8 lanes, into a cache held in 4 bits; y: the lane's two vectors, out:
+// where what the codes stand for goes (or nullptr).  The largest value decides by its bits, as
+// a number above all finite ones where an infinity or a NaN is among them: the scale is NaN
+// then.  The code of x 2^-e is rounded once, as the product is exact.
 __device__ __forceinline__ void store_fp4(const RowsParams &p, const Place &at, int kind, int head,
-                                          int row, int ca, int cb, bool grouped,
+                                          uint16_t *out, int ca, int cb, bool grouped,
                                           const float2 (&ya)[4], const float2 (&yb)[4]) {
     // (a warp's other heads may be queries: the eight lanes go by themselves)
     const unsigned mine = 0xffu << (threadIdx.x & 24);
-    uint32_t ta = 0, tb = 0;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        ta = max(max(ta, __float_as_uint(fabsf(ya[c].x))), __float_as_uint(fabsf(ya[c].y)));
-        tb = max(max(tb, __float_as_uint(fabsf(yb[c].x))), __float_as_uint(fabsf(yb[c].y)));
-    }
+    uint32_t ta = __float_as_uint(top_of(ya)), tb = __float_as_uint(top_of(yb));
     if (kind == 2) {                                             // values: one scale
         ta = max(ta, tb);
 #pragma unroll
@@ -529,33 +536,40 @@ __device__ __forceinline__ void store_fp4(const RowsParams &p, const Place &at, 
         ta = ca >> 5 == 0 ? m[0] : ca >> 5 == 1 ? m[1] : ca >> 5 == 2 ? m[2] : m[3];
         tb = cb >> 5 == 0 ? m[0] : cb >> 5 == 1 ? m[1] : cb >> 5 == 2 ? m[2] : m[3];
     }
-    const HeadRows &x = kind == 1 ? p.k : p.v;
-    const CacheOut &c = kind == 1 ? p.kc : p.vc;
-    const long long head_at = head * c.head_stride + (kind == 1 ? at.k_at : at.v_at);
-    uint8_t *scale = reinterpret_cast<uint8_t *>(c.scale + at.page * c.scale_page +
-                                                 at.slot * c.scale_block + head * c.scale_head);
-    const auto half = [&](uint32_t top, int ch, const float2 (&y)[4]) {
-        const bool whole = top < 0x7f800000u;
-        const int e = fp4_exponent(top);
-        const float f = pow2i(-e);
-        const float2 z[4] = {__fmul2_rn(y[0], make_float2(f, f)), __fmul2_rn(y[1], make_float2(f, f)),
-                             __fmul2_rn(y[2], make_float2(f, f)), __fmul2_rn(y[3], make_float2(f, f))};
-        uint32_t word = to_fp4x8(z);
-        if (!whole) word = 0;
-        if (at.stored > 0) {
-            *reinterpret_cast<uint32_t *>(c.base + head_at + ch / 2) = word;
-            if (kind == 1 && (ch & 31) == 0) scale[ch >> 5] = whole ? uint8_t(e + 127) : 255;
-            if (kind == 2 && ch == 0)
-                *reinterpret_cast<float *>(scale) = whole ? pow2i(e) : __uint_as_float(0x7fffffffu);
+    const bool na = ta >= 0x7f800000u, nb = tb >= 0x7f800000u;
+    const int ea = fp4_exponent(ta), eb = fp4_exponent(tb);
+    const float fa = pow2i(-ea), fb = pow2i(-eb);
+    float2 za[4], zb[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        za[i] = __fmul2_rn(ya[i], make_float2(fa, fa));
+        zb[i] = __fmul2_rn(yb[i], make_float2(fb, fb));
+    }
+    const uint32_t wa = na ? 0u : to_fp4x8(za), wb = nb ? 0u : to_fp4x8(zb);
+    const float nan = __uint_as_float(0x7fffffffu);
+    const float sa = na ? nan : pow2i(ea), sb = nb ? nan : pow2i(eb);
+    if (at.stored > 0) {
+        const CacheOut &c = kind == 1 ? p.kc : p.vc;
+        uint8_t *to = c.base + (head * c.head_stride + (kind == 1 ? at.k_at : at.v_at));
+        *reinterpret_cast<uint32_t *>(to + (ca >> 1)) = wa;
+        *reinterpret_cast<uint32_t *>(to + (cb >> 1)) = wb;
+        // (one of the lanes that share a scale has its first channel)
+        if (kind == 1 ? ((ca & 31) == 0 || (cb & 31) == 0) : ca == 0) {
+            float *scale = c.scale + at.page * c.scale_page + at.slot * c.scale_block +
+                           head * c.scale_head;
+            if (kind == 2) {
+                *scale = sa;
+            } else {
+                uint8_t *bytes = reinterpret_cast<uint8_t *>(scale);
+                if ((ca & 31) == 0) bytes[ca >> 5] = na ? 255 : uint8_t(ea + 127);
+                if ((cb & 31) == 0) bytes[cb >> 5] = nb ? 255 : uint8_t(eb + 127);
+            }
         }
-        if (x.out && at.stored >= 0) {                           // what the codes stand for
-            const float s = whole ? pow2i(e) : __uint_as_float(0x7fffffffu);
-            *reinterpret_cast<uint4 *>(x.out + row * x.out_row + head * x.out_head + ch) =
-                from_fp4x8(word, s);
-        }
-    };
-    half(ta, ca, ya);
-    half(tb, cb, yb);
+    }
+    if (out && at.stored >= 0) {
+        *reinterpret_cast<uint4 *>(out + ca) = from_fp4x8(wa, sa);
+        *reinterpret_cast<uint4 *>(out + cb) = from_fp4x8(wb, sb);
+    }
 }
 
 // kMany: a CTA has more heads than it works on at once (never with the 8-bit cache).
@@ -714,7 +728,8 @@ head_tiles_kernel(const __grid_constant__ RowsParams p, const __grid_constant__ 
                 rotate_pairs<kInter>(ya[k], yb[k], t[k * L], it.flags & Item::kTurnB);
         }
         if (kKind == kFp4 && it.kind != 0) {
-            store_fp4(p, at, it.kind, it.head, r0 + it.row, it.ca, it.cb, cut.grouped != 0, ya, yb);
+            store_fp4(p, at, it.kind, it.head, it.to_cache ? nullptr : it.dst, it.ca, it.cb,
+                      cut.grouped != 0, ya, yb);
         } else if (!kFp8 || it.kind == 0) {
             uint16_t *dst = it.dst;
             bool store = at.stored >= 0;
