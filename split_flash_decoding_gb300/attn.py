@@ -281,16 +281,16 @@ def _kv_pair(k_cache, v_cache, page_table, dtype):
 def _fp4_scales(k_scale, v_scale, k_shape, v_shape):
     """The scales of caches held in 4 bits [pages, page_size, heads, 64]: a key's four
     float8_e8m0fnu side by side, a value's fp32."""
-    k_strides, v_strides = k_scale.stride(), v_scale.stride()
     if k_scale.dtype != torch.float8_e8m0fnu or k_scale.shape != (*k_shape[:3], 4):
         raise ValueError("k_scale must be float8_e8m0fnu [pages, page_size, num_kv_heads, 4]")
     if v_scale.dtype != torch.float32 or v_scale.shape != v_shape[:3]:
         raise ValueError("v_scale must be fp32 [pages, page_size, num_kv_heads]")
-    words = [x // 4 for x in k_strides[:3]]
-    if k_strides[3] != 1 or tuple(4 * x for x in words) != k_strides[:3] or k_scale.data_ptr() % 4:
+    page, token, head, channel = k_scale.stride()
+    at = k_scale.data_ptr()
+    if channel != 1 or (page | token | head | at) & 3:
         raise ValueError("a key's four scales must be contiguous and 4-byte aligned")
-    return (_pack_kv_scale(k_scale.data_ptr(), *words, 1, 0),
-            _pack_kv_scale(v_scale.data_ptr(), *v_strides, 1, 0))
+    return (_pack_kv_scale(at, page >> 2, token >> 2, head >> 2, 1, 0),
+            _pack_kv_scale(v_scale.data_ptr(), *v_scale.stride(), 1, 0))
 
 
 def _scale_pair(k_scale, v_scale, k_shape, v_shape):
@@ -920,27 +920,31 @@ def attn_evict_kv(k_cache: torch.Tensor, v_cache: Optional[torch.Tensor], weight
     that is read), their weights beside them.  keep int32 [batch] on the device, at most
     max_keep.  v_cache and v_out None: a cache whose V is part of K.  Returns (kept_len
     int32 [batch], indices int32 [batch, num_kv_heads, max_keep]: the kept tokens)."""
-    batch, heads, dim = kv_len.shape[0], k_cache.shape[2], k_cache.shape[3]
+    k_shape, out_shape, batch = k_cache.shape, k_out.shape, kv_len.shape[0]
+    heads, dim = k_shape[2:]
     if (v_cache is None) != (v_out is None):
         raise ValueError("v_cache and v_out go together")
-    for table in (page_table, out_page_table):
-        if table is not None and table.shape[0] != batch:
-            raise ValueError("page tables must have one row per sequence")
-    if k_out.shape[2:] != k_cache.shape[2:]:
-        raise ValueError(f"a cache {tuple(k_cache.shape)} does not fit {tuple(k_out.shape)}")
-    kd = _pack_kv(*_kv_fields(k_cache, page_table, torch.bfloat16))
-    kod = _pack_kv(*_kv_fields(k_out, out_page_table, torch.bfloat16))
+    if ((page_table is not None and page_table.shape[0] != batch) or
+            (out_page_table is not None and out_page_table.shape[0] != batch)):
+        raise ValueError("page tables must have one row per sequence")
+    if out_shape[2:] != k_shape[2:]:
+        raise ValueError(f"a cache {tuple(k_shape)} does not fit {tuple(out_shape)}")
     vd = vod = None
     dim_v = 0
-    if v_cache is not None:
-        dim_v = v_cache.shape[3]
-        if (v_cache.shape[:3] != k_cache.shape[:3] or v_out.shape[:3] != k_out.shape[:3] or
-                v_out.shape[3] != dim_v):
+    if v_cache is None:
+        kd = _pack_kv(*_kv_fields(k_cache, page_table, torch.bfloat16))
+        kod = _pack_kv(*_kv_fields(k_out, out_page_table, torch.bfloat16))
+    else:
+        v_shape, v_out_shape = v_cache.shape, v_out.shape
+        dim_v = v_shape[3]
+        if ((v_shape != k_shape or v_out_shape != out_shape) and
+                (v_shape[:3] != k_shape[:3] or v_out_shape[:3] != out_shape[:3] or
+                 v_out_shape[3] != dim_v)):
             raise ValueError("v_cache and v_out must have the pages and heads of k_cache and k_out")
-        vd = _pack_kv(*_kv_fields(v_cache, page_table, torch.bfloat16))
-        vod = _pack_kv(*_kv_fields(v_out, out_page_table, torch.bfloat16))
-    wd = _token_floats(weights, k_cache.shape, "weights")
-    wod = None if weights_out is None else _token_floats(weights_out, k_out.shape, "weights_out")
+        kd, vd = _kv_pair(k_cache, v_cache, page_table, torch.bfloat16)
+        kod, vod = _kv_pair(k_out, v_out, out_page_table, torch.bfloat16)
+    wd = _token_floats(weights, k_shape, "weights")
+    wod = None if weights_out is None else _token_floats(weights_out, out_shape, "weights_out")
     lens, keeps = _int32(kv_len, batch, "kv_len"), _int32(keep, batch, "keep")
     if kept_len is None:
         kept_len = _empty((batch,), torch.int32, k_cache.device, stream)
