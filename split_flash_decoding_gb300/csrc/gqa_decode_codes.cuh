@@ -300,6 +300,19 @@ __device__ __forceinline__ void tmem_ld_groups(uint32_t t0, uint32_t t1,
         : "memory");
 }
 
+// Whether the phase with the given parity is complete, now.
+__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
 // Maximum over the 32 lanes of the warp (NaN ignored; every lane gets it).
 __device__ __forceinline__ float warp_max_redux(float v) {
     float r;
@@ -463,7 +476,10 @@ __device__ __forceinline__ void produce(const Fp8DecodeParams &p, const int2 *cu
             mbar_wait(&full[i % kN], (i / kN) & 1, p.err);
 }
 
-// Producer of the 4-bit kernel: the boxes of both operands of each tile, a box a lane.
+// Producer of the 4-bit kernel's variants of more columns: the boxes of both operands of each
+// tile, a box a lane, one operand after the other.  There the softmax is what the stages wait
+// for, and a warp that asks for both without a pause takes its issue slots (1 to 4 draft rows
+// 79.7 us against 83.6).
 template <int NC>
 __device__ __forceinline__ void produce_both(const Fp8DecodeParams &p, const int2 *cum,
                                              const Fp8Range &w, uint8_t *smem, uint64_t *bar,
@@ -519,6 +535,98 @@ __device__ __forceinline__ void produce_both(const Fp8DecodeParams &p, const int
         for (int i = max(0, k_end - kStages); i < k_end; ++i)
             mbar_wait(&bar[kKFull + i % kStages], (i / kStages) & 1, p.err);
         for (int i = max(0, g - kVs); i < g; ++i)
+            mbar_wait(&bar[kVFull + i % kVs], (i / kVs) & 1, p.err);
+    }
+}
+
+// Where one operand's producer is in the walk of a CTA's tiles.
+struct Walk {
+    Fp8Item it;
+    int j, t, g;                   // item, tile of it, tile of the walk
+    int cached, page, slot;        // 32 boxes' places, one per lane
+    bool more;
+};
+
+// Producer of the 4-bit kernel where the groups of softmax warps take turns: keys and values go
+// at their own pace.  (A value stage is free a softmax later than its tile's key stage, and keys
+// that waited for it came too late: 64 sequences 62.0 us in step and 60.2 so, 131072 keys 35.9
+// and 33.5.)
+template <int NC>
+__device__ __forceinline__ void produce_paced(const Fp8DecodeParams &p, const int2 *cum,
+                                             const Fp8Range &w, uint8_t *smem, uint64_t *bar,
+                                             int lane) {
+    using C = Cfg<NC, true>;
+    const int box_rows = p.box_rows;        // 128, 64, 32, 16 or 8
+    const int box_shift = 31 - __clz(box_rows);
+    const int nb = kBK >> box_shift;        // row boxes per tile
+    const uint32_t box_bytes = uint32_t(box_rows) * 64u;        // in memory: what a copy counts
+    const int items = w.count();
+    const auto open = [&](Walk &x) {        // the next item with tiles
+        x.more = false;
+        x.t = 0;
+        x.cached = -1;
+        while (!x.more && ++x.j < items) {
+            x.it = fp8_item(p, cum, w, x.j);
+            x.more = x.it.ntiles > 0;
+        }
+    };
+    // Sends for the walk's tile, if its stage is free; n stages.
+    const auto step = [&](Walk &x, bool is_k, uint64_t *full, uint64_t *empty, int n,
+                          const CUtensorMap *map, uint8_t *ring) -> bool {
+        if (!x.more) return false;
+        const int s = x.g % n;
+        if (x.g >= n) {
+            const bool is_free = mbar_test(&empty[s], ((x.g / n) - 1) & 1);
+            if (!__shfl_sync(0xffffffffu, is_free, 0)) return false;
+        }
+        const int key0 = x.it.start + x.t * kBK;
+        const int live = min(nb, (x.it.L - key0 + box_rows - 1) >> box_shift);
+        const int box0 = x.t * nb;                               // box index in the item
+        if ((box0 >> 5) != x.cached) {
+            x.cached = box0 >> 5;
+            lookup_boxes(p, x.it, x.cached, lane, is_k, x.page, x.slot);
+        }
+        if (lane == 0) mbar_arrive_expect_tx(&full[s], uint32_t(live) * box_bytes);
+        __syncwarp();
+        const int r = lane - (box0 & 31);
+        if (r >= 0 && r < live) {
+            if (x.page < 0)
+                mbar_complete_tx(&full[s], box_bytes);           // skipped bad page
+            else
+                tma_load_4d(ring + s * kTileBytes + r * box_rows * 128, map, &full[s], 0, x.slot,
+                            x.it.kvh, x.page);
+        }
+        __syncwarp();
+        ++x.g;
+        if (++x.t == x.it.ntiles) open(x);
+        return true;
+    };
+    constexpr int kVs = v_stages(true, NC);
+    Walk k, v;
+    k.j = v.j = -1;
+    k.g = v.g = 0;
+    open(k);
+    open(v);
+    unsigned long long since = 0;           // of the last step that found neither stage free
+    while (k.more || v.more) {
+        const bool a = step(k, true, bar + kKFull, bar + kKEmpty, kStages, &p.k_map, smem + C::kring);
+        const bool b = step(v, false, bar + kVFull, bar + kVEmpty, kVs, &p.v_map, smem + C::vring);
+        if (a || b) {
+            since = 0;
+            continue;
+        }
+        const unsigned long long now = __shfl_sync(0xffffffffu, global_ns(), 0);
+        if (since == 0) since = now;
+        if (now - since > kWaitLimitNs) {
+            if (lane == 0) atomicOr(p.err, kErrWaitTimeout);
+            break;
+        }
+    }
+    // Every copy this warp issued must land before the CTA may leave.
+    if (lane == 0) {
+        for (int i = max(0, k.g - kStages); i < k.g; ++i)
+            mbar_wait(&bar[kKFull + i % kStages], (i / kStages) & 1, p.err);
+        for (int i = max(0, v.g - kVs); i < v.g; ++i)
             mbar_wait(&bar[kVFull + i % kVs], (i / kVs) & 1, p.err);
     }
 }
@@ -709,10 +817,14 @@ gqa_decode_codes_kernel(const __grid_constant__ Fp8DecodeParams p) {
     const int items = walk.count();
 
     if (warp == C::kWarpK) {
-        if constexpr (kFp4)
-            produce_both<NC>(p, cum, walk, smem, bar, lane);
-        else
+        if constexpr (kFp4) {
+            if constexpr (C::kTurns)
+                produce_paced<NC>(p, cum, walk, smem, bar, lane);
+            else
+                produce_both<NC>(p, cum, walk, smem, bar, lane);
+        } else {
             produce<true, NC>(p, cum, walk, smem, bar, lane);
+        }
     } else if (!C::kTwoMmaWarps && warp == C::kWarpV) {
         produce<false, NC>(p, cum, walk, smem, bar, lane);
     } else if (warp == C::kWarpAux) {
