@@ -67,8 +67,12 @@ namespace codes {
 constexpr int kD = 128;
 constexpr int kBK = kGqaTcTileKeys;          // 128 keys per tile
 constexpr int kStages = 3;                   // K tiles in flight
-// V tiles in flight: as many as leave two CTAs room (8 bits: three measured the same).
+// V tiles in flight (kVs): as many as leave two CTAs room (8 bits: three measured the same).
+// 4 bits, 4 columns: three, and two where the table of that many sequences takes the third's
+// room (512 sequences of 512 to 1024 keys: 135 us, 168 with three and one CTA an SM; 1024 of 64
+// keys 97 and 183).
 __host__ __device__ constexpr int v_stages(bool fp4, int nc) { return fp4 && nc == 4 ? 3 : 2; }
+constexpr size_t kCtaSmem = 113 * 1024;      // a CTA of two on an SM
 constexpr int kTileBytes = kBK * kD;         // 16 KB (4 bits: 16 codes in the first 8 of 16 bytes)
 constexpr int kKGroups = 4;                  // 4 bits: scales of a key, 32 channels each
 constexpr int kScStages = 4;                 // tiles of scales in flight
@@ -89,7 +93,7 @@ constexpr int kMinVExp = -64, kMaxVExp = 64;
 // rows) are [2 terms][4], its O columns (and P columns) [4 terms][4].  More than one
 // chunk takes two groups of four softmax warps; group g has the chunks g, g + 2.  Chunks
 // past an item's columns are skipped.
-template <int NC, bool kFp4>
+template <int NC, bool kFp4, int kVs>
 struct Cfg {
     static constexpr int kChunks = NC / 4;
     // kTurns: the two groups of softmax warps take the tiles in turns, each with weights,
@@ -120,7 +124,7 @@ struct Cfg {
     // shared memory
     static constexpr int kring = 0;
     static constexpr int vring = kring + kStages * kTileBytes;
-    static constexpr int q = vring + v_stages(kFp4, NC) * kTileBytes;          // [kQBufs][terms, rows][128 B]
+    static constexpr int q = vring + kVs * kTileBytes;          // [kQBufs][terms, rows][128 B]
     static constexpr int p = q + kQBufs * kQBytes;                   // [chunks][128 keys][16 B]
     static constexpr int sc = p + kBufs * NP * 128;                  // [kScStages][128] {ks, vs}
     static constexpr int red = sc + kScStages * kBK * 8;             // float [4][16] tile max
@@ -145,9 +149,9 @@ static_assert((kScStages & (kScStages - 1)) == 0, "stages of scales are found wi
 static_assert(kStages == 3 && kNumBars * 8 <= kBarBytes, "barrier layout");
 static_assert(sizeof(Fp8Range) <= 32, "range slot");
 
-template <int NC, bool kFp4>
+template <int NC, bool kFp4, int kVs>
 size_t smem_bytes(int batch) {
-    return size_t(Cfg<NC, kFp4>::items) + sizeof(int2) * size_t(batch + 1);
+    return size_t(Cfg<NC, kFp4, kVs>::items) + sizeof(int2) * size_t(batch + 1);
 }
 
 // Element types of kind::f8f6f4.
@@ -420,14 +424,14 @@ __device__ __forceinline__ void lookup_boxes(const Fp8DecodeParams &p, const Fp8
 
 // K or V producer: walks this CTA's items and tiles and lets lane 0 issue the
 // boxes of each tile into the ring.
-template <bool kIsK, int NC>
+template <bool kIsK, int NC, int kVs>
 __device__ __forceinline__ void produce(const Fp8DecodeParams &p, const int2 *cum, const Fp8Range &w,
                                         uint8_t *smem, uint64_t *bar, int lane) {
     const CUtensorMap *map = kIsK ? &p.k_map : &p.v_map;
     uint64_t *full = bar + (kIsK ? kKFull : kVFull);
     uint64_t *empty = bar + (kIsK ? kKEmpty : kVEmpty);
-    uint8_t *ring = smem + (kIsK ? Cfg<NC, false>::kring : Cfg<NC, false>::vring);
-    constexpr int kN = kIsK ? kStages : v_stages(false, NC);
+    uint8_t *ring = smem + (kIsK ? Cfg<NC, false, kVs>::kring : Cfg<NC, false, kVs>::vring);
+    constexpr int kN = kIsK ? kStages : kVs;
     const int box_rows = p.box_rows;        // 128, 64, 32, 16 or 8
     const int box_shift = 31 - __clz(box_rows);
     const int nb = kBK >> box_shift;        // row boxes per tile
@@ -480,12 +484,11 @@ __device__ __forceinline__ void produce(const Fp8DecodeParams &p, const int2 *cu
 // tile, a box a lane, one operand after the other.  There the softmax is what the stages wait
 // for, and a warp that asks for both without a pause takes its issue slots (1 to 4 draft rows
 // 79.7 us against 83.6).
-template <int NC>
+template <int NC, int kVs>
 __device__ __forceinline__ void produce_both(const Fp8DecodeParams &p, const int2 *cum,
                                              const Fp8Range &w, uint8_t *smem, uint64_t *bar,
                                              int lane) {
-    using C = Cfg<NC, true>;
-    constexpr int kVs = v_stages(true, NC);
+    using C = Cfg<NC, true, kVs>;
     const int box_rows = p.box_rows;        // 128, 64, 32, 16 or 8
     const int box_shift = 31 - __clz(box_rows);
     const int nb = kBK >> box_shift;        // row boxes per tile
@@ -551,11 +554,11 @@ struct Walk {
 // at their own pace.  (A value stage is free a softmax later than its tile's key stage, and keys
 // that waited for it came too late: 64 sequences 62.0 us in step and 60.2 so, 131072 keys 35.9
 // and 33.5.)
-template <int NC>
+template <int NC, int kVs>
 __device__ __forceinline__ void produce_paced(const Fp8DecodeParams &p, const int2 *cum,
                                              const Fp8Range &w, uint8_t *smem, uint64_t *bar,
                                              int lane) {
-    using C = Cfg<NC, true>;
+    using C = Cfg<NC, true, kVs>;
     const int box_rows = p.box_rows;        // 128, 64, 32, 16 or 8
     const int box_shift = 31 - __clz(box_rows);
     const int nb = kBK >> box_shift;        // row boxes per tile
@@ -601,7 +604,6 @@ __device__ __forceinline__ void produce_paced(const Fp8DecodeParams &p, const in
         if (++x.t == x.it.ntiles) open(x);
         return true;
     };
-    constexpr int kVs = v_stages(true, NC);
     Walk k, v;
     k.j = v.j = -1;
     k.g = v.g = 0;
@@ -647,10 +649,10 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
 
 // Auxiliary warp: the terms of each item's queries and the scales of each
 // tile's keys.
-template <int NC, bool kFp4>
+template <int NC, bool kFp4, int kVs>
 __device__ __forceinline__ void feed(const Fp8DecodeParams &p, const int2 *cum, const Fp8Range &w,
                                      uint8_t *smem, uint64_t *bar, int lane) {
-    using C = Cfg<NC, kFp4>;
+    using C = Cfg<NC, kFp4, kVs>;
     const int G = p.group;
     const int g_inv = (1 << 16) / G + 1;            // (c * g_inv) >> 16 = c / G for c < 16
     const int box_shift = 31 - __clz(p.box_rows);   // a power of two
@@ -770,10 +772,10 @@ __device__ __forceinline__ void feed(const Fp8DecodeParams &p, const int2 *cum, 
     asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-template <int NC, bool kFp4>
-__global__ void __launch_bounds__(Cfg<NC, kFp4>::kThreads, kCtasPerSm)
+template <int NC, bool kFp4, int kVs>
+__global__ void __launch_bounds__(Cfg<NC, kFp4, kVs>::kThreads, kCtasPerSm)
 gqa_decode_codes_kernel(const __grid_constant__ Fp8DecodeParams p) {
-    using C = Cfg<NC, kFp4>;
+    using C = Cfg<NC, kFp4, kVs>;
     constexpr int NCH = C::NCH;
     extern __shared__ __align__(1024) uint8_t smem[];
     uint64_t *bar = reinterpret_cast<uint64_t *>(smem + C::bars);
@@ -819,16 +821,16 @@ gqa_decode_codes_kernel(const __grid_constant__ Fp8DecodeParams p) {
     if (warp == C::kWarpK) {
         if constexpr (kFp4) {
             if constexpr (C::kTurns)
-                produce_paced<NC>(p, cum, walk, smem, bar, lane);
+                produce_paced<NC, kVs>(p, cum, walk, smem, bar, lane);
             else
-                produce_both<NC>(p, cum, walk, smem, bar, lane);
+                produce_both<NC, kVs>(p, cum, walk, smem, bar, lane);
         } else {
-            produce<true, NC>(p, cum, walk, smem, bar, lane);
+            produce<true, NC, kVs>(p, cum, walk, smem, bar, lane);
         }
     } else if (!C::kTwoMmaWarps && warp == C::kWarpV) {
-        produce<false, NC>(p, cum, walk, smem, bar, lane);
+        produce<false, NC, kVs>(p, cum, walk, smem, bar, lane);
     } else if (warp == C::kWarpAux) {
-        feed<NC, kFp4>(p, cum, walk, smem, bar, lane);
+        feed<NC, kFp4, kVs>(p, cum, walk, smem, bar, lane);
     } else if (warp == C::kWarpMma || (C::kTwoMmaWarps && warp == C::kWarpV)) {
         // ---------------------------------------------------------- MMA issue
         // A warp for both contractions, or (4 bits, whose tiles come twice as fast) one for
@@ -885,11 +887,11 @@ gqa_decode_codes_kernel(const __grid_constant__ Fp8DecodeParams p) {
         };
         // O += V P of tile gp, the t-th of its item
         const auto issue_outputs = [&](int gp, int t) {
-            const int vs = gp % v_stages(kFp4, NC);
+            const int vs = gp % kVs;
             const int ob = C::kTurns ? gp & 1 : 0;               // buffer of P and O
             const int turn = C::kTurns ? gp >> 1 : gp;
             ok = arrived(kPFull + ob, turn & 1);
-            if (ok) ok = arrived(kVFull + vs, (gp / v_stages(kFp4, NC)) & 1);
+            if (ok) ok = arrived(kVFull + vs, (gp / kVs) & 1);
             if (!ok) return;
             tc::fence_after_sync();
             // V^T as the MN-major A operand: 128 channels are one 128-byte
@@ -1187,8 +1189,8 @@ gqa_decode_codes_kernel(const __grid_constant__ Fp8DecodeParams p) {
                                 }
                     }
                 } else if (tail) {
-                    const int vs = gg % v_stages(kFp4, NC);
-                    ok = ok && mbar_wait(&bar[kVFull + vs], (gg / v_stages(kFp4, NC)) & 1, p.err);
+                    const int vs = gg % kVs;
+                    ok = ok && mbar_wait(&bar[kVFull + vs], (gg / kVs) & 1, p.err);
                     uint4 *row = reinterpret_cast<uint4 *>(smem + C::vring + vs * kTileBytes) + k * 8;
                     bool clear = t0 + k >= it.L;     // past the end: may hold anything
                     if (t0 + k >= full && t0 + k < it.L) {
@@ -1367,14 +1369,14 @@ gqa_decode_codes_kernel(const __grid_constant__ Fp8DecodeParams p) {
     }
 }
 
-template <int NC, bool kFp4>
+template <int NC, bool kFp4, int kVs>
 cudaError_t launch_nc(const Fp8DecodeParams &p, int ctas, cudaStream_t stream) {
-    const size_t smem = smem_bytes<NC, kFp4>(p.batch);
-    auto kern = gqa_decode_codes_kernel<NC, kFp4>;
+    const size_t smem = smem_bytes<NC, kFp4, kVs>(p.batch);
+    auto kern = gqa_decode_codes_kernel<NC, kFp4, kVs>;
     const cudaError_t e =
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
     if (e != cudaSuccess) return e;
-    kern<<<dim3(static_cast<unsigned>(ctas)), Cfg<NC, kFp4>::kThreads, smem, stream>>>(p);
+    kern<<<dim3(static_cast<unsigned>(ctas)), Cfg<NC, kFp4, kVs>::kThreads, smem, stream>>>(p);
     return cudaGetLastError();
 }
 
@@ -1382,9 +1384,14 @@ template <bool kFp4>
 cudaError_t launch(const Fp8DecodeParams &p, int ctas, cudaStream_t stream) {
     const int cols = p.max_q_len * p.group;
     if (cols < 1 || cols > 16) return cudaErrorInvalidValue;
-    if (cols <= 4) return launch_nc<4, kFp4>(p, ctas, stream);
-    if (cols <= 8) return launch_nc<8, kFp4>(p, ctas, stream);
-    return launch_nc<16, kFp4>(p, ctas, stream);
+    if (cols <= 4) {
+        constexpr int kVs = v_stages(kFp4, 4);
+        if (kVs > 2 && smem_bytes<4, kFp4, kVs>(p.batch) > kCtaSmem)
+            return launch_nc<4, kFp4, 2>(p, ctas, stream);
+        return launch_nc<4, kFp4, kVs>(p, ctas, stream);
+    }
+    if (cols <= 8) return launch_nc<8, kFp4, 2>(p, ctas, stream);
+    return launch_nc<16, kFp4, 2>(p, ctas, stream);
 }
 
 }  // namespace codes

@@ -505,6 +505,13 @@ def test_many_sequences_cut_and_whole(attn):
     Case(torch.randint(0, 900, (150,), generator=g).tolist(), hq=4, hkv=1, page=16, seed=2).check(attn)
 
 
+@pytest.mark.parametrize("batch", [388, 2048])
+def test_more_sequences_than_leave_room_for_three_stages(attn, batch):
+    g = torch.Generator().manual_seed(batch)
+    Case(torch.randint(0, 600 if batch < 1000 else 200, (batch,), generator=g).tolist(), hq=4, hkv=1,
+         page=16, seed=2).check(attn)
+
+
 def test_long_sequence(attn):
     Case([20000], hq=4, hkv=1, page=128, seed=2, sink=True).check(attn)
 
