@@ -740,14 +740,13 @@ def attn_append_kv_fp4(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
     page_size, num_kv_heads], any strides (a head's tokens side by side read best).  k_out,
     v_out: bf16 rows as k and v that take what the new codes stand for, or None.
     Returns q_out."""
+    scales = _fp4_scales(k_scale, v_scale, k_cache.shape, v_cache.shape)
     q_out, head, tail, device = _append_args(k, v, k_cache, v_cache, kv_len, page_table, q, q_out,
                                              q_row_offsets, rope, positions, q_norm, k_norm, eps,
                                              stream, torch.uint8, k_scale, v_scale, k_out=k_out,
                                              v_out=v_out)
     _check("attn_append_kv_fp4",
-           lib().attn_append_kv_fp4(*head, *_fp4_scales(k_scale, v_scale, k_cache.shape,
-                                                       v_cache.shape), *tail, max_kv_len,
-                                    _stream_of(stream, device)))
+           lib().attn_append_kv_fp4(*head, *scales, *tail, max_kv_len, _stream_of(stream, device)))
     return q_out
 
 
@@ -948,6 +947,7 @@ def attn_evict_kv(k_cache: torch.Tensor, v_cache: Optional[torch.Tensor], weight
     lens, keeps = _int32(kv_len, batch, "kv_len"), _int32(keep, batch, "keep")
     if kept_len is None:
         kept_len = _empty((batch,), torch.int32, k_cache.device, stream)
+    kept = _int32(kept_len, batch, "kept_len")
     if indices is None:
         indices = _empty((batch, heads, max_keep), torch.int32, k_cache.device, stream)
     elif (indices.dtype != torch.int32 or indices.shape != (batch, heads, max_keep) or
@@ -957,8 +957,7 @@ def attn_evict_kv(k_cache: torch.Tensor, v_cache: Optional[torch.Tensor], weight
                                 page_table, out_page_table, kept_len, indices)
     _check("attn_evict_kv",
            lib().attn_evict_kv(kd, vd, wd, lens, keeps, batch, heads, dim, dim_v, max_kv_len,
-                               max_keep, first, recent, kod, vod, wod,
-                               _int32(kept_len, batch, "kept_len"), indices.data_ptr(),
+                               max_keep, first, recent, kod, vod, wod, kept, indices.data_ptr(),
                                _stream_of(stream, device)))
     return kept_len, indices
 
