@@ -634,7 +634,7 @@ int attn_decode_fp8(const void *q, const attn_kv_t *k, const attn_kv_t *v,
  * 64 bytes a token and head.  attn_kv_t then counts bytes: base 32-byte aligned,
  * strides multiples of 32.  The scales lie beside it, a 4-byte word for every token and
  * head, described by attn_kv_scale_t with block_tokens 1 (strides in words):
- *   keys    four e8m0 bytes (2^(byte - 127); 255: NaN; 0 counts as 0), one for every 32
+ *   keys    four e8m0 bytes (2^(byte - 127); 255: NaN), one for every 32
  *           channels;
  *   values  one fp32 number, finite and >= 0 (2^65 and more counts as NaN), for all
  *           128: it goes into the key's weight, of which there is one.
@@ -665,9 +665,11 @@ int attn_append_kv_fp4(const attn_head_rows_t *q, const attn_head_rows_t *k,
 /*
  * attn_decode_fp4 -- attn_decode over a cache held in 4 bits.
  *
- * Arguments, limits, workspace and the weights' rounding as for attn_decode_fp8, with k,
- * v, k_scale and v_scale as above.  A token whose key or value scale is NaN makes the out
- * of the rows that see it NaN (their lse is then undefined) and of no others.
+ * Arguments, limits and workspace as for attn_decode_fp8, with k, v, k_scale and v_scale
+ * as above.  A weight times its value scale's power of two errs by at most 2^-11 of itself,
+ * or by 2^-27 of the largest such product that the row's keys have with it, where that is
+ * more.  A token whose key or value scale is NaN makes the out of the rows that see it NaN
+ * (their lse is then undefined) and of no others.
  */
 int attn_decode_fp4_workspace(int num_sms, int batch, int num_q_heads, int group,
                               size_t *workspace_bytes);

@@ -377,10 +377,17 @@ __device__ __forceinline__ void half_terms(const float2 &a, const float2 &b, uin
     }
 }
 
-// The scale that e8m0 byte k of w stands for (2^-127 counts as 0; 255: NaN).
-__device__ __forceinline__ float e8m0(uint32_t w, int k) {
-    const uint32_t e = (w >> (8 * k)) & 0xffu;
-    return __uint_as_float(e == 0xffu ? 0x7fffffffu : e << 23);
+// The scales that the four e8m0 bytes of w stand for (255: NaN), by way of bf16.
+__device__ __forceinline__ void e8m0x4(uint32_t w, float (&f)[kKGroups]) {
+    uint32_t a, b;
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+        "cvt.rn.bf16x2.ue8m0x2 %0, l;\n\tcvt.rn.bf16x2.ue8m0x2 %1, h;\n\t}"
+        : "=r"(a), "=r"(b)
+        : "r"(w));
+    f[0] = __uint_as_float(a << 16);
+    f[1] = __uint_as_float(a & 0xffff0000u);
+    f[2] = __uint_as_float(b << 16);
+    f[3] = __uint_as_float(b & 0xffff0000u);
 }
 
 // Byte of element (row r, byte c) of an operand of 128-byte rows, 128-byte swizzle.
@@ -1001,7 +1008,8 @@ gqa_decode_codes_kernel(const __grid_constant__ Fp8DecodeParams p) {
                 float2 s[NCH][2];                                // score, then score - m
                 const uint32_t s_at = tmem + lane_base + sb * C::kSCols;
                 // (4 bits: the key's scales, a group of channels each)
-                const uint32_t exps = __float_as_uint(sc.x);
+                float by_group[kKGroups];
+                if constexpr (kFp4) e8m0x4(__float_as_uint(sc.x), by_group);
                 if constexpr (kFp4 && C::kTermCols) {
                     float raw[kKGroups][8];
                     tmem_ld_group_terms(s_at + 2 * col(0), raw);
@@ -1010,7 +1018,7 @@ gqa_decode_codes_kernel(const __grid_constant__ Fp8DecodeParams p) {
                     for (int c = 0; c < 2; ++c) s[0][c] = lo[c] = make_float2(0.f, 0.f);
 #pragma unroll
                     for (int kk = 0; kk < kKGroups; ++kk) {
-                        const float f4 = e8m0(exps, kk);
+                        const float f4 = by_group[kk];
                         const float2 f2 = make_float2(f4, f4);
 #pragma unroll
                         for (int c = 0; c < 2; ++c) {
@@ -1033,7 +1041,7 @@ gqa_decode_codes_kernel(const __grid_constant__ Fp8DecodeParams p) {
                             s[h][c] = make_float2(0.f, 0.f);
 #pragma unroll
                             for (int kk = 0; kk < kKGroups; ++kk) {
-                                const float f4 = e8m0(exps, kk);
+                                const float f4 = by_group[kk];
                                 s[h][c] = __ffma2_rn(
                                     make_float2(raw[h][kk][2 * c], raw[h][kk][2 * c + 1]),
                                     make_float2(f4, f4), s[h][c]);
