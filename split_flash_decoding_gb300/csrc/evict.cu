@@ -79,7 +79,7 @@ struct Shared {
     int warp_more[kWarps], warp_equal[kWarps];
     int counts[2];                   // this CTA's kept for sure, and equal to the threshold
     int merged[kPasses][kBins];      // first CTA of a cluster: the counts of all
-    int digit, rest, all;            // of a pass: the digit, what is wanted of its keys, how many it has
+    int digit, rest, all;            // of a pass: the digit, the keys wanted of it, all of its keys
 };
 
 // Sum over the warps before this one, of a value for each warp (in shared memory), by
@@ -186,7 +186,8 @@ evict_select_kernel(const __grid_constant__ EvictParams p, int held_keys) {
         for (int t = w0 + lane; t < w1; t += 32) keys[t - t0] = read_key(t);
     }
 
-    uint32_t least = 0, mask = choose ? 0u : ~0u;   // the smallest weight that stays, its known digits
+    // the smallest weight that stays, its known digits
+    uint32_t least = 0, mask = choose ? 0u : ~0u;
     int rest = wanted;                       // how many of those equal to it, as far as known
     if (choose) {
         for (int i = tid; i < kPasses * kBins; i += kThreads) (&sh.hist[0][0])[i] = 0;

@@ -1,8 +1,11 @@
-// gqa_decode_fp8.cu -- split-K decode attention over a cache held in 8 bits
-// (e4m3 codes, an fp32 scale per block of tokens and KV head), head_dim 128.
+// gqa_decode_codes.cuh -- split-K decode attention over a cache held in codes, head_dim 128:
+// 8 bits (e4m3, an fp32 scale per block of tokens and KV head) or 4 (e2m1; keys with a power of
+// two for every 32 channels, values with an fp32 scale a token).
 //
-//   s_j = scale q . (ks_j K8_j),  p_j = e^(s_j - m)
-//   out = sum_j p_j (vs_j V8_j) / (sum_j p_j + e^(sink - m))
+//   s_j = scale q . (ks_j K_j),  p_j = e^(s_j - m)
+//   out = sum_j p_j (vs_j V_j) / (sum_j p_j + e^(sink - m))
+//
+// First for 8 bits; what 4 bits change follows.
 //
 // The work list is the balanced split of fp8_items.cuh (the 128-key tiles of
 // the sequences dealt out in ranges of equal cost, KV heads side by side), with
@@ -41,7 +44,22 @@
 // than 4 columns), K producer and V producer (TMA), MMA issue, and one warp that
 // turns q into its terms and fetches the scales of each tile's keys (cp.async).
 //
-// What bounds it.  Up to 4 columns the stream of codes: 64 sequences of 32 + 8
+// 4 bits.  A copy unpacks 16 codes into the first 8 of 16 bytes, as the MMAs (e2m1 times e4m3
+// or e5m2) want them, so a tile is as large in shared memory and half as large in memory: its
+// softmax, not its stream, is what has to be quick.
+//   A key's scale differs between its four groups of channels, so each group's product goes to
+//     columns of its own and the thread that owns the key adds the four up.  With 16 columns
+//     the two terms of q are two MMAs into the same columns (q1 in e5m2, which holds q1 / 16).
+//   weights: f16, cut into four e5m2 terms of 3 of its 11 bits each (the upper byte of an f16
+//     number is an e5m2 number), so O's four terms simply add up: an error of at most 2^-11 of
+//     a weight or 2^-27 of the reference's.  (Fewer instructions than four e4m3 terms: with
+//     all lanes of the MMA warp walking, see there, 84.0 and 70.1 us for 64 sequences.)
+//   Up to 4 columns two groups of softmax warps take the tiles in turns, each with its own
+//     weights, reference and output, joined at an item's end: what one waits for (scores, the
+//     barrier, the last P.V) the other uses.  A warp for each contraction's MMAs (one for both
+//     held the scores of the next tile back: 72.5 and 62.0 us), and one producer for both.
+//
+// What bounds it, 8 bits.  Up to 4 columns the stream of codes: 64 sequences of 32 + 8
 // heads and 512 to 8192 keys (580 MB) take 98 us, 5.9 TB/s with everything,
 // about 7 while the stream runs.  The rest is 5 us until the first scores
 // (range, page table, first tile), the ends of the CTAs and the reduce.  With 16
@@ -49,9 +67,13 @@
 // rows of 4 heads: 89 us for 318 MB; 83 with three terms of the weights).  What runs
 // once an item (opening it, the first tile's maxima, the epilogue) runs from a cold
 // instruction cache, at 100 cycles and more per eight instructions: hence the rolled
-// loops and the care for code length there.  (Heads taken one after the other 114.9 us, P through a swizzled
-// K-major layout 201 instead of 158 us for the draft rows, one group of warps for
-// 16 columns 147 instead of 103, 3 V stages the same.)
+// loops and the care for code length there.  (Heads taken one after the other 114.9 us, P
+// through a swizzled K-major layout 201 instead of 158 us for the draft rows, one group of
+// warps for 16 columns 147 instead of 103, 3 V stages the same.)
+// 4 bits: the same 64 sequences (309 MB) take 58.9 us, 5.2 TB/s; 131072 keys of one sequence
+// (143 MB) 33.3 us, of which 5.5 are the reduce and about 6 the start; 1 to 4 draft rows 78 us,
+// the softmax's issue slots (half of all, the rest lost to waits between its steps and to
+// instructions that are not yet there).
 #pragma once
 
 #include <cuda_fp8.h>
@@ -119,7 +141,7 @@ struct Cfg {
     static __host__ __device__ constexpr int term0(int c) { return kTermCols ? 2 * c - (c & 3) : c; }
     static constexpr int kWarpK = 4 * kGroups, kWarpV = kWarpK + 1, kWarpMma = kWarpK + 2,
                          kWarpAux = kWarpK + 3;
-    static constexpr bool kTwoMmaWarps = kFp4;           // kWarpV's is the outputs' (kWarpK loads both)
+    static constexpr bool kTwoMmaWarps = kFp4;   // kWarpV's is the outputs' (kWarpK loads both)
     static constexpr int kThreads = 32 * (4 * kGroups + 4);
     // shared memory
     static constexpr int kring = 0;
@@ -129,7 +151,8 @@ struct Cfg {
     static constexpr int sc = p + kBufs * NP * 128;                  // [kScStages][128] {ks, vs}
     static constexpr int red = sc + kScStages * kBK * 8;             // float [4][16] tile max
     // (turns: of each group; the maxima have room for one row of 4 columns a group)
-    static constexpr int lred = red + 4 * 16 * 4;                    // float [2][kBufs][5][16] row sums, references
+    // float [2][kBufs][5][16]: row sums, references
+    static constexpr int lred = red + 4 * 16 * 4;
     static constexpr int qf = lred + 2 * kBufs * 5 * 16 * 4;         // float [kQBufs][16] 2^-a
     static constexpr int bars = qf + 2 * 16 * 4;
     static constexpr int tmem_slot = bars + kBarBytes;
@@ -618,7 +641,8 @@ __device__ __forceinline__ void produce_paced(const Fp8DecodeParams &p, const in
     open(v);
     unsigned long long since = 0;           // of the last step that found neither stage free
     while (k.more || v.more) {
-        const bool a = step(k, true, bar + kKFull, bar + kKEmpty, kStages, &p.k_map, smem + C::kring);
+        const bool a =
+            step(k, true, bar + kKFull, bar + kKEmpty, kStages, &p.k_map, smem + C::kring);
         const bool b = step(v, false, bar + kVFull, bar + kVEmpty, kVs, &p.v_map, smem + C::vring);
         if (a || b) {
             since = 0;
@@ -815,7 +839,8 @@ gqa_decode_codes_kernel(const __grid_constant__ Fp8DecodeParams p) {
     }
     // Rows of Q and P past the columns in use stay zero.
     if (warp >= 3)
-        for (int i = threadIdx.x - 96; i < (kQBufs * C::kQBytes + C::kBufs * C::NP * 128) / 16; i += C::kThreads - 96)
+        for (int i = threadIdx.x - 96; i < (kQBufs * C::kQBytes + C::kBufs * C::NP * 128) / 16;
+             i += C::kThreads - 96)
             reinterpret_cast<uint4 *>(smem + C::q)[i] = make_uint4(0u, 0u, 0u, 0u);
     tc::fence_async_smem();
     tc::fence_before_sync();
