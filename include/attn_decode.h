@@ -698,7 +698,7 @@ int attn_decode_fp4(const void *q, const attn_kv_t *k, const attn_kv_t *v,
  *   head_dim   64 or 128.  batch <= 2048.
  *   max_q_len  host upper bound of the rows of any sequence: it picks the kernel,
  *              more rows are taken as well.
- *   decay      factor of the weights from before.
+ *   decay      factor of the weights from before (0: they are not read).
  *   weights    read and written: for t < kv_len[b], with n the rows of sequence b,
  *     w_t = [t < kv_len[b] - n] decay w_t
  *           + sum over the rows that see t and the heads of the group of

@@ -872,8 +872,9 @@ def attn_key_weights(q: torch.Tensor, k_cache: torch.Tensor, lse: torch.Tensor,
 
     q bf16 [rows, num_q_heads, 64 or 128] and lse fp32 [rows, num_q_heads] of an
     attn_decode call (return_lse), the other arguments as there; weights fp32
-    [pages, page_size, num_kv_heads], any strides, read (times decay) and written, but
-    for a sequence's last tokens, one for each of its rows: theirs are written only.
+    [pages, page_size, num_kv_heads], any strides, read (times decay, unless that is 0) and
+    written, but for a sequence's last tokens, one for each of its rows: theirs are written
+    only.
     max_q_len picks the kernel; by default, with q_row_offsets, it is all rows.  Returns
     weights."""
     rows, hq, d = q.shape

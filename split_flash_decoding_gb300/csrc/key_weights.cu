@@ -486,7 +486,7 @@ key_weights_kernel(const __grid_constant__ WeightsParams p) {
             }
             const bool together = C::kHeads == 4 && it.heads == 4 && p.w.head == 1 &&
                                   (reinterpret_cast<uintptr_t>(where) & 15) == 0;
-            if (where && key < it.L - it.n) {
+            if (where && key < it.L - it.n && p.decay != 0.f) {
                 if (together) {
                     const float4 v = *reinterpret_cast<const float4 *>(where);
                     old[0] = v.x;

@@ -225,6 +225,19 @@ def test_any_bound_of_the_rows(attn, max_q_len):
     Case([300, 40], [70, 3], seed=9).check(attn, max_q_len=max_q_len)
 
 
+@pytest.mark.parametrize("q_lens", [None, [3, 40, 1]])
+@pytest.mark.parametrize("hq,hkv", [(8, 2), (16, 4)])
+def test_decay_of_zero_reads_no_weights(attn, q_lens, hq, hkv):
+    """As over memory that nothing was written to."""
+    c = Case([300, 64, 129], q_lens, hq=hq, hkv=hkv, decay=0.0, seed=6)
+    zeros = torch.where(c.owned[..., None], torch.zeros_like(c.w), c.w)
+    w = c.to_gpu(torch.where(c.owned[..., None], torch.full_like(c.w, math.nan), c.w))
+    pos, args = c.args()
+    attn.attn_key_weights(*pos, w, **args)
+    c.w = zeros
+    c.compare(w, "decay 0")
+
+
 def test_rows_of_no_sequence_are_not_read(attn):
     c = Case([300, 40], [30, 3], seed=9)
     c.q = torch.cat([c.q, torch.full((5, *c.q.shape[1:]), float("nan"), dtype=torch.bfloat16)])
