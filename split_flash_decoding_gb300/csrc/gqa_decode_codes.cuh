@@ -64,7 +64,7 @@
 // about 7 while the stream runs.  The rest is 5 us until the first scores
 // (range, page table, first tile), the ends of the CTAs and the reduce.  With 16
 // columns the softmax of a tile takes longer than its bytes (1 to 4 draft
-// rows of 4 heads: 89 us for 318 MB; 83 with three terms of the weights).  What runs
+// rows of 4 heads: 82 us for 318 MB).  What runs
 // once an item (opening it, the first tile's maxima, the epilogue) runs from a cold
 // instruction cache, at 100 cycles and more per eight instructions: hence the rolled
 // loops and the care for code length there.  (Heads taken one after the other 114.9 us, P
