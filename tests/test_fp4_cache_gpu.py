@@ -614,6 +614,28 @@ def test_offsets_beyond_32_bits(attn):
     c.compare(out, lse)
 
 
+def test_append_beyond_32_bits(attn):
+    """A prompt into pages past 4 GB of codes: what it leaves near the base."""
+    pages = (1 << 20) + 8
+    if torch.cuda.mem_get_info()[0] < 24 << 30:
+        pytest.skip("not enough memory")
+
+    def caches(n):
+        k, v = (torch.zeros((n, 64, 1, 64), dtype=torch.uint8, device=DEV) for _ in range(2))
+        ks = torch.zeros((n, 64, 1, 4), dtype=torch.uint8, device=DEV).view(torch.float8_e8m0fnu)
+        return k, v, ks, torch.zeros((n, 64, 1), device=DEV)
+
+    x = torch.randn(300, 2, 128, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).to(DEV)
+    table = i32([[3, 0, 7, 2, 5]])
+    near, far = caches(8), caches(pages)
+    for cache, at in ((near, 0), (far, pages - 8)):
+        attn.attn_append_kv_fp4(x[:, :1], x[:, 1:], *cache, i32([300]), max_kv_len=320,
+                                page_table=table + at, q_row_offsets=i32([0, 300]))
+    for a, b in zip(near, far):
+        a, b = (t.view(torch.uint8) for t in (a, b))
+        assert torch.equal(a, b[pages - 8:]) and bool(a.any()) and not bool(b[:8].any())
+
+
 # ---- together ---------------------------------------------------------------------------
 
 @pytest.mark.parametrize("q_lens", [None, [3, 1, 2]])

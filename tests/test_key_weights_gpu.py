@@ -289,6 +289,23 @@ def test_many_sequences(attn):
     Case(lens, [min(x, 30) for x in lens], hq=2, hkv=1, page=16, seed=2).check(attn)
 
 
+@pytest.mark.parametrize("q_lens", [None, [40]])
+def test_offsets_beyond_32_bits(attn, q_lens):
+    """Pages past 4 GB of keys, and weights past 4 GB of their base."""
+    if torch.cuda.mem_get_info()[0] < 32 << 30:
+        pytest.skip("not enough memory")
+    c = Case([300], q_lens, hq=4, hkv=1, dim=64, seed=5)
+    pages = (1 << 20) + 8
+    k = torch.empty((pages, 64, 1, 64), dtype=torch.bfloat16, device=DEV)        # 8 GB
+    w = torch.empty((pages, 64, 1, 16), device=DEV)[..., 3]                      # of 4 GB
+    far = pages - c.pages
+    k[far:], w[far:] = c.k.to(DEV), c.w.to(DEV)
+    (q, _, lse, lens), args = c.args()
+    args["page_table"] = args["page_table"] + far
+    attn.attn_key_weights(q, k, lse, lens, w, **args)
+    c.compare(w[far:], "far pages")
+
+
 def test_captured_and_replayed_with_other_lengths(attn):
     for q_lens in (None, [60, 8, 40]):
         big = Case([500, 300, 260], q_lens, seed=12)
