@@ -431,6 +431,11 @@ static int decode_codes(bool fp4, const void *q, const attn_kv_t *k, const attn_
     p.vs_head = v_scale->head_stride;
     p.block_shift = 0;
     while ((1 << p.block_shift) < k_scale->block_tokens) ++p.block_shift;
+    const auto in_runs = [&](const attn_kv_scale_t *x) {
+        return x->block_stride == 1 && aligned(x->base, 16) && x->page_stride % 4 == 0 &&
+               (hkv == 1 || x->head_stride % 4 == 0);
+    };
+    p.scale_runs = in_runs(k_scale) && in_runs(v_scale);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     st = map_cuda(fp4 ? launch_gqa_decode_fp4(p, ctas, s) : launch_gqa_decode_fp8(p, ctas, s));
     if (st || !cut) return st;

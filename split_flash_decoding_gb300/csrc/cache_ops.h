@@ -78,6 +78,7 @@ struct Fp8DecodeParams {
     const float *k_scale, *v_scale;
     long long ks_page, ks_block, ks_head, vs_page, vs_block, vs_head;
     int block_shift;              // log2(tokens per scale)
+    int scale_runs;               // 4 bits: four tokens' scales are 16 bytes, on such a boundary
 };
 
 cudaError_t launch_head_rows(const RowsParams &p, cudaStream_t stream);

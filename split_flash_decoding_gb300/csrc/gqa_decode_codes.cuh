@@ -70,8 +70,8 @@
 // loops and the care for code length there.  (Heads taken one after the other 114.9 us, P
 // through a swizzled K-major layout 201 instead of 158 us for the draft rows, one group of
 // warps for 16 columns 147 instead of 103, 3 V stages the same.)
-// 4 bits: the same 64 sequences (309 MB) take 58.9 us, 5.2 TB/s; 131072 keys of one sequence
-// (143 MB) 33.3 us, of which 5.5 are the reduce and about 6 the start; 1 to 4 draft rows 78 us,
+// 4 bits: the same 64 sequences (309 MB) take 57.2 us, 5.4 TB/s; 131072 keys of one sequence
+// (143 MB) 33.0 us, of which 5.5 are the reduce and about 6 the start; 1 to 4 draft rows 74 us,
 // the softmax's issue slots (half of all, the rest lost to waits between its steps and to
 // instructions that are not yet there).
 #pragma once
@@ -148,7 +148,7 @@ struct Cfg {
     static constexpr int vring = kring + kStages * kTileBytes;
     static constexpr int q = vring + kVs * kTileBytes;          // [kQBufs][terms, rows][128 B]
     static constexpr int p = q + kQBufs * kQBytes;                   // [chunks][128 keys][16 B]
-    static constexpr int sc = p + kBufs * NP * 128;                  // [kScStages][128] {ks, vs}
+    static constexpr int sc = p + kBufs * NP * 128;                  // [kScStages]: 128 {ks, vs}; 4 bits: ks, vs
     static constexpr int red = sc + kScStages * kBK * 8;             // float [4][16] tile max
     // (turns: of each group; the maxima have room for one row of 4 columns a group)
     // float [2][kBufs][5][16]: row sums, references
@@ -766,7 +766,11 @@ __device__ __forceinline__ void feed(const Fp8DecodeParams &p, const int2 *cum, 
         if (lane == 0) mbar_arrive(&bar[kQFull + qb]);
 
         // One box per lane and refill, as in the producers; the 32 keys of a step
-        // lie in one box or in whole boxes, within one refill.
+        // lie in one box or in whole boxes, within one refill.  (4 bits: a tile takes half as
+        // long, so the words of four keys side by side go in one copy, and those of a page of
+        // 128 and more from one address: a warp has an instruction in ten cycles here, and a
+        // copy a key took 1100 to 1600 of a tile's 1900 to 4400.  64 sequences 58.9 us and
+        // 57.2 so; draft rows, heads of a token side by side, 78.1 and 73.8.)
         const float *ksp = p.k_scale + it.kvh * p.ks_head;
         const float *vsp = p.v_scale + it.kvh * p.vs_head;
         int cached = -1, my_page = -1, my_slot = 0;
@@ -778,6 +782,58 @@ __device__ __forceinline__ void feed(const Fp8DecodeParams &p, const int2 *cum, 
                 ok = mbar_wait(&bar[kScEmpty + s], ((gg / kScStages) - 1) & 1, p.err);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
+            if constexpr (kFp4) {                                // keys' words, then values'
+                float *dst = reinterpret_cast<float *>(smem + C::sc) + s * 2 * kBK;
+                // A tile's boxes lie within one refill, four keys side by side in one box.
+                const int box0 = t << nb_shift;
+                if ((box0 >> 5) != cached) {
+                    cached = box0 >> 5;
+                    lookup_boxes(p, it, cached, lane, false, my_page, my_slot);
+                }
+                if (p.scale_runs) {
+                    const int k = 4 * lane, box = box0 + (k >> box_shift);
+                    const int page = __shfl_sync(0xffffffffu, my_page, box);
+                    const int slot =
+                        __shfl_sync(0xffffffffu, my_slot, box) + (k & (p.box_rows - 1));
+                    const float *ks = ksp + page * p.ks_page + slot;
+                    const float *vs = vsp + page * p.vs_page + slot;
+                    if (page >= 0 && k < left && slot + 4 <= p.page_size) {
+                        cp_async_16(dst + k, ks);
+                        cp_async_16(dst + kBK + k, vs);
+                    } else if (page >= 0) {                      // (a cache's end)
+                        for (int i = 0; i < 4 && k + i < left && slot + i < p.page_size; ++i) {
+                            cp_async_4(dst + k + i, ks + i);
+                            cp_async_4(dst + kBK + k + i, vs + i);
+                        }
+                    }
+                } else if (box_shift == 7) {
+                    const int page = __shfl_sync(0xffffffffu, my_page, box0);
+                    const int slot = __shfl_sync(0xffffffffu, my_slot, box0) + lane;
+                    const int live = page < 0 ? 0 : min(left, p.page_size - (slot - lane));
+                    const float *ks = ksp + page * p.ks_page + slot * p.ks_block;
+                    const float *vs = vsp + page * p.vs_page + slot * p.vs_block;
+#pragma unroll
+                    for (int u = 0; u < kBK / 32; ++u)
+                        if (lane + 32 * u < live) {
+                            cp_async_4(dst + lane + 32 * u, ks + 32 * u * p.ks_block);
+                            cp_async_4(dst + kBK + lane + 32 * u, vs + 32 * u * p.vs_block);
+                        }
+                } else {
+#pragma unroll
+                    for (int u = 0; u < kBK / 32; ++u) {
+                        const int k = 32 * u + lane, box = box0 + (k >> box_shift);
+                        const int page = __shfl_sync(0xffffffffu, my_page, box);
+                        const int slot =
+                            __shfl_sync(0xffffffffu, my_slot, box) + (k & (p.box_rows - 1));
+                        if (page >= 0 && k < left) {
+                            cp_async_4(dst + k, ksp + page * p.ks_page + slot * p.ks_block);
+                            cp_async_4(dst + kBK + k, vsp + page * p.vs_page + slot * p.vs_block);
+                        }
+                    }
+                }
+                cp_async_arrive(&bar[kScFull + s]);
+                continue;
+            }
             float2 *dst = reinterpret_cast<float2 *>(smem + C::sc) + s * kBK + lane;
 #pragma unroll
             for (int u = 0; u < kBK / 32; ++u) {
@@ -1027,7 +1083,13 @@ gqa_decode_codes_kernel(const __grid_constant__ Fp8DecodeParams p) {
                 const bool sc_in = mbar_try_wait(&bar[kScFull + ss], sph);
                 const bool s_in = mbar_try_wait(&bar[kSFull + sb], (gg >> 1) & 1);
                 if (!sc_in) ok = ok && mbar_wait(&bar[kScFull + ss], sph, p.err);
-                float2 sc = reinterpret_cast<const float2 *>(smem + C::sc)[ss * kBK + k];
+                float2 sc;
+                if constexpr (kFp4) {
+                    const float *at = reinterpret_cast<const float *>(smem + C::sc) + ss * 2 * kBK;
+                    sc = make_float2(at[k], at[kBK + k]);
+                } else {
+                    sc = reinterpret_cast<const float2 *>(smem + C::sc)[ss * kBK + k];
+                }
                 if (!s_in) ok = ok && mbar_wait(&bar[kSFull + sb], (gg >> 1) & 1, p.err);
                 tc::fence_after_sync();
                 float2 s[NCH][2];                                // score, then score - m

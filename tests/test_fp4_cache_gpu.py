@@ -636,6 +636,25 @@ def test_append_beyond_32_bits(attn):
         assert torch.equal(a, b[pages - 8:]) and bool(a.any()) and not bool(b[:8].any())
 
 
+@pytest.mark.parametrize("capacity,padded", [(703, 704), (702, 702), (701, 703)])
+@pytest.mark.parametrize("hkv", [1, 2])
+def test_scales_on_any_boundary(attn, capacity, padded, hkv):
+    """Contiguous caches whose scales end inside four tokens, begin on 16 bytes or do not."""
+    c = Case([capacity, 650], hq=4 * hkv, hkv=hkv, contiguous=True, head_major=True, seed=capacity)
+    assert c.cache.k.shape[1] == capacity
+    k, v, ks, vs = c.cache.gpu()
+    wide = [torch.zeros(2, hkv, padded, 4, dtype=torch.uint8, device=DEV),
+            torch.full((2, hkv, padded), math.nan, device=DEV)]
+    wide[0].fill_(255)
+    e, s = wide[0][:, :, :capacity].transpose(1, 2), wide[1][:, :, :capacity].transpose(1, 2)
+    e.copy_(ks.view(torch.uint8))
+    s.copy_(vs)
+    e = wide[0].view(torch.float8_e8m0fnu)[:, :, :capacity].transpose(1, 2)
+    out, lse = attn.attn_decode_fp4(c.q.to(DEV), k, v, e, s, i32(c.lens), group=4, scale=c.scale,
+                                    max_kv_len=capacity)
+    c.compare(out, lse)
+
+
 # ---- together ---------------------------------------------------------------------------
 
 @pytest.mark.parametrize("q_lens", [None, [3, 1, 2]])
