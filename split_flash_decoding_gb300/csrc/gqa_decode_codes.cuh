@@ -92,7 +92,7 @@ constexpr int kStages = 3;                   // K tiles in flight
 // V tiles in flight (kVs): as many as leave two CTAs room (8 bits: three measured the same).
 // 4 bits, 4 columns: three, and two where the table of that many sequences takes the third's
 // room (512 sequences of 512 to 1024 keys: 135 us, 168 with three and one CTA an SM; 1024 of 64
-// keys 97 and 183).
+// keys 97 and 183; 120 and 87 since).
 __host__ __device__ constexpr int v_stages(bool fp4, int nc) { return fp4 && nc == 4 ? 3 : 2; }
 constexpr size_t kCtaSmem = 113 * 1024;      // a CTA of two on an SM
 constexpr int kTileBytes = kBK * kD;         // 16 KB (4 bits: 16 codes in the first 8 of 16 bytes)
@@ -510,68 +510,6 @@ __device__ __forceinline__ void produce(const Fp8DecodeParams &p, const int2 *cu
             mbar_wait(&full[i % kN], (i / kN) & 1, p.err);
 }
 
-// Producer of the 4-bit kernel's variants of more columns: the boxes of both operands of each
-// tile, a box a lane, one operand after the other.  There the softmax is what the stages wait
-// for, and a warp that asks for both without a pause takes its issue slots (1 to 4 draft rows
-// 79.7 us against 83.6).
-template <int NC, int kVs>
-__device__ __forceinline__ void produce_both(const Fp8DecodeParams &p, const int2 *cum,
-                                             const Fp8Range &w, uint8_t *smem, uint64_t *bar,
-                                             int lane) {
-    using C = Cfg<NC, true, kVs>;
-    const int box_rows = p.box_rows;        // 128, 64, 32, 16 or 8
-    const int box_shift = 31 - __clz(box_rows);
-    const int nb = kBK >> box_shift;        // row boxes per tile
-    const uint32_t box_bytes = uint32_t(box_rows) * 64u;        // in memory: what a copy counts
-    int g = 0;
-    bool ok = true;
-    for (int j = 0, items = w.count(); j < items && ok; ++j) {
-        const Fp8Item it = fp8_item(p, cum, w, j);
-        if (it.ntiles == 0) continue;
-        int cached = -1, page = -1, slot = 0;
-        for (int t = 0; t < it.ntiles; ++t, ++g) {
-            const int key0 = it.start + t * kBK;
-            const int live = min(nb, (it.L - key0 + box_rows - 1) >> box_shift);
-            const int box0 = t * nb;                             // box index in the item
-            if ((box0 >> 5) != cached) {
-                cached = box0 >> 5;
-                lookup_boxes(p, it, cached, lane, true, page, slot);
-            }
-            const int r = lane - (box0 & 31);
-            const auto issue = [&](uint64_t *full, uint64_t *empty, int n, const CUtensorMap *map,
-                                   uint8_t *ring) {
-                const int s = g % n;
-                if (lane == 0) {
-                    if (g >= n) ok = mbar_wait(&empty[s], ((g / n) - 1) & 1, p.err);
-                    if (ok) mbar_arrive_expect_tx(&full[s], uint32_t(live) * box_bytes);
-                }
-                ok = __shfl_sync(0xffffffffu, ok, 0);
-                if (!ok || r < 0 || r >= live) return;
-                if (page < 0)
-                    mbar_complete_tx(&full[s], box_bytes);       // skipped bad page
-                else
-                    tma_load_4d(ring + s * kTileBytes + r * box_rows * 128, map, &full[s], 0, slot,
-                                it.kvh, page);
-            };
-            issue(bar + kKFull, bar + kKEmpty, kStages, &p.k_map, smem + C::kring);
-            if (!ok) break;
-            __syncwarp();
-            issue(bar + kVFull, bar + kVEmpty, kVs, &p.v_map, smem + C::vring);
-            if (!ok) break;
-            __syncwarp();
-        }
-    }
-    // Every copy this warp issued must land before the CTA may leave (after a wait that gave
-    // up, tile g's keys may have been sent for as well).
-    if (lane == 0) {
-        const int k_end = ok ? g : g + 1;
-        for (int i = max(0, k_end - kStages); i < k_end; ++i)
-            mbar_wait(&bar[kKFull + i % kStages], (i / kStages) & 1, p.err);
-        for (int i = max(0, g - kVs); i < g; ++i)
-            mbar_wait(&bar[kVFull + i % kVs], (i / kVs) & 1, p.err);
-    }
-}
-
 // Where one operand's producer is in the walk of a CTA's tiles.
 struct Walk {
     Fp8Item it;
@@ -580,12 +518,12 @@ struct Walk {
     bool more;
 };
 
-// Producer of the 4-bit kernel where the groups of softmax warps take turns: keys and values go
-// at their own pace.  (A value stage is free a softmax later than its tile's key stage, and keys
-// that waited for it came too late: 64 sequences 62.0 us in step and 60.2 so, 131072 keys 35.9
-// and 33.5.)
+// Producer of the 4-bit kernel: the boxes of both operands, a box a lane.  Keys and values go
+// at their own pace: a value stage is free a softmax later than its tile's key stage, and keys
+// that waited for it came too late (64 sequences 62.0 us in step and 60.2 so, 131072 keys 35.9
+// and 33.5; keys sent a tile ahead of the values, each wait blocking, 1.5 more than so).
 template <int NC, int kVs>
-__device__ __forceinline__ void produce_paced(const Fp8DecodeParams &p, const int2 *cum,
+__device__ __forceinline__ void produce_both(const Fp8DecodeParams &p, const int2 *cum,
                                              const Fp8Range &w, uint8_t *smem, uint64_t *bar,
                                              int lane) {
     using C = Cfg<NC, true, kVs>;
@@ -908,10 +846,7 @@ gqa_decode_codes_kernel(const __grid_constant__ Fp8DecodeParams p) {
 
     if (warp == C::kWarpK) {
         if constexpr (kFp4) {
-            if constexpr (C::kTurns)
-                produce_paced<NC, kVs>(p, cum, walk, smem, bar, lane);
-            else
-                produce_both<NC, kVs>(p, cum, walk, smem, bar, lane);
+            produce_both<NC, kVs>(p, cum, walk, smem, bar, lane);
         } else {
             produce<true, NC, kVs>(p, cum, walk, smem, bar, lane);
         }
