@@ -71,7 +71,7 @@
 // through a swizzled K-major layout 201 instead of 158 us for the draft rows, one group of
 // warps for 16 columns 147 instead of 103, 3 V stages the same.)
 // 4 bits: the same 64 sequences (309 MB) take 57.2 us, 5.4 TB/s; 131072 keys of one sequence
-// (143 MB) 33.0 us, of which 5.5 are the reduce and about 6 the start; 1 to 4 draft rows 74 us,
+// (143 MB) 33.0 us, of which 5.5 are the reduce and about 6 the start; 1 to 4 draft rows 71 us,
 // the softmax's issue slots (half of all, the rest lost to waits between its steps and to
 // instructions that are not yet there).
 #pragma once
@@ -452,6 +452,15 @@ __device__ __forceinline__ void lookup_boxes(const Fp8DecodeParams &p, const Fp8
     slot = tk & (p.page_size - 1);
 }
 
+// The CTA holding the unit's first tile publishes where its pieces are.  (4 bits: from the
+// producer warp, as the softmax warps' time between items counts: draft rows 73.7 us and 71.4.)
+__device__ __forceinline__ void publish(const Fp8DecodeParams &p, const int2 *cum,
+                                        const Fp8Range &w, const Fp8Item &it) {
+    if (it.first && p.unit_slots)
+        p.unit_slots[it.b * (p.num_q_heads / p.group) + it.kvh] =
+            make_int2(it.slot, it.direct ? 1 : fp8_pieces(p, cum, w, it));
+}
+
 // K or V producer: walks this CTA's items and tiles and lets lane 0 issue the
 // boxes of each tile into the ring.
 template <bool kIsK, int NC, int kVs>
@@ -532,6 +541,7 @@ __device__ __forceinline__ void produce_both(const Fp8DecodeParams &p, const int
     const int nb = kBK >> box_shift;        // row boxes per tile
     const uint32_t box_bytes = uint32_t(box_rows) * 64u;        // in memory: what a copy counts
     const int items = w.count();
+    Walk k, v;
     const auto open = [&](Walk &x) {        // the next item with tiles
         x.more = false;
         x.t = 0;
@@ -539,6 +549,7 @@ __device__ __forceinline__ void produce_both(const Fp8DecodeParams &p, const int
         while (!x.more && ++x.j < items) {
             x.it = fp8_item(p, cum, w, x.j);
             x.more = x.it.ntiles > 0;
+            if (&x == &k && lane == 0 && !x.more) publish(p, cum, w, x.it);   // (else: step)
         }
     };
     // Sends for the walk's tile, if its stage is free; n stages.
@@ -568,11 +579,11 @@ __device__ __forceinline__ void produce_both(const Fp8DecodeParams &p, const int
                             x.it.kvh, x.page);
         }
         __syncwarp();
+        if (is_k && x.t == 0 && lane == 0) publish(p, cum, w, x.it);
         ++x.g;
         if (++x.t == x.it.ntiles) open(x);
         return true;
     };
-    Walk k, v;
     k.j = v.j = -1;
     k.g = v.g = 0;
     open(k);
@@ -592,6 +603,11 @@ __device__ __forceinline__ void produce_both(const Fp8DecodeParams &p, const int
             if (lane == 0) atomicOr(p.err, kErrWaitTimeout);
             break;
         }
+    }
+    // (after a wait that gave up: the merge reads what every unit publishes)
+    if (lane == 0) {
+        if (k.more && k.t == 0) publish(p, cum, w, k.it);
+        for (int j = k.j + 1; j < items; ++j) publish(p, cum, w, fp8_item(p, cum, w, j));
     }
     // Every copy this warp issued must land before the CTA may leave.
     if (lane == 0) {
@@ -1382,10 +1398,7 @@ gqa_decode_codes_kernel(const __grid_constant__ Fp8DecodeParams p) {
             }
             tc::fence_before_sync();
             if (C::kTurns) named_sync(3, 256);   // both groups have read both outputs
-            // The CTA holding the unit's first tile publishes where its pieces are.
-            if (it.first && threadIdx.x == 0 && p.unit_slots)
-                p.unit_slots[it.b * (p.num_q_heads / G) + it.kvh] =
-                    make_int2(it.slot, fp8_pieces(p, cum, walk, it));
+            if (!kFp4 && threadIdx.x == 0) publish(p, cum, walk, it);   // (4 bits: its producer)
             g += it.ntiles;
         }
         pdl_launch_dependents();
