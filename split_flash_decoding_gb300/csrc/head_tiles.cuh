@@ -115,12 +115,18 @@ __device__ __forceinline__ void add_squares(const float2 (&y)[4], float2 &sum) {
     for (int c = 0; c < 4; ++c) sum = __ffma2_rn(y[c], y[c], sum);
 }
 
-// y *= f * weights (1 without weights)
+// y *= f * weights (1 without weights).  kStepwise, here and below: each operation rounded by
+// itself, as in the formula written out in fp32.  4 bits: a code is one of few, and a rounding
+// that differs may make it the next one (of 25 million codes of normed and rotated keys, 3.8
+// differed from those of the formula written out, and 1.9 do so).
+template <bool kStepwise = false>
 __device__ __forceinline__ void scale8(float2 (&y)[4], const uint4 &w, float f) {
     float2 g[4];
     unpack8(w, g);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) y[c] = __fmul2_rn(y[c], __fmul2_rn(g[c], make_float2(f, f)));
+    for (int c = 0; c < 4; ++c)
+        y[c] = kStepwise ? __fmul2_rn(__fmul2_rn(y[c], make_float2(f, f)), g[c])
+                         : __fmul2_rn(y[c], __fmul2_rn(g[c], make_float2(f, f)));
 }
 
 // Exponent of the scale of a block whose largest finite value is amax: the least e
@@ -217,10 +223,23 @@ __device__ __forceinline__ float largest_finite(const float2 (&ya)[4], const flo
 
 // Turn entry k of a lane's two vectors (turn_b: the second is rotated as well; in
 // the half layout always).
-template <bool kInter>
+template <bool kInter, bool kStepwise = false>
 __device__ __forceinline__ void rotate_pairs(float2 &ya, float2 &yb, const float4 &v, bool turn_b) {
     const float2 y = ya, z = yb;
-    if (kInter) {
+    if (kInter && kStepwise) {
+        ya = make_float2(__fsub_rn(__fmul_rn(y.x, v.x), __fmul_rn(y.y, v.y)),
+                         __fadd_rn(__fmul_rn(y.y, v.x), __fmul_rn(y.x, v.y)));
+        if (turn_b)
+            yb = make_float2(__fsub_rn(__fmul_rn(z.x, v.z), __fmul_rn(z.y, v.w)),
+                             __fadd_rn(__fmul_rn(z.y, v.z), __fmul_rn(z.x, v.w)));
+    } else if (kStepwise) {
+        const float2 c = make_float2(v.x, v.z), n = make_float2(v.y, v.w);
+        const float2 yc = __fmul2_rn(y, c), zn = __fmul2_rn(z, n), zc = __fmul2_rn(z, c),
+                     yn = __fmul2_rn(y, n);
+        // (not __fadd2_rn: that is joined with the products)
+        ya = make_float2(__fsub_rn(yc.x, zn.x), __fsub_rn(yc.y, zn.y));
+        yb = make_float2(__fadd_rn(zc.x, yn.x), __fadd_rn(zc.y, yn.y));
+    } else if (kInter) {
         ya = make_float2(fmaf(y.x, v.x, -y.y * v.y), fmaf(y.y, v.x, y.x * v.y));
         if (turn_b) yb = make_float2(fmaf(z.x, v.z, -z.y * v.w), fmaf(z.y, v.z, z.x * v.w));
     } else {
@@ -718,14 +737,14 @@ head_tiles_kernel(const __grid_constant__ RowsParams p, const __grid_constant__ 
 #pragma unroll
             for (int o = 1; o < L; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
             const float inv = rsqrtf(fmaf(sum, it.mean, it.eps));
-            if (it.flags & Item::kNormA) scale8(ya, it.ga, inv);
-            if (it.flags & Item::kNormB) scale8(yb, it.gb, inv);
+            if (it.flags & Item::kNormA) scale8<kKind == kFp4>(ya, it.ga, inv);
+            if (it.flags & Item::kNormB) scale8<kKind == kFp4>(yb, it.gb, inv);
         }
         if (it.flags & Item::kTurnA) {
             const float4 *t = angles + it.row * 4 * L + i0;
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-                rotate_pairs<kInter>(ya[k], yb[k], t[k * L], it.flags & Item::kTurnB);
+                rotate_pairs<kInter, kKind == kFp4>(ya[k], yb[k], t[k * L], it.flags & Item::kTurnB);
         }
         if (kKind == kFp4 && it.kind != 0) {
             store_fp4(p, at, it.kind, it.head, it.to_cache ? nullptr : it.dst, it.ca, it.cb,
