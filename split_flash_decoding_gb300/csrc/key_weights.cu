@@ -19,7 +19,7 @@
 //   the stream of keys.  Two CTAs per SM walk the units of all sequences, a unit being a
 //   tile of up to four KV heads, an item each: a thread then has its key's weights of four
 //   heads, neighbours in memory, and reads and writes them at once (a head at a time, four
-//   bytes of every 32 were 15 of 125 us).
+//   bytes of every 32 were 15 of 125 us).  64 sequences of 512 to 8192 keys 95 to 98 us, 6.2 TB/s.
 //   More (prompts): KT = 2, steps of 256 columns (MMAs of 128 columns wait for shared
 //   memory: 128 bytes a cycle for A and B).  Both key tiles stay in shared memory while
 //   column tiles pass; the score tiles of the two alternate in the two halves of tensor
