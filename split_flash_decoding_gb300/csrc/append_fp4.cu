@@ -3,10 +3,11 @@
 //
 // Every token's codes depend on that token alone, so this is the bf16 append with
 // another end: the tile kernel (head_tiles.cuh) takes the rows, and the lanes of a head
-// join their largest values before they store.  Prompts are bound by issue slots (72% in use:
-// conversions, scales and rotation of vectors that are there already; 24,768 rows of 32 + 8 heads,
-// keys normed, 121 us, 5.2 TB/s), 64 rows by latency (3.8 us).  Rotations whose pairs do not fall on whole
-// 16-byte vectors have the kernel here, one warp a row and head.
+// join their largest values before they store.  Prompts are bound by issue slots (72% in
+// use: conversions, scales and rotation of vectors that are there already; 24,768 rows of
+// 32 + 8 heads, keys normed, 121 us, 5.2 TB/s), 64 rows by latency (3.8 us).  Rotations
+// whose pairs do not fall on whole 16-byte vectors have the kernel here, one warp a row and
+// head.
 #include "head_tiles.cuh"
 
 namespace attn {

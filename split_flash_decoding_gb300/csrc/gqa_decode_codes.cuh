@@ -287,21 +287,7 @@ __device__ __forceinline__ void tmem_ld_group_terms(uint32_t t, float (&v)[kKGro
         : "r"(t), "r"(t + 16), "r"(t + 32), "r"(t + 48)
         : "memory");
 }
-// Four columns of each of the four groups' blocks, one chunk or two, one wait for all.
-__device__ __forceinline__ void tmem_ld_groups(uint32_t t0, uint32_t, float (&v)[1][kKGroups][4]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%16];\n\t"
-        "tcgen05.ld.sync.aligned.32x32b.x4.b32 {%4, %5, %6, %7}, [%17];\n\t"
-        "tcgen05.ld.sync.aligned.32x32b.x4.b32 {%8, %9, %10, %11}, [%18];\n\t"
-        "tcgen05.ld.sync.aligned.32x32b.x4.b32 {%12, %13, %14, %15}, [%19];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=&f"(v[0][0][0]), "=&f"(v[0][0][1]), "=&f"(v[0][0][2]), "=&f"(v[0][0][3]),
-          "=&f"(v[0][1][0]), "=&f"(v[0][1][1]), "=&f"(v[0][1][2]), "=&f"(v[0][1][3]),
-          "=&f"(v[0][2][0]), "=&f"(v[0][2][1]), "=&f"(v[0][2][2]), "=&f"(v[0][2][3]),
-          "=&f"(v[0][3][0]), "=&f"(v[0][3][1]), "=&f"(v[0][3][2]), "=&f"(v[0][3][3])
-        : "r"(t0), "r"(t0 + 16), "r"(t0 + 32), "r"(t0 + 48)
-        : "memory");
-}
+// Four columns of each of the four groups' blocks, of two chunks, one wait for all.
 __device__ __forceinline__ void tmem_ld_groups(uint32_t t0, uint32_t t1,
                                                float (&v)[2][kKGroups][4]) {
     asm volatile(
