@@ -354,7 +354,11 @@ evict_move_kernel(const __grid_constant__ EvictParams p, int slots_of_cta, int k
     const int tid = threadIdx.x;
     const Lengths x = lengths_of(p, b);
     const int slots = min(slots_of_cta, x.n - j0);
-    if (slots <= 0) return;
+    if (slots <= 0) {
+        // (where no sequence keeps a token, this grid still ends after the one before it)
+        if (blockIdx.x == 0 && b == 0) pdl_wait_primary();
+        return;
+    }
     const int count = slots * p.hkv;
     // an entry a thread, a token's heads side by side
     const int s = tid / p.hkv, h = tid - s * p.hkv;

@@ -218,6 +218,20 @@ def test_into_other_pages_of_the_same_pool(attn):
     assert torch.equal(pool[same], before[same])
 
 
+def test_lengths_are_there_where_no_token_stays(attn):
+    """What follows a call that moves nothing: the lengths are 0, whatever they were."""
+    c = Case([3000, 200, 0], [0, -5, 7], seed=2)
+    pos, kw = c.inputs()
+    want = torch.zeros(3, dtype=torch.int32, device=DEV)
+    seen = []
+    for _ in range(20):
+        kept = torch.full((3,), 77, dtype=torch.int32, device=DEV)
+        attn.attn_evict_kv(*pos, **kw, kept_len=kept)
+        seen.append(kept.clone())
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, want) for x in seen)
+
+
 def test_offsets_beyond_32_bits(attn):
     # pages far apart in one large pool: 3 G elements of keys, as much of values
     pages, page, dim = 1 << 15, 64, 1024
