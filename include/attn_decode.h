@@ -739,6 +739,8 @@ int attn_key_weights(const void *q, const attn_kv_t *k, const float *lse, const 
  *   kept_len   out, device uint32 [batch]: n, or NULL.
  *   indices    out, device int32 [batch][num_kv_heads][max_keep]: the kept tokens,
  *              rising; entries from n on are left.
+ *              Neither may share memory with the other, with kv_len, keep or a page
+ *              table (ATTN_ERR_INVALID_ARG): lengths are not brought up to date in place.
  *
  * A kept token has its place among the keys changed, not its rotation: rows that are
  * appended behind it need their positions given.  Pages outside a pool set bit 1 of the

@@ -919,7 +919,8 @@ def attn_evict_kv(k_cache: torch.Tensor, v_cache: Optional[torch.Tensor], weight
     0 on of the pages that out_page_table gives it in k_out and v_out (bf16; no page
     that is read), their weights beside them.  keep int32 [batch] on the device, at most
     max_keep.  v_cache and v_out None: a cache whose V is part of K.  Returns (kept_len
-    int32 [batch], indices int32 [batch, num_kv_heads, max_keep]: the kept tokens)."""
+    int32 [batch], indices int32 [batch, num_kv_heads, max_keep]: the kept tokens), which
+    share no memory with kv_len, keep or a page table."""
     k_shape, out_shape, batch = k_cache.shape, k_out.shape, kv_len.shape[0]
     heads, dim = k_shape[2:]
     if (v_cache is None) != (v_out is None):

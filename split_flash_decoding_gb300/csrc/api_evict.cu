@@ -62,6 +62,13 @@ bool same_layout(const attn_kv_t *a, const attn_kv_t *b) {
            a->max_pages == b->max_pages && a->num_pages == b->num_pages;
 }
 
+// Whether an output of n bytes shares any with an input of m bytes.
+bool overlap(const void *out, long long n, const void *in, long long m) {
+    if (!out || !in || n <= 0 || m <= 0) return false;
+    const uintptr_t a = reinterpret_cast<uintptr_t>(out), b = reinterpret_cast<uintptr_t>(in);
+    return a < b + m && b < a + n;
+}
+
 int device_sms(int *sms) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||
@@ -164,6 +171,20 @@ extern "C" int attn_evict_kv(const attn_kv_t *k, const attn_kv_t *v, const attn_
     }
     if ((st = take_floats(weights, &p.w))) return st;
     if (weights_out && (st = take_floats(weights_out, &p.w_to))) return st;
+    // Both kernels read the lengths, and every CTA for itself: nothing that the call writes may
+    // lie in what it reads, lengths brought up to date in place least of all.
+    const long long lens = 4LL * batch, list = 4LL * batch * num_kv_heads * max_keep;
+    const struct {
+        const void *at;
+        long long bytes;
+    } read[] = {{kv_len, lens},
+                {keep, lens},
+                {k->page_table, lens * k->max_pages},
+                {k_out->page_table, lens * k_out->max_pages}};
+    for (const auto &x : read)
+        if (overlap(kept_len, lens, x.at, x.bytes) || overlap(indices, list, x.at, x.bytes))
+            return ATTN_ERR_INVALID_ARG;
+    if (overlap(kept_len, lens, indices, list)) return ATTN_ERR_INVALID_ARG;
     if ((st = device_error_word(&p.err))) return st;
     p.k = moved(k, k_out, dim_k);
     p.kv_len = kv_len;
