@@ -23,6 +23,9 @@ __device__ unsigned g_error_word;
 // Address of g_error_word in the current device's context.  Looked up on
 // every call (a host-side table lookup, far cheaper than a launch), so a
 // device reset or a new primary context never leaves a stale address behind.
+// A call asks for it before it encodes a tensor map: this one gives a host
+// thread its context, which the driver's encoding wants to be there (without it
+// the first call of a thread was answered with ATTN_ERR_UNSUPPORTED).
 int error_word(unsigned **out) {
     void *ptr = nullptr;
     if (cudaGetSymbolAddress(&ptr, g_error_word) != cudaSuccess || ptr == nullptr)
@@ -218,6 +221,7 @@ int prefill_path(const void *q, const attn_kv_t *k, const attn_kv_t *v, const ui
     p.box_rows = ps < kTileKeys ? ps : kTileKeys;
     p.box_rows_v = p.box_rows;
     if (pair) p.box_rows = ps < 64 ? ps : 64;   // the K half of a pair: 64 keys
+    if ((st = error_word(&p.err))) return st;                // (before any map)
     st = encode_kv_map(&p.k_map, *k, head_dim, hkv, p.box_rows);
     if (st) return st;
     st = encode_kv_map(&p.v_map, *v, head_dim, hkv, p.box_rows_v);
@@ -237,8 +241,6 @@ int prefill_path(const void *q, const attn_kv_t *k, const attn_kv_t *v, const ui
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
         if (r != CUDA_SUCCESS) return ATTN_ERR_UNSUPPORTED;
     }
-    st = error_word(&p.err);
-    if (st) return st;
     p.kv_len = kv_len;
     p.q_row_offsets = q_row_offsets;
     p.page_table = k->page_table;
@@ -566,6 +568,7 @@ extern "C" int attn_decode(const void *q, const attn_kv_t *k, const attn_kv_t *v
     GqaParams p;
     std::memset(&p, 0, sizeof(p));
     p.box_rows = k->page_table ? (k->page_size < tile ? k->page_size : tile) : tile;
+    if ((st = error_word(&p.err))) return st;                // (before any map)
     st = encode_kv_map(&p.k_map, *k, head_dim, hkv, p.box_rows);
     if (st) return st;
     st = encode_kv_map(&p.v_map, *v, head_dim, hkv, p.box_rows);
@@ -585,8 +588,6 @@ extern "C" int attn_decode(const void *q, const attn_kv_t *k, const attn_kv_t *v
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
         if (r != CUDA_SUCCESS) return ATTN_ERR_UNSUPPORTED;
     }
-    st = error_word(&p.err);
-    if (st) return st;
 
     p.q = static_cast<const uint16_t *>(q);
     p.kv_len = kv_len;
@@ -758,6 +759,7 @@ int mla_decode_impl(const void *q, const attn_kv_t *kv, const uint32_t *kv_len,
     p.box_rows = sparse ? 1
                  : kv->page_table ? (kv->page_size < kMlaTileKeys ? kv->page_size : kMlaTileKeys)
                                   : kMlaTileKeys;
+    if ((st = error_word(&p.err))) return st;                // (before any map)
     st = sparse ? encode_rows_map(&p.kv_map, *kv, dim_qk)
                 : encode_kv_map(&p.kv_map, *kv, dim_qk, 1, p.box_rows);
     if (st) return st;
@@ -765,8 +767,6 @@ int mla_decode_impl(const void *q, const attn_kv_t *kv, const uint32_t *kv_len,
                 : encode_kv_map(&p.rope_map, *kv, dim_qk, 1, p.box_rows, kMlaRopeBoxCh);
     if (st) return st;
     p.q = static_cast<const uint16_t *>(q);
-    st = error_word(&p.err);
-    if (st) return st;
     p.kv_len = kv_len;
     p.q_row_offsets = q_row_offsets;
     p.num_q_rows = num_q_rows;

@@ -111,12 +111,13 @@ extern "C" int attn_key_weights(const void *q, const attn_kv_t *k, const float *
     const bool few = static_cast<long long>(max_q_len) * group <= kFewColumns;
     p.tile_rows = (few ? kFewColumns : kManyColumns) / group;
     p.box_rows = k->page_table && k->page_size < 128 ? k->page_size : 128;
-    if ((st = encode_kv_map_bf16(&p.k_map, k->base, k->token_stride, k->head_stride, k->page_stride,
+    // (the error word first: see error_word)
+    if ((st = device_error_word(&p.err)) ||
+        (st = encode_kv_map_bf16(&p.k_map, k->base, k->token_stride, k->head_stride, k->page_stride,
                                  head_dim, k->page_size, hkv, k->num_pages, p.box_rows)) ||
         // (without rows the map is not used, but has to be one)
         (st = encode_q_map_bf16(&p.q_map, num_q_rows > 0 ? q : k->base, head_dim, group, hkv,
-                                num_q_rows > 0 ? num_q_rows : 1, p.tile_rows)) ||
-        (st = device_error_word(&p.err)))
+                                num_q_rows > 0 ? num_q_rows : 1, p.tile_rows)))
         return st;
     p.lse = lse;
     p.kv_len = kv_len;
