@@ -35,8 +35,8 @@ struct RunCut {
 
 // Shared memory: angles [128][4][8] when there is a rotation, then the vectors in
 // flight [kS][2][kT].
-size_t run_smem(const RowsParams &p) {
-    return (p.rope.rot_dim > 0 ? size_t(kGroupTokens) * 4 * kL * sizeof(float4) : 0) +
+size_t run_smem(bool rotates) {
+    return (rotates ? size_t(kGroupTokens) * 4 * kL * sizeof(float4) : 0) +
            size_t(kT) * 2 * kS * sizeof(uint4);
 }
 
@@ -278,9 +278,8 @@ cudaError_t launch_fp8_runs(const RowsParams &p, bool behind_queries, cudaStream
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
     cut.k_ctas = static_cast<int>(tiles * cut.k_chunks);
     auto kern = p.rope.interleaved ? append_fp8_runs_kernel<true> : append_fp8_runs_kernel<false>;
-    const size_t smem = run_smem(p);
-    const cudaError_t e =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    const size_t smem = run_smem(p.rope.rot_dim > 0);
+    const cudaError_t e = allow_smem(kern, run_smem(true));
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(blocks));

@@ -22,6 +22,7 @@
 #include <cooperative_groups.h>
 
 #include "evict_ops.h"
+#include "launch.h"
 #include "ptx.cuh"
 
 namespace cg = cooperative_groups;
@@ -411,8 +412,8 @@ cudaError_t launch_select(const EvictParams &p, int slice, cudaStream_t stream) 
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         int(cfg.dynamicSmemBytes));
+    const cudaError_t e =
+        allow_smem(kern, sizeof(Shared) + (kPer > 0 ? 0 : sizeof(uint32_t) * size_t(kHeldKeys)));
     if (e != cudaSuccess) return e;
     return cudaLaunchKernelEx(&cfg, kern, p, held);
 }

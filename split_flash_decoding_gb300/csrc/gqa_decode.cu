@@ -509,8 +509,7 @@ template <int D, int G>
 cudaError_t launch_t(const GqaParams &p, cudaStream_t stream) {
     const size_t smem = gqa_smem_bytes<D, G>(p.batch);
     auto kern = gqa_decode_kernel<D, G>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         int(smem));
+    cudaError_t e = allow_smem(kern, gqa_smem_bytes<D, G>(kGqaMaxBatch));
     if (e != cudaSuccess) return e;
     int dev = 0;
     e = cudaGetDevice(&dev);

@@ -1402,8 +1402,7 @@ template <int NC, bool kFp4, int kVs>
 cudaError_t launch_nc(const Fp8DecodeParams &p, int ctas, cudaStream_t stream) {
     const size_t smem = smem_bytes<NC, kFp4, kVs>(p.batch);
     auto kern = gqa_decode_codes_kernel<NC, kFp4, kVs>;
-    const cudaError_t e =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    const cudaError_t e = allow_smem(kern, smem_bytes<NC, kFp4, kVs>(kGqaMaxBatch));
     if (e != cudaSuccess) return e;
     kern<<<dim3(static_cast<unsigned>(ctas)), Cfg<NC, kFp4, kVs>::kThreads, smem, stream>>>(p);
     return cudaGetLastError();

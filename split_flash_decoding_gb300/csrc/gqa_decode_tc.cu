@@ -740,8 +740,7 @@ template <int G, int NC, int C>
 cudaError_t launch_g(const GqaParams &p, cudaStream_t stream) {
     const size_t smem = tc_smem_bytes<C>(p.batch);
     auto kern = gqa_decode_tc_kernel<G, NC, C>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         int(smem));
+    cudaError_t e = allow_smem(kern, tc_smem_bytes<C>(kGqaMaxBatch));
     if (e != cudaSuccess) return e;
     int dev = 0;
     e = cudaGetDevice(&dev);

@@ -857,14 +857,15 @@ cudaError_t launch(const RowsParams &p, const Cut &cut, long long tiles, cudaStr
     const long long blocks = tiles * cut.chunks;
     if (blocks == 0) return cudaSuccess;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-    const size_t smem =                                              // up to 48 KB
-        (p.rope.rot_dim > 0 ? size_t(cut.tile_rows) * 4 * L * sizeof(float4) : 0) +
-        (kMany ? size_t(kAhead + 1) * 2 * kThreads * sizeof(uint4) : 0);
+    const auto bytes = [](int rows) {                                // up to 48 KB
+        return size_t(rows) * 4 * L * sizeof(float4) +
+               (kMany ? size_t(kAhead + 1) * 2 * kThreads * sizeof(uint4) : 0);
+    };
+    const size_t smem = bytes(p.rope.rot_dim > 0 ? cut.tile_rows : 0);
     auto kern = p.rope.interleaved ? head_tiles_kernel<L, true, kKind, kMany>
                                    : head_tiles_kernel<L, false, kKind, kMany>;
     if (smem > 40 * 1024) {                                          // (48 KB with the static part)
-        const cudaError_t e =
-            cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+        const cudaError_t e = allow_smem(kern, bytes(kItemsOf<L>));  // (rows of a tile, at most)
         if (e != cudaSuccess) return e;
     }
     kern<<<static_cast<unsigned>(blocks), kThreads, smem, stream>>>(p, cut);

@@ -589,10 +589,12 @@ key_weights_kernel(const __grid_constant__ WeightsParams p) {
 template <int D, bool kMany>
 cudaError_t launch(const WeightsParams &p, int sms, cudaStream_t stream) {
     using C = Cfg<D, kMany>;
-    const size_t smem = size_t(C::items) + (kMany ? 0 : sizeof(int) * size_t(p.batch + 1));
+    const auto bytes = [](int batch) {
+        return size_t(C::items) + (kMany ? 0 : sizeof(int) * size_t(batch + 1));
+    };
+    const size_t smem = bytes(p.batch);
     auto kern = key_weights_kernel<D, kMany>;
-    const cudaError_t e =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    const cudaError_t e = allow_smem(kern, bytes(kGqaMaxBatch));
     if (e != cudaSuccess) return e;
     const long long units = (static_cast<long long>(p.max_kv_len - 1) / (C::KT * kKeys) + 1) *
                             p.batch * (kMany ? p.hkv : p.head_groups);

@@ -18,6 +18,15 @@ constexpr int kGqaTcTileKeys = 128;
 // memory; batches above this size are rejected.
 constexpr int kGqaMaxBatch = 2048;
 
+// Lets launches of a kernel take up to `most` bytes of dynamic shared memory.  The limit is
+// the kernel's, for all host threads: `most` is what its largest call needs, never a call's
+// own bytes (those of a smaller call would come between another thread's and its launch).
+template <class Kernel>
+cudaError_t allow_smem(Kernel kern, size_t most) {
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(most));
+}
+
 struct GqaParams {
     CUtensorMap k_map;            // 4-D: (channel, slot, kv head, page)
     CUtensorMap v_map;

@@ -1,4 +1,6 @@
-"""Calls from host threads of the user's: the first that a thread makes."""
+"""Calls from host threads of the user's: the first that a thread makes, and calls of two threads
+at once whose kernels need unlike amounts of shared memory (a kernel's limit is the process's,
+so no call may set it to its own bytes)."""
 import threading
 
 import pytest
@@ -6,6 +8,7 @@ import torch
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
+CALLS = 5000                # of each thread
 
 
 @pytest.fixture(scope="module")
@@ -160,3 +163,63 @@ def test_first_call_of_a_thread(attn, name):
         if a.dtype == torch.int32 and a.dim() == 3:      # (kept tokens: eight of them are there)
             a, b = a[..., :8], b[..., :8]
         assert torch.equal(a, b)
+
+
+PAIRS = {
+    "decode of 64 channels": (lambda a, s: decode(a, 1, s, 64), lambda a, s: decode(a, 2048, s, 64)),
+    "decode of 128 channels": (lambda a, s: decode(a, 1, s, 128),
+                               lambda a, s: decode(a, 2048, s, 128)),
+    "decode in 4 bits": (lambda a, s: decode_fp4(a, 400, s), lambda a, s: decode_fp4(a, 2048, s)),
+    "decode in 8 bits": (lambda a, s: decode_fp8(a, 1, s), lambda a, s: decode_fp8(a, 2048, s)),
+    "key weights": (lambda a, s: key_weights(a, 1, s), lambda a, s: key_weights(a, 2048, s)),
+    "eviction": (lambda a, s: evict(a, 140000, s), lambda a, s: evict(a, 262144, s)),
+    "append": (lambda a, s: append(a, 4000, s), lambda a, s: append(a, 5000, s)),
+    "append in 8 bits": (lambda a, s: append_fp8(a, False, s), lambda a, s: append_fp8(a, True, s)),
+}
+
+
+class Recorder:
+    """In place of the library: what a call of the binding gives it, and nothing runs."""
+
+    def __init__(self, attn):
+        self.lib, self.calls = attn.lib(), []
+
+    def __getattr__(self, name):
+        if name.endswith("_workspace") or name == "attn_plan_partitions":
+            return getattr(self.lib, name)
+        return lambda *args: self.calls.append((getattr(self.lib, name), args)) or 0
+
+
+@pytest.mark.parametrize("name", list(PAIRS))
+def test_two_threads_at_once(attn, monkeypatch, name):
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    runs = [make(attn, s) for make, s in zip(PAIRS[name], streams)]
+    outs, calls = [], []
+    with monkeypatch.context() as m:
+        for run in runs:
+            recorder = Recorder(attn)
+            m.setattr(attn, "lib", lambda: recorder)
+            outs.append(run())                           # (held: the calls write them)
+            calls.append(recorder.calls[0])
+            m.undo()
+    torch.cuda.synchronize()
+    start, codes = threading.Barrier(2), [0, 0]
+
+    def work(me):
+        fn, args = calls[me]
+        start.wait(60)
+        for i in range(CALLS):
+            code = fn(*args)
+            if code != 0:
+                codes[me] = code
+                break
+            if i % 100 == 99:
+                streams[me].synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert codes == [attn.ATTN_OK, attn.ATTN_OK]
