@@ -743,9 +743,9 @@ int attn_key_weights(const void *q, const attn_kv_t *k, const float *lse, const 
  *              table (ATTN_ERR_INVALID_ARG): lengths are not brought up to date in place.
  *
  * A kept token has its place among the keys changed, not its rotation: rows that are
- * appended behind it need their positions given.  Pages outside a pool set bit 1 of the
- * error word (rows of theirs are not copied), kv_len and keep above their bounds bit 2
- * (they are clamped).  batch <= 2048, num_kv_heads <= 256.  Returns as attn_key_weights.
+ * appended behind it need their positions given.  A page outside its pool, of a token that
+ * is weighed, kept or written, sets bit 1 of the error word (rows of such pages are not
+ * copied), kv_len and keep above their bounds bit 2 (they are clamped).  batch <= 2048, num_kv_heads <= 256.  Returns as attn_key_weights.
  */
 int attn_evict_kv(const attn_kv_t *k, const attn_kv_t *v, const attn_kv_scale_t *weights,
                   const uint32_t *kv_len, const int32_t *keep, int batch, int num_kv_heads,

@@ -57,7 +57,7 @@ __device__ __forceinline__ int page_in(const int32_t *table, int max_pages, int 
     slot = t & (page_size - 1);
     const int e = pidx < max_pages ? table[size_t(b) * max_pages + pidx] : -1;
     if (e < 0 || e >= num_pages) {
-        if (err) atomicOr(err, kErrBadPage);
+        atomicOr(err, kErrBadPage);
         return -1;
     }
     return e;
@@ -372,7 +372,8 @@ evict_move_kernel(const __grid_constant__ EvictParams p, int slots_of_cta, int k
         const int t = p.indices[(size_t(b) * p.hkv + h) * p.max_keep + j0 + s];
         int slot = 0, page = -1;
         if (t >= 0 && t < x.L)
-            page = page_in(p.page_table, p.max_pages, p.num_pages, p.page_size, b, t, nullptr, slot);
+            // (reported here too: of tokens that stay in any case the choice has read no weight)
+            page = page_in(p.page_table, p.max_pages, p.num_pages, p.page_size, b, t, p.err, slot);
         Entry at;
         at.k_from = page * p.k.from_page + slot * p.k.from_token + h * p.k.from_head;
         at.v_from = page * p.v.from_page + slot * p.v.from_token + h * p.v.from_head;
