@@ -153,7 +153,8 @@ __device__ __forceinline__ bool find_unit(const WeightsParams &p, const int *cum
     return true;
 }
 
-// Page of token t of sequence b (-1: outside the pool) and its slot.
+// Page of token t of sequence b (-1: outside the pool) and its slot.  report: the threads that
+// own the keys, as they walk the units without rows too (the key producer skips those).
 __device__ __forceinline__ int page_at(const WeightsParams &p, int b, int t, bool report, int &slot) {
     if (!p.page_table) {
         slot = t;
@@ -291,7 +292,7 @@ key_weights_kernel(const __grid_constant__ WeightsParams p) {
             if (!find_unit<kMany>(p, cum, j, it) || it.steps == 0) continue;
             const int live = min(nb, (it.L - it.key0 + box_rows - 1) >> box_shift);
             int page = -1, slot = 0;                             // of the lane's box
-            if (lane < live) page = page_at(p, it.b, it.key0 + (lane << box_shift), true, slot);
+            if (lane < live) page = page_at(p, it.b, it.key0 + (lane << box_shift), false, slot);
             const int row = lane << box_shift;                   // in the item
             uint8_t *dst = smem + C::k + (row / kKeys) * C::kTileBytes + (row % kKeys) * 128;
             for (int h = 0; ok && h < it.heads; ++h) {
@@ -480,7 +481,7 @@ key_weights_kernel(const __grid_constant__ WeightsParams p) {
             for (int h = 0; h < C::kHeads; ++h) old[h] = w[h] = 0.f;
             if (part < KT && key < it.L) {
                 int slot;
-                const int page = page_at(p, it.b, key, false, slot);
+                const int page = page_at(p, it.b, key, true, slot);
                 if (page >= 0)
                     where = p.w.base + page * p.w.page + slot * p.w.token + it.kvh * p.w.head;
             }
