@@ -666,8 +666,8 @@ int attn_append_kv_fp4(const attn_head_rows_t *q, const attn_head_rows_t *k,
  * attn_decode_fp4 -- attn_decode over a cache held in 4 bits.
  *
  * Arguments, limits and workspace as for attn_decode_fp8, with k, v, k_scale and v_scale
- * as above.  A weight times its value scale's power of two errs by at most 2^-11 of itself,
- * or by 2^-27 of the largest such product that the row's keys have with it, where that is
+ * as above.  A weight times its value scale's power of two errs by at most 2^-12 of itself,
+ * or by 2^-34 of the largest such product that the row's keys have with it, where that is
  * more.  A token whose key or value scale is NaN makes the out of the rows that see it NaN
  * (their lse is then undefined) and of no others.
  */

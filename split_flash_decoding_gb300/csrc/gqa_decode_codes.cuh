@@ -50,10 +50,15 @@
 //   A key's scale differs between its four groups of channels, so each group's product goes to
 //     columns of its own and the thread that owns the key adds the four up.  With 16 columns
 //     the two terms of q are two MMAs into the same columns (q1 in e5m2, which holds q1 / 16).
-//   weights: f16, cut into four e5m2 terms of 3 of its 11 bits each (the upper byte of an f16
-//     number is an e5m2 number), so O's four terms simply add up: an error of at most 2^-11 of
-//     a weight or 2^-27 of the reference's.  (Fewer instructions than four e4m3 terms: with
-//     all lanes of the MMA warp walking, see there, 84.0 and 70.1 us for 64 sequences.)
+//   weights = w0 + 2^-4 (w1 + w2) + 2^-10 w3 in e5m2 (3 bits; the upper byte of an f16 number is
+//     one): w0 and w3 rounded, w1 and w2 what is left cut off.  Half a step of w0 is at most
+//     2^-3 of it, a cut leaves three bits less, half a step of w3 is three bits and one down: at
+//     most 2^-13 of a weight, 2^-15 more where what w0 leaves becomes an f16 number, so 2^-12;
+//     or 2^-34 of the reference's where that is more (what is below 2^-38 of it is lost).  w3
+//     cannot start lower: 64 times what is left of the largest weight is 2^15.  (Four cuts of
+//     an f16 number, all in one unit, erred by 2^-11, or 2^-27 and always toward 0, for the same
+//     time but with draft rows, 71.3 and 72.1 us.  Four e4m3 terms are those of 8 bits; they
+//     were not timed since the MMA warp walks as one.)
 //   Up to 4 columns two groups of softmax warps take the tiles in turns, each with its own
 //     weights, reference and output, joined at an item's end: what one waits for (scores, the
 //     barrier, the last P.V) the other uses.  A warp for each contraction's MMAs (one for both
@@ -107,7 +112,9 @@ constexpr float kLazy = 3.f;                 // base 2
 // Weights reach 2^kLazy * 2 * this: 256 of e4m3's 448, 2^15 of e5m2's 57344.
 __host__ __device__ constexpr float weight_top(bool fp4) { return fp4 ? 2048.f : 16.f; }
 // Each term's unit over the next one's (see above).
-__host__ __device__ constexpr float term_ratio(int u) { return u < 2 ? 32.f : 32768.f; }
+__host__ __device__ constexpr float term_ratio(bool fp4, int u) {
+    return fp4 ? (u == 0 ? 16.f : u == 1 ? 1.f : 64.f) : u < 2 ? 32.f : 32768.f;
+}
 constexpr int kBarBytes = 304;
 constexpr int kMinVExp = -64, kMaxVExp = 64;
 
@@ -364,26 +371,46 @@ __device__ __forceinline__ void take_rest(uint32_t c, float &a, float &b) {
     asm("fma.rn.f32.f16 %0, %1, %2, %0;" : "+f"(b) : "h"(h.y), "h"(minus1));
 }
 
+// r minus sixteen times the f16 numbers of c.
+__device__ __forceinline__ void take_sixteenfold(uint32_t c, float2 &r) {
+    const unsigned short minus16 = 0xcc00;   // f16
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+        "fma.rn.f32.f16 %0, l, %3, %0;\n\tfma.rn.f32.f16 %1, h, %3, %1;\n\t}"
+        : "+f"(r.x), "+f"(r.y)
+        : "r"(c), "h"(minus16));
+}
+
 // The same in e5m2.
 __device__ __forceinline__ uint32_t to_e5m2x2(float a, float b) {
     return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E5M2);
 }
 
-// Four weights as f16 and those as four e5m2 terms each, a term of all four to a word: an
-// e5m2 number is the upper half of an f16 one, so a term is what its upper half says, cut
-// off, and the next the (exact) rest's: 3 bits each of the 11.
-__device__ __forceinline__ void half_terms(const float2 &a, const float2 &b, uint32_t (&code)[4]) {
+// Four weights as four e5m2 terms each, a term of all four to a word.  The first is the
+// nearest; sixteen times what it leaves (exact in fp32, of either sign) becomes an f16 number.
+// The upper byte of such a number is an e5m2 number: that is the next term, cut off, and so
+// once more; 64 times the rest is rounded again.  (Every product is by a power of two.)
+__device__ __forceinline__ void e5m2_terms(const float2 &a, const float2 &b, uint32_t (&code)[4]) {
+    code[0] = to_e5m2x2(a.x, a.y) | (to_e5m2x2(b.x, b.y) << 16);
+    const float2 unit = make_float2(term_ratio(true, 0), term_ratio(true, 0));
+    float2 ra = __fmul2_rn(a, unit), rb = __fmul2_rn(b, unit);
+    take_sixteenfold(__byte_perm(code[0], 0, 0x1404), ra);
+    take_sixteenfold(__byte_perm(code[0], 0, 0x3424), rb);
     uint32_t x, y;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(x) : "f"(a.y), "f"(a.x));
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(b.y), "f"(b.x));
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(x) : "f"(ra.y), "f"(ra.x));
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(rb.y), "f"(rb.x));
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
+    for (int u = 1; u < 3; ++u) {
         code[u] = __byte_perm(x, y, 0x7531);
-        if (u < 3) {
-            asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(x) : "r"(x & 0xff00ff00u));
-            asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(y) : "r"(y & 0xff00ff00u));
-        }
+        asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(x) : "r"(x & 0xff00ff00u));
+        asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(y) : "r"(y & 0xff00ff00u));
     }
+    const uint32_t last = 0x54005400u;                           // term_ratio(true, 2), twice
+    asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(x) : "r"(last));
+    asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(y) : "r"(last));
+    uint16_t lo, hi;
+    asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(lo) : "r"(x));
+    asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(hi) : "r"(y));
+    code[3] = uint32_t(lo) | (uint32_t(hi) << 16);
 }
 
 // The scales that the four e8m0 bytes of w stand for (255: NaN), by way of bf16.
@@ -1166,7 +1193,7 @@ gqa_decode_codes_kernel(const __grid_constant__ Fp8DecodeParams p) {
                         w[c] = __fmul2_rn(e, make_float2(v_mul, v_mul));
                     }
                     if constexpr (kFp4) {
-                        half_terms(w[0], w[1], code[h]);
+                        e5m2_terms(w[0], w[1], code[h]);
                     } else {
 #pragma unroll
                         for (int u = 0; u < 4; ++u) {
@@ -1176,7 +1203,7 @@ gqa_decode_codes_kernel(const __grid_constant__ Fp8DecodeParams p) {
                             if (u < 3) {
                                 take_rest(lo, w[0].x, w[0].y);
                                 take_rest(hi, w[1].x, w[1].y);
-                                const float2 ratio = make_float2(term_ratio(u), term_ratio(u));
+                                const float2 ratio = make_float2(term_ratio(kFp4, u), term_ratio(kFp4, u));
                                 w[0] = __fmul2_rn(w[0], ratio);
                                 w[1] = __fmul2_rn(w[1], ratio);
                             }
@@ -1336,7 +1363,7 @@ gqa_decode_codes_kernel(const __grid_constant__ Fp8DecodeParams p) {
                         float acc = term[3][u];
 #pragma unroll
                         for (int v = 2; v >= 0; --v)
-                            acc = fmaf(acc, kFp4 ? 1.f : 1.f / term_ratio(v), term[v][u]);
+                            acc = fmaf(acc, 1.f / term_ratio(kFp4, v), term[v][u]);
                         o[q][u] = ok && tiles_of[q] > 0 ? acc * (1.f / weight_top(kFp4)) : 0.f;
                     }
                 }
