@@ -7,7 +7,7 @@
 // use: conversions, scales and rotation of vectors that are there already; 24,768 rows of
 // 32 + 8 heads, keys normed, 121 us, 5.2 TB/s), 64 rows by latency (3.8 us).  Rotations
 // whose pairs do not fall on whole 16-byte vectors have the kernel here, one warp a row and
-// head.
+// head, with the same roundings.
 #include "head_tiles.cuh"
 
 namespace attn {
@@ -41,7 +41,7 @@ append_fp4_kernel(const __grid_constant__ RowsParams p) {
     }
     if (p.positions) pos = p.positions[r];
     float *y = buf[warp];
-    load_head(p, x, r, h, pos, is_k && p.rope.rot_dim > 0, y, lane);
+    load_head<true>(p, x, r, h, pos, is_k && p.rope.rot_dim > 0, y, lane);
     __syncwarp();
     const float4 v = *reinterpret_cast<const float4 *>(y + 4 * lane);
     uint32_t top = max(max(__float_as_uint(fabsf(v.x)), __float_as_uint(fabsf(v.y))),

@@ -95,6 +95,9 @@ __device__ __forceinline__ int page_of(const RowsParams &p, int b, int t) {
 }
 
 // Head h of row r, normed and (rotate) rotated, into y (shared memory); one warp.
+// kStepwise: each operation rounded by itself, as in the 4-bit tiles (see there): a head's codes
+// then do not depend on which of the two kernels took it.
+template <bool kStepwise = false>
 __device__ __forceinline__ void load_head(const RowsParams &p, const HeadRows &x, int r, int h,
                                           int pos, bool rotate, float *y, int lane) {
     const uint16_t *src = x.in + r * x.in_row + h * x.in_head;
@@ -107,8 +110,10 @@ __device__ __forceinline__ void load_head(const RowsParams &p, const HeadRows &x
     __syncwarp();
     if (x.norm_dim > 0) {
         const float inv = rsqrtf(warp_sum(sq) / static_cast<float>(x.norm_dim) + x.eps);
-        for (int c = lane; c < x.norm_dim; c += 32)
-            y[c] *= inv * (x.norm ? bf16_lo(x.norm[c]) : 1.f);
+        for (int c = lane; c < x.norm_dim; c += 32) {
+            const float g = x.norm ? bf16_lo(x.norm[c]) : 1.f;
+            y[c] = kStepwise ? __fmul_rn(__fmul_rn(y[c], inv), g) : y[c] * (inv * g);
+        }
         __syncwarp();
     }
     if (rotate) {
@@ -119,8 +124,13 @@ __device__ __forceinline__ void load_head(const RowsParams &p, const HeadRows &x
             float c, s;
             rope_cos_sin(p.rope, i, pos, c, s);
             const float ya = y[a], yb = y[b];
-            y[a] = fmaf(ya, c, -yb * s);
-            y[b] = fmaf(yb, c, ya * s);
+            if (kStepwise) {
+                y[a] = __fsub_rn(__fmul_rn(ya, c), __fmul_rn(yb, s));
+                y[b] = __fadd_rn(__fmul_rn(yb, c), __fmul_rn(ya, s));
+            } else {
+                y[a] = fmaf(ya, c, -yb * s);
+                y[b] = fmaf(yb, c, ya * s);
+            }
         }
         __syncwarp();
     }
