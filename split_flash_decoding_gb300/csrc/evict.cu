@@ -422,11 +422,16 @@ cudaError_t launch_select(const EvictParams &p, int slice, cudaStream_t stream) 
 template <int kRanks>
 cudaError_t launch_ranks(const EvictParams &p, cudaStream_t stream) {
     const int slice = ((p.max_kv_len + kRanks - 1) / kRanks + kThreads - 1) / kThreads * kThreads;
-    if (slice <= kThreads && kRanks == 1) return launch_select<kRanks, 1>(p, slice, stream);
+    if constexpr (kRanks == 1) {
+        if (slice <= kThreads) return launch_select<kRanks, 1>(p, slice, stream);
+    }
     if (slice <= 4 * kThreads) return launch_select<kRanks, 4>(p, slice, stream);
     if (slice <= 8 * kThreads) return launch_select<kRanks, 8>(p, slice, stream);
-    if (slice <= kMostPer * kThreads) return launch_select<kRanks, kMostPer>(p, slice, stream);
-    return launch_select<kRanks, 0>(p, slice, stream);
+    // (fewer CTAs than a cluster's most never have longer slices)
+    if constexpr (kRanks == kMaxCluster) {
+        if (slice > kMostPer * kThreads) return launch_select<kRanks, 0>(p, slice, stream);
+    }
+    return launch_select<kRanks, kMostPer>(p, slice, stream);
 }
 
 }  // namespace
