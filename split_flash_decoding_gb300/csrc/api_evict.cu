@@ -69,6 +69,22 @@ bool overlap(const void *out, long long n, const void *in, long long m) {
     return a < b + m && b < a + n;
 }
 
+// Whether key weights take the kernel of few columns, whose CTAs walk units of four KV heads in
+// steps of kFewColumns, or the one of many, of whose CTAs there are `items`, one for 256 keys of a
+// head.  The latter takes 5.5 us for a round of them over the GPU whatever the columns, up to 256;
+// the former reads keys at the memory's rate up to 32 columns and about 14.5 us for each 16
+// more of 64 sequences.  us, few and many, 8 KV heads of 128 channels:
+//   columns                                32         64          128         160         192
+//   64 sequences, 512 to 8192 keys     95, 330   145, 339    259, 348    315, 351    373, 360
+//   131072 keys                        49, 150    72, 153    127, 159    155, 161    182, 167
+//   16 sequences, 300 to 700           8.1, 16   10.7, 17    16.5, 18    19.7, 18    22.5, 18
+//   4 sequences, 1024 to 4096          7.9, 13   10.8, 14    16.6, 14    19.6, 14    22.6, 15
+//   500 keys                          7.4, 6.4  10.2, 6.7   16.1, 6.7   19.1, 6.9   22.1, 7.3
+// (2 KV heads, 4 sequences of 1024 to 4096: 5.9, 6.8; 7.3, 6.8; 10.3, 6.9.)
+bool few_columns(long long columns, int group, long long items, int sms) {
+    return group <= kFewColumns && columns <= (items <= sms ? 32 : items <= 4LL * sms ? 64 : 128);
+}
+
 int device_sms(int *sms) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||
@@ -108,7 +124,10 @@ extern "C" int attn_key_weights(const void *q, const attn_kv_t *k, const float *
     std::memset(&p, 0, sizeof(p));
     int st = check_cache(k, batch, head_dim, hkv, max_kv_len);
     if (st || (st = take_floats(weights, &p.w))) return st;
-    const bool few = static_cast<long long>(max_q_len) * group <= kFewColumns;
+    int sms = 0;
+    if ((st = device_sms(&sms))) return st;
+    const bool few = few_columns(static_cast<long long>(max_q_len) * group, group,
+                                 (max_kv_len / 256 + 1LL) * batch * hkv, sms);
     p.tile_rows = (few ? kFewColumns : kManyColumns) / group;
     p.box_rows = k->page_table && k->page_size < 128 ? k->page_size : 128;
     // (the error word first: see error_word)
@@ -129,7 +148,6 @@ extern "C" int attn_key_weights(const void *q, const attn_kv_t *k, const float *
     p.group = group;
     p.hkv = hkv;
     p.head_groups = (hkv + 3) / 4;
-    p.max_q_len = max_q_len;
     p.max_kv_len = max_kv_len;
     p.causal = causal ? 1 : 0;
     p.max_pages = k->max_pages;
@@ -137,8 +155,6 @@ extern "C" int attn_key_weights(const void *q, const attn_kv_t *k, const float *
     p.num_pages = k->num_pages;
     p.scale = scale;
     p.decay = decay;
-    int sms = 0;
-    if ((st = device_sms(&sms))) return st;
     return map_cuda(launch_key_weights(p, head_dim, few, sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 

@@ -25,7 +25,7 @@ struct WeightsParams {
     const int32_t *page_table;    // [batch][max_pages] or nullptr
     TokenFloats w;
     unsigned *err;
-    int batch, num_q_rows, num_q_heads, group, hkv, max_q_len, max_kv_len;
+    int batch, num_q_rows, num_q_heads, group, hkv, max_kv_len;
     int causal;
     int max_pages, page_size, num_pages;
     int box_rows;                 // tokens per TMA box (min(128, page size))

@@ -15,8 +15,8 @@
 //
 // An item is KT tiles of 128 keys of one (sequence, KV head); its steps are the
 // column tiles of the rows that see one of its keys.
-//   Few columns (rows x group <= 16, decode): KT = 1, one step of 16 columns.  Bound by
-//   the stream of keys.  Two CTAs per SM walk the units of all sequences, a unit being a
+//   Few columns (decode, draft rows): KT = 1, steps of 16 columns.  Bound by the stream of
+//   keys up to 32 columns.  Two CTAs per SM walk the units of all sequences, a unit being a
 //   tile of up to four KV heads, an item each: a thread then has its key's weights of four
 //   heads, neighbours in memory, and reads and writes them at once (a head at a time, four
 //   bytes of every 32 were 15 of 125 us).  64 sequences of 512 to 8192 keys 95 to 98 us, 6.2 TB/s.
