@@ -20,6 +20,8 @@
  * - Arguments are validated on the host before anything is launched.  A
  *   failed check returns a status and launches nothing.  A failed launch
  *   returns ATTN_ERR_CUDA (the CUDA error is left for cudaGetLastError).
+ * - Several host threads may call at once, each call with buffers of its own
+ *   (attn_decode_noalloc: one scratch for all, so one stream at a time).
  * - bf16 for q, K, V and out (the entry points named _fp8 and _fp4: K
  *   and V in e4m3 or e2m1 codes with scales); fp32 for scale, sink logits, lse and the
  *   split-K workspace.  All element strides are in elements.
@@ -697,7 +699,8 @@ int attn_decode_fp4(const void *q, const attn_kv_t *k, const attn_kv_t *v,
  *              (sinks, if there were any, are in it).
  *   head_dim   64 or 128.  batch <= 2048.
  *   max_q_len  host upper bound of the rows of any sequence: it picks the kernel,
- *              more rows are taken as well.
+ *              more rows are taken as well (some three times slower where it says few
+ *              of many, or many of few).
  *   decay      factor of the weights from before (0: they are not read).
  *   weights    read and written: for t < kv_len[b], with n the rows of sequence b,
  *     w_t = [t < kv_len[b] - n] decay w_t
@@ -707,8 +710,10 @@ int attn_decode_fp4(const void *q, const attn_kv_t *k, const attn_kv_t *v,
  *              before is not read).  Tokens at and behind kv_len[b] are left.
  *              Sequences of a call must not share a page.
  *
- * A sequence without rows has its weights multiplied by decay.  Sums are fp32 in a
- * fixed order: equal calls give equal weights.  A page outside the pool sets bit 1 of
+ * A sequence without rows has its weights multiplied by decay.  Scores, exponents and
+ * sums are fp32: a term errs by at most (head_dim / 16 + 2) 2^-23 scale sum_c |q_c k_c| +
+ * 2^-23 (|scale q.k| + |lse|) + 2^-22 (|x| + 1) of itself, x its exponent, and a sum of N
+ * terms by (N / 4 + 8) 2^-24 of itself, in a fixed order: equal calls give equal weights.  A page outside the pool sets bit 1 of
  * the error word (its tokens' weights are left), a kv_len above max_kv_len bit 2 (it is
  * clamped).  Returns ATTN_OK, ATTN_ERR_INVALID_ARG, ATTN_ERR_UNSUPPORTED or
  * ATTN_ERR_CUDA.

@@ -76,7 +76,7 @@
 // through a swizzled K-major layout 201 instead of 158 us for the draft rows, one group of
 // warps for 16 columns 147 instead of 103, 3 V stages the same.)
 // 4 bits: the same 64 sequences (309 MB) take 57.2 us, 5.4 TB/s; 131072 keys of one sequence
-// (143 MB) 33.0 us, of which 5.5 are the reduce and about 6 the start; 1 to 4 draft rows 71 us,
+// (143 MB) 33.0 us, of which 5.5 are the reduce and about 6 the start; 1 to 4 draft rows 72 us,
 // the softmax's issue slots (half of all, the rest lost to waits between its steps and to
 // instructions that are not yet there).
 #pragma once
