@@ -713,10 +713,10 @@ int attn_decode_fp4(const void *q, const attn_kv_t *k, const attn_kv_t *v,
  * A sequence without rows has its weights multiplied by decay.  Scores, exponents and
  * sums are fp32: a term errs by at most (head_dim / 16 + 2) 2^-23 scale sum_c |q_c k_c| +
  * 2^-23 (|scale q.k| + |lse|) + 2^-22 (|x| + 1) of itself, x its exponent, and a sum of N
- * terms by (N / 4 + 8) 2^-24 of itself, in a fixed order: equal calls give equal weights.  A page outside the pool sets bit 1 of
- * the error word (its tokens' weights are left), a kv_len above max_kv_len bit 2 (it is
- * clamped).  Returns ATTN_OK, ATTN_ERR_INVALID_ARG, ATTN_ERR_UNSUPPORTED or
- * ATTN_ERR_CUDA.
+ * terms by (N / 4 + 8) 2^-24 of itself, in a fixed order: equal calls give equal weights.
+ * A page outside the pool sets bit 1 of the error word (its tokens' weights are left), a
+ * kv_len above max_kv_len bit 2 (it is clamped).  Returns ATTN_OK, ATTN_ERR_INVALID_ARG,
+ * ATTN_ERR_UNSUPPORTED or ATTN_ERR_CUDA.
  */
 int attn_key_weights(const void *q, const attn_kv_t *k, const float *lse, const uint32_t *kv_len,
                      const uint32_t *q_row_offsets, int batch, int num_q_rows, int num_q_heads,
@@ -750,7 +750,8 @@ int attn_key_weights(const void *q, const attn_kv_t *k, const float *lse, const 
  * A kept token has its place among the keys changed, not its rotation: rows that are
  * appended behind it need their positions given.  A page outside its pool, of a token that
  * is weighed, kept or written, sets bit 1 of the error word (rows of such pages are not
- * copied), kv_len and keep above their bounds bit 2 (they are clamped).  batch <= 2048, num_kv_heads <= 256.  Returns as attn_key_weights.
+ * copied), kv_len and keep above their bounds bit 2 (they are clamped).  batch <= 2048,
+ * num_kv_heads <= 256.  Returns as attn_key_weights.
  */
 int attn_evict_kv(const attn_kv_t *k, const attn_kv_t *v, const attn_kv_scale_t *weights,
                   const uint32_t *kv_len, const int32_t *keep, int batch, int num_kv_heads,
