@@ -117,8 +117,9 @@ __device__ __forceinline__ void add_squares(const float2 (&y)[4], float2 &sum) {
 
 // y *= f * weights (1 without weights).  kStepwise, here and below: each operation rounded by
 // itself, as in the formula written out in fp32.  4 bits: a code is one of few, and a rounding
-// that differs may make it the next one (of 25 million codes of normed and rotated keys, 3.8
-// differed from those of the formula written out, and 1.9 do so).
+// that differs may make it the next one.  Of 152 million codes of normed and rotated keys 8 differ
+// from those of the formula written out in fp32, 16 with fused products (118.9 us instead of
+// 120.7, 24,768 rows); from those of the formula in 64 bits 40 and 38, which is the same.
 template <bool kStepwise = false>
 __device__ __forceinline__ void scale8(float2 (&y)[4], const uint4 &w, float f) {
     float2 g[4];
